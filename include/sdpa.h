@@ -74,8 +74,10 @@ typedef enum {
   SDPA_ERR_BAD_SEQLENS = 6,      /* device-detected: cu_seqlens not compact / out of bounds */
   SDPA_ERR_TIMEOUT = 7,          /* device-detected: a bounded wait inside a kernel gave up */
   SDPA_ERR_CUDA = 8,             /* a CUDA runtime or driver call failed */
-  SDPA_ERR_ADDRESS = 9           /* device-detected, address-checked library only: a kernel access
+  SDPA_ERR_ADDRESS = 9,          /* device-detected, address-checked library only: a kernel access
                                     fell outside the call's buffers and was skipped */
+  SDPA_ERR_BAD_INDEX = 10        /* device-detected: a page number outside the cache or a position
+                                    outside the rotation table */
 } sdpa_status;
 
 typedef enum { SDPA_BSHD = 0, SDPA_SBHD = 1, SDPA_THD = 2 } sdpa_layout;
@@ -317,6 +319,103 @@ SDPA_API int sdpa_fwd_fp8(const sdpa_problem* p, const void* q8, const void* k8,
                           float descale_k, float descale_v, void* o, float* lse, const int32_t* cu_seqlens_q,
                           const int32_t* cu_seqlens_kv, void* workspace, size_t ws_bytes, void* stream);
 
+/* ---------------------------------------------------------------- norms, rotation, paged cache
+ * The steps between a projection and the attention kernels, and attention over a
+ * paged key/value cache. */
+
+/* Per-head norm of queries and keys with the position rotation in the same pass.
+ * For every row x (head_dim values of one head of one token), in float32:
+ *     r = 1 / sqrt(mean(x^2) + eps),   y = x * r * w        (w = q_weight or k_weight)
+ * and the first rotary_dim values of y are rotated in pairs (a, b) by the angle of the
+ * token's position:  a' = a cos - b sin,  b' = b cos + a sin.  Pair i is
+ * (i, i + rotary_dim/2), or (2i, 2i+1) with interleaved = 1. Results are rounded once.
+ *   cos_sin: float32 [max_positions][rotary_dim]: rotary_dim/2 cosines, then as many sines
+ *            of one position. NULL when rotary_dim is 0 (norm alone).
+ *   positions: device int32 [rows]. A position outside [0, max_positions) is recorded as
+ *            SDPA_ERR_BAD_INDEX in the device error word and the token's rows are not
+ *            written (the backward writes zeros and adds nothing to the weight gradients).
+ * head_dim 128, 192, 256 or 512; rotary_dim a multiple of 16, at most head_dim. Rows of q and k may lie
+ * apart (slices of one fused projection): the heads of a token are contiguous, tokens are
+ * q_stride / k_stride elements apart (multiples of 8; 0 = contiguous). Outputs are
+ * contiguous, but dq / dk of the backward may lie apart too (dq_stride, dk_stride). */
+typedef struct {
+  int dtype;             /* sdpa_dtype of q, k, the weights and the outputs */
+  int num_heads_q, num_heads_kv;
+  int head_dim;
+  int rotary_dim;        /* 0 = no rotation */
+  int interleaved;       /* pairs (2i, 2i+1) instead of (i, i + rotary_dim/2); 0 or 1 */
+  float eps;             /* >= 0 and finite */
+  int max_positions;     /* rows of cos_sin */
+  long long rows;        /* tokens */
+  long long q_stride, k_stride;    /* elements between tokens of q, k; 0 = contiguous */
+  long long dq_stride, dk_stride;  /* elements between tokens of dq, dk (backward); 0 = contiguous */
+} sdpa_norm_rope_problem;
+/* Forward: q_out [rows][Hq][D] and k_out [rows][Hkv][D] are written; they may not overlap
+ * any input. One launch. */
+SDPA_API int sdpa_qk_norm_rope(const sdpa_norm_rope_problem* p, const void* q, const void* k, const void* q_weight,
+                               const void* k_weight, const float* cos_sin, const int32_t* positions, void* q_out,
+                               void* k_out, void* stream);
+/* Backward of the same function: from the gradients dq_out, dk_out (contiguous) of its
+ * outputs and its inputs, with g the gradient rotated back and gw = g * w:
+ *     dx = r gw - x r^3 mean(gw x),   dw = sum over rows and heads of g x r.
+ * dq, dk (dtype) and dq_weight, dk_weight (float32 [head_dim]) are written. The sums over
+ * rows are formed in float32 in an order fixed by the problem: results are bitwise
+ * reproducible. workspace: sdpa_qk_norm_rope_bwd_workspace_size bytes, 16-byte aligned. */
+SDPA_API size_t sdpa_qk_norm_rope_bwd_workspace_size(const sdpa_norm_rope_problem* p);
+SDPA_API int sdpa_qk_norm_rope_bwd(const sdpa_norm_rope_problem* p, const void* dq_out, const void* dk_out,
+                                   const void* q, const void* k, const void* q_weight, const void* k_weight,
+                                   const float* cos_sin, const int32_t* positions, void* dq, void* dk,
+                                   float* dq_weight, float* dk_weight, void* workspace, size_t ws_bytes, void* stream);
+
+/* A paged key/value cache and a batch of new tokens over it.
+ * Cache: num_pages pages of page_size slots. Slot s, head h of page g of K starts at element
+ *   g * k_page_stride + s * k_slot_stride + h * k_head_stride (head_dim contiguous values; V
+ *   likewise with head_dim_v). All strides are multiples of 8 elements, so both orders,
+ *   [page][slot][head][D] and [page][head][slot][D], and pages that hold K and V together
+ *   are served.
+ * Batch: sequence b owns the new tokens cu_seqlens_q[b] .. cu_seqlens_q[b+1]-1 of the packed
+ *   [total_q][heads][D] rows (any number, 0 included; rows from cu_seqlens_q[batch] on are
+ *   left as they are), and kv_lens[b] cached keys, those of its new tokens last: new token i
+ *   sits at position kv_lens[b] - q_len + i. Position p is slot p % page_size of page
+ *   block_table[b * table_stride + p / page_size]. Entries behind a sequence's last page
+ *   are not read. */
+typedef struct {
+  int dtype;             /* sdpa_dtype */
+  int batch;
+  int num_heads_q, num_heads_kv;
+  int head_dim;          /* D: 128, 192, 256 or 512 */
+  int head_dim_v;        /* Dv: 0 or D, but 128 for D = 192 (0 = 128 there) */
+  int total_q;           /* rows of the new tokens' tensors */
+  int seqlen_q;          /* the most new tokens of a sequence (bounds the grid; more is refused on the device) */
+  int seqlen_kv;         /* the longest kv_len (likewise) */
+  int page_size;         /* a multiple of 16 */
+  int num_pages;
+  int max_pages;         /* columns of block_table */
+  int mask_type;         /* SDPA_MASK_NONE, or SDPA_MASK_CAUSAL_BOTTOM_RIGHT: query at position x sees keys <= x */
+  int window_left;       /* keys seen left of the diagonal, -1 = all; causal only */
+  float softmax_scale;   /* finite and >= 0 */
+  long long table_stride;  /* elements between rows of block_table; 0 = max_pages */
+  long long k_page_stride, k_slot_stride, k_head_stride;
+  long long v_page_stride, v_slot_stride, v_head_stride;
+  long long q_stride, k_stride, v_stride;  /* elements between tokens of q, k, v (multiples of 8); 0 = contiguous */
+} sdpa_paged_problem;
+
+/* Writes the new tokens' K [total_q][Hkv][D] and V [total_q][Hkv][Dv] rows into their pages;
+ * everything else in the cache stays as it is. With n (else NULL), K is normed and rotated on
+ * the way as by sdpa_qk_norm_rope, and so is q into q_out [total_q][Hq][D]; of n, the fields eps,
+ * rotary_dim, interleaved and max_positions are read. positions: device int32 [total_q], the
+ * rotation's positions, or NULL for the cache positions. One launch.
+ * A token is skipped, and the device error word set, when its sequence's lengths do not fit
+ * (SDPA_ERR_BAD_SEQLENS) or its page or position lies outside its table (SDPA_ERR_BAD_INDEX).
+ * Two tokens of one call that map to one slot leave one of their rows there. */
+SDPA_API int sdpa_paged_append(const sdpa_paged_problem* p, const sdpa_norm_rope_problem* n, const void* q,
+                               const void* k, const void* v, const void* q_weight, const void* k_weight,
+                               const float* cos_sin, const int32_t* positions, void* q_out, void* k_cache,
+                               void* v_cache, const int32_t* cu_seqlens_q, const int32_t* kv_lens,
+                               const int32_t* block_table, void* stream);
+
+SDPA_API int sdpa_check_paged(const sdpa_paged_problem* p);
+
 /* Kernel timing for benchmarks and tracing. Between sdpa_profile_begin and
  * sdpa_profile_end, every sdpa_fwd / sdpa_bwd call made by this host thread
  * (and sdpa_merge) records a pair of CUDA events on its stream around each kernel it
@@ -332,7 +431,11 @@ typedef enum {
   SDPA_KERNEL_MERGE = 5,      /* log-sum-exp merge of key-split partial results */
   SDPA_KERNEL_BWD_DQ = 6,     /* deterministic backward: the separate head_dim 128 dQ pass */
   SDPA_KERNEL_V_TRANSPOSE = 7, /* FP8 forward: V transposed into the workspace */
-  SDPA_KERNEL_KINDS = 8
+  SDPA_KERNEL_NORM_ROPE = 8,   /* per-head norm + rotation, forward or backward */
+  SDPA_KERNEL_APPEND = 9,      /* new rows into their pages (with the norm + rotation when fused) */
+  SDPA_KERNEL_PAGED = 10,      /* attention over the paged cache */
+  SDPA_KERNEL_PAGED_JOIN = 11, /* its join of partial results over a split of the keys */
+  SDPA_KERNEL_KINDS = 12
 } sdpa_kernel_kind;
 SDPA_API int sdpa_profile_begin(void);
 SDPA_API int sdpa_profile_end(double* ms_by_kind, int* launches_by_kind, int n_kinds);

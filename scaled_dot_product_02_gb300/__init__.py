@@ -27,14 +27,17 @@ LAYOUTS = {"bshd": 0, "sbhd": 1, "thd": 2}
 MASKS = {"none": 0, "causal": 1, "causal_br": 2}
 STATUS = {0: "SDPA_OK", 1: "SDPA_ERR_INVALID_ARG", 2: "SDPA_ERR_UNSUPPORTED", 3: "SDPA_ERR_ALIGNMENT",
           4: "SDPA_ERR_OVERLAP", 5: "SDPA_ERR_WORKSPACE_TOO_SMALL", 6: "SDPA_ERR_BAD_SEQLENS",
-          7: "SDPA_ERR_TIMEOUT", 8: "SDPA_ERR_CUDA", 9: "SDPA_ERR_ADDRESS"}
+          7: "SDPA_ERR_TIMEOUT", 8: "SDPA_ERR_CUDA", 9: "SDPA_ERR_ADDRESS",
+          10: "SDPA_ERR_BAD_INDEX"}
 EXPORTS = ("sdpa_fwd_workspace_size", "sdpa_bwd_workspace_size", "sdpa_check_problem", "sdpa_fwd", "sdpa_bwd",
            "sdpa_get_device_error", "sdpa_error_string", "sdpa_last_launch_count", "sdpa_profile_begin",
            "sdpa_profile_end", "sdpa_bwd_noalloc", "sdpa_selftest_bounded_wait", "sdpa_merge",
            "sdpa_fwd_fp8_workspace_size", "sdpa_fwd_fp8", "sdpa_debug_set_max_ctas", "sdpa_debug_address_report",
-           "sdpa_debug_address_shrink")
+           "sdpa_debug_address_shrink", "sdpa_qk_norm_rope", "sdpa_qk_norm_rope_bwd_workspace_size",
+           "sdpa_qk_norm_rope_bwd", "sdpa_check_paged", "sdpa_paged_append")
 NOALLOC_MAX_BYTES = 32 << 20  # SDPA_BWD_NOALLOC_MAX_BYTES
-KERNEL_KINDS = ("fwd", "bwd", "preprocess", "dq_finalize", "guard", "merge", "bwd_dq", "v_transpose")
+KERNEL_KINDS = ("fwd", "bwd", "preprocess", "dq_finalize", "guard", "merge", "bwd_dq", "v_transpose",
+                "norm_rope", "append", "paged", "paged_join")
 
 
 class SdpaError(RuntimeError):
@@ -47,6 +50,24 @@ class MergeProblem(ctypes.Structure):
     """sdpa_merge_problem (include/sdpa.h)."""
     _fields_ = [("dtype", ctypes.c_int), ("items", ctypes.c_longlong), ("head_dim", ctypes.c_int),
                 ("n_parts", ctypes.c_int)]
+
+
+class NormRopeProblem(ctypes.Structure):
+    """sdpa_norm_rope_problem (include/sdpa.h)."""
+    _fields_ = [(n, ctypes.c_int) for n in ("dtype", "num_heads_q", "num_heads_kv", "head_dim", "rotary_dim",
+                                            "interleaved")] + [("eps", ctypes.c_float),
+                                                               ("max_positions", ctypes.c_int)] + [
+        (n, ctypes.c_longlong) for n in ("rows", "q_stride", "k_stride", "dq_stride", "dk_stride")]
+
+
+class PagedProblem(ctypes.Structure):
+    """sdpa_paged_problem (include/sdpa.h)."""
+    _fields_ = [(n, ctypes.c_int) for n in ("dtype", "batch", "num_heads_q", "num_heads_kv", "head_dim", "head_dim_v",
+                                            "total_q", "seqlen_q", "seqlen_kv", "page_size", "num_pages", "max_pages",
+                                            "mask_type", "window_left")] + [("softmax_scale", ctypes.c_float)] + [
+        (n, ctypes.c_longlong) for n in ("table_stride", "k_page_stride", "k_slot_stride", "k_head_stride",
+                                         "v_page_stride", "v_slot_stride", "v_head_stride", "q_stride", "k_stride",
+                                         "v_stride")]
 
 
 class Problem(ctypes.Structure):
@@ -94,6 +115,13 @@ def _load(path):
         L.sdpa_fwd_fp8_workspace_size.restype = ctypes.c_size_t
         fl = ctypes.c_float
         L.sdpa_fwd_fp8.argtypes = [pp, vp, vp, vp, fl, fl, fl, vp, vp, vp, vp, vp, ctypes.c_size_t, vp]
+        npp, ppp = ctypes.POINTER(NormRopeProblem), ctypes.POINTER(PagedProblem)
+        L.sdpa_qk_norm_rope.argtypes = [npp] + [vp] * 9
+        L.sdpa_qk_norm_rope_bwd_workspace_size.argtypes = [npp]
+        L.sdpa_qk_norm_rope_bwd_workspace_size.restype = ctypes.c_size_t
+        L.sdpa_qk_norm_rope_bwd.argtypes = [npp] + [vp] * 13 + [ctypes.c_size_t, vp]
+        L.sdpa_check_paged.argtypes = [ppp]
+        L.sdpa_paged_append.argtypes = [ppp, npp] + [vp] * 14
         _libs[path] = L
     return _libs[path]
 
@@ -466,6 +494,270 @@ def sdpa_merge(o_parts, lse_parts, *, out=None, lse=None, stream=None):
     if rc:
         raise SdpaError(rc, "sdpa_merge")
     return out, lse
+
+# ---------------------------------------------------------------- norms, rotation, paged cache
+_DTYPE_CODE = {}
+
+
+def _dtype_code(t, name):
+    import torch
+
+    if not _DTYPE_CODE:
+        _DTYPE_CODE.update({torch.bfloat16: 0, torch.float16: 1})
+    code = _DTYPE_CODE.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name} must be bfloat16 or float16, got {t.dtype}")
+    return code
+
+
+def _on(device, stream, call):
+    """call(raw stream) with `device` current: the C entry points launch on the
+    calling thread's current device, so tensors of another one select theirs
+    for the call. stream: a torch stream of that device, or None for its
+    current one."""
+    import torch
+
+    if stream is not None and stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+    if device.index == torch.cuda.current_device():
+        return call((torch.cuda.current_stream(device) if stream is None else stream).cuda_stream)
+    with torch.cuda.device(device):
+        return call((torch.cuda.current_stream(device) if stream is None else stream).cuda_stream)
+
+
+def _refuse_cpu(t):
+    if not t.is_cuda:
+        raise ValueError("sdpa tensors must be CUDA tensors (there is no CPU implementation)")
+
+
+def _rows_of_heads(name, t, like=None):
+    """(rows, heads, head_dim, elements between rows) of [..., H, D] whose
+    leading dimensions are one evenly spaced row index (contiguous, or a slice
+    of a fused projection's output) and whose heads are contiguous."""
+    shape, st = t.shape, t.stride()
+    if len(shape) < 3:
+        raise ValueError(f"{name} must have at least 3 dimensions [..., heads, head_dim], got {tuple(shape)}")
+    if like is not None and (t.dtype != like.dtype or t.device != like.device):
+        raise ValueError(f"{name} must have dtype {like.dtype} on {like.device}, got {t.dtype} on {t.device}")
+    h, d = shape[-2], shape[-1]
+    rows, step, spaced = 1, h * d, st[-1] == 1 and (st[-2] == d or h == 1)
+    found = False
+    for n, s in zip(reversed(shape[:-2]), reversed(st[:-2])):
+        if n != 1:
+            if not found:
+                step, found = s, True
+            elif s != rows * step:
+                spaced = False
+            rows *= n
+    if rows and not spaced:
+        raise ValueError(f"{name} must hold contiguous heads in evenly spaced rows, got shape {tuple(shape)} and "
+                         f"strides {tuple(st)}")
+    return rows, h, d, step if found and rows else h * d
+
+
+def _expect(name, t, shape, dtype, device):
+    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, got "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def _norm_rope_args(p, q, d, q_weight, k_weight, cos_sin, positions, eps, interleaved, rows):
+    """Fill p's rotation fields and check the weights, the table and the positions."""
+    import torch
+
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        _expect(name, w, (d,), q.dtype, q.device)
+    p.eps, p.interleaved = eps, 1 if interleaved else 0
+    if cos_sin is None:
+        p.rotary_dim = p.max_positions = 0
+        return
+    if cos_sin.dim() != 2 or cos_sin.dtype != torch.float32 or cos_sin.device != q.device or not cos_sin.is_contiguous():
+        raise ValueError(f"cos_sin must be a contiguous float32 [positions, rotary_dim] tensor on {q.device}")
+    p.max_positions, p.rotary_dim = cos_sin.shape
+    if positions is not None and (positions.dtype != torch.int32 or positions.device != q.device or
+                                  positions.numel() != rows or not positions.is_contiguous()):
+        raise ValueError(f"positions must be a contiguous int32 tensor of one entry per token ({rows}) on {q.device}")
+
+
+def sdpa_qk_norm_rope(q, k, q_weight, k_weight, cos_sin=None, positions=None, *, eps=1e-6, interleaved=False, q_out=None,
+                      k_out=None, stream=None):
+    """Per-head norm of q [..., Hq, D] and k [..., Hkv, D] with the position
+    rotation in the same pass (sdpa_qk_norm_rope in include/sdpa.h). Any
+    layout's tensors do: the leading dimensions are the tokens. q and k may be
+    slices of one projection's output. q_weight, k_weight: [D] of q's dtype.
+    cos_sin: float32 [positions, rotary_dim], half cosines and half sines, or
+    None for the norm alone; positions: int32, one per token. Returns
+    contiguous (q_out, k_out)."""
+    import torch
+
+    rows, hq, d, qs = _rows_of_heads("q", q)
+    rows_k, hkv, dk, ks = _rows_of_heads("k", k, q)
+    if dk != d or q.shape[:-2] != k.shape[:-2]:
+        raise ValueError(f"q and k must agree on every dimension but the heads, got {tuple(q.shape)} and {tuple(k.shape)}")
+    p = NormRopeProblem(_dtype_code(q, "q"), hq, hkv, d)
+    p.rows, p.q_stride, p.k_stride = rows, qs, ks
+    _norm_rope_args(p, q, d, q_weight, k_weight, cos_sin, positions, eps, interleaved, rows)
+    if p.rotary_dim and positions is None:
+        raise ValueError("a rotation needs the tokens' positions")
+    _refuse_cpu(q)
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    else:
+        _expect("q_out", q_out, q.shape, q.dtype, q.device)
+    if k_out is None:
+        k_out = torch.empty(k.shape, dtype=q.dtype, device=q.device)
+    else:
+        _expect("k_out", k_out, k.shape, q.dtype, q.device)
+    rc = _on(q.device, stream, lambda s: lib().sdpa_qk_norm_rope(
+        ctypes.byref(p), q.data_ptr(), k.data_ptr(), q_weight.data_ptr(), k_weight.data_ptr(),
+        None if cos_sin is None else cos_sin.data_ptr(), None if positions is None else positions.data_ptr(),
+        q_out.data_ptr(), k_out.data_ptr(), s))
+    if rc:
+        raise SdpaError(rc, "sdpa_qk_norm_rope")
+    return q_out, k_out
+
+
+def sdpa_qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, cos_sin=None, positions=None, *, eps=1e-6,
+                          interleaved=False, dq=None, dk=None, dq_weight=None, dk_weight=None, workspace=None,
+                          stream=None):
+    """Gradient of sdpa_qk_norm_rope: from the (contiguous) gradients of its
+    outputs and its inputs, returns (dq, dk, dq_weight, dk_weight), the weights'
+    in float32. dq and dk may be slices of one fused gradient's rows. Bitwise
+    reproducible."""
+    import torch
+
+    rows, hq, d, qs = _rows_of_heads("q", q)
+    rows_k, hkv, d_k, ks = _rows_of_heads("k", k, q)
+    if d_k != d or q.shape[:-2] != k.shape[:-2]:
+        raise ValueError(f"q and k must agree on every dimension but the heads, got {tuple(q.shape)} and {tuple(k.shape)}")
+    p = NormRopeProblem(_dtype_code(q, "q"), hq, hkv, d)
+    p.rows, p.q_stride, p.k_stride = rows, qs, ks
+    _norm_rope_args(p, q, d, q_weight, k_weight, cos_sin, positions, eps, interleaved, rows)
+    if p.rotary_dim and positions is None:
+        raise ValueError("a rotation needs the tokens' positions")
+    _refuse_cpu(q)
+    _expect("dq_out", dq_out, q.shape, q.dtype, q.device)
+    _expect("dk_out", dk_out, k.shape, q.dtype, q.device)
+    for name, t, like in (("dq", dq, q), ("dk", dk, k)):
+        if t is not None and t.shape != like.shape:
+            raise ValueError(f"{name} must have shape {tuple(like.shape)}, got {tuple(t.shape)}")
+    dq = torch.empty(q.shape, dtype=q.dtype, device=q.device) if dq is None else dq
+    dk = torch.empty(k.shape, dtype=q.dtype, device=q.device) if dk is None else dk
+    p.dq_stride, p.dk_stride = _rows_of_heads("dq", dq, q)[3], _rows_of_heads("dk", dk, q)[3]
+    grads = []
+    for name, t in (("dq_weight", dq_weight), ("dk_weight", dk_weight)):
+        if t is None:
+            t = torch.empty(d, dtype=torch.float32, device=q.device)
+        else:
+            _expect(name, t, (d,), torch.float32, q.device)
+        grads.append(t)
+    need = int(lib().sdpa_qk_norm_rope_bwd_workspace_size(ctypes.byref(p)))
+    if workspace is None:
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+    elif workspace.device != q.device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {q.device}")
+    rc = _on(q.device, stream, lambda s: lib().sdpa_qk_norm_rope_bwd(
+        ctypes.byref(p), dq_out.data_ptr(), dk_out.data_ptr(), q.data_ptr(), k.data_ptr(), q_weight.data_ptr(),
+        k_weight.data_ptr(), None if cos_sin is None else cos_sin.data_ptr(),
+        None if positions is None else positions.data_ptr(), dq.data_ptr(), dk.data_ptr(), grads[0].data_ptr(),
+        grads[1].data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(), s))
+    if rc:
+        raise SdpaError(rc, "sdpa_qk_norm_rope_bwd")
+    return dq, dk, grads[0], grads[1]
+
+
+CACHE_LAYOUTS = ("nhd", "hnd")  # [pages, page_size, Hkv, D] and [pages, Hkv, page_size, D]
+
+
+def _paged_problem(q_like, hq, k_cache, v_cache, block_table, kv_lens, cu_seqlens_q, cache_layout) -> PagedProblem:
+    """The cache's and the batch's part of an sdpa_paged_problem, checked from
+    the tensors' metadata (no device access). Cache strides are free but for
+    contiguous head_dim, so a cache may be a slice of a larger tensor."""
+    import torch
+
+    if cache_layout not in CACHE_LAYOUTS:
+        raise ValueError(f"cache_layout must be one of {CACHE_LAYOUTS}, got {cache_layout!r}")
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        if t.dim() != 4 or t.dtype != q_like.dtype or t.device != q_like.device or t.stride(3) != 1:
+            raise ValueError(f"{name} must be a 4-dimensional {q_like.dtype} tensor on {q_like.device} with contiguous "
+                             f"head_dim, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    ks, vs = k_cache.shape, v_cache.shape
+    if ks[:3] != vs[:3]:
+        raise ValueError(f"k_cache and v_cache must agree on every dimension but the last, got {tuple(ks)} and {tuple(vs)}")
+    dev = q_like.device
+    if block_table.dim() != 2 or block_table.dtype != torch.int32 or block_table.device != dev or \
+            (block_table.shape[1] > 1 and block_table.stride(1) != 1):
+        raise ValueError(f"block_table must be a 2-D int32 [batch, pages] tensor on {dev} with contiguous rows")
+    batch, max_pages = block_table.shape
+    if kv_lens.dtype != torch.int32 or kv_lens.shape != (batch,) or kv_lens.device != dev or not kv_lens.is_contiguous():
+        raise ValueError(f"kv_lens must be a contiguous int32 tensor of {batch} entries on {dev}")
+    if cu_seqlens_q.dtype != torch.int32 or cu_seqlens_q.shape != (batch + 1,) or cu_seqlens_q.device != dev or \
+            not cu_seqlens_q.is_contiguous():
+        raise ValueError(f"cu_seqlens_q must be a contiguous int32 tensor of {batch + 1} entries on {dev}")
+    slot, head = (1, 2) if cache_layout == "nhd" else (2, 1)
+    k_st, v_st = k_cache.stride(), v_cache.stride()
+    p = PagedProblem(_dtype_code(q_like, "q"), batch, hq, ks[head], ks[3], vs[3])
+    p.page_size, p.num_pages, p.max_pages = ks[slot], ks[0], max_pages
+    p.table_stride = block_table.stride(0) if batch > 1 else 0
+    # a dimension of one entry may carry any stride: its own row's width stands for it
+    p.k_page_stride = k_st[0] if ks[0] > 1 else ks[3]
+    p.k_slot_stride, p.k_head_stride = k_st[slot], k_st[head] if ks[head] > 1 else ks[3]
+    p.v_page_stride = v_st[0] if vs[0] > 1 else vs[3]
+    p.v_slot_stride, p.v_head_stride = v_st[slot], v_st[head] if vs[head] > 1 else vs[3]
+    return p
+
+
+def sdpa_check_paged(p: PagedProblem) -> int:
+    return int(lib().sdpa_check_paged(ctypes.byref(p)))
+
+
+def sdpa_paged_append(k, v, k_cache, v_cache, block_table, kv_lens, cu_seqlens_q, *, cache_layout="nhd", q=None,
+                      q_weight=None, k_weight=None, cos_sin=None, positions=None, eps=1e-6, interleaved=False,
+                      q_out=None, stream=None):
+    """Write the new tokens' k [T, Hkv, D] and v [T, Hkv, Dv] into their pages
+    of k_cache and v_cache (sdpa_paged_append in include/sdpa.h). kv_lens count
+    the new tokens already. With q [T, Hq, D] (and q_weight, k_weight), k is
+    normed and rotated on its way into the cache and q into q_out, as by
+    sdpa_qk_norm_rope; positions default to the cache positions. Returns q_out
+    (None without q). k, v and q may be slices of one projection's output."""
+    import torch
+
+    rows, hkv, d, ks = _rows_of_heads("k", k)
+    rows_v, hkv_v, dv, vs = _rows_of_heads("v", v, k)
+    if k.dim() != 3 or v.dim() != 3 or rows != rows_v or hkv != hkv_v:
+        raise ValueError(f"k and v must be [tokens, heads, width] of the same tokens and heads, got {tuple(k.shape)} and "
+                         f"{tuple(v.shape)}")
+    hq, qs, n = hkv, 0, None
+    if q is not None:
+        rows_q, hq, d_q, qs = _rows_of_heads("q", q, k)
+        if q.dim() != 3 or rows_q != rows or d_q != d:
+            raise ValueError(f"q must be [tokens, heads, head_dim] of k's tokens and head_dim, got {tuple(q.shape)}")
+        if q_weight is None or k_weight is None:
+            raise ValueError("q needs q_weight and k_weight")
+    elif any(x is not None for x in (q_weight, k_weight, cos_sin, positions, q_out)):
+        raise ValueError("weights, cos_sin, positions and q_out go with q")
+    p = _paged_problem(k, hq, k_cache, v_cache, block_table, kv_lens, cu_seqlens_q, cache_layout)
+    if p.num_heads_kv != hkv or p.head_dim != d or p.head_dim_v != dv:
+        raise ValueError(f"k and v {tuple(k.shape)}, {tuple(v.shape)} do not fit the caches {tuple(k_cache.shape)}, "
+                         f"{tuple(v_cache.shape)} in layout {cache_layout}")
+    p.total_q, p.window_left = rows, -1
+    p.q_stride, p.k_stride, p.v_stride = qs, ks, vs
+    _refuse_cpu(k)
+    if q is not None:
+        n = NormRopeProblem()
+        _norm_rope_args(n, q, d, q_weight, k_weight, cos_sin, positions, eps, interleaved, rows)
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        else:
+            _expect("q_out", q_out, q.shape, q.dtype, q.device)
+    ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    rc = _on(k.device, stream, lambda s: lib().sdpa_paged_append(
+        ctypes.byref(p), None if n is None else ctypes.byref(n), ptr(q), k.data_ptr(), v.data_ptr(), ptr(q_weight),
+        ptr(k_weight), ptr(cos_sin), ptr(positions), ptr(q_out), k_cache.data_ptr(), v_cache.data_ptr(),
+        cu_seqlens_q.data_ptr(), kv_lens.data_ptr(), block_table.data_ptr(), s))
+    if rc:
+        raise SdpaError(rc, "sdpa_paged_append")
+    return q_out
 
 
 def sdpa_selftest_bounded_wait(limit_us: int = 20000, stream=None) -> None:

@@ -367,6 +367,71 @@ int bwd_head_block(const sdpa_problem* p) {
   return hb;
 }
 
+// ---- norms, rotation and the paged cache
+
+int check_norm_rope(const sdpa_norm_rope_problem* p) {
+  if (!p) return SDPA_ERR_INVALID_ARG;
+  if (p->dtype != SDPA_BF16 && p->dtype != SDPA_FP16) return SDPA_ERR_UNSUPPORTED;
+  if (p->head_dim != 128 && p->head_dim != 192 && p->head_dim != 256 && p->head_dim != 512)
+    return SDPA_ERR_UNSUPPORTED;
+  if (p->num_heads_q <= 0 || p->num_heads_kv <= 0 || p->rows < 0) return SDPA_ERR_INVALID_ARG;
+  if (p->num_heads_q > 65536 || p->num_heads_kv > 65536 || p->rows > 0x7fffffffLL) return SDPA_ERR_UNSUPPORTED;
+  if (p->rotary_dim < 0 || p->rotary_dim > p->head_dim || p->rotary_dim % 16) return SDPA_ERR_INVALID_ARG;
+  if (p->rotary_dim > 0 && p->max_positions < 1) return SDPA_ERR_INVALID_ARG;
+  if (p->interleaved != 0 && p->interleaved != 1) return SDPA_ERR_INVALID_ARG;
+  if (!std::isfinite(p->eps) || p->eps < 0.f) return SDPA_ERR_INVALID_ARG;
+  const long long qw = (long long)p->num_heads_q * p->head_dim, kw = (long long)p->num_heads_kv * p->head_dim;
+  for (const auto& [st, wd] : {std::pair<long long, long long>{p->q_stride, qw}, {p->k_stride, kw},
+                               {p->dq_stride, qw}, {p->dk_stride, kw}})
+    if (st != 0 && (st < wd || st % 8 || st >= (1LL << 32))) return SDPA_ERR_INVALID_ARG;
+  return SDPA_OK;
+}
+
+// Bytes spanned by `rows` rows of `width` 16-bit values, `stride` elements apart.
+size_t span(long long rows, long long stride, long long width) {
+  return rows > 0 ? (size_t)((rows - 1) * stride + width) * 2 : 0;
+}
+
+// Width of V rows of a paged problem (192 pairs with 128).
+int paged_dv(const sdpa_paged_problem* p) {
+  if (p->head_dim_v) return p->head_dim_v;
+  return p->head_dim == 192 ? 128 : p->head_dim;
+}
+
+int check_paged(const sdpa_paged_problem* p) {
+  if (!p) return SDPA_ERR_INVALID_ARG;
+  if (p->dtype != SDPA_BF16 && p->dtype != SDPA_FP16) return SDPA_ERR_UNSUPPORTED;
+  if (p->head_dim_v < 0) return SDPA_ERR_INVALID_ARG;
+  if (!head_dims_supported(p->head_dim, paged_dv(p))) return SDPA_ERR_UNSUPPORTED;
+  if (p->batch < 0 || p->total_q < 0 || p->seqlen_q < 0 || p->seqlen_kv < 0) return SDPA_ERR_INVALID_ARG;
+  if (p->num_heads_q <= 0 || p->num_heads_kv <= 0 || p->num_heads_q % p->num_heads_kv) return SDPA_ERR_INVALID_ARG;
+  if (p->num_heads_q > 65536 || p->batch > (1 << 20)) return SDPA_ERR_UNSUPPORTED;
+  if (p->page_size <= 0 || p->num_pages <= 0 || p->max_pages <= 0) return SDPA_ERR_INVALID_ARG;
+  if (p->page_size % 16 || p->page_size > (1 << 20)) return SDPA_ERR_UNSUPPORTED;
+  if ((long long)p->max_pages * p->page_size < p->seqlen_kv) return SDPA_ERR_INVALID_ARG;
+  if (p->table_stride != 0 && p->table_stride < p->max_pages) return SDPA_ERR_INVALID_ARG;
+  if (p->mask_type < SDPA_MASK_NONE || p->mask_type > SDPA_MASK_CAUSAL_BOTTOM_RIGHT) return SDPA_ERR_INVALID_ARG;
+  if (p->mask_type == SDPA_MASK_CAUSAL_TOP_LEFT) return SDPA_ERR_UNSUPPORTED;  // cached keys precede the new ones
+  if (p->window_left < -1) return SDPA_ERR_INVALID_ARG;
+  if (p->window_left >= 0 && p->mask_type == SDPA_MASK_NONE) return SDPA_ERR_UNSUPPORTED;
+  if (!std::isfinite(p->softmax_scale) || p->softmax_scale < 0.f) return SDPA_ERR_INVALID_ARG;
+  const int d = p->head_dim, dv = paged_dv(p);
+  for (const auto& [st, wd] : {std::pair<long long, long long>{p->k_page_stride, d}, {p->k_slot_stride, d},
+                               {p->k_head_stride, d}, {p->v_page_stride, dv}, {p->v_slot_stride, dv},
+                               {p->v_head_stride, dv}})
+    if (st < wd || st % 8 || st >= (1LL << 36)) return SDPA_ERR_INVALID_ARG;
+  for (const auto& [st, wd] : {std::pair<long long, long long>{p->q_stride, (long long)p->num_heads_q * d},
+                               {p->k_stride, (long long)p->num_heads_kv * d},
+                               {p->v_stride, (long long)p->num_heads_kv * dv}})
+    if (st != 0 && (st < wd || st % 8 || st >= (1LL << 32))) return SDPA_ERR_INVALID_ARG;
+  return SDPA_OK;
+}
+
+// Bytes from a cache's first element to its last.
+size_t cache_span(const sdpa_paged_problem* p, long long page, long long slot, long long head, int width) {
+  return (size_t)((p->num_pages - 1) * page + (p->page_size - 1) * slot + (p->num_heads_kv - 1) * head + width) * 2;
+}
+
 }  // namespace
 
 static std::atomic<int> g_max_ctas{0};
@@ -803,6 +868,253 @@ int sdpa_merge(const sdpa_merge_problem* p, const void* o_parts, const float* ls
   return SDPA_OK;
 }
 
+int sdpa_qk_norm_rope(const sdpa_norm_rope_problem* p, const void* q, const void* k, const void* q_weight,
+                      const void* k_weight, const float* cos_sin, const int32_t* positions, void* q_out, void* k_out,
+                      void* stream) {
+  t_last_launches = 0;
+  int rc = check_norm_rope(p);
+  if (rc) return rc;
+  if (p->rows == 0) return SDPA_OK;
+  if (!q || !k || !q_weight || !k_weight || !q_out || !k_out) return SDPA_ERR_INVALID_ARG;
+  if (p->rotary_dim > 0 && (!cos_sin || !positions)) return SDPA_ERR_INVALID_ARG;
+  for (const void* ptr : {q, k, q_weight, k_weight, (const void*)cos_sin, (const void*)q_out, (const void*)k_out})
+    if (!aligned16(ptr)) return SDPA_ERR_ALIGNMENT;
+  const long long qw = (long long)p->num_heads_q * p->head_dim, kw = (long long)p->num_heads_kv * p->head_dim;
+  NormRopeParams L;
+  std::memset(&L, 0, sizeof(L));
+  L.rows = p->rows;
+  L.hq = p->num_heads_q;
+  L.hkv = p->num_heads_kv;
+  L.rot = p->rotary_dim;
+  L.interleaved = p->interleaved;
+  L.eps = p->eps;
+  L.q = q;
+  L.k = k;
+  L.qs = p->q_stride ? p->q_stride : qw;
+  L.ks = p->k_stride ? p->k_stride : kw;
+  L.wq = q_weight;
+  L.wk = k_weight;
+  L.table = cos_sin;
+  L.max_pos = p->max_positions;
+  L.pos = positions;
+  L.q_out = q_out;
+  L.k_out = k_out;
+  const size_t wb = (size_t)p->head_dim * 2;
+  const Extent eq = extent(q_out, (size_t)p->rows * qw * 2), ek = extent(k_out, (size_t)p->rows * kw * 2);
+  const Extent ins[6] = {extent(q, span(p->rows, L.qs, qw)), extent(k, span(p->rows, L.ks, kw)),
+                         extent(q_weight, wb), extent(k_weight, wb),
+                         extent(cos_sin, p->rotary_dim ? (size_t)p->max_positions * p->rotary_dim * 4 : 0),
+                         extent(positions, p->rotary_dim ? (size_t)p->rows * 4 : 0)};
+  for (const Extent& in : ins)
+    if (overlaps(eq, in) || overlaps(ek, in)) return SDPA_ERR_OVERLAP;
+  if (overlaps(eq, ek)) return SDPA_ERR_OVERLAP;
+  L.err = error_word();
+  if (!L.err) return SDPA_ERR_CUDA;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  L.chk = bind_extents({eq, ek, ins[0], ins[1], ins[2], ins[3], ins[4], ins[5]}, L.err, s);
+  if (kAddrCheck && !L.chk) return SDPA_ERR_CUDA;
+  rc = timed(SDPA_KERNEL_NORM_ROPE, s,
+             [&] { return launch_norm_rope(L, p->head_dim, p->dtype == SDPA_BF16, false, s); });
+  if (rc) return rc;
+  t_last_launches = 1;
+  return SDPA_OK;
+}
+
+size_t sdpa_qk_norm_rope_bwd_workspace_size(const sdpa_norm_rope_problem* p) {
+  if (check_norm_rope(p) != SDPA_OK || p->rows == 0) return 0;
+  int parts;
+  return (size_t)norm_rope_bwd_blocks(p->rows, p->num_heads_q, p->num_heads_kv, p->head_dim, &parts) * 2 *
+         p->head_dim * 4;
+}
+
+int sdpa_qk_norm_rope_bwd(const sdpa_norm_rope_problem* p, const void* dq_out, const void* dk_out, const void* q,
+                          const void* k, const void* q_weight, const void* k_weight, const float* cos_sin,
+                          const int32_t* positions, void* dq, void* dk, float* dq_weight, float* dk_weight,
+                          void* workspace, size_t ws_bytes, void* stream) {
+  t_last_launches = 0;
+  int rc = check_norm_rope(p);
+  if (rc) return rc;
+  if (!dq_weight || !dk_weight) return SDPA_ERR_INVALID_ARG;
+  if (!aligned16(dq_weight) || !aligned16(dk_weight)) return SDPA_ERR_ALIGNMENT;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const size_t gw = (size_t)p->head_dim * 4;
+  if (p->rows == 0) {  // the weights' gradients of no rows are zeros
+    if (overlaps(extent(dq_weight, gw), extent(dk_weight, gw))) return SDPA_ERR_OVERLAP;
+    if (cudaMemsetAsync(dq_weight, 0, gw, s) != cudaSuccess || cudaMemsetAsync(dk_weight, 0, gw, s) != cudaSuccess)
+      return SDPA_ERR_CUDA;
+    return SDPA_OK;
+  }
+  if (!dq_out || !dk_out || !q || !k || !q_weight || !k_weight || !dq || !dk) return SDPA_ERR_INVALID_ARG;
+  if (p->rotary_dim > 0 && (!cos_sin || !positions)) return SDPA_ERR_INVALID_ARG;
+  for (const void* ptr : {dq_out, dk_out, q, k, q_weight, k_weight, (const void*)cos_sin, (const void*)dq,
+                          (const void*)dk})
+    if (!aligned16(ptr)) return SDPA_ERR_ALIGNMENT;
+  const size_t need = sdpa_qk_norm_rope_bwd_workspace_size(p);
+  if (!workspace || ws_bytes < need) return SDPA_ERR_WORKSPACE_TOO_SMALL;
+  if (!aligned16(workspace)) return SDPA_ERR_ALIGNMENT;
+  const long long qw = (long long)p->num_heads_q * p->head_dim, kw = (long long)p->num_heads_kv * p->head_dim;
+  NormRopeBwdParams L;
+  std::memset(&L, 0, sizeof(L));
+  L.rows = p->rows;
+  L.hq = p->num_heads_q;
+  L.hkv = p->num_heads_kv;
+  L.rot = p->rotary_dim;
+  L.interleaved = p->interleaved;
+  L.eps = p->eps;
+  L.gq = dq_out;
+  L.gk = dk_out;
+  L.q = q;
+  L.k = k;
+  L.qs = p->q_stride ? p->q_stride : qw;
+  L.ks = p->k_stride ? p->k_stride : kw;
+  L.wq = q_weight;
+  L.wk = k_weight;
+  L.table = cos_sin;
+  L.max_pos = p->max_positions;
+  L.pos = positions;
+  L.dq = dq;
+  L.dk = dk;
+  L.dqs = p->dq_stride ? p->dq_stride : qw;
+  L.dks = p->dk_stride ? p->dk_stride : kw;
+  L.part = static_cast<float*>(workspace);
+  L.dwq = dq_weight;
+  L.dwk = dk_weight;
+  L.blocks = norm_rope_bwd_blocks(p->rows, p->num_heads_q, p->num_heads_kv, p->head_dim, &L.parts);
+  const size_t wb = (size_t)p->head_dim * 2;
+  const Extent outs[5] = {extent(dq, span(p->rows, L.dqs, qw)), extent(dk, span(p->rows, L.dks, kw)),
+                          extent(dq_weight, gw), extent(dk_weight, gw), extent(workspace, need)};
+  const Extent ins[8] = {extent(dq_out, (size_t)p->rows * qw * 2), extent(dk_out, (size_t)p->rows * kw * 2),
+                         extent(q, span(p->rows, L.qs, qw)), extent(k, span(p->rows, L.ks, kw)),
+                         extent(q_weight, wb), extent(k_weight, wb),
+                         extent(cos_sin, p->rotary_dim ? (size_t)p->max_positions * p->rotary_dim * 4 : 0),
+                         extent(positions, p->rotary_dim ? (size_t)p->rows * 4 : 0)};
+  for (int a = 0; a < 5; ++a) {
+    for (const Extent& in : ins)
+      if (overlaps(outs[a], in)) return SDPA_ERR_OVERLAP;
+    for (int b = a + 1; b < 5; ++b) {
+      // dq and dk may be slices of one fused gradient: their rows interleave
+      const bool slices = a == 0 && b == 1 && L.dqs == L.dks && outs[0].lo != outs[1].lo &&
+                          (outs[1].lo > outs[0].lo ? outs[1].lo - outs[0].lo >= (uintptr_t)qw * 2 &&
+                                                         outs[1].lo - outs[0].lo + kw * 2 <= (uintptr_t)L.dqs * 2
+                                                   : outs[0].lo - outs[1].lo >= (uintptr_t)kw * 2 &&
+                                                         outs[0].lo - outs[1].lo + qw * 2 <= (uintptr_t)L.dqs * 2);
+      if (!slices && overlaps(outs[a], outs[b])) return SDPA_ERR_OVERLAP;
+    }
+  }
+  L.err = error_word();
+  if (!L.err) return SDPA_ERR_CUDA;
+  L.chk = bind_extents({outs[0], outs[1], outs[2], outs[3], outs[4], ins[0], ins[1], ins[2], ins[3], ins[4], ins[5],
+                        ins[6], ins[7]},
+                       L.err, s);
+  if (kAddrCheck && !L.chk) return SDPA_ERR_CUDA;
+  int n = 0;
+  rc = timed(SDPA_KERNEL_NORM_ROPE, s,
+             [&] { return launch_norm_rope_bwd(L, p->head_dim, p->dtype == SDPA_BF16, &n, s); });
+  if (rc) return rc;
+  t_last_launches = n;
+  return SDPA_OK;
+}
+
+int sdpa_check_paged(const sdpa_paged_problem* p) { return check_paged(p); }
+
+int sdpa_paged_append(const sdpa_paged_problem* p, const sdpa_norm_rope_problem* n, const void* q, const void* k,
+                      const void* v, const void* q_weight, const void* k_weight, const float* cos_sin,
+                      const int32_t* positions, void* q_out, void* k_cache, void* v_cache,
+                      const int32_t* cu_seqlens_q, const int32_t* kv_lens, const int32_t* block_table, void* stream) {
+  t_last_launches = 0;
+  int rc = check_paged(p);
+  if (rc) return rc;
+  if (n) {
+    sdpa_norm_rope_problem full = *n;  // its sizes are the paged problem's
+    full.dtype = p->dtype;
+    full.num_heads_q = p->num_heads_q;
+    full.num_heads_kv = p->num_heads_kv;
+    full.head_dim = p->head_dim;
+    full.rows = p->total_q;
+    full.q_stride = full.k_stride = full.dq_stride = full.dk_stride = 0;
+    if ((rc = check_norm_rope(&full))) return rc;
+  }
+  if (p->batch == 0 || p->total_q == 0) return SDPA_OK;
+  if (!k || !v || !k_cache || !v_cache || !cu_seqlens_q || !kv_lens || !block_table) return SDPA_ERR_INVALID_ARG;
+  const bool rot = n && n->rotary_dim > 0;
+  if (n && (!q || !q_out || !q_weight || !k_weight)) return SDPA_ERR_INVALID_ARG;
+  if (rot && !cos_sin) return SDPA_ERR_INVALID_ARG;
+  for (const void* ptr : {k, v, (const void*)k_cache, (const void*)v_cache})
+    if (!aligned16(ptr)) return SDPA_ERR_ALIGNMENT;
+  if (n)
+    for (const void* ptr : {q, (const void*)q_out, q_weight, k_weight, (const void*)cos_sin})
+      if (!aligned16(ptr)) return SDPA_ERR_ALIGNMENT;
+  const int d = p->head_dim, dv = paged_dv(p);
+  const long long qw = (long long)p->num_heads_q * d, kw = (long long)p->num_heads_kv * d,
+                  vw = (long long)p->num_heads_kv * dv;
+  NormRopeParams L;
+  std::memset(&L, 0, sizeof(L));
+  L.rows = p->total_q;
+  L.hq = n ? p->num_heads_q : 0;
+  L.hkv = p->num_heads_kv;
+  L.k = k;
+  L.v = v;
+  L.ks = p->k_stride ? p->k_stride : kw;
+  L.vs = p->v_stride ? p->v_stride : vw;
+  if (n) {
+    L.rot = n->rotary_dim;
+    L.interleaved = n->interleaved;
+    L.eps = n->eps;
+    L.q = q;
+    L.qs = p->q_stride ? p->q_stride : qw;
+    L.wq = q_weight;
+    L.wk = k_weight;
+    L.table = cos_sin;
+    L.max_pos = n->max_positions;
+    L.pos = rot ? positions : nullptr;
+    L.q_out = q_out;
+  }
+  L.batch = p->batch;
+  L.max_pages = p->max_pages;
+  L.num_pages = p->num_pages;
+  L.page_size = p->page_size;
+  L.cu_q = cu_seqlens_q;
+  L.kv_lens = kv_lens;
+  L.table_ids = block_table;
+  L.table_stride = p->table_stride ? p->table_stride : p->max_pages;
+  L.kc = k_cache;
+  L.vc = v_cache;
+  L.kc_page = p->k_page_stride;
+  L.kc_slot = p->k_slot_stride;
+  L.kc_head = p->k_head_stride;
+  L.vc_page = p->v_page_stride;
+  L.vc_slot = p->v_slot_stride;
+  L.vc_head = p->v_head_stride;
+  const size_t wb = (size_t)d * 2;
+  const Extent outs[3] = {
+      extent(k_cache, cache_span(p, p->k_page_stride, p->k_slot_stride, p->k_head_stride, d)),
+      extent(v_cache, cache_span(p, p->v_page_stride, p->v_slot_stride, p->v_head_stride, dv)),
+      extent(q_out, n ? (size_t)p->total_q * qw * 2 : 0)};
+  const Extent ins[10] = {extent(k, span(p->total_q, L.ks, kw)), extent(v, span(p->total_q, L.vs, vw)),
+                          extent(q, n ? span(p->total_q, L.qs, qw) : 0), extent(q_weight, n ? wb : 0),
+                          extent(k_weight, n ? wb : 0),
+                          extent(cos_sin, rot ? (size_t)n->max_positions * n->rotary_dim * 4 : 0),
+                          extent(positions, L.pos ? (size_t)p->total_q * 4 : 0),
+                          extent(cu_seqlens_q, 4 * ((size_t)p->batch + 1)), extent(kv_lens, 4 * (size_t)p->batch),
+                          extent(block_table, 4 * (size_t)((p->batch - 1) * L.table_stride + p->max_pages))};
+  for (const Extent& out : outs)
+    for (const Extent& in : ins)
+      if (overlaps(out, in)) return SDPA_ERR_OVERLAP;
+  // the caches' spans may interleave (pages that hold K and V together), q_out's may not
+  if (overlaps(outs[2], outs[0]) || overlaps(outs[2], outs[1])) return SDPA_ERR_OVERLAP;
+  L.err = error_word();
+  if (!L.err) return SDPA_ERR_CUDA;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  L.chk = bind_extents({outs[0], outs[1], outs[2], ins[0], ins[1], ins[2], ins[3], ins[4], ins[5], ins[6], ins[7],
+                        ins[8], ins[9]},
+                       L.err, s);
+  if (kAddrCheck && !L.chk) return SDPA_ERR_CUDA;
+  rc = timed(SDPA_KERNEL_APPEND, s, [&] { return launch_norm_rope(L, d, p->dtype == SDPA_BF16, true, s); });
+  if (rc) return rc;
+  t_last_launches = 1;
+  return SDPA_OK;
+}
+
 int sdpa_get_device_error(void* stream) {
   int* err = error_word();
   if (!err) return SDPA_ERR_CUDA;
@@ -827,6 +1139,7 @@ const char* sdpa_error_string(int status) {
     case SDPA_ERR_TIMEOUT: return "a bounded wait inside a kernel gave up";
     case SDPA_ERR_CUDA: return "a CUDA runtime or driver call failed";
     case SDPA_ERR_ADDRESS: return "a kernel access fell outside the call's buffers (address-checked library)";
+    case SDPA_ERR_BAD_INDEX: return "a page number or a position lies outside its table";
     default: return "unknown status";
   }
 }

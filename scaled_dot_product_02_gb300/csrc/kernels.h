@@ -182,6 +182,56 @@ int launch_preprocess(const PrepParams& pp, bool bf16, cudaStream_t s);
 int launch_wait_selftest(uint64_t limit_ns, int* err, cudaStream_t s);
 int launch_dq_finalize(const Geom& g, const float* dq_acc, void* dq, const int* guard, bool bf16, cudaStream_t s);
 
+// Per-head norm + rotation, and the append to a paged cache (norm_rope.cu).
+struct NormRopeParams {
+  long long rows;              // tokens
+  int hq, hkv;                 // heads of q (0: none given) and of k (and v)
+  int rot;                     // leading values rotated (0: none)
+  int interleaved;
+  float eps;
+  const void *q, *k, *v;       // v: append only
+  long long qs, ks, vs;        // elements between tokens
+  const void *wq, *wk;         // nullptr: rows are copied as they are (append)
+  const float* table;          // [max_pos][rot]
+  int max_pos;
+  const int32_t* pos;          // [rows]; nullptr: cache positions (append)
+  void *q_out, *k_out;         // contiguous (k_out: not for the append)
+  int parts;                   // warps that share one token's heads
+  // append: the batch and the cache
+  int batch, max_pages, num_pages, page_size;
+  const int32_t *cu_q, *kv_lens, *table_ids;
+  long long table_stride;
+  void *kc, *vc;
+  long long kc_page, kc_slot, kc_head, vc_page, vc_slot, vc_head;
+  int* err;
+  AddrTable* chk;
+};
+int launch_norm_rope(NormRopeParams p, int head_dim, bool bf16, bool append, cudaStream_t s);
+
+struct NormRopeBwdParams {
+  long long rows;
+  int hq, hkv, rot, interleaved;
+  float eps;
+  const void *gq, *gk;         // gradients of the outputs, contiguous
+  const void *q, *k;
+  long long qs, ks;
+  const void *wq, *wk;
+  const float* table;
+  int max_pos;
+  const int32_t* pos;
+  void *dq, *dk;
+  long long dqs, dks;
+  float* part;                 // [blocks][2][D] partial sums of dw
+  float *dwq, *dwk;
+  int parts, blocks;
+  int* err;
+  AddrTable* chk;
+};
+// Blocks of the backward (each writes one partial sum of dw): a function of
+// the problem and the device alone, so the order of the sums is fixed.
+int norm_rope_bwd_blocks(long long rows, int hq, int hkv, int head_dim, int* parts);
+int launch_norm_rope_bwd(const NormRopeBwdParams& p, int head_dim, bool bf16, int* launches, cudaStream_t s);
+
 // Log-sum-exp merge of partial results over a split of the keys (merge.cu).
 int launch_merge(const void* o_parts, const float* lse_parts, void* o, float* lse, long long items, int head_dim,
                  int n_parts, bool bf16, AddrTable* chk, cudaStream_t s);

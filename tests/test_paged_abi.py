@@ -1,0 +1,166 @@
+"""Host-side refusals of the norm + rotation and paged-cache entry points (no GPU)."""
+import ctypes
+
+import pytest
+import torch
+
+import scaled_dot_product_02_gb300 as sdpa
+
+PTR = ctypes.c_void_p
+BASE = 1 << 40
+M = 1 << 24
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    from scaled_dot_product_02_gb300 import build
+
+    build.build()
+
+
+def norm_problem(**kw):
+    p = sdpa.NormRopeProblem()
+    base = dict(dtype=0, num_heads_q=8, num_heads_kv=2, head_dim=128, rotary_dim=128, interleaved=0, eps=1e-6,
+                max_positions=1000, rows=100, q_stride=0, k_stride=0, dq_stride=0, dk_stride=0)
+    base.update(kw)
+    for k, v in base.items():
+        setattr(p, k, v)
+    return p
+
+
+def paged_problem(**kw):
+    p = sdpa.PagedProblem()
+    base = dict(dtype=0, batch=4, num_heads_q=8, num_heads_kv=2, head_dim=128, head_dim_v=0, total_q=40, seqlen_q=10,
+                seqlen_kv=1000, page_size=16, num_pages=300, max_pages=63, mask_type=2, window_left=-1,
+                softmax_scale=0.1, table_stride=0, q_stride=0, k_stride=0, v_stride=0)
+    d = kw.get("head_dim", 128)
+    base.update(k_page_stride=16 * 2 * d, k_slot_stride=2 * d, k_head_stride=d, v_page_stride=16 * 2 * d,
+                v_slot_stride=2 * d, v_head_stride=d)
+    base.update(kw)
+    for k, v in base.items():
+        setattr(p, k, v)
+    return p
+
+
+def norm_call(p, **kw):
+    a = dict(q=BASE, k=BASE + M, wq=BASE + 2 * M, wk=BASE + 3 * M, t=BASE + 4 * M, pos=BASE + 5 * M, qo=BASE + 6 * M,
+             ko=BASE + 7 * M)
+    a.update(kw)
+    return sdpa.lib().sdpa_qk_norm_rope(ctypes.byref(p) if p is not None else None, *[PTR(x) if x else None for x in a.values()],
+                                        None)
+
+
+def test_norm_rope_refusals():
+    assert norm_call(None) == 1
+    assert norm_call(norm_problem(rows=0)) == 0
+    for bad, code in ((dict(dtype=2), 2), (dict(head_dim=64), 2), (dict(num_heads_q=0), 1), (dict(num_heads_kv=-1), 1),
+                      (dict(rows=-1), 1), (dict(rotary_dim=8), 1), (dict(rotary_dim=144), 1), (dict(rotary_dim=-16), 1),
+                      (dict(max_positions=0), 1), (dict(interleaved=2), 1), (dict(eps=-1.0), 1),
+                      (dict(eps=float("nan")), 1), (dict(q_stride=1000), 1), (dict(q_stride=1028), 1),
+                      (dict(rows=1 << 31), 2)):
+        assert norm_call(norm_problem(**bad)) == code, bad
+    ok = norm_problem()
+    for name in ("q", "k", "wq", "wk", "qo", "ko", "t", "pos"):
+        assert norm_call(ok, **{name: None}) == 1, name
+    for name in ("q", "k", "wq", "wk", "qo", "ko", "t"):
+        at = {"q": 0, "k": 1, "wq": 2, "wk": 3, "t": 4, "qo": 6, "ko": 7}[name]
+        assert norm_call(ok, **{name: BASE + at * M + 8}) == 3, name
+    assert norm_call(ok, qo=BASE + 64) == 4           # in place is refused too
+    assert norm_call(ok, ko=BASE + 6 * M + 100 * 8 * 128 * 2 - 16) == 4
+    # a row further down a strided q is part of its extent
+    assert norm_call(norm_problem(q_stride=4096), ko=BASE + 99 * 4096 * 2) == 4
+
+
+def test_norm_rope_bwd_refusals():
+    def call(p, ws=BASE + 20 * M, n=None, **kw):
+        a = dict(gq=BASE, gk=BASE + M, q=BASE + 2 * M, k=BASE + 3 * M, wq=BASE + 4 * M, wk=BASE + 5 * M, t=BASE + 6 * M,
+                 pos=BASE + 7 * M, dq=BASE + 8 * M, dk=BASE + 9 * M, dwq=BASE + 10 * M, dwk=BASE + 11 * M)
+        a.update(kw)
+        n = sdpa.lib().sdpa_qk_norm_rope_bwd_workspace_size(ctypes.byref(p)) if n is None else n
+        return sdpa.lib().sdpa_qk_norm_rope_bwd(ctypes.byref(p), *[PTR(x) if x else None for x in a.values()],
+                                                PTR(ws) if ws else None, n, None)
+
+    ok = norm_problem()
+    assert sdpa.lib().sdpa_qk_norm_rope_bwd_workspace_size(ctypes.byref(norm_problem(head_dim=64))) == 0
+    assert call(ok, n=16) == 5 and call(ok, ws=None) == 5 and call(ok, ws=BASE + 20 * M + 8) == 3
+    for name in ("gq", "gk", "q", "k", "wq", "wk", "t", "pos", "dq", "dk", "dwq", "dwk"):
+        assert call(ok, **{name: None}) == 1, name
+    assert call(ok, dq=BASE + 2 * M) == 4             # dq over q
+    assert call(ok, dwq=BASE + 20 * M) == 4           # dw over the workspace
+    assert call(ok, dk=BASE + 8 * M + 1024) == 4      # dk inside dq
+    # slices of one fused gradient interleave, but may not share values
+    w = (8 + 2 + 2) * 128
+    fused = norm_problem(dq_stride=w, dk_stride=w)
+    assert call(fused, dk=BASE + 8 * M + (8 * 128 - 8) * 2) == 4
+    assert call(norm_problem(dq_stride=w, dk_stride=w + 8), dk=BASE + 8 * M + 8 * 128 * 2) == 4
+
+
+def test_paged_refusals():
+    check = lambda **kw: sdpa.sdpa_check_paged(paged_problem(**kw))  # noqa: E731
+    assert check() == 0 and check(head_dim=192, head_dim_v=128) == 0 and check(head_dim=192) == 0
+    assert check(head_dim=512) == 0 and check(mask_type=0) == 0 and check(window_left=0) == 0
+    for bad, code in ((dict(dtype=3), 2), (dict(head_dim=64), 2), (dict(head_dim=128, head_dim_v=64), 2),
+                      (dict(head_dim_v=-1), 1), (dict(batch=-1), 1), (dict(total_q=-1), 1), (dict(seqlen_kv=-1), 1),
+                      (dict(num_heads_q=7), 1), (dict(page_size=0), 1), (dict(page_size=24), 2), (dict(num_pages=0), 1),
+                      (dict(max_pages=62), 1), (dict(table_stride=10), 1), (dict(mask_type=1), 2), (dict(mask_type=3), 1),
+                      (dict(window_left=-2), 1), (dict(mask_type=0, window_left=5), 2), (dict(softmax_scale=-1.0), 1),
+                      (dict(softmax_scale=float("inf")), 1), (dict(k_slot_stride=100), 1), (dict(v_head_stride=132), 1),
+                      (dict(k_page_stride=0), 1), (dict(q_stride=512), 1), (dict(k_stride=260), 1)):
+        assert check(**bad) == code, bad
+
+
+def test_append_refusals():
+    def call(p, n=None, **kw):
+        a = dict(q=BASE, k=BASE + M, v=BASE + 2 * M, wq=BASE + 3 * M, wk=BASE + 4 * M, t=BASE + 5 * M, pos=BASE + 6 * M,
+                 qo=BASE + 7 * M, kc=BASE + 8 * M, vc=BASE + 20 * M, cu=BASE + 30 * M, lens=BASE + 31 * M, tab=BASE + 32 * M)
+        a.update(kw)
+        return sdpa.lib().sdpa_paged_append(ctypes.byref(p), ctypes.byref(n) if n is not None else None,
+                                            *[PTR(x) if x else None for x in a.values()], None)
+
+    ok = paged_problem()
+    assert call(paged_problem(total_q=0)) == 0 and call(paged_problem(batch=0)) == 0
+    assert call(paged_problem(page_size=8)) == 2
+    for name in ("k", "v", "kc", "vc", "cu", "lens", "tab"):
+        assert call(ok, **{name: None}) == 1, name
+    assert call(ok, k=BASE + M + 2) == 3 and call(ok, vc=BASE + 20 * M + 8) == 3
+    assert call(ok, k=BASE + 8 * M + 4096) == 4       # new rows inside the cache
+    assert call(ok, tab=BASE + 20 * M) == 4           # the block table inside the cache
+    n = norm_problem(rotary_dim=24)
+    assert call(ok, n) == 1
+    n = norm_problem()
+    for name in ("q", "wq", "wk", "t", "qo"):
+        assert call(ok, n, **{name: None}) == 1, name
+    assert call(ok, n, qo=BASE + 64) == 4 and call(ok, n, qo=BASE + 8 * M) == 4
+
+
+def test_binding_refuses_what_does_not_fit():
+    bf = torch.bfloat16
+    z = lambda *s, dt=bf: torch.zeros(*s, dtype=dt)  # noqa: E731
+    q, k, w = z(6, 4, 128), z(6, 2, 128), z(128)
+    pos, table = z(6, dt=torch.int32), torch.zeros(50, 128)
+    f = sdpa.sdpa_qk_norm_rope
+    with pytest.raises(ValueError, match="CUDA"):
+        f(q, k, w, w, table, pos)
+    for args in ((q, z(5, 2, 128), w, w, table, pos), (q, z(6, 2, 256), w, w, table, pos), (q, k, z(64), w, table, pos),
+                 (q, k, w, w.float(), table, pos), (q, k, w, w, table.half(), pos), (q, k, w, w, table, pos.long()),
+                 (q, k, w, w, table, pos[:5]), (q, k, w, w, table, None), (q, k.half(), w, w, table, pos),
+                 (q.float(), k.float(), w.float(), w.float(), table, pos), (q.transpose(1, 2), k, w, w, table, pos),
+                 (z(4, 6, 128).transpose(0, 1), k, w, w, table, pos)):
+        with pytest.raises(ValueError):
+            f(*args)
+    kc, vc = z(9, 16, 2, 128), z(9, 16, 2, 128)
+    tab, lens, cu = z(2, 4, dt=torch.int32), z(2, dt=torch.int32), z(3, dt=torch.int32)
+    a = sdpa.sdpa_paged_append
+    good = dict(k=k, v=k, k_cache=kc, v_cache=vc, block_table=tab, kv_lens=lens, cu_seqlens_q=cu)
+    with pytest.raises(ValueError, match="CUDA"):
+        a(**good)
+    for bad in (dict(k=z(6, 3, 128)), dict(v=z(5, 2, 128)), dict(k_cache=z(9, 2, 16, 128)), dict(v_cache=z(9, 16, 2, 256)),
+                dict(block_table=tab.long()), dict(kv_lens=lens[:1]), dict(cu_seqlens_q=cu[:2]), dict(cache_layout="dnh"),
+                dict(q=z(6, 4, 128)), dict(q=z(5, 4, 128), q_weight=w, k_weight=w), dict(cos_sin=table),
+                dict(k_cache=kc.half()), dict(q=q, q_weight=w, k_weight=w, cos_sin=table[:, :64].t())):
+        with pytest.raises(ValueError):
+            a(**{**good, **bad})
+
+
+def test_new_error_has_a_string():
+    assert "table" in sdpa.error_string(10)
