@@ -370,9 +370,10 @@ SDPA_API int sdpa_qk_norm_rope_bwd(const sdpa_norm_rope_problem* p, const void* 
 /* A paged key/value cache and a batch of new tokens over it.
  * Cache: num_pages pages of page_size slots. Slot s, head h of page g of K starts at element
  *   g * k_page_stride + s * k_slot_stride + h * k_head_stride (head_dim contiguous values; V
- *   likewise with head_dim_v). All strides are multiples of 8 elements, so both orders,
- *   [page][slot][head][D] and [page][head][slot][D], and pages that hold K and V together
- *   are served.
+ *   likewise with head_dim_v). All strides are multiples of 8 elements, and of page, slot and
+ *   head stride each is a multiple of the smaller ones: both orders, [page][slot][head][D] and
+ *   [page][head][slot][D] (the same for K and V), and pages that hold K and V together are
+ *   served.
  * Batch: sequence b owns the new tokens cu_seqlens_q[b] .. cu_seqlens_q[b+1]-1 of the packed
  *   [total_q][heads][D] rows (any number, 0 included; rows from cu_seqlens_q[batch] on are
  *   left as they are), and kv_lens[b] cached keys, those of its new tokens last: new token i
@@ -414,7 +415,26 @@ SDPA_API int sdpa_paged_append(const sdpa_paged_problem* p, const sdpa_norm_rope
                                void* v_cache, const int32_t* cu_seqlens_q, const int32_t* kv_lens,
                                const int32_t* block_table, void* stream);
 
+/* Attention of the new tokens over the cache (their own keys and values already in it):
+ *   S = softmax_scale Q K^T, masked; O = softmax(S) V; LSE = ln sum_j exp(S_ij)
+ * for single tokens (decoding), chunks of a prompt, and batches that mix them. q
+ * [total_q][Hq][D]; o [total_q][Hq][Dv] (dtype) and lse float32 [total_q][Hq] are written for
+ * the sequences' rows; a row that sees no key gets o = 0 and lse = -inf. Keys that no
+ * query row of a tile sees (other slots of a page, pages behind a window) may hold anything, NaN
+ * included, in K and V.
+ * workspace: sdpa_paged_fwd_workspace_size bytes, 256-byte aligned; never more than
+ * SDPA_PAGED_WORKSPACE_MAX, so a program may keep one buffer of that size for every shape.
+ * Lengths that do not fit the problem (cu_seqlens_q not from 0 and non-decreasing up to at
+ * most total_q, a q_len or kv_len out of bounds) are recorded as SDPA_ERR_BAD_SEQLENS and
+ * nothing is written. A page number outside [0, num_pages) is recorded as
+ * SDPA_ERR_BAD_INDEX; its keys and values read as zeros and the call's output is
+ * then not meaningful. */
+#define SDPA_PAGED_WORKSPACE_MAX (256u << 20)
 SDPA_API int sdpa_check_paged(const sdpa_paged_problem* p);
+SDPA_API size_t sdpa_paged_fwd_workspace_size(const sdpa_paged_problem* p);
+SDPA_API int sdpa_paged_fwd(const sdpa_paged_problem* p, const void* q, const void* k_cache, const void* v_cache,
+                            void* o, float* lse, const int32_t* cu_seqlens_q, const int32_t* kv_lens,
+                            const int32_t* block_table, void* workspace, size_t ws_bytes, void* stream);
 
 /* Kernel timing for benchmarks and tracing. Between sdpa_profile_begin and
  * sdpa_profile_end, every sdpa_fwd / sdpa_bwd call made by this host thread
@@ -433,9 +453,8 @@ typedef enum {
   SDPA_KERNEL_V_TRANSPOSE = 7, /* FP8 forward: V transposed into the workspace */
   SDPA_KERNEL_NORM_ROPE = 8,   /* per-head norm + rotation, forward or backward */
   SDPA_KERNEL_APPEND = 9,      /* new rows into their pages (with the norm + rotation when fused) */
-  SDPA_KERNEL_PAGED = 10,      /* attention over the paged cache */
-  SDPA_KERNEL_PAGED_JOIN = 11, /* its join of partial results over a split of the keys */
-  SDPA_KERNEL_KINDS = 12
+  SDPA_KERNEL_PAGED = 10,      /* attention over the paged cache, the join of its partial results included */
+  SDPA_KERNEL_KINDS = 11
 } sdpa_kernel_kind;
 SDPA_API int sdpa_profile_begin(void);
 SDPA_API int sdpa_profile_end(double* ms_by_kind, int* launches_by_kind, int n_kinds);

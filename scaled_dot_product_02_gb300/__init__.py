@@ -34,10 +34,12 @@ EXPORTS = ("sdpa_fwd_workspace_size", "sdpa_bwd_workspace_size", "sdpa_check_pro
            "sdpa_profile_end", "sdpa_bwd_noalloc", "sdpa_selftest_bounded_wait", "sdpa_merge",
            "sdpa_fwd_fp8_workspace_size", "sdpa_fwd_fp8", "sdpa_debug_set_max_ctas", "sdpa_debug_address_report",
            "sdpa_debug_address_shrink", "sdpa_qk_norm_rope", "sdpa_qk_norm_rope_bwd_workspace_size",
-           "sdpa_qk_norm_rope_bwd", "sdpa_check_paged", "sdpa_paged_append")
+           "sdpa_qk_norm_rope_bwd", "sdpa_check_paged", "sdpa_paged_append", "sdpa_paged_fwd_workspace_size",
+           "sdpa_paged_fwd")
 NOALLOC_MAX_BYTES = 32 << 20  # SDPA_BWD_NOALLOC_MAX_BYTES
+PAGED_WORKSPACE_MAX = 256 << 20  # SDPA_PAGED_WORKSPACE_MAX
 KERNEL_KINDS = ("fwd", "bwd", "preprocess", "dq_finalize", "guard", "merge", "bwd_dq", "v_transpose",
-                "norm_rope", "append", "paged", "paged_join")
+                "norm_rope", "append", "paged")
 
 
 class SdpaError(RuntimeError):
@@ -122,6 +124,9 @@ def _load(path):
         L.sdpa_qk_norm_rope_bwd.argtypes = [npp] + [vp] * 13 + [ctypes.c_size_t, vp]
         L.sdpa_check_paged.argtypes = [ppp]
         L.sdpa_paged_append.argtypes = [ppp, npp] + [vp] * 14
+        L.sdpa_paged_fwd_workspace_size.argtypes = [ppp]
+        L.sdpa_paged_fwd_workspace_size.restype = ctypes.c_size_t
+        L.sdpa_paged_fwd.argtypes = [ppp] + [vp] * 9 + [ctypes.c_size_t, vp]
         _libs[path] = L
     return _libs[path]
 
@@ -758,6 +763,61 @@ def sdpa_paged_append(k, v, k_cache, v_cache, block_table, kv_lens, cu_seqlens_q
     if rc:
         raise SdpaError(rc, "sdpa_paged_append")
     return q_out
+
+
+def sdpa_paged_fwd_workspace_size(p: PagedProblem) -> int:
+    return int(lib().sdpa_paged_fwd_workspace_size(ctypes.byref(p)))
+
+
+def sdpa_paged_fwd(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens_q, *, max_seqlen_q, max_seqlen_kv=None,
+                   cache_layout="nhd", mask="causal_br", window=(-1, -1), scale=None, out=None, lse=None, workspace=None,
+                   stream=None):
+    """Attention of the new tokens q [T, Hq, D] over a paged cache that holds
+    their keys and values already (sdpa_paged_fwd in include/sdpa.h).
+    k_cache, v_cache: [pages, page_size, Hkv, D] ("nhd") or [pages, Hkv,
+    page_size, D] ("hnd"); block_table int32 [batch, pages per sequence];
+    kv_lens int32 [batch], the new tokens included; cu_seqlens_q int32
+    [batch + 1]. max_seqlen_q, max_seqlen_kv: the most new tokens and the
+    longest kv_len (default: what the block table can hold). mask: "causal_br"
+    or "none"; window = (left, -1 or 0). Returns (o [T, Hq, Dv], lse float32
+    [T, Hq]); rows behind the last sequence are left as they are. A workspace
+    of PAGED_WORKSPACE_MAX bytes serves every shape."""
+    import torch
+
+    rows, hq, d, qs = _rows_of_heads("q", q)
+    if q.dim() != 3:
+        raise ValueError(f"q must be [tokens, heads, head_dim], got {tuple(q.shape)}")
+    p = _paged_problem(q, hq, k_cache, v_cache, block_table, kv_lens, cu_seqlens_q, cache_layout)
+    if p.head_dim != d or hq % p.num_heads_kv:
+        raise ValueError(f"q {tuple(q.shape)} does not fit the cache {tuple(k_cache.shape)} in layout {cache_layout}")
+    if window[1] not in (-1, 0):
+        raise ValueError(f"a paged window is (left, -1 or 0), got {tuple(window)}")
+    p.total_q, p.q_stride = rows, qs
+    p.seqlen_q = max_seqlen_q
+    p.seqlen_kv = p.max_pages * p.page_size if max_seqlen_kv is None else max_seqlen_kv
+    p.mask_type, p.window_left = MASKS[mask], window[0]
+    p.softmax_scale = d ** -0.5 if scale is None else scale
+    _refuse_cpu(q)
+    dev, shape = q.device, (rows, hq, v_cache.shape[3])
+    if out is None:
+        out = torch.empty(shape, dtype=q.dtype, device=dev)
+    else:
+        _expect("out", out, shape, q.dtype, dev)
+    if lse is None:
+        lse = torch.empty(shape[:2], dtype=torch.float32, device=dev)
+    else:
+        _expect("lse", lse, shape[:2], torch.float32, dev)
+    if workspace is None:
+        workspace = torch.empty(max(sdpa_paged_fwd_workspace_size(p), 256), dtype=torch.uint8, device=dev)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+    rc = _on(dev, stream, lambda s: lib().sdpa_paged_fwd(
+        ctypes.byref(p), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(), lse.data_ptr(),
+        cu_seqlens_q.data_ptr(), kv_lens.data_ptr(), block_table.data_ptr(), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), s))
+    if rc:
+        raise SdpaError(rc, "sdpa_paged_fwd")
+    return out, lse
 
 
 def sdpa_selftest_bounded_wait(limit_us: int = 20000, stream=None) -> None:

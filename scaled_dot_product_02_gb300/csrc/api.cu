@@ -10,6 +10,7 @@
 #include <cstddef>
 #include <cstdint>
 #include <algorithm>
+#include <array>
 #include <atomic>
 #include <cstring>
 #include <mutex>
@@ -420,11 +421,78 @@ int check_paged(const sdpa_paged_problem* p) {
                                {p->k_head_stride, d}, {p->v_page_stride, dv}, {p->v_slot_stride, dv},
                                {p->v_head_stride, dv}})
     if (st < wd || st % 8 || st >= (1LL << 36)) return SDPA_ERR_INVALID_ARG;
+  // the order of head and slot is the strides', K's and V's the same, and each stride a multiple of the smaller one
+  // (a dimension of one head has no order)
+  const bool one = p->num_heads_kv == 1;
+  for (const auto& [page, slot, head] :
+       {std::array<long long, 3>{p->k_page_stride, p->k_slot_stride, p->k_head_stride},
+        std::array<long long, 3>{p->v_page_stride, p->v_slot_stride, p->v_head_stride}}) {
+    const long long lo = one ? slot : std::min(slot, head), hi = one ? slot : std::max(slot, head);
+    if ((!one && lo == hi) || hi % lo || (p->num_pages > 1 && page % hi)) return SDPA_ERR_UNSUPPORTED;
+  }
+  if (!one && (p->k_slot_stride < p->k_head_stride) != (p->v_slot_stride < p->v_head_stride)) return SDPA_ERR_UNSUPPORTED;
   for (const auto& [st, wd] : {std::pair<long long, long long>{p->q_stride, (long long)p->num_heads_q * d},
                                {p->k_stride, (long long)p->num_heads_kv * d},
                                {p->v_stride, (long long)p->num_heads_kv * dv}})
     if (st != 0 && (st < wd || st % 8 || st >= (1LL << 32))) return SDPA_ERR_INVALID_ARG;
   return SDPA_OK;
+}
+
+// How the rows of a batch are cut into items (see paged.cu), and the workspace.
+struct PagedPlan {
+  int n;                         // rows of an item: 16, 32 or 64
+  int block_heads, head_blocks;  // heads of a group in an item, items a group takes
+  int tokens;                    // tokens in an item
+  int workers;                   // CTAs, at most kPagedWorkers
+  size_t cuts_off, parts_off, total;
+};
+// The SMs of the device the library is written for: the plan and with it the
+// workspace size must not depend on a device.
+constexpr int kPagedWorkers = 152;
+PagedPlan paged_plan(const sdpa_paged_problem* p) {
+  PagedPlan pl;
+  const int group = p->num_heads_q / p->num_heads_kv, dv = paged_dv(p);
+  const int most = dv == 512 ? 32 : 64;  // a 64-row Q of 512 columns leaves the ring too few stages
+  const long long rows = (long long)group * std::max(p->seqlen_q, 1);
+  pl.n = rows <= 16 ? 16 : (rows <= 32 || most == 32) ? 32 : 64;
+  pl.block_heads = std::min(group, pl.n);
+  pl.head_blocks = (group + pl.block_heads - 1) / pl.block_heads;
+  pl.tokens = std::max(1, std::min(pl.n / pl.block_heads, p->seqlen_q));
+  // the most tiles the batch can have: no more CTAs than that
+  const long long blocks = std::min<long long>(p->total_q, (long long)p->batch * ((p->seqlen_q + pl.tokens - 1) / pl.tokens));
+  long long tiles = (p->seqlen_kv + 127) / 128;
+  if (p->window_left >= 0) tiles = std::min<long long>(tiles, ((long long)p->window_left + pl.tokens) / 128 + 2);
+  const long long units = blocks * p->num_heads_kv * pl.head_blocks;
+  pl.workers = (int)std::max<long long>(1, std::min<long long>(kPagedWorkers, units >= kPagedWorkers ? units : units * std::max(tiles, 1LL)));
+  pl.cuts_off = 256;
+  pl.parts_off = round_up(pl.cuts_off + (size_t)pl.workers * paged_cut_bytes(), 256);
+  pl.total = pl.parts_off + (size_t)pl.workers * 2 * pl.n * (dv + 2) * 4;
+  return pl;
+}
+
+// Whether a slot's heads lie apart by more than its pages' slots ([page][head][slot]);
+// a single head counts as [page][slot][head].
+bool slot_first(const sdpa_paged_problem* p) { return p->num_heads_kv > 1 && p->k_slot_stride < p->k_head_stride; }
+
+// 4-D map of a paged cache {width, then head and slot by increasing stride, page}:
+// boxes are 64 columns (128 bytes, 128-byte swizzle) x box_rows slots of one head of one page.
+int encode_cache(CUtensorMap* m, const void* base, const sdpa_paged_problem* p, int width, long long page, long long slot,
+                 long long head, int box_rows, bool bf16) {
+  auto fn = encode_fn();
+  if (!fn) return SDPA_ERR_CUDA;
+  const bool first = slot_first(p);
+  if (p->num_heads_kv == 1) head = slot;  // strides of single entries are never taken: keep the map's order
+  const long long lo = std::min(slot, head), hi = std::max(slot, head);
+  if (p->num_pages == 1) page = hi;
+  const cuuint64_t dims[4] = {(cuuint64_t)width, (cuuint64_t)(first ? p->page_size : p->num_heads_kv),
+                              (cuuint64_t)(first ? p->num_heads_kv : p->page_size), (cuuint64_t)p->num_pages};
+  const cuuint64_t strides[3] = {(cuuint64_t)lo * 2, (cuuint64_t)hi * 2, (cuuint64_t)page * 2};
+  const cuuint32_t box[4] = {64, (cuuint32_t)(first ? box_rows : 1), (cuuint32_t)(first ? 1 : box_rows), 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult r = fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+                  const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? SDPA_OK : SDPA_ERR_CUDA;
 }
 
 // Bytes from a cache's first element to its last.
@@ -1112,6 +1180,107 @@ int sdpa_paged_append(const sdpa_paged_problem* p, const sdpa_norm_rope_problem*
   rc = timed(SDPA_KERNEL_APPEND, s, [&] { return launch_norm_rope(L, d, p->dtype == SDPA_BF16, true, s); });
   if (rc) return rc;
   t_last_launches = 1;
+  return SDPA_OK;
+}
+
+size_t sdpa_paged_fwd_workspace_size(const sdpa_paged_problem* p) {
+  if (check_paged(p) != SDPA_OK || p->batch == 0 || p->total_q == 0) return 0;
+  return paged_plan(p).total;
+}
+
+int sdpa_paged_fwd(const sdpa_paged_problem* p, const void* q, const void* k_cache, const void* v_cache, void* o,
+                   float* lse, const int32_t* cu_seqlens_q, const int32_t* kv_lens, const int32_t* block_table,
+                   void* workspace, size_t ws_bytes, void* stream) {
+  t_last_launches = 0;
+  int rc = check_paged(p);
+  if (rc) return rc;
+  if (p->batch == 0 || p->total_q == 0) return SDPA_OK;
+  if (!q || !k_cache || !v_cache || !o || !lse || !cu_seqlens_q || !kv_lens || !block_table) return SDPA_ERR_INVALID_ARG;
+  for (const void* ptr : {q, k_cache, v_cache, (const void*)o, (const void*)lse})
+    if (!aligned16(ptr)) return SDPA_ERR_ALIGNMENT;
+  const int d = p->head_dim, dv = paged_dv(p);
+  const long long qw = (long long)p->num_heads_q * d, qs = p->q_stride ? p->q_stride : qw;
+  if (qs % d) return SDPA_ERR_UNSUPPORTED;  // a copy's strides are multiples of one another
+  const PagedPlan pl = paged_plan(p);
+  if (!workspace || ws_bytes < pl.total) return SDPA_ERR_WORKSPACE_TOO_SMALL;
+  if (reinterpret_cast<uintptr_t>(workspace) & 255u) return SDPA_ERR_ALIGNMENT;
+  const long long ts = p->table_stride ? p->table_stride : p->max_pages;
+  const Extent outs[3] = {extent(o, (size_t)p->total_q * p->num_heads_q * dv * 2),
+                          extent(lse, (size_t)p->total_q * p->num_heads_q * 4), extent(workspace, pl.total)};
+  const Extent ins[6] = {extent(q, span(p->total_q, qs, qw)),
+                         extent(k_cache, cache_span(p, p->k_page_stride, p->k_slot_stride, p->k_head_stride, d)),
+                         extent(v_cache, cache_span(p, p->v_page_stride, p->v_slot_stride, p->v_head_stride, dv)),
+                         extent(cu_seqlens_q, 4 * ((size_t)p->batch + 1)), extent(kv_lens, 4 * (size_t)p->batch),
+                         extent(block_table, 4 * (size_t)((p->batch - 1) * ts + p->max_pages))};
+  for (int a = 0; a < 3; ++a) {
+    for (const Extent& in : ins)
+      if (overlaps(outs[a], in)) return SDPA_ERR_OVERLAP;
+    for (int b = a + 1; b < 3; ++b)
+      if (overlaps(outs[a], outs[b])) return SDPA_ERR_OVERLAP;
+  }
+  int* err = error_word();
+  if (!err) return SDPA_ERR_CUDA;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool bf16 = p->dtype == SDPA_BF16;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  PagedLaunch L;
+  std::memset(&L, 0, sizeof(L));
+  PagedParams& P = L.p;
+  P.batch = p->batch;
+  P.total_q = p->total_q;
+  P.max_q = p->seqlen_q;
+  P.max_kv = p->seqlen_kv;
+  P.hq = p->num_heads_q;
+  P.group = p->num_heads_q / p->num_heads_kv;
+  P.block_heads = pl.block_heads;
+  P.head_blocks = pl.head_blocks;
+  P.tokens = pl.tokens;
+  P.units_per_block = p->num_heads_kv * pl.head_blocks;
+  P.q_box_rows = pl.tokens * pl.block_heads;
+  P.causal = p->mask_type != SDPA_MASK_NONE;
+  P.window = p->window_left;
+  P.scale_log2 = p->softmax_scale * 1.4426950408889634f;
+  P.page_size = p->page_size;
+  P.num_pages = p->num_pages;
+  P.box_rows = std::min(p->page_size & -p->page_size, 128);
+  P.slot_first = slot_first(p);
+  P.cu_q = cu_seqlens_q;
+  P.kv_lens = kv_lens;
+  P.block_table = block_table;
+  P.table_stride = ts;
+  P.o = o;
+  P.lse = lse;
+  P.total_tiles = reinterpret_cast<long long*>(ws);
+  P.cuts = reinterpret_cast<PagedCut*>(ws + pl.cuts_off);
+  P.parts = reinterpret_cast<float*>(ws + pl.parts_off);
+  P.err = err;
+  P.chk = bind_extents({outs[0], outs[1], outs[2], ins[0], ins[1], ins[2], ins[3], ins[4], ins[5]}, err, s);
+  if (kAddrCheck && !P.chk) return SDPA_ERR_CUDA;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return SDPA_ERR_CUDA;
+  L.workers = std::min(pl.workers, sms);
+  if (debug_max_ctas() > 0) L.workers = std::min(L.workers, debug_max_ctas());
+  L.stream = s;
+  {
+    auto fn = encode_fn();
+    if (!fn) return SDPA_ERR_CUDA;
+    const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)p->num_heads_q, (cuuint64_t)p->total_q};
+    const cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)qs * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)pl.block_heads, (cuuint32_t)pl.tokens}, estr[3] = {1, 1, 1};
+    if (fn(&L.tmQ, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(q),
+           dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return SDPA_ERR_CUDA;
+  }
+  if ((rc = encode_cache(&L.tmK, k_cache, p, d, p->k_page_stride, p->k_slot_stride, p->k_head_stride, P.box_rows, bf16)))
+    return rc;
+  if ((rc = encode_cache(&L.tmV, v_cache, p, dv, p->v_page_stride, p->v_slot_stride, p->v_head_stride, P.box_rows, bf16)))
+    return rc;
+  int n = 0;
+  if ((rc = timed(SDPA_KERNEL_PAGED, s, [&] { return launch_paged_rows(L, pl.n, d, bf16, &n); }))) return rc;
+  t_last_launches = n;
   return SDPA_OK;
 }
 

@@ -232,6 +232,39 @@ struct NormRopeBwdParams {
 int norm_rope_bwd_blocks(long long rows, int hq, int hkv, int head_dim, int* parts);
 int launch_norm_rope_bwd(const NormRopeBwdParams& p, int head_dim, bool bf16, int* launches, cudaStream_t s);
 
+// Attention over a paged cache (paged.cu).
+struct PagedCut;  // a worker's record for the join, in the workspace
+struct PagedParams {
+  int batch, total_q, max_q, max_kv;
+  int hq, group;               // heads of q, and of q per kv head
+  int block_heads, head_blocks;  // heads of a group in one item, items a group takes
+  int tokens;                  // tokens in one item
+  int units_per_block;         // items of one block of tokens: kv heads x head_blocks
+  int q_box_rows;              // rows the Q copy brings: tokens x block_heads
+  int causal, window;          // window < 0: none
+  float scale_log2;
+  int page_size, num_pages, box_rows;  // box_rows: slots one copy brings (divides page_size and 128)
+  int slot_first;              // cache order [page][head][slot]: slots vary before heads
+  const int32_t *cu_q, *kv_lens, *block_table;
+  long long table_stride;
+  void* o;
+  float* lse;
+  long long* total_tiles;      // workspace: tiles of all items (0: refused)
+  PagedCut* cuts;              // [workers]
+  float* parts;                // [workers][2] partial results
+  int* err;
+  AddrTable* chk;
+};
+struct PagedLaunch {
+  CUtensorMap tmQ, tmK, tmV;
+  PagedParams p;
+  int workers;
+  cudaStream_t stream;
+};
+size_t paged_cut_bytes();
+// n: rows of an item, 16, 32 or 64 (64 not with head_dim 512)
+int launch_paged_rows(const PagedLaunch& L, int n, int head_dim, bool bf16, int* launches);
+
 // Log-sum-exp merge of partial results over a split of the keys (merge.cu).
 int launch_merge(const void* o_parts, const float* lse_parts, void* o, float* lse, long long items, int head_dim,
                  int n_parts, bool bf16, AddrTable* chk, cudaStream_t s);

@@ -88,10 +88,12 @@ def make_pages(rng, lens, page, spare=3, cols=None):
 
 
 def paged_attention(q, kc, vc, table, lens, cu, page, order, causal, window, scale):
-    """(O float64, LSE float64) of the packed rows; rows of no sequence are zero. kc, vc: CPU tensors in `order`."""
+    """(O, LSE, sum p |v| / sum p, largest sum |q| |k| scale of a row), float64, of the packed rows; rows of no
+    sequence are zero. kc, vc: CPU tensors in `order`."""
     q = q.double()
     rows, hq, _ = q.shape
     o, lse = torch.zeros(rows, hq, vc.shape[-1], dtype=torch.float64), torch.zeros(rows, hq, dtype=torch.float64)
+    pv, mag = torch.zeros_like(o), torch.zeros_like(lse)
     if order == "hnd":
         kc, vc = kc.transpose(1, 2), vc.transpose(1, 2)
     hkv = kc.shape[2]
@@ -120,6 +122,11 @@ def paged_attention(q, kc, vc, table, lens, cu, page, order, causal, window, sca
             vv = v[:, h // g]
             # a key that no row of the batch's rows sees may hold anything
             vv = torch.where(torch.from_numpy(seen.any(0))[:, None], vv, torch.zeros_like(vv))
-            o[lo:hi, h] = (p @ vv) / torch.where(t == 0, torch.ones_like(t), t)
+            t1 = torch.where(t == 0, torch.ones_like(t), t)
+            o[lo:hi, h] = (p @ vv) / t1
+            pv[lo:hi, h] = (p @ vv.abs()) / t1
             lse[lo:hi, h] = (m0 + torch.log(t))[:, 0]
-    return o, lse
+            a = q[lo:hi, h].abs() @ k[:, h // g].abs().T * scale
+            a[hidden] = 0
+            mag[lo:hi, h] = a.amax(-1) if n else 0
+    return o, lse, pv, mag

@@ -133,6 +133,49 @@ def test_append_refusals():
     assert call(ok, n, qo=BASE + 64) == 4 and call(ok, n, qo=BASE + 8 * M) == 4
 
 
+def test_paged_fwd_refusals():
+    def call(p, n=None, **kw):
+        a = dict(q=BASE, kc=BASE + M, vc=BASE + 12 * M, o=BASE + 24 * M, lse=BASE + 25 * M, cu=BASE + 26 * M,
+                 lens=BASE + 27 * M, tab=BASE + 28 * M, ws=BASE + 30 * M)
+        a.update(kw)
+        n = sdpa.sdpa_paged_fwd_workspace_size(p) if n is None else n
+        return sdpa.lib().sdpa_paged_fwd(ctypes.byref(p), *[PTR(x) if x else None for x in a.values()], n, None)
+
+    ok = paged_problem()
+    assert call(paged_problem(total_q=0)) == 0 and call(paged_problem(batch=0)) == 0
+    assert call(paged_problem(head_dim=64)) == 2 and call(paged_problem(mask_type=1)) == 2
+    for name in ("q", "kc", "vc", "o", "lse", "cu", "lens", "tab"):
+        assert call(ok, **{name: None}) == 1, name
+    for name, at in (("q", 0), ("kc", 1), ("vc", 12), ("o", 24), ("lse", 25)):
+        assert call(ok, **{name: BASE + at * M + 8}) == 3, name
+    assert call(ok, n=0) == 5 and call(ok, ws=None) == 5 and call(ok, ws=BASE + 30 * M + 16) == 3
+    assert call(ok, n=sdpa.sdpa_paged_fwd_workspace_size(ok) - 1) == 5
+    assert call(ok, o=BASE + M + 4096) == 4 and call(ok, lse=BASE + 24 * M) == 4 and call(ok, o=BASE + 30 * M) == 4
+    assert call(ok, tab=BASE + 30 * M + 256) == 4
+    assert call(paged_problem(q_stride=8 * 128 + 8)) == 2
+    # cache strides that are not multiples of one another, or K and V in different orders
+    assert sdpa.sdpa_check_paged(paged_problem(k_page_stride=16 * 256 + 8)) == 2
+    assert sdpa.sdpa_check_paged(paged_problem(k_slot_stride=264)) == 2
+    assert sdpa.sdpa_check_paged(paged_problem(v_slot_stride=128, v_head_stride=2048)) == 2
+    assert sdpa.sdpa_check_paged(paged_problem(num_heads_kv=1, k_head_stride=8 * 99, v_head_stride=4096)) == 0
+
+
+@pytest.mark.parametrize("d,dv", [(128, 128), (192, 128), (256, 256), (512, 512)])
+def test_the_paged_workspace_is_bounded(d, dv):
+    most = 0
+    for hq, hkv in ((1, 1), (8, 2), (32, 8), (128, 1), (300, 1)):
+        for batch, new, kv in ((1, 1, 1), (1, 1, 1 << 20), (64, 1, 16384), (4096, 8, 1 << 17), (3, 5000, 1 << 17)):
+            p = paged_problem(num_heads_q=hq, num_heads_kv=hkv, head_dim=d, head_dim_v=dv, batch=batch, total_q=batch * new,
+                              seqlen_q=new, seqlen_kv=kv, max_pages=kv // 16 + 1, k_page_stride=16 * hkv * d,
+                              k_slot_stride=hkv * d, k_head_stride=d, v_page_stride=16 * hkv * dv, v_slot_stride=hkv * dv,
+                              v_head_stride=dv)
+            assert sdpa.sdpa_check_paged(p) == 0
+            n = sdpa.sdpa_paged_fwd_workspace_size(p)
+            assert n > 0
+            most = max(most, n)
+    assert most <= sdpa.PAGED_WORKSPACE_MAX
+
+
 def test_binding_refuses_what_does_not_fit():
     bf = torch.bfloat16
     z = lambda *s, dt=bf: torch.zeros(*s, dtype=dt)  # noqa: E731
@@ -160,6 +203,18 @@ def test_binding_refuses_what_does_not_fit():
                 dict(k_cache=kc.half()), dict(q=q, q_weight=w, k_weight=w, cos_sin=table[:, :64].t())):
         with pytest.raises(ValueError):
             a(**{**good, **bad})
+
+
+    a = sdpa.sdpa_paged_fwd
+    good = dict(q=q, k_cache=kc, v_cache=vc, block_table=tab, kv_lens=lens, cu_seqlens_q=cu, max_seqlen_q=6)
+    with pytest.raises(ValueError, match="CUDA"):
+        a(**good)
+    for bad in (dict(q=z(6, 4, 256)), dict(q=z(6, 5, 128)), dict(q=z(1, 6, 4, 128)), dict(window=(4, 3)),
+                dict(kv_lens=lens.long()), dict(k_cache=kc[:5]), dict(block_table=tab[:, ::2]), dict(cache_layout="hnd")):
+        with pytest.raises(ValueError):
+            a(**{**good, **bad})
+    with pytest.raises(KeyError):
+        a(**{**good, "mask": "causal_tl"})
 
 
 def test_new_error_has_a_string():
