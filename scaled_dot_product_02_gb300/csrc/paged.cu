@@ -618,6 +618,12 @@ __global__ void __launch_bounds__(192, 1)
           // keys that none of the item's rows sees have P = 0, but their values
           // may be anything (unused slots): zeros in their place keep 0 x NaN out
           if (kb < w.span.lo || kb + kTile > w.span.hi) {
+            // a stage barrier tells a phase from its neighbour only: what used V's slots before must be done, which
+            // is P V of the tile before (its V) and S^T of the next tile (its K, copied ahead of this tile's V)
+            if (j > 0 && !__all_sync(0xffffffffu, mbar_wait(&bar_o[(sj - 1) & 1], ((sj - 1) >> 1) & 1, abort_flag)))
+              ok = false;
+            if (j + 1 < n && !__all_sync(0xffffffffu, mbar_wait(&bar_s[(sj + 1) & 1], ((sj + 1) >> 1) & 1, abort_flag)))
+              ok = false;
             const int cv = c0 + (j == n - 1 ? n * C::KST + (n - 1) * C::VST : (j + 2) * C::KST + j * C::VST);
             for (int vb = 0; vb < C::VST; ++vb) {
               const int slot = (cv + vb) % C::NST;

@@ -267,6 +267,14 @@ def test_an_empty_batch_and_empty_sequences():
     assert bool((out == 2).all()) and bool((lse == 2).all()) and sdpa.sdpa_get_device_error() == 0
 
 
+@pytest.mark.parametrize("d,page", [(128, 16), (256, 64), (512, 128)])
+@pytest.mark.parametrize("window", [-1, 777])
+def test_many_tiles_and_many_items_per_cta(d, page, window):
+    """Every ring slot is taken again and again before the tile whose unseen values are cleared."""
+    c = case([150, 1, 60, 7], [3001, 2777, 1900, 2050], hq=16, hkv=4, d=d, page=page)
+    check(c, *call(c, window=window), window=window)
+
+
 def test_a_large_batch():
     rng = np.random.default_rng(5)
     total = rng.integers(1, 200, 700)
