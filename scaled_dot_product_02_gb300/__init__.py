@@ -501,33 +501,46 @@ def sdpa_merge(o_parts, lse_parts, *, out=None, lse=None, stream=None):
     return out, lse
 
 # ---------------------------------------------------------------- norms, rotation, paged cache
-_DTYPE_CODE = {}
+_torch_state = {}  # what the calls below take from torch, looked up once
+
+
+def _torch():
+    if not _torch_state:
+        import torch
+
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        _torch_state.update(torch=torch, codes={torch.bfloat16: 0, torch.float16: 1}, f32=torch.float32, i32=torch.int32,
+                            raw=raw or (lambda index: torch.cuda.current_stream(index).cuda_stream))
+    return _torch_state
 
 
 def _dtype_code(t, name):
-    import torch
-
-    if not _DTYPE_CODE:
-        _DTYPE_CODE.update({torch.bfloat16: 0, torch.float16: 1})
-    code = _DTYPE_CODE.get(t.dtype)
+    code = _torch()["codes"].get(t.dtype)
     if code is None:
         raise ValueError(f"{name} must be bfloat16 or float16, got {t.dtype}")
     return code
 
 
-def _on(device, stream, call):
-    """call(raw stream) with `device` current: the C entry points launch on the
-    calling thread's current device, so tensors of another one select theirs
-    for the call. stream: a torch stream of that device, or None for its
-    current one."""
-    import torch
-
-    if stream is not None and stream.device != device:
+def _launch(name, device, stream, *args):
+    """Call the entry point `name` with the stream's raw handle appended and
+    `device` current: it launches on the calling thread's current device, so
+    tensors of another one select theirs for the call. stream: a torch stream
+    of that device, or None for its current one."""
+    torch = _torch_state["torch"]
+    index = device.index
+    if stream is None:
+        raw = _torch_state["raw"](index)
+    elif stream.device != device:
         raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
-    if device.index == torch.cuda.current_device():
-        return call((torch.cuda.current_stream(device) if stream is None else stream).cuda_stream)
-    with torch.cuda.device(device):
-        return call((torch.cuda.current_stream(device) if stream is None else stream).cuda_stream)
+    else:
+        raw = stream.cuda_stream
+    if index == torch.cuda.current_device():
+        rc = getattr(lib(), name)(*args, raw)
+    else:
+        with torch.cuda.device(device):
+            rc = getattr(lib(), name)(*args, raw)
+    if rc:
+        raise SdpaError(rc, name)
 
 
 def _refuse_cpu(t):
@@ -535,53 +548,70 @@ def _refuse_cpu(t):
         raise ValueError("sdpa tensors must be CUDA tensors (there is no CPU implementation)")
 
 
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
 def _rows_of_heads(name, t, like=None):
     """(rows, heads, head_dim, elements between rows) of [..., H, D] whose
     leading dimensions are one evenly spaced row index (contiguous, or a slice
     of a fused projection's output) and whose heads are contiguous."""
+    if like is not None and (t.dtype is not like.dtype or t.device != like.device):
+        raise ValueError(f"{name} must have dtype {like.dtype} on {like.device}, got {t.dtype} on {t.device}")
     shape, st = t.shape, t.stride()
+    if len(shape) == 3:
+        rows, h, d = shape
+        if st[2] == 1 and (st[1] == d or h == 1):
+            return rows, h, d, st[0] if rows > 1 else h * d
     if len(shape) < 3:
         raise ValueError(f"{name} must have at least 3 dimensions [..., heads, head_dim], got {tuple(shape)}")
-    if like is not None and (t.dtype != like.dtype or t.device != like.device):
-        raise ValueError(f"{name} must have dtype {like.dtype} on {like.device}, got {t.dtype} on {t.device}")
     h, d = shape[-2], shape[-1]
-    rows, step, spaced = 1, h * d, st[-1] == 1 and (st[-2] == d or h == 1)
-    found = False
+    rows, step, spaced = 1, 0, st[-1] == 1 and (st[-2] == d or h == 1)
     for n, s in zip(reversed(shape[:-2]), reversed(st[:-2])):
         if n != 1:
-            if not found:
-                step, found = s, True
+            if not step:
+                step = s
             elif s != rows * step:
                 spaced = False
             rows *= n
     if rows and not spaced:
         raise ValueError(f"{name} must hold contiguous heads in evenly spaced rows, got shape {tuple(shape)} and "
                          f"strides {tuple(st)}")
-    return rows, h, d, step if found and rows else h * d
+    return rows, h, d, step if step and rows else h * d
 
 
 def _expect(name, t, shape, dtype, device):
-    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
+    if t.dtype is not dtype or t.device != device or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, got "
                          f"{t.dtype} {tuple(t.shape)} on {t.device}")
 
 
-def _norm_rope_args(p, q, d, q_weight, k_weight, cos_sin, positions, eps, interleaved, rows):
-    """Fill p's rotation fields and check the weights, the table and the positions."""
-    import torch
-
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        _expect(name, w, (d,), q.dtype, q.device)
-    p.eps, p.interleaved = eps, 1 if interleaved else 0
+def _rotation(q, d, rows, q_weight, k_weight, cos_sin, positions, needs_positions):
+    """(max_positions, rotary_dim) of the table; checks the weights, the table and the positions."""
+    dtype, dev, T = q.dtype, q.device, _torch()
+    _expect("q_weight", q_weight, (d,), dtype, dev)
+    _expect("k_weight", k_weight, (d,), dtype, dev)
     if cos_sin is None:
-        p.rotary_dim = p.max_positions = 0
-        return
-    if cos_sin.dim() != 2 or cos_sin.dtype != torch.float32 or cos_sin.device != q.device or not cos_sin.is_contiguous():
-        raise ValueError(f"cos_sin must be a contiguous float32 [positions, rotary_dim] tensor on {q.device}")
-    p.max_positions, p.rotary_dim = cos_sin.shape
-    if positions is not None and (positions.dtype != torch.int32 or positions.device != q.device or
-                                  positions.numel() != rows or not positions.is_contiguous()):
-        raise ValueError(f"positions must be a contiguous int32 tensor of one entry per token ({rows}) on {q.device}")
+        return 0, 0
+    if cos_sin.dtype is not T["f32"] or cos_sin.dim() != 2 or cos_sin.device != dev or not cos_sin.is_contiguous():
+        raise ValueError(f"cos_sin must be a contiguous float32 [positions, rotary_dim] tensor on {dev}")
+    if positions is not None:
+        if positions.dtype is not T["i32"] or positions.numel() != rows or positions.device != dev or \
+                not positions.is_contiguous():
+            raise ValueError(f"positions must be a contiguous int32 tensor of one entry per token ({rows}) on {dev}")
+    elif needs_positions and cos_sin.shape[1]:
+        raise ValueError("a rotation needs the tokens' positions")
+    return cos_sin.shape
+
+
+def _norm_rope_problem(q, k, q_weight, k_weight, cos_sin, positions, eps, interleaved, dq_stride=0, dk_stride=0):
+    rows, hq, d, qs = _rows_of_heads("q", q)
+    rows_k, hkv, dk, ks = _rows_of_heads("k", k, q)
+    if dk != d or rows_k != rows or (q.dim() > 3 and q.shape[:-2] != k.shape[:-2]) or q.dim() != k.dim():
+        raise ValueError(f"q and k must agree on every dimension but the heads, got {tuple(q.shape)} and {tuple(k.shape)}")
+    max_pos, rot = _rotation(q, d, rows, q_weight, k_weight, cos_sin, positions, True)
+    return NormRopeProblem(_dtype_code(q, "q"), hq, hkv, d, rot, 1 if interleaved else 0, eps, max_pos, rows, qs, ks,
+                           dq_stride, dk_stride)
 
 
 def sdpa_qk_norm_rope(q, k, q_weight, k_weight, cos_sin=None, positions=None, *, eps=1e-6, interleaved=False, q_out=None,
@@ -593,32 +623,19 @@ def sdpa_qk_norm_rope(q, k, q_weight, k_weight, cos_sin=None, positions=None, *,
     cos_sin: float32 [positions, rotary_dim], half cosines and half sines, or
     None for the norm alone; positions: int32, one per token. Returns
     contiguous (q_out, k_out)."""
-    import torch
-
-    rows, hq, d, qs = _rows_of_heads("q", q)
-    rows_k, hkv, dk, ks = _rows_of_heads("k", k, q)
-    if dk != d or q.shape[:-2] != k.shape[:-2]:
-        raise ValueError(f"q and k must agree on every dimension but the heads, got {tuple(q.shape)} and {tuple(k.shape)}")
-    p = NormRopeProblem(_dtype_code(q, "q"), hq, hkv, d)
-    p.rows, p.q_stride, p.k_stride = rows, qs, ks
-    _norm_rope_args(p, q, d, q_weight, k_weight, cos_sin, positions, eps, interleaved, rows)
-    if p.rotary_dim and positions is None:
-        raise ValueError("a rotation needs the tokens' positions")
+    p = _norm_rope_problem(q, k, q_weight, k_weight, cos_sin, positions, eps, interleaved)
     _refuse_cpu(q)
+    dev = q.device
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        q_out = q.new_empty(q.shape)
     else:
-        _expect("q_out", q_out, q.shape, q.dtype, q.device)
+        _expect("q_out", q_out, q.shape, q.dtype, dev)
     if k_out is None:
-        k_out = torch.empty(k.shape, dtype=q.dtype, device=q.device)
+        k_out = q.new_empty(k.shape)
     else:
-        _expect("k_out", k_out, k.shape, q.dtype, q.device)
-    rc = _on(q.device, stream, lambda s: lib().sdpa_qk_norm_rope(
-        ctypes.byref(p), q.data_ptr(), k.data_ptr(), q_weight.data_ptr(), k_weight.data_ptr(),
-        None if cos_sin is None else cos_sin.data_ptr(), None if positions is None else positions.data_ptr(),
-        q_out.data_ptr(), k_out.data_ptr(), s))
-    if rc:
-        raise SdpaError(rc, "sdpa_qk_norm_rope")
+        _expect("k_out", k_out, k.shape, q.dtype, dev)
+    _launch("sdpa_qk_norm_rope", dev, stream, ctypes.byref(p), q.data_ptr(), k.data_ptr(), q_weight.data_ptr(),
+            k_weight.data_ptr(), _addr(cos_sin), _addr(positions), q_out.data_ptr(), k_out.data_ptr())
     return q_out, k_out
 
 
@@ -629,87 +646,71 @@ def sdpa_qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, cos_sin=None
     outputs and its inputs, returns (dq, dk, dq_weight, dk_weight), the weights'
     in float32. dq and dk may be slices of one fused gradient's rows. Bitwise
     reproducible."""
-    import torch
-
-    rows, hq, d, qs = _rows_of_heads("q", q)
-    rows_k, hkv, d_k, ks = _rows_of_heads("k", k, q)
-    if d_k != d or q.shape[:-2] != k.shape[:-2]:
-        raise ValueError(f"q and k must agree on every dimension but the heads, got {tuple(q.shape)} and {tuple(k.shape)}")
-    p = NormRopeProblem(_dtype_code(q, "q"), hq, hkv, d)
-    p.rows, p.q_stride, p.k_stride = rows, qs, ks
-    _norm_rope_args(p, q, d, q_weight, k_weight, cos_sin, positions, eps, interleaved, rows)
-    if p.rotary_dim and positions is None:
-        raise ValueError("a rotation needs the tokens' positions")
-    _refuse_cpu(q)
-    _expect("dq_out", dq_out, q.shape, q.dtype, q.device)
-    _expect("dk_out", dk_out, k.shape, q.dtype, q.device)
+    strides = []
     for name, t, like in (("dq", dq, q), ("dk", dk, k)):
         if t is not None and t.shape != like.shape:
             raise ValueError(f"{name} must have shape {tuple(like.shape)}, got {tuple(t.shape)}")
-    dq = torch.empty(q.shape, dtype=q.dtype, device=q.device) if dq is None else dq
-    dk = torch.empty(k.shape, dtype=q.dtype, device=q.device) if dk is None else dk
-    p.dq_stride, p.dk_stride = _rows_of_heads("dq", dq, q)[3], _rows_of_heads("dk", dk, q)[3]
-    grads = []
-    for name, t in (("dq_weight", dq_weight), ("dk_weight", dk_weight)):
-        if t is None:
-            t = torch.empty(d, dtype=torch.float32, device=q.device)
-        else:
-            _expect(name, t, (d,), torch.float32, q.device)
-        grads.append(t)
-    need = int(lib().sdpa_qk_norm_rope_bwd_workspace_size(ctypes.byref(p)))
+        strides.append(0 if t is None else _rows_of_heads(name, t, q)[3])
+    p = _norm_rope_problem(q, k, q_weight, k_weight, cos_sin, positions, eps, interleaved, *strides)
+    _refuse_cpu(q)
+    dtype, dev, f32 = q.dtype, q.device, _torch()["f32"]
+    _expect("dq_out", dq_out, q.shape, dtype, dev)
+    _expect("dk_out", dk_out, k.shape, dtype, dev)
+    dq = q.new_empty(q.shape) if dq is None else dq
+    dk = q.new_empty(k.shape) if dk is None else dk
+    d = p.head_dim
+    if dq_weight is None:
+        dq_weight = q.new_empty(d, dtype=f32)
+    else:
+        _expect("dq_weight", dq_weight, (d,), f32, dev)
+    if dk_weight is None:
+        dk_weight = q.new_empty(d, dtype=f32)
+    else:
+        _expect("dk_weight", dk_weight, (d,), f32, dev)
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
-    elif workspace.device != q.device or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous tensor on {q.device}")
-    rc = _on(q.device, stream, lambda s: lib().sdpa_qk_norm_rope_bwd(
-        ctypes.byref(p), dq_out.data_ptr(), dk_out.data_ptr(), q.data_ptr(), k.data_ptr(), q_weight.data_ptr(),
-        k_weight.data_ptr(), None if cos_sin is None else cos_sin.data_ptr(),
-        None if positions is None else positions.data_ptr(), dq.data_ptr(), dk.data_ptr(), grads[0].data_ptr(),
-        grads[1].data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(), s))
-    if rc:
-        raise SdpaError(rc, "sdpa_qk_norm_rope_bwd")
-    return dq, dk, grads[0], grads[1]
+        need = int(lib().sdpa_qk_norm_rope_bwd_workspace_size(ctypes.byref(p)))
+        workspace = dq_weight.new_empty(max(need // 4, 4))
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+    _launch("sdpa_qk_norm_rope_bwd", dev, stream, ctypes.byref(p), dq_out.data_ptr(), dk_out.data_ptr(), q.data_ptr(),
+            k.data_ptr(), q_weight.data_ptr(), k_weight.data_ptr(), _addr(cos_sin), _addr(positions), dq.data_ptr(),
+            dk.data_ptr(), dq_weight.data_ptr(), dk_weight.data_ptr(), workspace.data_ptr(), workspace.nbytes)
+    return dq, dk, dq_weight, dk_weight
 
 
 CACHE_LAYOUTS = ("nhd", "hnd")  # [pages, page_size, Hkv, D] and [pages, Hkv, page_size, D]
 
 
-def _paged_problem(q_like, hq, k_cache, v_cache, block_table, kv_lens, cu_seqlens_q, cache_layout) -> PagedProblem:
-    """The cache's and the batch's part of an sdpa_paged_problem, checked from
-    the tensors' metadata (no device access). Cache strides are free but for
-    contiguous head_dim, so a cache may be a slice of a larger tensor."""
-    import torch
-
+def _paged_problem(q, hq, k_cache, v_cache, block_table, kv_lens, cu_seqlens_q, cache_layout, total_q, seqlen_q, seqlen_kv,
+                   mask_type, window_left, scale, q_stride, k_stride, v_stride) -> PagedProblem:
+    """sdpa_paged_problem of a batch over a cache, checked from the tensors'
+    metadata (no device access). Cache strides are free but for contiguous
+    head_dim, so a cache may be a slice of a larger tensor."""
     if cache_layout not in CACHE_LAYOUTS:
         raise ValueError(f"cache_layout must be one of {CACHE_LAYOUTS}, got {cache_layout!r}")
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        if t.dim() != 4 or t.dtype != q_like.dtype or t.device != q_like.device or t.stride(3) != 1:
-            raise ValueError(f"{name} must be a 4-dimensional {q_like.dtype} tensor on {q_like.device} with contiguous "
-                             f"head_dim, got {t.dtype} {tuple(t.shape)} on {t.device}")
-    ks, vs = k_cache.shape, v_cache.shape
-    if ks[:3] != vs[:3]:
+    dtype, dev, i32 = q.dtype, q.device, _torch()["i32"]
+    ks, vs, k_st, v_st = k_cache.shape, v_cache.shape, k_cache.stride(), v_cache.stride()
+    for name, t, st in (("k_cache", k_cache, k_st), ("v_cache", v_cache, v_st)):
+        if len(st) != 4 or t.dtype is not dtype or t.device != dev or st[3] != 1:
+            raise ValueError(f"{name} must be a 4-dimensional {dtype} tensor on {dev} with contiguous head_dim, got "
+                             f"{t.dtype} {tuple(t.shape)} on {t.device}")
+    pages, a, b, d = ks
+    if vs[0] != pages or vs[1] != a or vs[2] != b:
         raise ValueError(f"k_cache and v_cache must agree on every dimension but the last, got {tuple(ks)} and {tuple(vs)}")
-    dev = q_like.device
-    if block_table.dim() != 2 or block_table.dtype != torch.int32 or block_table.device != dev or \
-            (block_table.shape[1] > 1 and block_table.stride(1) != 1):
+    tab, tab_st = block_table.shape, block_table.stride()
+    if len(tab) != 2 or block_table.dtype is not i32 or block_table.device != dev or (tab[1] > 1 and tab_st[1] != 1):
         raise ValueError(f"block_table must be a 2-D int32 [batch, pages] tensor on {dev} with contiguous rows")
-    batch, max_pages = block_table.shape
-    if kv_lens.dtype != torch.int32 or kv_lens.shape != (batch,) or kv_lens.device != dev or not kv_lens.is_contiguous():
-        raise ValueError(f"kv_lens must be a contiguous int32 tensor of {batch} entries on {dev}")
-    if cu_seqlens_q.dtype != torch.int32 or cu_seqlens_q.shape != (batch + 1,) or cu_seqlens_q.device != dev or \
-            not cu_seqlens_q.is_contiguous():
-        raise ValueError(f"cu_seqlens_q must be a contiguous int32 tensor of {batch + 1} entries on {dev}")
+    batch, max_pages = tab
+    _expect("kv_lens", kv_lens, (batch,), i32, dev)
+    _expect("cu_seqlens_q", cu_seqlens_q, (batch + 1,), i32, dev)
     slot, head = (1, 2) if cache_layout == "nhd" else (2, 1)
-    k_st, v_st = k_cache.stride(), v_cache.stride()
-    p = PagedProblem(_dtype_code(q_like, "q"), batch, hq, ks[head], ks[3], vs[3])
-    p.page_size, p.num_pages, p.max_pages = ks[slot], ks[0], max_pages
-    p.table_stride = block_table.stride(0) if batch > 1 else 0
+    hkv, dv = ks[head], vs[3]
     # a dimension of one entry may carry any stride: its own row's width stands for it
-    p.k_page_stride = k_st[0] if ks[0] > 1 else ks[3]
-    p.k_slot_stride, p.k_head_stride = k_st[slot], k_st[head] if ks[head] > 1 else ks[3]
-    p.v_page_stride = v_st[0] if vs[0] > 1 else vs[3]
-    p.v_slot_stride, p.v_head_stride = v_st[slot], v_st[head] if vs[head] > 1 else vs[3]
-    return p
+    return PagedProblem(_dtype_code(q, "q"), batch, hq, hkv, d, dv, total_q, seqlen_q,
+                        max_pages * ks[slot] if seqlen_kv is None else seqlen_kv, ks[slot], pages, max_pages, mask_type,
+                        window_left, scale, tab_st[0] if batch > 1 else 0, k_st[0] if pages > 1 else d, k_st[slot],
+                        k_st[head] if hkv > 1 else d, v_st[0] if pages > 1 else dv, v_st[slot],
+                        v_st[head] if hkv > 1 else dv, q_stride, k_stride, v_stride)
 
 
 def sdpa_check_paged(p: PagedProblem) -> int:
@@ -725,8 +726,6 @@ def sdpa_paged_append(k, v, k_cache, v_cache, block_table, kv_lens, cu_seqlens_q
     normed and rotated on its way into the cache and q into q_out, as by
     sdpa_qk_norm_rope; positions default to the cache positions. Returns q_out
     (None without q). k, v and q may be slices of one projection's output."""
-    import torch
-
     rows, hkv, d, ks = _rows_of_heads("k", k)
     rows_v, hkv_v, dv, vs = _rows_of_heads("v", v, k)
     if k.dim() != 3 or v.dim() != 3 or rows != rows_v or hkv != hkv_v:
@@ -739,29 +738,25 @@ def sdpa_paged_append(k, v, k_cache, v_cache, block_table, kv_lens, cu_seqlens_q
             raise ValueError(f"q must be [tokens, heads, head_dim] of k's tokens and head_dim, got {tuple(q.shape)}")
         if q_weight is None or k_weight is None:
             raise ValueError("q needs q_weight and k_weight")
-    elif any(x is not None for x in (q_weight, k_weight, cos_sin, positions, q_out)):
+        max_pos, rot = _rotation(q, d, rows, q_weight, k_weight, cos_sin, positions, False)
+        n = ctypes.byref(NormRopeProblem(0, 0, 0, 0, rot, 1 if interleaved else 0, eps, max_pos))
+    elif not (q_weight is k_weight is cos_sin is positions is q_out is None):
         raise ValueError("weights, cos_sin, positions and q_out go with q")
-    p = _paged_problem(k, hq, k_cache, v_cache, block_table, kv_lens, cu_seqlens_q, cache_layout)
+    p = _paged_problem(k, hq, k_cache, v_cache, block_table, kv_lens, cu_seqlens_q, cache_layout, rows, 0, 0,
+                       MASKS["none"], -1, 0.0, qs, ks, vs)
     if p.num_heads_kv != hkv or p.head_dim != d or p.head_dim_v != dv:
         raise ValueError(f"k and v {tuple(k.shape)}, {tuple(v.shape)} do not fit the caches {tuple(k_cache.shape)}, "
                          f"{tuple(v_cache.shape)} in layout {cache_layout}")
-    p.total_q, p.window_left = rows, -1
-    p.q_stride, p.k_stride, p.v_stride = qs, ks, vs
     _refuse_cpu(k)
+    dev = k.device
     if q is not None:
-        n = NormRopeProblem()
-        _norm_rope_args(n, q, d, q_weight, k_weight, cos_sin, positions, eps, interleaved, rows)
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            q_out = q.new_empty(q.shape)
         else:
-            _expect("q_out", q_out, q.shape, q.dtype, q.device)
-    ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
-    rc = _on(k.device, stream, lambda s: lib().sdpa_paged_append(
-        ctypes.byref(p), None if n is None else ctypes.byref(n), ptr(q), k.data_ptr(), v.data_ptr(), ptr(q_weight),
-        ptr(k_weight), ptr(cos_sin), ptr(positions), ptr(q_out), k_cache.data_ptr(), v_cache.data_ptr(),
-        cu_seqlens_q.data_ptr(), kv_lens.data_ptr(), block_table.data_ptr(), s))
-    if rc:
-        raise SdpaError(rc, "sdpa_paged_append")
+            _expect("q_out", q_out, q.shape, q.dtype, dev)
+    _launch("sdpa_paged_append", dev, stream, ctypes.byref(p), n, _addr(q), k.data_ptr(), v.data_ptr(), _addr(q_weight),
+            _addr(k_weight), _addr(cos_sin), _addr(positions), _addr(q_out), k_cache.data_ptr(), v_cache.data_ptr(),
+            cu_seqlens_q.data_ptr(), kv_lens.data_ptr(), block_table.data_ptr())
     return q_out
 
 
@@ -782,41 +777,32 @@ def sdpa_paged_fwd(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens_q, *, m
     or "none"; window = (left, -1 or 0). Returns (o [T, Hq, Dv], lse float32
     [T, Hq]); rows behind the last sequence are left as they are. A workspace
     of PAGED_WORKSPACE_MAX bytes serves every shape."""
-    import torch
-
     rows, hq, d, qs = _rows_of_heads("q", q)
     if q.dim() != 3:
         raise ValueError(f"q must be [tokens, heads, head_dim], got {tuple(q.shape)}")
-    p = _paged_problem(q, hq, k_cache, v_cache, block_table, kv_lens, cu_seqlens_q, cache_layout)
-    if p.head_dim != d or hq % p.num_heads_kv:
-        raise ValueError(f"q {tuple(q.shape)} does not fit the cache {tuple(k_cache.shape)} in layout {cache_layout}")
     if window[1] not in (-1, 0):
         raise ValueError(f"a paged window is (left, -1 or 0), got {tuple(window)}")
-    p.total_q, p.q_stride = rows, qs
-    p.seqlen_q = max_seqlen_q
-    p.seqlen_kv = p.max_pages * p.page_size if max_seqlen_kv is None else max_seqlen_kv
-    p.mask_type, p.window_left = MASKS[mask], window[0]
-    p.softmax_scale = d ** -0.5 if scale is None else scale
+    p = _paged_problem(q, hq, k_cache, v_cache, block_table, kv_lens, cu_seqlens_q, cache_layout, rows, max_seqlen_q,
+                       max_seqlen_kv, MASKS[mask], window[0], d ** -0.5 if scale is None else scale, qs, 0, 0)
+    if p.head_dim != d or hq % p.num_heads_kv:
+        raise ValueError(f"q {tuple(q.shape)} does not fit the cache {tuple(k_cache.shape)} in layout {cache_layout}")
     _refuse_cpu(q)
-    dev, shape = q.device, (rows, hq, v_cache.shape[3])
+    dev, dv, f32 = q.device, p.head_dim_v, _torch()["f32"]
     if out is None:
-        out = torch.empty(shape, dtype=q.dtype, device=dev)
+        out = q.new_empty((rows, hq, dv))
     else:
-        _expect("out", out, shape, q.dtype, dev)
+        _expect("out", out, (rows, hq, dv), q.dtype, dev)
     if lse is None:
-        lse = torch.empty(shape[:2], dtype=torch.float32, device=dev)
+        lse = q.new_empty((rows, hq), dtype=f32)
     else:
-        _expect("lse", lse, shape[:2], torch.float32, dev)
+        _expect("lse", lse, (rows, hq), f32, dev)
     if workspace is None:
-        workspace = torch.empty(max(sdpa_paged_fwd_workspace_size(p), 256), dtype=torch.uint8, device=dev)
+        workspace = lse.new_empty(max(sdpa_paged_fwd_workspace_size(p) // 4, 64))
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {dev}")
-    rc = _on(dev, stream, lambda s: lib().sdpa_paged_fwd(
-        ctypes.byref(p), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(), lse.data_ptr(),
-        cu_seqlens_q.data_ptr(), kv_lens.data_ptr(), block_table.data_ptr(), workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), s))
-    if rc:
-        raise SdpaError(rc, "sdpa_paged_fwd")
+    _launch("sdpa_paged_fwd", dev, stream, ctypes.byref(p), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+            out.data_ptr(), lse.data_ptr(), cu_seqlens_q.data_ptr(), kv_lens.data_ptr(), block_table.data_ptr(),
+            workspace.data_ptr(), workspace.nbytes)
     return out, lse
 
 

@@ -438,35 +438,77 @@ int check_paged(const sdpa_paged_problem* p) {
   return SDPA_OK;
 }
 
-// How the rows of a batch are cut into items (see paged.cu), and the workspace.
-struct PagedPlan {
-  int n;                         // rows of an item: 16, 32 or 64
+// One launch of the paged attention: how it cuts a sequence's rows into items.
+struct PagedCutting {
+  bool used;
+  int n;                         // rows of an item
   int block_heads, head_blocks;  // heads of a group in an item, items a group takes
   int tokens;                    // tokens in an item
-  int workers;                   // CTAs, at most kPagedWorkers
-  size_t cuts_off, parts_off, total;
+  int dv_item, dv_splits;        // value columns an item accumulates, items that share a row
+  bool split;                    // items may be split over workers
+  int workers;                   // CTAs (at most one per SM)
 };
-// The SMs of the device the library is written for: the plan and with it the
-// workspace size must not depend on a device.
+struct PagedPlan {
+  int small_q;         // sequences of at most this many new tokens go to the rows kernel, longer ones to the chunk kernel
+  PagedCutting rows, chunk;
+  size_t cuts_off, parts_off, total;  // the launches run in turn and share the workspace
+};
+// The SMs of the device the library is written for: the plan, and with it the
+// workspace size, must not depend on the device in use.
 constexpr int kPagedWorkers = 152;
+
+PagedCutting paged_cutting(const sdpa_paged_problem* p, int n, int max_q, int dv_item) {
+  PagedCutting c;
+  const int group = p->num_heads_q / p->num_heads_kv, dv = paged_dv(p);
+  c.used = true;
+  c.n = n;
+  c.block_heads = std::min(group, n);
+  c.head_blocks = (group + c.block_heads - 1) / c.block_heads;
+  c.tokens = std::max(1, std::min(n / c.block_heads, max_q));
+  c.dv_item = dv_item;
+  c.dv_splits = dv / dv_item;
+  // the most items the batch can have, and the most key tiles one of them sees
+  const long long blocks = std::min((long long)p->batch * ((max_q + c.tokens - 1) / c.tokens),
+                                    (long long)p->total_q / c.tokens + p->batch);
+  const long long items = blocks * p->num_heads_kv * c.head_blocks * c.dv_splits;
+  long long tiles = (p->seqlen_kv + 127) / 128;
+  if (p->window_left >= 0) tiles = std::min<long long>(tiles, ((long long)p->window_left + c.tokens) / 128 + 2);
+  if (n <= 64) {
+    // short items are not worth the join (and its launch)
+    c.split = tiles > 4;
+  } else {
+    // with items enough the ticket order, which keeps the CTAs on the same keys; else equal shares
+    c.split = tiles > 1 && items < 4 * kPagedWorkers;
+    if (!c.split && (long long)p->batch * ((max_q + c.tokens - 1) / c.tokens) * (items / blocks) > 0x7fff0000LL) c.split = true;
+  }
+  const long long pieces = c.split && items < kPagedWorkers ? items * std::max(tiles, 1LL) : items;
+  c.workers = (int)std::max(1LL, std::min<long long>(kPagedWorkers, pieces));
+  return c;
+}
+
 PagedPlan paged_plan(const sdpa_paged_problem* p) {
   PagedPlan pl;
   const int group = p->num_heads_q / p->num_heads_kv, dv = paged_dv(p);
-  const int most = dv == 512 ? 32 : 64;  // a 64-row Q of 512 columns leaves the ring too few stages
-  const long long rows = (long long)group * std::max(p->seqlen_q, 1);
-  pl.n = rows <= 16 ? 16 : (rows <= 32 || most == 32) ? 32 : 64;
-  pl.block_heads = std::min(group, pl.n);
-  pl.head_blocks = (group + pl.block_heads - 1) / pl.block_heads;
-  pl.tokens = std::max(1, std::min(pl.n / pl.block_heads, p->seqlen_q));
-  // the most tiles the batch can have: no more CTAs than that
-  const long long blocks = std::min<long long>(p->total_q, (long long)p->batch * ((p->seqlen_q + pl.tokens - 1) / pl.tokens));
-  long long tiles = (p->seqlen_kv + 127) / 128;
-  if (p->window_left >= 0) tiles = std::min<long long>(tiles, ((long long)p->window_left + pl.tokens) / 128 + 2);
-  const long long units = blocks * p->num_heads_kv * pl.head_blocks;
-  pl.workers = (int)std::max<long long>(1, std::min<long long>(kPagedWorkers, units >= kPagedWorkers ? units : units * std::max(tiles, 1LL)));
+  const int most = dv == 512 ? 32 : 64;  // rows of the rows kernel: a 64-row Q of 512 columns leaves the ring too few stages
+  const int few = std::max(1, most / group);
+  pl.rows.used = pl.chunk.used = false;
+  pl.small_q = p->seqlen_q <= few ? p->seqlen_q : p->batch == 1 ? -1 : few;  // one sequence: one launch
+  if (pl.small_q >= 0) {
+    const int max_q = std::min(p->seqlen_q, pl.small_q);
+    const long long rows = (long long)group * std::max(max_q, 1);
+    pl.rows = paged_cutting(p, rows <= 16 ? 16 : (rows <= 32 || most == 32) ? 32 : 64, max_q, dv);
+  }
+  if (p->seqlen_q > pl.small_q) pl.chunk = paged_cutting(p, 128, p->seqlen_q, std::min(dv, 256));
   pl.cuts_off = 256;
-  pl.parts_off = round_up(pl.cuts_off + (size_t)pl.workers * paged_cut_bytes(), 256);
-  pl.total = pl.parts_off + (size_t)pl.workers * 2 * pl.n * (dv + 2) * 4;
+  int workers = 0;
+  size_t parts = 0;
+  for (const PagedCutting* c : {&pl.rows, &pl.chunk})
+    if (c->used) {
+      workers = std::max(workers, c->workers);
+      if (c->split) parts = std::max(parts, (size_t)c->workers * 2 * c->n * (c->dv_item + 2) * 4);
+    }
+  pl.parts_off = round_up(pl.cuts_off + (size_t)workers * paged_cut_bytes(), 256);
+  pl.total = pl.parts_off + parts;
   return pl;
 }
 
@@ -1220,67 +1262,81 @@ int sdpa_paged_fwd(const sdpa_paged_problem* p, const void* q, const void* k_cac
   }
   int* err = error_word();
   if (!err) return SDPA_ERR_CUDA;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const bool bf16 = p->dtype == SDPA_BF16;
-  uint8_t* ws = static_cast<uint8_t*>(workspace);
-  PagedLaunch L;
-  std::memset(&L, 0, sizeof(L));
-  PagedParams& P = L.p;
-  P.batch = p->batch;
-  P.total_q = p->total_q;
-  P.max_q = p->seqlen_q;
-  P.max_kv = p->seqlen_kv;
-  P.hq = p->num_heads_q;
-  P.group = p->num_heads_q / p->num_heads_kv;
-  P.block_heads = pl.block_heads;
-  P.head_blocks = pl.head_blocks;
-  P.tokens = pl.tokens;
-  P.units_per_block = p->num_heads_kv * pl.head_blocks;
-  P.q_box_rows = pl.tokens * pl.block_heads;
-  P.causal = p->mask_type != SDPA_MASK_NONE;
-  P.window = p->window_left;
-  P.scale_log2 = p->softmax_scale * 1.4426950408889634f;
-  P.page_size = p->page_size;
-  P.num_pages = p->num_pages;
-  P.box_rows = std::min(p->page_size & -p->page_size, 128);
-  P.slot_first = slot_first(p);
-  P.cu_q = cu_seqlens_q;
-  P.kv_lens = kv_lens;
-  P.block_table = block_table;
-  P.table_stride = ts;
-  P.o = o;
-  P.lse = lse;
-  P.total_tiles = reinterpret_cast<long long*>(ws);
-  P.cuts = reinterpret_cast<PagedCut*>(ws + pl.cuts_off);
-  P.parts = reinterpret_cast<float*>(ws + pl.parts_off);
-  P.err = err;
-  P.chk = bind_extents({outs[0], outs[1], outs[2], ins[0], ins[1], ins[2], ins[3], ins[4], ins[5]}, err, s);
-  if (kAddrCheck && !P.chk) return SDPA_ERR_CUDA;
+  auto encode_map = encode_fn();
+  if (!encode_map) return SDPA_ERR_CUDA;
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return SDPA_ERR_CUDA;
-  L.workers = std::min(pl.workers, sms);
-  if (debug_max_ctas() > 0) L.workers = std::min(L.workers, debug_max_ctas());
-  L.stream = s;
-  {
-    auto fn = encode_fn();
-    if (!fn) return SDPA_ERR_CUDA;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool bf16 = p->dtype == SDPA_BF16;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  AddrTable* chk = bind_extents({outs[0], outs[1], outs[2], ins[0], ins[1], ins[2], ins[3], ins[4], ins[5]}, err, s);
+  if (kAddrCheck && !chk) return SDPA_ERR_CUDA;
+  int launches = 0;
+  for (const PagedCutting* c : {&pl.rows, &pl.chunk}) {
+    if (!c->used) continue;
+    const bool small = c == &pl.rows;
+    PagedLaunch L;
+    std::memset(&L, 0, sizeof(L));
+    PagedParams& P = L.p;
+    P.batch = p->batch;
+    P.total_q = p->total_q;
+    P.max_q = p->seqlen_q;
+    P.max_kv = p->seqlen_kv;
+    P.hq = p->num_heads_q;
+    P.group = p->num_heads_q / p->num_heads_kv;
+    P.block_heads = c->block_heads;
+    P.head_blocks = c->head_blocks;
+    P.tokens = c->tokens;
+    P.dv = dv;
+    P.dv_splits = c->dv_splits;
+    P.units_per_block = p->num_heads_kv * c->head_blocks * c->dv_splits;
+    P.small_q = pl.small_q;
+    P.small = small;
+    P.split = c->split;
+    P.q_box_rows = c->tokens * c->block_heads;
+    P.causal = p->mask_type != SDPA_MASK_NONE;
+    P.window = p->window_left;
+    P.scale_log2 = p->softmax_scale * 1.4426950408889634f;
+    P.page_size = p->page_size;
+    P.num_pages = p->num_pages;
+    // slots one copy brings: within a page and, for the chunk kernel, within a V stage
+    P.box_rows = std::min(p->page_size & -p->page_size, small || c->dv_item == 128 ? 128 : 64);
+    P.slot_first = slot_first(p);
+    P.cu_q = cu_seqlens_q;
+    P.kv_lens = kv_lens;
+    P.block_table = block_table;
+    P.table_stride = ts;
+    P.o = o;
+    P.lse = lse;
+    P.total_tiles = reinterpret_cast<long long*>(ws);
+    P.tickets = reinterpret_cast<int*>(ws + 128);
+    P.cuts = reinterpret_cast<PagedCut*>(ws + pl.cuts_off);
+    P.parts = reinterpret_cast<float*>(ws + pl.parts_off);
+    P.err = err;
+    P.chk = chk;
+    L.workers = std::min(c->workers, sms);
+    if (debug_max_ctas() > 0) L.workers = std::min(L.workers, debug_max_ctas());
+    L.stream = s;
     const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)p->num_heads_q, (cuuint64_t)p->total_q};
     const cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)qs * 2};
-    const cuuint32_t box[3] = {64, (cuuint32_t)pl.block_heads, (cuuint32_t)pl.tokens}, estr[3] = {1, 1, 1};
-    if (fn(&L.tmQ, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(q),
-           dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    const cuuint32_t box[3] = {64, (cuuint32_t)c->block_heads, (cuuint32_t)c->tokens}, estr[3] = {1, 1, 1};
+    if (encode_map(&L.tmQ, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+                   const_cast<void*>(q), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return SDPA_ERR_CUDA;
+    if ((rc = encode_cache(&L.tmK, k_cache, p, d, p->k_page_stride, p->k_slot_stride, p->k_head_stride, P.box_rows, bf16)))
+      return rc;
+    if ((rc = encode_cache(&L.tmV, v_cache, p, dv, p->v_page_stride, p->v_slot_stride, p->v_head_stride, P.box_rows, bf16)))
+      return rc;
+    rc = timed(SDPA_KERNEL_PAGED, s, [&] {
+      return small ? launch_paged_rows(L, c->n, d, bf16, &launches) : launch_paged_chunk(L, d, bf16, &launches);
+    });
+    if (rc) return rc;
   }
-  if ((rc = encode_cache(&L.tmK, k_cache, p, d, p->k_page_stride, p->k_slot_stride, p->k_head_stride, P.box_rows, bf16)))
-    return rc;
-  if ((rc = encode_cache(&L.tmV, v_cache, p, dv, p->v_page_stride, p->v_slot_stride, p->v_head_stride, P.box_rows, bf16)))
-    return rc;
-  int n = 0;
-  if ((rc = timed(SDPA_KERNEL_PAGED, s, [&] { return launch_paged_rows(L, pl.n, d, bf16, &n); }))) return rc;
-  t_last_launches = n;
+  t_last_launches = launches;
   return SDPA_OK;
 }
 

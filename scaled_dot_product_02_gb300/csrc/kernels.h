@@ -232,14 +232,18 @@ struct NormRopeBwdParams {
 int norm_rope_bwd_blocks(long long rows, int hq, int hkv, int head_dim, int* parts);
 int launch_norm_rope_bwd(const NormRopeBwdParams& p, int head_dim, bool bf16, int* launches, cudaStream_t s);
 
-// Attention over a paged cache (paged.cu).
+// Attention over a paged cache: paged.cu serves sequences with few query rows,
+// paged_chunk.cu the others.
 struct PagedCut;  // a worker's record for the join, in the workspace
 struct PagedParams {
   int batch, total_q, max_q, max_kv;
   int hq, group;               // heads of q, and of q per kv head
   int block_heads, head_blocks;  // heads of a group in one item, items a group takes
   int tokens;                  // tokens in one item
-  int units_per_block;         // items of one block of tokens: kv heads x head_blocks
+  int dv, dv_splits;           // width of O rows; parts of it that separate items accumulate
+  int units_per_block;         // items of one block of tokens: kv heads x head_blocks x dv_splits
+  int small_q, small;          // this launch serves the sequences of at most small_q tokens (small), or the others
+  int split;                   // items may be split over workers
   int q_box_rows;              // rows the Q copy brings: tokens x block_heads
   int causal, window;          // window < 0: none
   float scale_log2;
@@ -249,7 +253,8 @@ struct PagedParams {
   long long table_stride;
   void* o;
   float* lse;
-  long long* total_tiles;      // workspace: tiles of all items (0: refused)
+  long long* total_tiles;      // workspace: length of all items (0: refused)
+  int* tickets;                // workspace: the next item (chunk kernel without split)
   PagedCut* cuts;              // [workers]
   float* parts;                // [workers][2] partial results
   int* err;
@@ -258,12 +263,16 @@ struct PagedParams {
 struct PagedLaunch {
   CUtensorMap tmQ, tmK, tmV;
   PagedParams p;
-  int workers;
+  int workers;                 // rows kernel: CTAs; chunk kernel: pipelines
   cudaStream_t stream;
 };
 size_t paged_cut_bytes();
 // n: rows of an item, 16, 32 or 64 (64 not with head_dim 512)
 int launch_paged_rows(const PagedLaunch& L, int n, int head_dim, bool bf16, int* launches);
+// Items of 128 rows.
+int launch_paged_chunk(const PagedLaunch& L, int head_dim, bool bf16, int* launches);
+// Joins the items that cross a cut: n rows of dv values an item.
+int launch_paged_join(const PagedLaunch& L, int n, int dv, bool bf16);
 
 // Log-sum-exp merge of partial results over a split of the keys (merge.cu).
 int launch_merge(const void* o_parts, const float* lse_parts, void* o, float* lse, long long items, int head_dim,

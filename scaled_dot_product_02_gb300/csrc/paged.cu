@@ -28,123 +28,11 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
-#include "common.cuh"
-#include "kernels.h"
-#include "ptx.cuh"
+#include "paged.cuh"
 
 namespace sdpa {
 
-// What a CTA records of the item its share starts in, for the join.
-struct PagedCut {
-  long long at;      // first tile of that item
-  int n, b, i0, unit;
-};
-
 namespace {
-
-constexpr int kTile = 128;            // keys of a tile
-constexpr int kStage = 32768;         // bytes of a ring stage
-constexpr int kSmemMax = 232448;      // 227 KB
-constexpr float kLn2 = 0.6931471805599453f;
-
-// ---------------------------------------------------------------- shape of the work
-
-// One sequence of the batch: its rows and its cached keys.
-struct PagedSeq {
-  int row0, q_len, kv_len;
-};
-__device__ __forceinline__ PagedSeq paged_seq(const PagedParams& p, int b) {
-  PagedSeq s;
-  s.row0 = s.q_len = s.kv_len = 0;
-  if (SDPA_ADDR_OK(p.chk, p.cu_q + b, 8) && SDPA_ADDR_OK(p.chk, p.kv_lens + b, 4)) {
-    s.row0 = __ldg(p.cu_q + b);
-    s.q_len = __ldg(p.cu_q + b + 1) - s.row0;
-    s.kv_len = __ldg(p.kv_lens + b);
-  }
-  return s;
-}
-// Whether it fits what the host was told (every other index follows from it).
-__device__ __forceinline__ bool paged_seq_ok(const PagedParams& p, const PagedSeq& s) {
-  return s.row0 >= 0 && s.q_len >= 0 && s.q_len <= p.max_q && s.kv_len >= 0 && s.kv_len <= p.max_kv &&
-         s.row0 <= p.total_q - s.q_len;
-}
-
-// Keys that the tokens [i0, i1] of a sequence see between them: [lo, hi).
-struct PagedSpan {
-  int lo, hi, tile0, tiles;  // tiles: 128-key tiles that hold them (0: none)
-};
-__device__ __forceinline__ PagedSpan paged_span(const PagedParams& p, const PagedSeq& s, int i0, int i1) {
-  PagedSpan r;
-  const int off = s.kv_len - s.q_len;
-  r.hi = p.causal ? max(0, i1 + off + 1) : s.kv_len;  // i1 < q_len: never past kv_len
-  r.lo = p.window >= 0 ? max(0, i0 + off - p.window) : 0;
-  r.tile0 = r.lo / kTile;
-  r.tiles = r.hi > r.lo ? (r.hi + kTile - 1) / kTile - r.tile0 : 0;
-  return r;
-}
-
-// Items of one sequence: blocks of `tokens` tokens, and within a block the kv
-// heads (times the head blocks of a wide group). An item without keys counts
-// as one tile, so that someone writes its zeros.
-__device__ __forceinline__ long long paged_units(const PagedParams& p, const PagedSeq& s) {
-  long long n = 0;
-  for (int i0 = 0; i0 < s.q_len; i0 += p.tokens)
-    n += max(1, paged_span(p, s, i0, min(i0 + p.tokens, s.q_len) - 1).tiles);
-  return n * p.units_per_block;
-}
-
-// A CTA's share of the tiles, walked item by item. Every role walks its own copy.
-struct PagedWalk {
-  long long u, u_end;     // tiles of all items, end to end
-  long long block_at;     // first tile of block (b, i0)
-  int b, i0;
-  PagedSeq s;
-  PagedSpan span;
-  // the current item
-  int unit;               // kv head and head block
-  long long at;           // its first tile
-  int j0, j1;             // its tiles in this share
-
-  __device__ __forceinline__ int n() const { return max(1, span.tiles); }
-  __device__ __forceinline__ int i1(const PagedParams& p) const { return min(i0 + p.tokens, s.q_len) - 1; }
-  __device__ __forceinline__ bool whole() const { return j0 == 0 && j1 == n(); }
-  __device__ __forceinline__ void locate() {
-    const int k = n();
-    unit = (int)((u - block_at) / k);
-    at = block_at + (long long)unit * k;
-    j0 = (int)(u - at);
-    j1 = (int)min((long long)k, u_end - at);
-  }
-  __device__ __forceinline__ void start(const PagedParams& p, int b_, int i0_, long long block_at_, long long u_,
-                                        long long u_end_) {
-    u = u_;
-    u_end = u_end_;
-    block_at = block_at_;
-    b = b_;
-    i0 = i0_;
-    s = paged_seq(p, b);
-    span = paged_span(p, s, i0, i1(p));
-    locate();
-  }
-  // The next item of the share; false when it is done.
-  __device__ __forceinline__ bool next(const PagedParams& p) {
-    u = at + j1;
-    if (u >= u_end) return false;
-    if (unit + 1 == p.units_per_block) {
-      block_at += (long long)p.units_per_block * n();
-      i0 += p.tokens;
-      while (i0 >= s.q_len) {  // u < u_end: a later sequence has rows
-        s = paged_seq(p, ++b);
-        i0 = 0;
-      }
-      span = paged_span(p, s, i0, i1(p));
-    }
-    locate();
-    return true;
-  }
-};
-
-__device__ __forceinline__ long long share_at(long long total, int w, int workers) { return total * w / workers; }
 
 // ---------------------------------------------------------------- the kernel
 
@@ -258,9 +146,8 @@ __global__ void __launch_bounds__(192, 1)
   uint64_t* bar_o = bar_p + 2;         // [2] O^T has this tile (and P may be replaced)
   uint64_t* o_free = bar_o + 2;        // the item's O^T has been read
   uint64_t* bar_drain = o_free + 1;
-  long long* s_scan = reinterpret_cast<long long*>(bar_drain + 1);  // [6] warp sums, then total, block_at
-  int* s_start = reinterpret_cast<int*>(s_scan + 8);                // b, i0, bad
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(s_start + 4);
+  PagedScan* scan = reinterpret_cast<PagedScan*>(bar_drain + 1);
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(scan + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   float* s_m = reinterpret_cast<float*>(sStage + C::NST * kStage + 1024);  // [N] running maxima (log2 units)
   float* s_f = s_m + N;        // [N] factors of a rescale
@@ -270,18 +157,6 @@ __global__ void __launch_bounds__(192, 1)
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  // ---- every CTA adds up the batch's tiles: thread t takes sequences [t per, (t + 1) per)
-  const int per = (p.batch + C::THREADS - 1) / C::THREADS;
-  const int b_lo = min(p.batch, (int)threadIdx.x * per), b_hi = min(p.batch, b_lo + per);
-  long long own = 0;
-  bool fits = true;
-  for (int b = b_lo; b < b_hi; ++b) {
-    const PagedSeq s = paged_seq(p, b);
-    if (paged_seq_ok(p, s) && (b > 0 || s.row0 == 0))
-      own += paged_units(p, s);
-    else
-      fits = false;
-  }
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::NST; ++i) {
       mbar_init(&full[i], 1);
@@ -305,55 +180,25 @@ __global__ void __launch_bounds__(192, 1)
     tmem_alloc(tmem_holder, C::TM_COLS);
     tmem_relinquish();
   }
-  long long upto = own;  // inclusive sum over the warp
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, upto, o);
-    if (lane >= o) upto += y;
-  }
-  if (lane == 31) s_scan[warp] = upto;
   tc_fence_before();
-  const bool all_fit = __syncthreads_and(fits);
+  const int me = blockIdx.x;
+  const PagedShares all = paged_scan<C::THREADS>(p, scan, me, 1, gridDim.x);
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
-  long long before = upto - own, total = 0;
-  for (int w = 0; w < 6; ++w) {
-    if (w < warp) before += s_scan[w];
-    total += s_scan[w];
+  const int workers = (int)min((long long)gridDim.x, all.total);
+  const bool work = me < workers;
+  const long long u0 = work ? share_at(all.total, me, workers) : 0;
+  if (threadIdx.x == 0 && me == 0) {
+    if (SDPA_ADDR_OK(p.chk, p.total_tiles, 8)) *p.total_tiles = all.total;
+    if (!all.fit) record_error(p.err, SDPA_ERR_BAD_SEQLENS);
   }
-  const int workers = (int)min((long long)gridDim.x, total);
-  const int me = blockIdx.x;
-  const bool work = all_fit && me < workers;
-  const long long u0 = work ? share_at(total, me, workers) : 0, u1 = work ? share_at(total, me + 1, workers) : 0;
-  if (work && u0 >= before && u0 < before + own) {  // one thread: the share starts in its sequences
-    int b = b_lo;
-    long long at = before;
-    PagedSeq s = paged_seq(p, b);
-    for (long long n = paged_units(p, s); u0 >= at + n; n = paged_units(p, s)) {
-      at += n;
-      s = paged_seq(p, ++b);
-    }
-    int i0 = 0;
-    while (true) {
-      const long long n =
-          (long long)p.units_per_block * max(1, paged_span(p, s, i0, min(i0 + p.tokens, s.q_len) - 1).tiles);
-      if (u0 < at + n) break;
-      at += n;
-      i0 += p.tokens;
-    }
-    s_start[0] = b;
-    s_start[1] = i0;
-    s_scan[7] = at;
-  }
-  if (threadIdx.x == 0 && me == 0 && SDPA_ADDR_OK(p.chk, p.total_tiles, 8)) *p.total_tiles = all_fit ? total : 0;
-  if (!all_fit && threadIdx.x == 0 && me == 0) record_error(p.err, SDPA_ERR_BAD_SEQLENS);
-  __syncthreads();
 
   if (work) {
     PagedWalk w;
-    w.start(p, s_start[0], s_start[1], s_scan[7], u0, u1);
+    w.start(p, scan->b[0], scan->i0[0], scan->block_at[0], u0, share_at(all.total, me + 1, workers));
     if (threadIdx.x == 0) {
       PagedCut* cut = p.cuts + me;
-      if (SDPA_ADDR_OK(p.chk, cut, sizeof(PagedCut))) *cut = PagedCut{w.at, w.n(), w.b, w.i0, w.unit};
+      if (SDPA_ADDR_OK(p.chk, cut, sizeof(PagedCut))) *cut = PagedCut{w.at, w.weight, w.b, w.i0, w.unit};
     }
     if (warp == 4) {
       // ---------------------------------------------------------- producer
@@ -362,13 +207,12 @@ __global__ void __launch_bounds__(192, 1)
         prefetch_tmap(&tmK);
         prefetch_tmap(&tmV);
       }
-      const int boxes = kTile / p.box_rows;
       const uint32_t box_bytes = p.box_rows * 128;
       int c = 0, nq = 0;
       bool ok = true;
       do {
         if (w.span.tiles == 0) continue;
-        const int kvh = w.unit / p.head_blocks, hb = w.unit - kvh * p.head_blocks;
+        const PagedUnit un = paged_unit(p, w.unit);
         const int qb = nq % C::NQ;
         if (nq >= C::NQ && !__all_sync(0xffffffffu, mbar_wait(&q_free[qb], (nq / C::NQ - 1) & 1, abort_flag))) {
           ok = false;
@@ -377,36 +221,11 @@ __global__ void __launch_bounds__(192, 1)
         if (lane == 0) {
           mbar_arrive_expect_tx(&bar_q[qb], (uint32_t)p.q_box_rows * DQK * 2);
           for (int a = 0; a < DQK / 64; ++a)
-            tma_load_3d(&tmQ, &bar_q[qb], sQ + qb * C::Q_BYTES + a * (N * 128), a * 64,
-                        kvh * p.group + hb * p.block_heads, w.s.row0 + w.i0);
+            tma_load_3d(&tmQ, &bar_q[qb], sQ + qb * C::Q_BYTES + a * (N * 128), a * 64, un.head0, w.s.row0 + w.i0);
         }
         ++nq;
-        // this lane's box of a tile: its page and slot, whether any of its keys is seen
-        struct Box {
-          int page, slot;
-          uint32_t live;  // lanes with a box to fetch
-          bool mine;
-        };
-        const int32_t* row = p.block_table + w.b * p.table_stride;
-        auto box_of = [&](int j) {
-          Box x;
-          const int key = (w.span.tile0 + j) * kTile + lane * p.box_rows;
-          x.mine = lane < boxes && key < w.span.hi && key + p.box_rows > w.span.lo;
-          x.page = p.num_pages;  // outside the map: reads as zeros
-          x.slot = 0;
-          if (x.mine) {
-            const int col = key / p.page_size;
-            x.slot = key - col * p.page_size;
-            const int id = SDPA_ADDR_OK(p.chk, row + col, 4) ? __ldg(row + col) : -1;
-            if (id >= 0 && id < p.num_pages)
-              x.page = id;
-            else
-              record_error(p.err, SDPA_ERR_BAD_INDEX);
-          }
-          x.live = __popc(__ballot_sync(0xffffffffu, x.mine));
-          return x;
-        };
-        auto fetch = [&](const CUtensorMap* m, const Box& x, int col, int atoms) -> bool {
+        auto box_of = [&](int j) { return paged_box(p, w.span, w.b, (w.span.tile0 + j) * kTile, lane); };
+        auto fetch = [&](const CUtensorMap* m, const PagedBox& x, int col, int atoms) -> bool {
           const int slot = c % C::NST;
           if (!__all_sync(0xffffffffu, mbar_wait(&empty[slot], ((c / C::NST) & 1) ^ 1, abort_flag))) return false;
           if (lane == 0) mbar_arrive_expect_tx(&full[slot], x.live * atoms * box_bytes);
@@ -414,15 +233,15 @@ __global__ void __launch_bounds__(192, 1)
           if (x.mine) {
             uint8_t* dst = sStage + slot * kStage + lane * box_bytes;
             for (int a = 0; a < atoms; ++a)
-              tma_load_4d(m, &full[slot], dst + a * 16384, col + a * 64, p.slot_first ? x.slot : kvh,
-                          p.slot_first ? kvh : x.slot, x.page);
+              tma_load_4d(m, &full[slot], dst + a * 16384, col + a * 64, p.slot_first ? x.slot : un.kvh,
+                          p.slot_first ? un.kvh : x.slot, x.page);
           }
           ++c;
           return true;
         };
-        Box cur = box_of(w.j0), prev = cur;
+        PagedBox cur = box_of(w.j0), prev = cur;
         for (int j = w.j0; j < w.j1 && ok; ++j) {
-          const Box ahead = j + 1 < w.j1 ? box_of(j + 1) : cur;  // its table entry arrives while this tile's copies go out
+          const PagedBox ahead = j + 1 < w.j1 ? box_of(j + 1) : cur;  // its table entry arrives while this tile's copies go out
           for (int kb = 0; kb < C::KST && ok; ++kb) ok = fetch(&tmK, cur, kb * 128, C::k_atoms(kb));
           if (j > w.j0)
             for (int vb = 0; vb < C::VST && ok; ++vb) ok = fetch(&tmV, prev, vb * 128, 2);
@@ -524,7 +343,7 @@ __global__ void __launch_bounds__(192, 1)
       do {
         const int n = w.j1 - w.j0;
         const bool keys = w.span.tiles > 0;
-        const int kvh = w.unit / p.head_blocks, hb = w.unit - kvh * p.head_blocks;
+        const PagedUnit un = paged_unit(p, w.unit);
         const int tok = w.i1(p) - w.i0 + 1, rows = tok * p.block_heads;
         const int off = w.s.kv_len - w.s.q_len;
         if (tid < N) s_m[tid] = -INFINITY;
@@ -654,16 +473,14 @@ __global__ void __launch_bounds__(192, 1)
         }
         if (tid < N) s_l[tid] = (s_w[tid] + s_w[N + tid]) + (s_w[2 * N + tid] + s_w[3 * N + tid]);
         named_bar_sync(1, 128);
-        const int gv = min(p.block_heads, p.group - hb * p.block_heads);  // heads of the block that exist
-        const int head0 = kvh * p.group + hb * p.block_heads;
         const long long row0 = w.s.row0 + w.i0;
         const bool whole = w.whole();
         // at most one item continues from the CTA before, and one into the next
         float* part = p.parts + ((long long)me * 2 + (w.at < u0 ? 0 : 1)) * (N * (DV + 2));
-        if (tid < rows && tid % p.block_heads < gv) {
+        if (tid < rows && tid % p.block_heads < un.heads) {
           const float m = s_m[tid], sum = s_l[tid];
           if (whole) {
-            float* at = p.lse + (row0 + tid / p.block_heads) * p.hq + head0 + tid % p.block_heads;
+            float* at = p.lse + (row0 + tid / p.block_heads) * p.hq + un.head0 + tid % p.block_heads;
             if (SDPA_ADDR_OK(p.chk, at, 4)) *at = sum == 0.f ? -INFINITY : m * kLn2 + logf(sum);
           } else if (SDPA_ADDR_OK(p.chk, part + N * DV + tid, 4) && SDPA_ADDR_OK(p.chk, part + N * DV + N + tid, 4)) {
             part[N * DV + tid] = m;
@@ -695,10 +512,10 @@ __global__ void __launch_bounds__(192, 1)
           int ti = 0, h = 0;
 #pragma unroll
           for (int i = 0; i < N; ++i) {
-            if (i < rows && h < gv) {
+            if (i < rows && h < un.heads) {
               if (whole) {
                 const float sum = s_l[i];
-                T* at = static_cast<T*>(p.o) + ((row0 + ti) * p.hq + head0 + h) * DV + vb * 128 + tid;
+                T* at = static_cast<T*>(p.o) + ((row0 + ti) * p.hq + un.head0 + h) * DV + vb * 128 + tid;
                 const float v = o[i] * (sum == 0.f ? 0.f : 1.f / sum);
                 const uint32_t packed = E::pack(v, 0.f);
                 if (SDPA_ADDR_OK(p.chk, at, 2)) *reinterpret_cast<uint16_t*>(at) = (uint16_t)packed;
@@ -737,6 +554,7 @@ __global__ void __launch_bounds__(192, 1)
 // w's share) falls into, if w is the first cut inside it. Its parts come from
 // worker w - 1 (which began it) and the workers whose shares start in it:
 //   m = max m_k,  l = sum l_k 2^(m_k - m),  O = sum O_k 2^(m_k - m) / l.
+// A part holds N rows of DV values, then N maxima and N sums.
 template <int DV, int N, bool BF16>
 __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__ PagedParams p, int grid) {
   using E = Elem<BF16>;
@@ -757,35 +575,36 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__
 
   const PagedSeq s = paged_seq(p, cut.b);
   const int tok = min(cut.i0 + p.tokens, s.q_len) - cut.i0, rows = tok * p.block_heads;
-  const int kvh = cut.unit / p.head_blocks, hb = cut.unit - kvh * p.head_blocks;
-  const int gv = min(p.block_heads, p.group - hb * p.block_heads), head0 = kvh * p.group + hb * p.block_heads;
+  const PagedUnit un = paged_unit(p, cut.unit);
   const long long row0 = s.row0 + cut.i0;
   auto stat = [&](int k, int i) {
     const float* at = part(k) + N * DV + i;
     return SDPA_ADDR_OK(p.chk, at, 4) ? *at : -INFINITY;
   };
-  const int i = threadIdx.x / 4, q = threadIdx.x % 4;  // four threads a row
-  float m = -INFINITY, l = 0.f;
-  const bool live = i < rows && i % p.block_heads < gv;
-  if (live)
-    for (int k = q; k < parts; k += 4) m = fmaxf(m, stat(k, i));
-  m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-  m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-  if (live && m != -INFINITY)
-    for (int k = q; k < parts; k += 4) l += stat(k, N + i) * exp2f(stat(k, i) - m);
-  l += __shfl_xor_sync(0xffffffffu, l, 1);
-  l += __shfl_xor_sync(0xffffffffu, l, 2);
-  if (live && q == 0) {
-    s_m[i] = m;
-    s_inv[i] = l == 0.f ? 0.f : 1.f / l;
-    float* at = p.lse + (row0 + i / p.block_heads) * p.hq + head0 + i % p.block_heads;
-    if (SDPA_ADDR_OK(p.chk, at, 4)) *at = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
+  for (int i = threadIdx.x / 4; i < N; i += 64) {  // four threads a row
+    const int q = threadIdx.x % 4;
+    float m = -INFINITY, l = 0.f;
+    const bool live = i < rows && i % p.block_heads < un.heads;
+    if (live)
+      for (int k = q; k < parts; k += 4) m = fmaxf(m, stat(k, i));
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    if (live && m != -INFINITY)
+      for (int k = q; k < parts; k += 4) l += stat(k, N + i) * exp2f(stat(k, i) - m);
+    l += __shfl_xor_sync(0xffffffffu, l, 1);
+    l += __shfl_xor_sync(0xffffffffu, l, 2);
+    if (live && q == 0) {
+      s_m[i] = m;
+      s_inv[i] = l == 0.f ? 0.f : 1.f / l;
+      float* at = p.lse + (row0 + i / p.block_heads) * p.hq + un.head0 + i % p.block_heads;
+      if (un.split == 0 && SDPA_ADDR_OK(p.chk, at, 4)) *at = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
+    }
   }
   __syncthreads();
   constexpr int V4 = DV / 4;
   for (int x = threadIdx.x; x < rows * V4; x += 256) {
     const int r = x / V4, d = (x % V4) * 4;
-    if (r % p.block_heads >= gv) continue;
+    if (r % p.block_heads >= un.heads) continue;
     const float mr = s_m[r];
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
     if (mr != -INFINITY) {
@@ -801,22 +620,16 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__
       }
     }
     const float inv = s_inv[r];
-    T* dst = static_cast<T*>(p.o) + ((row0 + r / p.block_heads) * p.hq + head0 + r % p.block_heads) * DV + d;
+    T* dst = static_cast<T*>(p.o) + ((row0 + r / p.block_heads) * p.hq + un.head0 + r % p.block_heads) * p.dv +
+             un.split * DV + d;
     if (SDPA_ADDR_OK(p.chk, dst, 8))
       *reinterpret_cast<uint2*>(dst) = make_uint2(E::pack(a.x * inv, a.y * inv), E::pack(a.z * inv, a.w * inv));
   }
 }
 
-template <int DQK, int DV, int N, bool BF16>
-int launch_rows_t(const PagedLaunch& L, int* launches) {
-  using C = RowsCfg<DQK, DV, N>;
-  auto kern = paged_rows_kernel<DQK, DV, N, BF16>;
-  if (const int rc = set_kernel_smem(reinterpret_cast<const void*>(kern), C::SMEM, -1)) return rc;
-  kern<<<(unsigned)L.workers, C::THREADS, C::SMEM, L.stream>>>(L.tmQ, L.tmK, L.tmV, L.p);
-  if (cudaGetLastError() != cudaSuccess) return SDPA_ERR_CUDA;
-  *launches = 1;
-  if (L.workers == 1) return SDPA_OK;  // no cuts
-  // launched while the kernel above runs; it waits for it before reading
+// Launched while the attention kernel runs; it waits for it before reading.
+template <int DV, int N, bool BF16>
+int launch_join_t(const PagedLaunch& L) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)L.workers - 1);
   cfg.blockDim = dim3(256);
@@ -826,9 +639,20 @@ int launch_rows_t(const PagedLaunch& L, int* launches) {
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, paged_join_kernel<DV, N, BF16>, L.p, L.workers) != cudaSuccess) return SDPA_ERR_CUDA;
-  *launches = 2;
-  return SDPA_OK;
+  return cudaLaunchKernelEx(&cfg, paged_join_kernel<DV, N, BF16>, L.p, L.workers) == cudaSuccess ? SDPA_OK : SDPA_ERR_CUDA;
+}
+
+template <int DQK, int DV, int N, bool BF16>
+int launch_rows_t(const PagedLaunch& L, int* launches) {
+  using C = RowsCfg<DQK, DV, N>;
+  auto kern = paged_rows_kernel<DQK, DV, N, BF16>;
+  if (const int rc = set_kernel_smem(reinterpret_cast<const void*>(kern), C::SMEM, -1)) return rc;
+  kern<<<(unsigned)L.workers, C::THREADS, C::SMEM, L.stream>>>(L.tmQ, L.tmK, L.tmV, L.p);
+  if (cudaGetLastError() != cudaSuccess) return SDPA_ERR_CUDA;
+  ++*launches;
+  if (L.workers == 1 || !L.p.split) return SDPA_OK;  // no item crosses a cut
+  ++*launches;
+  return launch_join_t<DV, N, BF16>(L);
 }
 
 template <int DQK, int DV, bool BF16>
@@ -840,6 +664,14 @@ int launch_rows_n(const PagedLaunch& L, int n, int* launches) {
 }
 
 }  // namespace
+
+int launch_paged_join(const PagedLaunch& L, int n, int dv, bool bf16) {
+#define JOIN(A, B) return bf16 ? launch_join_t<A, B, true>(L) : launch_join_t<A, B, false>(L)
+  if (n == 128 && dv == 128) JOIN(128, 128);
+  if (n == 128 && dv == 256) JOIN(256, 128);
+#undef JOIN
+  return SDPA_ERR_UNSUPPORTED;
+}
 
 size_t paged_cut_bytes() { return sizeof(PagedCut); }
 

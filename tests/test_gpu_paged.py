@@ -163,7 +163,7 @@ def test_reproducible_and_independent_of_the_split(name, d):
     a, b = call(c), call(c)
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
     try:
-        for cap in (1, 2, 3, 7, 50):
+        for cap in (1, 2, 3, 7, 50):  # workers of either kernel
             sdpa.sdpa_debug_set_max_ctas(cap)
             check(c, *call(c))
     finally:
@@ -273,6 +273,23 @@ def test_many_tiles_and_many_items_per_cta(d, page, window):
     """Every ring slot is taken again and again before the tile whose unseen values are cleared."""
     c = case([150, 1, 60, 7], [3001, 2777, 1900, 2050], hq=16, hkv=4, d=d, page=page)
     check(c, *call(c, window=window), window=window)
+
+
+@pytest.mark.parametrize("d,page,order", [(128, 64, "nhd"), (192, 16, "nhd"), (256, 256, "hnd"), (512, 32, "nhd")])
+@pytest.mark.parametrize("window", [-1, 100])
+def test_long_chunks_and_single_tokens_in_one_batch(d, page, order, window):
+    """Sequences on both sides of the cut between the two kernels, one and many items per CTA."""
+    c = case([300, 1, 0, 17, 700, 16, 1], [300, 900, 30, 800, 1500, 16, 1], hq=16, hkv=4, d=d, page=page, order=order, pad=3)
+    check(c, *call(c, window=window), window=window)
+    c = case([1111], [2000], hq=8, hkv=2, d=d, page=page, order=order, dtype=HF)
+    check(c, *call(c, window=window), window=window)
+
+
+@pytest.mark.parametrize("d", [128, 256])
+def test_items_enough_for_the_ticket_order(d):
+    c = case([600, 1, 333], [700, 50, 1300], hq=64, hkv=32, d=d, page=64)
+    check(c, *call(c))
+    check(c, *call(c, window=200), window=200)
 
 
 def test_a_large_batch():
