@@ -446,7 +446,7 @@ struct PagedCutting {
   int tokens;                    // tokens in an item
   int dv_item, dv_splits;        // value columns an item accumulates, items that share a row
   bool split;                    // items may be split over workers
-  int workers;                   // CTAs (at most one per SM)
+  int workers;                   // CTAs (at most one per SM); head_dim 128 chunks: pipelines, two a CTA
 };
 struct PagedPlan {
   int small_q;         // sequences of at most this many new tokens go to the rows kernel, longer ones to the chunk kernel
@@ -459,6 +459,7 @@ constexpr int kPagedWorkers = 152;
 
 PagedCutting paged_cutting(const sdpa_paged_problem* p, int n, int max_q, int dv_item) {
   PagedCutting c;
+  const int most = n == 128 && p->head_dim == 128 ? 2 * kPagedWorkers : kPagedWorkers;
   const int group = p->num_heads_q / p->num_heads_kv, dv = paged_dv(p);
   c.used = true;
   c.n = n;
@@ -478,11 +479,11 @@ PagedCutting paged_cutting(const sdpa_paged_problem* p, int n, int max_q, int dv
     c.split = tiles > 4;
   } else {
     // with items enough the ticket order, which keeps the CTAs on the same keys; else equal shares
-    c.split = tiles > 1 && items < 4 * kPagedWorkers;
+    c.split = tiles > 1 && items < 4 * most;
     if (!c.split && (long long)p->batch * ((max_q + c.tokens - 1) / c.tokens) * (items / blocks) > 0x7fff0000LL) c.split = true;
   }
-  const long long pieces = c.split && items < kPagedWorkers ? items * std::max(tiles, 1LL) : items;
-  c.workers = (int)std::max(1LL, std::min<long long>(kPagedWorkers, pieces));
+  const long long pieces = c.split && items < most ? items * std::max(tiles, 1LL) : items;
+  c.workers = (int)std::max(1LL, std::min<long long>(most, pieces));
   return c;
 }
 
@@ -1316,7 +1317,8 @@ int sdpa_paged_fwd(const sdpa_paged_problem* p, const void* q, const void* k_cac
     P.parts = reinterpret_cast<float*>(ws + pl.parts_off);
     P.err = err;
     P.chk = chk;
-    L.workers = std::min(c->workers, sms);
+    const bool pair = !small && d == 128;
+    L.workers = std::min(c->workers, pair ? 2 * sms : sms);
     if (debug_max_ctas() > 0) L.workers = std::min(L.workers, debug_max_ctas());
     L.stream = s;
     const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)p->num_heads_q, (cuuint64_t)p->total_q};
@@ -1332,7 +1334,9 @@ int sdpa_paged_fwd(const sdpa_paged_problem* p, const void* q, const void* k_cac
     if ((rc = encode_cache(&L.tmV, v_cache, p, dv, p->v_page_stride, p->v_slot_stride, p->v_head_stride, P.box_rows, bf16)))
       return rc;
     rc = timed(SDPA_KERNEL_PAGED, s, [&] {
-      return small ? launch_paged_rows(L, c->n, d, bf16, &launches) : launch_paged_chunk(L, d, bf16, &launches);
+      return small  ? launch_paged_rows(L, c->n, d, bf16, &launches)
+             : pair ? launch_paged_pair(L, sms, bf16, &launches)
+                    : launch_paged_chunk(L, d, bf16, &launches);
     });
     if (rc) return rc;
   }

@@ -233,7 +233,7 @@ int norm_rope_bwd_blocks(long long rows, int hq, int hkv, int head_dim, int* par
 int launch_norm_rope_bwd(const NormRopeBwdParams& p, int head_dim, bool bf16, int* launches, cudaStream_t s);
 
 // Attention over a paged cache: paged.cu serves sequences with few query rows,
-// paged_chunk.cu the others.
+// paged_pair.cu (head_dim 128) and paged_chunk.cu the others.
 struct PagedCut;  // a worker's record for the join, in the workspace
 struct PagedParams {
   int batch, total_q, max_q, max_kv;
@@ -263,7 +263,7 @@ struct PagedParams {
 struct PagedLaunch {
   CUtensorMap tmQ, tmK, tmV;
   PagedParams p;
-  int workers;                 // rows kernel: CTAs; chunk kernel: pipelines
+  int workers;                 // CTAs, or pipelines
   cudaStream_t stream;
 };
 size_t paged_cut_bytes();
@@ -271,6 +271,8 @@ size_t paged_cut_bytes();
 int launch_paged_rows(const PagedLaunch& L, int n, int head_dim, bool bf16, int* launches);
 // Items of 128 rows.
 int launch_paged_chunk(const PagedLaunch& L, int head_dim, bool bf16, int* launches);
+// The same at head_dim 128, two pipelines a CTA (L.workers pipelines on at most sms CTAs).
+int launch_paged_pair(const PagedLaunch& L, int sms, bool bf16, int* launches);
 // Joins the items that cross a cut: n rows of dv values an item.
 int launch_paged_join(const PagedLaunch& L, int n, int dv, bool bf16);
 

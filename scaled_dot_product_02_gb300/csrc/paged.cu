@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(192, 1)
   }
   tc_fence_before();
   const int me = blockIdx.x;
-  const PagedShares all = paged_scan<C::THREADS>(p, scan, me, 1, gridDim.x);
+  const PagedShares all = paged_scan<C::THREADS>(p, scan, me, 1, 1, gridDim.x);
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
   const int workers = (int)min((long long)gridDim.x, all.total);
@@ -554,12 +554,15 @@ __global__ void __launch_bounds__(192, 1)
 // w's share) falls into, if w is the first cut inside it. Its parts come from
 // worker w - 1 (which began it) and the workers whose shares start in it:
 //   m = max m_k,  l = sum l_k 2^(m_k - m),  O = sum O_k 2^(m_k - m) / l.
-// A part holds N rows of DV values, then N maxima and N sums.
+// A part holds N rows of DV values, then N maxima and N sums. CTA (w, y) joins
+// rows 16 y to 16 y + 15: with all rows of an item in one CTA the join of a
+// chunk's 128-row items took 29 us (128 columns) to 49 us (256), one round of
+// loads after another.
 template <int DV, int N, bool BF16>
 __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__ PagedParams p, int grid) {
   using E = Elem<BF16>;
   using T = typename E::T;
-  __shared__ float s_m[N], s_inv[N];
+  __shared__ float s_m[16], s_inv[16];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (!SDPA_ADDR_OK(p.chk, p.total_tiles, 8)) return;
   const long long total = *reinterpret_cast<volatile long long*>(p.total_tiles);
@@ -568,49 +571,51 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__
   if (w >= workers || !SDPA_ADDR_OK(p.chk, p.cuts + w, sizeof(PagedCut))) return;
   const PagedCut cut = p.cuts[w];
   if (share_at(total, w, workers) == cut.at || share_at(total, w - 1, workers) > cut.at) return;
+  const PagedSeq s = paged_seq(p, cut.b);
+  const int tok = min(cut.i0 + p.tokens, s.q_len) - cut.i0, r0 = blockIdx.y * 16;
+  const int rows = min(16, tok * p.block_heads - r0);
+  if (rows <= 0) return;
   int parts = 1;  // worker w - 1, then w, w + 1, ...
   while (w - 1 + parts < workers && share_at(total, w - 1 + parts, workers) < cut.at + cut.n) ++parts;
   constexpr int SLOT = N * (DV + 2);
   auto part = [&](int k) { return p.parts + ((long long)(w - 1 + k) * 2 + (k == 0 ? 1 : 0)) * SLOT; };
-
-  const PagedSeq s = paged_seq(p, cut.b);
-  const int tok = min(cut.i0 + p.tokens, s.q_len) - cut.i0, rows = tok * p.block_heads;
   const PagedUnit un = paged_unit(p, cut.unit);
   const long long row0 = s.row0 + cut.i0;
   auto stat = [&](int k, int i) {
     const float* at = part(k) + N * DV + i;
     return SDPA_ADDR_OK(p.chk, at, 4) ? *at : -INFINITY;
   };
-  for (int i = threadIdx.x / 4; i < N; i += 64) {  // four threads a row
-    const int q = threadIdx.x % 4;
+  {
+    const int i = threadIdx.x / 16, q = threadIdx.x % 16, r = r0 + i;  // 16 threads a row
     float m = -INFINITY, l = 0.f;
-    const bool live = i < rows && i % p.block_heads < un.heads;
+    const bool live = i < rows && r % p.block_heads < un.heads;
     if (live)
-      for (int k = q; k < parts; k += 4) m = fmaxf(m, stat(k, i));
-    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+      for (int k = q; k < parts; k += 16) m = fmaxf(m, stat(k, r));
+#pragma unroll
+    for (int o = 8; o > 0; o /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     if (live && m != -INFINITY)
-      for (int k = q; k < parts; k += 4) l += stat(k, N + i) * exp2f(stat(k, i) - m);
-    l += __shfl_xor_sync(0xffffffffu, l, 1);
-    l += __shfl_xor_sync(0xffffffffu, l, 2);
+      for (int k = q; k < parts; k += 16) l += stat(k, N + r) * ex2(stat(k, r) - m);
+#pragma unroll
+    for (int o = 8; o > 0; o /= 2) l += __shfl_xor_sync(0xffffffffu, l, o);
     if (live && q == 0) {
       s_m[i] = m;
       s_inv[i] = l == 0.f ? 0.f : 1.f / l;
-      float* at = p.lse + (row0 + i / p.block_heads) * p.hq + un.head0 + i % p.block_heads;
+      float* at = p.lse + (row0 + r / p.block_heads) * p.hq + un.head0 + r % p.block_heads;
       if (un.split == 0 && SDPA_ADDR_OK(p.chk, at, 4)) *at = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
     }
   }
   __syncthreads();
   constexpr int V4 = DV / 4;
+#pragma unroll 2
   for (int x = threadIdx.x; x < rows * V4; x += 256) {
-    const int r = x / V4, d = (x % V4) * 4;
+    const int i = x / V4, r = r0 + i, d = (x % V4) * 4;
     if (r % p.block_heads >= un.heads) continue;
-    const float mr = s_m[r];
+    const float mr = s_m[i];
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
     if (mr != -INFINITY) {
 #pragma unroll 4
       for (int k = 0; k < parts; ++k) {
-        const float mk = stat(k, r), f = mk == -INFINITY ? 0.f : exp2f(mk - mr);
+        const float mk = stat(k, r), f = mk == -INFINITY ? 0.f : ex2(mk - mr);
         const float* at = part(k) + r * DV + d;
         const float4 v = SDPA_ADDR_OK(p.chk, at, 16) ? *reinterpret_cast<const float4*>(at) : make_float4(0.f, 0.f, 0.f, 0.f);
         a.x = fmaf(f, v.x, a.x);
@@ -619,7 +624,7 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__
         a.w = fmaf(f, v.w, a.w);
       }
     }
-    const float inv = s_inv[r];
+    const float inv = s_inv[i];
     T* dst = static_cast<T*>(p.o) + ((row0 + r / p.block_heads) * p.hq + un.head0 + r % p.block_heads) * p.dv +
              un.split * DV + d;
     if (SDPA_ADDR_OK(p.chk, dst, 8))
@@ -631,7 +636,7 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__
 template <int DV, int N, bool BF16>
 int launch_join_t(const PagedLaunch& L) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)L.workers - 1);
+  cfg.gridDim = dim3((unsigned)L.workers - 1, N / 16);
   cfg.blockDim = dim3(256);
   cfg.stream = L.stream;
   cudaLaunchAttribute attr;

@@ -183,9 +183,11 @@ struct PagedScan {    // shared memory of the scan
   int b[2], i0[2];
 };
 // Adds up all sequences and finds the blocks of tokens in which the shares of
-// workers w0 .. w0 + n_w - 1 (at most two) start. All THREADS threads call it.
+// workers w0, w0 + step, ... (n_w of them, at most two) start. All THREADS
+// threads call it.
 template <int THREADS>
-__device__ __forceinline__ PagedShares paged_scan(const PagedParams& p, PagedScan* sc, int w0, int n_w, int grid_workers) {
+__device__ __forceinline__ PagedShares paged_scan(const PagedParams& p, PagedScan* sc, int w0, int step, int n_w,
+                                                  int most_workers) {
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int per = (p.batch + THREADS - 1) / THREADS;  // thread t takes sequences [t per, (t + 1) per)
   const int b_lo = min(p.batch, (int)threadIdx.x * per), b_hi = min(p.batch, b_lo + per);
@@ -213,10 +215,11 @@ __device__ __forceinline__ PagedShares paged_scan(const PagedParams& p, PagedSca
     r.total += sc->warp_sum[w];
   }
   if (!r.fit) r.total = 0;
-  const int workers = (int)min((long long)grid_workers, r.total);
+  const int workers = (int)min((long long)most_workers, r.total);
   for (int x = 0; x < n_w; ++x) {
-    if (w0 + x >= workers) break;
-    const long long u = share_at(r.total, w0 + x, workers);
+    const int w = w0 + x * step;
+    if (w >= workers) break;
+    const long long u = share_at(r.total, w, workers);
     if (u < before || u >= before + own) continue;  // one thread: the share starts in its sequences
     int b = b_lo;
     long long at = before;
@@ -240,5 +243,71 @@ __device__ __forceinline__ PagedShares paged_scan(const PagedParams& p, PagedSca
   __syncthreads();
   return r;
 }
+
+// A piece of work as the scheduler of a pipeline publishes it.
+struct PagedPiece {
+  int row0, q_len, kv_len, i0, unit;  // row0 < 0: no more
+  int j0, j1;                         // its key tiles, counted from the span's first
+  int slot;                           // its partial result, or -1: the whole item
+};
+
+// Where a pipeline's pieces come from: its share of the tiles (p.split), or
+// the tickets, last block of tokens first and the items of a block together.
+// A whole warp walks it.
+struct PagedFeed {
+  PagedWalk w;
+  bool more;
+  long long u0;
+  int blocks, tickets;
+
+  __device__ __forceinline__ void take(const PagedParams& p, int lane) {
+    while (true) {
+      int t = tickets;  // a counter the address check rejects hands out none
+      if (lane == 0 && SDPA_ADDR_OK(p.chk, p.tickets, 4)) t = atomicAdd(p.tickets, 1);
+      t = __shfl_sync(0xffffffffu, t, 0);
+      more = t < tickets;
+      if (!more) return;
+      w.unit = t % p.units_per_block;
+      t /= p.units_per_block;
+      w.b = t % p.batch;
+      w.i0 = (blocks - 1 - t / p.batch) * p.tokens;
+      w.s = paged_mine(p, paged_seq(p, w.b));
+      if (w.i0 >= w.s.q_len) continue;
+      w.span = paged_span(p, w.s, w.i0, w.i1(p));
+      w.at = 0;
+      w.j0 = 0;
+      w.j1 = w.span.tiles;
+      return;
+    }
+  }
+  // Worker `me` of `workers`; x: its place in the scan.
+  __device__ __forceinline__ void start(const PagedParams& p, const PagedScan* sc, int x, long long total, int me,
+                                        int workers, int lane) {
+    u0 = 0;
+    tickets = blocks = 0;
+    more = me < workers;
+    if (!more) return;
+    if (p.split) {
+      u0 = share_at(total, me, workers);
+      w.start(p, sc->b[x], sc->i0[x], sc->block_at[x], u0, share_at(total, me + 1, workers));
+      PagedCut* cut = p.cuts + me;
+      if (lane == 0 && SDPA_ADDR_OK(p.chk, cut, sizeof(PagedCut))) *cut = PagedCut{w.at, w.weight, w.b, w.i0, w.unit};
+    } else {
+      blocks = (p.max_q + p.tokens - 1) / p.tokens;
+      tickets = blocks * p.batch * p.units_per_block;
+      take(p, lane);
+    }
+  }
+  __device__ __forceinline__ void next(const PagedParams& p, int lane) {
+    if (p.split)
+      more = w.next(p);
+    else
+      take(p, lane);
+  }
+  __device__ __forceinline__ PagedPiece piece() const {
+    return PagedPiece{more ? w.s.row0 : -1, w.s.q_len, w.s.kv_len, w.i0, w.unit, w.j0, w.j1,
+                      w.whole() ? -1 : (w.at < u0 ? 0 : 1)};
+  }
+};
 
 }  // namespace sdpa

@@ -1,5 +1,5 @@
 // paged_chunk.cu -- attention over a paged cache for sequences with many new
-// tokens (chunks of a prompt): the work is bound by the tensor pipe and the
+// tokens (chunks of a prompt) at head dims 192 to 512 (paged_pair.cu serves 128): the work is bound by the tensor pipe and the
 // exponentials, as in the contiguous forward.
 //
 // An item is 128 query rows that share one kv head (tokens times the heads of
@@ -24,13 +24,6 @@
 namespace sdpa {
 
 namespace {
-
-// A piece of work as the scheduler publishes it.
-struct Piece {
-  int row0, q_len, kv_len, i0, unit;  // row0 < 0: no more
-  int j0, j1;                         // its key tiles, counted from the span's first
-  int slot;                           // its partial result, or -1: the whole item
-};
 
 template <int DQK, int DV>
 struct ChunkCfg {
@@ -72,7 +65,7 @@ __global__ void __launch_bounds__(256, 1)
   uint64_t* sched_empty = sched_full + 2;
   uint64_t* bar_drain = sched_empty + 2;
   PagedScan* scan = reinterpret_cast<PagedScan*>(bar_drain + 1);
-  Piece* pieces = reinterpret_cast<Piece*>(scan + 1);  // [2]
+  PagedPiece* pieces = reinterpret_cast<PagedPiece*>(scan + 1);  // [2]
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(pieces + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -100,7 +93,7 @@ __global__ void __launch_bounds__(256, 1)
   }
   tc_fence_before();
   const int me = blockIdx.x;
-  const PagedShares all = paged_scan<C::THREADS>(p, scan, me, p.split, gridDim.x);
+  const PagedShares all = paged_scan<C::THREADS>(p, scan, me, 1, p.split, gridDim.x);
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
   const int workers = (int)min((long long)gridDim.x, all.total);
@@ -120,41 +113,9 @@ __global__ void __launch_bounds__(256, 1)
       const uint32_t box_bytes = p.box_rows * 128;
       int c = 0, nq = 0, np = 0;
       bool ok = true;
-      PagedWalk w;
-      bool more;
-      const long long u0 = p.split ? share_at(all.total, me, workers) : 0;
-      const int blocks = (p.max_q + p.tokens - 1) / p.tokens;
-      const int tickets = p.split ? 0 : blocks * p.batch * p.units_per_block;
-      // the next item of the ticket order (a counter the address check rejects hands out none)
-      auto take = [&]() -> bool {
-        while (true) {
-          int t = tickets;
-          if (lane == 0 && SDPA_ADDR_OK(p.chk, p.tickets, 4)) t = atomicAdd(p.tickets, 1);
-          t = __shfl_sync(0xffffffffu, t, 0);
-          if (t >= tickets) return false;
-          w.unit = t % p.units_per_block;
-          t /= p.units_per_block;
-          w.b = t % p.batch;
-          w.i0 = (blocks - 1 - t / p.batch) * p.tokens;
-          w.s = paged_mine(p, paged_seq(p, w.b));
-          if (w.i0 >= w.s.q_len) continue;
-          w.span = paged_span(p, w.s, w.i0, w.i1(p));
-          w.j0 = 0;
-          w.j1 = w.span.tiles;
-          w.at = 0;
-          return true;
-        }
-      };
-      if (p.split) {
-        w.start(p, scan->b[0], scan->i0[0], scan->block_at[0], u0, share_at(all.total, me + 1, workers));
-        more = true;
-        if (lane == 0) {
-          PagedCut* cut = p.cuts + me;
-          if (SDPA_ADDR_OK(p.chk, cut, sizeof(PagedCut))) *cut = PagedCut{w.at, w.weight, w.b, w.i0, w.unit};
-        }
-      } else {
-        more = take();
-      }
+      PagedFeed feed;
+      feed.start(p, scan, 0, all.total, me, workers, lane);
+      const PagedWalk& w = feed.w;
       while (true) {
         const int e = np & 1;
         if (!__all_sync(0xffffffffu, mbar_wait(&sched_empty[e], ((np >> 1) & 1) ^ 1, abort_flag))) {
@@ -162,12 +123,11 @@ __global__ void __launch_bounds__(256, 1)
           break;
         }
         if (lane == 0) {
-          pieces[e] = Piece{more ? w.s.row0 : -1, w.s.q_len, w.s.kv_len, w.i0, w.unit, w.j0, w.j1,
-                            w.whole() ? -1 : (w.at < u0 ? 0 : 1)};
+          pieces[e] = feed.piece();
           mbar_arrive(&sched_full[e]);
         }
         ++np;
-        if (!more) break;
+        if (!feed.more) break;
         if (w.span.tiles > 0) {
           const PagedUnit un = paged_unit(p, w.unit);
           if (nq > 0 && !__all_sync(0xffffffffu, mbar_wait(q_free, (nq - 1) & 1, abort_flag))) {
@@ -227,7 +187,7 @@ __global__ void __launch_bounds__(256, 1)
           if (ok) ok = load_v(prev);
           if (!ok) break;
         }
-        more = p.split ? w.next(p) : take();
+        feed.next(p, lane);
       }
       if (lane == 0) {
         if (!ok) {
@@ -333,7 +293,7 @@ __global__ void __launch_bounds__(256, 1)
           ok = false;
           break;
         }
-        const Piece w = pieces[e];
+        const PagedPiece w = pieces[e];
         __syncwarp();
         mbar_arrive(&sched_empty[e]);
         ++np;
@@ -560,7 +520,6 @@ int launch_chunk_t(const PagedLaunch& L, int* launches) {
 
 int launch_paged_chunk(const PagedLaunch& L, int head_dim, bool bf16, int* launches) {
 #define CHUNK(A, B) return bf16 ? launch_chunk_t<A, B, true>(L, launches) : launch_chunk_t<A, B, false>(L, launches)
-  if (head_dim == 128) CHUNK(128, 128);
   if (head_dim == 192) CHUNK(192, 128);
   if (head_dim == 256) CHUNK(256, 256);
   if (head_dim == 512) CHUNK(512, 256);
