@@ -479,7 +479,7 @@ PagedCutting paged_cutting(const sdpa_paged_problem* p, int n, int max_q, int dv
     c.split = tiles > 4;
   } else {
     // with items enough the ticket order, which keeps the CTAs on the same keys; else equal shares
-    c.split = tiles > 1 && items < 4 * most;
+    c.split = tiles > 1 && 2 * items < 3 * most;
     if (!c.split && (long long)p->batch * ((max_q + c.tokens - 1) / c.tokens) * (items / blocks) > 0x7fff0000LL) c.split = true;
   }
   const long long pieces = c.split && items < most ? items * std::max(tiles, 1LL) : items;
@@ -1033,9 +1033,7 @@ int sdpa_qk_norm_rope(const sdpa_norm_rope_problem* p, const void* q, const void
 
 size_t sdpa_qk_norm_rope_bwd_workspace_size(const sdpa_norm_rope_problem* p) {
   if (check_norm_rope(p) != SDPA_OK || p->rows == 0) return 0;
-  int parts;
-  return (size_t)norm_rope_bwd_blocks(p->rows, p->num_heads_q, p->num_heads_kv, p->head_dim, &parts) * 2 *
-         p->head_dim * 4;
+  return (size_t)norm_rope_bwd_plan(p->rows, p->num_heads_q, p->num_heads_kv, p->head_dim).blocks * p->head_dim * 4;
 }
 
 int sdpa_qk_norm_rope_bwd(const sdpa_norm_rope_problem* p, const void* dq_out, const void* dk_out, const void* q,
@@ -1090,7 +1088,11 @@ int sdpa_qk_norm_rope_bwd(const sdpa_norm_rope_problem* p, const void* dq_out, c
   L.part = static_cast<float*>(workspace);
   L.dwq = dq_weight;
   L.dwk = dk_weight;
-  L.blocks = norm_rope_bwd_blocks(p->rows, p->num_heads_q, p->num_heads_kv, p->head_dim, &L.parts);
+  const NormRopeBwdPlan pl = norm_rope_bwd_plan(p->rows, p->num_heads_q, p->num_heads_kv, p->head_dim);
+  L.parts_q = pl.parts_q;
+  L.parts_k = pl.parts_k;
+  L.blocks_q = pl.blocks_q;
+  L.blocks = pl.blocks;
   const size_t wb = (size_t)p->head_dim * 2;
   const Extent outs[5] = {extent(dq, span(p->rows, L.dqs, qw)), extent(dk, span(p->rows, L.dks, kw)),
                           extent(dq_weight, gw), extent(dk_weight, gw), extent(workspace, need)};

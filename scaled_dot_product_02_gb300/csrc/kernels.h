@@ -196,7 +196,7 @@ struct NormRopeParams {
   int max_pos;
   const int32_t* pos;          // [rows]; nullptr: cache positions (append)
   void *q_out, *k_out;         // contiguous (k_out: not for the append)
-  int parts;                   // warps that share one token's heads
+  int parts, parts_q, parts_k;  // warps that share one token, its q heads, its k (and v) heads
   // append: the batch and the cache
   int batch, max_pages, num_pages, page_size;
   const int32_t *cu_q, *kv_lens, *table_ids;
@@ -221,15 +221,19 @@ struct NormRopeBwdParams {
   const int32_t* pos;
   void *dq, *dk;
   long long dqs, dks;
-  float* part;                 // [blocks][2][D] partial sums of dw
+  float* part;                 // [blocks][D] partial sums of dw
   float *dwq, *dwk;
-  int parts, blocks;
+  int parts_q, parts_k;        // warps that share one token's heads
+  int blocks_q, blocks;        // blocks that serve q, all blocks
   int* err;
   AddrTable* chk;
 };
-// Blocks of the backward (each writes one partial sum of dw): a function of
-// the problem and the device alone, so the order of the sums is fixed.
-int norm_rope_bwd_blocks(long long rows, int hq, int hkv, int head_dim, int* parts);
+// How the backward is cut (each block writes one partial sum of dw): a function
+// of the problem alone, so the order of the sums is fixed.
+struct NormRopeBwdPlan {
+  int parts_q, parts_k, blocks_q, blocks;
+};
+NormRopeBwdPlan norm_rope_bwd_plan(long long rows, int hq, int hkv, int head_dim);
 int launch_norm_rope_bwd(const NormRopeBwdParams& p, int head_dim, bool bf16, int* launches, cudaStream_t s);
 
 // Attention over a paged cache: paged.cu serves sequences with few query rows,

@@ -12,16 +12,19 @@
 // Memory-bound: every row is read once and written once. A row is shared by
 // LPH lanes of a warp, each holding VPL 16-byte vectors of it, so a warp reads
 // SUB = 32 / LPH rows of one token side by side and the statistics are one
-// butterfly over LPH lanes. A warp walks the heads of its share of a token
-// with UNROLL rows per lane in flight, and keeps the token's cosines and sines
-// and the weights in registers. A pair (i, i + rot/2) lies in two vectors: the
-// partner's vector is loaded a second time (an L1 hit, issued with the first
-// load), which serves every rot with one code path and no exchange of lanes.
+// butterfly over LPH lanes. What keeps it from the memory's rate is the number
+// of instructions per value, so a token's cosines and sines and the weights
+// are folded into two coefficients a value, shared by all heads of a warp:
+//   y' = r (x A + z B),   A = w cos,  B = +-(partner's w) sin,  z = x's partner,
+// in packed pairs. A pair (i, i + rot/2) lies in two vectors: the partner's
+// vector is loaded a second time (an L1 hit, issued with the first load), which
+// serves every rot with one code path and no exchange of lanes.
 #include <algorithm>
 #include <cuda_runtime.h>
 
 #include "common.cuh"
 #include "kernels.h"
+#include "ptx.cuh"
 
 namespace sdpa {
 
@@ -33,13 +36,17 @@ constexpr int kWarps = kThreads / 32;
 template <int D>
 struct Row {
   static constexpr int VECS = D / 8;  // 16-byte vectors of a row
-  static constexpr int LPH = D == 128 ? 16 : (D == 192 ? 8 : 32);
-  static constexpr int VPL = VECS / LPH;
+  static constexpr int LPH = D == 128 ? 16 : 32;           // D = 192: the last eight lanes of a row idle
+  static constexpr int VPL = (VECS + LPH - 1) / LPH;
   static constexpr int SUB = 32 / LPH;
-  static constexpr int UNROLL = 4 / VPL > 1 ? 4 / VPL : 1;
+  static constexpr int UNROLL = 4 / VPL > 1 ? 4 / VPL : 1;  // rows a lane has in flight
+  static constexpr int STEP = SUB * UNROLL;                 // heads of one step of a warp
+  // heads of one tensor that a warp takes: a step, or several where a step is so
+  // few rows that loading the angles for it would cost as much as the rows
+  static constexpr int HEADS = STEP > 4 ? STEP : 4;
   static constexpr int DV = D == 192 ? 128 : D;  // width of a value row
-  static constexpr int VPL_V = DV / 8 / LPH;
-  static_assert(VPL * LPH == VECS && VPL_V * LPH == DV / 8, "rows are whole vectors of their lanes");
+  // whether vector idx lies in a row of `width` values (always, but for the idle lanes)
+  static __device__ __forceinline__ bool in(int idx, int width) { return VPL * LPH == DV / 8 || idx * 8 < width; }
 };
 
 __device__ __forceinline__ uint4 load16(AddrTable* chk, const void* p) {
@@ -53,18 +60,15 @@ __device__ __forceinline__ int load_i32(AddrTable* chk, const int32_t* p, int ot
 }
 
 template <class E>
-__device__ __forceinline__ void unpack8(const uint4& x, float (&f)[8]) {
-  const uint32_t u[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const float2 t = E::unpack(u[e]);
-    f[2 * e] = t.x;
-    f[2 * e + 1] = t.y;
-  }
+__device__ __forceinline__ void unpack8(const uint4& x, float2 (&f)[4]) {
+  f[0] = E::unpack(x.x);
+  f[1] = E::unpack(x.y);
+  f[2] = E::unpack(x.z);
+  f[3] = E::unpack(x.w);
 }
 template <class E>
-__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
-  return make_uint4(E::pack(f[0], f[1]), E::pack(f[2], f[3]), E::pack(f[4], f[5]), E::pack(f[6], f[7]));
+__device__ __forceinline__ uint4 pack8(const float2 (&f)[4]) {
+  return make_uint4(E::pack(f[0].x, f[0].y), E::pack(f[1].x, f[1].y), E::pack(f[2].x, f[2].y), E::pack(f[3].x, f[3].y));
 }
 
 template <int LPH>
@@ -73,68 +77,66 @@ __device__ __forceinline__ float row_sum(float v) {
   for (int o = LPH / 2; o > 0; o /= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
-
-// A lane's share of one token's rotation: for each of its vectors whether it
-// turns, the vector its pairs' other halves lie in (itself for adjacent pairs),
-// and the eight cosines and sines; the sine carries the sign of the half.
-template <int VPL>
-struct Turn {
-  bool on[VPL];
-  int partner[VPL];
-  float c[VPL][8], s[VPL][8];
-};
-
-template <int D>
-__device__ __forceinline__ void load_turn(Turn<Row<D>::VPL>& t, const float* row, int rot, bool interleaved, int sub,
-                                          AddrTable* chk) {
-  using R = Row<D>;
-  const int half = rot / 2;
+// Both sums over the LPH lanes of a row, with one exchange more than one sum's:
+// half of the lanes reduce a, the other half b.
+template <int LPH>
+__device__ __forceinline__ void row_sums(float& a, float& b, int lane) {
+  constexpr int H = LPH / 2;
+  const bool up = lane & H;
+  float v = (up ? b : a) + __shfl_xor_sync(0xffffffffu, up ? a : b, H);
 #pragma unroll
-  for (int v = 0; v < R::VPL; ++v) {
-    const int idx = v * R::LPH + sub;
-    t.on[v] = idx * 8 < rot;
-    t.partner[v] = idx;
-    if (!t.on[v]) continue;
-    if (interleaved) {
-      const uint4 c = load16(chk, row + idx * 4), s = load16(chk, row + half + idx * 4);
-      const uint32_t cu[4] = {c.x, c.y, c.z, c.w}, su[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        t.c[v][2 * e] = t.c[v][2 * e + 1] = __uint_as_float(cu[e]);
-        t.s[v][2 * e] = -__uint_as_float(su[e]);
-        t.s[v][2 * e + 1] = __uint_as_float(su[e]);
-      }
-    } else {
-      const bool second = idx * 8 >= half;  // half is a multiple of 8: a vector lies in one half
-      t.partner[v] = second ? idx - half / 8 : idx + half / 8;
-      const int i0 = idx * 8 - (second ? half : 0);
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        const uint4 c = load16(chk, row + i0 + q * 4), s = load16(chk, row + half + i0 + q * 4);
-        const uint32_t cu[4] = {c.x, c.y, c.z, c.w}, su[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          t.c[v][q * 4 + e] = __uint_as_float(cu[e]);
-          t.s[v][q * 4 + e] = second ? __uint_as_float(su[e]) : -__uint_as_float(su[e]);
-        }
-      }
-    }
-  }
+  for (int o = H / 2; o > 0; o /= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
+  const float w = __shfl_xor_sync(0xffffffffu, v, H);
+  a = up ? w : v;
+  b = up ? v : w;
 }
 
-// One vector turned: y the values, z their partners' values (the other halves'
-// vector, or for adjacent pairs y itself with neighbours exchanged).
-// sign = -1 turns back.
-__device__ __forceinline__ void turn8(float (&y)[8], const float (&z)[8], const float (&c)[8], const float (&s)[8],
-                                      bool interleaved, float sign) {
-  float o[8];
+// Which of a lane's vectors turns, and the vector that holds its pairs' other
+// halves (itself for adjacent pairs).
+struct Place {
+  bool on, second;
+  int partner;
+};
+__device__ __forceinline__ Place place_of(int idx, int rot, bool interleaved) {
+  Place t;
+  const int half = rot / 2;  // a multiple of 8: a vector lies in one half
+  t.on = idx * 8 < rot;
+  t.second = !interleaved && idx * 8 >= half;
+  t.partner = !t.on || interleaved ? idx : t.second ? idx - half / 8 : idx + half / 8;
+  return t;
+}
+// The cosines of vector idx and its sines, signed for turning forwards: value e
+// becomes y_e c_e + partner_e s_e.
+__device__ __forceinline__ void angles_of(const Place& t, int idx, const float* row, int rot, bool interleaved,
+                                          float2 (&c)[4], float2 (&s)[4], AddrTable* chk) {
+  const int half = rot / 2;
+  if (!t.on) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const float other = interleaved ? y[e ^ 1] : z[e];
-    o[e] = fmaf(other, sign * s[e], y[e] * c[e]);
+    for (int e = 0; e < 4; ++e) {
+      c[e] = make_float2(1.f, 1.f);
+      s[e] = make_float2(0.f, 0.f);
+    }
+  } else if (interleaved) {
+    const uint4 a = load16(chk, row + idx * 4), b = load16(chk, row + half + idx * 4);
+    const float cs[4] = {__uint_as_float(a.x), __uint_as_float(a.y), __uint_as_float(a.z), __uint_as_float(a.w)};
+    const float sn[4] = {__uint_as_float(b.x), __uint_as_float(b.y), __uint_as_float(b.z), __uint_as_float(b.w)};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      c[e] = make_float2(cs[e], cs[e]);
+      s[e] = make_float2(-sn[e], sn[e]);
+    }
+  } else {
+    const int i0 = idx * 8 - (t.second ? half : 0);
+    const float sg = t.second ? 1.f : -1.f;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const uint4 a = load16(chk, row + i0 + q * 4), b = load16(chk, row + half + i0 + q * 4);
+      c[2 * q] = make_float2(__uint_as_float(a.x), __uint_as_float(a.y));
+      c[2 * q + 1] = make_float2(__uint_as_float(a.z), __uint_as_float(a.w));
+      s[2 * q] = make_float2(sg * __uint_as_float(b.x), sg * __uint_as_float(b.y));
+      s[2 * q + 1] = make_float2(sg * __uint_as_float(b.z), sg * __uint_as_float(b.w));
+    }
   }
-#pragma unroll
-  for (int e = 0; e < 8; ++e) y[e] = o[e];
 }
 
 // Where a token of the packed batch goes in the cache.
@@ -178,9 +180,10 @@ __device__ __forceinline__ Slot find_slot(const NormRopeParams& p, long long row
   return s;
 }
 
-// Heads of a token in order: q, k and (append) v; p.parts warps share a token.
+// A warp takes Row::HEADS heads of one tensor (q, k or, appending, v) of one token.
 template <bool BF16, int D, bool APPEND, bool NORM>
-__global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
+__global__ void __launch_bounds__(kThreads, Row<D>::VPL == 1 ? 6 : 4)
+    norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
   using E = Elem<BF16>;
   using T = typename E::T;
   using R = Row<D>;
@@ -188,291 +191,286 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
   const long long w = (long long)blockIdx.x * kWarps + threadIdx.x / 32;
   const long long row = w / p.parts;
   if (row >= p.rows) return;
-  const int part = (int)(w - row * p.parts);
-  const int heads = p.hq + (APPEND ? 2 : 1) * p.hkv;
-  const int per = (heads + p.parts - 1) / p.parts;
-  const int h_end = min(heads, (part + 1) * per);
+  int part = (int)(w - row * p.parts);
+  const bool is_q = part < p.parts_q;
+  if (!is_q) part -= p.parts_q;
+  const bool is_v = APPEND && !is_q && part >= p.parts_k;
+  if (is_v) part -= p.parts_k;
+  const int heads = is_q ? p.hq : p.hkv;
+  const int h_end = min(heads, (part + 1) * R::HEADS);
+  const int width = is_v ? R::DV : D;
+  const T* src = is_q   ? static_cast<const T*>(p.q) + row * p.qs
+                 : is_v ? static_cast<const T*>(p.v) + row * p.vs
+                        : static_cast<const T*>(p.k) + row * p.ks;
+  const bool inter = p.interleaved != 0;
+  Place at[R::VPL];
+#pragma unroll
+  for (int v = 0; v < R::VPL; ++v) at[v] = place_of(v * R::LPH + sub, NORM ? p.rot : 0, inter);
+
+  uint4 x[R::UNROLL][R::VPL], z[R::UNROLL][R::VPL];
+  auto fetch = [&](int h0) {
+#pragma unroll
+    for (int u = 0; u < R::UNROLL; ++u) {
+      const int h = h0 + grp + u * R::SUB;
+#pragma unroll
+      for (int v = 0; v < R::VPL; ++v) {
+        const bool in = h < h_end && R::in(v * R::LPH + sub, width);
+        x[u][v] = z[u][v] = make_uint4(0u, 0u, 0u, 0u);
+        if (in) x[u][v] = load16(p.chk, src + h * width + (v * R::LPH + sub) * 8);
+        if (NORM && in && !is_v && at[v].on && !inter) z[u][v] = load16(p.chk, src + h * width + at[v].partner * 8);
+      }
+    }
+  };
+  int h0 = part * R::HEADS;
+  fetch(h0);
 
   Slot slot;
   if (APPEND) {
     slot = find_slot(p, row, lane);
     if (!slot.live) return;
   }
-  Turn<R::VPL> turn;
-  const bool inter = p.interleaved != 0;
-  uint4 wq[R::VPL], wk[R::VPL], wqp[R::VPL], wkp[R::VPL];
-  if (NORM) {
+  // where head h of this tensor goes
+  T* dst = is_q ? static_cast<T*>(p.q_out) + row * p.hq * D : static_cast<T*>(p.k_out) + row * p.hkv * D;
+  long long step = D;
+  if (APPEND && !is_q) {
+    dst = is_v ? static_cast<T*>(p.vc) + slot.v_at : static_cast<T*>(p.kc) + slot.k_at;
+    step = is_v ? p.vc_head : p.kc_head;
+  }
+  float2 ca[R::VPL][4], cb[R::VPL][4];
+  if (NORM && !is_v) {
+    const float* angles = nullptr;
     if (p.rot > 0) {
       const int pos = APPEND && !p.pos ? slot.position : load_i32(p.chk, p.pos + row, -1);
       if (pos < 0 || pos >= p.max_pos) {
         if (lane == 0) record_error(p.err, SDPA_ERR_BAD_INDEX);
         return;
       }
-      load_turn<D>(turn, p.table + (long long)pos * p.rot, p.rot, inter, sub, p.chk);
-    } else {
-#pragma unroll
-      for (int v = 0; v < R::VPL; ++v) {
-        turn.on[v] = false;
-        turn.partner[v] = v * R::LPH + sub;
-      }
+      angles = p.table + (long long)pos * p.rot;
     }
+    const T* weight = static_cast<const T*>(is_q ? p.wq : p.wk);
 #pragma unroll
     for (int v = 0; v < R::VPL; ++v) {
-      const int own = (v * R::LPH + sub) * 8, other = turn.partner[v] * 8;
-      wk[v] = load16(p.chk, static_cast<const T*>(p.wk) + own);
-      wkp[v] = load16(p.chk, static_cast<const T*>(p.wk) + other);
-      if (p.hq > 0) {
-        wq[v] = load16(p.chk, static_cast<const T*>(p.wq) + own);
-        wqp[v] = load16(p.chk, static_cast<const T*>(p.wq) + other);
+      const int idx = v * R::LPH + sub;
+      float2 c[4], s[4], wt[4], wp[4];
+      const bool in = R::in(idx, D);
+      unpack8<E>(in ? load16(p.chk, weight + idx * 8) : make_uint4(0u, 0u, 0u, 0u), wt);
+      unpack8<E>(in ? load16(p.chk, weight + at[v].partner * 8) : make_uint4(0u, 0u, 0u, 0u), wp);
+      angles_of(at[v], idx, angles, p.rot, inter, c, s, p.chk);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        ca[v][e] = fmul2(wt[e], c[e]);
+        cb[v][e] = fmul2(inter ? make_float2(wp[e].y, wp[e].x) : wp[e], s[e]);
       }
     }
+  } else if (NORM && APPEND && p.rot > 0 && p.pos) {
+    const int pos = load_i32(p.chk, p.pos + row, -1);  // a token with a bad position is skipped whole
+    if (pos < 0 || pos >= p.max_pos) return;
   }
 
-  for (int h0 = part * per + grp; __any_sync(0xffffffffu, h0 < h_end); h0 += R::SUB * R::UNROLL) {
-    uint4 x[R::UNROLL][R::VPL], z[R::UNROLL][R::VPL];
+  while (true) {
 #pragma unroll
     for (int u = 0; u < R::UNROLL; ++u) {
-      const int h = h0 + u * R::SUB;
-      const bool is_v = APPEND && h >= p.hq + p.hkv;
-      const T* src = h < p.hq ? static_cast<const T*>(p.q) + row * p.qs + (long long)h * D
-                     : !is_v  ? static_cast<const T*>(p.k) + row * p.ks + (long long)(h - p.hq) * D
-                              : static_cast<const T*>(p.v) + row * p.vs + (long long)(h - p.hq - p.hkv) * R::DV;
-#pragma unroll
-      for (int v = 0; v < R::VPL; ++v) {
-        const bool in = h < h_end && (!is_v || v < R::VPL_V);
-        x[u][v] = z[u][v] = make_uint4(0u, 0u, 0u, 0u);
-        if (in) x[u][v] = load16(p.chk, src + (v * R::LPH + sub) * 8);
-        if (NORM && !inter && in && !is_v && turn.on[v]) z[u][v] = load16(p.chk, src + turn.partner[v] * 8);
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < R::UNROLL; ++u) {
-      const int h = h0 + u * R::SUB;
-      const bool is_q = h < p.hq, is_v = APPEND && h >= p.hq + p.hkv;
-      if (NORM) {
-        float ss = 0.f;
+      const int h = h0 + grp + u * R::SUB;
+      if (NORM && !is_v) {
+        float2 f[R::VPL][4], ss = make_float2(0.f, 0.f);
 #pragma unroll
         for (int v = 0; v < R::VPL; ++v) {
-          float f[8];
-          unpack8<E>(x[u][v], f);
+          unpack8<E>(x[u][v], f[v]);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) ss = fmaf(f[e], f[e], ss);
+          for (int e = 0; e < 4; ++e) ss = ffma2(f[v][e], f[v][e], ss);
         }
-        const float r = rsqrtf(row_sum<R::LPH>(ss) * (1.f / D) + p.eps);
-        if (!is_v) {
+        const float r1 = rsqrtf(row_sum<R::LPH>(ss.x + ss.y) * (1.f / D) + p.eps);
+        const float2 r = make_float2(r1, r1);
 #pragma unroll
-          for (int v = 0; v < R::VPL; ++v) {
-            float f[8], wt[8];
-            unpack8<E>(x[u][v], f);
-            unpack8<E>(is_q ? wq[v] : wk[v], wt);
+        for (int v = 0; v < R::VPL; ++v) {
+          float2 g[4];
+          unpack8<E>(z[u][v], g);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] = f[e] * r * wt[e];
-            if (turn.on[v]) {
-              float g[8];
-              unpack8<E>(z[u][v], g);
-              unpack8<E>(is_q ? wqp[v] : wkp[v], wt);
-#pragma unroll
-              for (int e = 0; e < 8; ++e) g[e] = g[e] * r * wt[e];
-              turn8(f, g, turn.c[v], turn.s[v], inter, 1.f);
-            }
-            x[u][v] = pack8<E>(f);
+          for (int e = 0; e < 4; ++e) {
+            const float2 other = inter ? make_float2(f[v][e].y, f[v][e].x) : g[e];
+            const float2 t = fmul2(f[v][e], ca[v][e]);
+            g[e] = fmul2(at[v].on ? ffma2(other, cb[v][e], t) : t, r);
           }
+          x[u][v] = pack8<E>(g);
         }
       }
       if (h >= h_end) continue;
-      T* dst;
-      if (is_q)
-        dst = static_cast<T*>(p.q_out) + (row * p.hq + h) * D;
-      else if (!APPEND)
-        dst = static_cast<T*>(p.k_out) + (row * p.hkv + (h - p.hq)) * D;
-      else if (!is_v)
-        dst = static_cast<T*>(p.kc) + slot.k_at + (h - p.hq) * p.kc_head;
-      else
-        dst = static_cast<T*>(p.vc) + slot.v_at + (h - p.hq - p.hkv) * p.vc_head;
 #pragma unroll
       for (int v = 0; v < R::VPL; ++v)
-        if (!is_v || v < R::VPL_V) store16(p.chk, dst + (v * R::LPH + sub) * 8, x[u][v]);
+        if (R::in(v * R::LPH + sub, width)) store16(p.chk, dst + h * step + (v * R::LPH + sub) * 8, x[u][v]);
     }
+    h0 += R::STEP;
+    if (h0 >= h_end) break;
+    fetch(h0);
   }
 }
 
-// Gradient. Each block walks (token, share of its heads) in strides of the
-// grid, keeps the sums of dw in registers (one set for q, one for k), and
-// writes one partial sum per block; dw_kernel adds the blocks' in order.
+// Gradient. Blocks [0, blocks_q) serve q, the others k, in proportion to their
+// heads, so a block holds one tensor's weights and one set of sums. Its warps
+// walk (token, share of the heads) in strides of their blocks, keep the sums
+// of dw in registers, and write one partial sum per block; dw_kernel adds the
+// blocks' in order.
+constexpr int kBwdThreads = 256;
+constexpr int kBwdWarps = kBwdThreads / 32;
+
 template <bool BF16, int D>
-__global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(const __grid_constant__ NormRopeBwdParams p) {
+__global__ void __launch_bounds__(kBwdThreads, 2) norm_rope_bwd_kernel(const __grid_constant__ NormRopeBwdParams p) {
   using E = Elem<BF16>;
   using T = typename E::T;
   using R = Row<D>;
-  constexpr int UN = R::VPL == 1 ? 2 : 1;
+  constexpr int UN = R::VPL == 1 ? 2 : 1;  // rows a lane has in flight: three loads each
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int lane = threadIdx.x % 32, sub = lane % R::LPH, grp = lane / R::LPH, warp = threadIdx.x / 32;
-  const int heads = p.hq + p.hkv, per = (heads + p.parts - 1) / p.parts;
-  const long long units = p.rows * p.parts;
+  const bool is_q = (int)blockIdx.x < p.blocks_q;
+  const int block = is_q ? blockIdx.x : blockIdx.x - p.blocks_q, blocks = is_q ? p.blocks_q : p.blocks - p.blocks_q;
+  const int heads = is_q ? p.hq : p.hkv, parts = is_q ? p.parts_q : p.parts_k, per = (heads + parts - 1) / parts;
+  const long long units = p.rows * parts, xs = is_q ? p.qs : p.ks, ds = is_q ? p.dqs : p.dks;
+  const T* const x0 = static_cast<const T*>(is_q ? p.q : p.k);
+  const T* const g0 = static_cast<const T*>(is_q ? p.gq : p.gk);
+  T* const d0 = static_cast<T*>(is_q ? p.dq : p.dk);
   const bool inter = p.interleaved != 0;
-  uint4 wq[R::VPL], wk[R::VPL];
-  float aq[R::VPL][8], ak[R::VPL][8];
+  Place at[R::VPL];
+  float2 wt[R::VPL][4], acc[R::VPL][4];
 #pragma unroll
   for (int v = 0; v < R::VPL; ++v) {
-    wq[v] = load16(p.chk, static_cast<const T*>(p.wq) + (v * R::LPH + sub) * 8);
-    wk[v] = load16(p.chk, static_cast<const T*>(p.wk) + (v * R::LPH + sub) * 8);
+    at[v] = place_of(v * R::LPH + sub, p.rot, inter);
+    unpack8<E>(R::in(v * R::LPH + sub, D) ? load16(p.chk, static_cast<const T*>(is_q ? p.wq : p.wk) + (v * R::LPH + sub) * 8)
+                                          : make_uint4(0u, 0u, 0u, 0u),
+               wt[v]);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) aq[v][e] = ak[v][e] = 0.f;
+    for (int e = 0; e < 4; ++e) acc[v][e] = make_float2(0.f, 0.f);
   }
-  for (long long w = (long long)blockIdx.x * kWarps + warp; w < units; w += (long long)gridDim.x * kWarps) {
-    const long long row = w / p.parts;
-    const int part = (int)(w - row * p.parts), h_end = min(heads, (part + 1) * per);
-    Turn<R::VPL> turn;
-    bool skip = false;  // a position outside the table: zeros
-    if (p.rot > 0) {
-      const int pos = load_i32(p.chk, p.pos + row, -1);
-      skip = pos < 0 || pos >= p.max_pos;
-      if (skip && lane == 0) record_error(p.err, SDPA_ERR_BAD_INDEX);
-      load_turn<D>(turn, p.table + (skip ? 0ll : (long long)pos * p.rot), p.rot, inter, sub, p.chk);
-    } else {
-#pragma unroll
-      for (int v = 0; v < R::VPL; ++v) {
-        turn.on[v] = false;
-        turn.partner[v] = v * R::LPH + sub;
-      }
-    }
-    for (int h0 = part * per + grp; __any_sync(0xffffffffu, h0 < h_end); h0 += R::SUB * UN) {
-      uint4 x[UN][R::VPL], y[UN][R::VPL], z[UN][R::VPL];
+  const long long stride = (long long)blocks * kBwdWarps;
+  long long w = (long long)block * kBwdWarps + warp;
+  int next_pos = w < units && p.rot > 0 ? load_i32(p.chk, p.pos + w / parts, -1) : 0;
+  for (; w < units; w += stride) {
+    const long long row = w / parts;
+    const int part = (int)(w - row * parts), h_end = min(heads, (part + 1) * per);
+    const int pos = next_pos;
+    const bool skip = p.rot > 0 && (pos < 0 || pos >= p.max_pos);  // a position outside the table: zeros
+    if (skip && lane == 0) record_error(p.err, SDPA_ERR_BAD_INDEX);
+    uint4 x[UN][R::VPL], y[UN][R::VPL], z[UN][R::VPL];
+    auto fetch = [&](int h0) {
 #pragma unroll
       for (int u = 0; u < UN; ++u) {
-        const int h = h0 + u * R::SUB;
-        const bool is_q = h < p.hq;
-        const T* xs = is_q ? static_cast<const T*>(p.q) + row * p.qs + (long long)h * D
-                           : static_cast<const T*>(p.k) + row * p.ks + (long long)(h - p.hq) * D;
-        const T* gs = is_q ? static_cast<const T*>(p.gq) + (row * p.hq + h) * D
-                           : static_cast<const T*>(p.gk) + (row * p.hkv + (h - p.hq)) * D;
-        const bool in = h < h_end && !skip;
+        const int h = h0 + grp + u * R::SUB;
+        const bool row_in = h < h_end && !skip;
+        const T* xr = x0 + row * xs + h * D;
+        const T* gr = g0 + (row * heads + h) * D;
 #pragma unroll
         for (int v = 0; v < R::VPL; ++v) {
+          const bool in = row_in && R::in(v * R::LPH + sub, D);
           x[u][v] = y[u][v] = z[u][v] = make_uint4(0u, 0u, 0u, 0u);
-          if (in) x[u][v] = load16(p.chk, xs + (v * R::LPH + sub) * 8);
-          if (in) y[u][v] = load16(p.chk, gs + (v * R::LPH + sub) * 8);
-          if (in && !inter && turn.on[v]) z[u][v] = load16(p.chk, gs + turn.partner[v] * 8);
+          if (in) x[u][v] = load16(p.chk, xr + (v * R::LPH + sub) * 8);
+          if (in) y[u][v] = load16(p.chk, gr + (v * R::LPH + sub) * 8);
+          if (in && at[v].on && !inter) z[u][v] = load16(p.chk, gr + at[v].partner * 8);
         }
       }
+    };
+    int h0 = part * per;
+    fetch(h0);
+    if (p.rot > 0 && w + stride < units) next_pos = load_i32(p.chk, p.pos + (w + stride) / parts, -1);
+    float2 c[R::VPL][4], s[R::VPL][4];
+#pragma unroll
+    for (int v = 0; v < R::VPL; ++v)
+      angles_of(at[v], v * R::LPH + sub, p.table + (skip ? 0ll : (long long)pos * p.rot), p.rot, inter, c[v], s[v], p.chk);
+    while (true) {
 #pragma unroll
       for (int u = 0; u < UN; ++u) {
-        const int h = h0 + u * R::SUB;
-        const bool is_q = h < p.hq;
-        float ss = 0.f, dot = 0.f;
-        float g[R::VPL][8];
+        const int h = h0 + grp + u * R::SUB;
+        float2 f[R::VPL][4], g[R::VPL][4];
+        float2 ss = make_float2(0.f, 0.f), dot = make_float2(0.f, 0.f);
 #pragma unroll
         for (int v = 0; v < R::VPL; ++v) {
-          float f[8], o[8], wt[8];
-          unpack8<E>(x[u][v], f);
+          float2 o[4];
+          unpack8<E>(x[u][v], f[v]);
           unpack8<E>(y[u][v], g[v]);
-          if (turn.on[v]) {
-            unpack8<E>(z[u][v], o);
-            turn8(g[v], o, turn.c[v], turn.s[v], inter, -1.f);
-          }
-          unpack8<E>(is_q ? wq[v] : wk[v], wt);
+          unpack8<E>(z[u][v], o);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            ss = fmaf(f[e], f[e], ss);
-            dot = fmaf(g[v][e] * wt[e], f[e], dot);
+          for (int e = 0; e < 4; ++e) {
+            // turned back: y c - partner s
+            const float2 other = inter ? make_float2(-g[v][e].y, -g[v][e].x) : make_float2(-o[e].x, -o[e].y);
+            if (at[v].on) g[v][e] = ffma2(other, s[v][e], fmul2(g[v][e], c[v][e]));
+            ss = ffma2(f[v][e], f[v][e], ss);
+            dot = ffma2(fmul2(g[v][e], wt[v][e]), f[v][e], dot);
           }
         }
-#pragma unroll
-        for (int o = R::LPH / 2; o > 0; o /= 2) {
-          ss += __shfl_xor_sync(0xffffffffu, ss, o);
-          dot += __shfl_xor_sync(0xffffffffu, dot, o);
-        }
+        float a = ss.x + ss.y, b = dot.x + dot.y;
+        row_sums<R::LPH>(a, b, lane);
         if (h >= h_end) continue;
-        const float r = skip ? 0.f : rsqrtf(ss * (1.f / D) + p.eps), k3 = r * r * r * (dot * (1.f / D));
-        T* dst = is_q ? static_cast<T*>(p.dq) + row * p.dqs + (long long)h * D
-                      : static_cast<T*>(p.dk) + row * p.dks + (long long)(h - p.hq) * D;
+        const float r1 = skip ? 0.f : rsqrtf(a * (1.f / D) + p.eps), k1 = -r1 * r1 * r1 * (b * (1.f / D));
+        const float2 r = make_float2(r1, r1), k3 = make_float2(k1, k1);
+        T* dst = d0 + row * ds + h * D;
 #pragma unroll
         for (int v = 0; v < R::VPL; ++v) {
-          float f[8], wt[8];
-          unpack8<E>(x[u][v], f);
-          unpack8<E>(is_q ? wq[v] : wk[v], wt);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float t = g[v][e] * f[e] * r;
-            aq[v][e] += is_q ? t : 0.f;
-            ak[v][e] += is_q ? 0.f : t;
-            f[e] = fmaf(-k3, f[e], r * g[v][e] * wt[e]);
+          for (int e = 0; e < 4; ++e) {
+            const float2 gr = fmul2(g[v][e], r);
+            acc[v][e] = ffma2(gr, f[v][e], acc[v][e]);
+            f[v][e] = ffma2(k3, f[v][e], fmul2(gr, wt[v][e]));
           }
-          store16(p.chk, dst + (v * R::LPH + sub) * 8, pack8<E>(f));
+          if (R::in(v * R::LPH + sub, D)) store16(p.chk, dst + (v * R::LPH + sub) * 8, pack8<E>(f[v]));
         }
       }
+      h0 += R::SUB * UN;
+      if (h0 >= h_end) break;
+      fetch(h0);
     }
   }
   // the block's sum of dw: row groups of a warp by shuffles, warps in order
-  __shared__ float sum[kWarps][2][D];
+  __shared__ float sum[kBwdWarps][D];
 #pragma unroll
   for (int v = 0; v < R::VPL; ++v)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
+    for (int e = 0; e < 4; ++e) {
 #pragma unroll
       for (int o = R::LPH; o < 32; o *= 2) {
-        aq[v][e] += __shfl_xor_sync(0xffffffffu, aq[v][e], o);
-        ak[v][e] += __shfl_xor_sync(0xffffffffu, ak[v][e], o);
+        acc[v][e].x += __shfl_xor_sync(0xffffffffu, acc[v][e].x, o);
+        acc[v][e].y += __shfl_xor_sync(0xffffffffu, acc[v][e].y, o);
       }
-      if (grp == 0) {
-        sum[warp][0][(v * R::LPH + sub) * 8 + e] = aq[v][e];
-        sum[warp][1][(v * R::LPH + sub) * 8 + e] = ak[v][e];
-      }
+      if (grp == 0 && R::in(v * R::LPH + sub, D)) *reinterpret_cast<float2*>(&sum[warp][(v * R::LPH + sub) * 8 + 2 * e]) = acc[v][e];
     }
   __syncthreads();
-  for (int i = threadIdx.x; i < 2 * D; i += kThreads) {
+  for (int i = threadIdx.x; i < D; i += kBwdThreads) {
     float t = 0.f;
 #pragma unroll
-    for (int k = 0; k < kWarps; ++k) t += sum[k][i / D][i % D];
-    float* at = p.part + (long long)blockIdx.x * 2 * D + i;
-    if (SDPA_ADDR_OK(p.chk, at, 4)) *at = t;
+    for (int k = 0; k < kBwdWarps; ++k) t += sum[k][i];
+    float* to = p.part + (long long)blockIdx.x * D + i;
+    if (SDPA_ADDR_OK(p.chk, to, 4)) *to = t;
   }
 }
 
-// dw = the blocks' partial sums, added in a fixed order: 32 columns per CTA,
-// eight threads a column, each over every eighth block.
-__global__ void __launch_bounds__(256) dw_kernel(const float* part, int blocks, int d, float* dwq, float* dwk,
-                                                 AddrTable* chk) {
-  __shared__ float sum[8][32];
-  const int col = blockIdx.x * 32 + threadIdx.x % 32, k = threadIdx.x / 32;
+// dw = the blocks' partial sums, added in a fixed order: 16 columns of q's or
+// k's weights per CTA, 32 threads a column, each over every 32nd block.
+__global__ void __launch_bounds__(512) dw_kernel(const float* part, int blocks_q, int blocks, int d, float* dwq,
+                                                 float* dwk, AddrTable* chk) {
+  __shared__ float sum[32][17];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int x = threadIdx.x % 16, k = threadIdx.x / 16, at = blockIdx.x * 16 + x;
+  const bool is_q = at < d;
+  const int col = is_q ? at : at - d, end = is_q ? blocks_q : blocks;
   float t = 0.f;
 #pragma unroll 8
-  for (int b = k; b < blocks; b += 8) {
-    const float* at = part + (long long)b * 2 * d + col;
-    t += SDPA_ADDR_OK(chk, at, 4) ? *at : 0.f;
+  for (int b = (is_q ? 0 : blocks_q) + k; b < end; b += 32) {
+    const float* from = part + (long long)b * d + col;
+    t += SDPA_ADDR_OK(chk, from, 4) ? *from : 0.f;
   }
-  sum[k][threadIdx.x % 32] = t;
+  sum[k][x] = t;
   __syncthreads();
   if (k == 0) {
 #pragma unroll
-    for (int i = 1; i < 8; ++i) t += sum[i][threadIdx.x % 32];
-    float* at = col < d ? dwq + col : dwk + (col - d);
-    if (SDPA_ADDR_OK(chk, at, 4)) *at = t;
+    for (int i = 1; i < 32; ++i) t += sum[i][x];
+    float* to = is_q ? dwq + col : dwk + col;
+    if (SDPA_ADDR_OK(chk, to, 4)) *to = t;
   }
-}
-
-// Warps that share a token's heads: one when there are tokens enough for
-// `want` warps (the token's angles and the weights are then loaded once), else
-// more, down to one unrolled step of heads per warp.
-int share(long long rows, int heads, int step, long long want) {
-  const long long most = (heads + step - 1) / step;
-  return (int)std::max<long long>(1, std::min(most, (want + rows - 1) / std::max<long long>(rows, 1)));
-}
-
-int sm_count(int* sms) {
-  int dev = 0;
-  return cudaGetDevice(&dev) == cudaSuccess &&
-                 cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess
-             ? SDPA_OK
-             : SDPA_ERR_CUDA;
 }
 
 template <bool BF16, int D>
 int launch_t(NormRopeParams p, bool append, cudaStream_t s) {
   using R = Row<D>;
-  int sms = 0;
-  if (const int rc = sm_count(&sms)) return rc;
-  const int heads = p.hq + (append ? 2 : 1) * p.hkv;
-  p.parts = share(p.rows, heads, R::SUB * R::UNROLL, (long long)sms * 32);
+  p.parts_q = (p.hq + R::HEADS - 1) / R::HEADS;
+  p.parts_k = (p.hkv + R::HEADS - 1) / R::HEADS;
+  p.parts = p.parts_q + (append ? 2 : 1) * p.parts_k;
   const long long blocks = (p.rows * p.parts + kWarps - 1) / kWarps;
   if (blocks > 0x7fffffffLL) return SDPA_ERR_UNSUPPORTED;
   const unsigned grid = (unsigned)blocks;
@@ -487,21 +485,44 @@ int launch_t(NormRopeParams p, bool append, cudaStream_t s) {
 
 template <bool BF16, int D>
 int launch_bwd_t(const NormRopeBwdParams& p, cudaStream_t s) {
-  norm_rope_bwd_kernel<BF16, D><<<(unsigned)p.blocks, kThreads, 0, s>>>(p);
+  norm_rope_bwd_kernel<BF16, D><<<(unsigned)p.blocks, kBwdThreads, 0, s>>>(p);
   if (cudaGetLastError() != cudaSuccess) return SDPA_ERR_CUDA;
-  dw_kernel<<<2 * D / 32, 256, 0, s>>>(p.part, p.blocks, D, p.dwq, p.dwk, p.chk);
-  return cudaGetLastError() == cudaSuccess ? SDPA_OK : SDPA_ERR_CUDA;
+  // launched while the kernel above runs; it waits for it before reading
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * D / 16);
+  cfg.blockDim = dim3(512);
+  cfg.stream = s;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, dw_kernel, (const float*)p.part, p.blocks_q, p.blocks, D, p.dwq, p.dwk, p.chk) == cudaSuccess
+             ? SDPA_OK
+             : SDPA_ERR_CUDA;
 }
 
 }  // namespace
 
-int norm_rope_bwd_blocks(long long rows, int hq, int hkv, int head_dim, int* parts) {
-  // written for 152 SMs: the count must not depend on the device in use, since
-  // the workspace size is asked for without one
-  constexpr long long kBlocks = 152 * 6;
-  const int step = head_dim == 128 ? 4 : head_dim == 192 ? 4 : 1;
-  *parts = share(rows, hq + hkv, step, kBlocks * kWarps);
-  return (int)std::max<long long>(1, std::min<long long>(kBlocks, (rows * *parts + kWarps - 1) / kWarps));
+NormRopeBwdPlan norm_rope_bwd_plan(long long rows, int hq, int hkv, int head_dim) {
+  // two blocks on each of the 152 SMs of the device this is written for: the
+  // plan must not depend on the device in use, since the workspace size is
+  // asked for without one, and the order of the sums follows from it
+  constexpr long long kBlocks = 152 * 2;
+  const int step = head_dim == 128 ? 4 : head_dim <= 256 ? 2 : 1;  // heads of one step of a warp
+  // a token's heads shared by several warps only where there are few tokens
+  auto share = [&](int heads) {
+    const long long most = (heads + step - 1) / step, want = kBlocks * kBwdWarps * heads / (hq + hkv);
+    return (int)std::max<long long>(1, std::min(most, (want + rows - 1) / std::max<long long>(rows, 1)));
+  };
+  NormRopeBwdPlan pl;
+  pl.parts_q = share(hq);
+  pl.parts_k = share(hkv);
+  const long long need_q = (rows * pl.parts_q + kBwdWarps - 1) / kBwdWarps, need_k = (rows * pl.parts_k + kBwdWarps - 1) / kBwdWarps;
+  const long long give_q = std::max<long long>(1, std::min(kBlocks - 1, (kBlocks * hq + (hq + hkv) / 2) / (hq + hkv)));
+  pl.blocks_q = (int)std::max<long long>(1, std::min(give_q, need_q));
+  pl.blocks = pl.blocks_q + (int)std::max<long long>(1, std::min(kBlocks - give_q, need_k));
+  return pl;
 }
 
 int launch_norm_rope(NormRopeParams p, int head_dim, bool bf16, bool append, cudaStream_t s) {
