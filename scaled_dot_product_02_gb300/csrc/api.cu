@@ -1033,7 +1033,7 @@ int sdpa_qk_norm_rope(const sdpa_norm_rope_problem* p, const void* q, const void
 
 size_t sdpa_qk_norm_rope_bwd_workspace_size(const sdpa_norm_rope_problem* p) {
   if (check_norm_rope(p) != SDPA_OK || p->rows == 0) return 0;
-  return (size_t)norm_rope_bwd_plan(p->rows, p->num_heads_q, p->num_heads_kv, p->head_dim).blocks * p->head_dim * 4;
+  return (size_t)(norm_rope_bwd_plan(p->rows, p->num_heads_q, p->num_heads_kv, p->head_dim).blocks + 1) * p->head_dim * 4;
 }
 
 int sdpa_qk_norm_rope_bwd(const sdpa_norm_rope_problem* p, const void* dq_out, const void* dk_out, const void* q,
@@ -1089,9 +1089,7 @@ int sdpa_qk_norm_rope_bwd(const sdpa_norm_rope_problem* p, const void* dq_out, c
   L.dwq = dq_weight;
   L.dwk = dk_weight;
   const NormRopeBwdPlan pl = norm_rope_bwd_plan(p->rows, p->num_heads_q, p->num_heads_kv, p->head_dim);
-  L.parts_q = pl.parts_q;
-  L.parts_k = pl.parts_k;
-  L.blocks_q = pl.blocks_q;
+  L.warps_q = pl.warps_q;
   L.blocks = pl.blocks;
   const size_t wb = (size_t)p->head_dim * 2;
   const Extent outs[5] = {extent(dq, span(p->rows, L.dqs, qw)), extent(dk, span(p->rows, L.dks, kw)),

@@ -197,6 +197,7 @@ struct NormRopeParams {
   const int32_t* pos;          // [rows]; nullptr: cache positions (append)
   void *q_out, *k_out;         // contiguous (k_out: not for the append)
   int parts, parts_q, parts_k;  // warps that share one token, its q heads, its k (and v) heads
+  int stage_bytes, stages;     // a warp's ring in shared memory (many tokens)
   // append: the batch and the cache
   int batch, max_pages, num_pages, page_size;
   const int32_t *cu_q, *kv_lens, *table_ids;
@@ -221,17 +222,17 @@ struct NormRopeBwdParams {
   const int32_t* pos;
   void *dq, *dk;
   long long dqs, dks;
-  float* part;                 // [blocks][D] partial sums of dw
+  float* part;                 // [blocks + 1][D] partial sums of dw
   float *dwq, *dwk;
-  int parts_q, parts_k;        // warps that share one token's heads
-  int blocks_q, blocks;        // blocks that serve q, all blocks
+  int warps_q, blocks;         // warps that serve q (the others k), all blocks
+  int stage_bytes, stages;     // a warp's ring in shared memory
   int* err;
   AddrTable* chk;
 };
-// How the backward is cut (each block writes one partial sum of dw): a function
-// of the problem alone, so the order of the sums is fixed.
+// How the backward is cut: a function of the problem alone, so the order of the
+// sums of dw is fixed.
 struct NormRopeBwdPlan {
-  int parts_q, parts_k, blocks_q, blocks;
+  int warps_q, blocks;
 };
 NormRopeBwdPlan norm_rope_bwd_plan(long long rows, int hq, int hkv, int head_dim);
 int launch_norm_rope_bwd(const NormRopeBwdParams& p, int head_dim, bool bf16, int* launches, cudaStream_t s);

@@ -107,9 +107,11 @@ __device__ __forceinline__ Place place_of(int idx, int rot, bool interleaved) {
 }
 // The cosines of vector idx and its sines, signed for turning forwards: value e
 // becomes y_e c_e + partner_e s_e.
+template <bool SHARED = false>
 __device__ __forceinline__ void angles_of(const Place& t, int idx, const float* row, int rot, bool interleaved,
                                           float2 (&c)[4], float2 (&s)[4], AddrTable* chk) {
   const int half = rot / 2;
+  auto get = [&](const float* from) { return SHARED ? *reinterpret_cast<const uint4*>(from) : load16(chk, from); };
   if (!t.on) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -117,7 +119,7 @@ __device__ __forceinline__ void angles_of(const Place& t, int idx, const float* 
       s[e] = make_float2(0.f, 0.f);
     }
   } else if (interleaved) {
-    const uint4 a = load16(chk, row + idx * 4), b = load16(chk, row + half + idx * 4);
+    const uint4 a = get(row + idx * 4), b = get(row + half + idx * 4);
     const float cs[4] = {__uint_as_float(a.x), __uint_as_float(a.y), __uint_as_float(a.z), __uint_as_float(a.w)};
     const float sn[4] = {__uint_as_float(b.x), __uint_as_float(b.y), __uint_as_float(b.z), __uint_as_float(b.w)};
 #pragma unroll
@@ -130,7 +132,7 @@ __device__ __forceinline__ void angles_of(const Place& t, int idx, const float* 
     const float sg = t.second ? 1.f : -1.f;
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
-      const uint4 a = load16(chk, row + i0 + q * 4), b = load16(chk, row + half + i0 + q * 4);
+      const uint4 a = get(row + i0 + q * 4), b = get(row + half + i0 + q * 4);
       c[2 * q] = make_float2(__uint_as_float(a.x), __uint_as_float(a.y));
       c[2 * q + 1] = make_float2(__uint_as_float(a.z), __uint_as_float(a.w));
       s[2 * q] = make_float2(sg * __uint_as_float(b.x), sg * __uint_as_float(b.y));
@@ -305,26 +307,226 @@ __global__ void __launch_bounds__(kThreads, Row<D>::VPL == 1 ? 6 : 4)
   }
 }
 
-// Gradient. Blocks [0, blocks_q) serve q, the others k, in proportion to their
-// heads, so a block holds one tensor's weights and one set of sums. Its warps
-// walk (token, share of the heads) in strides of their blocks, keep the sums
-// of dw in registers, and write one partial sum per block; dw_kernel adds the
-// blocks' in order.
-constexpr int kBwdThreads = 256;
-constexpr int kBwdWarps = kBwdThreads / 32;
+// ---------------------------------------------------------------- many tokens
+// With many tokens the rows come through shared memory: every warp owns a ring
+// of stages and walks its own units -- a share of one tensor's heads of one
+// token, with the token's angles -- so the next units' bulk copies are in flight
+// while it works on one, without costing registers. (Loads to registers, one
+// unit a warp, reached 3.8 TB/s with 24 warps an SM: too few bytes in flight for
+// a chain of position, angles, rows and stores.) The warps meet nowhere.
+constexpr int kRingWarps = 16;
+constexpr int kRingThreads = kRingWarps * 32;
+constexpr int kRingSmem = 232448 - 2048;  // of the 227 KB, less the barriers
+
+// Shared memory of a warp's stage: bytes of rows, then the angles.
+template <int D>
+struct RingRows {
+  static constexpr int FWD_HEADS = 4096 / (2 * D);  // heads of a unit: 4 KB of rows
+  static constexpr int BWD_HEADS = 2048 / (2 * D);  // of each of x and dy
+};
+
+struct RingUnit {
+  long long row;
+  int part;
+};
+
+// The stages of one warp. Filled by its lane 0; `pos` of the units in flight
+// are in the callers' registers.
+struct Ring {
+  uint8_t* base;
+  uint64_t* bar;
+  int stage_bytes, stages;
+  volatile int* abort_flag;
+  __device__ __forceinline__ uint8_t* at(int i) const { return base + (i % stages) * stage_bytes; }
+  __device__ __forceinline__ uint64_t* bar_of(int i) const { return &bar[i % stages]; }
+  __device__ __forceinline__ bool wait(int i) const {
+    return __all_sync(0xffffffffu, mbar_wait(bar_of(i), (i / stages) & 1, abort_flag));
+  }
+};
+__device__ __forceinline__ void ring_copy(AddrTable* chk, void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  if (SDPA_ADDR_OK(chk, src, bytes))
+    bulk_load(dst, src, bytes, bar);
+  else
+    mbar_complete_tx(bar, bytes);
+}
 
 template <bool BF16, int D>
-__global__ void __launch_bounds__(kBwdThreads, 2) norm_rope_bwd_kernel(const __grid_constant__ NormRopeBwdParams p) {
+__global__ void __launch_bounds__(kRingThreads, 1) norm_rope_ring_kernel(const __grid_constant__ NormRopeParams p) {
   using E = Elem<BF16>;
   using T = typename E::T;
   using R = Row<D>;
-  constexpr int UN = R::VPL == 1 ? 2 : 1;  // rows a lane has in flight: three loads each
+  constexpr int HEADS = RingRows<D>::FWD_HEADS;
+  constexpr int UN = R::VPL == 1 ? 4 : 2;  // rows a lane works on at a time
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ uint64_t bars[kRingWarps][8];
+  __shared__ int s_abort;
+  const int lane = threadIdx.x % 32, sub = lane % R::LPH, grp = lane / R::LPH, warp = threadIdx.x / 32;
+  Ring ring{smem + warp * p.stages * p.stage_bytes, bars[warp], p.stage_bytes, p.stages, &s_abort};
+  if (threadIdx.x == 0) s_abort = 0;
+  if (lane == 0) {
+    for (int i = 0; i < p.stages; ++i) mbar_init(&ring.bar[i], 1);
+    fence_mbar_init();
+  }
+  __syncthreads();
+  const bool inter = p.interleaved != 0;
+  Place at[R::VPL];
+#pragma unroll
+  for (int v = 0; v < R::VPL; ++v) at[v] = place_of(v * R::LPH + sub, p.rot, inter);
+  const long long units = p.rows * p.parts, stride = (long long)gridDim.x * kRingWarps;
+  const long long first = (long long)blockIdx.x * kRingWarps + warp;
+  auto unit_of = [&](int i) {
+    const long long u = first + i * stride;
+    RingUnit r;
+    r.row = u / p.parts;
+    r.part = (int)(u - r.row * p.parts);
+    return r;
+  };
+  const int mine = first < units ? (int)((units - first + stride - 1) / stride) : 0;
+  auto position = [&](int i) { return p.rot > 0 && i < mine ? load_i32(p.chk, p.pos + unit_of(i).row, -1) : 0; };
+  auto bad = [&](int pos) { return p.rot > 0 && (pos < 0 || pos >= p.max_pos); };
+  // heads of a unit and where they start
+  auto heads_of = [&](int part, bool& is_q, int& h0) {
+    is_q = part < p.parts_q;
+    h0 = (is_q ? part : part - p.parts_q) * HEADS;
+    return min(HEADS, (is_q ? p.hq : p.hkv) - h0);
+  };
+  auto fill = [&](int i, int pos) {
+    if (lane != 0 || i >= mine || bad(pos)) return;
+    const RingUnit u = unit_of(i);
+    bool is_q;
+    int h0;
+    const int n = heads_of(u.part, is_q, h0);
+    const T* src = (is_q ? static_cast<const T*>(p.q) + u.row * p.qs : static_cast<const T*>(p.k) + u.row * p.ks) + h0 * D;
+    uint64_t* bar = ring.bar_of(i);
+    mbar_arrive_expect_tx(bar, n * D * 2 + p.rot * 4);
+    ring_copy(p.chk, ring.at(i), src, n * D * 2, bar);
+    if (p.rot > 0) ring_copy(p.chk, ring.at(i) + HEADS * D * 2, p.table + (long long)pos * p.rot, p.rot * 4, bar);
+  };
+  // a unit with a bad position is not copied: its stage's phase is passed by an empty arrival
+  auto pass = [&](int i, int pos) {
+    if (lane == 0 && i < mine && bad(pos)) mbar_arrive(ring.bar_of(i));
+  };
+  // positions of the units in flight, oldest first, and of the next one
+  int pos[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) pos[i] = position(i);
+#pragma unroll
+  for (int i = 0; i < 3; ++i)
+    if (i < p.stages) {
+      fill(i, pos[i]);
+      pass(i, pos[i]);
+    }
+  int filled = min(p.stages, mine);
+  for (int i = 0; i < mine; ++i) {
+    const int later = position(i + 4);
+    if (!ring.wait(i)) {
+      if (lane == 0) {
+        *ring.abort_flag = 1;
+        record_error(p.err, SDPA_ERR_TIMEOUT);
+      }
+      break;
+    }
+    const RingUnit u = unit_of(i);
+    if (bad(pos[0])) {
+      if (lane == 0) record_error(p.err, SDPA_ERR_BAD_INDEX);
+    } else {
+      bool is_q;
+      int h0;
+      const int n = heads_of(u.part, is_q, h0);
+      const uint8_t* st = ring.at(i);
+      const T* weight = static_cast<const T*>(is_q ? p.wq : p.wk);
+      float2 ca[R::VPL][4], cb[R::VPL][4];
+#pragma unroll
+      for (int v = 0; v < R::VPL; ++v) {
+        const int idx = v * R::LPH + sub;
+        float2 c[4], s[4], wt[4], wp[4];
+        const bool in = R::in(idx, D);
+        unpack8<E>(in ? load16(p.chk, weight + idx * 8) : make_uint4(0u, 0u, 0u, 0u), wt);
+        unpack8<E>(in ? load16(p.chk, weight + at[v].partner * 8) : make_uint4(0u, 0u, 0u, 0u), wp);
+        angles_of<true>(at[v], idx, reinterpret_cast<const float*>(st + HEADS * D * 2), p.rot, inter, c, s, p.chk);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          ca[v][e] = fmul2(wt[e], c[e]);
+          cb[v][e] = fmul2(inter ? make_float2(wp[e].y, wp[e].x) : wp[e], s[e]);
+        }
+      }
+      T* dst = (is_q ? static_cast<T*>(p.q_out) + u.row * p.hq * D : static_cast<T*>(p.k_out) + u.row * p.hkv * D) + h0 * D;
+#pragma unroll 1
+      for (int hh = 0; hh < n; hh += R::SUB * UN) {
+#pragma unroll
+        for (int x = 0; x < UN; ++x) {
+          const int h = min(hh + grp + x * R::SUB, n - 1);  // rows past the end repeat the last one, unstored
+          const T* row = reinterpret_cast<const T*>(st) + h * D;
+          float2 f[R::VPL][4], g[R::VPL][4], ss = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int v = 0; v < R::VPL; ++v) {
+            const int idx = v * R::LPH + sub;
+            const bool in = R::in(idx, D);
+            unpack8<E>(in ? *reinterpret_cast<const uint4*>(row + idx * 8) : make_uint4(0u, 0u, 0u, 0u), f[v]);
+            unpack8<E>(in && at[v].on && !inter ? *reinterpret_cast<const uint4*>(row + at[v].partner * 8)
+                                                : make_uint4(0u, 0u, 0u, 0u),
+                       g[v]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) ss = ffma2(f[v][e], f[v][e], ss);
+          }
+          const float r1 = rsqrtf(row_sum<R::LPH>(ss.x + ss.y) * (1.f / D) + p.eps);
+          const float2 r = make_float2(r1, r1);
+#pragma unroll
+          for (int v = 0; v < R::VPL; ++v) {
+            const int idx = v * R::LPH + sub;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 other = inter ? make_float2(f[v][e].y, f[v][e].x) : g[v][e];
+              const float2 t = fmul2(f[v][e], ca[v][e]);
+              g[v][e] = fmul2(at[v].on ? ffma2(other, cb[v][e], t) : t, r);
+            }
+            if (hh + grp + x * R::SUB < n && R::in(idx, D)) store16(p.chk, dst + h * D + idx * 8, pack8<E>(g[v]));
+          }
+        }
+      }
+    }
+    __syncwarp();  // every lane has read the stage
+    const int next = p.stages == 3 ? pos[3] : p.stages == 2 ? pos[2] : pos[1];
+    fill(i + p.stages, next);
+    pass(i + p.stages, next);
+    filled = min(i + 1 + p.stages, mine);
+#pragma unroll
+    for (int x = 0; x < 3; ++x) pos[x] = pos[x + 1];
+    pos[3] = later;
+  }
+  // every copy lands before the CTA ends (all have, unless a wait gave up)
+  if (lane == 0)
+    for (int i = max(0, filled - p.stages); i < filled; ++i) mbar_wait_drain(ring.bar_of(i), (i / p.stages) & 1);
+}
+
+// Gradient, through the same rings. Warps [0, warps_q) of the grid serve q, the
+// others k, in proportion to their heads; a warp keeps its sums of dw in
+// registers. Block b writes the sum of its q warps to slot b and that of its k
+// warps to slot b + 1 (only one block can have both); dw_kernel adds the slots
+// in order.
+template <bool BF16, int D>
+__global__ void __launch_bounds__(kRingThreads, 1) norm_rope_bwd_kernel(const __grid_constant__ NormRopeBwdParams p) {
+  using E = Elem<BF16>;
+  using T = typename E::T;
+  using R = Row<D>;
+  constexpr int HEADS = RingRows<D>::BWD_HEADS;
+  constexpr int UN = R::VPL == 1 ? 2 : 1;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ uint64_t bars[kRingWarps][8];
+  __shared__ int s_abort;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int lane = threadIdx.x % 32, sub = lane % R::LPH, grp = lane / R::LPH, warp = threadIdx.x / 32;
-  const bool is_q = (int)blockIdx.x < p.blocks_q;
-  const int block = is_q ? blockIdx.x : blockIdx.x - p.blocks_q, blocks = is_q ? p.blocks_q : p.blocks - p.blocks_q;
-  const int heads = is_q ? p.hq : p.hkv, parts = is_q ? p.parts_q : p.parts_k, per = (heads + parts - 1) / parts;
-  const long long units = p.rows * parts, xs = is_q ? p.qs : p.ks, ds = is_q ? p.dqs : p.dks;
+  Ring ring{smem + warp * p.stages * p.stage_bytes, bars[warp], p.stage_bytes, p.stages, &s_abort};
+  if (threadIdx.x == 0) s_abort = 0;
+  if (lane == 0) {
+    for (int i = 0; i < p.stages; ++i) mbar_init(&ring.bar[i], 1);
+    fence_mbar_init();
+  }
+  __syncthreads();
+  const int gw = blockIdx.x * kRingWarps + warp;
+  const bool is_q = gw < p.warps_q;
+  const int heads = is_q ? p.hq : p.hkv, parts = (heads + HEADS - 1) / HEADS;
+  const long long xs = is_q ? p.qs : p.ks, ds = is_q ? p.dqs : p.dks;
   const T* const x0 = static_cast<const T*>(is_q ? p.q : p.k);
   const T* const g0 = static_cast<const T*>(is_q ? p.gq : p.gk);
   T* const d0 = static_cast<T*>(is_q ? p.dq : p.dk);
@@ -340,85 +542,121 @@ __global__ void __launch_bounds__(kBwdThreads, 2) norm_rope_bwd_kernel(const __g
 #pragma unroll
     for (int e = 0; e < 4; ++e) acc[v][e] = make_float2(0.f, 0.f);
   }
-  const long long stride = (long long)blocks * kBwdWarps;
-  long long w = (long long)block * kBwdWarps + warp;
-  int next_pos = w < units && p.rot > 0 ? load_i32(p.chk, p.pos + w / parts, -1) : 0;
-  for (; w < units; w += stride) {
-    const long long row = w / parts;
-    const int part = (int)(w - row * parts), h_end = min(heads, (part + 1) * per);
-    const int pos = next_pos;
-    const bool skip = p.rot > 0 && (pos < 0 || pos >= p.max_pos);  // a position outside the table: zeros
-    if (skip && lane == 0) record_error(p.err, SDPA_ERR_BAD_INDEX);
-    uint4 x[UN][R::VPL], y[UN][R::VPL], z[UN][R::VPL];
-    auto fetch = [&](int h0) {
-#pragma unroll
-      for (int u = 0; u < UN; ++u) {
-        const int h = h0 + grp + u * R::SUB;
-        const bool row_in = h < h_end && !skip;
-        const T* xr = x0 + row * xs + h * D;
-        const T* gr = g0 + (row * heads + h) * D;
-#pragma unroll
-        for (int v = 0; v < R::VPL; ++v) {
-          const bool in = row_in && R::in(v * R::LPH + sub, D);
-          x[u][v] = y[u][v] = z[u][v] = make_uint4(0u, 0u, 0u, 0u);
-          if (in) x[u][v] = load16(p.chk, xr + (v * R::LPH + sub) * 8);
-          if (in) y[u][v] = load16(p.chk, gr + (v * R::LPH + sub) * 8);
-          if (in && at[v].on && !inter) z[u][v] = load16(p.chk, gr + at[v].partner * 8);
-        }
-      }
-    };
-    int h0 = part * per;
-    fetch(h0);
-    if (p.rot > 0 && w + stride < units) next_pos = load_i32(p.chk, p.pos + (w + stride) / parts, -1);
-    float2 c[R::VPL][4], s[R::VPL][4];
-#pragma unroll
-    for (int v = 0; v < R::VPL; ++v)
-      angles_of(at[v], v * R::LPH + sub, p.table + (skip ? 0ll : (long long)pos * p.rot), p.rot, inter, c[v], s[v], p.chk);
-    while (true) {
-#pragma unroll
-      for (int u = 0; u < UN; ++u) {
-        const int h = h0 + grp + u * R::SUB;
-        float2 f[R::VPL][4], g[R::VPL][4];
-        float2 ss = make_float2(0.f, 0.f), dot = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int v = 0; v < R::VPL; ++v) {
-          float2 o[4];
-          unpack8<E>(x[u][v], f[v]);
-          unpack8<E>(y[u][v], g[v]);
-          unpack8<E>(z[u][v], o);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            // turned back: y c - partner s
-            const float2 other = inter ? make_float2(-g[v][e].y, -g[v][e].x) : make_float2(-o[e].x, -o[e].y);
-            if (at[v].on) g[v][e] = ffma2(other, s[v][e], fmul2(g[v][e], c[v][e]));
-            ss = ffma2(f[v][e], f[v][e], ss);
-            dot = ffma2(fmul2(g[v][e], wt[v][e]), f[v][e], dot);
-          }
-        }
-        float a = ss.x + ss.y, b = dot.x + dot.y;
-        row_sums<R::LPH>(a, b, lane);
-        if (h >= h_end) continue;
-        const float r1 = skip ? 0.f : rsqrtf(a * (1.f / D) + p.eps), k1 = -r1 * r1 * r1 * (b * (1.f / D));
-        const float2 r = make_float2(r1, r1), k3 = make_float2(k1, k1);
-        T* dst = d0 + row * ds + h * D;
-#pragma unroll
-        for (int v = 0; v < R::VPL; ++v) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 gr = fmul2(g[v][e], r);
-            acc[v][e] = ffma2(gr, f[v][e], acc[v][e]);
-            f[v][e] = ffma2(k3, f[v][e], fmul2(gr, wt[v][e]));
-          }
-          if (R::in(v * R::LPH + sub, D)) store16(p.chk, dst + (v * R::LPH + sub) * 8, pack8<E>(f[v]));
-        }
-      }
-      h0 += R::SUB * UN;
-      if (h0 >= h_end) break;
-      fetch(h0);
+  const long long units = p.rows * parts, stride = is_q ? p.warps_q : gridDim.x * kRingWarps - p.warps_q;
+  const long long first = is_q ? gw : gw - p.warps_q;
+  const int mine = first < units ? (int)((units - first + stride - 1) / stride) : 0;
+  auto unit_of = [&](int i) {
+    const long long u = first + i * stride;
+    RingUnit r;
+    r.row = u / parts;
+    r.part = (int)(u - r.row * parts);
+    return r;
+  };
+  auto position = [&](int i) { return p.rot > 0 && i < mine ? load_i32(p.chk, p.pos + unit_of(i).row, -1) : 0; };
+  auto bad = [&](int pos) { return p.rot > 0 && (pos < 0 || pos >= p.max_pos); };
+  constexpr int SIDE = HEADS * D * 2;  // x, then dy, then the angles
+  auto fill = [&](int i, int pos) {
+    if (lane != 0 || i >= mine) return;
+    uint64_t* bar = ring.bar_of(i);
+    if (bad(pos)) {  // not copied: an empty arrival passes the stage's phase
+      mbar_arrive(bar);
+      return;
     }
+    const RingUnit u = unit_of(i);
+    const int h0 = u.part * HEADS, n = min(HEADS, heads - h0);
+    mbar_arrive_expect_tx(bar, 2 * n * D * 2 + p.rot * 4);
+    ring_copy(p.chk, ring.at(i), x0 + u.row * xs + h0 * D, n * D * 2, bar);
+    ring_copy(p.chk, ring.at(i) + SIDE, g0 + (u.row * heads + h0) * D, n * D * 2, bar);
+    if (p.rot > 0) ring_copy(p.chk, ring.at(i) + 2 * SIDE, p.table + (long long)pos * p.rot, p.rot * 4, bar);
+  };
+  int pos[4];  // positions of the units in flight, oldest first, and of the next one
+#pragma unroll
+  for (int i = 0; i < 4; ++i) pos[i] = position(i);
+#pragma unroll
+  for (int i = 0; i < 3; ++i)
+    if (i < p.stages) fill(i, pos[i]);
+  int filled = min(p.stages, mine);
+  for (int i = 0; i < mine; ++i) {
+    const int later = position(i + 4);
+    if (!ring.wait(i)) {
+      if (lane == 0) {
+        *ring.abort_flag = 1;
+        record_error(p.err, SDPA_ERR_TIMEOUT);
+      }
+      break;
+    }
+    const RingUnit u = unit_of(i);
+    const int h0 = u.part * HEADS, n = min(HEADS, heads - h0);
+    const uint8_t* st = ring.at(i);
+    T* dst = d0 + u.row * ds + h0 * D;
+    if (bad(pos[0])) {  // a position outside the table: zeros
+      if (lane == 0) record_error(p.err, SDPA_ERR_BAD_INDEX);
+      for (int x = lane; x < n * D / 8; x += 32) store16(p.chk, dst + x * 8, make_uint4(0u, 0u, 0u, 0u));
+    } else {
+      float2 c[R::VPL][4], s[R::VPL][4];
+#pragma unroll
+      for (int v = 0; v < R::VPL; ++v)
+        angles_of<true>(at[v], v * R::LPH + sub, reinterpret_cast<const float*>(st + 2 * SIDE), p.rot, inter, c[v], s[v],
+                        p.chk);
+#pragma unroll 1
+      for (int hh = 0; hh < n; hh += R::SUB * UN) {
+#pragma unroll
+        for (int x = 0; x < UN; ++x) {
+          const int h = min(hh + grp + x * R::SUB, n - 1);  // rows past the end repeat the last one, unused
+          const T* xr = reinterpret_cast<const T*>(st) + h * D;
+          const T* gr = reinterpret_cast<const T*>(st + SIDE) + h * D;
+          float2 f[R::VPL][4], g[R::VPL][4];
+          float2 ss = make_float2(0.f, 0.f), dot = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int v = 0; v < R::VPL; ++v) {
+            const int idx = v * R::LPH + sub;
+            const bool in = R::in(idx, D);
+            const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+            float2 o[4];
+            unpack8<E>(in ? *reinterpret_cast<const uint4*>(xr + idx * 8) : none, f[v]);
+            unpack8<E>(in ? *reinterpret_cast<const uint4*>(gr + idx * 8) : none, g[v]);
+            unpack8<E>(in && at[v].on && !inter ? *reinterpret_cast<const uint4*>(gr + at[v].partner * 8) : none, o);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              // turned back: y c - partner s
+              const float2 other = inter ? make_float2(-g[v][e].y, -g[v][e].x) : make_float2(-o[e].x, -o[e].y);
+              if (at[v].on) g[v][e] = ffma2(other, s[v][e], fmul2(g[v][e], c[v][e]));
+              ss = ffma2(f[v][e], f[v][e], ss);
+              dot = ffma2(fmul2(g[v][e], wt[v][e]), f[v][e], dot);
+            }
+          }
+          float a = ss.x + ss.y, b = dot.x + dot.y;
+          row_sums<R::LPH>(a, b, lane);
+          if (hh + grp + x * R::SUB >= n) continue;
+          const float r1 = rsqrtf(a * (1.f / D) + p.eps), k1 = -r1 * r1 * r1 * (b * (1.f / D));
+          const float2 r = make_float2(r1, r1), k3 = make_float2(k1, k1);
+#pragma unroll
+          for (int v = 0; v < R::VPL; ++v) {
+            const int idx = v * R::LPH + sub;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 t = fmul2(g[v][e], r);
+              acc[v][e] = ffma2(t, f[v][e], acc[v][e]);
+              f[v][e] = ffma2(k3, f[v][e], fmul2(t, wt[v][e]));
+            }
+            if (R::in(idx, D)) store16(p.chk, dst + h * D + idx * 8, pack8<E>(f[v]));
+          }
+        }
+      }
+    }
+    __syncwarp();  // every lane has read the stage
+    fill(i + p.stages, p.stages == 3 ? pos[3] : p.stages == 2 ? pos[2] : pos[1]);
+    filled = min(i + 1 + p.stages, mine);
+#pragma unroll
+    for (int x = 0; x < 3; ++x) pos[x] = pos[x + 1];
+    pos[3] = later;
   }
-  // the block's sum of dw: row groups of a warp by shuffles, warps in order
-  __shared__ float sum[kBwdWarps][D];
+  // every copy lands before the CTA ends (all have, unless a wait gave up)
+  if (lane == 0)
+    for (int i = max(0, filled - p.stages); i < filled; ++i) mbar_wait_drain(ring.bar_of(i), (i / p.stages) & 1);
+  // the block's sums of dw, in the rings' memory: row groups of a warp by shuffles, warps in order
+  __syncthreads();
+  float* sum = reinterpret_cast<float*>(smem);  // [kRingWarps][D]
 #pragma unroll
   for (int v = 0; v < R::VPL; ++v)
 #pragma unroll
@@ -428,30 +666,34 @@ __global__ void __launch_bounds__(kBwdThreads, 2) norm_rope_bwd_kernel(const __g
         acc[v][e].x += __shfl_xor_sync(0xffffffffu, acc[v][e].x, o);
         acc[v][e].y += __shfl_xor_sync(0xffffffffu, acc[v][e].y, o);
       }
-      if (grp == 0 && R::in(v * R::LPH + sub, D)) *reinterpret_cast<float2*>(&sum[warp][(v * R::LPH + sub) * 8 + 2 * e]) = acc[v][e];
+      if (grp == 0 && R::in(v * R::LPH + sub, D))
+        *reinterpret_cast<float2*>(sum + warp * D + (v * R::LPH + sub) * 8 + 2 * e) = acc[v][e];
     }
   __syncthreads();
-  for (int i = threadIdx.x; i < D; i += kBwdThreads) {
+  const int q_warps = min(max(p.warps_q - (int)blockIdx.x * kRingWarps, 0), kRingWarps);
+  for (int i = threadIdx.x; i < 2 * D; i += kRingThreads) {
+    const bool q_side = i < D;
+    if (q_side ? q_warps == 0 : q_warps == kRingWarps) continue;
     float t = 0.f;
-#pragma unroll
-    for (int k = 0; k < kBwdWarps; ++k) t += sum[k][i];
-    float* to = p.part + (long long)blockIdx.x * D + i;
+    for (int k = q_side ? 0 : q_warps; k < (q_side ? q_warps : kRingWarps); ++k) t += sum[k * D + i % D];
+    float* to = p.part + (long long)(blockIdx.x + (q_side ? 0 : 1)) * D + i % D;
     if (SDPA_ADDR_OK(p.chk, to, 4)) *to = t;
   }
 }
 
 // dw = the blocks' partial sums, added in a fixed order: 16 columns of q's or
-// k's weights per CTA, 32 threads a column, each over every 32nd block.
-__global__ void __launch_bounds__(512) dw_kernel(const float* part, int blocks_q, int blocks, int d, float* dwq,
+// k's weights per CTA, 32 threads a column, each over every 32nd slot.
+// Slots [0, end_q) are q's, [first_k, slots) k's.
+__global__ void __launch_bounds__(512) dw_kernel(const float* part, int end_q, int first_k, int slots, int d, float* dwq,
                                                  float* dwk, AddrTable* chk) {
   __shared__ float sum[32][17];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int x = threadIdx.x % 16, k = threadIdx.x / 16, at = blockIdx.x * 16 + x;
   const bool is_q = at < d;
-  const int col = is_q ? at : at - d, end = is_q ? blocks_q : blocks;
+  const int col = is_q ? at : at - d, end = is_q ? end_q : slots;
   float t = 0.f;
 #pragma unroll 8
-  for (int b = (is_q ? 0 : blocks_q) + k; b < end; b += 32) {
+  for (int b = (is_q ? 0 : first_k) + k; b < end; b += 32) {
     const float* from = part + (long long)b * d + col;
     t += SDPA_ADDR_OK(chk, from, 4) ? *from : 0.f;
   }
@@ -465,9 +707,31 @@ __global__ void __launch_bounds__(512) dw_kernel(const float* part, int blocks_q
   }
 }
 
+// Stages of a warp's ring, each `bytes`: at most three, as many as fit.
+int ring_stages(int bytes) { return std::min(3, kRingSmem / (kRingWarps * bytes)); }
+
 template <bool BF16, int D>
 int launch_t(NormRopeParams p, bool append, cudaStream_t s) {
   using R = Row<D>;
+  if (!append) {
+    constexpr int HEADS = RingRows<D>::FWD_HEADS;
+    const int parts_q = (p.hq + HEADS - 1) / HEADS, parts_k = (p.hkv + HEADS - 1) / HEADS;
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+      return SDPA_ERR_CUDA;
+    // the rings pay from a few units a warp on; below, registers are quicker to start
+    if (p.rows * (parts_q + parts_k) >= (long long)sms * kRingWarps * 2) {
+      auto kern = norm_rope_ring_kernel<BF16, D>;
+      p.parts_q = parts_q;
+      p.parts = parts_q + parts_k;
+      p.stage_bytes = HEADS * D * 2 + p.rot * 4;
+      p.stages = ring_stages(p.stage_bytes);
+      if (const int rc = set_kernel_smem(reinterpret_cast<const void*>(kern), kRingSmem, 100)) return rc;
+      kern<<<(unsigned)sms, kRingThreads, kRingWarps * p.stages * p.stage_bytes, s>>>(p);
+      return cudaGetLastError() == cudaSuccess ? SDPA_OK : SDPA_ERR_CUDA;
+    }
+  }
   p.parts_q = (p.hq + R::HEADS - 1) / R::HEADS;
   p.parts_k = (p.hkv + R::HEADS - 1) / R::HEADS;
   p.parts = p.parts_q + (append ? 2 : 1) * p.parts_k;
@@ -484,8 +748,13 @@ int launch_t(NormRopeParams p, bool append, cudaStream_t s) {
 }
 
 template <bool BF16, int D>
-int launch_bwd_t(const NormRopeBwdParams& p, cudaStream_t s) {
-  norm_rope_bwd_kernel<BF16, D><<<(unsigned)p.blocks, kBwdThreads, 0, s>>>(p);
+int launch_bwd_t(NormRopeBwdParams p, cudaStream_t s) {
+  auto kern = norm_rope_bwd_kernel<BF16, D>;
+  p.stage_bytes = 2 * RingRows<D>::BWD_HEADS * D * 2 + p.rot * 4;
+  p.stages = ring_stages(p.stage_bytes);
+  if (const int rc = set_kernel_smem(reinterpret_cast<const void*>(kern), kRingSmem, 100)) return rc;
+  const int bytes = std::max(kRingWarps * p.stages * p.stage_bytes, kRingWarps * D * 4);
+  kern<<<(unsigned)p.blocks, kRingThreads, bytes, s>>>(p);
   if (cudaGetLastError() != cudaSuccess) return SDPA_ERR_CUDA;
   // launched while the kernel above runs; it waits for it before reading
   cudaLaunchConfig_t cfg = {};
@@ -497,7 +766,8 @@ int launch_bwd_t(const NormRopeBwdParams& p, cudaStream_t s) {
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, dw_kernel, (const float*)p.part, p.blocks_q, p.blocks, D, p.dwq, p.dwk, p.chk) == cudaSuccess
+  return cudaLaunchKernelEx(&cfg, dw_kernel, (const float*)p.part, (p.warps_q + kRingWarps - 1) / kRingWarps,
+                            p.warps_q / kRingWarps + 1, p.blocks + 1, D, p.dwq, p.dwk, p.chk) == cudaSuccess
              ? SDPA_OK
              : SDPA_ERR_CUDA;
 }
@@ -505,23 +775,16 @@ int launch_bwd_t(const NormRopeBwdParams& p, cudaStream_t s) {
 }  // namespace
 
 NormRopeBwdPlan norm_rope_bwd_plan(long long rows, int hq, int hkv, int head_dim) {
-  // two blocks on each of the 152 SMs of the device this is written for: the
+  // one block on each of the 152 SMs of the device this is written for: the
   // plan must not depend on the device in use, since the workspace size is
   // asked for without one, and the order of the sums follows from it
-  constexpr long long kBlocks = 152 * 2;
-  const int step = head_dim == 128 ? 4 : head_dim <= 256 ? 2 : 1;  // heads of one step of a warp
-  // a token's heads shared by several warps only where there are few tokens
-  auto share = [&](int heads) {
-    const long long most = (heads + step - 1) / step, want = kBlocks * kBwdWarps * heads / (hq + hkv);
-    return (int)std::max<long long>(1, std::min(most, (want + rows - 1) / std::max<long long>(rows, 1)));
-  };
+  constexpr long long kBlocks = 152;
+  const int per = 2048 / (2 * head_dim);  // heads of a unit
+  const long long units = rows * ((hq + per - 1) / per + (hkv + per - 1) / per);
   NormRopeBwdPlan pl;
-  pl.parts_q = share(hq);
-  pl.parts_k = share(hkv);
-  const long long need_q = (rows * pl.parts_q + kBwdWarps - 1) / kBwdWarps, need_k = (rows * pl.parts_k + kBwdWarps - 1) / kBwdWarps;
-  const long long give_q = std::max<long long>(1, std::min(kBlocks - 1, (kBlocks * hq + (hq + hkv) / 2) / (hq + hkv)));
-  pl.blocks_q = (int)std::max<long long>(1, std::min(give_q, need_q));
-  pl.blocks = pl.blocks_q + (int)std::max<long long>(1, std::min(kBlocks - give_q, need_k));
+  pl.blocks = (int)std::max<long long>(1, std::min<long long>(kBlocks, (units + kRingWarps - 1) / kRingWarps));
+  const long long warps = (long long)pl.blocks * kRingWarps;
+  pl.warps_q = (int)std::max<long long>(1, std::min(warps - 1, (warps * hq + (hq + hkv) / 2) / (hq + hkv)));
   return pl;
 }
 

@@ -100,6 +100,40 @@ def test_backward(rows, hq, hkv, d, rot, inter, fused, dtype):
     assert sdpa.sdpa_get_device_error() == 0
 
 
+@pytest.mark.parametrize("rows,hq,hkv,d,rot,inter", [(2500, 8, 2, 128, 128, False), (1700, 5, 3, 192, 64, False),
+                                                     (1301, 9, 1, 256, 256, True), (900, 7, 2, 512, 512, False),
+                                                     (3001, 17, 1, 128, 0, False)])
+def test_many_tokens(rows, hq, hkv, d, rot, inter):
+    """Enough units for every warp of the rings to go round several times; a few positions are bad."""
+    q, k, qd, kd, wq, wk, table, pos = make(rows, hq, hkv, d, rot, torch.bfloat16, True)
+    bad = torch.zeros(rows, dtype=torch.bool)
+    p = pos.clone()
+    if rot:
+        bad[torch.tensor([0, 5, rows // 2, rows - 1])] = True
+        p[bad] = torch.tensor([-1, 5000, 2 ** 31 - 1, -2 ** 31], dtype=torch.int32)
+    qo, ko = torch.full((rows, hq, d), 6.0, device="cuda").bfloat16(), torch.full((rows, hkv, d), 6.0, device="cuda").bfloat16()
+    sdpa.sdpa_qk_norm_rope(qd, kd, dev(wq), dev(wk), dev(table), dev(p) if rot else None, eps=EPS, interleaved=inter,
+                           q_out=qo, k_out=ko)
+    assert sdpa.sdpa_get_device_error() == (10 if rot else 0)
+    assert bool((qo.cpu()[bad] == 6).all()) and bool((ko.cpu()[bad] == 6).all())
+    check_forward(qo.cpu()[~bad], q[~bad], wq, table, pos[~bad], rot, inter, torch.bfloat16)
+    check_forward(ko.cpu()[~bad], k[~bad], wk, table, pos[~bad], rot, inter, torch.bfloat16)
+    g = torch.Generator().manual_seed(4)
+    gq, gk = torch.randn(q.shape, generator=g).bfloat16(), torch.randn(k.shape, generator=g).bfloat16()
+    args = (dev(gq), dev(gk), qd, kd, dev(wq), dev(wk), dev(table), dev(p) if rot else None)
+    got = sdpa.sdpa_qk_norm_rope_bwd(*args, eps=EPS, interleaved=inter)
+    again = sdpa.sdpa_qk_norm_rope_bwd(*args, eps=EPS, interleaved=inter)
+    assert all(torch.equal(a, b) for a, b in zip(got, again))
+    assert sdpa.sdpa_get_device_error() == (10 if rot else 0)
+    keep = ~bad
+    rows_t = None if rot == 0 else table[pos[keep].long()]
+    for x, w, dy, dx, dw in ((q, wq, gq, got[0], got[2]), (k, wk, gk, got[1], got[3])):
+        want, mag, want_w, mag_w = ref.norm_rope_bwd(dy[keep], x[keep], w, rows_t, rot, EPS, inter)
+        within(dx.cpu()[keep], want, mag, ref.U[torch.bfloat16], 0.0, 2.0 ** -17)
+        within(dw, want_w, mag_w, 0.0, 0.0, 2.0 ** -15)
+        assert not dx.cpu()[bad].any()
+
+
 @pytest.mark.parametrize("layout", ["bshd", "sbhd"])
 def test_batched_layouts(layout):
     a, b = (3, 41) if layout == "bshd" else (41, 3)
@@ -184,10 +218,11 @@ def test_captured_and_on_another_stream():
 
 
 @pytest.mark.parametrize("d,rot,inter", [(128, 128, False), (192, 96, True), (256, 64, False), (512, 512, False)])
-def test_every_access_is_inside_the_buffers(d, rot, inter):
-    q, k, qd, kd, wq, wk, table, pos = make(37, 6, 2, d, rot, torch.float16, True)
+@pytest.mark.parametrize("n", [37, 2600])
+def test_every_access_is_inside_the_buffers(d, rot, inter, n):
+    q, k, qd, kd, wq, wk, table, pos = make(n, 6, 2, d, rot, torch.float16, True)
     args = (dev(wq), dev(wk), dev(table), dev(pos))
-    gq, gk = torch.randn(37, 6, d, device="cuda").half(), torch.randn(37, 2, d, device="cuda").half()
+    gq, gk = torch.randn(n, 6, d, device="cuda").half(), torch.randn(n, 2, d, device="cuda").half()
     plain = sdpa.sdpa_qk_norm_rope(qd, kd, *args, interleaved=inter) + sdpa.sdpa_qk_norm_rope_bwd(
         gq, gk, qd, kd, *args, interleaved=inter)
     with sdpa.address_checked():
