@@ -314,8 +314,8 @@ __global__ void __launch_bounds__(kThreads, Row<D>::VPL == 1 ? 6 : 4)
 // while it works on one, without costing registers. (Loads to registers, one
 // unit a warp, reached 3.8 TB/s with 24 warps an SM: too few bytes in flight for
 // a chain of position, angles, rows and stores.) The warps meet nowhere.
-constexpr int kRingWarps = 16;
-constexpr int kRingThreads = kRingWarps * 32;
+constexpr int kFwdWarps = 24;  // 24 x 32 threads of at most 85 registers; the gradient needs 128
+constexpr int kBwdWarps = 16;
 constexpr int kRingSmem = 232448 - 2048;  // of the 227 KB, less the barriers
 
 // Shared memory of a warp's stage: bytes of rows, then the angles.
@@ -325,9 +325,26 @@ struct RingRows {
   static constexpr int BWD_HEADS = 2048 / (2 * D);  // of each of x and dy
 };
 
-struct RingUnit {
-  long long row;
-  int part;
+// A warp's units lie `stride` apart in the order (row, part): a cursor steps
+// through them without dividing.
+struct RingCursor {
+  long long row, step_row;
+  int part, step_part, parts;
+  __device__ __forceinline__ void start(long long unit, long long stride, int parts_) {
+    parts = parts_;
+    row = unit / parts;
+    part = (int)(unit - row * parts);
+    step_row = stride / parts;
+    step_part = (int)(stride - step_row * parts);
+  }
+  __device__ __forceinline__ void next() {
+    row += step_row;
+    part += step_part;
+    if (part >= parts) {
+      part -= parts;
+      ++row;
+    }
+  }
 };
 
 // The stages of one warp. Filled by its lane 0; `pos` of the units in flight
@@ -350,15 +367,15 @@ __device__ __forceinline__ void ring_copy(AddrTable* chk, void* dst, const void*
     mbar_complete_tx(bar, bytes);
 }
 
-template <bool BF16, int D>
-__global__ void __launch_bounds__(kRingThreads, 1) norm_rope_ring_kernel(const __grid_constant__ NormRopeParams p) {
+template <bool BF16, int D, bool INTER>
+__global__ void __launch_bounds__(kFwdWarps * 32, 1) norm_rope_ring_kernel(const __grid_constant__ NormRopeParams p) {
   using E = Elem<BF16>;
   using T = typename E::T;
   using R = Row<D>;
   constexpr int HEADS = RingRows<D>::FWD_HEADS;
-  constexpr int UN = R::VPL == 1 ? 4 : 2;  // rows a lane works on at a time
+  constexpr int UN = R::VPL == 1 ? 4 : 1;  // rows a lane works on at a time
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ uint64_t bars[kRingWarps][8];
+  __shared__ uint64_t bars[kFwdWarps][4];
   __shared__ int s_abort;
   const int lane = threadIdx.x % 32, sub = lane % R::LPH, grp = lane / R::LPH, warp = threadIdx.x / 32;
   Ring ring{smem + warp * p.stages * p.stage_bytes, bars[warp], p.stage_bytes, p.stages, &s_abort};
@@ -368,21 +385,22 @@ __global__ void __launch_bounds__(kRingThreads, 1) norm_rope_ring_kernel(const _
     fence_mbar_init();
   }
   __syncthreads();
-  const bool inter = p.interleaved != 0;
   Place at[R::VPL];
 #pragma unroll
-  for (int v = 0; v < R::VPL; ++v) at[v] = place_of(v * R::LPH + sub, p.rot, inter);
-  const long long units = p.rows * p.parts, stride = (long long)gridDim.x * kRingWarps;
-  const long long first = (long long)blockIdx.x * kRingWarps + warp;
-  auto unit_of = [&](int i) {
-    const long long u = first + i * stride;
-    RingUnit r;
-    r.row = u / p.parts;
-    r.part = (int)(u - r.row * p.parts);
-    return r;
-  };
+  for (int v = 0; v < R::VPL; ++v) at[v] = place_of(v * R::LPH + sub, p.rot, INTER);
+  const long long units = p.rows * p.parts, stride = (long long)gridDim.x * kFwdWarps;
+  const long long first = (long long)blockIdx.x * kFwdWarps + warp;
   const int mine = first < units ? (int)((units - first + stride - 1) / stride) : 0;
-  auto position = [&](int i) { return p.rot > 0 && i < mine ? load_i32(p.chk, p.pos + unit_of(i).row, -1) : 0; };
+  RingCursor cur, fil, ahead;  // the unit at work, the next to copy, the next whose position is read
+  cur.start(first, stride, p.parts);
+  fil = ahead = cur;
+  int n_ahead = 0;
+  auto position = [&]() {
+    const int x = p.rot > 0 && n_ahead < mine ? load_i32(p.chk, p.pos + ahead.row, -1) : 0;
+    ++n_ahead;
+    ahead.next();
+    return x;
+  };
   auto bad = [&](int pos) { return p.rot > 0 && (pos < 0 || pos >= p.max_pos); };
   // heads of a unit and where they start
   auto heads_of = [&](int part, bool& is_q, int& h0) {
@@ -390,35 +408,34 @@ __global__ void __launch_bounds__(kRingThreads, 1) norm_rope_ring_kernel(const _
     h0 = (is_q ? part : part - p.parts_q) * HEADS;
     return min(HEADS, (is_q ? p.hq : p.hkv) - h0);
   };
-  auto fill = [&](int i, int pos) {
-    if (lane != 0 || i >= mine || bad(pos)) return;
-    const RingUnit u = unit_of(i);
-    bool is_q;
-    int h0;
-    const int n = heads_of(u.part, is_q, h0);
-    const T* src = (is_q ? static_cast<const T*>(p.q) + u.row * p.qs : static_cast<const T*>(p.k) + u.row * p.ks) + h0 * D;
-    uint64_t* bar = ring.bar_of(i);
-    mbar_arrive_expect_tx(bar, n * D * 2 + p.rot * 4);
-    ring_copy(p.chk, ring.at(i), src, n * D * 2, bar);
-    if (p.rot > 0) ring_copy(p.chk, ring.at(i) + HEADS * D * 2, p.table + (long long)pos * p.rot, p.rot * 4, bar);
+  int filled = 0;
+  auto fill = [&](int pos) {
+    if (filled < mine && lane == 0) {
+      uint64_t* bar = ring.bar_of(filled);
+      if (bad(pos)) {  // not copied: an empty arrival passes the stage's phase
+        mbar_arrive(bar);
+      } else {
+        bool is_q;
+        int h0;
+        const int n = heads_of(fil.part, is_q, h0);
+        const T* src = (is_q ? static_cast<const T*>(p.q) + fil.row * p.qs : static_cast<const T*>(p.k) + fil.row * p.ks) + h0 * D;
+        mbar_arrive_expect_tx(bar, n * D * 2 + p.rot * 4);
+        ring_copy(p.chk, ring.at(filled), src, n * D * 2, bar);
+        if (p.rot > 0)
+          ring_copy(p.chk, ring.at(filled) + HEADS * D * 2, p.table + (long long)pos * p.rot, p.rot * 4, bar);
+      }
+    }
+    if (filled < mine) ++filled;
+    fil.next();
   };
-  // a unit with a bad position is not copied: its stage's phase is passed by an empty arrival
-  auto pass = [&](int i, int pos) {
-    if (lane == 0 && i < mine && bad(pos)) mbar_arrive(ring.bar_of(i));
-  };
-  // positions of the units in flight, oldest first, and of the next one
-  int pos[4];
+  int pos[4];  // positions of the units in flight, oldest first, and of the next one
 #pragma unroll
-  for (int i = 0; i < 4; ++i) pos[i] = position(i);
+  for (int i = 0; i < 4; ++i) pos[i] = position();
 #pragma unroll
   for (int i = 0; i < 3; ++i)
-    if (i < p.stages) {
-      fill(i, pos[i]);
-      pass(i, pos[i]);
-    }
-  int filled = min(p.stages, mine);
+    if (i < p.stages) fill(pos[i]);
   for (int i = 0; i < mine; ++i) {
-    const int later = position(i + 4);
+    const int later = position();
     if (!ring.wait(i)) {
       if (lane == 0) {
         *ring.abort_flag = 1;
@@ -426,13 +443,12 @@ __global__ void __launch_bounds__(kRingThreads, 1) norm_rope_ring_kernel(const _
       }
       break;
     }
-    const RingUnit u = unit_of(i);
     if (bad(pos[0])) {
       if (lane == 0) record_error(p.err, SDPA_ERR_BAD_INDEX);
     } else {
       bool is_q;
       int h0;
-      const int n = heads_of(u.part, is_q, h0);
+      const int n = heads_of(cur.part, is_q, h0);
       const uint8_t* st = ring.at(i);
       const T* weight = static_cast<const T*>(is_q ? p.wq : p.wk);
       float2 ca[R::VPL][4], cb[R::VPL][4];
@@ -443,14 +459,14 @@ __global__ void __launch_bounds__(kRingThreads, 1) norm_rope_ring_kernel(const _
         const bool in = R::in(idx, D);
         unpack8<E>(in ? load16(p.chk, weight + idx * 8) : make_uint4(0u, 0u, 0u, 0u), wt);
         unpack8<E>(in ? load16(p.chk, weight + at[v].partner * 8) : make_uint4(0u, 0u, 0u, 0u), wp);
-        angles_of<true>(at[v], idx, reinterpret_cast<const float*>(st + HEADS * D * 2), p.rot, inter, c, s, p.chk);
+        angles_of<true>(at[v], idx, reinterpret_cast<const float*>(st + HEADS * D * 2), p.rot, INTER, c, s, p.chk);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           ca[v][e] = fmul2(wt[e], c[e]);
-          cb[v][e] = fmul2(inter ? make_float2(wp[e].y, wp[e].x) : wp[e], s[e]);
+          cb[v][e] = fmul2(INTER ? make_float2(wp[e].y, wp[e].x) : wp[e], s[e]);
         }
       }
-      T* dst = (is_q ? static_cast<T*>(p.q_out) + u.row * p.hq * D : static_cast<T*>(p.k_out) + u.row * p.hkv * D) + h0 * D;
+      T* dst = (is_q ? static_cast<T*>(p.q_out) + cur.row * p.hq * D : static_cast<T*>(p.k_out) + cur.row * p.hkv * D) + h0 * D;
 #pragma unroll 1
       for (int hh = 0; hh < n; hh += R::SUB * UN) {
 #pragma unroll
@@ -463,7 +479,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) norm_rope_ring_kernel(const _
             const int idx = v * R::LPH + sub;
             const bool in = R::in(idx, D);
             unpack8<E>(in ? *reinterpret_cast<const uint4*>(row + idx * 8) : make_uint4(0u, 0u, 0u, 0u), f[v]);
-            unpack8<E>(in && at[v].on && !inter ? *reinterpret_cast<const uint4*>(row + at[v].partner * 8)
+            unpack8<E>(!INTER && in && at[v].on ? *reinterpret_cast<const uint4*>(row + at[v].partner * 8)
                                                 : make_uint4(0u, 0u, 0u, 0u),
                        g[v]);
 #pragma unroll
@@ -476,9 +492,9 @@ __global__ void __launch_bounds__(kRingThreads, 1) norm_rope_ring_kernel(const _
             const int idx = v * R::LPH + sub;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const float2 other = inter ? make_float2(f[v][e].y, f[v][e].x) : g[v][e];
-              const float2 t = fmul2(f[v][e], ca[v][e]);
-              g[v][e] = fmul2(at[v].on ? ffma2(other, cb[v][e], t) : t, r);
+              // where nothing turns, g or cb are zeros; a neighbour that is not finite must not meet them
+              const float2 other = !INTER ? g[v][e] : at[v].on ? make_float2(f[v][e].y, f[v][e].x) : make_float2(0.f, 0.f);
+              g[v][e] = fmul2(ffma2(other, cb[v][e], fmul2(f[v][e], ca[v][e])), r);
             }
             if (hh + grp + x * R::SUB < n && R::in(idx, D)) store16(p.chk, dst + h * D + idx * 8, pack8<E>(g[v]));
           }
@@ -486,10 +502,8 @@ __global__ void __launch_bounds__(kRingThreads, 1) norm_rope_ring_kernel(const _
       }
     }
     __syncwarp();  // every lane has read the stage
-    const int next = p.stages == 3 ? pos[3] : p.stages == 2 ? pos[2] : pos[1];
-    fill(i + p.stages, next);
-    pass(i + p.stages, next);
-    filled = min(i + 1 + p.stages, mine);
+    fill(p.stages == 3 ? pos[3] : p.stages == 2 ? pos[2] : pos[1]);
+    cur.next();
 #pragma unroll
     for (int x = 0; x < 3; ++x) pos[x] = pos[x + 1];
     pos[3] = later;
@@ -504,15 +518,15 @@ __global__ void __launch_bounds__(kRingThreads, 1) norm_rope_ring_kernel(const _
 // registers. Block b writes the sum of its q warps to slot b and that of its k
 // warps to slot b + 1 (only one block can have both); dw_kernel adds the slots
 // in order.
-template <bool BF16, int D>
-__global__ void __launch_bounds__(kRingThreads, 1) norm_rope_bwd_kernel(const __grid_constant__ NormRopeBwdParams p) {
+template <bool BF16, int D, bool INTER>
+__global__ void __launch_bounds__(kBwdWarps * 32, 1) norm_rope_bwd_kernel(const __grid_constant__ NormRopeBwdParams p) {
   using E = Elem<BF16>;
   using T = typename E::T;
   using R = Row<D>;
   constexpr int HEADS = RingRows<D>::BWD_HEADS;
-  constexpr int UN = R::VPL == 1 ? 2 : 1;
+  constexpr int UN = D == 128 ? 2 : 1;  // rows a lane works on at a time (two at 192 to 512 spill)
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ uint64_t bars[kRingWarps][8];
+  __shared__ uint64_t bars[kBwdWarps][4];
   __shared__ int s_abort;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int lane = threadIdx.x % 32, sub = lane % R::LPH, grp = lane / R::LPH, warp = threadIdx.x / 32;
@@ -523,61 +537,65 @@ __global__ void __launch_bounds__(kRingThreads, 1) norm_rope_bwd_kernel(const __
     fence_mbar_init();
   }
   __syncthreads();
-  const int gw = blockIdx.x * kRingWarps + warp;
+  const int gw = blockIdx.x * kBwdWarps + warp;
   const bool is_q = gw < p.warps_q;
   const int heads = is_q ? p.hq : p.hkv, parts = (heads + HEADS - 1) / HEADS;
   const long long xs = is_q ? p.qs : p.ks, ds = is_q ? p.dqs : p.dks;
   const T* const x0 = static_cast<const T*>(is_q ? p.q : p.k);
   const T* const g0 = static_cast<const T*>(is_q ? p.gq : p.gk);
   T* const d0 = static_cast<T*>(is_q ? p.dq : p.dk);
-  const bool inter = p.interleaved != 0;
   Place at[R::VPL];
   float2 wt[R::VPL][4], acc[R::VPL][4];
 #pragma unroll
   for (int v = 0; v < R::VPL; ++v) {
-    at[v] = place_of(v * R::LPH + sub, p.rot, inter);
+    at[v] = place_of(v * R::LPH + sub, p.rot, INTER);
     unpack8<E>(R::in(v * R::LPH + sub, D) ? load16(p.chk, static_cast<const T*>(is_q ? p.wq : p.wk) + (v * R::LPH + sub) * 8)
                                           : make_uint4(0u, 0u, 0u, 0u),
                wt[v]);
 #pragma unroll
     for (int e = 0; e < 4; ++e) acc[v][e] = make_float2(0.f, 0.f);
   }
-  const long long units = p.rows * parts, stride = is_q ? p.warps_q : gridDim.x * kRingWarps - p.warps_q;
+  const long long units = p.rows * parts, stride = is_q ? p.warps_q : gridDim.x * kBwdWarps - p.warps_q;
   const long long first = is_q ? gw : gw - p.warps_q;
   const int mine = first < units ? (int)((units - first + stride - 1) / stride) : 0;
-  auto unit_of = [&](int i) {
-    const long long u = first + i * stride;
-    RingUnit r;
-    r.row = u / parts;
-    r.part = (int)(u - r.row * parts);
-    return r;
+  RingCursor cur, fil, ahead;  // the unit at work, the next to copy, the next whose position is read
+  cur.start(first, stride, parts);
+  fil = ahead = cur;
+  int n_ahead = 0;
+  auto position = [&]() {
+    const int x = p.rot > 0 && n_ahead < mine ? load_i32(p.chk, p.pos + ahead.row, -1) : 0;
+    ++n_ahead;
+    ahead.next();
+    return x;
   };
-  auto position = [&](int i) { return p.rot > 0 && i < mine ? load_i32(p.chk, p.pos + unit_of(i).row, -1) : 0; };
   auto bad = [&](int pos) { return p.rot > 0 && (pos < 0 || pos >= p.max_pos); };
   constexpr int SIDE = HEADS * D * 2;  // x, then dy, then the angles
-  auto fill = [&](int i, int pos) {
-    if (lane != 0 || i >= mine) return;
-    uint64_t* bar = ring.bar_of(i);
-    if (bad(pos)) {  // not copied: an empty arrival passes the stage's phase
-      mbar_arrive(bar);
-      return;
+  int filled = 0;
+  auto fill = [&](int pos) {
+    if (filled < mine && lane == 0) {
+      uint64_t* bar = ring.bar_of(filled);
+      if (bad(pos)) {  // not copied: an empty arrival passes the stage's phase
+        mbar_arrive(bar);
+      } else {
+        const int h0 = fil.part * HEADS, n = min(HEADS, heads - h0);
+        uint8_t* st = ring.at(filled);
+        mbar_arrive_expect_tx(bar, 2 * n * D * 2 + p.rot * 4);
+        ring_copy(p.chk, st, x0 + fil.row * xs + h0 * D, n * D * 2, bar);
+        ring_copy(p.chk, st + SIDE, g0 + (fil.row * heads + h0) * D, n * D * 2, bar);
+        if (p.rot > 0) ring_copy(p.chk, st + 2 * SIDE, p.table + (long long)pos * p.rot, p.rot * 4, bar);
+      }
     }
-    const RingUnit u = unit_of(i);
-    const int h0 = u.part * HEADS, n = min(HEADS, heads - h0);
-    mbar_arrive_expect_tx(bar, 2 * n * D * 2 + p.rot * 4);
-    ring_copy(p.chk, ring.at(i), x0 + u.row * xs + h0 * D, n * D * 2, bar);
-    ring_copy(p.chk, ring.at(i) + SIDE, g0 + (u.row * heads + h0) * D, n * D * 2, bar);
-    if (p.rot > 0) ring_copy(p.chk, ring.at(i) + 2 * SIDE, p.table + (long long)pos * p.rot, p.rot * 4, bar);
+    if (filled < mine) ++filled;
+    fil.next();
   };
   int pos[4];  // positions of the units in flight, oldest first, and of the next one
 #pragma unroll
-  for (int i = 0; i < 4; ++i) pos[i] = position(i);
+  for (int i = 0; i < 4; ++i) pos[i] = position();
 #pragma unroll
   for (int i = 0; i < 3; ++i)
-    if (i < p.stages) fill(i, pos[i]);
-  int filled = min(p.stages, mine);
+    if (i < p.stages) fill(pos[i]);
   for (int i = 0; i < mine; ++i) {
-    const int later = position(i + 4);
+    const int later = position();
     if (!ring.wait(i)) {
       if (lane == 0) {
         *ring.abort_flag = 1;
@@ -585,19 +603,21 @@ __global__ void __launch_bounds__(kRingThreads, 1) norm_rope_bwd_kernel(const __
       }
       break;
     }
-    const RingUnit u = unit_of(i);
-    const int h0 = u.part * HEADS, n = min(HEADS, heads - h0);
+    const int h0 = cur.part * HEADS, n = min(HEADS, heads - h0);
     const uint8_t* st = ring.at(i);
-    T* dst = d0 + u.row * ds + h0 * D;
+    T* dst = d0 + cur.row * ds + h0 * D;
     if (bad(pos[0])) {  // a position outside the table: zeros
       if (lane == 0) record_error(p.err, SDPA_ERR_BAD_INDEX);
       for (int x = lane; x < n * D / 8; x += 32) store16(p.chk, dst + x * 8, make_uint4(0u, 0u, 0u, 0u));
     } else {
       float2 c[R::VPL][4], s[R::VPL][4];
 #pragma unroll
-      for (int v = 0; v < R::VPL; ++v)
-        angles_of<true>(at[v], v * R::LPH + sub, reinterpret_cast<const float*>(st + 2 * SIDE), p.rot, inter, c[v], s[v],
+      for (int v = 0; v < R::VPL; ++v) {
+        angles_of<true>(at[v], v * R::LPH + sub, reinterpret_cast<const float*>(st + 2 * SIDE), p.rot, INTER, c[v], s[v],
                         p.chk);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[v][e] = make_float2(-s[v][e].x, -s[v][e].y);  // turned back
+      }
 #pragma unroll 1
       for (int hh = 0; hh < n; hh += R::SUB * UN) {
 #pragma unroll
@@ -615,12 +635,12 @@ __global__ void __launch_bounds__(kRingThreads, 1) norm_rope_bwd_kernel(const __
             float2 o[4];
             unpack8<E>(in ? *reinterpret_cast<const uint4*>(xr + idx * 8) : none, f[v]);
             unpack8<E>(in ? *reinterpret_cast<const uint4*>(gr + idx * 8) : none, g[v]);
-            unpack8<E>(in && at[v].on && !inter ? *reinterpret_cast<const uint4*>(gr + at[v].partner * 8) : none, o);
+            unpack8<E>(!INTER && in && at[v].on ? *reinterpret_cast<const uint4*>(gr + at[v].partner * 8) : none, o);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              // turned back: y c - partner s
-              const float2 other = inter ? make_float2(-g[v][e].y, -g[v][e].x) : make_float2(-o[e].x, -o[e].y);
-              if (at[v].on) g[v][e] = ffma2(other, s[v][e], fmul2(g[v][e], c[v][e]));
+              // where nothing turns, o or s are zeros; a neighbour that is not finite must not meet them
+              const float2 other = !INTER ? o[e] : at[v].on ? make_float2(g[v][e].y, g[v][e].x) : make_float2(0.f, 0.f);
+              g[v][e] = ffma2(other, s[v][e], fmul2(g[v][e], c[v][e]));
               ss = ffma2(f[v][e], f[v][e], ss);
               dot = ffma2(fmul2(g[v][e], wt[v][e]), f[v][e], dot);
             }
@@ -645,8 +665,8 @@ __global__ void __launch_bounds__(kRingThreads, 1) norm_rope_bwd_kernel(const __
       }
     }
     __syncwarp();  // every lane has read the stage
-    fill(i + p.stages, p.stages == 3 ? pos[3] : p.stages == 2 ? pos[2] : pos[1]);
-    filled = min(i + 1 + p.stages, mine);
+    fill(p.stages == 3 ? pos[3] : p.stages == 2 ? pos[2] : pos[1]);
+    cur.next();
 #pragma unroll
     for (int x = 0; x < 3; ++x) pos[x] = pos[x + 1];
     pos[3] = later;
@@ -656,7 +676,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) norm_rope_bwd_kernel(const __
     for (int i = max(0, filled - p.stages); i < filled; ++i) mbar_wait_drain(ring.bar_of(i), (i / p.stages) & 1);
   // the block's sums of dw, in the rings' memory: row groups of a warp by shuffles, warps in order
   __syncthreads();
-  float* sum = reinterpret_cast<float*>(smem);  // [kRingWarps][D]
+  float* sum = reinterpret_cast<float*>(smem);  // [kBwdWarps][D]
 #pragma unroll
   for (int v = 0; v < R::VPL; ++v)
 #pragma unroll
@@ -670,12 +690,12 @@ __global__ void __launch_bounds__(kRingThreads, 1) norm_rope_bwd_kernel(const __
         *reinterpret_cast<float2*>(sum + warp * D + (v * R::LPH + sub) * 8 + 2 * e) = acc[v][e];
     }
   __syncthreads();
-  const int q_warps = min(max(p.warps_q - (int)blockIdx.x * kRingWarps, 0), kRingWarps);
-  for (int i = threadIdx.x; i < 2 * D; i += kRingThreads) {
+  const int q_warps = min(max(p.warps_q - (int)blockIdx.x * kBwdWarps, 0), kBwdWarps);
+  for (int i = threadIdx.x; i < 2 * D; i += kBwdWarps * 32) {
     const bool q_side = i < D;
-    if (q_side ? q_warps == 0 : q_warps == kRingWarps) continue;
+    if (q_side ? q_warps == 0 : q_warps == kBwdWarps) continue;
     float t = 0.f;
-    for (int k = q_side ? 0 : q_warps; k < (q_side ? q_warps : kRingWarps); ++k) t += sum[k * D + i % D];
+    for (int k = q_side ? 0 : q_warps; k < (q_side ? q_warps : kBwdWarps); ++k) t += sum[k * D + i % D];
     float* to = p.part + (long long)(blockIdx.x + (q_side ? 0 : 1)) * D + i % D;
     if (SDPA_ADDR_OK(p.chk, to, 4)) *to = t;
   }
@@ -708,7 +728,7 @@ __global__ void __launch_bounds__(512) dw_kernel(const float* part, int end_q, i
 }
 
 // Stages of a warp's ring, each `bytes`: at most three, as many as fit.
-int ring_stages(int bytes) { return std::min(3, kRingSmem / (kRingWarps * bytes)); }
+int ring_stages(int bytes, int warps) { return std::min(3, kRingSmem / (warps * bytes)); }
 
 template <bool BF16, int D>
 int launch_t(NormRopeParams p, bool append, cudaStream_t s) {
@@ -721,14 +741,14 @@ int launch_t(NormRopeParams p, bool append, cudaStream_t s) {
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
       return SDPA_ERR_CUDA;
     // the rings pay from a few units a warp on; below, registers are quicker to start
-    if (p.rows * (parts_q + parts_k) >= (long long)sms * kRingWarps * 2) {
-      auto kern = norm_rope_ring_kernel<BF16, D>;
+    if (p.rows * (parts_q + parts_k) >= (long long)sms * kFwdWarps * 2) {
+      auto kern = p.interleaved ? norm_rope_ring_kernel<BF16, D, true> : norm_rope_ring_kernel<BF16, D, false>;
       p.parts_q = parts_q;
       p.parts = parts_q + parts_k;
       p.stage_bytes = HEADS * D * 2 + p.rot * 4;
-      p.stages = ring_stages(p.stage_bytes);
+      p.stages = ring_stages(p.stage_bytes, kFwdWarps);
       if (const int rc = set_kernel_smem(reinterpret_cast<const void*>(kern), kRingSmem, 100)) return rc;
-      kern<<<(unsigned)sms, kRingThreads, kRingWarps * p.stages * p.stage_bytes, s>>>(p);
+      kern<<<(unsigned)sms, kFwdWarps * 32, kFwdWarps * p.stages * p.stage_bytes, s>>>(p);
       return cudaGetLastError() == cudaSuccess ? SDPA_OK : SDPA_ERR_CUDA;
     }
   }
@@ -749,12 +769,12 @@ int launch_t(NormRopeParams p, bool append, cudaStream_t s) {
 
 template <bool BF16, int D>
 int launch_bwd_t(NormRopeBwdParams p, cudaStream_t s) {
-  auto kern = norm_rope_bwd_kernel<BF16, D>;
+  auto kern = p.interleaved ? norm_rope_bwd_kernel<BF16, D, true> : norm_rope_bwd_kernel<BF16, D, false>;
   p.stage_bytes = 2 * RingRows<D>::BWD_HEADS * D * 2 + p.rot * 4;
-  p.stages = ring_stages(p.stage_bytes);
+  p.stages = ring_stages(p.stage_bytes, kBwdWarps);
   if (const int rc = set_kernel_smem(reinterpret_cast<const void*>(kern), kRingSmem, 100)) return rc;
-  const int bytes = std::max(kRingWarps * p.stages * p.stage_bytes, kRingWarps * D * 4);
-  kern<<<(unsigned)p.blocks, kRingThreads, bytes, s>>>(p);
+  const int bytes = std::max(kBwdWarps * p.stages * p.stage_bytes, kBwdWarps * D * 4);
+  kern<<<(unsigned)p.blocks, kBwdWarps * 32, bytes, s>>>(p);
   if (cudaGetLastError() != cudaSuccess) return SDPA_ERR_CUDA;
   // launched while the kernel above runs; it waits for it before reading
   cudaLaunchConfig_t cfg = {};
@@ -766,8 +786,8 @@ int launch_bwd_t(NormRopeBwdParams p, cudaStream_t s) {
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, dw_kernel, (const float*)p.part, (p.warps_q + kRingWarps - 1) / kRingWarps,
-                            p.warps_q / kRingWarps + 1, p.blocks + 1, D, p.dwq, p.dwk, p.chk) == cudaSuccess
+  return cudaLaunchKernelEx(&cfg, dw_kernel, (const float*)p.part, (p.warps_q + kBwdWarps - 1) / kBwdWarps,
+                            p.warps_q / kBwdWarps + 1, p.blocks + 1, D, p.dwq, p.dwk, p.chk) == cudaSuccess
              ? SDPA_OK
              : SDPA_ERR_CUDA;
 }
@@ -782,8 +802,8 @@ NormRopeBwdPlan norm_rope_bwd_plan(long long rows, int hq, int hkv, int head_dim
   const int per = 2048 / (2 * head_dim);  // heads of a unit
   const long long units = rows * ((hq + per - 1) / per + (hkv + per - 1) / per);
   NormRopeBwdPlan pl;
-  pl.blocks = (int)std::max<long long>(1, std::min<long long>(kBlocks, (units + kRingWarps - 1) / kRingWarps));
-  const long long warps = (long long)pl.blocks * kRingWarps;
+  pl.blocks = (int)std::max<long long>(1, std::min<long long>(kBlocks, (units + kBwdWarps - 1) / kBwdWarps));
+  const long long warps = (long long)pl.blocks * kBwdWarps;
   pl.warps_q = (int)std::max<long long>(1, std::min(warps - 1, (warps * hq + (hq + hkv) / 2) / (hq + hkv)));
   return pl;
 }
