@@ -440,7 +440,7 @@ int check_paged(const sdpa_paged_problem* p) {
 
 // One launch of the paged attention: how it cuts a sequence's rows into items.
 struct PagedCutting {
-  bool used;
+  bool used, fits;
   int n;                         // rows of an item
   int block_heads, head_blocks;  // heads of a group in an item, items a group takes
   int tokens;                    // tokens in an item
@@ -482,6 +482,8 @@ PagedCutting paged_cutting(const sdpa_paged_problem* p, int n, int max_q, int dv
     c.split = tiles > 1 && 2 * items < 3 * most;
     if (!c.split && (long long)p->batch * ((max_q + c.tokens - 1) / c.tokens) * (items / blocks) > 0x7fff0000LL) c.split = true;
   }
+  // a block's length is a 32-bit number in the kernels
+  c.fits = (long long)p->num_heads_kv * c.head_blocks * c.dv_splits * std::max(tiles, 1LL) < (1LL << 31);
   const long long pieces = c.split && items < most ? items * std::max(tiles, 1LL) : items;
   c.workers = (int)std::max(1LL, std::min<long long>(most, pieces));
   return c;
@@ -1245,6 +1247,7 @@ int sdpa_paged_fwd(const sdpa_paged_problem* p, const void* q, const void* k_cac
   const long long qw = (long long)p->num_heads_q * d, qs = p->q_stride ? p->q_stride : qw;
   if (qs % d) return SDPA_ERR_UNSUPPORTED;  // a copy's strides are multiples of one another
   const PagedPlan pl = paged_plan(p);
+  if ((pl.rows.used && !pl.rows.fits) || (pl.chunk.used && !pl.chunk.fits)) return SDPA_ERR_UNSUPPORTED;
   if (!workspace || ws_bytes < pl.total) return SDPA_ERR_WORKSPACE_TOO_SMALL;
   if (reinterpret_cast<uintptr_t>(workspace) & 255u) return SDPA_ERR_ALIGNMENT;
   const long long ts = p->table_stride ? p->table_stride : p->max_pages;

@@ -18,10 +18,11 @@
 // per CTA, which paged_join_kernel combines in a fixed order: results are
 // bitwise reproducible.
 //
-// Roles (192 threads): warps 0-3 softmax and output, one thread per key of a
-// tile (and per value column of the output); warp 4 TMA producer, its lanes
-// each fetching one page's rows of a tile; warp 5 TMEM allocator and MMA
-// issuer. K and V tiles go through a ring of 32 KB stages (128 keys x 128
+// Roles (256 threads): warps 0-3 softmax and output, one thread per key of a
+// tile (and per value column of the output); warps 4-6 TMA producers, each
+// lane fetching one page's rows of a tile (a warp issues its lanes' copies one
+// after another, about 100 cycles each: with pages of 16 one producer warp was
+// the bound); warp 7 TMEM allocator and MMA issuer. K and V tiles go through a ring of 32 KB stages (128 keys x 128
 // columns); S^T and P are double-buffered, so S^T of the next tile is formed
 // while the softmax works on this one.
 #include <algorithm>
@@ -38,7 +39,8 @@ namespace {
 
 template <int DQK, int DV, int N>
 struct RowsCfg {
-  static constexpr int THREADS = 192;
+  static constexpr int THREADS = 256;
+  static constexpr int PRODUCERS = 3;
   static constexpr int KST = (DQK + 127) / 128;  // K stages of a tile
   static constexpr int VST = DV / 128;           // V stages of a tile
   static __device__ __forceinline__ constexpr int k_atoms(int kb) { return DQK / 64 - 2 * kb >= 2 ? 2 : 1; }
@@ -126,7 +128,7 @@ __device__ __forceinline__ void tmem_cols(uint32_t taddr, float (&s)[N]) {
 }
 
 template <int DQK, int DV, int N, bool BF16>
-__global__ void __launch_bounds__(192, 1)
+__global__ void __launch_bounds__(256, 1)
     paged_rows_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                       const __grid_constant__ CUtensorMap tmV, const __grid_constant__ PagedParams p) {
   using C = RowsCfg<DQK, DV, N>;
@@ -157,7 +159,7 @@ __global__ void __launch_bounds__(192, 1)
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  if (threadIdx.x == 0) {
+  if (threadIdx.x == 128) {  // not one of the threads that read a small batch
     for (int i = 0; i < C::NST; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
@@ -176,7 +178,7 @@ __global__ void __launch_bounds__(192, 1)
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 5) {
+  if (warp == 7) {
     tmem_alloc(tmem_holder, C::TM_COLS);
     tmem_relinquish();
   }
@@ -185,24 +187,22 @@ __global__ void __launch_bounds__(192, 1)
   const PagedShares all = paged_scan<C::THREADS>(p, scan, me, 1, 1, gridDim.x);
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
-  const int workers = (int)min((long long)gridDim.x, all.total);
-  const bool work = me < workers;
-  const long long u0 = work ? share_at(all.total, me, workers) : 0;
   if (threadIdx.x == 0 && me == 0) {
     if (SDPA_ADDR_OK(p.chk, p.total_tiles, 8)) *p.total_tiles = all.total;
     if (!all.fit) record_error(p.err, SDPA_ERR_BAD_SEQLENS);
   }
 
-  if (work) {
-    PagedWalk w;
-    w.start(p, scan->b[0], scan->i0[0], scan->block_at[0], u0, share_at(all.total, me + 1, workers));
+  if (me < min((long long)gridDim.x, all.total)) {
+    PagedWalk w = scan->start[0];
+    const long long u0 = w.u;
     if (threadIdx.x == 0) {
       PagedCut* cut = p.cuts + me;
-      if (SDPA_ADDR_OK(p.chk, cut, sizeof(PagedCut))) *cut = PagedCut{w.at, w.weight, w.b, w.i0, w.unit};
+      if (SDPA_ADDR_OK(p.chk, cut, sizeof(PagedCut))) *cut = w.cut(p);
     }
-    if (warp == 4) {
-      // ---------------------------------------------------------- producer
-      if (lane == 0) {
+    if (warp >= 4 && warp < 7) {
+      // ---------------------------------------------------------- producers
+      const int pw = warp - 4, box = lane * C::PRODUCERS + pw;  // this lane's box of a tile
+      if (lane == 0 && pw == 0) {
         prefetch_tmap(&tmQ);
         prefetch_tmap(&tmK);
         prefetch_tmap(&tmV);
@@ -214,41 +214,48 @@ __global__ void __launch_bounds__(192, 1)
         if (w.span.tiles == 0) continue;
         const PagedUnit un = paged_unit(p, w.unit);
         const int qb = nq % C::NQ;
-        if (nq >= C::NQ && !__all_sync(0xffffffffu, mbar_wait(&q_free[qb], (nq / C::NQ - 1) & 1, abort_flag))) {
+        if (pw == 0 && nq >= C::NQ &&
+            !__all_sync(0xffffffffu, mbar_wait(&q_free[qb], (nq / C::NQ - 1) & 1, abort_flag))) {
           ok = false;
           break;
         }
-        if (lane == 0) {
+        if (lane == 0 && pw == 0) {
           mbar_arrive_expect_tx(&bar_q[qb], (uint32_t)p.q_box_rows * DQK * 2);
           for (int a = 0; a < DQK / 64; ++a)
             tma_load_3d(&tmQ, &bar_q[qb], sQ + qb * C::Q_BYTES + a * (N * 128), a * 64, un.head0, w.s.row0 + w.i0);
         }
         ++nq;
-        auto box_of = [&](int j) { return paged_box(p, w.span, w.b, (w.span.tile0 + j) * kTile, lane); };
-        auto fetch = [&](const CUtensorMap* m, const PagedBox& x, int col, int atoms) -> bool {
+        auto box_of = [&](int j) { return paged_box(p, w.span, w.b, (w.span.tile0 + j) * kTile, box); };
+        auto fetch = [&](const CUtensorMap* m, const PagedBox& x, int boxes, int col, int atoms) -> bool {
           const int slot = c % C::NST;
           if (!__all_sync(0xffffffffu, mbar_wait(&empty[slot], ((c / C::NST) & 1) ^ 1, abort_flag))) return false;
-          if (lane == 0) mbar_arrive_expect_tx(&full[slot], x.live * atoms * box_bytes);
-          __syncwarp();
+          // the other warps' copies may complete before the count is set: the phase waits for this arrival
+          if (lane == 0 && pw == 0) mbar_arrive_expect_tx(&full[slot], boxes * atoms * box_bytes);
           if (x.mine) {
-            uint8_t* dst = sStage + slot * kStage + lane * box_bytes;
+            uint8_t* dst = sStage + slot * kStage + box * box_bytes;
             for (int a = 0; a < atoms; ++a)
               tma_load_4d(m, &full[slot], dst + a * 16384, col + a * 64, p.slot_first ? x.slot : un.kvh,
                           p.slot_first ? un.kvh : x.slot, x.page);
           }
+          __syncwarp();
           ++c;
           return true;
         };
+        auto boxes_of = [&](int j) { return paged_boxes(p, w.span, (w.span.tile0 + j) * kTile, 0, kTile); };
         PagedBox cur = box_of(w.j0), prev = cur;
         for (int j = w.j0; j < w.j1 && ok; ++j) {
           const PagedBox ahead = j + 1 < w.j1 ? box_of(j + 1) : cur;  // its table entry arrives while this tile's copies go out
-          for (int kb = 0; kb < C::KST && ok; ++kb) ok = fetch(&tmK, cur, kb * 128, C::k_atoms(kb));
-          if (j > w.j0)
-            for (int vb = 0; vb < C::VST && ok; ++vb) ok = fetch(&tmV, prev, vb * 128, 2);
+          const int boxes = boxes_of(j);
+          for (int kb = 0; kb < C::KST && ok; ++kb) ok = fetch(&tmK, cur, boxes, kb * 128, C::k_atoms(kb));
+          if (j > w.j0) {
+            const int before = boxes_of(j - 1);
+            for (int vb = 0; vb < C::VST && ok; ++vb) ok = fetch(&tmV, prev, before, vb * 128, 2);
+          }
           prev = cur;
           cur = ahead;
         }
-        for (int vb = 0; vb < C::VST && ok; ++vb) ok = fetch(&tmV, prev, vb * 128, 2);
+        const int last = boxes_of(w.j1 - 1);
+        for (int vb = 0; vb < C::VST && ok; ++vb) ok = fetch(&tmV, prev, last, vb * 128, 2);
       } while (ok && w.next(p));
       if (lane == 0) {
         if (!ok) {
@@ -257,9 +264,9 @@ __global__ void __launch_bounds__(192, 1)
         }
         // every copy lands before the CTA ends
         for (int k = max(0, c - C::NST); k < c; ++k) mbar_wait_drain(&full[k % C::NST], (k / C::NST) & 1);
-        for (int k = max(0, nq - C::NQ); k < nq; ++k) mbar_wait_drain(&bar_q[k % C::NQ], (k / C::NQ) & 1);
+        for (int k = max(0, nq - C::NQ); pw == 0 && k < nq; ++k) mbar_wait_drain(&bar_q[k % C::NQ], (k / C::NQ) & 1);
       }
-    } else if (warp == 5) {
+    } else if (warp == 7) {
       // ---------------------------------------------------------- MMA issuer
       if (elect_one()) {
         constexpr uint32_t ID_S = idesc_f16(128, N, BF16, false, false);
@@ -471,20 +478,21 @@ __global__ void __launch_bounds__(192, 1)
           ok = false;
           break;
         }
-        if (tid < N) s_l[tid] = (s_w[tid] + s_w[N + tid]) + (s_w[2 * N + tid] + s_w[3 * N + tid]);
-        named_bar_sync(1, 128);
         const long long row0 = w.s.row0 + w.i0;
         const bool whole = w.whole();
         // at most one item continues from the CTA before, and one into the next
         float* part = p.parts + ((long long)me * 2 + (w.at < u0 ? 0 : 1)) * (N * (DV + 2));
-        if (tid < rows && tid % p.block_heads < un.heads) {
-          const float m = s_m[tid], sum = s_l[tid];
-          if (whole) {
-            float* at = p.lse + (row0 + tid / p.block_heads) * p.hq + un.head0 + tid % p.block_heads;
-            if (SDPA_ADDR_OK(p.chk, at, 4)) *at = sum == 0.f ? -INFINITY : m * kLn2 + logf(sum);
-          } else if (SDPA_ADDR_OK(p.chk, part + N * DV + tid, 4) && SDPA_ADDR_OK(p.chk, part + N * DV + N + tid, 4)) {
-            part[N * DV + tid] = m;
-            part[N * DV + N + tid] = sum;
+        if (tid < N) {
+          const float m = s_m[tid], sum = (s_w[tid] + s_w[N + tid]) + (s_w[2 * N + tid] + s_w[3 * N + tid]);
+          s_l[tid] = whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
+          if (tid < rows && tid % p.block_heads < un.heads) {
+            if (whole) {
+              float* at = p.lse + (row0 + tid / p.block_heads) * p.hq + un.head0 + tid % p.block_heads;
+              if (SDPA_ADDR_OK(p.chk, at, 4)) *at = sum == 0.f ? -INFINITY : m * kLn2 + logf(sum);
+            } else if (SDPA_ADDR_OK(p.chk, part + N * DV + tid, 4) && SDPA_ADDR_OK(p.chk, part + N * DV + N + tid, 4)) {
+              part[N * DV + tid] = m;
+              part[N * DV + N + tid] = sum;
+            }
           }
         }
         if (keys) {
@@ -496,39 +504,41 @@ __global__ void __launch_bounds__(192, 1)
           ok = false;
           break;
         }
+        // four rows at a time: unrolled over all N, the code took longer to fetch than to run
 #pragma unroll 1
         for (int vb = 0; vb < C::VST; ++vb) {
-          float o[N];
-          if (keys) {
-            tmem_cols<N>(lanes + vb * N, o);
-          } else {
-#pragma unroll
-            for (int i = 0; i < N; ++i) o[i] = 0.f;
-          }
-          if (keys && vb == C::VST - 1) {
-            tc_fence_before();
-            mbar_arrive(o_free);
-          }
           int ti = 0, h = 0;
+#pragma unroll 1
+          for (int i0 = 0; i0 < rows; i0 += 4) {
+            uint32_t o[4] = {0u, 0u, 0u, 0u};
+            if (keys) {
+              tmem_ld4(lanes + vb * N + i0, o);
+              tmem_wait_ld();
+            }
 #pragma unroll
-          for (int i = 0; i < N; ++i) {
-            if (i < rows && h < un.heads) {
-              if (whole) {
-                const float sum = s_l[i];
-                T* at = static_cast<T*>(p.o) + ((row0 + ti) * p.hq + un.head0 + h) * DV + vb * 128 + tid;
-                const float v = o[i] * (sum == 0.f ? 0.f : 1.f / sum);
-                const uint32_t packed = E::pack(v, 0.f);
-                if (SDPA_ADDR_OK(p.chk, at, 2)) *reinterpret_cast<uint16_t*>(at) = (uint16_t)packed;
-              } else {
-                float* at = part + i * DV + vb * 128 + tid;
-                if (SDPA_ADDR_OK(p.chk, at, 4)) *at = o[i];
+            for (int e = 0; e < 4; ++e) {
+              asm volatile("" : "+r"(o[e]));
+              const int i = i0 + e;
+              const float v = __uint_as_float(o[e]) * s_l[i];
+              if (i < rows && h < un.heads) {
+                if (whole) {
+                  T* at = static_cast<T*>(p.o) + ((row0 + ti) * p.hq + un.head0 + h) * DV + vb * 128 + tid;
+                  if (SDPA_ADDR_OK(p.chk, at, 2)) *reinterpret_cast<uint16_t*>(at) = (uint16_t)E::pack(v, 0.f);
+                } else {
+                  float* at = part + i * DV + vb * 128 + tid;
+                  if (SDPA_ADDR_OK(p.chk, at, 4)) *at = v;
+                }
+              }
+              if (++h == p.block_heads) {
+                h = 0;
+                ++ti;
               }
             }
-            if (++h == p.block_heads) {
-              h = 0;
-              ++ti;
-            }
           }
+        }
+        if (keys) {
+          tc_fence_before();
+          mbar_arrive(o_free);
         }
         if (keys) {
           gs += n;
@@ -544,7 +554,7 @@ __global__ void __launch_bounds__(192, 1)
 
   tc_fence_before();
   __syncthreads();
-  if (warp == 5) {
+  if (warp == 7) {
     tc_fence_after();
     tmem_dealloc(tmem, C::TM_COLS);
   }
@@ -555,80 +565,67 @@ __global__ void __launch_bounds__(192, 1)
 // worker w - 1 (which began it) and the workers whose shares start in it:
 //   m = max m_k,  l = sum l_k 2^(m_k - m),  O = sum O_k 2^(m_k - m) / l.
 // A part holds N rows of DV values, then N maxima and N sums. CTA (w, y) joins
-// rows 16 y to 16 y + 15: with all rows of an item in one CTA the join of a
-// chunk's 128-row items took 29 us (128 columns) to 49 us (256), one round of
-// loads after another.
+// rows 8 y to 8 y + 7, each thread four columns of a row with its own copy of the
+// row's statistics: after the wait there are two rounds of loads, the cut and the
+// parts. (One CTA per item, statistics first, took 4 us where the parts were
+// small and 29 to 49 us for the 128-row items of chunks.)
+constexpr int kJoinRows = 8;
+
 template <int DV, int N, bool BF16>
 __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__ PagedParams p, int grid) {
   using E = Elem<BF16>;
   using T = typename E::T;
-  __shared__ float s_m[16], s_inv[16];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (!SDPA_ADDR_OK(p.chk, p.total_tiles, 8)) return;
-  const long long total = *reinterpret_cast<volatile long long*>(p.total_tiles);
-  const int workers = (int)min((long long)grid, total);
   const int w = blockIdx.x + 1;
-  if (w >= workers || !SDPA_ADDR_OK(p.chk, p.cuts + w, sizeof(PagedCut))) return;
-  const PagedCut cut = p.cuts[w];
-  if (share_at(total, w, workers) == cut.at || share_at(total, w - 1, workers) > cut.at) return;
-  const PagedSeq s = paged_seq(p, cut.b);
-  const int tok = min(cut.i0 + p.tokens, s.q_len) - cut.i0, r0 = blockIdx.y * 16;
-  const int rows = min(16, tok * p.block_heads - r0);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (!SDPA_ADDR_OK(p.chk, p.total_tiles, 8) || !SDPA_ADDR_OK(p.chk, p.cuts + w, sizeof(PagedCut))) return;
+  const long long total = *reinterpret_cast<volatile long long*>(p.total_tiles);
+  const PagedCut cut = p.cuts[w];  // read with the total; a worker without a share leaves it unset
+  const PagedShare share(total, grid);
+  if (w >= share.workers || share.at(w) == cut.at || share.at(w - 1) > cut.at) return;
+  const int r0 = blockIdx.y * kJoinRows, rows = min(kJoinRows, cut.tokens * p.block_heads - r0);
   if (rows <= 0) return;
   int parts = 1;  // worker w - 1, then w, w + 1, ...
-  while (w - 1 + parts < workers && share_at(total, w - 1 + parts, workers) < cut.at + cut.n) ++parts;
-  constexpr int SLOT = N * (DV + 2);
-  auto part = [&](int k) { return p.parts + ((long long)(w - 1 + k) * 2 + (k == 0 ? 1 : 0)) * SLOT; };
+  while (w - 1 + parts < share.workers && share.at(w - 1 + parts) < cut.at + cut.n) ++parts;
+  constexpr int SLOT = N * (DV + 2), V4 = DV / 4;
   const PagedUnit un = paged_unit(p, cut.unit);
-  const long long row0 = s.row0 + cut.i0;
-  auto stat = [&](int k, int i) {
-    const float* at = part(k) + N * DV + i;
-    return SDPA_ADDR_OK(p.chk, at, 4) ? *at : -INFINITY;
-  };
-  {
-    const int i = threadIdx.x / 16, q = threadIdx.x % 16, r = r0 + i;  // 16 threads a row
-    float m = -INFINITY, l = 0.f;
-    const bool live = i < rows && r % p.block_heads < un.heads;
-    if (live)
-      for (int k = q; k < parts; k += 16) m = fmaxf(m, stat(k, r));
-#pragma unroll
-    for (int o = 8; o > 0; o /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (live && m != -INFINITY)
-      for (int k = q; k < parts; k += 16) l += stat(k, N + r) * ex2(stat(k, r) - m);
-#pragma unroll
-    for (int o = 8; o > 0; o /= 2) l += __shfl_xor_sync(0xffffffffu, l, o);
-    if (live && q == 0) {
-      s_m[i] = m;
-      s_inv[i] = l == 0.f ? 0.f : 1.f / l;
-      float* at = p.lse + (row0 + r / p.block_heads) * p.hq + un.head0 + r % p.block_heads;
-      if (un.split == 0 && SDPA_ADDR_OK(p.chk, at, 4)) *at = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
-    }
-  }
-  __syncthreads();
-  constexpr int V4 = DV / 4;
-#pragma unroll 2
   for (int x = threadIdx.x; x < rows * V4; x += 256) {
-    const int i = x / V4, r = r0 + i, d = (x % V4) * 4;
-    if (r % p.block_heads >= un.heads) continue;
-    const float mr = s_m[i];
+    const int r = r0 + x / V4, d = (x % V4) * 4;
+    const int ti = r / p.block_heads, h = r - ti * p.block_heads;
+    if (h >= un.heads) continue;
+    float m = -INFINITY, l = 0.f;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (mr != -INFINITY) {
-#pragma unroll 4
-      for (int k = 0; k < parts; ++k) {
-        const float mk = stat(k, r), f = mk == -INFINITY ? 0.f : ex2(mk - mr);
-        const float* at = part(k) + r * DV + d;
-        const float4 v = SDPA_ADDR_OK(p.chk, at, 16) ? *reinterpret_cast<const float4*>(at) : make_float4(0.f, 0.f, 0.f, 0.f);
-        a.x = fmaf(f, v.x, a.x);
-        a.y = fmaf(f, v.y, a.y);
-        a.z = fmaf(f, v.z, a.z);
-        a.w = fmaf(f, v.w, a.w);
+    for (int k0 = 0; k0 < parts; k0 += 4) {
+      float mk[4], lk[4];
+      float4 v[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int k = k0 + e;
+        const float* part = p.parts + ((long long)(w - 1 + k) * 2 + (k == 0 ? 1 : 0)) * SLOT;
+        const bool in = k < parts && SDPA_ADDR_OK(p.chk, part + N * DV + r, 4) &&
+                        SDPA_ADDR_OK(p.chk, part + N * DV + N + r, 4) && SDPA_ADDR_OK(p.chk, part + r * DV + d, 16);
+        mk[e] = in ? part[N * DV + r] : -INFINITY;
+        lk[e] = in ? part[N * DV + N + r] : 0.f;
+        v[e] = in ? *reinterpret_cast<const float4*>(part + r * DV + d) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (mk[e] == -INFINITY) continue;  // a part without keys for this row
+        const float top = fmaxf(m, mk[e]), f = m == -INFINITY ? 0.f : ex2(m - top), g = ex2(mk[e] - top);
+        m = top;
+        l = l * f + lk[e] * g;
+        a.x = a.x * f + v[e].x * g;
+        a.y = a.y * f + v[e].y * g;
+        a.z = a.z * f + v[e].z * g;
+        a.w = a.w * f + v[e].w * g;
       }
     }
-    const float inv = s_inv[i];
-    T* dst = static_cast<T*>(p.o) + ((row0 + r / p.block_heads) * p.hq + un.head0 + r % p.block_heads) * p.dv +
-             un.split * DV + d;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const long long at = (long long)(cut.row0 + ti) * p.hq + un.head0 + h;
+    T* dst = static_cast<T*>(p.o) + at * p.dv + un.split * DV + d;
     if (SDPA_ADDR_OK(p.chk, dst, 8))
       *reinterpret_cast<uint2*>(dst) = make_uint2(E::pack(a.x * inv, a.y * inv), E::pack(a.z * inv, a.w * inv));
+    if (d == 0 && un.split == 0 && SDPA_ADDR_OK(p.chk, p.lse + at, 4))
+      p.lse[at] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
   }
 }
 
@@ -636,7 +633,7 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__
 template <int DV, int N, bool BF16>
 int launch_join_t(const PagedLaunch& L) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)L.workers - 1, N / 16);
+  cfg.gridDim = dim3((unsigned)L.workers - 1, N / kJoinRows);
   cfg.blockDim = dim3(256);
   cfg.stream = L.stream;
   cudaLaunchAttribute attr;

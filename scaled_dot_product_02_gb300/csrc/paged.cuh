@@ -13,13 +13,31 @@ constexpr int kStage = 32768;         // bytes of a ring stage
 constexpr int kSmemMax = 232448;      // 227 KB
 constexpr float kLn2 = 0.6931471805599453f;
 
-// What a CTA records of the item its share starts in, for the join.
+// What a worker records of the item its share starts in, for the join.
 struct PagedCut {
-  long long at;      // first tile of that item
-  int n, b, i0, unit;
+  long long at;          // where that item starts
+  int n, row0, tokens, unit;  // its length, first row, tokens, and place in its block
 };
 
-__device__ __forceinline__ long long share_at(long long total, int w, int workers) { return total * w / workers; }
+// Equal shares of the row of all items: where share w starts.
+struct PagedShare {
+  long long base;
+  int rest, workers;
+  __device__ __forceinline__ PagedShare(long long total, int most_workers) {
+    workers = (int)min((long long)most_workers, total);
+    base = 0;
+    rest = 0;
+    if (workers > 0) {
+      if (total < (1ll << 32)) {  // a 64-bit division costs several times as much
+        base = (unsigned)total / (unsigned)workers;
+      } else {
+        base = total / workers;
+      }
+      rest = (int)(total - base * workers);
+    }
+  }
+  __device__ __forceinline__ long long at(int w) const { return base * w + min(w, rest); }
+};
 
 // One sequence of the batch: its rows and its cached keys.
 struct PagedSeq {
@@ -112,21 +130,13 @@ struct PagedWalk {
   __device__ __forceinline__ bool whole() const { return j0 == 0 && j1 == span.tiles; }
   __device__ __forceinline__ void locate(const PagedParams& p) {
     weight = paged_weight(p, span);
-    unit = (int)((u - block_at) / weight);
+    unit = (int)((unsigned)(u - block_at) / (unsigned)weight);  // the host bounds a block's length
     at = block_at + (long long)unit * weight;
     j0 = (int)(u - at);
     j1 = p.split ? min(span.tiles, (int)min((long long)weight, u_end - at)) : span.tiles;
   }
-  __device__ __forceinline__ void start(const PagedParams& p, int b_, int i0_, long long block_at_, long long u_,
-                                        long long u_end_) {
-    u = u_;
-    u_end = u_end_;
-    block_at = block_at_;
-    b = b_;
-    i0 = i0_;
-    s = paged_mine(p, paged_seq(p, b));
-    span = paged_span(p, s, i0, i1(p));
-    locate(p);
+  __device__ __forceinline__ PagedCut cut(const PagedParams& p) const {
+    return PagedCut{at, weight, s.row0 + i0, i1(p) - i0 + 1, unit};
   }
   // The next item of the share; false when it is done.
   __device__ __forceinline__ bool next(const PagedParams& p) {
@@ -146,17 +156,16 @@ struct PagedWalk {
   }
 };
 
-// One lane's part of a key tile's copy: box_rows slots of one page.
+// One copy of a key tile: box_rows slots of one page.
 struct PagedBox {
   int page, slot;
-  uint32_t live;  // lanes with slots to copy
-  bool mine;
+  bool mine;  // its keys are seen
 };
-// Lane's box of the tile that starts at key0, of a span; every lane of the warp calls it.
-__device__ __forceinline__ PagedBox paged_box(const PagedParams& p, const PagedSpan& span, int b, int key0, int lane) {
+// Box `box` of the tile that starts at key0, of a span.
+__device__ __forceinline__ PagedBox paged_box(const PagedParams& p, const PagedSpan& span, int b, int key0, int box) {
   PagedBox x;
-  const int key = key0 + lane * p.box_rows;
-  x.mine = lane * p.box_rows < kTile && key < span.hi && key + p.box_rows > span.lo;
+  const int key = key0 + box * p.box_rows;
+  x.mine = box * p.box_rows < kTile && key < span.hi && key + p.box_rows > span.lo;
   x.page = p.num_pages;  // outside the map: reads as zeros
   x.slot = 0;
   if (x.mine) {
@@ -169,8 +178,12 @@ __device__ __forceinline__ PagedBox paged_box(const PagedParams& p, const PagedS
     else
       record_error(p.err, SDPA_ERR_BAD_INDEX);
   }
-  x.live = __popc(__ballot_sync(0xffffffffu, x.mine));
   return x;
+}
+// How many boxes of the tile's keys [k_lo, k_hi) (multiples of box_rows) are copied.
+__device__ __forceinline__ int paged_boxes(const PagedParams& p, const PagedSpan& span, int key0, int k_lo, int k_hi) {
+  const int lo = max(span.lo - key0, k_lo), hi = min(span.hi - key0, k_hi);
+  return hi > lo ? (hi + p.box_rows - 1) / p.box_rows - lo / p.box_rows : 0;
 }
 
 // Where the shares of a launch lie. Every CTA adds up the batch itself.
@@ -178,9 +191,9 @@ struct PagedShares {
   bool fit;           // every sequence fits what the host was told
   long long total;    // length of all items end to end (0 unless they fit)
 };
-struct PagedScan {    // shared memory of the scan
-  long long warp_sum[16], block_at[2];
-  int b[2], i0[2];
+struct PagedScan {    // shared memory of the scan: sums, and the walks as their shares start
+  long long warp_sum[16];
+  PagedWalk start[2];
 };
 // Adds up all sequences and finds the blocks of tokens in which the shares of
 // workers w0, w0 + step, ... (n_w of them, at most two) start. All THREADS
@@ -193,10 +206,12 @@ __device__ __forceinline__ PagedShares paged_scan(const PagedParams& p, PagedSca
   const int b_lo = min(p.batch, (int)threadIdx.x * per), b_hi = min(p.batch, b_lo + per);
   long long own = 0;
   bool fits = true;
+  PagedSeq first{0, 0, 0};
   for (int b = b_lo; b < b_hi; ++b) {
-    const PagedSeq s = paged_seq(p, b);
+    const PagedSeq s = paged_seq(p, b), mine = paged_mine(p, s);
+    if (b == b_lo) first = mine;
     if (paged_seq_ok(p, s) && (b > 0 || s.row0 == 0))
-      own += paged_units(p, paged_mine(p, s));
+      own += paged_units(p, mine);
     else
       fits = false;
   }
@@ -215,30 +230,32 @@ __device__ __forceinline__ PagedShares paged_scan(const PagedParams& p, PagedSca
     r.total += sc->warp_sum[w];
   }
   if (!r.fit) r.total = 0;
-  const int workers = (int)min((long long)most_workers, r.total);
+  const PagedShare share(r.total, most_workers);
   for (int x = 0; x < n_w; ++x) {
     const int w = w0 + x * step;
-    if (w >= workers) break;
-    const long long u = share_at(r.total, w, workers);
+    if (w >= share.workers) break;
+    const long long u = share.at(w);
     if (u < before || u >= before + own) continue;  // one thread: the share starts in its sequences
-    int b = b_lo;
-    long long at = before;
-    PagedSeq s = paged_mine(p, paged_seq(p, b));
-    for (long long n = paged_units(p, s); u >= at + n; n = paged_units(p, s)) {
-      at += n;
-      s = paged_mine(p, paged_seq(p, ++b));
-    }
-    int i0 = 0;
+    PagedWalk& k = sc->start[x];
+    k.u = u;
+    k.u_end = share.at(w + 1);
+    k.b = b_lo;
+    k.block_at = before;
+    k.s = b_hi - b_lo == 1 ? first : paged_mine(p, paged_seq(p, b_lo));
+    if (b_hi - b_lo > 1)
+      for (long long n = paged_units(p, k.s); u >= k.block_at + n; n = paged_units(p, k.s)) {
+        k.block_at += n;
+        k.s = paged_mine(p, paged_seq(p, ++k.b));
+      }
+    k.i0 = 0;
     while (true) {
-      const long long n = (long long)p.units_per_block *
-                          paged_weight(p, paged_span(p, s, i0, min(i0 + p.tokens, s.q_len) - 1));
-      if (u < at + n) break;
-      at += n;
-      i0 += p.tokens;
+      k.span = paged_span(p, k.s, k.i0, k.i1(p));
+      const long long n = (long long)p.units_per_block * paged_weight(p, k.span);
+      if (u < k.block_at + n) break;
+      k.block_at += n;
+      k.i0 += p.tokens;
     }
-    sc->b[x] = b;
-    sc->i0[x] = i0;
-    sc->block_at[x] = at;
+    k.locate(p);
   }
   __syncthreads();
   return r;
@@ -281,17 +298,16 @@ struct PagedFeed {
     }
   }
   // Worker `me` of `workers`; x: its place in the scan.
-  __device__ __forceinline__ void start(const PagedParams& p, const PagedScan* sc, int x, long long total, int me,
-                                        int workers, int lane) {
+  __device__ __forceinline__ void start(const PagedParams& p, const PagedScan* sc, int x, int me, int workers, int lane) {
     u0 = 0;
     tickets = blocks = 0;
     more = me < workers;
     if (!more) return;
     if (p.split) {
-      u0 = share_at(total, me, workers);
-      w.start(p, sc->b[x], sc->i0[x], sc->block_at[x], u0, share_at(total, me + 1, workers));
+      w = sc->start[x];
+      u0 = w.u;
       PagedCut* cut = p.cuts + me;
-      if (lane == 0 && SDPA_ADDR_OK(p.chk, cut, sizeof(PagedCut))) *cut = PagedCut{w.at, w.weight, w.b, w.i0, w.unit};
+      if (lane == 0 && SDPA_ADDR_OK(p.chk, cut, sizeof(PagedCut))) *cut = w.cut(p);
     } else {
       blocks = (p.max_q + p.tokens - 1) / p.tokens;
       tickets = blocks * p.batch * p.units_per_block;

@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(256, 1)
       int c = 0, nq = 0, np = 0;
       bool ok = true;
       PagedFeed feed;
-      feed.start(p, scan, 0, all.total, me, workers, lane);
+      feed.start(p, scan, 0, me, workers, lane);
       const PagedWalk& w = feed.w;
       while (true) {
         const int e = np & 1;
@@ -151,10 +151,10 @@ __global__ void __launch_bounds__(256, 1)
           auto copy = [&](const CUtensorMap* m, int slot, uint8_t* dst, int col, const PagedBox& x) {
             tma_load_4d(m, &full[slot], dst, col, p.slot_first ? x.slot : un.kvh, p.slot_first ? un.kvh : x.slot, x.page);
           };
-          auto load_k = [&](const PagedBox& x) -> bool {
+          auto load_k = [&](const PagedBox& x, int key0) -> bool {
             for (int kb = 0; kb < C::KST; ++kb) {
               const int atoms = C::k_atoms(kb);
-              const int slot = next_slot(x.live * atoms * box_bytes);
+              const int slot = next_slot(paged_boxes(p, w.span, key0, 0, kTile) * atoms * box_bytes);
               if (slot < 0) return false;
               uint8_t* dst = sStage + slot * kStage + lane * box_bytes;
               if (x.mine)
@@ -162,11 +162,11 @@ __global__ void __launch_bounds__(256, 1)
             }
             return true;
           };
-          auto load_v = [&](const PagedBox& x) -> bool {
+          auto load_v = [&](const PagedBox& x, int key0) -> bool {
             const int first = lane * p.box_rows;  // this lane's first key of the tile
             for (int vs = 0; vs < C::VST; ++vs) {
               const bool here = x.mine && first >= vs * C::VROWS && first < (vs + 1) * C::VROWS;
-              const int n = __popc(__ballot_sync(0xffffffffu, here));
+              const int n = paged_boxes(p, w.span, key0, vs * C::VROWS, (vs + 1) * C::VROWS);
               const int slot = next_slot(n * (DV / 64) * box_bytes);
               if (slot < 0) return false;
               uint8_t* dst = sStage + slot * kStage + (first - vs * C::VROWS) * 128;
@@ -179,12 +179,13 @@ __global__ void __launch_bounds__(256, 1)
           PagedBox cur = box_of(w.j0), prev = cur;
           for (int j = w.j0; j < w.j1 && ok; ++j) {
             const PagedBox ahead = j + 1 < w.j1 ? box_of(j + 1) : cur;
-            ok = load_k(cur);
-            if (ok && j > w.j0) ok = load_v(prev);
+            const int key0 = (w.span.tile0 + j) * kTile;
+            ok = load_k(cur, key0);
+            if (ok && j > w.j0) ok = load_v(prev, key0 - kTile);
             prev = cur;
             cur = ahead;
           }
-          if (ok) ok = load_v(prev);
+          if (ok) ok = load_v(prev, (w.span.tile0 + w.j1 - 1) * kTile);
           if (!ok) break;
         }
         feed.next(p, lane);

@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(PairCfg::THREADS, 1)
       int c = 0, nq = 0, np = 0;
       bool ok = true;
       PagedFeed feed;
-      feed.start(p, scan, warp - 8, all.total, (warp - 8) * gridDim.x + blockIdx.x, workers, lane);
+      feed.start(p, scan, warp - 8, (warp - 8) * gridDim.x + blockIdx.x, workers, lane);
       const PagedWalk& w = feed.w;
       while (true) {
         const int e = np & 1;
@@ -172,13 +172,14 @@ __global__ void __launch_bounds__(PairCfg::THREADS, 1)
           PagedBox cur = box_of(w.j0);
           for (int j = w.j0; j < w.j1 && ok; ++j) {
             const PagedBox ahead = j + 1 < w.j1 ? box_of(j + 1) : cur;  // arrives while this tile's copies go out
+            const int key0 = (w.span.tile0 + j) * kTile;
             for (int kv = 0; kv < 2; ++kv, ++c) {
               const int slot = c % C::NST;
               if (!__all_sync(0xffffffffu, mbar_wait(&P.empty[slot], ((c / C::NST) & 1) ^ 1, abort_flag))) {
                 ok = false;
                 break;
               }
-              if (lane == 0) mbar_arrive_expect_tx(&P.full[slot], cur.live * 2 * box_bytes);
+              if (lane == 0) mbar_arrive_expect_tx(&P.full[slot], paged_boxes(p, w.span, key0, 0, kTile) * 2 * box_bytes);
               __syncwarp();
               if (cur.mine) {
                 uint8_t* dst = P.sStage + slot * kStage + lane * box_bytes;
