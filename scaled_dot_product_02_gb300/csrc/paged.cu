@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(256, 1)
 
   if (threadIdx.x == 128) {  // not one of the threads that read a small batch
     for (int i = 0; i < C::NST; ++i) {
-      mbar_init(&full[i], 1);
+      mbar_init(&full[i], C::PRODUCERS);  // every producer, so that none falls a phase behind
       mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < C::NQ; ++i) {
@@ -229,8 +229,14 @@ __global__ void __launch_bounds__(256, 1)
         auto fetch = [&](const CUtensorMap* m, const PagedBox& x, int boxes, int col, int atoms) -> bool {
           const int slot = c % C::NST;
           if (!__all_sync(0xffffffffu, mbar_wait(&empty[slot], ((c / C::NST) & 1) ^ 1, abort_flag))) return false;
-          // the other warps' copies may complete before the count is set: the phase waits for this arrival
-          if (lane == 0 && pw == 0) mbar_arrive_expect_tx(&full[slot], boxes * atoms * box_bytes);
+          // every producer arrives, with copies in this stage or not (the ring could go on without one otherwise and
+          // leave it a phase behind); the others' copies may complete before producer 0 sets the byte count
+          if (lane == 0) {
+            if (pw == 0)
+              mbar_arrive_expect_tx(&full[slot], boxes * atoms * box_bytes);
+            else
+              mbar_arrive(&full[slot]);
+          }
           if (x.mine) {
             uint8_t* dst = sStage + slot * kStage + box * box_bytes;
             for (int a = 0; a < atoms; ++a)

@@ -180,6 +180,49 @@ __device__ __forceinline__ PagedBox paged_box(const PagedParams& p, const PagedS
   }
   return x;
 }
+// All boxes of a tile, known to every lane of a warp, so that one elected thread
+// can issue the copies back to back.
+struct PagedIds {
+  int page[8], slot[8];
+  uint32_t mine;  // bit e: box e is copied
+};
+__device__ __forceinline__ PagedIds paged_ids(const PagedBox& x) {  // lane e holds box e
+  PagedIds r;
+  r.mine = __ballot_sync(0xffffffffu, x.mine);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    r.page[e] = __shfl_sync(0xffffffffu, x.page, e);
+    r.slot[e] = __shfl_sync(0xffffffffu, x.slot, e);
+  }
+  return r;
+}
+// Copies NB boxes of 128 columns to a stage (two blocks of 64 columns, 16 KB
+// apart); a single thread calls it. ALL: every box, without a test for each.
+template <int NB, bool ALL>
+__device__ __forceinline__ void paged_copy128(const PagedParams& p, const CUtensorMap* m, uint64_t* bar, uint8_t* stage,
+                                              int kvh, const PagedIds& x) {
+#pragma unroll
+  for (int e = 0; e < NB; ++e)
+    if (ALL || (x.mine >> e & 1)) {
+      const int c1 = p.slot_first ? x.slot[e] : kvh, c2 = p.slot_first ? kvh : x.slot[e];
+      uint8_t* dst = stage + e * p.box_rows * 128;
+      tma_load_4d(m, bar, dst, 0, c1, c2, x.page[e]);
+      tma_load_4d(m, bar, dst + 16384, 64, c1, c2, x.page[e]);
+    }
+}
+__device__ __forceinline__ void paged_copy128(const PagedParams& p, const CUtensorMap* m, uint64_t* bar, uint8_t* stage,
+                                              int kvh, const PagedIds& x) {
+  if (x.mine == 0xffu)
+    paged_copy128<8, true>(p, m, bar, stage, kvh, x);
+  else if (p.box_rows == 32 && x.mine == 0xfu)
+    paged_copy128<4, true>(p, m, bar, stage, kvh, x);
+  else if (p.box_rows == 64 && x.mine == 0x3u)
+    paged_copy128<2, true>(p, m, bar, stage, kvh, x);
+  else if (p.box_rows == 128)
+    paged_copy128<1, true>(p, m, bar, stage, kvh, x);
+  else
+    paged_copy128<8, false>(p, m, bar, stage, kvh, x);
+}
 // How many boxes of the tile's keys [k_lo, k_hi) (multiples of box_rows) are copied.
 __device__ __forceinline__ int paged_boxes(const PagedParams& p, const PagedSpan& span, int key0, int k_lo, int k_hi) {
   const int lo = max(span.lo - key0, k_lo), hi = min(span.hi - key0, k_hi);
@@ -263,7 +306,7 @@ __device__ __forceinline__ PagedShares paged_scan(const PagedParams& p, PagedSca
 
 // A piece of work as the scheduler of a pipeline publishes it.
 struct PagedPiece {
-  int row0, q_len, kv_len, i0, unit;  // row0 < 0: no more
+  int row0, q_len, kv_len, b, i0, unit;  // row0 < 0: no more
   int j0, j1;                         // its key tiles, counted from the span's first
   int slot;                           // its partial result, or -1: the whole item
 };
@@ -321,7 +364,7 @@ struct PagedFeed {
       take(p, lane);
   }
   __device__ __forceinline__ PagedPiece piece() const {
-    return PagedPiece{more ? w.s.row0 : -1, w.s.q_len, w.s.kv_len, w.i0, w.unit, w.j0, w.j1,
+    return PagedPiece{more ? w.s.row0 : -1, w.s.q_len, w.s.kv_len, w.b, w.i0, w.unit, w.j0, w.j1,
                       w.whole() ? -1 : (w.at < u0 ? 0 : 1)};
   }
 };

@@ -11,8 +11,9 @@
 // same keys at the same time; or, when the items are few, as equal shares of
 // all key tiles with the crossing items joined afterwards (paged.cu).
 //
-// Roles (256 threads): warp 0 scheduler and TMA producer (its lanes each fetch
-// one page's rows), warp 1 TMEM allocator and MMA issuer, warps 4-7 softmax
+// Roles (256 threads): warp 0 scheduler and TMA producer, warps 2 and 3 further
+// producers (each lane fetches one page's rows; a warp issues its lanes' copies
+// one after another), warp 1 TMEM allocator and MMA issuer, warps 4-7 softmax
 // and output, one thread per query row. The scheduler hands each piece of work
 // to the others through a two-entry queue in shared memory.
 #include <algorithm>
@@ -30,6 +31,7 @@ struct ChunkCfg {
   static constexpr int THREADS = 256;
   static constexpr int KST = (DQK + 127) / 128;  // K stages of a tile (128 keys x up to 128 columns)
   static __device__ __forceinline__ constexpr int k_atoms(int kb) { return DQK / 64 - 2 * kb >= 2 ? 2 : 1; }
+  static constexpr int DV_ITEM = DV;
   static constexpr int VROWS = kStage / (DV * 2);  // keys of a V stage
   static constexpr int VST = kTile / VROWS;
   static constexpr int V_ATOM = VROWS * 128;       // bytes of 64 columns of a V stage
@@ -41,6 +43,69 @@ struct ChunkCfg {
   static constexpr int TM_S = DV;                  // TMEM columns: O, then two S / P buffers
   static_assert(SMEM <= kSmemMax && NST >= VST && DV + 256 <= 512, "the tile plan fits one SM");
 };
+
+// Producer `pw` of three copies its boxes (3 e + pw, one a lane) of the K and V
+// tiles [j0, j1) of an item through the ring, in the order the MMA issuer takes
+// them; c counts the stages. Every producer arrives on each stage, with copies in
+// it or not, or the ring could go on without one and leave it a phase behind.
+// Producer 0 sets the byte count; the others' copies may complete before it.
+template <class C>
+__device__ __forceinline__ bool load_tiles(const PagedParams& p, const CUtensorMap& tmK, const CUtensorMap& tmV,
+                                           const PagedSpan& span, int b, const PagedUnit& un, int j0, int j1, uint64_t* full,
+                                           uint64_t* empty, uint8_t* sStage, int& c, int pw, int lane,
+                                           volatile int* abort_flag) {
+  const int box = lane * 3 + pw, first = box * p.box_rows;  // this lane's box of a tile, its first key
+  const uint32_t box_bytes = p.box_rows * 128;
+  auto next_slot = [&](uint32_t bytes) -> int {
+    const int slot = c % C::NST;
+    if (!__all_sync(0xffffffffu, mbar_wait(&empty[slot], ((c / C::NST) & 1) ^ 1, abort_flag))) return -1;
+    if (lane == 0) {
+      if (pw == 0)
+        mbar_arrive_expect_tx(&full[slot], bytes);
+      else
+        mbar_arrive(&full[slot]);
+    }
+    ++c;
+    return slot;
+  };
+  auto copy = [&](const CUtensorMap* m, int slot, uint8_t* dst, int col, const PagedBox& x) {
+    tma_load_4d(m, &full[slot], dst, col, p.slot_first ? x.slot : un.kvh, p.slot_first ? un.kvh : x.slot, x.page);
+  };
+  auto load_k = [&](const PagedBox& x, int key0) -> bool {
+    const int boxes = paged_boxes(p, span, key0, 0, kTile);
+    for (int kb = 0; kb < C::KST; ++kb) {
+      const int atoms = C::k_atoms(kb), slot = next_slot(boxes * atoms * box_bytes);
+      if (slot < 0) return false;
+      uint8_t* dst = sStage + slot * kStage + first * 128;
+      if (x.mine)
+        for (int a = 0; a < atoms; ++a) copy(&tmK, slot, dst + a * 16384, kb * 128 + a * 64, x);
+      __syncwarp();
+    }
+    return true;
+  };
+  auto load_v = [&](const PagedBox& x, int key0) -> bool {
+    for (int vs = 0; vs < C::VST; ++vs) {
+      const int slot = next_slot(paged_boxes(p, span, key0, vs * C::VROWS, (vs + 1) * C::VROWS) * (C::DV_ITEM / 64) * box_bytes);
+      if (slot < 0) return false;
+      uint8_t* dst = sStage + slot * kStage + (first - vs * C::VROWS) * 128;
+      if (x.mine && first / C::VROWS == vs)
+        for (int a = 0; a < C::DV_ITEM / 64; ++a) copy(&tmV, slot, dst + a * C::V_ATOM, un.split * C::DV_ITEM + a * 64, x);
+      __syncwarp();
+    }
+    return true;
+  };
+  auto box_of = [&](int j) { return paged_box(p, span, b, (span.tile0 + j) * kTile, box); };
+  PagedBox cur = box_of(j0), prev = cur;
+  for (int j = j0; j < j1; ++j) {
+    const PagedBox ahead = j + 1 < j1 ? box_of(j + 1) : cur;  // its table entry arrives while this tile's copies go out
+    const int key0 = (span.tile0 + j) * kTile;
+    if (!load_k(cur, key0)) return false;
+    if (j > j0 && !load_v(prev, key0 - kTile)) return false;
+    prev = cur;
+    cur = ahead;
+  }
+  return load_v(prev, (span.tile0 + j1 - 1) * kTile);
+}
 
 template <int DQK, int DV, bool BF16>
 __global__ void __launch_bounds__(256, 1)
@@ -73,14 +138,14 @@ __global__ void __launch_bounds__(256, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::NST; ++i) {
-      mbar_init(&full[i], 1);
+      mbar_init(&full[i], 3);  // every producer, so that none falls a phase behind
       mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar_s[i], 1);
       mbar_init(&bar_p[i], 128);
       mbar_init(&sched_full[i], 1);
-      mbar_init(&sched_empty[i], 129);
+      mbar_init(&sched_empty[i], 131);  // issuer, two producers, 128 softmax threads
     }
     for (uint64_t* b : {bar_q, bar_o, q_free, bar_drain}) mbar_init(b, 1);
     mbar_init(o_free, 128);
@@ -110,7 +175,6 @@ __global__ void __launch_bounds__(256, 1)
         prefetch_tmap(&tmK);
         prefetch_tmap(&tmV);
       }
-      const uint32_t box_bytes = p.box_rows * 128;
       int c = 0, nq = 0, np = 0;
       bool ok = true;
       PagedFeed feed;
@@ -140,52 +204,7 @@ __global__ void __launch_bounds__(256, 1)
               tma_load_3d(&tmQ, bar_q, sQ + a * 16384, a * 64, un.head0, w.s.row0 + w.i0);
           }
           ++nq;
-          auto next_slot = [&](uint32_t bytes) -> int {
-            const int slot = c % C::NST;
-            if (!__all_sync(0xffffffffu, mbar_wait(&empty[slot], ((c / C::NST) & 1) ^ 1, abort_flag))) return -1;
-            if (lane == 0) mbar_arrive_expect_tx(&full[slot], bytes);
-            __syncwarp();
-            ++c;
-            return slot;
-          };
-          auto copy = [&](const CUtensorMap* m, int slot, uint8_t* dst, int col, const PagedBox& x) {
-            tma_load_4d(m, &full[slot], dst, col, p.slot_first ? x.slot : un.kvh, p.slot_first ? un.kvh : x.slot, x.page);
-          };
-          auto load_k = [&](const PagedBox& x, int key0) -> bool {
-            for (int kb = 0; kb < C::KST; ++kb) {
-              const int atoms = C::k_atoms(kb);
-              const int slot = next_slot(paged_boxes(p, w.span, key0, 0, kTile) * atoms * box_bytes);
-              if (slot < 0) return false;
-              uint8_t* dst = sStage + slot * kStage + lane * box_bytes;
-              if (x.mine)
-                for (int a = 0; a < atoms; ++a) copy(&tmK, slot, dst + a * 16384, kb * 128 + a * 64, x);
-            }
-            return true;
-          };
-          auto load_v = [&](const PagedBox& x, int key0) -> bool {
-            const int first = lane * p.box_rows;  // this lane's first key of the tile
-            for (int vs = 0; vs < C::VST; ++vs) {
-              const bool here = x.mine && first >= vs * C::VROWS && first < (vs + 1) * C::VROWS;
-              const int n = paged_boxes(p, w.span, key0, vs * C::VROWS, (vs + 1) * C::VROWS);
-              const int slot = next_slot(n * (DV / 64) * box_bytes);
-              if (slot < 0) return false;
-              uint8_t* dst = sStage + slot * kStage + (first - vs * C::VROWS) * 128;
-              if (here)
-                for (int a = 0; a < DV / 64; ++a) copy(&tmV, slot, dst + a * C::V_ATOM, un.split * DV + a * 64, x);
-            }
-            return true;
-          };
-          auto box_of = [&](int j) { return paged_box(p, w.span, w.b, (w.span.tile0 + j) * kTile, lane); };
-          PagedBox cur = box_of(w.j0), prev = cur;
-          for (int j = w.j0; j < w.j1 && ok; ++j) {
-            const PagedBox ahead = j + 1 < w.j1 ? box_of(j + 1) : cur;
-            const int key0 = (w.span.tile0 + j) * kTile;
-            ok = load_k(cur, key0);
-            if (ok && j > w.j0) ok = load_v(prev, key0 - kTile);
-            prev = cur;
-            cur = ahead;
-          }
-          if (ok) ok = load_v(prev, (w.span.tile0 + w.j1 - 1) * kTile);
+          ok = load_tiles<C>(p, tmK, tmV, w.span, w.b, un, w.j0, w.j1, full, empty, sStage, c, 0, lane, abort_flag);
           if (!ok) break;
         }
         feed.next(p, lane);
@@ -198,6 +217,35 @@ __global__ void __launch_bounds__(256, 1)
         // every copy lands before the CTA ends
         for (int k = max(0, c - C::NST); k < c; ++k) mbar_wait_drain(&full[k % C::NST], (k / C::NST) & 1);
         if (nq > 0) mbar_wait_drain(bar_q, (nq - 1) & 1);
+      }
+    } else if (warp == 2 || warp == 3) {
+      // ---------------------------------------------------------- further producers
+      int c = 0, np = 0;
+      bool ok = true;
+      while (true) {
+        const int e = np & 1;
+        if (!__all_sync(0xffffffffu, mbar_wait(&sched_full[e], (np >> 1) & 1, abort_flag))) {
+          ok = false;
+          break;
+        }
+        const PagedPiece w = pieces[e];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sched_empty[e]);
+        ++np;
+        if (w.row0 < 0) break;
+        if (w.j1 == w.j0) continue;
+        const PagedSpan span =
+            paged_span(p, PagedSeq{w.row0, w.q_len, w.kv_len}, w.i0, min(w.i0 + p.tokens, w.q_len) - 1);
+        ok = load_tiles<C>(p, tmK, tmV, span, w.b, paged_unit(p, w.unit), w.j0, w.j1, full, empty, sStage, c, warp - 1, lane,
+                           abort_flag);
+        if (!ok) break;
+      }
+      if (lane == 0) {
+        if (!ok) {
+          *abort_flag = 1;
+          record_error(p.err, SDPA_ERR_TIMEOUT);
+        }
+        for (int k = max(0, c - C::NST); k < c; ++k) mbar_wait_drain(&full[k % C::NST], (k / C::NST) & 1);
       }
     } else if (warp == 1) {
       // ---------------------------------------------------------- MMA issuer

@@ -169,26 +169,27 @@ __global__ void __launch_bounds__(PairCfg::THREADS, 1)
           }
           ++nq;
           auto box_of = [&](int j) { return paged_box(p, w.span, w.b, (w.span.tile0 + j) * kTile, lane); };
-          PagedBox cur = box_of(w.j0);
+          PagedIds cur = paged_ids(box_of(w.j0));
           for (int j = w.j0; j < w.j1 && ok; ++j) {
-            const PagedBox ahead = j + 1 < w.j1 ? box_of(j + 1) : cur;  // arrives while this tile's copies go out
-            const int key0 = (w.span.tile0 + j) * kTile;
+            PagedBox ahead;  // its table entry arrives while this tile's copies go out
+            if (j + 1 < w.j1) ahead = box_of(j + 1);
+            const uint32_t bytes = paged_boxes(p, w.span, (w.span.tile0 + j) * kTile, 0, kTile) * 2 * box_bytes;
             for (int kv = 0; kv < 2; ++kv, ++c) {
               const int slot = c % C::NST;
               if (!__all_sync(0xffffffffu, mbar_wait(&P.empty[slot], ((c / C::NST) & 1) ^ 1, abort_flag))) {
                 ok = false;
                 break;
               }
-              if (lane == 0) mbar_arrive_expect_tx(&P.full[slot], paged_boxes(p, w.span, key0, 0, kTile) * 2 * box_bytes);
-              __syncwarp();
-              if (cur.mine) {
-                uint8_t* dst = P.sStage + slot * kStage + lane * box_bytes;
-                for (int a = 0; a < 2; ++a)
-                  tma_load_4d(kv ? &tmV : &tmK, &P.full[slot], dst + a * 16384, a * 64, p.slot_first ? cur.slot : un.kvh,
-                              p.slot_first ? un.kvh : cur.slot, cur.page);
+              // one thread issues: with two stages a pipeline, the time that the copies take to go out is on
+              // the way of the next S (issued by the lanes that hold the boxes they are serialised at some
+              // 100 cycles each)
+              if (elect_one()) {
+                mbar_arrive_expect_tx(&P.full[slot], bytes);
+                paged_copy128(p, kv ? &tmV : &tmK, &P.full[slot], P.sStage + slot * kStage, un.kvh, cur);
               }
+              __syncwarp();
             }
-            cur = ahead;
+            if (j + 1 < w.j1) cur = paged_ids(ahead);
           }
           if (!ok) break;
         }
