@@ -451,7 +451,7 @@ struct PagedCutting {
 struct PagedPlan {
   int small_q;         // sequences of at most this many new tokens go to the rows kernel, longer ones to the chunk kernel
   PagedCutting rows, chunk;
-  size_t cuts_off, parts_off, total;  // the launches run in turn and share the workspace
+  size_t cuts_off[2], parts_off[2], total;  // workspace of the rows and of the chunk kernel
 };
 // The SMs of the device the library is written for: the plan, and with it the
 // workspace size, must not depend on the device in use.
@@ -478,8 +478,11 @@ PagedCutting paged_cutting(const sdpa_paged_problem* p, int n, int max_q, int dv
     // short items are not worth the join (and its launch)
     c.split = tiles > 4;
   } else {
-    // with items enough the ticket order, which keeps the CTAs on the same keys; else equal shares
-    c.split = tiles > 1 && 2 * items < 3 * most;
+    // Whole items by ticket keep the CTAs on the same keys; splitting pays only where items are fewer than
+    // pipelines and so long that a pipeline left idle costs more than the join, some 15 tiles' time. (Items split
+    // in all cases: 2048 tokens over 131072 keys 3290 -> 3750 us, 8 x 1024 over 32768 3110 -> 4400 us, 8 x 100 over
+    // 2000 62 -> 85 us; 2048 over 16384, 1.7 items a pipeline, 413 -> 405 us.)
+    c.split = items < most && tiles * (most - items) > 15LL * most;
     if (!c.split && (long long)p->batch * ((max_q + c.tokens - 1) / c.tokens) * (items / blocks) > 0x7fff0000LL) c.split = true;
   }
   // a block's length is a 32-bit number in the kernels
@@ -502,16 +505,15 @@ PagedPlan paged_plan(const sdpa_paged_problem* p) {
     pl.rows = paged_cutting(p, rows <= 16 ? 16 : (rows <= 32 || most == 32) ? 32 : 64, max_q, dv);
   }
   if (p->seqlen_q > pl.small_q) pl.chunk = paged_cutting(p, 128, p->seqlen_q, std::min(dv, 256));
-  pl.cuts_off = 256;
-  int workers = 0;
-  size_t parts = 0;
-  for (const PagedCutting* c : {&pl.rows, &pl.chunk})
-    if (c->used) {
-      workers = std::max(workers, c->workers);
-      if (c->split) parts = std::max(parts, (size_t)c->workers * 2 * c->n * (c->dv_item + 2) * 4);
-    }
-  pl.parts_off = round_up(pl.cuts_off + (size_t)workers * paged_cut_bytes(), 256);
-  pl.total = pl.parts_off + parts;
+  size_t at = 256;  // totals and tickets
+  for (int x = 0; x < 2; ++x) {
+    const PagedCutting& c = x ? pl.chunk : pl.rows;
+    pl.cuts_off[x] = at;
+    if (c.used) at = round_up(at + (size_t)c.workers * paged_cut_bytes(), 256);
+    pl.parts_off[x] = at;
+    if (c.used && c.split) at = round_up(at + (size_t)c.workers * 2 * c.n * (c.dv_item + 2) * 4, 256);
+  }
+  pl.total = at;
   return pl;
 }
 
@@ -1278,7 +1280,8 @@ int sdpa_paged_fwd(const sdpa_paged_problem* p, const void* q, const void* k_cac
   AddrTable* chk = bind_extents({outs[0], outs[1], outs[2], ins[0], ins[1], ins[2], ins[3], ins[4], ins[5]}, err, s);
   if (kAddrCheck && !chk) return SDPA_ERR_CUDA;
   int launches = 0;
-  for (const PagedCutting* c : {&pl.rows, &pl.chunk}) {
+  // the chunk kernel first: the rows kernel is launched while it runs and fills its tail
+  for (const PagedCutting* c : {&pl.chunk, &pl.rows}) {
     if (!c->used) continue;
     const bool small = c == &pl.rows;
     PagedLaunch L;
@@ -1314,10 +1317,11 @@ int sdpa_paged_fwd(const sdpa_paged_problem* p, const void* q, const void* k_cac
     P.table_stride = ts;
     P.o = o;
     P.lse = lse;
-    P.total_tiles = reinterpret_cast<long long*>(ws);
+    P.behind = small && pl.chunk.used;
+    P.total_tiles = reinterpret_cast<long long*>(ws + (small ? 0 : 64));
     P.tickets = reinterpret_cast<int*>(ws + 128);
-    P.cuts = reinterpret_cast<PagedCut*>(ws + pl.cuts_off);
-    P.parts = reinterpret_cast<float*>(ws + pl.parts_off);
+    P.cuts = reinterpret_cast<PagedCut*>(ws + pl.cuts_off[small ? 0 : 1]);
+    P.parts = reinterpret_cast<float*>(ws + pl.parts_off[small ? 0 : 1]);
     P.err = err;
     P.chk = chk;
     const bool pair = !small && d == 128;

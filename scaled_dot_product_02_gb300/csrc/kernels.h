@@ -249,6 +249,7 @@ struct PagedParams {
   int units_per_block;         // items of one block of tokens: kv heads x head_blocks x dv_splits
   int small_q, small;          // this launch serves the sequences of at most small_q tokens (small), or the others
   int split;                   // items may be split over workers
+  int behind;                  // rows kernel: launched behind the chunk kernel of the same call, to fill its tail
   int q_box_rows;              // rows the Q copy brings: tokens x block_heads
   int causal, window;          // window < 0: none
   float scale_log2;

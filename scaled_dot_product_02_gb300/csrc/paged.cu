@@ -564,6 +564,8 @@ __global__ void __launch_bounds__(256, 1)
     tc_fence_after();
     tmem_dealloc(tmem, C::TM_COLS);
   }
+  // launched while the chunk kernel of the same call runs, this one ends after it
+  if (p.behind && blockIdx.x == 0 && threadIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // Items that cross cuts: CTA w joins the item that cut w (the start of worker
@@ -655,8 +657,17 @@ int launch_rows_t(const PagedLaunch& L, int* launches) {
   using C = RowsCfg<DQK, DV, N>;
   auto kern = paged_rows_kernel<DQK, DV, N, BF16>;
   if (const int rc = set_kernel_smem(reinterpret_cast<const void*>(kern), C::SMEM, -1)) return rc;
-  kern<<<(unsigned)L.workers, C::THREADS, C::SMEM, L.stream>>>(L.tmQ, L.tmK, L.tmV, L.p);
-  if (cudaGetLastError() != cudaSuccess) return SDPA_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)L.workers);
+  cfg.blockDim = dim3(C::THREADS);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = L.stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = L.p.behind ? 1 : 0;
+  if (cudaLaunchKernelEx(&cfg, kern, L.tmQ, L.tmK, L.tmV, L.p) != cudaSuccess) return SDPA_ERR_CUDA;
   ++*launches;
   if (L.workers == 1 || !L.p.split) return SDPA_OK;  // no item crosses a cut
   ++*launches;

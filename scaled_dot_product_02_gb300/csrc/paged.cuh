@@ -2,6 +2,8 @@
 // kernels: sequences, the keys that a block of tokens sees, and the cutting of
 // all key tiles into equal shares (paged.cu describes it).
 #pragma once
+#include <climits>
+
 #include "common.cuh"
 #include "kernels.h"
 #include "ptx.cuh"
@@ -312,38 +314,75 @@ struct PagedPiece {
 };
 
 // Where a pipeline's pieces come from: its share of the tiles (p.split), or
-// the tickets, last block of tokens first and the items of a block together.
-// A whole warp walks it.
+// the tickets. The ticket order takes the sequences with the most keys first (up
+// to kSorted of them; a larger batch in its own order), the last blocks of
+// tokens first, and the items of a block together: the longest items start
+// first, and the CTAs at work share the same few sequences' keys. A whole warp
+// walks it.
+constexpr int kSorted = 128;
+
 struct PagedFeed {
   PagedWalk w;
   bool more;
   long long u0;
-  int blocks, tickets;
+  long long key;          // of the current sequence in the order: its keys, then its place
+  int blocks, done;       // its blocks of tokens, those of the sequences before it
 
-  __device__ __forceinline__ void take(const PagedParams& p, int lane) {
-    while (true) {
-      int t = tickets;  // a counter the address check rejects hands out none
-      if (lane == 0 && SDPA_ADDR_OK(p.chk, p.tickets, 4)) t = atomicAdd(p.tickets, 1);
-      t = __shfl_sync(0xffffffffu, t, 0);
-      more = t < tickets;
-      if (!more) return;
-      w.unit = t % p.units_per_block;
-      t /= p.units_per_block;
-      w.b = t % p.batch;
-      w.i0 = (blocks - 1 - t / p.batch) * p.tokens;
-      w.s = paged_mine(p, paged_seq(p, w.b));
-      if (w.i0 >= w.s.q_len) continue;
-      w.span = paged_span(p, w.s, w.i0, w.i1(p));
-      w.at = 0;
-      w.j0 = 0;
-      w.j1 = w.span.tiles;
-      return;
+  // The next sequence of the order with rows; false when there is none.
+  __device__ __forceinline__ bool advance(const PagedParams& p, int lane) {
+    long long best = -1;  // the largest key below the current one
+    if (p.batch <= kSorted) {
+      for (int b = lane; b < p.batch; b += 32) {
+        const PagedSeq s = paged_mine(p, paged_seq(p, b));
+        const long long k = (long long)s.kv_len << 32 | (unsigned)(p.batch - b);
+        if (s.q_len > 0 && k < key && k > best) best = k;
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o /= 2) {
+        const long long other = __shfl_xor_sync(0xffffffffu, best, o);
+        best = other > best ? other : best;
+      }
+      w.b = p.batch - (int)(best & 0xffffffff);
+    } else {
+      for (int b0 = key == LLONG_MAX ? 0 : w.b + 1; b0 < p.batch && best < 0; b0 += 32) {
+        const int b = b0 + lane;
+        const uint32_t live =
+            __ballot_sync(0xffffffffu, b < p.batch && paged_mine(p, paged_seq(p, b)).q_len > 0);
+        if (live) {
+          w.b = b0 + __ffs(live) - 1;
+          best = 0;
+        }
+      }
     }
+    if (best < 0) return false;
+    key = best;
+    w.s = paged_mine(p, paged_seq(p, w.b));
+    blocks = (w.s.q_len + p.tokens - 1) / p.tokens;
+    return true;
+  }
+  __device__ __forceinline__ void take(const PagedParams& p, int lane) {
+    int t = 0x7fffffff;  // a counter the address check rejects hands out none
+    if (lane == 0 && SDPA_ADDR_OK(p.chk, p.tickets, 4)) t = atomicAdd(p.tickets, 1);
+    t = __shfl_sync(0xffffffffu, t, 0);
+    const int block = t / p.units_per_block;
+    while (block >= done + blocks) {
+      done += blocks;
+      blocks = 0;
+      more = advance(p, lane);
+      if (!more) return;
+    }
+    w.unit = t - block * p.units_per_block;
+    w.i0 = (blocks - 1 - (block - done)) * p.tokens;
+    w.span = paged_span(p, w.s, w.i0, w.i1(p));
+    w.at = 0;
+    w.j0 = 0;
+    w.j1 = w.span.tiles;
   }
   // Worker `me` of `workers`; x: its place in the scan.
   __device__ __forceinline__ void start(const PagedParams& p, const PagedScan* sc, int x, int me, int workers, int lane) {
     u0 = 0;
-    tickets = blocks = 0;
+    key = LLONG_MAX;
+    blocks = done = 0;
     more = me < workers;
     if (!more) return;
     if (p.split) {
@@ -352,8 +391,6 @@ struct PagedFeed {
       PagedCut* cut = p.cuts + me;
       if (lane == 0 && SDPA_ADDR_OK(p.chk, cut, sizeof(PagedCut))) *cut = w.cut(p);
     } else {
-      blocks = (p.max_q + p.tokens - 1) / p.tokens;
-      tickets = blocks * p.batch * p.units_per_block;
       take(p, lane);
     }
   }

@@ -292,6 +292,18 @@ def test_items_enough_for_the_ticket_order(d):
     check(c, *call(c, window=200), window=200)
 
 
+@pytest.mark.parametrize("d", [128, 192])
+@pytest.mark.parametrize("n", [3, 128, 129, 200])
+def test_ticket_order_of_many_sequences(d, n):
+    """Sorted by their keys up to 128 sequences, in their own order above; equal lengths and empty ones among them."""
+    rng = np.random.default_rng(n)
+    new = rng.integers(0, 60, n)
+    new[:2] = 59
+    total = np.maximum(new, rng.integers(0, 4, n) * 70 + 5)
+    c = case(new.tolist(), total.tolist(), hq=8, hkv=4, d=d, page=16, pad=2)
+    check(c, *call(c))
+
+
 def test_a_large_batch():
     rng = np.random.default_rng(5)
     total = rng.integers(1, 200, 700)
