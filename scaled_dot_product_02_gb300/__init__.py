@@ -16,6 +16,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 import threading
 
@@ -501,7 +502,12 @@ def sdpa_merge(o_parts, lse_parts, *, out=None, lse=None, stream=None):
     return out, lse
 
 # ---------------------------------------------------------------- norms, rotation, paged cache
-_torch_state = {}  # what the calls below take from torch, looked up once
+# The checks below depend on the tensors' metadata alone, so they are made once
+# per combination of it (_meta is the key) and kept, with the problem struct that
+# they lead to: a decoding step repeats its calls with the same shapes, and the
+# checks took longer than the kernels. Nothing is kept by address or contents.
+_torch_state = {}  # what the calls take from torch, looked up once
+_PLANS = 512       # combinations kept per entry point
 
 
 def _torch():
@@ -509,15 +515,20 @@ def _torch():
         import torch
 
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        _torch_state.update(torch=torch, codes={torch.bfloat16: 0, torch.float16: 1}, f32=torch.float32, i32=torch.int32,
+        like = functools.partial(torch.empty_like, memory_format=torch.contiguous_format)  # quicker than new_empty
+        _torch_state.update(torch=torch, like=like, codes={torch.bfloat16: 0, torch.float16: 1}, f32=torch.float32, i32=torch.int32,
                             raw=raw or (lambda index: torch.cuda.current_stream(index).cuda_stream))
     return _torch_state
 
 
-def _dtype_code(t, name):
-    code = _torch()["codes"].get(t.dtype)
+def _meta(t):
+    return None if t is None else (t.shape, t.stride(), t.dtype, t.device)
+
+
+def _dtype_code(dtype, name):
+    code = _torch()["codes"].get(dtype)
     if code is None:
-        raise ValueError(f"{name} must be bfloat16 or float16, got {t.dtype}")
+        raise ValueError(f"{name} must be bfloat16 or float16, got {dtype}")
     return code
 
 
@@ -552,17 +563,29 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
-def _rows_of_heads(name, t, like=None):
+def _contiguous(shape, st):
+    step = 1
+    for n, s in zip(reversed(shape), reversed(st)):
+        if n != 1 and s != step:
+            return 0 in shape
+        step *= n
+    return True
+
+
+def _expect(name, meta, shape, dtype, device):
+    got, st, got_dtype, got_device = meta
+    if got_dtype is not dtype or got_device != device or tuple(got) != tuple(shape) or not _contiguous(got, st):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, got "
+                         f"{got_dtype} {tuple(got)} on {got_device}")
+
+
+def _rows_of_heads(name, meta, like=None):
     """(rows, heads, head_dim, elements between rows) of [..., H, D] whose
     leading dimensions are one evenly spaced row index (contiguous, or a slice
     of a fused projection's output) and whose heads are contiguous."""
-    if like is not None and (t.dtype is not like.dtype or t.device != like.device):
-        raise ValueError(f"{name} must have dtype {like.dtype} on {like.device}, got {t.dtype} on {t.device}")
-    shape, st = t.shape, t.stride()
-    if len(shape) == 3:
-        rows, h, d = shape
-        if st[2] == 1 and (st[1] == d or h == 1):
-            return rows, h, d, st[0] if rows > 1 else h * d
+    shape, st, dtype, device = meta
+    if like is not None and (dtype is not like[2] or device != like[3]):
+        raise ValueError(f"{name} must have dtype {like[2]} on {like[3]}, got {dtype} on {device}")
     if len(shape) < 3:
         raise ValueError(f"{name} must have at least 3 dimensions [..., heads, head_dim], got {tuple(shape)}")
     h, d = shape[-2], shape[-1]
@@ -580,38 +603,54 @@ def _rows_of_heads(name, t, like=None):
     return rows, h, d, step if step and rows else h * d
 
 
-def _expect(name, t, shape, dtype, device):
-    if t.dtype is not dtype or t.device != device or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, got "
-                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
-
-
 def _rotation(q, d, rows, q_weight, k_weight, cos_sin, positions, needs_positions):
     """(max_positions, rotary_dim) of the table; checks the weights, the table and the positions."""
-    dtype, dev, T = q.dtype, q.device, _torch()
+    _, _, dtype, dev = q
     _expect("q_weight", q_weight, (d,), dtype, dev)
     _expect("k_weight", k_weight, (d,), dtype, dev)
     if cos_sin is None:
         return 0, 0
-    if cos_sin.dtype is not T["f32"] or cos_sin.dim() != 2 or cos_sin.device != dev or not cos_sin.is_contiguous():
-        raise ValueError(f"cos_sin must be a contiguous float32 [positions, rotary_dim] tensor on {dev}")
+    shape = cos_sin[0]
+    if len(shape) != 2:
+        raise ValueError(f"cos_sin must be [positions, rotary_dim], got {tuple(shape)}")
+    _expect("cos_sin", cos_sin, shape, _torch()["f32"], dev)
     if positions is not None:
-        if positions.dtype is not T["i32"] or positions.numel() != rows or positions.device != dev or \
-                not positions.is_contiguous():
-            raise ValueError(f"positions must be a contiguous int32 tensor of one entry per token ({rows}) on {dev}")
-    elif needs_positions and cos_sin.shape[1]:
+        n = 1
+        for x in positions[0]:
+            n *= x
+        if n != rows:
+            raise ValueError(f"positions must have one entry per token ({rows}), got {tuple(positions[0])}")
+        _expect("positions", positions, positions[0], _torch()["i32"], dev)
+    elif needs_positions and shape[1]:
         raise ValueError("a rotation needs the tokens' positions")
-    return cos_sin.shape
+    return shape
 
 
-def _norm_rope_problem(q, k, q_weight, k_weight, cos_sin, positions, eps, interleaved, dq_stride=0, dk_stride=0):
+@functools.lru_cache(maxsize=_PLANS)
+def _norm_rope_plan(q, k, q_weight, k_weight, cos_sin, positions, q_out, k_out, dq, dk, dq_out, dk_out, dq_weight,
+                    dk_weight, eps, interleaved):
+    """The struct of a norm + rotation call and its gradient's workspace size, from the tensors' metadata (an
+    output that is None is allocated by the caller)."""
     rows, hq, d, qs = _rows_of_heads("q", q)
-    rows_k, hkv, dk, ks = _rows_of_heads("k", k, q)
-    if dk != d or rows_k != rows or (q.dim() > 3 and q.shape[:-2] != k.shape[:-2]) or q.dim() != k.dim():
-        raise ValueError(f"q and k must agree on every dimension but the heads, got {tuple(q.shape)} and {tuple(k.shape)}")
+    _, hkv, d_k, ks = _rows_of_heads("k", k, q)
+    if d_k != d or q[0][:-2] != k[0][:-2]:
+        raise ValueError(f"q and k must agree on every dimension but the heads, got {tuple(q[0])} and {tuple(k[0])}")
     max_pos, rot = _rotation(q, d, rows, q_weight, k_weight, cos_sin, positions, True)
-    return NormRopeProblem(_dtype_code(q, "q"), hq, hkv, d, rot, 1 if interleaved else 0, eps, max_pos, rows, qs, ks,
-                           dq_stride, dk_stride)
+    _, _, dtype, dev = q
+    for name, t, like in (("q_out", q_out, q), ("k_out", k_out, k), ("dq_out", dq_out, q), ("dk_out", dk_out, k)):
+        if t is not None:
+            _expect(name, t, like[0], dtype, dev)
+    strides = []
+    for name, t, like in (("dq", dq, q), ("dk", dk, k)):
+        if t is not None and t[0] != like[0]:
+            raise ValueError(f"{name} must have shape {tuple(like[0])}, got {tuple(t[0])}")
+        strides.append(0 if t is None else _rows_of_heads(name, t, q)[3])
+    for name, t in (("dq_weight", dq_weight), ("dk_weight", dk_weight)):
+        if t is not None:
+            _expect(name, t, (d,), _torch()["f32"], dev)
+    p = NormRopeProblem(_dtype_code(dtype, "q"), hq, hkv, d, rot, 1 if interleaved else 0, eps, max_pos, rows, qs, ks,
+                        *strides)
+    return p, int(lib().sdpa_qk_norm_rope_bwd_workspace_size(ctypes.byref(p)))
 
 
 def sdpa_qk_norm_rope(q, k, q_weight, k_weight, cos_sin=None, positions=None, *, eps=1e-6, interleaved=False, q_out=None,
@@ -623,18 +662,15 @@ def sdpa_qk_norm_rope(q, k, q_weight, k_weight, cos_sin=None, positions=None, *,
     cos_sin: float32 [positions, rotary_dim], half cosines and half sines, or
     None for the norm alone; positions: int32, one per token. Returns
     contiguous (q_out, k_out)."""
-    p = _norm_rope_problem(q, k, q_weight, k_weight, cos_sin, positions, eps, interleaved)
+    p, _ = _norm_rope_plan(_meta(q), _meta(k), _meta(q_weight), _meta(k_weight), _meta(cos_sin), _meta(positions),
+                           _meta(q_out), _meta(k_out), None, None, None, None, None, None, eps, interleaved)
     _refuse_cpu(q)
-    dev = q.device
+    like = _torch_state["like"]
     if q_out is None:
-        q_out = q.new_empty(q.shape)
-    else:
-        _expect("q_out", q_out, q.shape, q.dtype, dev)
+        q_out = like(q)
     if k_out is None:
-        k_out = q.new_empty(k.shape)
-    else:
-        _expect("k_out", k_out, k.shape, q.dtype, dev)
-    _launch("sdpa_qk_norm_rope", dev, stream, ctypes.byref(p), q.data_ptr(), k.data_ptr(), q_weight.data_ptr(),
+        k_out = like(k)
+    _launch("sdpa_qk_norm_rope", q.device, stream, ctypes.byref(p), q.data_ptr(), k.data_ptr(), q_weight.data_ptr(),
             k_weight.data_ptr(), _addr(cos_sin), _addr(positions), q_out.data_ptr(), k_out.data_ptr())
     return q_out, k_out
 
@@ -646,29 +682,17 @@ def sdpa_qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, cos_sin=None
     outputs and its inputs, returns (dq, dk, dq_weight, dk_weight), the weights'
     in float32. dq and dk may be slices of one fused gradient's rows. Bitwise
     reproducible."""
-    strides = []
-    for name, t, like in (("dq", dq, q), ("dk", dk, k)):
-        if t is not None and t.shape != like.shape:
-            raise ValueError(f"{name} must have shape {tuple(like.shape)}, got {tuple(t.shape)}")
-        strides.append(0 if t is None else _rows_of_heads(name, t, q)[3])
-    p = _norm_rope_problem(q, k, q_weight, k_weight, cos_sin, positions, eps, interleaved, *strides)
+    p, need = _norm_rope_plan(_meta(q), _meta(k), _meta(q_weight), _meta(k_weight), _meta(cos_sin), _meta(positions),
+                              None, None, _meta(dq), _meta(dk), _meta(dq_out), _meta(dk_out), _meta(dq_weight),
+                              _meta(dk_weight), eps, interleaved)
     _refuse_cpu(q)
-    dtype, dev, f32 = q.dtype, q.device, _torch()["f32"]
-    _expect("dq_out", dq_out, q.shape, dtype, dev)
-    _expect("dk_out", dk_out, k.shape, dtype, dev)
-    dq = q.new_empty(q.shape) if dq is None else dq
-    dk = q.new_empty(k.shape) if dk is None else dk
-    d = p.head_dim
-    if dq_weight is None:
-        dq_weight = q.new_empty(d, dtype=f32)
-    else:
-        _expect("dq_weight", dq_weight, (d,), f32, dev)
-    if dk_weight is None:
-        dk_weight = q.new_empty(d, dtype=f32)
-    else:
-        _expect("dk_weight", dk_weight, (d,), f32, dev)
+    dev, f32 = q.device, _torch_state["f32"]
+    like = _torch_state["like"]
+    dq = like(q) if dq is None else dq
+    dk = like(k) if dk is None else dk
+    dq_weight = like(q_weight, dtype=f32) if dq_weight is None else dq_weight
+    dk_weight = like(q_weight, dtype=f32) if dk_weight is None else dk_weight
     if workspace is None:
-        need = int(lib().sdpa_qk_norm_rope_bwd_workspace_size(ctypes.byref(p)))
         workspace = dq_weight.new_empty(max(need // 4, 4))
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {dev}")
@@ -684,33 +708,83 @@ CACHE_LAYOUTS = ("nhd", "hnd")  # [pages, page_size, Hkv, D] and [pages, Hkv, pa
 def _paged_problem(q, hq, k_cache, v_cache, block_table, kv_lens, cu_seqlens_q, cache_layout, total_q, seqlen_q, seqlen_kv,
                    mask_type, window_left, scale, q_stride, k_stride, v_stride) -> PagedProblem:
     """sdpa_paged_problem of a batch over a cache, checked from the tensors'
-    metadata (no device access). Cache strides are free but for contiguous
-    head_dim, so a cache may be a slice of a larger tensor."""
+    metadata. Cache strides are free but for contiguous head_dim, so a cache
+    may be a slice of a larger tensor."""
     if cache_layout not in CACHE_LAYOUTS:
         raise ValueError(f"cache_layout must be one of {CACHE_LAYOUTS}, got {cache_layout!r}")
-    dtype, dev, i32 = q.dtype, q.device, _torch()["i32"]
-    ks, vs, k_st, v_st = k_cache.shape, v_cache.shape, k_cache.stride(), v_cache.stride()
-    for name, t, st in (("k_cache", k_cache, k_st), ("v_cache", v_cache, v_st)):
-        if len(st) != 4 or t.dtype is not dtype or t.device != dev or st[3] != 1:
+    _, _, dtype, dev = q
+    i32 = _torch()["i32"]
+    for name, (shape, st, got, got_dev) in (("k_cache", k_cache), ("v_cache", v_cache)):
+        if len(shape) != 4 or got is not dtype or got_dev != dev or st[3] != 1:
             raise ValueError(f"{name} must be a 4-dimensional {dtype} tensor on {dev} with contiguous head_dim, got "
-                             f"{t.dtype} {tuple(t.shape)} on {t.device}")
-    pages, a, b, d = ks
-    if vs[0] != pages or vs[1] != a or vs[2] != b:
+                             f"{got} {tuple(shape)} on {got_dev}")
+    (ks, k_st), (vs, v_st) = k_cache[:2], v_cache[:2]
+    if ks[:3] != vs[:3]:
         raise ValueError(f"k_cache and v_cache must agree on every dimension but the last, got {tuple(ks)} and {tuple(vs)}")
-    tab, tab_st = block_table.shape, block_table.stride()
-    if len(tab) != 2 or block_table.dtype is not i32 or block_table.device != dev or (tab[1] > 1 and tab_st[1] != 1):
+    tab, tab_st, tab_dtype, tab_dev = block_table
+    if len(tab) != 2 or tab_dtype is not i32 or tab_dev != dev or (tab[1] > 1 and tab_st[1] != 1):
         raise ValueError(f"block_table must be a 2-D int32 [batch, pages] tensor on {dev} with contiguous rows")
     batch, max_pages = tab
     _expect("kv_lens", kv_lens, (batch,), i32, dev)
     _expect("cu_seqlens_q", cu_seqlens_q, (batch + 1,), i32, dev)
     slot, head = (1, 2) if cache_layout == "nhd" else (2, 1)
-    hkv, dv = ks[head], vs[3]
+    pages, hkv, d, dv = ks[0], ks[head], ks[3], vs[3]
     # a dimension of one entry may carry any stride: its own row's width stands for it
-    return PagedProblem(_dtype_code(q, "q"), batch, hq, hkv, d, dv, total_q, seqlen_q,
+    return PagedProblem(_dtype_code(dtype, "q"), batch, hq, hkv, d, dv, total_q, seqlen_q,
                         max_pages * ks[slot] if seqlen_kv is None else seqlen_kv, ks[slot], pages, max_pages, mask_type,
                         window_left, scale, tab_st[0] if batch > 1 else 0, k_st[0] if pages > 1 else d, k_st[slot],
                         k_st[head] if hkv > 1 else d, v_st[0] if pages > 1 else dv, v_st[slot],
                         v_st[head] if hkv > 1 else dv, q_stride, k_stride, v_stride)
+
+
+@functools.lru_cache(maxsize=_PLANS)
+def _append_plan(k, v, k_cache, v_cache, block_table, kv_lens, cu_seqlens_q, cache_layout, q, q_weight, k_weight, cos_sin,
+                 positions, q_out, eps, interleaved):
+    """The structs of an append (the second None without q)."""
+    rows, hkv, d, ks = _rows_of_heads("k", k)
+    rows_v, hkv_v, dv, vs = _rows_of_heads("v", v, k)
+    if len(k[0]) != 3 or len(v[0]) != 3 or rows != rows_v or hkv != hkv_v:
+        raise ValueError(f"k and v must be [tokens, heads, width] of the same tokens and heads, got {tuple(k[0])} and "
+                         f"{tuple(v[0])}")
+    hq, qs, n = hkv, 0, None
+    if q is not None:
+        rows_q, hq, d_q, qs = _rows_of_heads("q", q, k)
+        if len(q[0]) != 3 or rows_q != rows or d_q != d:
+            raise ValueError(f"q must be [tokens, heads, head_dim] of k's tokens and head_dim, got {tuple(q[0])}")
+        if q_weight is None or k_weight is None:
+            raise ValueError("q needs q_weight and k_weight")
+        max_pos, rot = _rotation(q, d, rows, q_weight, k_weight, cos_sin, positions, False)
+        n = NormRopeProblem(0, 0, 0, 0, rot, 1 if interleaved else 0, eps, max_pos)
+        if q_out is not None:
+            _expect("q_out", q_out, q[0], q[2], q[3])
+    elif not (q_weight is k_weight is cos_sin is positions is q_out is None):
+        raise ValueError("weights, cos_sin, positions and q_out go with q")
+    p = _paged_problem(k, hq, k_cache, v_cache, block_table, kv_lens, cu_seqlens_q, cache_layout, rows, 0, 0,
+                       MASKS["none"], -1, 0.0, qs, ks, vs)
+    if p.num_heads_kv != hkv or p.head_dim != d or p.head_dim_v != dv:
+        raise ValueError(f"k and v {tuple(k[0])}, {tuple(v[0])} do not fit the caches {tuple(k_cache[0])}, "
+                         f"{tuple(v_cache[0])} in layout {cache_layout}")
+    return p, n
+
+
+@functools.lru_cache(maxsize=_PLANS)
+def _paged_plan(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens_q, max_seqlen_q, max_seqlen_kv, cache_layout, mask,
+                window_left, window_right, scale, out, lse):
+    """The struct of an attention call over a cache, and its workspace size."""
+    rows, hq, d, qs = _rows_of_heads("q", q)
+    if len(q[0]) != 3:
+        raise ValueError(f"q must be [tokens, heads, head_dim], got {tuple(q[0])}")
+    if window_right not in (-1, 0):
+        raise ValueError(f"a paged window is (left, -1 or 0), got ({window_left}, {window_right})")
+    p = _paged_problem(q, hq, k_cache, v_cache, block_table, kv_lens, cu_seqlens_q, cache_layout, rows, max_seqlen_q,
+                       max_seqlen_kv, MASKS[mask], window_left, d ** -0.5 if scale is None else scale, qs, 0, 0)
+    if p.head_dim != d or hq % p.num_heads_kv:
+        raise ValueError(f"q {tuple(q[0])} does not fit the cache {tuple(k_cache[0])} in layout {cache_layout}")
+    if out is not None:
+        _expect("out", out, (rows, hq, p.head_dim_v), q[2], q[3])
+    if lse is not None:
+        _expect("lse", lse, (rows, hq), _torch()["f32"], q[3])
+    return p, sdpa_paged_fwd_workspace_size(p)
 
 
 def sdpa_check_paged(p: PagedProblem) -> int:
@@ -726,37 +800,15 @@ def sdpa_paged_append(k, v, k_cache, v_cache, block_table, kv_lens, cu_seqlens_q
     normed and rotated on its way into the cache and q into q_out, as by
     sdpa_qk_norm_rope; positions default to the cache positions. Returns q_out
     (None without q). k, v and q may be slices of one projection's output."""
-    rows, hkv, d, ks = _rows_of_heads("k", k)
-    rows_v, hkv_v, dv, vs = _rows_of_heads("v", v, k)
-    if k.dim() != 3 or v.dim() != 3 or rows != rows_v or hkv != hkv_v:
-        raise ValueError(f"k and v must be [tokens, heads, width] of the same tokens and heads, got {tuple(k.shape)} and "
-                         f"{tuple(v.shape)}")
-    hq, qs, n = hkv, 0, None
-    if q is not None:
-        rows_q, hq, d_q, qs = _rows_of_heads("q", q, k)
-        if q.dim() != 3 or rows_q != rows or d_q != d:
-            raise ValueError(f"q must be [tokens, heads, head_dim] of k's tokens and head_dim, got {tuple(q.shape)}")
-        if q_weight is None or k_weight is None:
-            raise ValueError("q needs q_weight and k_weight")
-        max_pos, rot = _rotation(q, d, rows, q_weight, k_weight, cos_sin, positions, False)
-        n = ctypes.byref(NormRopeProblem(0, 0, 0, 0, rot, 1 if interleaved else 0, eps, max_pos))
-    elif not (q_weight is k_weight is cos_sin is positions is q_out is None):
-        raise ValueError("weights, cos_sin, positions and q_out go with q")
-    p = _paged_problem(k, hq, k_cache, v_cache, block_table, kv_lens, cu_seqlens_q, cache_layout, rows, 0, 0,
-                       MASKS["none"], -1, 0.0, qs, ks, vs)
-    if p.num_heads_kv != hkv or p.head_dim != d or p.head_dim_v != dv:
-        raise ValueError(f"k and v {tuple(k.shape)}, {tuple(v.shape)} do not fit the caches {tuple(k_cache.shape)}, "
-                         f"{tuple(v_cache.shape)} in layout {cache_layout}")
+    p, n = _append_plan(_meta(k), _meta(v), _meta(k_cache), _meta(v_cache), _meta(block_table), _meta(kv_lens),
+                        _meta(cu_seqlens_q), cache_layout, _meta(q), _meta(q_weight), _meta(k_weight), _meta(cos_sin),
+                        _meta(positions), _meta(q_out), eps, interleaved)
     _refuse_cpu(k)
-    dev = k.device
-    if q is not None:
-        if q_out is None:
-            q_out = q.new_empty(q.shape)
-        else:
-            _expect("q_out", q_out, q.shape, q.dtype, dev)
-    _launch("sdpa_paged_append", dev, stream, ctypes.byref(p), n, _addr(q), k.data_ptr(), v.data_ptr(), _addr(q_weight),
-            _addr(k_weight), _addr(cos_sin), _addr(positions), _addr(q_out), k_cache.data_ptr(), v_cache.data_ptr(),
-            cu_seqlens_q.data_ptr(), kv_lens.data_ptr(), block_table.data_ptr())
+    if q is not None and q_out is None:
+        q_out = _torch_state["like"](q)
+    _launch("sdpa_paged_append", k.device, stream, ctypes.byref(p), None if n is None else ctypes.byref(n), _addr(q),
+            k.data_ptr(), v.data_ptr(), _addr(q_weight), _addr(k_weight), _addr(cos_sin), _addr(positions), _addr(q_out),
+            k_cache.data_ptr(), v_cache.data_ptr(), cu_seqlens_q.data_ptr(), kv_lens.data_ptr(), block_table.data_ptr())
     return q_out
 
 
@@ -777,27 +829,17 @@ def sdpa_paged_fwd(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens_q, *, m
     or "none"; window = (left, -1 or 0). Returns (o [T, Hq, Dv], lse float32
     [T, Hq]); rows behind the last sequence are left as they are. A workspace
     of PAGED_WORKSPACE_MAX bytes serves every shape."""
-    rows, hq, d, qs = _rows_of_heads("q", q)
-    if q.dim() != 3:
-        raise ValueError(f"q must be [tokens, heads, head_dim], got {tuple(q.shape)}")
-    if window[1] not in (-1, 0):
-        raise ValueError(f"a paged window is (left, -1 or 0), got {tuple(window)}")
-    p = _paged_problem(q, hq, k_cache, v_cache, block_table, kv_lens, cu_seqlens_q, cache_layout, rows, max_seqlen_q,
-                       max_seqlen_kv, MASKS[mask], window[0], d ** -0.5 if scale is None else scale, qs, 0, 0)
-    if p.head_dim != d or hq % p.num_heads_kv:
-        raise ValueError(f"q {tuple(q.shape)} does not fit the cache {tuple(k_cache.shape)} in layout {cache_layout}")
+    p, need = _paged_plan(_meta(q), _meta(k_cache), _meta(v_cache), _meta(block_table), _meta(kv_lens),
+                          _meta(cu_seqlens_q), max_seqlen_q, max_seqlen_kv, cache_layout, mask, window[0], window[1], scale,
+                          _meta(out), _meta(lse))
     _refuse_cpu(q)
-    dev, dv, f32 = q.device, p.head_dim_v, _torch()["f32"]
+    dev = q.device
     if out is None:
-        out = q.new_empty((rows, hq, dv))
-    else:
-        _expect("out", out, (rows, hq, dv), q.dtype, dev)
+        out = q.new_empty((p.total_q, p.num_heads_q, p.head_dim_v))
     if lse is None:
-        lse = q.new_empty((rows, hq), dtype=f32)
-    else:
-        _expect("lse", lse, (rows, hq), f32, dev)
+        lse = q.new_empty((p.total_q, p.num_heads_q), dtype=_torch_state["f32"])
     if workspace is None:
-        workspace = lse.new_empty(max(sdpa_paged_fwd_workspace_size(p) // 4, 64))
+        workspace = lse.new_empty(max(need // 4, 64))
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {dev}")
     _launch("sdpa_paged_fwd", dev, stream, ctypes.byref(p), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),

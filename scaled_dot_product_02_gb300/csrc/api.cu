@@ -498,7 +498,10 @@ PagedPlan paged_plan(const sdpa_paged_problem* p) {
   const int most = dv == 512 ? 32 : 64;  // rows of the rows kernel: a 64-row Q of 512 columns leaves the ring too few stages
   const int few = std::max(1, most / group);
   pl.rows.used = pl.chunk.used = false;
-  pl.small_q = p->seqlen_q <= few ? p->seqlen_q : p->batch == 1 ? -1 : few;  // one sequence: one launch
+  // where the rows add up to seqlen_q for every sequence there is none for the rows kernel, whose launch and join cost
+  // some 10 us even so; the chunk kernel serves a shorter sequence as well, only less well
+  const bool uniform = p->total_q >= (long long)p->batch * p->seqlen_q;
+  pl.small_q = p->seqlen_q <= few ? p->seqlen_q : uniform ? -1 : few;
   if (pl.small_q >= 0) {
     const int max_q = std::min(p->seqlen_q, pl.small_q);
     const long long rows = (long long)group * std::max(max_q, 1);
@@ -1280,8 +1283,9 @@ int sdpa_paged_fwd(const sdpa_paged_problem* p, const void* q, const void* k_cac
   AddrTable* chk = bind_extents({outs[0], outs[1], outs[2], ins[0], ins[1], ins[2], ins[3], ins[4], ins[5]}, err, s);
   if (kAddrCheck && !chk) return SDPA_ERR_CUDA;
   int launches = 0;
-  // the chunk kernel first: the rows kernel is launched while it runs and fills its tail
-  for (const PagedCutting* c : {&pl.chunk, &pl.rows}) {
+  if (pl.chunk.used && !pl.chunk.split && cudaMemsetAsync(ws + 128, 0, sizeof(int), s) != cudaSuccess) return SDPA_ERR_CUDA;
+  // the chunk kernel starts while the rows kernel and its join still run: each SM turns to it as it gets free
+  for (const PagedCutting* c : {&pl.rows, &pl.chunk}) {
     if (!c->used) continue;
     const bool small = c == &pl.rows;
     PagedLaunch L;
@@ -1317,7 +1321,7 @@ int sdpa_paged_fwd(const sdpa_paged_problem* p, const void* q, const void* k_cac
     P.table_stride = ts;
     P.o = o;
     P.lse = lse;
-    P.behind = small && pl.chunk.used;
+    P.behind = !small && pl.rows.used;
     P.total_tiles = reinterpret_cast<long long*>(ws + (small ? 0 : 64));
     P.tickets = reinterpret_cast<int*>(ws + 128);
     P.cuts = reinterpret_cast<PagedCut*>(ws + pl.cuts_off[small ? 0 : 1]);

@@ -27,6 +27,25 @@ int launch_in_grids(long long total, F&& fn) {
   return 0;
 }
 
+// Launch a kernel; early = true lets it start while the kernel before it in the
+// stream still runs (once all of that one's CTAs have allowed it or ended). It
+// may not touch what that kernel writes before griddepcontrol.wait, and must
+// execute that wait before it ends, so that its own end implies the other's.
+template <class... P, class... A>
+int launch_early(void (*kern)(P...), dim3 grid, int threads, int smem, cudaStream_t s, bool early, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = early ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, P(args)...) == cudaSuccess ? SDPA_OK : SDPA_ERR_CUDA;
+}
+
 // Raise a kernel's dynamic shared-memory limit to `bytes` and, when
 // carveout >= 0, set its preferred shared-memory carveout (percent), once per
 // (kernel, current device): function attributes belong to each device's
@@ -249,7 +268,7 @@ struct PagedParams {
   int units_per_block;         // items of one block of tokens: kv heads x head_blocks x dv_splits
   int small_q, small;          // this launch serves the sequences of at most small_q tokens (small), or the others
   int split;                   // items may be split over workers
-  int behind;                  // rows kernel: launched behind the chunk kernel of the same call, to fill its tail
+  int behind;                  // started while the rows kernel of the same call (and its join) still run
   int q_box_rows;              // rows the Q copy brings: tokens x block_heads
   int causal, window;          // window < 0: none
   float scale_log2;

@@ -776,20 +776,11 @@ int launch_bwd_t(NormRopeBwdParams p, cudaStream_t s) {
   const int bytes = std::max(kBwdWarps * p.stages * p.stage_bytes, kBwdWarps * D * 4);
   kern<<<(unsigned)p.blocks, kBwdWarps * 32, bytes, s>>>(p);
   if (cudaGetLastError() != cudaSuccess) return SDPA_ERR_CUDA;
-  // launched while the kernel above runs; it waits for it before reading
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2 * D / 16);
-  cfg.blockDim = dim3(512);
-  cfg.stream = s;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, dw_kernel, (const float*)p.part, (p.warps_q + kBwdWarps - 1) / kBwdWarps,
-                            p.warps_q / kBwdWarps + 1, p.blocks + 1, D, p.dwq, p.dwk, p.chk) == cudaSuccess
-             ? SDPA_OK
-             : SDPA_ERR_CUDA;
+  // started while the kernel above runs (with its split of an SM between L1 and shared memory); it waits for it
+  // before reading
+  if (const int rc = set_kernel_smem(reinterpret_cast<const void*>(&dw_kernel), 0, 100)) return rc;
+  return launch_early(dw_kernel, dim3(2 * D / 16), 512, 0, s, true, (const float*)p.part, (p.warps_q + kBwdWarps - 1) / kBwdWarps,
+                      p.warps_q / kBwdWarps + 1, p.blocks + 1, D, p.dwq, p.dwk, p.chk);
 }
 
 }  // namespace

@@ -564,8 +564,6 @@ __global__ void __launch_bounds__(256, 1)
     tc_fence_after();
     tmem_dealloc(tmem, C::TM_COLS);
   }
-  // launched while the chunk kernel of the same call runs, this one ends after it
-  if (p.behind && blockIdx.x == 0 && threadIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // Items that cross cuts: CTA w joins the item that cut w (the start of worker
@@ -584,6 +582,7 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__
   using E = Elem<BF16>;
   using T = typename E::T;
   const int w = blockIdx.x + 1;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // a chunk kernel behind needs nothing of this
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (!SDPA_ADDR_OK(p.chk, p.total_tiles, 8) || !SDPA_ADDR_OK(p.chk, p.cuts + w, sizeof(PagedCut))) return;
   const long long total = *reinterpret_cast<volatile long long*>(p.total_tiles);
@@ -640,16 +639,11 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__
 // Launched while the attention kernel runs; it waits for it before reading.
 template <int DV, int N, bool BF16>
 int launch_join_t(const PagedLaunch& L) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)L.workers - 1, N / kJoinRows);
-  cfg.blockDim = dim3(256);
-  cfg.stream = L.stream;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_join_kernel<DV, N, BF16>, L.p, L.workers) == cudaSuccess ? SDPA_OK : SDPA_ERR_CUDA;
+  auto kern = paged_join_kernel<DV, N, BF16>;
+  // the attention kernels' split of an SM between L1 and shared memory
+  if (const int rc = set_kernel_smem(reinterpret_cast<const void*>(kern), 0, 100)) return rc;
+  return launch_early(kern, dim3((unsigned)L.workers - 1, N / kJoinRows), 256, 0, L.stream, true,
+                      L.p, L.workers);
 }
 
 template <int DQK, int DV, int N, bool BF16>
@@ -657,17 +651,8 @@ int launch_rows_t(const PagedLaunch& L, int* launches) {
   using C = RowsCfg<DQK, DV, N>;
   auto kern = paged_rows_kernel<DQK, DV, N, BF16>;
   if (const int rc = set_kernel_smem(reinterpret_cast<const void*>(kern), C::SMEM, -1)) return rc;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)L.workers);
-  cfg.blockDim = dim3(C::THREADS);
-  cfg.dynamicSmemBytes = C::SMEM;
-  cfg.stream = L.stream;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = L.p.behind ? 1 : 0;
-  if (cudaLaunchKernelEx(&cfg, kern, L.tmQ, L.tmK, L.tmV, L.p) != cudaSuccess) return SDPA_ERR_CUDA;
+  if (const int rc = launch_early(kern, dim3((unsigned)L.workers), C::THREADS, C::SMEM, L.stream, false, L.tmQ, L.tmK, L.tmV, L.p))
+    return rc;
   ++*launches;
   if (L.workers == 1 || !L.p.split) return SDPA_OK;  // no item crosses a cut
   ++*launches;

@@ -549,6 +549,7 @@ __global__ void __launch_bounds__(256, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+  if (p.behind && blockIdx.x == 0 && threadIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 template <int DQK, int DV, bool BF16>
@@ -556,9 +557,9 @@ int launch_chunk_t(const PagedLaunch& L, int* launches) {
   using C = ChunkCfg<DQK, DV>;
   auto kern = paged_chunk_kernel<DQK, DV, BF16>;
   if (const int rc = set_kernel_smem(reinterpret_cast<const void*>(kern), C::SMEM, -1)) return rc;
-  if (!L.p.split && cudaMemsetAsync(L.p.tickets, 0, sizeof(int), L.stream) != cudaSuccess) return SDPA_ERR_CUDA;
-  kern<<<(unsigned)L.workers, C::THREADS, C::SMEM, L.stream>>>(L.tmQ, L.tmK, L.tmV, L.p);
-  if (cudaGetLastError() != cudaSuccess) return SDPA_ERR_CUDA;
+  if (const int rc = launch_early(kern, dim3((unsigned)L.workers), C::THREADS, C::SMEM, L.stream, L.p.behind != 0, L.tmQ,
+                                  L.tmK, L.tmV, L.p))
+    return rc;
   ++*launches;
   if (L.workers == 1 || !L.p.split) return SDPA_OK;  // no item crosses a cut
   ++*launches;

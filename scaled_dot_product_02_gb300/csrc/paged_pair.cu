@@ -514,16 +514,17 @@ __global__ void __launch_bounds__(PairCfg::THREADS, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+  if (p.behind && blockIdx.x == 0 && threadIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 template <bool BF16>
 int launch_pair_t(const PagedLaunch& L, int sms, int* launches) {
   auto kern = paged_pair_kernel<BF16>;
   if (const int rc = set_kernel_smem(reinterpret_cast<const void*>(kern), PairCfg::SMEM, 100)) return rc;
-  if (!L.p.split && cudaMemsetAsync(L.p.tickets, 0, sizeof(int), L.stream) != cudaSuccess) return SDPA_ERR_CUDA;
   const int grid = std::min(L.workers, sms);
-  kern<<<(unsigned)grid, PairCfg::THREADS, PairCfg::SMEM, L.stream>>>(L.tmQ, L.tmK, L.tmV, L.p, L.workers);
-  if (cudaGetLastError() != cudaSuccess) return SDPA_ERR_CUDA;
+  if (const int rc = launch_early(kern, dim3((unsigned)grid), PairCfg::THREADS, PairCfg::SMEM, L.stream, L.p.behind != 0,
+                                  L.tmQ, L.tmK, L.tmV, L.p, L.workers))
+    return rc;
   ++*launches;
   if (L.workers == 1 || !L.p.split) return SDPA_OK;  // no item crosses a cut
   ++*launches;
