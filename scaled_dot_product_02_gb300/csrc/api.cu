@@ -445,7 +445,8 @@ struct PagedCutting {
   int block_heads, head_blocks;  // heads of a group in an item, items a group takes
   int tokens;                    // tokens in an item
   int dv_item, dv_splits;        // value columns an item accumulates, items that share a row
-  bool split;                    // items may be split over workers
+  bool split;                    // rows kernel: items may be split over workers
+  int tail;                      // chunk kernels: shares that the last items are cut into
   int workers;                   // CTAs (at most one per SM); head_dim 128 chunks: pipelines, two a CTA
 };
 struct PagedPlan {
@@ -477,17 +478,20 @@ PagedCutting paged_cutting(const sdpa_paged_problem* p, int n, int max_q, int dv
   if (n <= 64) {
     // short items are not worth the join (and its launch)
     c.split = tiles > 4;
+    c.tail = 0;
   } else {
-    // Whole items by ticket keep the CTAs on the same keys; splitting pays only where items are fewer than
-    // pipelines and so long that a pipeline left idle costs more than the join, some 15 tiles' time. (Items split
-    // in all cases: 2048 tokens over 131072 keys 3290 -> 3750 us, 8 x 1024 over 32768 3110 -> 4400 us, 8 x 100 over
-    // 2000 62 -> 85 us; 2048 over 16384, 1.7 items a pipeline, 413 -> 405 us.)
-    c.split = items < most && tiles * (most - items) > 15LL * most;
-    if (!c.split && (long long)p->batch * ((max_q + c.tokens - 1) / c.tokens) * (items / blocks) > 0x7fff0000LL) c.split = true;
+    // Whole items by ticket keep the CTAs on the same keys (all items split into equal shares: 2048 tokens over
+    // 131072 keys 3290 -> 3750 us, 8 x 1024 over 32768 3110 -> 4400 us). The last, uneven round costs half an item
+    // on average: cut into shares where items are few and long enough to pay for the join (2048 tokens over 16384
+    // keys: D192 643 -> 567 us, D512 1256 -> 1116 us). Not at head_dim 128, where an SM's other pipeline goes on
+    // faster alone and the rest costs as much as it saves (413 -> 421 us).
+    c.split = false;
+    c.tail = p->head_dim != 128 && tiles >= 48 && items < 6 * most ? 2 * most : 0;
   }
-  // a block's length is a 32-bit number in the kernels
-  c.fits = (long long)p->num_heads_kv * c.head_blocks * c.dv_splits * std::max(tiles, 1LL) < (1LL << 31);
-  const long long pieces = c.split && items < most ? items * std::max(tiles, 1LL) : items;
+  // the length of a block and the ticket counter are 32-bit numbers
+  c.fits = (long long)p->num_heads_kv * c.head_blocks * c.dv_splits * std::max(tiles, 1LL) < (1LL << 31) &&
+           items < 0x7fff0000LL;
+  const long long pieces = (c.split || c.tail) && items < most ? items * std::max(tiles, 1LL) : items;
   c.workers = (int)std::max(1LL, std::min<long long>(most, pieces));
   return c;
 }
@@ -512,9 +516,10 @@ PagedPlan paged_plan(const sdpa_paged_problem* p) {
   for (int x = 0; x < 2; ++x) {
     const PagedCutting& c = x ? pl.chunk : pl.rows;
     pl.cuts_off[x] = at;
-    if (c.used) at = round_up(at + (size_t)c.workers * paged_cut_bytes(), 256);
+    const size_t shares = !c.used ? 0 : c.tail ? c.tail : c.split ? c.workers : 0;
+    at = round_up(at + shares * paged_cut_bytes(), 256);
     pl.parts_off[x] = at;
-    if (c.used && c.split) at = round_up(at + (size_t)c.workers * 2 * c.n * (c.dv_item + 2) * 4, 256);
+    at = round_up(at + shares * 2 * c.n * (c.dv_item + 2) * 4, 256);
   }
   pl.total = at;
   return pl;
@@ -1283,7 +1288,8 @@ int sdpa_paged_fwd(const sdpa_paged_problem* p, const void* q, const void* k_cac
   AddrTable* chk = bind_extents({outs[0], outs[1], outs[2], ins[0], ins[1], ins[2], ins[3], ins[4], ins[5]}, err, s);
   if (kAddrCheck && !chk) return SDPA_ERR_CUDA;
   int launches = 0;
-  if (pl.chunk.used && !pl.chunk.split && cudaMemsetAsync(ws + 128, 0, sizeof(int), s) != cudaSuccess) return SDPA_ERR_CUDA;
+  // the chunk kernel's length of the rest (at 64) and ticket counter (at 128)
+  if (pl.chunk.used && cudaMemsetAsync(ws + 64, 0, 68, s) != cudaSuccess) return SDPA_ERR_CUDA;
   // the chunk kernel starts while the rows kernel and its join still run: each SM turns to it as it gets free
   for (const PagedCutting* c : {&pl.rows, &pl.chunk}) {
     if (!c->used) continue;
@@ -1306,6 +1312,7 @@ int sdpa_paged_fwd(const sdpa_paged_problem* p, const void* q, const void* k_cac
     P.small_q = pl.small_q;
     P.small = small;
     P.split = c->split;
+    P.tail = c->tail;
     P.q_box_rows = c->tokens * c->block_heads;
     P.causal = p->mask_type != SDPA_MASK_NONE;
     P.window = p->window_left;

@@ -267,7 +267,8 @@ struct PagedParams {
   int dv, dv_splits;           // width of O rows; parts of it that separate items accumulate
   int units_per_block;         // items of one block of tokens: kv heads x head_blocks x dv_splits
   int small_q, small;          // this launch serves the sequences of at most small_q tokens (small), or the others
-  int split;                   // items may be split over workers
+  int split;                   // rows kernel: items may be split over workers
+  int tail;                    // chunk kernels: shares that the last items are cut into (0: none)
   int behind;                  // started while the rows kernel of the same call (and its join) still run
   int q_box_rows;              // rows the Q copy brings: tokens x block_heads
   int causal, window;          // window < 0: none
@@ -278,10 +279,10 @@ struct PagedParams {
   long long table_stride;
   void* o;
   float* lse;
-  long long* total_tiles;      // workspace: length of all items (0: refused)
-  int* tickets;                // workspace: the next item (chunk kernel without split)
-  PagedCut* cuts;              // [workers]
-  float* parts;                // [workers][2] partial results
+  long long* total_tiles;      // workspace: length of what the shares cut (0: refused, or nothing)
+  int* tickets;                // workspace: the next item or share (chunk kernels)
+  PagedCut* cuts;              // [shares]
+  float* parts;                // [shares][2] partial results
   int* err;
   AddrTable* chk;
 };
@@ -298,8 +299,8 @@ int launch_paged_rows(const PagedLaunch& L, int n, int head_dim, bool bf16, int*
 int launch_paged_chunk(const PagedLaunch& L, int head_dim, bool bf16, int* launches);
 // The same at head_dim 128, two pipelines a CTA (L.workers pipelines on at most sms CTAs).
 int launch_paged_pair(const PagedLaunch& L, int sms, bool bf16, int* launches);
-// Joins the items that cross a cut: n rows of dv values an item.
-int launch_paged_join(const PagedLaunch& L, int n, int dv, bool bf16);
+// Joins the items that cross a cut between `shares` shares: n rows of dv values an item.
+int launch_paged_join(const PagedLaunch& L, int n, int dv, int shares, bool bf16);
 
 // Log-sum-exp merge of partial results over a split of the keys (merge.cu).
 int launch_merge(const void* o_parts, const float* lse_parts, void* o, float* lse, long long items, int head_dim,

@@ -571,11 +571,11 @@ __global__ void __launch_bounds__(256, 1)
 // worker w - 1 (which began it) and the workers whose shares start in it:
 //   m = max m_k,  l = sum l_k 2^(m_k - m),  O = sum O_k 2^(m_k - m) / l.
 // A part holds N rows of DV values, then N maxima and N sums. CTA (w, y) joins
-// rows 8 y to 8 y + 7, each thread four columns of a row with its own copy of the
+// join_rows(N) rows, each thread four columns of a row with its own copy of the
 // row's statistics: after the wait there are two rounds of loads, the cut and the
 // parts. (One CTA per item, statistics first, took 4 us where the parts were
 // small and 29 to 49 us for the 128-row items of chunks.)
-constexpr int kJoinRows = 8;
+constexpr int join_rows(int n) { return n == 128 ? 32 : 8; }
 
 template <int DV, int N, bool BF16>
 __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__ PagedParams p, int grid) {
@@ -589,7 +589,8 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__
   const PagedCut cut = p.cuts[w];  // read with the total; a worker without a share leaves it unset
   const PagedShare share(total, grid);
   if (w >= share.workers || share.at(w) == cut.at || share.at(w - 1) > cut.at) return;
-  const int r0 = blockIdx.y * kJoinRows, rows = min(kJoinRows, cut.tokens * p.block_heads - r0);
+  constexpr int ROWS = join_rows(N);
+  const int r0 = blockIdx.y * ROWS, rows = min(ROWS, cut.tokens * p.block_heads - r0);
   if (rows <= 0) return;
   int parts = 1;  // worker w - 1, then w, w + 1, ...
   while (w - 1 + parts < share.workers && share.at(w - 1 + parts) < cut.at + cut.n) ++parts;
@@ -638,12 +639,11 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__
 
 // Launched while the attention kernel runs; it waits for it before reading.
 template <int DV, int N, bool BF16>
-int launch_join_t(const PagedLaunch& L) {
+int launch_join_t(const PagedLaunch& L, int shares) {
   auto kern = paged_join_kernel<DV, N, BF16>;
-  // the attention kernels' split of an SM between L1 and shared memory
+  // the attention kernels' division of an SM between L1 and shared memory
   if (const int rc = set_kernel_smem(reinterpret_cast<const void*>(kern), 0, 100)) return rc;
-  return launch_early(kern, dim3((unsigned)L.workers - 1, N / kJoinRows), 256, 0, L.stream, true,
-                      L.p, L.workers);
+  return launch_early(kern, dim3((unsigned)shares - 1, N / join_rows(N)), 256, 0, L.stream, true, L.p, shares);
 }
 
 template <int DQK, int DV, int N, bool BF16>
@@ -656,7 +656,7 @@ int launch_rows_t(const PagedLaunch& L, int* launches) {
   ++*launches;
   if (L.workers == 1 || !L.p.split) return SDPA_OK;  // no item crosses a cut
   ++*launches;
-  return launch_join_t<DV, N, BF16>(L);
+  return launch_join_t<DV, N, BF16>(L, L.workers);
 }
 
 template <int DQK, int DV, bool BF16>
@@ -669,8 +669,9 @@ int launch_rows_n(const PagedLaunch& L, int n, int* launches) {
 
 }  // namespace
 
-int launch_paged_join(const PagedLaunch& L, int n, int dv, bool bf16) {
-#define JOIN(A, B) return bf16 ? launch_join_t<A, B, true>(L) : launch_join_t<A, B, false>(L)
+int launch_paged_join(const PagedLaunch& L, int n, int dv, int shares, bool bf16) {
+  if (shares < 2) return SDPA_OK;
+#define JOIN(A, B) return bf16 ? launch_join_t<A, B, true>(L, shares) : launch_join_t<A, B, false>(L, shares)
   if (n == 128 && dv == 128) JOIN(128, 128);
   if (n == 128 && dv == 256) JOIN(256, 128);
 #undef JOIN

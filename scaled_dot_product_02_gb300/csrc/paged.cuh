@@ -310,99 +310,202 @@ __device__ __forceinline__ PagedShares paged_scan(const PagedParams& p, PagedSca
 struct PagedPiece {
   int row0, q_len, kv_len, b, i0, unit;  // row0 < 0: no more
   int j0, j1;                         // its key tiles, counted from the span's first
-  int slot;                           // its partial result, or -1: the whole item
+  int slot;                           // where its partial result goes, or -1: the whole item
 };
 
-// Where a pipeline's pieces come from: its share of the tiles (p.split), or
-// the tickets. The ticket order takes the sequences with the most keys first (up
-// to kSorted of them; a larger batch in its own order), the last blocks of
-// tokens first, and the items of a block together: the longest items start
-// first, and the CTAs at work share the same few sequences' keys. A whole warp
-// walks it.
+// A place in the order that the tickets follow: the sequences with the most
+// keys first (up to kSorted of them; a larger batch in its own order), the last
+// blocks of tokens first, and the items of a block together. So the longest
+// items start first, and the CTAs at work share the same few sequences' keys.
 constexpr int kSorted = 128;
 
-struct PagedFeed {
-  PagedWalk w;
-  bool more;
-  long long u0;
-  long long key;          // of the current sequence in the order: its keys, then its place
-  int blocks, done;       // its blocks of tokens, those of the sequences before it
+struct PagedOrder {
+  long long key;      // of the sequence: its keys, then its place
+  PagedSeq s;
+  int b, blocks, blk;  // the sequence, its blocks of tokens, the current one counted from the last
 
-  // The next sequence of the order with rows; false when there is none.
-  __device__ __forceinline__ bool advance(const PagedParams& p, int lane) {
+  __device__ __forceinline__ void before_all() {
+    key = LLONG_MAX;
+    b = -1;
+    blocks = blk = 0;
+  }
+  __device__ __forceinline__ int first_token(const PagedParams& p, int k) const { return (blocks - 1 - k) * p.tokens; }
+  __device__ __forceinline__ PagedSpan span_of(const PagedParams& p, int k) const {
+    const int i0 = first_token(p, k);
+    return paged_span(p, s, i0, min(i0 + p.tokens, s.q_len) - 1);
+  }
+  // The first block of the next sequence with rows; false when there is none. A whole warp calls it.
+  __device__ __forceinline__ bool next_sequence(const PagedParams& p, int lane) {
     long long best = -1;  // the largest key below the current one
     if (p.batch <= kSorted) {
-      for (int b = lane; b < p.batch; b += 32) {
-        const PagedSeq s = paged_mine(p, paged_seq(p, b));
-        const long long k = (long long)s.kv_len << 32 | (unsigned)(p.batch - b);
-        if (s.q_len > 0 && k < key && k > best) best = k;
+      for (int i = lane; i < p.batch; i += 32) {
+        const PagedSeq x = paged_mine(p, paged_seq(p, i));
+        const long long k = (long long)x.kv_len << 32 | (unsigned)(p.batch - i);
+        if (x.q_len > 0 && k < key && k > best) best = k;
       }
 #pragma unroll
       for (int o = 16; o > 0; o /= 2) {
         const long long other = __shfl_xor_sync(0xffffffffu, best, o);
         best = other > best ? other : best;
       }
-      w.b = p.batch - (int)(best & 0xffffffff);
+      if (best >= 0) b = p.batch - (int)(best & 0xffffffff);
     } else {
-      for (int b0 = key == LLONG_MAX ? 0 : w.b + 1; b0 < p.batch && best < 0; b0 += 32) {
-        const int b = b0 + lane;
+      for (int b0 = b + 1; b0 < p.batch && best < 0; b0 += 32) {
         const uint32_t live =
-            __ballot_sync(0xffffffffu, b < p.batch && paged_mine(p, paged_seq(p, b)).q_len > 0);
+            __ballot_sync(0xffffffffu, b0 + lane < p.batch && paged_mine(p, paged_seq(p, b0 + lane)).q_len > 0);
         if (live) {
-          w.b = b0 + __ffs(live) - 1;
+          b = b0 + __ffs(live) - 1;
           best = 0;
         }
       }
     }
     if (best < 0) return false;
     key = best;
-    w.s = paged_mine(p, paged_seq(p, w.b));
-    blocks = (w.s.q_len + p.tokens - 1) / p.tokens;
+    s = paged_mine(p, paged_seq(p, b));
+    blocks = (s.q_len + p.tokens - 1) / p.tokens;
+    blk = 0;
     return true;
   }
-  __device__ __forceinline__ void take(const PagedParams& p, int lane) {
-    int t = 0x7fffffff;  // a counter the address check rejects hands out none
-    if (lane == 0 && SDPA_ADDR_OK(p.chk, p.tickets, 4)) t = atomicAdd(p.tickets, 1);
-    t = __shfl_sync(0xffffffffu, t, 0);
-    const int block = t / p.units_per_block;
-    while (block >= done + blocks) {
-      done += blocks;
-      blocks = 0;
-      more = advance(p, lane);
-      if (!more) return;
-    }
-    w.unit = t - block * p.units_per_block;
-    w.i0 = (blocks - 1 - (block - done)) * p.tokens;
-    w.span = paged_span(p, w.s, w.i0, w.i1(p));
-    w.at = 0;
-    w.j0 = 0;
-    w.j1 = w.span.tiles;
+};
+
+// Where a pipeline's pieces come from. The tickets hand out whole items, as
+// many as go round all pipelines evenly (all items when p.tail is 0: the items
+// are many, or too short for more); the key tiles of the rest, laid end to end
+// in the same order, are cut into p.tail equal shares and handed out by further
+// tickets, and the items that cross a cut are joined afterwards. A whole warp
+// walks it.
+struct PagedFeed {
+  PagedWalk w;          // the current piece; u .. u_end: of its share
+  bool more;
+  PagedOrder at;        // the block of the last whole item's ticket, or of the current piece of a share
+  int done;             // blocks of the sequences before at's
+  int whole, share;     // whole items handed out; the current share, or -1
+  PagedOrder rest;      // where the rest begins
+  long long rest_at;    // its block's start, counted from the rest's first item
+  long long total;      // length of the rest, -1: not yet added up
+  int asked;            // lane 0: the next ticket, when it has been asked for
+  bool has_asked;
+
+  // Ask for the next ticket, so that it is there when the current item's last copies are out (but no earlier: a
+  // ticket kept behind a long item is work that waits).
+  __device__ __forceinline__ void ask(const PagedParams& p, int lane) {
+    if (has_asked) return;
+    has_asked = true;
+    asked = 0x7fffffff;  // a counter the address check rejects hands out none
+    if (lane == 0 && SDPA_ADDR_OK(p.chk, p.tickets, 4)) asked = atomicAdd(p.tickets, 1);
   }
-  // Worker `me` of `workers`; x: its place in the scan.
-  __device__ __forceinline__ void start(const PagedParams& p, const PagedScan* sc, int x, int me, int workers, int lane) {
-    u0 = 0;
-    key = LLONG_MAX;
-    blocks = done = 0;
-    more = me < workers;
-    if (!more) return;
-    if (p.split) {
-      w = sc->start[x];
-      u0 = w.u;
-      PagedCut* cut = p.cuts + me;
-      if (lane == 0 && SDPA_ADDR_OK(p.chk, cut, sizeof(PagedCut))) *cut = w.cut(p);
+  __device__ __forceinline__ void set_piece(const PagedParams& p) {
+    w.b = at.b;
+    w.s = at.s;
+    w.i0 = at.first_token(p, at.blk);
+    w.span = at.span_of(p, at.blk);
+    w.weight = max(1, w.span.tiles);
+  }
+  // Moves `o`, whose block starts at `start`, to the block that holds position u; false behind the last one, with
+  // start the length of all.
+  __device__ __forceinline__ bool seek(const PagedParams& p, PagedOrder& o, long long& start, long long u, int lane) {
+    while (true) {
+      while (o.blk < o.blocks) {
+        const int k = o.blk + lane;
+        const long long own = k < o.blocks ? (long long)p.units_per_block * max(1, o.span_of(p, k).tiles) : 0;
+        long long upto = own;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const long long y = __shfl_up_sync(0xffffffffu, upto, d);
+          if (lane >= d) upto += y;
+        }
+        const uint32_t past = __ballot_sync(0xffffffffu, u < start + upto);
+        if (past) {
+          const int l = __ffs(past) - 1;
+          start += __shfl_sync(0xffffffffu, upto - own, l);
+          o.blk += l;
+          return true;
+        }
+        start += __shfl_sync(0xffffffffu, upto, 31);
+        o.blk += 32;
+      }
+      if (!o.next_sequence(p, lane)) return false;
+    }
+  }
+  __device__ __forceinline__ void take(const PagedParams& p, int lane) {
+    ask(p, lane);
+    has_asked = false;
+    const int t = __shfl_sync(0xffffffffu, asked, 0);
+    more = false;
+    share = -1;
+    if (t < whole || total < 0) {
+      const int goal = min(t, whole), block = goal / p.units_per_block;  // the rest's first item, once it has begun
+      while (block >= done + at.blocks) {
+        done += at.blocks;
+        at.blocks = 0;
+        if (!at.next_sequence(p, lane)) return;
+      }
+      at.blk = block - done;
+      w.unit = goal - block * p.units_per_block;
+      if (t < whole) {
+        set_piece(p);
+        w.at = 0;
+        w.j0 = 0;
+        w.j1 = w.span.tiles;
+        more = true;
+        return;
+      }
+      if (p.tail == 0) return;
+      rest = at;
+      rest_at = -(long long)w.unit * max(1, at.span_of(p, at.blk).tiles);
+      PagedOrder end = rest;
+      total = rest_at;
+      seek(p, end, total, LLONG_MAX, lane);
+    }
+    const PagedShare cut(total, p.tail);
+    if (t - whole >= cut.workers) return;
+    share = t - whole;
+    w.u = cut.at(share);
+    w.u_end = cut.at(share + 1);
+    at = rest;
+    w.block_at = rest_at;
+    more = seek(p, at, w.block_at, w.u, lane);
+    set_piece(p);
+    locate(p);
+    PagedCut* to = p.cuts + share;
+    if (lane == 0 && SDPA_ADDR_OK(p.chk, to, sizeof(PagedCut))) *to = w.cut(p);
+    if (lane == 0 && SDPA_ADDR_OK(p.chk, p.total_tiles, 8)) *p.total_tiles = total;
+  }
+  // The piece of the share that starts at w.u, in the block at w.block_at.
+  __device__ __forceinline__ void locate(const PagedParams& p) {
+    w.unit = (int)((unsigned)(w.u - w.block_at) / (unsigned)w.weight);
+    w.at = w.block_at + (long long)w.unit * w.weight;
+    w.j0 = (int)(w.u - w.at);
+    w.j1 = min(w.span.tiles, (int)min((long long)w.weight, w.u_end - w.at));
+  }
+  // items: all items of the launch; pipes: the pipelines that share them.
+  __device__ __forceinline__ void start(const PagedParams& p, long long items, int pipes, bool mine, int lane) {
+    at.before_all();
+    done = 0;
+    share = total = -1;
+    whole = p.tail ? (int)(items - items % pipes) : 0x7fffffff;
+    more = has_asked = false;
+    if (mine) take(p, lane);
+  }
+  // Whether the current piece is the last before the next ticket.
+  __device__ __forceinline__ bool last() const { return share < 0 || w.at + w.weight >= w.u_end; }
+  __device__ __forceinline__ void next(const PagedParams& p, int lane) {
+    if (!last()) {
+      w.u = w.at + w.weight;
+      if (w.unit + 1 == p.units_per_block) {
+        w.block_at += (long long)p.units_per_block * w.weight;
+        if (++at.blk >= at.blocks) at.next_sequence(p, lane);  // w.u < w.u_end: there is one
+        set_piece(p);
+      }
+      locate(p);
     } else {
       take(p, lane);
     }
   }
-  __device__ __forceinline__ void next(const PagedParams& p, int lane) {
-    if (p.split)
-      more = w.next(p);
-    else
-      take(p, lane);
-  }
-  __device__ __forceinline__ PagedPiece piece() const {
-    return PagedPiece{more ? w.s.row0 : -1, w.s.q_len, w.s.kv_len, w.b, w.i0, w.unit, w.j0, w.j1,
-                      w.whole() ? -1 : (w.at < u0 ? 0 : 1)};
+  __device__ __forceinline__ PagedPiece piece(const PagedParams& p) const {
+    // at most one item continues from the share before, and one into the next
+    const int slot = share < 0 || w.whole() ? -1 : share * 2 + (w.at < PagedShare(total, p.tail).at(share) ? 0 : 1);
+    return PagedPiece{more ? w.s.row0 : -1, w.s.q_len, w.s.kv_len, w.b, w.i0, w.unit, w.j0, w.j1, slot};
   }
 };
 

@@ -6,10 +6,9 @@
 // its GQA group, so a tile of keys serves the whole group) and, for head_dim
 // 512, one half of the value columns, which keeps O within 256 TMEM columns:
 //   S = Q K^T (M = 128 rows, N = 128 keys),  O += P V (P from TMEM).
-// CTAs take items either from a ticket counter, last (longest) block of tokens
-// first and the heads of a block together, so that the CTAs at work walk the
-// same keys at the same time; or, when the items are few, as equal shares of
-// all key tiles with the crossing items joined afterwards (paged.cu).
+// CTAs take items from a ticket counter, the longest first; where items are few
+// and long, the last ones are cut into equal shares of their key tiles and
+// joined afterwards (PagedFeed in paged.cuh).
 //
 // Roles (256 threads): warp 0 scheduler and TMA producer, warps 2 and 3 further
 // producers (each lane fetches one page's rows; a warp issues its lanes' copies
@@ -48,12 +47,13 @@ struct ChunkCfg {
 // tiles [j0, j1) of an item through the ring, in the order the MMA issuer takes
 // them; c counts the stages. Every producer arrives on each stage, with copies in
 // it or not, or the ring could go on without one and leave it a phase behind.
-// Producer 0 sets the byte count; the others' copies may complete before it.
+// Producer 0 sets the byte count; the others' copies may complete before it. feed:
+// asked for the next ticket with the last tile.
 template <class C>
 __device__ __forceinline__ bool load_tiles(const PagedParams& p, const CUtensorMap& tmK, const CUtensorMap& tmV,
                                            const PagedSpan& span, int b, const PagedUnit& un, int j0, int j1, uint64_t* full,
                                            uint64_t* empty, uint8_t* sStage, int& c, int pw, int lane,
-                                           volatile int* abort_flag) {
+                                           volatile int* abort_flag, PagedFeed* feed = nullptr) {
   const int box = lane * 3 + pw, first = box * p.box_rows;  // this lane's box of a tile, its first key
   const uint32_t box_bytes = p.box_rows * 128;
   auto next_slot = [&](uint32_t bytes) -> int {
@@ -99,6 +99,7 @@ __device__ __forceinline__ bool load_tiles(const PagedParams& p, const CUtensorM
   for (int j = j0; j < j1; ++j) {
     const PagedBox ahead = j + 1 < j1 ? box_of(j + 1) : cur;  // its table entry arrives while this tile's copies go out
     const int key0 = (span.tile0 + j) * kTile;
+    if (feed && j + 1 == j1) feed->ask(p, lane);
     if (!load_k(cur, key0)) return false;
     if (j > j0 && !load_v(prev, key0 - kTile)) return false;
     prev = cur;
@@ -158,16 +159,12 @@ __global__ void __launch_bounds__(256, 1)
   }
   tc_fence_before();
   const int me = blockIdx.x;
-  const PagedShares all = paged_scan<C::THREADS>(p, scan, me, 1, p.split, gridDim.x);
+  const PagedShares all = paged_scan<C::THREADS>(p, scan, me, 1, 0, gridDim.x);
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
-  const int workers = (int)min((long long)gridDim.x, all.total);
-  if (threadIdx.x == 0 && me == 0) {
-    if (SDPA_ADDR_OK(p.chk, p.total_tiles, 8)) *p.total_tiles = all.total;
-    if (!all.fit) record_error(p.err, SDPA_ERR_BAD_SEQLENS);
-  }
+  if (threadIdx.x == 0 && me == 0 && !all.fit) record_error(p.err, SDPA_ERR_BAD_SEQLENS);
 
-  if (me < workers) {
+  if (all.total > 0) {
     if (warp == 0) {
       // ---------------------------------------------------------- scheduler + producer
       if (lane == 0) {
@@ -178,7 +175,7 @@ __global__ void __launch_bounds__(256, 1)
       int c = 0, nq = 0, np = 0;
       bool ok = true;
       PagedFeed feed;
-      feed.start(p, scan, 0, me, workers, lane);
+      feed.start(p, all.total, gridDim.x, true, lane);
       const PagedWalk& w = feed.w;
       while (true) {
         const int e = np & 1;
@@ -187,7 +184,7 @@ __global__ void __launch_bounds__(256, 1)
           break;
         }
         if (lane == 0) {
-          pieces[e] = feed.piece();
+          pieces[e] = feed.piece(p);
           mbar_arrive(&sched_full[e]);
         }
         ++np;
@@ -204,7 +201,8 @@ __global__ void __launch_bounds__(256, 1)
               tma_load_3d(&tmQ, bar_q, sQ + a * 16384, a * 64, un.head0, w.s.row0 + w.i0);
           }
           ++nq;
-          ok = load_tiles<C>(p, tmK, tmV, w.span, w.b, un, w.j0, w.j1, full, empty, sStage, c, 0, lane, abort_flag);
+          ok = load_tiles<C>(p, tmK, tmV, w.span, w.b, un, w.j0, w.j1, full, empty, sStage, c, 0, lane, abort_flag,
+                             feed.last() ? &feed : nullptr);
           if (!ok) break;
         }
         feed.next(p, lane);
@@ -488,7 +486,7 @@ __global__ void __launch_bounds__(256, 1)
         const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
         const long long row = w.row0 + i;
         T* orow = static_cast<T*>(p.o) + (row * p.hq + un.head0 + h) * p.dv + un.split * DV;
-        float* part = p.parts + ((long long)me * 2 + (whole ? 0 : w.slot)) * (128 * (DV + 2));
+        float* part = p.parts + (long long)(whole ? 0 : w.slot) * (128 * (DV + 2));
 #pragma unroll 1
         for (int k = 0; k < DV / 32; ++k) {
           uint32_t u[32];
@@ -561,9 +559,9 @@ int launch_chunk_t(const PagedLaunch& L, int* launches) {
                                   L.tmK, L.tmV, L.p))
     return rc;
   ++*launches;
-  if (L.workers == 1 || !L.p.split) return SDPA_OK;  // no item crosses a cut
+  if (!L.p.tail) return SDPA_OK;  // no item crosses a cut
   ++*launches;
-  return launch_paged_join(L, 128, DV, BF16);
+  return launch_paged_join(L, 128, DV, L.p.tail, BF16);
 }
 
 }  // namespace

@@ -74,7 +74,7 @@ template <bool BF16>
 __global__ void __launch_bounds__(PairCfg::THREADS, 1)
     paged_pair_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                       const __grid_constant__ CUtensorMap tmV, const __grid_constant__ PagedParams p,
-                      const int most_workers) {
+                      const int pipes) {
   using C = PairCfg;
   using E = Elem<BF16>;
   extern __shared__ uint8_t smem_raw[];
@@ -115,18 +115,12 @@ __global__ void __launch_bounds__(PairCfg::THREADS, 1)
     tmem_relinquish();
   }
   tc_fence_before();
-  // pipeline x of CTA c is worker x * gridDim.x + c
-  const PagedShares all =
-      paged_scan<C::THREADS>(p, scan, blockIdx.x, gridDim.x, p.split ? 2 : 0, most_workers);
+  const PagedShares all = paged_scan<C::THREADS>(p, scan, 0, 0, 0, 1);
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
-  const int workers = (int)min((long long)most_workers, all.total);
-  if (threadIdx.x == 0 && blockIdx.x == 0) {
-    if (SDPA_ADDR_OK(p.chk, p.total_tiles, 8)) *p.total_tiles = all.total;
-    if (!all.fit) record_error(p.err, SDPA_ERR_BAD_SEQLENS);
-  }
+  if (threadIdx.x == 0 && blockIdx.x == 0 && !all.fit) record_error(p.err, SDPA_ERR_BAD_SEQLENS);
 
-  if (blockIdx.x >= workers) {
+  if (all.total == 0) {
     // no work: fall through to the end
   } else if (warp >= 8) {
     regs_dec<C::REGS_OTHER>();
@@ -142,7 +136,8 @@ __global__ void __launch_bounds__(PairCfg::THREADS, 1)
       int c = 0, nq = 0, np = 0;
       bool ok = true;
       PagedFeed feed;
-      feed.start(p, scan, warp - 8, (warp - 8) * gridDim.x + blockIdx.x, workers, lane);
+      // pipeline x of CTA c is pipeline x * gridDim.x + c
+      feed.start(p, all.total, pipes, (warp - 8) * (int)gridDim.x + (int)blockIdx.x < pipes, lane);
       const PagedWalk& w = feed.w;
       while (true) {
         const int e = np & 1;
@@ -151,7 +146,7 @@ __global__ void __launch_bounds__(PairCfg::THREADS, 1)
           break;
         }
         if (lane == 0) {
-          P.pieces[e] = feed.piece();
+          P.pieces[e] = feed.piece(p);
           mbar_arrive(&P.sched_full[e]);
         }
         ++np;
@@ -172,7 +167,10 @@ __global__ void __launch_bounds__(PairCfg::THREADS, 1)
           PagedIds cur = paged_ids(box_of(w.j0));
           for (int j = w.j0; j < w.j1 && ok; ++j) {
             PagedBox ahead;  // its table entry arrives while this tile's copies go out
-            if (j + 1 < w.j1) ahead = box_of(j + 1);
+            if (j + 1 < w.j1)
+              ahead = box_of(j + 1);
+            else if (feed.last())
+              feed.ask(p, lane);
             const uint32_t bytes = paged_boxes(p, w.span, (w.span.tile0 + j) * kTile, 0, kTile) * 2 * box_bytes;
             for (int kv = 0; kv < 2; ++kv, ++c) {
               const int slot = c % C::NST;
@@ -357,7 +355,7 @@ __global__ void __launch_bounds__(PairCfg::THREADS, 1)
         n = w.j1 - w.j0;
         out_row = (long long)(w.row0 + i) * p.hq + un.head0 + h;
         part = w.slot < 0 ? nullptr
-                          : p.parts + ((long long)(x * gridDim.x + blockIdx.x) * 2 + w.slot) * (128 * 130);
+                          : p.parts + (long long)w.slot * (128 * 130);
       }
       float mbs = -INFINITY, l = 0.f;  // running maximum of S * scale * log2 e, and the sum
       for (int j = 0; j < n; ++j) {
@@ -526,9 +524,9 @@ int launch_pair_t(const PagedLaunch& L, int sms, int* launches) {
                                   L.tmQ, L.tmK, L.tmV, L.p, L.workers))
     return rc;
   ++*launches;
-  if (L.workers == 1 || !L.p.split) return SDPA_OK;  // no item crosses a cut
+  if (!L.p.tail) return SDPA_OK;  // no item crosses a cut
   ++*launches;
-  return launch_paged_join(L, 128, 128, BF16);
+  return launch_paged_join(L, 128, 128, L.p.tail, BF16);
 }
 
 }  // namespace

@@ -20,13 +20,15 @@ pytestmark = pytest.mark.gpu
 BF, HF = torch.bfloat16, torch.float16
 
 
-def case(new, total, hq=8, hkv=2, d=128, dv=None, page=16, order="nhd", dtype=BF, pad=0, seed=0, poison=True, std=1.0):
-    """A batch on the CPU and the GPU; slots that hold no key of their sequence are NaN."""
+def case(new, total, hq=8, hkv=2, d=128, dv=None, page=16, order="nhd", dtype=BF, pad=0, seed=0, poison=True, std=1.0,
+         max_kv=0):
+    """A batch on the CPU and the GPU; slots that hold no key of their sequence are NaN. max_kv: the bound given for
+    the lengths, when larger than they are."""
     rng = np.random.default_rng(seed)
     g = torch.Generator().manual_seed(seed)
     dv = dv or (128 if d == 192 else d)
     n = lambda *s: (torch.randn(*s, generator=g) * std).to(dtype)  # noqa: E731
-    table, pages = ref.make_pages(rng, total, page)
+    table, pages = ref.make_pages(rng, total, page, cols=max(1, -(-max(max_kv, max(total)) // page)))
     kc, vc = n(pages, page, hkv, d), n(pages, page, hkv, dv)
     used = torch.zeros(pages, page, dtype=torch.bool)
     for b, k in enumerate(total):
@@ -40,7 +42,7 @@ def case(new, total, hq=8, hkv=2, d=128, dv=None, page=16, order="nhd", dtype=BF
     cu = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
     q = n(int(sum(new)) + pad, hq, d)
     c = dict(q=q, kc=kc, vc=vc, table=table, cu=cu, lens=np.array(total, dtype=np.int32), page=page, order=order,
-             max_q=max(max(new), 1), max_kv=max(max(total), 1), scale=d ** -0.5, dtype=dtype)
+             max_q=max(max(new), 1), max_kv=max(max(total), max_kv, 1), scale=d ** -0.5, dtype=dtype)
     c["dev"] = [q.cuda(), kc.cuda(), vc.cuda()] + [torch.from_numpy(x).cuda() for x in (table, c["lens"], cu)]
     return c
 
@@ -302,6 +304,25 @@ def test_ticket_order_of_many_sequences(d, n):
     total = np.maximum(new, rng.integers(0, 4, n) * 70 + 5)
     c = case(new.tolist(), total.tolist(), hq=8, hkv=4, d=d, page=16, pad=2)
     check(c, *call(c))
+
+
+@pytest.mark.parametrize("d,hq,hkv", [(128, 8, 2), (128, 3, 3), (192, 8, 2), (256, 16, 4), (512, 4, 1)])
+@pytest.mark.parametrize("new,total", [([300], [2000]), ([700, 40, 33, 500], [700, 41, 3000, 900]), ([40] * 60, [50] * 60),
+                                       ([64, 200, 0, 3], [10, 0, 0, 1000])])
+def test_the_last_items_cut_into_shares(d, hq, hkv, new, total):
+    """Long contexts (by their bound) of few items: with no, one and several rounds of whole items before the rest."""
+    c = case(new, total, hq=hq, hkv=hkv, d=d, page=64, max_kv=7000)
+    a, b = call(c), call(c)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])  # the shares do not depend on who takes them
+    check(c, *a)
+    try:
+        for cap in (1, 2, 5, 33):
+            sdpa.sdpa_debug_set_max_ctas(cap)
+            check(c, *call(c))
+    finally:
+        sdpa.sdpa_debug_set_max_ctas(0)
+    check(c, *call(c, window=150), window=150)
+    check(c, *call(c, causal=False), causal=False)
 
 
 def test_a_large_batch():
