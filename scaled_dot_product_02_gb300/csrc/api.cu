@@ -443,11 +443,11 @@ struct PagedCutting {
   bool used, fits;
   int n;                         // rows of an item
   int block_heads, head_blocks;  // heads of a group in an item, items a group takes
-  int tokens;                    // tokens in an item
+  int q_tokens, tokens;          // tokens of one Q copy, and in an item
   int dv_item, dv_splits;        // value columns an item accumulates, items that share a row
   bool split;                    // rows kernel: items may be split over workers
   int tail;                      // chunk kernels: shares that the last items are cut into
-  int workers;                   // CTAs (at most one per SM); head_dim 128 chunks: pipelines, two a CTA
+  int workers;                   // CTAs, at most one per SM
 };
 struct PagedPlan {
   int small_q;         // sequences of at most this many new tokens go to the rows kernel, longer ones to the chunk kernel
@@ -458,15 +458,17 @@ struct PagedPlan {
 // workspace size, must not depend on the device in use.
 constexpr int kPagedWorkers = 152;
 
-PagedCutting paged_cutting(const sdpa_paged_problem* p, int n, int max_q, int dv_item) {
+// n: rows of an item, in copies of q_rows.
+PagedCutting paged_cutting(const sdpa_paged_problem* p, int n, int q_rows, int max_q, int dv_item) {
   PagedCutting c;
-  const int most = n == 128 && p->head_dim == 128 ? 2 * kPagedWorkers : kPagedWorkers;
+  constexpr int most = kPagedWorkers;
   const int group = p->num_heads_q / p->num_heads_kv, dv = paged_dv(p);
   c.used = true;
   c.n = n;
-  c.block_heads = std::min(group, n);
+  c.block_heads = std::min(group, q_rows);
   c.head_blocks = (group + c.block_heads - 1) / c.block_heads;
-  c.tokens = std::max(1, std::min(n / c.block_heads, max_q));
+  c.q_tokens = std::max(1, std::min(q_rows / c.block_heads, max_q));
+  c.tokens = c.q_tokens * (n / q_rows);
   c.dv_item = dv_item;
   c.dv_splits = dv / dv_item;
   // the most items the batch can have, and the most key tiles one of them sees
@@ -480,13 +482,13 @@ PagedCutting paged_cutting(const sdpa_paged_problem* p, int n, int max_q, int dv
     c.split = tiles > 4;
     c.tail = 0;
   } else {
-    // Whole items by ticket keep the CTAs on the same keys (all items split into equal shares: 2048 tokens over
-    // 131072 keys 3290 -> 3750 us, 8 x 1024 over 32768 3110 -> 4400 us). The last, uneven round costs half an item
-    // on average: cut into shares where items are few and long enough to pay for the join (2048 tokens over 16384
-    // keys: D192 643 -> 567 us, D512 1256 -> 1116 us). Not at head_dim 128, where an SM's other pipeline goes on
-    // faster alone and the rest costs as much as it saves (413 -> 421 us).
+    // Whole items by ticket keep the CTAs on the same keys (with all items cut into equal shares, 2048 tokens over
+    // 131072 keys took 14 % longer, 8 x 1024 over 32768 40 %). The last, uneven round costs half an item on average:
+    // it is cut into shares where items are few and long enough to pay for the join (2048 tokens over 16384 keys, 3.4
+    // rounds: D192 643 -> 580 us, D512 1244 -> 1125 us; at head_dim 128, 2048 over 131072, 1.7 rounds: 2856 -> 2708
+    // us, but 8 x 512 over 4096 to 8192, 3.4 rounds: 285 -> 306 us).
     c.split = false;
-    c.tail = p->head_dim != 128 && tiles >= 48 && items < 6 * most ? 2 * most : 0;
+    c.tail = tiles >= 48 && items < (n == 256 ? 2 : 6) * most ? 2 * most : 0;
   }
   // the length of a block and the ticket counter are 32-bit numbers
   c.fits = (long long)p->num_heads_kv * c.head_blocks * c.dv_splits * std::max(tiles, 1LL) < (1LL << 31) &&
@@ -509,9 +511,10 @@ PagedPlan paged_plan(const sdpa_paged_problem* p) {
   if (pl.small_q >= 0) {
     const int max_q = std::min(p->seqlen_q, pl.small_q);
     const long long rows = (long long)group * std::max(max_q, 1);
-    pl.rows = paged_cutting(p, rows <= 16 ? 16 : (rows <= 32 || most == 32) ? 32 : 64, max_q, dv);
+    const int n = rows <= 16 ? 16 : (rows <= 32 || most == 32) ? 32 : 64;
+    pl.rows = paged_cutting(p, n, n, max_q, dv);
   }
-  if (p->seqlen_q > pl.small_q) pl.chunk = paged_cutting(p, 128, p->seqlen_q, std::min(dv, 256));
+  if (p->seqlen_q > pl.small_q) pl.chunk = paged_cutting(p, p->head_dim == 128 ? 256 : 128, 128, p->seqlen_q, std::min(dv, 256));
   size_t at = 256;  // totals and tickets
   for (int x = 0; x < 2; ++x) {
     const PagedCutting& c = x ? pl.chunk : pl.rows;
@@ -1313,7 +1316,7 @@ int sdpa_paged_fwd(const sdpa_paged_problem* p, const void* q, const void* k_cac
     P.small = small;
     P.split = c->split;
     P.tail = c->tail;
-    P.q_box_rows = c->tokens * c->block_heads;
+    P.q_box_rows = c->q_tokens * c->block_heads;
     P.causal = p->mask_type != SDPA_MASK_NONE;
     P.window = p->window_left;
     P.scale_log2 = p->softmax_scale * 1.4426950408889634f;
@@ -1336,12 +1339,12 @@ int sdpa_paged_fwd(const sdpa_paged_problem* p, const void* q, const void* k_cac
     P.err = err;
     P.chk = chk;
     const bool pair = !small && d == 128;
-    L.workers = std::min(c->workers, pair ? 2 * sms : sms);
+    L.workers = std::min(c->workers, sms);
     if (debug_max_ctas() > 0) L.workers = std::min(L.workers, debug_max_ctas());
     L.stream = s;
     const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)p->num_heads_q, (cuuint64_t)p->total_q};
     const cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)qs * 2};
-    const cuuint32_t box[3] = {64, (cuuint32_t)c->block_heads, (cuuint32_t)c->tokens}, estr[3] = {1, 1, 1};
+    const cuuint32_t box[3] = {64, (cuuint32_t)c->block_heads, (cuuint32_t)c->q_tokens}, estr[3] = {1, 1, 1};
     if (encode_map(&L.tmQ, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
                    const_cast<void*>(q), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -1353,7 +1356,7 @@ int sdpa_paged_fwd(const sdpa_paged_problem* p, const void* q, const void* k_cac
       return rc;
     rc = timed(SDPA_KERNEL_PAGED, s, [&] {
       return small  ? launch_paged_rows(L, c->n, d, bf16, &launches)
-             : pair ? launch_paged_pair(L, sms, bf16, &launches)
+             : pair ? launch_paged_pair(L, bf16, &launches)
                     : launch_paged_chunk(L, d, bf16, &launches);
     });
     if (rc) return rc;

@@ -270,7 +270,7 @@ struct PagedParams {
   int split;                   // rows kernel: items may be split over workers
   int tail;                    // chunk kernels: shares that the last items are cut into (0: none)
   int behind;                  // started while the rows kernel of the same call (and its join) still run
-  int q_box_rows;              // rows the Q copy brings: tokens x block_heads
+  int q_box_rows;              // rows one Q copy brings (half of an item's at head_dim 128 chunks)
   int causal, window;          // window < 0: none
   float scale_log2;
   int page_size, num_pages, box_rows;  // box_rows: slots one copy brings (divides page_size and 128)
@@ -289,16 +289,16 @@ struct PagedParams {
 struct PagedLaunch {
   CUtensorMap tmQ, tmK, tmV;
   PagedParams p;
-  int workers;                 // CTAs, or pipelines
+  int workers;                 // CTAs
   cudaStream_t stream;
 };
 size_t paged_cut_bytes();
 // n: rows of an item, 16, 32 or 64 (64 not with head_dim 512)
 int launch_paged_rows(const PagedLaunch& L, int n, int head_dim, bool bf16, int* launches);
-// Items of 128 rows.
+// Items of 128 rows, head dims 192 to 512.
 int launch_paged_chunk(const PagedLaunch& L, int head_dim, bool bf16, int* launches);
-// The same at head_dim 128, two pipelines a CTA (L.workers pipelines on at most sms CTAs).
-int launch_paged_pair(const PagedLaunch& L, int sms, bool bf16, int* launches);
+// Items of 256 rows, head_dim 128.
+int launch_paged_pair(const PagedLaunch& L, bool bf16, int* launches);
 // Joins the items that cross a cut between `shares` shares: n rows of dv values an item.
 int launch_paged_join(const PagedLaunch& L, int n, int dv, int shares, bool bf16);
 

@@ -575,7 +575,7 @@ __global__ void __launch_bounds__(256, 1)
 // row's statistics: after the wait there are two rounds of loads, the cut and the
 // parts. (One CTA per item, statistics first, took 4 us where the parts were
 // small and 29 to 49 us for the 128-row items of chunks.)
-constexpr int join_rows(int n) { return n == 128 ? 32 : 8; }
+constexpr int join_rows(int n) { return n >= 128 ? 32 : 8; }
 
 template <int DV, int N, bool BF16>
 __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__ PagedParams p, int grid) {
@@ -673,6 +673,7 @@ int launch_paged_join(const PagedLaunch& L, int n, int dv, int shares, bool bf16
   if (shares < 2) return SDPA_OK;
 #define JOIN(A, B) return bf16 ? launch_join_t<A, B, true>(L, shares) : launch_join_t<A, B, false>(L, shares)
   if (n == 128 && dv == 128) JOIN(128, 128);
+  if (n == 256 && dv == 128) JOIN(128, 256);
   if (n == 128 && dv == 256) JOIN(256, 128);
 #undef JOIN
   return SDPA_ERR_UNSUPPORTED;

@@ -182,49 +182,6 @@ __device__ __forceinline__ PagedBox paged_box(const PagedParams& p, const PagedS
   }
   return x;
 }
-// All boxes of a tile, known to every lane of a warp, so that one elected thread
-// can issue the copies back to back.
-struct PagedIds {
-  int page[8], slot[8];
-  uint32_t mine;  // bit e: box e is copied
-};
-__device__ __forceinline__ PagedIds paged_ids(const PagedBox& x) {  // lane e holds box e
-  PagedIds r;
-  r.mine = __ballot_sync(0xffffffffu, x.mine);
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    r.page[e] = __shfl_sync(0xffffffffu, x.page, e);
-    r.slot[e] = __shfl_sync(0xffffffffu, x.slot, e);
-  }
-  return r;
-}
-// Copies NB boxes of 128 columns to a stage (two blocks of 64 columns, 16 KB
-// apart); a single thread calls it. ALL: every box, without a test for each.
-template <int NB, bool ALL>
-__device__ __forceinline__ void paged_copy128(const PagedParams& p, const CUtensorMap* m, uint64_t* bar, uint8_t* stage,
-                                              int kvh, const PagedIds& x) {
-#pragma unroll
-  for (int e = 0; e < NB; ++e)
-    if (ALL || (x.mine >> e & 1)) {
-      const int c1 = p.slot_first ? x.slot[e] : kvh, c2 = p.slot_first ? kvh : x.slot[e];
-      uint8_t* dst = stage + e * p.box_rows * 128;
-      tma_load_4d(m, bar, dst, 0, c1, c2, x.page[e]);
-      tma_load_4d(m, bar, dst + 16384, 64, c1, c2, x.page[e]);
-    }
-}
-__device__ __forceinline__ void paged_copy128(const PagedParams& p, const CUtensorMap* m, uint64_t* bar, uint8_t* stage,
-                                              int kvh, const PagedIds& x) {
-  if (x.mine == 0xffu)
-    paged_copy128<8, true>(p, m, bar, stage, kvh, x);
-  else if (p.box_rows == 32 && x.mine == 0xfu)
-    paged_copy128<4, true>(p, m, bar, stage, kvh, x);
-  else if (p.box_rows == 64 && x.mine == 0x3u)
-    paged_copy128<2, true>(p, m, bar, stage, kvh, x);
-  else if (p.box_rows == 128)
-    paged_copy128<1, true>(p, m, bar, stage, kvh, x);
-  else
-    paged_copy128<8, false>(p, m, bar, stage, kvh, x);
-}
 // How many boxes of the tile's keys [k_lo, k_hi) (multiples of box_rows) are copied.
 __device__ __forceinline__ int paged_boxes(const PagedParams& p, const PagedSpan& span, int key0, int k_lo, int k_hi) {
   const int lo = max(span.lo - key0, k_lo), hi = min(span.hi - key0, k_hi);
@@ -508,5 +465,75 @@ struct PagedFeed {
     return PagedPiece{more ? w.s.row0 : -1, w.s.q_len, w.s.kv_len, w.b, w.i0, w.unit, w.j0, w.j1, slot};
   }
 };
+
+// Producer `pw` of three copies its boxes (3 e + pw, one a lane) of the K and V
+// tiles [j0, j1) of an item through the ring (V of a tile behind its K, or behind
+// the next tile's, as C says); c counts the stages. Every producer arrives on each stage, with copies in
+// it or not, or the ring could go on without one and leave it a phase behind.
+// Producer 0 sets the byte count; the others' copies may complete before it. feed:
+// asked for the next ticket with the last tile.
+template <class C>
+__device__ __forceinline__ bool load_tiles(const PagedParams& p, const CUtensorMap& tmK, const CUtensorMap& tmV,
+                                           const PagedSpan& span, int b, const PagedUnit& un, int j0, int j1, uint64_t* full,
+                                           uint64_t* empty, uint8_t* sStage, int& c, int pw, int lane,
+                                           volatile int* abort_flag, PagedFeed* feed = nullptr) {
+  const int box = lane * 3 + pw, first = box * p.box_rows;  // this lane's box of a tile, its first key
+  const uint32_t box_bytes = p.box_rows * 128;
+  auto next_slot = [&](uint32_t bytes) -> int {
+    const int slot = c % C::NST;
+    if (!__all_sync(0xffffffffu, mbar_wait(&empty[slot], ((c / C::NST) & 1) ^ 1, abort_flag))) return -1;
+    if (lane == 0) {
+      if (pw == 0)
+        mbar_arrive_expect_tx(&full[slot], bytes);
+      else
+        mbar_arrive(&full[slot]);
+    }
+    ++c;
+    return slot;
+  };
+  auto copy = [&](const CUtensorMap* m, int slot, uint8_t* dst, int col, const PagedBox& x) {
+    tma_load_4d(m, &full[slot], dst, col, p.slot_first ? x.slot : un.kvh, p.slot_first ? un.kvh : x.slot, x.page);
+  };
+  auto load_k = [&](const PagedBox& x, int key0) -> bool {
+    const int boxes = paged_boxes(p, span, key0, 0, kTile);
+    for (int kb = 0; kb < C::KST; ++kb) {
+      const int atoms = C::k_atoms(kb), slot = next_slot(boxes * atoms * box_bytes);
+      if (slot < 0) return false;
+      uint8_t* dst = sStage + slot * kStage + first * 128;
+      if (x.mine)
+        for (int a = 0; a < atoms; ++a) copy(&tmK, slot, dst + a * 16384, kb * 128 + a * 64, x);
+      __syncwarp();
+    }
+    return true;
+  };
+  auto load_v = [&](const PagedBox& x, int key0) -> bool {
+    for (int vs = 0; vs < C::VST; ++vs) {
+      const int slot = next_slot(paged_boxes(p, span, key0, vs * C::VROWS, (vs + 1) * C::VROWS) * (C::DV_ITEM / 64) * box_bytes);
+      if (slot < 0) return false;
+      uint8_t* dst = sStage + slot * kStage + (first - vs * C::VROWS) * 128;
+      if (x.mine && first / C::VROWS == vs)
+        for (int a = 0; a < C::DV_ITEM / 64; ++a) copy(&tmV, slot, dst + a * C::V_ATOM, un.split * C::DV_ITEM + a * 64, x);
+      __syncwarp();
+    }
+    return true;
+  };
+  auto box_of = [&](int j) { return paged_box(p, span, b, (span.tile0 + j) * kTile, box); };
+  PagedBox cur = box_of(j0), prev = cur;
+#pragma unroll 1
+  for (int j = j0; j < j1; ++j) {
+    const PagedBox ahead = j + 1 < j1 ? box_of(j + 1) : cur;  // its table entry arrives while this tile's copies go out
+    const int key0 = (span.tile0 + j) * kTile;
+    if (feed && j + 1 == j1) feed->ask(p, lane);
+    if (!load_k(cur, key0)) return false;
+    if (!C::V_BEHIND) {
+      if (!load_v(cur, key0)) return false;
+    } else if (j > j0 && !load_v(prev, key0 - kTile)) {
+      return false;
+    }
+    prev = cur;
+    cur = ahead;
+  }
+  return !C::V_BEHIND || load_v(prev, (span.tile0 + j1 - 1) * kTile);
+}
 
 }  // namespace sdpa

@@ -31,6 +31,7 @@ struct ChunkCfg {
   static constexpr int KST = (DQK + 127) / 128;  // K stages of a tile (128 keys x up to 128 columns)
   static __device__ __forceinline__ constexpr int k_atoms(int kb) { return DQK / 64 - 2 * kb >= 2 ? 2 : 1; }
   static constexpr int DV_ITEM = DV;
+  static constexpr bool V_BEHIND = true;           // V of a tile follows K of the next one in the ring
   static constexpr int VROWS = kStage / (DV * 2);  // keys of a V stage
   static constexpr int VST = kTile / VROWS;
   static constexpr int V_ATOM = VROWS * 128;       // bytes of 64 columns of a V stage
@@ -42,71 +43,6 @@ struct ChunkCfg {
   static constexpr int TM_S = DV;                  // TMEM columns: O, then two S / P buffers
   static_assert(SMEM <= kSmemMax && NST >= VST && DV + 256 <= 512, "the tile plan fits one SM");
 };
-
-// Producer `pw` of three copies its boxes (3 e + pw, one a lane) of the K and V
-// tiles [j0, j1) of an item through the ring, in the order the MMA issuer takes
-// them; c counts the stages. Every producer arrives on each stage, with copies in
-// it or not, or the ring could go on without one and leave it a phase behind.
-// Producer 0 sets the byte count; the others' copies may complete before it. feed:
-// asked for the next ticket with the last tile.
-template <class C>
-__device__ __forceinline__ bool load_tiles(const PagedParams& p, const CUtensorMap& tmK, const CUtensorMap& tmV,
-                                           const PagedSpan& span, int b, const PagedUnit& un, int j0, int j1, uint64_t* full,
-                                           uint64_t* empty, uint8_t* sStage, int& c, int pw, int lane,
-                                           volatile int* abort_flag, PagedFeed* feed = nullptr) {
-  const int box = lane * 3 + pw, first = box * p.box_rows;  // this lane's box of a tile, its first key
-  const uint32_t box_bytes = p.box_rows * 128;
-  auto next_slot = [&](uint32_t bytes) -> int {
-    const int slot = c % C::NST;
-    if (!__all_sync(0xffffffffu, mbar_wait(&empty[slot], ((c / C::NST) & 1) ^ 1, abort_flag))) return -1;
-    if (lane == 0) {
-      if (pw == 0)
-        mbar_arrive_expect_tx(&full[slot], bytes);
-      else
-        mbar_arrive(&full[slot]);
-    }
-    ++c;
-    return slot;
-  };
-  auto copy = [&](const CUtensorMap* m, int slot, uint8_t* dst, int col, const PagedBox& x) {
-    tma_load_4d(m, &full[slot], dst, col, p.slot_first ? x.slot : un.kvh, p.slot_first ? un.kvh : x.slot, x.page);
-  };
-  auto load_k = [&](const PagedBox& x, int key0) -> bool {
-    const int boxes = paged_boxes(p, span, key0, 0, kTile);
-    for (int kb = 0; kb < C::KST; ++kb) {
-      const int atoms = C::k_atoms(kb), slot = next_slot(boxes * atoms * box_bytes);
-      if (slot < 0) return false;
-      uint8_t* dst = sStage + slot * kStage + first * 128;
-      if (x.mine)
-        for (int a = 0; a < atoms; ++a) copy(&tmK, slot, dst + a * 16384, kb * 128 + a * 64, x);
-      __syncwarp();
-    }
-    return true;
-  };
-  auto load_v = [&](const PagedBox& x, int key0) -> bool {
-    for (int vs = 0; vs < C::VST; ++vs) {
-      const int slot = next_slot(paged_boxes(p, span, key0, vs * C::VROWS, (vs + 1) * C::VROWS) * (C::DV_ITEM / 64) * box_bytes);
-      if (slot < 0) return false;
-      uint8_t* dst = sStage + slot * kStage + (first - vs * C::VROWS) * 128;
-      if (x.mine && first / C::VROWS == vs)
-        for (int a = 0; a < C::DV_ITEM / 64; ++a) copy(&tmV, slot, dst + a * C::V_ATOM, un.split * C::DV_ITEM + a * 64, x);
-      __syncwarp();
-    }
-    return true;
-  };
-  auto box_of = [&](int j) { return paged_box(p, span, b, (span.tile0 + j) * kTile, box); };
-  PagedBox cur = box_of(j0), prev = cur;
-  for (int j = j0; j < j1; ++j) {
-    const PagedBox ahead = j + 1 < j1 ? box_of(j + 1) : cur;  // its table entry arrives while this tile's copies go out
-    const int key0 = (span.tile0 + j) * kTile;
-    if (feed && j + 1 == j1) feed->ask(p, lane);
-    if (!load_k(cur, key0)) return false;
-    if (j > j0 && !load_v(prev, key0 - kTile)) return false;
-    prev = cur;
-    cur = ahead;
-  }
-  return load_v(prev, (span.tile0 + j1 - 1) * kTile);
-}
 
 template <int DQK, int DV, bool BF16>
 __global__ void __launch_bounds__(256, 1)

@@ -1,15 +1,18 @@
 // paged_pair.cu -- attention over a paged cache for chunks of many tokens at
-// head_dim 128: as paged_chunk.cu, with two items in flight per CTA. One item's
-// softmax runs while the tensor pipe works on the other's MMAs, which at this
-// width (as many exponentials per MMA flop as it gets) one item cannot overlap
-// by itself.
+// head_dim 128: as paged_chunk.cu, with items of 256 rows, two 128-row tiles of Q
+// against one stream of key tiles. While one tile's softmax runs the tensor pipe
+// works on the other's MMAs, which at this width (as many exponentials per MMA
+// flop as it gets) one tile cannot overlap by itself; and each K and V tile that
+// comes from the L2 serves 256 rows. (Two pipelines with an item and a ring of
+// two stages each read 11.6 TB/s from the L2 at 1.25 PFLOP/s, which bound them.)
 //
-// 384 threads: warps 0-3 / 4-7 softmax and output of pipeline 0 / 1 (one thread
-// per query row), warps 8 / 9 their schedulers and TMA producers, warp 10 TMEM
-// allocator and MMA issuer for both, warp 11 completes its warpgroup. Pipeline
-// x has O at TMEM columns [256 x, 256 x + 128) and S / P behind it; within a
-// pipeline S_j, softmax_j and P V_j follow one another, and the issuer serves
-// the two strictly in turn, which keeps them half a period apart.
+// 384 threads: warps 0-3 / 4-7 softmax and output of rows 0-127 / 128-255 (one
+// thread per query row), warp 8 scheduler and TMA producer, warps 9 and 11 further
+// producers, warp 10 TMEM allocator and MMA issuer. Half x has O at TMEM columns
+// [256 x, 256 x + 128) and S / P behind it; within a half S_j, softmax_j and P V_j
+// follow one another, and the issuer serves the two in turn, which keeps them
+// half a period apart. A block of fewer tokens than one tile holds leaves the
+// second half out.
 #include <algorithm>
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -23,88 +26,64 @@ namespace {
 
 struct PairCfg {
   static constexpr int THREADS = 384;
-  static constexpr int Q_BYTES = 32768;
-  static constexpr int NST = 2;
-  static constexpr int PIPE_BYTES = Q_BYTES + NST * kStage;
-  static constexpr int PIPE_BARS = 16;                             // mbarriers of a pipeline
+  static constexpr int Q_BYTES = 32768;                            // of one half
+  static constexpr int KST = 1, VST = 1, DV_ITEM = 128, VROWS = 128, V_ATOM = 16384;
+  static constexpr bool V_BEHIND = false;
+  static constexpr int NST = 4;
   static constexpr int STG_BYTES = 8 * 2048;                       // per softmax warp: 32 rows x 64 bytes of output
-  static constexpr int SMEM = 1024 + 2 * PIPE_BYTES + 2 * PIPE_BARS * 8 + STG_BYTES + 1024;
-  static constexpr uint32_t TM_S = 128, TM_PIPE = 256;
+  static constexpr int MISC = 1024;
+  static constexpr int SMEM = 1024 + 2 * Q_BYTES + NST * kStage + STG_BYTES + MISC;
+  static constexpr uint32_t TM_S = 128, TM_HALF = 256;
+  static __device__ __forceinline__ constexpr int k_atoms(int) { return 2; }
   // two softmax warpgroups and the third out of 3 x 168, the registers the block is launched with
   static constexpr int REGS_SOFTMAX = 192, REGS_OTHER = 120;
   static_assert(2 * REGS_SOFTMAX + REGS_OTHER <= 3 * 168 && SMEM <= kSmemMax, "register split and tile plan");
 };
 
-// Shared-memory objects of one pipeline.
-struct Pipe {
-  uint8_t *sQ, *sStage;
-  uint64_t* full;         // [NST]
-  uint64_t* empty;        // [NST]
-  uint64_t* bar_q;        // Q landed
-  uint64_t* bar_s;        // S_j in TMEM
-  uint64_t* bar_p;        // P_j in TMEM (and O rescaled)
-  uint64_t* bar_o;        // an item's last P V is done
-  uint64_t* q_free;       // an item's last S is done: Q may be replaced
-  uint64_t* o_free;       // the output has read O
-  uint64_t* sched_full;   // [2] a piece published
-  uint64_t* sched_empty;  // [2] read by the issuer and the softmax warps
-  PagedPiece* pieces;     // [2]
-};
-__device__ __forceinline__ Pipe pipe_of(uint8_t* smem, PagedPiece* pieces, int x) {
-  using C = PairCfg;
-  Pipe P;
-  P.sQ = smem + x * C::PIPE_BYTES;
-  P.sStage = P.sQ + C::Q_BYTES;
-  uint64_t* b = reinterpret_cast<uint64_t*>(smem + 2 * C::PIPE_BYTES) + x * C::PIPE_BARS;
-  P.full = b;
-  P.empty = b + C::NST;
-  P.bar_q = b + 2 * C::NST;
-  P.bar_s = P.bar_q + 1;
-  P.bar_p = P.bar_q + 2;
-  P.bar_o = P.bar_q + 3;
-  P.q_free = P.bar_q + 4;
-  P.o_free = P.bar_q + 5;
-  P.sched_full = P.bar_q + 6;
-  P.sched_empty = P.bar_q + 8;
-  P.pieces = pieces + 2 * x;
-  return P;
-}
-
 template <bool BF16>
 __global__ void __launch_bounds__(PairCfg::THREADS, 1)
     paged_pair_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                      const __grid_constant__ CUtensorMap tmV, const __grid_constant__ PagedParams p,
-                      const int pipes) {
+                      const __grid_constant__ CUtensorMap tmV, const __grid_constant__ PagedParams p) {
   using C = PairCfg;
   using E = Elem<BF16>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  uint8_t* stg = smem + 2 * C::PIPE_BYTES + 2 * C::PIPE_BARS * 8;
-  PagedScan* scan = reinterpret_cast<PagedScan*>(stg + C::STG_BYTES);
-  PagedPiece* pieces = reinterpret_cast<PagedPiece*>(scan + 1);  // [2][2]
-  uint64_t* bar_drain = reinterpret_cast<uint64_t*>(pieces + 4);
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bar_drain + 1);
+  uint8_t* sQ = smem;
+  uint8_t* sStage = smem + 2 * C::Q_BYTES;
+  uint8_t* stg = sStage + C::NST * kStage;
+  uint64_t* full = reinterpret_cast<uint64_t*>(stg + C::STG_BYTES);
+  uint64_t* empty = full + C::NST;
+  uint64_t* bar_q = empty + C::NST;   // both halves' Q landed
+  uint64_t* q_free = bar_q + 1;       // an item's last S is done: Q may be replaced
+  uint64_t* bar_s = q_free + 1;       // [2] S_j of a half in TMEM
+  uint64_t* bar_p = bar_s + 2;        // [2] its P_j in TMEM (and O rescaled)
+  uint64_t* bar_o = bar_p + 2;        // [2] its last P V is done
+  uint64_t* o_free = bar_o + 2;       // [2] its output has read O
+  uint64_t* sched_full = o_free + 2;  // [2] a piece published
+  uint64_t* sched_empty = sched_full + 2;
+  uint64_t* bar_drain = sched_empty + 2;
+  PagedScan* scan = reinterpret_cast<PagedScan*>(bar_drain + 1);
+  PagedPiece* pieces = reinterpret_cast<PagedPiece*>(scan + 1);  // [2]
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(pieces + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int half_tokens = p.tokens / 2;  // tokens of one half
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   if (threadIdx.x == 0) {
-    for (int x = 0; x < 2; ++x) {
-      const Pipe P = pipe_of(smem, pieces, x);
-      for (int i = 0; i < C::NST; ++i) {
-        mbar_init(&P.full[i], 1);
-        mbar_init(&P.empty[i], 1);
-      }
-      mbar_init(P.bar_q, 1);
-      mbar_init(P.bar_s, 1);
-      mbar_init(P.bar_p, 128);
-      mbar_init(P.bar_o, 1);
-      mbar_init(P.q_free, 1);
-      mbar_init(P.o_free, 128);
-      for (int i = 0; i < 2; ++i) {
-        mbar_init(&P.sched_full[i], 1);
-        mbar_init(&P.sched_empty[i], 129);
-      }
+    for (int i = 0; i < C::NST; ++i) {
+      mbar_init(&full[i], 3);  // every producer, so that none falls a phase behind
+      mbar_init(&empty[i], 1);
+    }
+    mbar_init(bar_q, 1);
+    mbar_init(q_free, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bar_s[i], 1);
+      mbar_init(&bar_p[i], 128);
+      mbar_init(&bar_o[i], 1);
+      mbar_init(&o_free[i], 128);
+      mbar_init(&sched_full[i], 1);
+      mbar_init(&sched_empty[i], 259);  // issuer, two producers, 256 softmax threads
     }
     mbar_init(bar_drain, 1);
     *abort_flag = 0;
@@ -124,71 +103,47 @@ __global__ void __launch_bounds__(PairCfg::THREADS, 1)
     // no work: fall through to the end
   } else if (warp >= 8) {
     regs_dec<C::REGS_OTHER>();
-    if (warp == 8 || warp == 9) {
-      // ---------------------------------------------------------- scheduler + producer of pipeline warp - 8
-      const Pipe P = pipe_of(smem, pieces, warp - 8);
+    if (warp == 8) {
+      // ---------------------------------------------------------- scheduler + producer
       if (lane == 0) {
         prefetch_tmap(&tmQ);
         prefetch_tmap(&tmK);
         prefetch_tmap(&tmV);
       }
-      const uint32_t box_bytes = p.box_rows * 128;
       int c = 0, nq = 0, np = 0;
       bool ok = true;
       PagedFeed feed;
-      // pipeline x of CTA c is pipeline x * gridDim.x + c
-      feed.start(p, all.total, pipes, (warp - 8) * (int)gridDim.x + (int)blockIdx.x < pipes, lane);
+      feed.start(p, all.total, gridDim.x, true, lane);
       const PagedWalk& w = feed.w;
       while (true) {
         const int e = np & 1;
-        if (!__all_sync(0xffffffffu, mbar_wait(&P.sched_empty[e], ((np >> 1) & 1) ^ 1, abort_flag))) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&sched_empty[e], ((np >> 1) & 1) ^ 1, abort_flag))) {
           ok = false;
           break;
         }
         if (lane == 0) {
-          P.pieces[e] = feed.piece(p);
-          mbar_arrive(&P.sched_full[e]);
+          pieces[e] = feed.piece(p);
+          mbar_arrive(&sched_full[e]);
         }
         ++np;
         if (!feed.more) break;
         if (w.span.tiles > 0) {
           const PagedUnit un = paged_unit(p, w.unit);
-          if (nq > 0 && !__all_sync(0xffffffffu, mbar_wait(P.q_free, (nq - 1) & 1, abort_flag))) {
+          if (nq > 0 && !__all_sync(0xffffffffu, mbar_wait(q_free, (nq - 1) & 1, abort_flag))) {
             ok = false;
             break;
           }
           if (lane == 0) {
-            mbar_arrive_expect_tx(P.bar_q, (uint32_t)p.q_box_rows * 256);
-            tma_load_3d(&tmQ, P.bar_q, P.sQ, 0, un.head0, w.s.row0 + w.i0);
-            tma_load_3d(&tmQ, P.bar_q, P.sQ + 16384, 64, un.head0, w.s.row0 + w.i0);
+            const int halves = w.i1(p) - w.i0 >= half_tokens ? 2 : 1;
+            mbar_arrive_expect_tx(bar_q, (uint32_t)(halves * p.q_box_rows * 256));
+            for (int x = 0; x < halves; ++x)
+              for (int a = 0; a < 2; ++a)
+                tma_load_3d(&tmQ, bar_q, sQ + x * C::Q_BYTES + a * 16384, a * 64, un.head0,
+                            w.s.row0 + w.i0 + x * half_tokens);
           }
           ++nq;
-          auto box_of = [&](int j) { return paged_box(p, w.span, w.b, (w.span.tile0 + j) * kTile, lane); };
-          PagedIds cur = paged_ids(box_of(w.j0));
-          for (int j = w.j0; j < w.j1 && ok; ++j) {
-            PagedBox ahead;  // its table entry arrives while this tile's copies go out
-            if (j + 1 < w.j1)
-              ahead = box_of(j + 1);
-            else if (feed.last())
-              feed.ask(p, lane);
-            const uint32_t bytes = paged_boxes(p, w.span, (w.span.tile0 + j) * kTile, 0, kTile) * 2 * box_bytes;
-            for (int kv = 0; kv < 2; ++kv, ++c) {
-              const int slot = c % C::NST;
-              if (!__all_sync(0xffffffffu, mbar_wait(&P.empty[slot], ((c / C::NST) & 1) ^ 1, abort_flag))) {
-                ok = false;
-                break;
-              }
-              // one thread issues: with two stages a pipeline, the time that the copies take to go out is on
-              // the way of the next S (issued by the lanes that hold the boxes they are serialised at some
-              // 100 cycles each)
-              if (elect_one()) {
-                mbar_arrive_expect_tx(&P.full[slot], bytes);
-                paged_copy128(p, kv ? &tmV : &tmK, &P.full[slot], P.sStage + slot * kStage, un.kvh, cur);
-              }
-              __syncwarp();
-            }
-            if (j + 1 < w.j1) cur = paged_ids(ahead);
-          }
+          ok = load_tiles<C>(p, tmK, tmV, w.span, w.b, un, w.j0, w.j1, full, empty, sStage, c, 0, lane, abort_flag,
+                             feed.last() ? &feed : nullptr);
           if (!ok) break;
         }
         feed.next(p, lane);
@@ -199,109 +154,122 @@ __global__ void __launch_bounds__(PairCfg::THREADS, 1)
           record_error(p.err, SDPA_ERR_TIMEOUT);
         }
         // every copy lands before the CTA ends
-        for (int k = max(0, c - C::NST); k < c; ++k) mbar_wait_drain(&P.full[k % C::NST], (k / C::NST) & 1);
-        if (nq > 0) mbar_wait_drain(P.bar_q, (nq - 1) & 1);
+        for (int k = max(0, c - C::NST); k < c; ++k) mbar_wait_drain(&full[k % C::NST], (k / C::NST) & 1);
+        if (nq > 0) mbar_wait_drain(bar_q, (nq - 1) & 1);
       }
-    } else if (warp == 10) {
-      // ---------------------------------------------------------- MMA issuer for both pipelines
+    } else if (warp == 9 || warp == 11) {
+      // ---------------------------------------------------------- further producers
+      int c = 0, np = 0;
+      bool ok = true;
+      while (true) {
+        const int e = np & 1;
+        if (!__all_sync(0xffffffffu, mbar_wait(&sched_full[e], (np >> 1) & 1, abort_flag))) {
+          ok = false;
+          break;
+        }
+        const PagedPiece w = pieces[e];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sched_empty[e]);
+        ++np;
+        if (w.row0 < 0) break;
+        if (w.j1 == w.j0) continue;
+        const PagedSpan span =
+            paged_span(p, PagedSeq{w.row0, w.q_len, w.kv_len}, w.i0, min(w.i0 + p.tokens, w.q_len) - 1);
+        ok = load_tiles<C>(p, tmK, tmV, span, w.b, paged_unit(p, w.unit), w.j0, w.j1, full, empty, sStage, c,
+                           warp == 9 ? 1 : 2, lane, abort_flag);
+        if (!ok) break;
+      }
+      if (lane == 0) {
+        if (!ok) {
+          *abort_flag = 1;
+          record_error(p.err, SDPA_ERR_TIMEOUT);
+        }
+        for (int k = max(0, c - C::NST); k < c; ++k) mbar_wait_drain(&full[k % C::NST], (k / C::NST) & 1);
+      }
+    } else {
+      // ---------------------------------------------------------- MMA issuer
       if (elect_one()) {
         constexpr uint32_t ID_S = idesc_f16(128, 128, BF16, false, false);
         constexpr uint32_t ID_O = idesc_f16(128, 128, BF16, false, true);
-        struct State {
-          int np, c, nq, tiles, no, n, j;  // pieces, ring stages, Q loads, P V MMAs, items done; this item's tiles, tile
-          bool done;
-        };
-        State st[2];
-        for (int x = 0; x < 2; ++x) st[x] = State{0, 0, 0, 0, 0, 0, 0, false};
+        const uint32_t q_base = smem_u32(sQ);
+        int np = 0, c = 0, nq = 0;            // pieces, ring stages, Q loads
+        int pv[2] = {0, 0}, no[2] = {0, 0};   // of a half: P V MMAs, items done
         bool ok = true;
-        // next piece with keys of pipeline x (false: its work is out, or a wait failed)
-        auto next_item = [&](int x) -> bool {
-          const Pipe P = pipe_of(smem, pieces, x);
-          State& m = st[x];
-          while (true) {
-            const int e = m.np & 1;
-            if (!mbar_wait(&P.sched_full[e], (m.np >> 1) & 1, abort_flag)) {
-              ok = false;
-              return false;
-            }
-            const bool end = P.pieces[e].row0 < 0;
-            const int n = P.pieces[e].j1 - P.pieces[e].j0;
-            mbar_arrive(&P.sched_empty[e]);
-            ++m.np;
-            if (end) {
-              m.done = true;
-              return false;
-            }
-            if (n == 0) continue;
-            if (!mbar_wait(P.bar_q, m.nq & 1, abort_flag)) {
-              ok = false;
-              return false;
-            }
-            ++m.nq;
+        while (ok) {
+          const int e = np & 1;
+          if (!mbar_wait(&sched_full[e], (np >> 1) & 1, abort_flag)) {
+            ok = false;
+            break;
+          }
+          const PagedPiece w = pieces[e];
+          mbar_arrive(&sched_empty[e]);
+          ++np;
+          if (w.row0 < 0) break;
+          const int n = w.j1 - w.j0;
+          if (n == 0) continue;
+          const int halves = min(w.q_len - w.i0, p.tokens) > half_tokens ? 2 : 1;
+          if (!mbar_wait(bar_q, nq & 1, abort_flag)) {
+            ok = false;
+            break;
+          }
+          ++nq;
+          tc_fence_after();
+          // tile j is at ring stages c + 2 j (K) and c + 2 j + 1 (V)
+          auto landed = [&](int stage) {
+            if (!mbar_wait(&full[stage % C::NST], (stage / C::NST) & 1, abort_flag)) return false;
             tc_fence_after();
-            m.n = n;
-            m.j = 0;
             return true;
-          }
-        };
-        // S_j = Q K_j^T of pipeline x (its previous P V has been issued, so P_{j-1} is consumed first)
-        auto issue_s = [&](int x) -> bool {
-          const Pipe P = pipe_of(smem, pieces, x);
-          State& m = st[x];
-          const int slot = m.c % C::NST;
-          if (!mbar_wait(&P.full[slot], (m.c / C::NST) & 1, abort_flag)) return false;
-          tc_fence_after();
-          const uint32_t q_base = smem_u32(P.sQ), base = smem_u32(P.sStage + slot * kStage);
+          };
+          auto issue_s = [&](int x, int j) {  // S = Q_x K_j^T
+            const uint32_t base = smem_u32(sStage + ((c + 2 * j) % C::NST) * kStage), qa = q_base + x * C::Q_BYTES;
 #pragma unroll
-          for (int ks = 0; ks < 8; ++ks) {
-            const uint32_t off = (ks >> 2) * 16384 + (ks & 3) * 32;
-            mma_ss(tmem + x * C::TM_PIPE + C::TM_S, smem_desc_sw128(q_base + off, 16, 1024),
-                   smem_desc_sw128(base + off, 16, 1024), ID_S, ks != 0);
-          }
-          mma_commit(&P.empty[slot]);
-          if (m.j == m.n - 1) mma_commit(P.q_free);
-          mma_commit(P.bar_s);
-          ++m.c;
-          return true;
-        };
-        // O += P_j V_j of pipeline x; an item's first one overwrites O, which the output before must have read
-        auto issue_pv = [&](int x) -> bool {
-          const Pipe P = pipe_of(smem, pieces, x);
-          State& m = st[x];
-          if (m.j == 0 && m.no > 0 && !mbar_wait(P.o_free, (m.no - 1) & 1, abort_flag)) return false;
-          if (!mbar_wait(P.bar_p, m.tiles & 1, abort_flag)) return false;
-          ++m.tiles;
-          const int slot = m.c % C::NST;
-          if (!mbar_wait(&P.full[slot], (m.c / C::NST) & 1, abort_flag)) return false;
-          tc_fence_after();
-          const uint32_t base = smem_u32(P.sStage + slot * kStage);
+            for (int ks = 0; ks < 8; ++ks) {
+              const uint32_t off = (ks >> 2) * 16384 + (ks & 3) * 32;
+              mma_ss(tmem + x * C::TM_HALF + C::TM_S, smem_desc_sw128(qa + off, 16, 1024),
+                     smem_desc_sw128(base + off, 16, 1024), ID_S, ks != 0);
+            }
+            mma_commit(&bar_s[x]);
+            if (x == halves - 1) {  // both halves have used K_j
+              mma_commit(&empty[(c + 2 * j) % C::NST]);
+              if (j == n - 1) mma_commit(q_free);
+            }
+          };
+          auto issue_pv = [&](int x, int j) {  // O_x += P V_j
+            const uint32_t base = smem_u32(sStage + ((c + 2 * j + 1) % C::NST) * kStage);
 #pragma unroll
-          for (int ks = 0; ks < 8; ++ks)
-            mma_ts(tmem + x * C::TM_PIPE, tmem + x * C::TM_PIPE + C::TM_S + ks * 8,
-                   smem_desc_sw128(base + ks * 2048, 16384, 1024), ID_O, (m.j | ks) != 0);
-          mma_commit(&P.empty[slot]);
-          ++m.c;
-          return true;
-        };
-        for (int x = 0; x < 2 && ok; ++x)
-          if (next_item(x) && !issue_s(x)) ok = false;
-        while (ok && !(st[0].done && st[1].done)) {
-          for (int x = 0; x < 2 && ok; ++x) {
-            State& m = st[x];
-            if (m.done) continue;
-            if (!issue_pv(x)) {
-              ok = false;
-              break;
+            for (int ks = 0; ks < 8; ++ks)
+              mma_ts(tmem + x * C::TM_HALF, tmem + x * C::TM_HALF + C::TM_S + ks * 8,
+                     smem_desc_sw128(base + ks * 2048, 16384, 1024), ID_O, (j | ks) != 0);
+            if (x == halves - 1) mma_commit(&empty[(c + 2 * j + 1) % C::NST]);
+            if (j == n - 1) mma_commit(&bar_o[x]);
+          };
+          ok = landed(c);
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+            if (ok && x < halves) issue_s(x, 0);
+          for (int j = 0; ok && j < n; ++j) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              if (!ok || x >= halves) continue;
+              // an item's first P V overwrites O, which the output before must have read
+              if (j == 0 && no[x] > 0 && !mbar_wait(&o_free[x], (no[x] - 1) & 1, abort_flag)) ok = false;
+              if (ok && !mbar_wait(&bar_p[x], pv[x] & 1, abort_flag)) ok = false;
+              ++pv[x];
+              if (!ok || !landed(c + 2 * j + 1)) {
+                ok = false;
+                continue;
+              }
+              issue_pv(x, j);
+              // the next S of this half: its P has been issued, so the columns are free behind it
+              if (j + 1 < n) {
+                ok = landed(c + 2 * j + 2);
+                if (ok) issue_s(x, j + 1);
+              } else {
+                ++no[x];
+              }
             }
-            if (m.j == m.n - 1) {
-              mma_commit(pipe_of(smem, pieces, x).bar_o);
-              ++m.no;
-              if (!next_item(x)) continue;  // out of work (or ok cleared)
-            } else {
-              ++m.j;
-            }
-            if (!issue_s(x)) ok = false;
           }
+          c += 2 * n;
         }
         if (!ok) {
           *abort_flag = 1;
@@ -313,53 +281,58 @@ __global__ void __launch_bounds__(PairCfg::THREADS, 1)
     }
   } else {
     regs_inc<C::REGS_SOFTMAX>();
-    // ------------------------------------------------------------ softmax + output of pipeline warp / 4
+    // ------------------------------------------------------------ softmax + output of half warp / 4
     const int x = warp >> 2;
-    const Pipe P = pipe_of(smem, pieces, x);
-    const int r = (warp & 3) * 32 + lane;  // row of the item, and key of a tile
-    const uint32_t lanes = tmem + x * C::TM_PIPE + ((uint32_t)((warp & 3) * 32) << 16);
+    const int r = (warp & 3) * 32 + lane;  // row of the half, and key of a tile
+    const uint32_t lanes = tmem + x * C::TM_HALF + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t scol = lanes + C::TM_S;
     const float sl2 = p.scale_log2;
-    int np = 0, tiles = 0, no = 0;
+    int np = 0, tiles = 0, no = 0, c = 0;  // pieces, tiles and items of this half, ring stages
     bool ok = true;
     while (ok) {
       const int e = np & 1;
-      if (!__all_sync(0xffffffffu, mbar_wait(&P.sched_full[e], (np >> 1) & 1, abort_flag))) {
+      if (!__all_sync(0xffffffffu, mbar_wait(&sched_full[e], (np >> 1) & 1, abort_flag))) {
         ok = false;
         break;
       }
       int lo, hi, lo_last, hi_first, kb0, n, span_lo, span_hi;
       bool valid;
       long long out_row;  // row x head of the output
-      float* part;        // this row's partial result, or nullptr: the whole item
+      float* part;        // the item's partial result, or nullptr: the whole item
+      int part_row;
       {
-        const PagedPiece w = P.pieces[e];
+        const PagedPiece w = pieces[e];
         __syncwarp();
-        mbar_arrive(&P.sched_empty[e]);
+        mbar_arrive(&sched_empty[e]);
         ++np;
         if (w.row0 < 0) break;
         const int i1 = min(w.i0 + p.tokens, w.q_len) - 1;
         const PagedSpan span = paged_span(p, PagedSeq{w.row0, w.q_len, w.kv_len}, w.i0, i1);
         const PagedUnit un = paged_unit(p, w.unit);
         const int ti = r / p.block_heads, h = r - ti * p.block_heads;
-        const int off = w.kv_len - w.q_len, i = w.i0 + ti;
-        valid = i <= i1 && h < un.heads;
-        // keys of this row's token, and of the block's last and first
+        const int h0 = w.i0 + x * half_tokens, h1 = min(i1, h0 + half_tokens - 1);  // tokens of this half
+        const int off = w.kv_len - w.q_len, i = h0 + ti;
+        n = w.j1 - w.j0;
+        if (h0 > i1) {  // none in this half
+          c += 2 * n;
+          continue;
+        }
+        valid = i <= h1 && h < un.heads;
+        // keys of this row's token, and of the half's last and first
         lo = p.window >= 0 ? max(0, i + off - p.window) : 0;
         hi = p.causal ? min(w.kv_len, max(0, i + off + 1)) : w.kv_len;
-        lo_last = p.window >= 0 ? max(0, i1 + off - p.window) : 0;
-        hi_first = p.causal ? max(0, w.i0 + off + 1) : w.kv_len;
+        lo_last = p.window >= 0 ? max(0, h1 + off - p.window) : 0;
+        hi_first = p.causal ? max(0, h0 + off + 1) : w.kv_len;
         span_lo = span.lo;
         span_hi = span.hi;
         kb0 = (span.tile0 + w.j0) * kTile;
-        n = w.j1 - w.j0;
         out_row = (long long)(w.row0 + i) * p.hq + un.head0 + h;
-        part = w.slot < 0 ? nullptr
-                          : p.parts + (long long)w.slot * (128 * 130);
+        part = w.slot < 0 ? nullptr : p.parts + (long long)w.slot * (256 * 130);
+        part_row = x * half_tokens * p.block_heads + r;
       }
       float mbs = -INFINITY, l = 0.f;  // running maximum of S * scale * log2 e, and the sum
       for (int j = 0; j < n; ++j) {
-        if (!__all_sync(0xffffffffu, mbar_wait(P.bar_s, tiles & 1, abort_flag))) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&bar_s[x], tiles & 1, abort_flag))) {
           ok = false;
           break;
         }
@@ -411,16 +384,17 @@ __global__ void __launch_bounds__(PairCfg::THREADS, 1)
           }
         }
         // keys that no row of the item sees have P = 0, but their values may be anything
-        // (unused slots): zeros in their place keep 0 x NaN out. V is in the slot behind
-        // K's, whose use before was the V that the P V before consumed.
-        if (kb < span_lo || kb + kTile > span_hi) {
-          const int cv = 2 * tiles + 1, slot = cv % C::NST;
-          if (!__all_sync(0xffffffffu, mbar_wait(&P.full[slot], (cv / C::NST) & 1, abort_flag))) {
+        // (unused slots): zeros in their place keep 0 x NaN out. The first half's warps
+        // write them, ahead of its P V and so of the second's. (The slot's use before was
+        // V of an earlier tile, which both halves were done with when this S was formed.)
+        if (x == 0 && (kb < span_lo || kb + kTile > span_hi)) {
+          const int cv = c + 2 * j + 1;
+          if (!__all_sync(0xffffffffu, mbar_wait(&full[cv % C::NST], (cv / C::NST) & 1, abort_flag))) {
             ok = false;
             break;
           }
           if (kb + r < span_lo || kb + r >= span_hi) {
-            uint8_t* v = P.sStage + slot * kStage + r * 128;
+            uint8_t* v = sStage + (cv % C::NST) * kStage + r * 128;
 #pragma unroll
             for (int y = 0; y < 16; ++y)
               *reinterpret_cast<uint4*>(v + (y >> 3) * 16384 + (((y + r) & 7) << 4)) = make_uint4(0u, 0u, 0u, 0u);
@@ -430,12 +404,13 @@ __global__ void __launch_bounds__(PairCfg::THREADS, 1)
         ++tiles;
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(P.bar_p);
+        mbar_arrive(&bar_p[x]);
       }
       if (!ok) break;
+      c += 2 * n;
       const float inv = part ? 1.f : (l == 0.f ? 0.f : 1.f / l);
       if (n > 0) {
-        if (!__all_sync(0xffffffffu, mbar_wait(P.bar_o, no & 1, abort_flag))) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&bar_o[x], no & 1, abort_flag))) {
           ok = false;
           break;
         }
@@ -454,14 +429,14 @@ __global__ void __launch_bounds__(PairCfg::THREADS, 1)
           reg_fence(u);
           if (cc == 3) {
             tc_fence_before();
-            mbar_arrive(P.o_free);
+            mbar_arrive(&o_free[x]);
           }
         } else {
 #pragma unroll
           for (int k2 = 0; k2 < 32; ++k2) u[k2] = 0u;
         }
-        if (part) {  // the same for the whole CTA's pipeline
-          float* at = part + r * 128 + cc * 32;
+        if (part) {  // the same for the whole half
+          float* at = part + part_row * 128 + cc * 32;
           if (valid && SDPA_ADDR_OK(p.chk, at, 128)) {
 #pragma unroll
             for (int k2 = 0; k2 < 8; ++k2)
@@ -494,9 +469,10 @@ __global__ void __launch_bounds__(PairCfg::THREADS, 1)
         if (!part) {
           float* at = p.lse + out_row;
           if (SDPA_ADDR_OK(p.chk, at, 4)) *at = l == 0.f ? -INFINITY : mbs * kLn2 + logf(l);
-        } else if (SDPA_ADDR_OK(p.chk, part + 128 * 128 + r, 4) && SDPA_ADDR_OK(p.chk, part + 128 * 129 + r, 4)) {
-          part[128 * 128 + r] = mbs;
-          part[128 * 129 + r] = l;
+        } else if (SDPA_ADDR_OK(p.chk, part + 256 * 128 + part_row, 4) &&
+                   SDPA_ADDR_OK(p.chk, part + 256 * 129 + part_row, 4)) {
+          part[256 * 128 + part_row] = mbs;
+          part[256 * 129 + part_row] = l;
         }
       }
     }
@@ -516,23 +492,22 @@ __global__ void __launch_bounds__(PairCfg::THREADS, 1)
 }
 
 template <bool BF16>
-int launch_pair_t(const PagedLaunch& L, int sms, int* launches) {
+int launch_pair_t(const PagedLaunch& L, int* launches) {
   auto kern = paged_pair_kernel<BF16>;
   if (const int rc = set_kernel_smem(reinterpret_cast<const void*>(kern), PairCfg::SMEM, 100)) return rc;
-  const int grid = std::min(L.workers, sms);
-  if (const int rc = launch_early(kern, dim3((unsigned)grid), PairCfg::THREADS, PairCfg::SMEM, L.stream, L.p.behind != 0,
-                                  L.tmQ, L.tmK, L.tmV, L.p, L.workers))
+  if (const int rc = launch_early(kern, dim3((unsigned)L.workers), PairCfg::THREADS, PairCfg::SMEM, L.stream,
+                                  L.p.behind != 0, L.tmQ, L.tmK, L.tmV, L.p))
     return rc;
   ++*launches;
   if (!L.p.tail) return SDPA_OK;  // no item crosses a cut
   ++*launches;
-  return launch_paged_join(L, 128, 128, L.p.tail, BF16);
+  return launch_paged_join(L, 256, 128, L.p.tail, BF16);
 }
 
 }  // namespace
 
-int launch_paged_pair(const PagedLaunch& L, int sms, bool bf16, int* launches) {
-  return bf16 ? launch_pair_t<true>(L, sms, launches) : launch_pair_t<false>(L, sms, launches);
+int launch_paged_pair(const PagedLaunch& L, bool bf16, int* launches) {
+  return bf16 ? launch_pair_t<true>(L, launches) : launch_pair_t<false>(L, launches);
 }
 
 }  // namespace sdpa
