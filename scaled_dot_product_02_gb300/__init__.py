@@ -648,7 +648,7 @@ def _norm_rope_plan(q, k, q_weight, k_weight, cos_sin, positions, q_out, k_out, 
     for name, t in (("dq_weight", dq_weight), ("dk_weight", dk_weight)):
         if t is not None:
             _expect(name, t, (d,), _torch()["f32"], dev)
-    p = NormRopeProblem(_dtype_code(dtype, "q"), hq, hkv, d, rot, 1 if interleaved else 0, eps, max_pos, rows, qs, ks,
+    p = NormRopeProblem(_dtype_code(dtype, "q"), hq, hkv, d, rot, 1 if interleaved else 0, float(eps), max_pos, rows, qs, ks,
                         *strides)
     return p, int(lib().sdpa_qk_norm_rope_bwd_workspace_size(ctypes.byref(p)))
 
@@ -754,7 +754,7 @@ def _append_plan(k, v, k_cache, v_cache, block_table, kv_lens, cu_seqlens_q, cac
         if q_weight is None or k_weight is None:
             raise ValueError("q needs q_weight and k_weight")
         max_pos, rot = _rotation(q, d, rows, q_weight, k_weight, cos_sin, positions, False)
-        n = NormRopeProblem(0, 0, 0, 0, rot, 1 if interleaved else 0, eps, max_pos)
+        n = NormRopeProblem(0, 0, 0, 0, rot, 1 if interleaved else 0, float(eps), max_pos)
         if q_out is not None:
             _expect("q_out", q_out, q[0], q[2], q[3])
     elif not (q_weight is k_weight is cos_sin is positions is q_out is None):
@@ -776,8 +776,9 @@ def _paged_plan(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens_q, max_seq
         raise ValueError(f"q must be [tokens, heads, head_dim], got {tuple(q[0])}")
     if window_right not in (-1, 0):
         raise ValueError(f"a paged window is (left, -1 or 0), got ({window_left}, {window_right})")
-    p = _paged_problem(q, hq, k_cache, v_cache, block_table, kv_lens, cu_seqlens_q, cache_layout, rows, max_seqlen_q,
-                       max_seqlen_kv, MASKS[mask], window_left, d ** -0.5 if scale is None else scale, qs, 0, 0)
+    p = _paged_problem(q, hq, k_cache, v_cache, block_table, kv_lens, cu_seqlens_q, cache_layout, rows, int(max_seqlen_q),
+                       None if max_seqlen_kv is None else int(max_seqlen_kv), MASKS[mask], int(window_left),
+                       d ** -0.5 if scale is None else float(scale), qs, 0, 0)
     if p.head_dim != d or hq % p.num_heads_kv:
         raise ValueError(f"q {tuple(q[0])} does not fit the cache {tuple(k_cache[0])} in layout {cache_layout}")
     if out is not None:

@@ -406,7 +406,8 @@ int check_paged(const sdpa_paged_problem* p) {
   if (!head_dims_supported(p->head_dim, paged_dv(p))) return SDPA_ERR_UNSUPPORTED;
   if (p->batch < 0 || p->total_q < 0 || p->seqlen_q < 0 || p->seqlen_kv < 0) return SDPA_ERR_INVALID_ARG;
   if (p->num_heads_q <= 0 || p->num_heads_kv <= 0 || p->num_heads_q % p->num_heads_kv) return SDPA_ERR_INVALID_ARG;
-  if (p->num_heads_q > 65536 || p->batch > (1 << 20)) return SDPA_ERR_UNSUPPORTED;
+  if (p->num_heads_q > 65536 || p->batch > (1 << 20) || p->seqlen_kv > (1 << 30) || p->seqlen_q > (1 << 30))
+    return SDPA_ERR_UNSUPPORTED;
   if (p->page_size <= 0 || p->num_pages <= 0 || p->max_pages <= 0) return SDPA_ERR_INVALID_ARG;
   if (p->page_size % 16 || p->page_size > (1 << 20)) return SDPA_ERR_UNSUPPORTED;
   if ((long long)p->max_pages * p->page_size < p->seqlen_kv) return SDPA_ERR_INVALID_ARG;
@@ -1318,7 +1319,7 @@ int sdpa_paged_fwd(const sdpa_paged_problem* p, const void* q, const void* k_cac
     P.tail = c->tail;
     P.q_box_rows = c->q_tokens * c->block_heads;
     P.causal = p->mask_type != SDPA_MASK_NONE;
-    P.window = p->window_left;
+    P.window = p->window_left < p->seqlen_kv ? p->window_left : -1;  // as wide as every length: no window
     P.scale_log2 = p->softmax_scale * 1.4426950408889634f;
     P.page_size = p->page_size;
     P.num_pages = p->num_pages;

@@ -372,11 +372,12 @@ __global__ void __launch_bounds__(256, 1)
           tmem_cols<N>(lanes + C::TM_S + (sj & 1) * N, s);
           // the rows that see this thread's key: [r_lo, r_hi). Row r is head r % block_heads of token r / block_heads
           const int kb = (w.span.tile0 + w.j0 + j) * kTile, key = kb + tid;
-          int r_lo = 0, r_hi = key < w.span.hi ? rows : 0;
+          int t_lo = 0, t_hi = key < w.span.hi ? tok : 0;
           if (p.causal) {
-            r_lo = min(rows, max(0, key - off - w.i0) * p.block_heads);
-            if (p.window >= 0) r_hi = min(r_hi, max(0, key - off + p.window - w.i0 + 1) * p.block_heads);
+            t_lo = min(tok, max(0, key - off - w.i0));
+            if (p.window >= 0) t_hi = min(t_hi, max(0, key - off + p.window - w.i0 + 1));
           }
+          const int r_lo = t_lo * p.block_heads, r_hi = t_hi * p.block_heads;
           const unsigned span = max(0, r_hi - r_lo);
 #pragma unroll
           for (int i = 0; i < N; ++i) s[i] = (unsigned)(i - r_lo) < span ? s[i] * sl2 : -INFINITY;

@@ -99,7 +99,7 @@ def test_lengths(batch, d, page, order, dtype):
     assert bool((out[-2:] == 9).all()) and bool((lse[-2:] == 9).all())  # rows behind the last sequence
 
 
-@pytest.mark.parametrize("hq,hkv", [(1, 1), (4, 4), (14, 2), (32, 8), (16, 1), (40, 1), (80, 1), (33, 1), (96, 2)])
+@pytest.mark.parametrize("hq,hkv", [(1, 1), (4, 4), (14, 2), (32, 8), (16, 1), (40, 1), (80, 1), (33, 1), (96, 2), (200, 1)])
 @pytest.mark.parametrize("d", [128, 192, 256, 512])
 def test_head_groups(hq, hkv, d):
     for new, total in (([1, 1, 1], [5, 200, 700]), ([9, 2], [140, 300])):
@@ -107,7 +107,7 @@ def test_head_groups(hq, hkv, d):
         check(c, *call(c))
 
 
-@pytest.mark.parametrize("window", [0, 5, 127, 128, 300, 5000])
+@pytest.mark.parametrize("window", [0, 5, 127, 128, 300, 5000, 2 ** 31 - 1])
 @pytest.mark.parametrize("d,page,order", DIMS[:4])
 def test_windows(window, d, page, order):
     for name in ("ragged", "chunk", "spec"):
@@ -248,6 +248,33 @@ def test_captured_calls_follow_the_lengths_and_share_a_workspace():
         torch.cuda.synchronize()
         check(c, *a)
         check(e, *b)
+
+
+def test_two_calls_at_once_on_two_streams():
+    c = case([60, 1, 5], [900, 2000, 300], pad=1)
+    e = case([1, 3, 200], [1500, 700, 800], d=256, page=64, order="hnd")
+    streams = torch.cuda.Stream(), torch.cuda.Stream()
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = [(call(c, stream=streams[0]), call(e, stream=streams[1])) for _ in range(10)]
+    torch.cuda.synchronize()
+    for a, b in got:
+        assert torch.equal(a[0][:-1], got[0][0][0][:-1]) and torch.equal(b[0], got[0][1][0])
+    check(c, *got[-1][0])
+    check(e, *got[-1][1])
+
+
+def test_a_mixed_call_is_timed_and_follows_other_work():
+    """Events around its launches, which then run strictly in turn; and calls back to back on one workspace."""
+    c = case([90, 1, 0, 2], [500, 1200, 7, 300])
+    ws = torch.empty(sdpa.PAGED_WORKSPACE_MAX, dtype=torch.uint8, device="cuda")
+    sdpa.sdpa_profile_begin()
+    a = call(c, workspace=ws)
+    kinds = sdpa.sdpa_profile_end()
+    assert kinds["paged"][1] >= 1 and kinds["paged"][0] > 0
+    check(c, *a)
+    keep = [call(c, workspace=ws) for _ in range(20)]
+    assert all(torch.equal(x[0], a[0]) and torch.equal(x[1], a[1]) for x in keep)
 
 
 def test_another_stream():

@@ -105,7 +105,8 @@ def test_paged_refusals():
                       (dict(max_pages=62), 1), (dict(table_stride=10), 1), (dict(mask_type=1), 2), (dict(mask_type=3), 1),
                       (dict(window_left=-2), 1), (dict(mask_type=0, window_left=5), 2), (dict(softmax_scale=-1.0), 1),
                       (dict(softmax_scale=float("inf")), 1), (dict(k_slot_stride=100), 1), (dict(v_head_stride=132), 1),
-                      (dict(k_page_stride=0), 1), (dict(q_stride=512), 1), (dict(k_stride=260), 1)):
+                      (dict(k_page_stride=0), 1), (dict(q_stride=512), 1),
+                      (dict(seqlen_kv=(1 << 30) + 1, max_pages=1 << 27), 2), (dict(batch=(1 << 20) + 1), 2), (dict(k_stride=260), 1)):
         assert check(**bad) == code, bad
 
 
