@@ -572,6 +572,85 @@ def merge_arm(args, w, inp):
         print(json.dumps(line), flush=True)
 
 
+def paged_arm(args, w, inp):
+    """One decoding step of a layer: every sequence of the workload (its key
+    lengths) gets a token, whose q and k are normed, rotated and, with v,
+    appended to a paged cache (sdpa_paged_append), and which then attends to
+    all of it (sdpa_paged_fwd). Memory-bound: prints its own JSON line (GB/s of
+    the keys and values read, against the measured HBM copy bandwidth)."""
+    import torch
+
+    import scaled_dot_product_02_gb300 as sdpa
+
+    world, rank, local = rank_env()
+    torch.cuda.set_device(local)
+    dev = torch.device("cuda", local)
+    lens = np.asarray(seq_lengths(w, inp)[1], dtype=np.int64)
+    n, page, d, dv = len(lens), 64, w.head_dim, w.dv
+    dt = torch.bfloat16 if w.dtype == "bf16" else torch.float16
+    g = torch.Generator(device=dev)
+    g.manual_seed(2025)
+    rnd = lambda *s: torch.randn(s, device=dev, generator=g).to(dt)  # noqa: E731
+    need = -(-lens // page)
+    ids = np.random.default_rng(2025).permutation(int(need.sum())).astype(np.int32)
+    table = np.full((n, int(need.max())), -1, dtype=np.int32)
+    for b, at in enumerate(np.cumsum(need) - need):
+        table[b, :need[b]] = ids[at:at + need[b]]
+    table = torch.from_numpy(table).to(dev)
+    kv_lens = torch.from_numpy(lens.astype(np.int32)).to(dev)
+    cu = torch.arange(n + 1, dtype=torch.int32, device=dev)
+    kc, vc = rnd(len(ids), page, w.heads_kv, d), rnd(len(ids), page, w.heads_kv, dv)
+    q, k, v = rnd(n, w.heads_q, d), rnd(n, w.heads_kv, d), rnd(n, w.heads_kv, dv)
+    qw, kw = 1 + 0.1 * rnd(d), 1 + 0.1 * rnd(d)
+    angle = torch.arange(int(lens.max()), device=dev, dtype=torch.float64)[:, None] * 10000.0 ** (
+        -torch.arange(0, d, 2, device=dev, dtype=torch.float64) / d)
+    cos_sin = torch.cat([angle.cos(), angle.sin()], dim=1).float().contiguous()
+    q_out, out = torch.empty_like(q), torch.empty((n, w.heads_q, dv), dtype=dt, device=dev)
+    lse = torch.empty((n, w.heads_q), device=dev)
+    ws = torch.empty(sdpa.PAGED_WORKSPACE_MAX, dtype=torch.uint8, device=dev)
+    flush = torch.empty(256 << 20, dtype=torch.uint8, device=dev)
+
+    def step():
+        sdpa.sdpa_paged_append(k, v, kc, vc, table, kv_lens, cu, q=q, q_weight=qw, k_weight=kw, cos_sin=cos_sin, q_out=q_out)
+        launches = sdpa.sdpa_last_launch_count()
+        sdpa.sdpa_paged_fwd(q_out, kc, vc, table, kv_lens, cu, max_seqlen_q=1, max_seqlen_kv=int(lens.max()), scale=w.scale,
+                            out=out, lse=lse, workspace=ws)
+        return launches + sdpa.sdpa_last_launch_count()
+
+    for _ in range(args.warmup):
+        step()
+    torch.cuda.synchronize()
+    starts = [torch.cuda.Event(enable_timing=True) for _ in range(args.steps)]
+    ends = [torch.cuda.Event(enable_timing=True) for _ in range(args.steps)]
+    clocks = ClockSampler(local)
+    clocks.start()
+    launches = 0
+    for i in range(args.steps):
+        flush.fill_(i & 255)
+        starts[i].record()
+        launches += step()
+        ends[i].record()
+    torch.cuda.synchronize()
+    clk = clocks.stop()
+    if sdpa.sdpa_get_device_error() != 0:
+        raise RuntimeError("device error during the decoding steps")
+    ms = sum(a.elapsed_time(b) for a, b in zip(starts, ends)) / args.steps
+    (ms,) = max_over_ranks([ms], world, device=dev)
+    nbytes = int(lens.sum()) * w.heads_kv * (d + dv) * 2
+    gbs = nbytes / (ms * 1e-3) / 1e9
+    pk, pk_kind = peaks()
+    line = {"metric": "decoding step over a paged cache (append + attention), GB/s", "value": world * gbs, "unit": "GB/s",
+            "n_gpus": world, "steps": args.steps, "warmup": args.warmup, "ms_per_step": ms, "higher_is_better": True,
+            "scaling": "weak", "vs_baseline": None, "dtype": w.dtype, "data": "synthetic",
+            "config": {"workload": f"paged_decode_{w.name}", "sequences": n, "keys": int(lens.sum()), "page_size": page,
+                       "bytes_per_step": nbytes, "l2": "flushed between timed steps (256 MiB write)"},
+            "clocks": clk, "gpu_launches": launches,
+            "roofline": {"bound": "hbm", "kernel": "paged_rows_kernel", "achieved": gbs, "peak": pk["hbm_gbs"],
+                         "unit": "GB/s", "frac": gbs / pk["hbm_gbs"], "traffic": None, "peak_source": f"{pk_kind} hbm_gbs"}}
+    if rank == 0:
+        print(json.dumps(line), flush=True)
+
+
 def companion_measure(w, steps, warmup, dev, flush, peak):
     """Forward and backward of a second workload, timed in the same process
     the same way (CUDA events around each step, L2 flushed between steps,
@@ -821,10 +900,11 @@ def main():
     ap.add_argument("--impl", default="ours", choices=["ours", "reference"])
     ap.add_argument("--workload", default="varlen_thd_gqa", choices=[w.name for w in workloads.ALL])
     ap.add_argument("--no-cpu-baseline", action="store_true")
-    ap.add_argument("--op", default="step", choices=["step", "fwd", "merge", "fp8"],
+    ap.add_argument("--op", default="step", choices=["step", "fwd", "merge", "fp8", "paged"],
                     help="step: the fwd+bwd hot path (the headline; the forward alone for forward-only "
                          "workloads); fwd: the forward alone; merge: the LSE merge of key-split results; "
-                         "fp8: the FP8 E4M3 forward (head_dim 128 or 256 workloads)")
+                         "fp8: the FP8 E4M3 forward (head_dim 128 or 256 workloads); paged: a decoding step "
+                         "over a paged cache (append + attention)")
     ap.add_argument("--merge-parts", type=int, default=4)
     ap.add_argument("--kv-chunk", type=int, default=0,
                     help="head_dim 256/512 backward: key positions per chunk (multiple of 128; 0 = library choice)")
@@ -839,6 +919,8 @@ def main():
     inp = workloads.make_inputs(w)
     if args.op == "merge":
         merge_arm(args, w, inp)
+    elif args.op == "paged" and args.impl == "ours":
+        paged_arm(args, w, inp)
     elif args.op == "fp8" and args.impl == "ours":
         fp8_arm(args, w, inp)
     elif args.impl == "reference":

@@ -489,7 +489,7 @@ PagedCutting paged_cutting(const sdpa_paged_problem* p, int n, int q_rows, int m
     // rounds: D192 643 -> 580 us, D512 1244 -> 1125 us; at head_dim 128, 2048 over 131072, 1.7 rounds: 2856 -> 2708
     // us, but 8 x 512 over 4096 to 8192, 3.4 rounds: 285 -> 306 us).
     c.split = false;
-    c.tail = tiles >= 48 && items < (n == 256 ? 2 : 6) * most ? 2 * most : 0;
+    c.tail = tiles >= (n == 256 ? 256 : 48) && items < (n == 256 ? 2 : 6) * most ? 2 * most : 0;
   }
   // the length of a block and the ticket counter are 32-bit numbers
   c.fits = (long long)p->num_heads_kv * c.head_blocks * c.dv_splits * std::max(tiles, 1LL) < (1LL << 31) &&

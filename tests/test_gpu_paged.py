@@ -338,7 +338,7 @@ def test_ticket_order_of_many_sequences(d, n):
                                        ([64, 200, 0, 3], [10, 0, 0, 1000])])
 def test_the_last_items_cut_into_shares(d, hq, hkv, new, total):
     """Long contexts (by their bound) of few items: with no, one and several rounds of whole items before the rest."""
-    c = case(new, total, hq=hq, hkv=hkv, d=d, page=64, max_kv=7000)
+    c = case(new, total, hq=hq, hkv=hkv, d=d, page=64, max_kv=33000 if d == 128 else 7000)
     a, b = call(c), call(c)
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])  # the shares do not depend on who takes them
     check(c, *a)
