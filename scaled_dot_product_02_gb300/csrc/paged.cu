@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(256, 1)
   }
   tc_fence_before();
   const int me = blockIdx.x;
-  const PagedShares all = paged_scan<C::THREADS>(p, scan, me, 1, 1, gridDim.x);
+  const PagedShares all = paged_scan<C::THREADS, true>(p, scan, me, gridDim.x);
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
   if (threadIdx.x == 0 && me == 0) {
@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(256, 1)
   }
 
   if (me < min((long long)gridDim.x, all.total)) {
-    PagedWalk w = scan->start[0];
+    PagedWalk w = scan->start;
     const long long u0 = w.u;
     if (threadIdx.x == 0) {
       PagedCut* cut = p.cuts + me;

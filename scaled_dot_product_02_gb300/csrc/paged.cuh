@@ -193,16 +193,14 @@ struct PagedShares {
   bool fit;           // every sequence fits what the host was told
   long long total;    // length of all items end to end (0 unless they fit)
 };
-struct PagedScan {    // shared memory of the scan: sums, and the walks as their shares start
+struct PagedScan {    // shared memory of the scan: sums, and the walk as the share starts
   long long warp_sum[16];
-  PagedWalk start[2];
+  PagedWalk start;
 };
-// Adds up all sequences and finds the blocks of tokens in which the shares of
-// workers w0, w0 + step, ... (n_w of them, at most two) start. All THREADS
-// threads call it.
-template <int THREADS>
-__device__ __forceinline__ PagedShares paged_scan(const PagedParams& p, PagedScan* sc, int w0, int step, int n_w,
-                                                  int most_workers) {
+// Adds up all sequences and, with LOCATE, finds the block of tokens in which the
+// share of worker w of at most most_workers starts. All THREADS threads call it.
+template <int THREADS, bool LOCATE>
+__device__ __forceinline__ PagedShares paged_scan(const PagedParams& p, PagedScan* sc, int w = 0, int most_workers = 1) {
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int per = (p.batch + THREADS - 1) / THREADS;  // thread t takes sequences [t per, (t + 1) per)
   const int b_lo = min(p.batch, (int)threadIdx.x * per), b_hi = min(p.batch, b_lo + per);
@@ -233,12 +231,9 @@ __device__ __forceinline__ PagedShares paged_scan(const PagedParams& p, PagedSca
   }
   if (!r.fit) r.total = 0;
   const PagedShare share(r.total, most_workers);
-  for (int x = 0; x < n_w; ++x) {
-    const int w = w0 + x * step;
-    if (w >= share.workers) break;
-    const long long u = share.at(w);
-    if (u < before || u >= before + own) continue;  // one thread: the share starts in its sequences
-    PagedWalk& k = sc->start[x];
+  const long long u = LOCATE && w < share.workers ? share.at(w) : -1;
+  if (LOCATE && u >= before && u < before + own) {  // one thread: the share starts in its sequences
+    PagedWalk& k = sc->start;
     k.u = u;
     k.u_end = share.at(w + 1);
     k.b = b_lo;

@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(256, 1)
   }
   tc_fence_before();
   const int me = blockIdx.x;
-  const PagedShares all = paged_scan<C::THREADS>(p, scan, me, 1, 0, gridDim.x);
+  const PagedShares all = paged_scan<C::THREADS, false>(p, scan);
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
   if (threadIdx.x == 0 && me == 0 && !all.fit) record_error(p.err, SDPA_ERR_BAD_SEQLENS);

@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(PairCfg::THREADS, 1)
     tmem_relinquish();
   }
   tc_fence_before();
-  const PagedShares all = paged_scan<C::THREADS>(p, scan, 0, 0, 0, 1);
+  const PagedShares all = paged_scan<C::THREADS, false>(p, scan);
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
   if (threadIdx.x == 0 && blockIdx.x == 0 && !all.fit) record_error(p.err, SDPA_ERR_BAD_SEQLENS);
