@@ -589,18 +589,19 @@ def _rows_of_heads(name, meta, like=None):
     if len(shape) < 3:
         raise ValueError(f"{name} must have at least 3 dimensions [..., heads, head_dim], got {tuple(shape)}")
     h, d = shape[-2], shape[-1]
-    rows, step, spaced = 1, 0, st[-1] == 1 and (st[-2] == d or h == 1)
+    rows, step, spaced = 1, None, st[-1] == 1 and (st[-2] == d or h == 1)
     for n, s in zip(reversed(shape[:-2]), reversed(st[:-2])):
         if n != 1:
-            if not step:
+            if step is None:
                 step = s
+                spaced = spaced and s >= h * d  # broadcast rows too: the C entry takes a stride of zero for contiguous
             elif s != rows * step:
                 spaced = False
             rows *= n
     if rows and not spaced:
         raise ValueError(f"{name} must hold contiguous heads in evenly spaced rows, got shape {tuple(shape)} and "
                          f"strides {tuple(st)}")
-    return rows, h, d, step if step and rows else h * d
+    return rows, h, d, step if step is not None and rows else h * d
 
 
 def _rotation(q, d, rows, q_weight, k_weight, cos_sin, positions, needs_positions):
@@ -722,8 +723,10 @@ def _paged_problem(q, hq, k_cache, v_cache, block_table, kv_lens, cu_seqlens_q, 
     if ks[:3] != vs[:3]:
         raise ValueError(f"k_cache and v_cache must agree on every dimension but the last, got {tuple(ks)} and {tuple(vs)}")
     tab, tab_st, tab_dtype, tab_dev = block_table
-    if len(tab) != 2 or tab_dtype is not i32 or tab_dev != dev or (tab[1] > 1 and tab_st[1] != 1):
-        raise ValueError(f"block_table must be a 2-D int32 [batch, pages] tensor on {dev} with contiguous rows")
+    if (len(tab) != 2 or tab_dtype is not i32 or tab_dev != dev or (tab[1] > 1 and tab_st[1] != 1)
+            or (tab[0] > 1 and tab_st[0] < tab[1])):  # an expanded row too: a stride of zero stands for contiguous rows
+        raise ValueError(f"block_table must be a 2-D int32 [batch, pages] tensor on {dev} with contiguous rows that do "
+                         "not overlap")
     batch, max_pages = tab
     _expect("kv_lens", kv_lens, (batch,), i32, dev)
     _expect("cu_seqlens_q", cu_seqlens_q, (batch + 1,), i32, dev)

@@ -220,3 +220,55 @@ def test_binding_refuses_what_does_not_fit():
 
 def test_new_error_has_a_string():
     assert "table" in sdpa.error_string(10)
+
+
+# ---- calls from Python
+
+def _batch(tokens=6, batch=3, dtype=torch.bfloat16):
+    return dict(q=torch.zeros(tokens, 4, 128, dtype=dtype), k=torch.zeros(tokens, 2, 128, dtype=dtype),
+                v=torch.zeros(tokens, 2, 128, dtype=dtype), kc=torch.zeros(8, 16, 2, 128, dtype=dtype),
+                vc=torch.zeros(8, 16, 2, 128, dtype=dtype), table=torch.zeros(batch, 4, dtype=torch.int32),
+                lens=torch.full((batch,), 2, dtype=torch.int32),
+                cu=torch.arange(batch + 1, dtype=torch.int32) * (tokens // batch), w=torch.ones(128, dtype=dtype))
+
+
+def _paged(c, **kw):
+    return sdpa.sdpa_paged_fwd(c["q"], c["kc"], c["vc"], c["table"], c["lens"], c["cu"], **{"max_seqlen_q": 2, **kw})
+
+
+@pytest.mark.parametrize("lead", [(6,), (2, 3), (1, 6)])
+@pytest.mark.parametrize("dim", [0, -1])
+def test_broadcast_tokens_are_refused(lead, dim):
+    """A stride of zero in C stands for contiguous rows: an expanded tensor holds fewer rows than that."""
+    one = list(lead)
+    one[dim if dim == 0 and lead[0] > 1 else -1] = 1
+    wide, w = torch.zeros(*lead, 4, 128, dtype=torch.bfloat16), torch.ones(128, dtype=torch.bfloat16)
+    thin = torch.zeros(*one, 4, 128, dtype=torch.bfloat16).expand(*lead, 4, 128)
+    for q, k in ((thin, wide), (wide, thin)):
+        with pytest.raises(ValueError, match="evenly spaced rows"):
+            sdpa.sdpa_qk_norm_rope(q, k, w, w)
+        with pytest.raises(ValueError, match="evenly spaced rows"):
+            sdpa.sdpa_qk_norm_rope_bwd(wide, wide, q, k, w, w)
+    with pytest.raises(ValueError, match="evenly spaced rows"):
+        sdpa.sdpa_qk_norm_rope_bwd(wide, wide, wide, wide, w, w, dq=thin)
+
+
+@pytest.mark.parametrize("name", ["q", "k", "v"])
+def test_broadcast_tokens_of_a_batch_are_refused(name):
+    c = _batch()
+    c[name] = c[name][:1].expand(6, -1, -1)
+    with pytest.raises(ValueError, match="evenly spaced rows"):
+        if name == "q":
+            _paged(c)
+        sdpa.sdpa_paged_append(c["k"], c["v"], c["kc"], c["vc"], c["table"], c["lens"], c["cu"])
+
+
+@pytest.mark.parametrize("shape", ["expanded", "overlapping"])
+def test_a_block_table_whose_rows_overlap_is_refused(shape):
+    c = _batch()
+    c["table"] = (torch.zeros(1, 4, dtype=torch.int32).expand(3, 4) if shape == "expanded"
+                  else torch.zeros(8, dtype=torch.int32).as_strided((3, 4), (2, 1)))
+    with pytest.raises(ValueError, match="block_table"):
+        _paged(c)
+    with pytest.raises(ValueError, match="block_table"):
+        sdpa.sdpa_paged_append(c["k"], c["v"], c["kc"], c["vc"], c["table"], c["lens"], c["cu"])
