@@ -505,7 +505,8 @@ def sdpa_merge(o_parts, lse_parts, *, out=None, lse=None, stream=None):
 # The checks below depend on the tensors' metadata alone, so they are made once
 # per combination of it (_meta is the key) and kept, with the problem struct that
 # they lead to: a decoding step repeats its calls with the same shapes, and the
-# checks took longer than the kernels. Nothing is kept by address or contents.
+# checks took longer than the kernels. Nothing is kept by address or contents
+# (scalars are turned into numbers before: a tensor's key would be its identity).
 _torch_state = {}  # what the calls take from torch, looked up once
 _PLANS = 512       # combinations kept per entry point
 
@@ -649,7 +650,7 @@ def _norm_rope_plan(q, k, q_weight, k_weight, cos_sin, positions, q_out, k_out, 
     for name, t in (("dq_weight", dq_weight), ("dk_weight", dk_weight)):
         if t is not None:
             _expect(name, t, (d,), _torch()["f32"], dev)
-    p = NormRopeProblem(_dtype_code(dtype, "q"), hq, hkv, d, rot, 1 if interleaved else 0, float(eps), max_pos, rows, qs, ks,
+    p = NormRopeProblem(_dtype_code(dtype, "q"), hq, hkv, d, rot, 1 if interleaved else 0, eps, max_pos, rows, qs, ks,
                         *strides)
     return p, int(lib().sdpa_qk_norm_rope_bwd_workspace_size(ctypes.byref(p)))
 
@@ -664,7 +665,7 @@ def sdpa_qk_norm_rope(q, k, q_weight, k_weight, cos_sin=None, positions=None, *,
     None for the norm alone; positions: int32, one per token. Returns
     contiguous (q_out, k_out)."""
     p, _ = _norm_rope_plan(_meta(q), _meta(k), _meta(q_weight), _meta(k_weight), _meta(cos_sin), _meta(positions),
-                           _meta(q_out), _meta(k_out), None, None, None, None, None, None, eps, interleaved)
+                           _meta(q_out), _meta(k_out), None, None, None, None, None, None, float(eps), bool(interleaved))
     _refuse_cpu(q)
     like = _torch_state["like"]
     if q_out is None:
@@ -685,7 +686,7 @@ def sdpa_qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, cos_sin=None
     reproducible."""
     p, need = _norm_rope_plan(_meta(q), _meta(k), _meta(q_weight), _meta(k_weight), _meta(cos_sin), _meta(positions),
                               None, None, _meta(dq), _meta(dk), _meta(dq_out), _meta(dk_out), _meta(dq_weight),
-                              _meta(dk_weight), eps, interleaved)
+                              _meta(dk_weight), float(eps), bool(interleaved))
     _refuse_cpu(q)
     dev, f32 = q.device, _torch_state["f32"]
     like = _torch_state["like"]
@@ -757,7 +758,7 @@ def _append_plan(k, v, k_cache, v_cache, block_table, kv_lens, cu_seqlens_q, cac
         if q_weight is None or k_weight is None:
             raise ValueError("q needs q_weight and k_weight")
         max_pos, rot = _rotation(q, d, rows, q_weight, k_weight, cos_sin, positions, False)
-        n = NormRopeProblem(0, 0, 0, 0, rot, 1 if interleaved else 0, float(eps), max_pos)
+        n = NormRopeProblem(0, 0, 0, 0, rot, 1 if interleaved else 0, eps, max_pos)
         if q_out is not None:
             _expect("q_out", q_out, q[0], q[2], q[3])
     elif not (q_weight is k_weight is cos_sin is positions is q_out is None):
@@ -779,9 +780,8 @@ def _paged_plan(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens_q, max_seq
         raise ValueError(f"q must be [tokens, heads, head_dim], got {tuple(q[0])}")
     if window_right not in (-1, 0):
         raise ValueError(f"a paged window is (left, -1 or 0), got ({window_left}, {window_right})")
-    p = _paged_problem(q, hq, k_cache, v_cache, block_table, kv_lens, cu_seqlens_q, cache_layout, rows, int(max_seqlen_q),
-                       None if max_seqlen_kv is None else int(max_seqlen_kv), MASKS[mask], int(window_left),
-                       d ** -0.5 if scale is None else float(scale), qs, 0, 0)
+    p = _paged_problem(q, hq, k_cache, v_cache, block_table, kv_lens, cu_seqlens_q, cache_layout, rows, max_seqlen_q,
+                       max_seqlen_kv, MASKS[mask], window_left, d ** -0.5 if scale is None else scale, qs, 0, 0)
     if p.head_dim != d or hq % p.num_heads_kv:
         raise ValueError(f"q {tuple(q[0])} does not fit the cache {tuple(k_cache[0])} in layout {cache_layout}")
     if out is not None:
@@ -806,7 +806,7 @@ def sdpa_paged_append(k, v, k_cache, v_cache, block_table, kv_lens, cu_seqlens_q
     (None without q). k, v and q may be slices of one projection's output."""
     p, n = _append_plan(_meta(k), _meta(v), _meta(k_cache), _meta(v_cache), _meta(block_table), _meta(kv_lens),
                         _meta(cu_seqlens_q), cache_layout, _meta(q), _meta(q_weight), _meta(k_weight), _meta(cos_sin),
-                        _meta(positions), _meta(q_out), eps, interleaved)
+                        _meta(positions), _meta(q_out), float(eps), bool(interleaved))
     _refuse_cpu(k)
     if q is not None and q_out is None:
         q_out = _torch_state["like"](q)
@@ -834,7 +834,8 @@ def sdpa_paged_fwd(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens_q, *, m
     [T, Hq]); rows behind the last sequence are left as they are. A workspace
     of PAGED_WORKSPACE_MAX bytes serves every shape."""
     p, need = _paged_plan(_meta(q), _meta(k_cache), _meta(v_cache), _meta(block_table), _meta(kv_lens),
-                          _meta(cu_seqlens_q), max_seqlen_q, max_seqlen_kv, cache_layout, mask, window[0], window[1], scale,
+                          _meta(cu_seqlens_q), int(max_seqlen_q), None if max_seqlen_kv is None else int(max_seqlen_kv),
+                          cache_layout, mask, int(window[0]), int(window[1]), None if scale is None else float(scale),
                           _meta(out), _meta(lse))
     _refuse_cpu(q)
     dev = q.device

@@ -272,3 +272,21 @@ def test_a_block_table_whose_rows_overlap_is_refused(shape):
         _paged(c)
     with pytest.raises(ValueError, match="block_table"):
         sdpa.sdpa_paged_append(c["k"], c["v"], c["kc"], c["vc"], c["table"], c["lens"], c["cu"])
+
+def test_scalars_given_as_tensors_are_read_on_every_call(monkeypatch):
+    seen = []
+    monkeypatch.setattr(sdpa, "_refuse_cpu", lambda t: None)
+    monkeypatch.setattr(sdpa, "_launch", lambda name, device, *args: seen.append(
+        next(a._obj for a in args if hasattr(a, "_obj"))))
+    c = _batch()
+    most, scale, left = torch.tensor(2), torch.tensor(0.5), torch.tensor(4)
+    for n in (2, 5):
+        most.fill_(n), scale.fill_(n / 4), left.fill_(n + 8)
+        _paged(c, max_seqlen_q=most, max_seqlen_kv=most, scale=scale, window=(left, 0))
+        p = seen.pop()
+        assert (p.seqlen_q, p.seqlen_kv, p.softmax_scale, p.window_left) == (n, n, n / 4, n + 8)
+    eps = torch.tensor(0.25)
+    for e in (0.25, 0.5):
+        eps.fill_(e)
+        sdpa.sdpa_qk_norm_rope(c["q"], c["k"], c["w"], c["w"], eps=eps)
+        assert seen.pop().eps == e
