@@ -533,19 +533,35 @@ def _dtype_code(dtype, name):
     return code
 
 
-def _launch(name, device, stream, *args):
-    """Call the entry point `name` with the stream's raw handle appended and
-    `device` current: it launches on the calling thread's current device, so
-    tensors of another one select theirs for the call. stream: a torch stream
-    of that device, or None for its current one."""
+def _on(stream, entry, args):
+    """entry(**args) with `stream` current, as torch's own operators run on a
+    stream: the workspace and the outputs are allocated on it (from the current
+    stream's memory the workspace would be handed out again while the kernels
+    use it). Memory of other streams that the call uses, and what it returns to
+    the calling stream, is kept until both are done with it."""
+    torch = _torch()["torch"]
+    tensors = [t for t in args.values() if isinstance(t, torch.Tensor)]
+    for t in tensors:
+        if t.device != stream.device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {t.device}")
+    caller = torch.cuda.current_stream(stream.device)
+    with torch.cuda.stream(stream):
+        got = entry(**{**args, "stream": None})
+    for t in tensors:
+        t.record_stream(stream)
+    for t in got if isinstance(got, tuple) else (got,):
+        if t is not None:
+            t.record_stream(caller)
+    return got
+
+
+def _launch(name, device, *args):
+    """Call the entry point `name` with the raw handle of the device's current
+    stream appended and `device` current: it launches on the calling thread's
+    current device, so tensors of another one select theirs for the call."""
     torch = _torch_state["torch"]
     index = device.index
-    if stream is None:
-        raw = _torch_state["raw"](index)
-    elif stream.device != device:
-        raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
-    else:
-        raw = stream.cuda_stream
+    raw = _torch_state["raw"](index)
     if index == torch.cuda.current_device():
         rc = getattr(lib(), name)(*args, raw)
     else:
@@ -664,6 +680,8 @@ def sdpa_qk_norm_rope(q, k, q_weight, k_weight, cos_sin=None, positions=None, *,
     cos_sin: float32 [positions, rotary_dim], half cosines and half sines, or
     None for the norm alone; positions: int32, one per token. Returns
     contiguous (q_out, k_out)."""
+    if stream is not None:
+        return _on(stream, sdpa_qk_norm_rope, locals())
     p, _ = _norm_rope_plan(_meta(q), _meta(k), _meta(q_weight), _meta(k_weight), _meta(cos_sin), _meta(positions),
                            _meta(q_out), _meta(k_out), None, None, None, None, None, None, float(eps), bool(interleaved))
     _refuse_cpu(q)
@@ -672,7 +690,7 @@ def sdpa_qk_norm_rope(q, k, q_weight, k_weight, cos_sin=None, positions=None, *,
         q_out = like(q)
     if k_out is None:
         k_out = like(k)
-    _launch("sdpa_qk_norm_rope", q.device, stream, ctypes.byref(p), q.data_ptr(), k.data_ptr(), q_weight.data_ptr(),
+    _launch("sdpa_qk_norm_rope", q.device, ctypes.byref(p), q.data_ptr(), k.data_ptr(), q_weight.data_ptr(),
             k_weight.data_ptr(), _addr(cos_sin), _addr(positions), q_out.data_ptr(), k_out.data_ptr())
     return q_out, k_out
 
@@ -684,6 +702,8 @@ def sdpa_qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, cos_sin=None
     outputs and its inputs, returns (dq, dk, dq_weight, dk_weight), the weights'
     in float32. dq and dk may be slices of one fused gradient's rows. Bitwise
     reproducible."""
+    if stream is not None:
+        return _on(stream, sdpa_qk_norm_rope_bwd, locals())
     p, need = _norm_rope_plan(_meta(q), _meta(k), _meta(q_weight), _meta(k_weight), _meta(cos_sin), _meta(positions),
                               None, None, _meta(dq), _meta(dk), _meta(dq_out), _meta(dk_out), _meta(dq_weight),
                               _meta(dk_weight), float(eps), bool(interleaved))
@@ -698,7 +718,7 @@ def sdpa_qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, cos_sin=None
         workspace = dq_weight.new_empty(max(need // 4, 4))
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {dev}")
-    _launch("sdpa_qk_norm_rope_bwd", dev, stream, ctypes.byref(p), dq_out.data_ptr(), dk_out.data_ptr(), q.data_ptr(),
+    _launch("sdpa_qk_norm_rope_bwd", dev, ctypes.byref(p), dq_out.data_ptr(), dk_out.data_ptr(), q.data_ptr(),
             k.data_ptr(), q_weight.data_ptr(), k_weight.data_ptr(), _addr(cos_sin), _addr(positions), dq.data_ptr(),
             dk.data_ptr(), dq_weight.data_ptr(), dk_weight.data_ptr(), workspace.data_ptr(), workspace.nbytes)
     return dq, dk, dq_weight, dk_weight
@@ -804,13 +824,15 @@ def sdpa_paged_append(k, v, k_cache, v_cache, block_table, kv_lens, cu_seqlens_q
     normed and rotated on its way into the cache and q into q_out, as by
     sdpa_qk_norm_rope; positions default to the cache positions. Returns q_out
     (None without q). k, v and q may be slices of one projection's output."""
+    if stream is not None:
+        return _on(stream, sdpa_paged_append, locals())
     p, n = _append_plan(_meta(k), _meta(v), _meta(k_cache), _meta(v_cache), _meta(block_table), _meta(kv_lens),
                         _meta(cu_seqlens_q), cache_layout, _meta(q), _meta(q_weight), _meta(k_weight), _meta(cos_sin),
                         _meta(positions), _meta(q_out), float(eps), bool(interleaved))
     _refuse_cpu(k)
     if q is not None and q_out is None:
         q_out = _torch_state["like"](q)
-    _launch("sdpa_paged_append", k.device, stream, ctypes.byref(p), None if n is None else ctypes.byref(n), _addr(q),
+    _launch("sdpa_paged_append", k.device, ctypes.byref(p), None if n is None else ctypes.byref(n), _addr(q),
             k.data_ptr(), v.data_ptr(), _addr(q_weight), _addr(k_weight), _addr(cos_sin), _addr(positions), _addr(q_out),
             k_cache.data_ptr(), v_cache.data_ptr(), cu_seqlens_q.data_ptr(), kv_lens.data_ptr(), block_table.data_ptr())
     return q_out
@@ -833,6 +855,8 @@ def sdpa_paged_fwd(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens_q, *, m
     or "none"; window = (left, -1 or 0). Returns (o [T, Hq, Dv], lse float32
     [T, Hq]); rows behind the last sequence are left as they are. A workspace
     of PAGED_WORKSPACE_MAX bytes serves every shape."""
+    if stream is not None:
+        return _on(stream, sdpa_paged_fwd, locals())
     p, need = _paged_plan(_meta(q), _meta(k_cache), _meta(v_cache), _meta(block_table), _meta(kv_lens),
                           _meta(cu_seqlens_q), int(max_seqlen_q), None if max_seqlen_kv is None else int(max_seqlen_kv),
                           cache_layout, mask, int(window[0]), int(window[1]), None if scale is None else float(scale),
@@ -847,7 +871,7 @@ def sdpa_paged_fwd(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens_q, *, m
         workspace = lse.new_empty(max(need // 4, 64))
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {dev}")
-    _launch("sdpa_paged_fwd", dev, stream, ctypes.byref(p), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+    _launch("sdpa_paged_fwd", dev, ctypes.byref(p), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
             out.data_ptr(), lse.data_ptr(), cu_seqlens_q.data_ptr(), kv_lens.data_ptr(), block_table.data_ptr(),
             workspace.data_ptr(), workspace.nbytes)
     return out, lse

@@ -409,3 +409,33 @@ def test_every_access_is_inside_the_buffers(d, order):
         assert sdpa.sdpa_debug_address_report()[0] == 0
         assert sdpa.sdpa_get_device_error() == 0
     check(c, o, lse)
+
+
+@pytest.mark.parametrize("capture", [False, True])
+def test_memory_of_a_call_on_another_stream(monkeypatch, capture):
+    """The workspace of a call is not handed out again on the calling stream, and its outputs outlive a use there."""
+    c = case([3, 1, 5], [900, 400, 2000])
+    want = call(c)
+    side, here = torch.cuda.Stream(), torch.cuda.current_stream()
+    side.wait_stream(here)
+    seen, launch = [], sdpa._launch
+    monkeypatch.setattr(sdpa, "_launch", lambda name, device, *a: (seen.append((a[-2], a[-1])), launch(name, device, *a)))
+    o, lse = call(c, stream=side)
+    (at, size), = seen
+    again = [torch.empty(size, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    assert all(x.data_ptr() + size <= at or at + size <= x.data_ptr() for x in again)
+    assert torch.cuda.current_stream() == here
+    here.wait_stream(side)
+    torch.cuda.synchronize()
+    assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+    if capture:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            inner = torch.cuda.Stream()
+            inner.wait_stream(torch.cuda.current_stream())
+            o, lse = call(c, stream=inner)
+            torch.cuda.current_stream().wait_stream(inner)
+        for _ in range(2):
+            graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
