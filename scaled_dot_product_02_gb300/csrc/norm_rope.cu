@@ -264,8 +264,8 @@ __global__ void __launch_bounds__(kThreads, Row<D>::VPL == 1 ? 6 : 4)
         cb[v][e] = fmul2(inter ? make_float2(wp[e].y, wp[e].x) : wp[e], s[e]);
       }
     }
-  } else if (NORM && APPEND && p.rot > 0 && p.pos) {
-    const int pos = load_i32(p.chk, p.pos + row, -1);  // a token with a bad position is skipped whole
+  } else if (NORM && APPEND && p.rot > 0) {
+    const int pos = p.pos ? load_i32(p.chk, p.pos + row, -1) : slot.position;  // a token with a bad one is skipped whole
     if (pos < 0 || pos >= p.max_pos) return;
   }
 

@@ -147,3 +147,22 @@ def test_every_access_is_inside_the_buffers(rot):
         sdpa.sdpa_paged_append(s["k"], s["v"], s["kc"], s["vc"], *s["dev"], cache_layout="hnd", **kw)
         assert sdpa.sdpa_debug_address_report()[0] == 0
         assert sdpa.sdpa_get_device_error() == 0
+
+
+@pytest.mark.parametrize("given", [False, True])
+def test_a_token_whose_position_has_no_angles_is_skipped_whole(given):
+    s = batch(4, [3, 2], [22, 9], 16, 2, 128, 128, "nhd", torch.bfloat16, hq=4)  # positions 19 to 21, 7 and 8
+    w, table = torch.ones(128, device="cuda").bfloat16(), ref.angles_table(20, 128).cuda()
+    positions = torch.tensor([19, 20, 21, 7, 8], dtype=torch.int32, device="cuda")
+    _, k_ref = sdpa.sdpa_qk_norm_rope(s["q"], s["k"], w, w, table, positions.clamp(max=19))
+    kept = s["kc"].clone(), s["vc"].clone()
+    kc, vc = expected(s, k_ref, s["v"])
+    _, page, slot, _, _ = ref.token_places(s["cu"], s["lens"], 16, s["table"])
+    i, j = torch.from_numpy(page[1:3]).cuda(), torch.from_numpy(slot[1:3]).cuda()
+    kc[i, j], vc[i, j] = kept[0][i, j], kept[1][i, j]
+    q_out = torch.full_like(s["q"], 5.0, memory_format=torch.contiguous_format)
+    sdpa.sdpa_paged_append(s["k"], s["v"], s["kc"], s["vc"], *s["dev"], q=s["q"], q_weight=w, k_weight=w, cos_sin=table,
+                           positions=positions if given else None, q_out=q_out)
+    assert sdpa.sdpa_get_device_error() == 10
+    assert torch.equal(s["kc"], kc) and torch.equal(s["vc"], vc)
+    assert bool((q_out[1:3] == 5).all()) and bool((q_out[[0, 3, 4]] != 5).any())
