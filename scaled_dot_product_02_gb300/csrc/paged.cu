@@ -22,9 +22,14 @@
 // tile (and per value column of the output); warps 4-6 TMA producers, each
 // lane fetching one page's rows of a tile (a warp issues its lanes' copies one
 // after another, about 100 cycles each: with pages of 16 one producer warp was
-// the bound); warp 7 TMEM allocator and MMA issuer. K and V tiles go through a ring of 32 KB stages (128 keys x 128
-// columns); S^T and P are double-buffered, so S^T of the next tile is formed
-// while the softmax works on this one.
+// the bound: 64 sequences of 500 to 16384 keys took 397 us, with three 350);
+// warp 7 TMEM allocator and MMA issuer. K and V tiles go through a ring of 32 KB
+// stages (128 keys x 128 columns); S^T and P are double-buffered, so S^T of the
+// next tile is formed while the softmax works on this one.
+//
+// Measured with the join: that batch 345 to 352 us, 6.3 TB/s; 48 sequences at
+// head_dim 256 with a window of 1024 71 us, 5.2 TB/s; one token over 999 keys
+// 9.2 us in a captured graph.
 #include <algorithm>
 #include <cuda.h>
 #include <cuda_runtime.h>
