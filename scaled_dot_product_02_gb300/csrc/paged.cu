@@ -572,49 +572,61 @@ __global__ void __launch_bounds__(256, 1)
   }
 }
 
-// Items that cross cuts: CTA w joins the item that cut w (the start of worker
-// w's share) falls into, if w is the first cut inside it. Its parts come from
-// worker w - 1 (which began it) and the workers whose shares start in it:
+// Items that cross cuts. Their parts come from the worker that began the item
+// and from those whose shares start in it:
 //   m = max m_k,  l = sum l_k 2^(m_k - m),  O = sum O_k 2^(m_k - m) / l.
-// A part holds N rows of DV values, then N maxima and N sums. CTA (w, y) joins
-// join_rows(N) rows, each thread four columns of a row with its own copy of the
-// row's statistics: after the wait there are two rounds of loads, the cut and the
-// parts. (One CTA per item, statistics first, took 4 us where the parts were
-// small and 29 to 49 us for the 128-row items of chunks.)
+// A part holds N rows of DV values, then N maxima and N sums. Every cut inside an
+// item (the start of worker w's share, CTAs (w, y)) takes an equal portion of its
+// elements, four columns of a row each with its own copy of the row's
+// statistics: after the wait there are two rounds of loads, the cut and the
+// parts. Of an item of more than eight parts four lanes share an element, so
+// that no thread walks many of them in turn. (With the item's first cut alone
+// at work, 4 sequences of 4 tokens over 10786 keys at head_dim 512, 38 parts an
+// item, took 58 us; one item of 64 parts of 128 rows 96 us.)
 constexpr int join_rows(int n) { return n >= 128 ? 32 : 8; }
 
 template <int DV, int N, bool BF16>
 __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__ PagedParams p, int grid) {
   using E = Elem<BF16>;
   using T = typename E::T;
-  const int w = blockIdx.x + 1;
+  const int w = blockIdx.x + 1, lane = threadIdx.x % 32;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // a chunk kernel behind needs nothing of this
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (!SDPA_ADDR_OK(p.chk, p.total_tiles, 8) || !SDPA_ADDR_OK(p.chk, p.cuts + w, sizeof(PagedCut))) return;
   const long long total = *reinterpret_cast<volatile long long*>(p.total_tiles);
   const PagedCut cut = p.cuts[w];  // read with the total; a worker without a share leaves it unset
   const PagedShare share(total, grid);
-  if (w >= share.workers || share.at(w) == cut.at || share.at(w - 1) > cut.at) return;
-  constexpr int ROWS = join_rows(N);
-  const int r0 = blockIdx.y * ROWS, rows = min(ROWS, cut.tokens * p.block_heads - r0);
-  if (rows <= 0) return;
-  int parts = 1;  // worker w - 1, then w, w + 1, ...
-  while (w - 1 + parts < share.workers && share.at(w - 1 + parts) < cut.at + cut.n) ++parts;
+  if (w >= share.workers || share.at(w) == cut.at) return;
+  const int first = share.of(cut.at), parts = share.of(cut.at + cut.n - 1) - first + 1;
+  const int helper = (w - first - 1) * gridDim.y + blockIdx.y, helpers = (parts - 1) * gridDim.y;
   constexpr int SLOT = N * (DV + 2), V4 = DV / 4;
+  static_assert(V4 % 32 == 0, "a warp's elements lie in one row");
   const PagedUnit un = paged_unit(p, cut.unit);
-  for (int x = threadIdx.x; x < rows * V4; x += 256) {
-    const int r = r0 + x / V4, d = (x % V4) * 4;
+  const int lanes = parts > 8 ? 4 : 1, width = 32 / lanes;  // lanes that share an element, elements of a warp
+  const int elements = cut.tokens * p.block_heads * V4, mine = lane / width;
+  for (int x = (helper * 8 + threadIdx.x / 32) * width; x < elements; x += helpers * 8 * width) {
+    const int r = x / V4, d = (x % V4 + lane % width) * 4;
     const int ti = r / p.block_heads, h = r - ti * p.block_heads;
     if (h >= un.heads) continue;
     float m = -INFINITY, l = 0.f;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k0 = 0; k0 < parts; k0 += 4) {
+    auto add = [&](float mk, float lk, const float4& v) {
+      if (mk == -INFINITY) return;  // a part without keys for this row
+      const float top = fmaxf(m, mk), f = m == -INFINITY ? 0.f : ex2(m - top), g = ex2(mk - top);
+      m = top;
+      l = l * f + lk * g;
+      a.x = a.x * f + v.x * g;
+      a.y = a.y * f + v.y * g;
+      a.z = a.z * f + v.z * g;
+      a.w = a.w * f + v.w * g;
+    };
+    for (int k0 = mine; k0 < parts; k0 += 4 * lanes) {
       float mk[4], lk[4];
       float4 v[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int k = k0 + e;
-        const float* part = p.parts + ((long long)(w - 1 + k) * 2 + (k == 0 ? 1 : 0)) * SLOT;
+        const int k = k0 + e * lanes;
+        const float* part = p.parts + ((long long)(first + k) * 2 + (k == 0 ? 1 : 0)) * SLOT;
         const bool in = k < parts && SDPA_ADDR_OK(p.chk, part + N * DV + r, 4) &&
                         SDPA_ADDR_OK(p.chk, part + N * DV + N + r, 4) && SDPA_ADDR_OK(p.chk, part + r * DV + d, 16);
         mk[e] = in ? part[N * DV + r] : -INFINITY;
@@ -622,16 +634,17 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__
         v[e] = in ? *reinterpret_cast<const float4*>(part + r * DV + d) : make_float4(0.f, 0.f, 0.f, 0.f);
       }
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if (mk[e] == -INFINITY) continue;  // a part without keys for this row
-        const float top = fmaxf(m, mk[e]), f = m == -INFINITY ? 0.f : ex2(m - top), g = ex2(mk[e] - top);
-        m = top;
-        l = l * f + lk[e] * g;
-        a.x = a.x * f + v[e].x * g;
-        a.y = a.y * f + v[e].y * g;
-        a.z = a.z * f + v[e].z * g;
-        a.w = a.w * f + v[e].w * g;
+      for (int e = 0; e < 4; ++e) add(mk[e], lk[e], v[e]);
+    }
+    if (lanes > 1) {
+#pragma unroll
+      for (int o = 8; o <= 16; o *= 2) {
+        const float mk = __shfl_xor_sync(0xffffffffu, m, o), lk = __shfl_xor_sync(0xffffffffu, l, o);
+        const float4 v = make_float4(__shfl_xor_sync(0xffffffffu, a.x, o), __shfl_xor_sync(0xffffffffu, a.y, o),
+                                     __shfl_xor_sync(0xffffffffu, a.z, o), __shfl_xor_sync(0xffffffffu, a.w, o));
+        add(mk, lk, v);
       }
+      if (mine > 0) continue;
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;
     const long long at = (long long)(cut.row0 + ti) * p.hq + un.head0 + h;

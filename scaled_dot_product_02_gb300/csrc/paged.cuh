@@ -39,6 +39,12 @@ struct PagedShare {
     }
   }
   __device__ __forceinline__ long long at(int w) const { return base * w + min(w, rest); }
+  // The share that holds position u.
+  __device__ __forceinline__ int of(long long u) const {
+    const long long longer = (base + 1) * rest;  // the first `rest` shares hold one more
+    const long long past = u < longer ? u : u - longer, n = u < longer ? base + 1 : base;
+    return (u < longer ? 0 : rest) + (int)(past < (1ll << 32) && n < (1ll << 32) ? (unsigned)past / (unsigned)n : past / n);
+  }
 };
 
 // One sequence of the batch: its rows and its cached keys.

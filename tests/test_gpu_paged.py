@@ -439,3 +439,15 @@ def test_memory_of_a_call_on_another_stream(monkeypatch, capture):
             graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+
+
+@pytest.mark.parametrize("d", [128, 192, 256, 512])
+@pytest.mark.parametrize("new,window", [([2], -1), ([5, 1], -1), ([40], -1), ([33, 20], 7000), ([1, 16, 3], -1)])
+def test_few_items_of_many_parts(d, new, window):
+    """Items that most of the CTAs share: their parts are joined by all the cuts inside them."""
+    total = [9001, 7777, 8200][:len(new)]
+    c = case(new, total, hq=9, hkv=1 if d != 192 else 3, d=d, page=32, seed=31, max_kv=33000 if d == 128 else 0)
+    o, lse = call(c, window=window)
+    check(c, o, lse, window=window)
+    again = call(c, window=window)
+    assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
