@@ -484,12 +484,18 @@ PagedCutting paged_cutting(const sdpa_paged_problem* p, int n, int q_rows, int m
     c.tail = 0;
   } else {
     // Whole items by ticket keep the CTAs on the same keys (with all items cut into equal shares, 2048 tokens over
-    // 131072 keys took 14 % longer, 8 x 1024 over 32768 40 %). The last, uneven round costs half an item on average:
+    // 131072 keys took 14 % longer, 8 x 1024 over 32768 41 %). The last, uneven round costs half an item on average:
     // it is cut into shares where items are few and long enough to pay for the join (2048 tokens over 16384 keys, 3.4
     // rounds: D192 643 -> 580 us, D512 1244 -> 1125 us; at head_dim 128, 2048 over 131072, 1.7 rounds: 2856 -> 2708
-    // us, but 8 x 512 over 4096 to 8192, 3.4 rounds: 285 -> 306 us).
+    // us, but 8 x 512 over 4096 to 8192, 3.4 rounds: 285 -> 306 us). Items for at most half of the SMs are cut when
+    // much shorter (head_dim 256, 16 tokens over 4096 keys, one item: 66 -> 25 us; head_dim 128, 64 tokens on 8 kv
+    // heads over 2048 keys 35 -> 31 us, over 8192 100 -> 46 us; but 128 items of 16 tiles: 43 -> 80 us). A share for
+    // every CTA where all items are cut: 17 sequences at head_dim 256, 163 -> 143 us against two.
     c.split = false;
-    c.tail = tiles >= (n == 256 ? 256 : 48) && items < (n == 256 ? 2 : 6) * most ? 2 * most : 0;
+    const bool cut = items * 2 <= most  ? tiles >= 16
+                     : items < most * 2 ? tiles >= (n == 256 ? 256 : 48)
+                                        : n != 256 && tiles >= 48 && items < 6 * most;
+    c.tail = !cut ? 0 : items < most ? most : 2 * most;
   }
   // the length of a block and the ticket counter are 32-bit numbers
   c.fits = (long long)p->num_heads_kv * c.head_blocks * c.dv_splits * std::max(tiles, 1LL) < (1LL << 31) &&
