@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(256, 1)
   if (me < min((long long)gridDim.x, all.total)) {
     PagedWalk w = scan->start;
     const long long u0 = w.u;
-    if (threadIdx.x == 0) {
+    if (threadIdx.x == 0 && p.split) {  // whole items need no join, and the workspace holds no records for one
       PagedCut* cut = p.cuts + me;
       if (SDPA_ADDR_OK(p.chk, cut, sizeof(PagedCut))) *cut = w.cut(p);
     }

@@ -451,3 +451,50 @@ def test_few_items_of_many_parts(d, new, window):
     check(c, o, lse, window=window)
     again = call(c, window=window)
     assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
+
+
+def bare_call(c, monkeypatch, **kw):
+    """The problem struct of a call, which is not made."""
+    seen = []
+    with monkeypatch.context() as m:
+        m.setattr(sdpa, "_launch", lambda name, device, *a: seen.append(a[0]._obj))
+        call(c, **kw)
+    return seen[0]
+
+
+# (new, total, bound of the lengths, window): shares cut or not, in the rows kernel, the chunk kernel and both
+EXACT = {
+    "whole_items": ([1] * 80, [40 + 3 * i for i in range(80)], 512, -1),
+    "split_items": ([1] * 80, [40 + 3 * i for i in range(80)], 513, -1),
+    "small_window": ([1] * 80, [1000 + 3 * i for i in range(80)], 4000, 100),
+    "whole_chunks": ([40] * 30, [300 + i for i in range(30)], 512, -1),
+    "cut_chunks": ([40, 33], [700, 300], 33000, -1),
+    "mixed_whole": ([1, 40, 0, 17, 2], [400, 90, 7, 300, 512], 512, -1),
+    "mixed_cut": ([1, 40, 0, 17, 2], [4000, 90, 7, 300, 512], 33000, -1),
+}
+
+
+@pytest.mark.parametrize("name", EXACT)
+@pytest.mark.parametrize("d", [128, 192, 256, 512])
+def test_a_workspace_of_the_reported_size_is_enough(name, d, monkeypatch):
+    """Nothing in front of the workspace or behind it is written."""
+    new, total, max_kv, window = EXACT[name]
+    c = case(new, total, hq=16, hkv=8, d=d, max_kv=max_kv)
+    need = sdpa.sdpa_paged_fwd_workspace_size(bare_call(c, monkeypatch, window=window))
+    edge = 1 << 16
+    whole = torch.full((edge + need + edge,), 0xA5, dtype=torch.uint8, device="cuda")
+    check(c, *call(c, window=window, workspace=whole[edge:edge + need]), window=window)
+    assert bool((whole[:edge] == 0xA5).all()) and bool((whole[edge + need:] == 0xA5).all())
+
+
+@pytest.mark.parametrize("name", EXACT)
+@pytest.mark.parametrize("d", [128, 192, 256, 512])
+def test_every_access_is_inside_a_workspace_of_the_reported_size(name, d):
+    new, total, max_kv, window = EXACT[name]
+    c = case(new, total, hq=16, hkv=8, d=d, max_kv=max_kv)
+    with sdpa.address_checked():
+        sdpa.sdpa_debug_address_report()
+        o, lse = call(c, window=window)
+        assert sdpa.sdpa_debug_address_report()[0] == 0
+        assert sdpa.sdpa_get_device_error() == 0
+    check(c, o, lse, window=window)
