@@ -498,3 +498,15 @@ def test_every_access_is_inside_a_workspace_of_the_reported_size(name, d):
         assert sdpa.sdpa_debug_address_report()[0] == 0
         assert sdpa.sdpa_get_device_error() == 0
     check(c, o, lse, window=window)
+
+
+@pytest.mark.parametrize("d,page,order", DIMS[:4])
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("causal,window", [(True, -1), (True, 33), (False, -1)])
+def test_a_scale_of_zero(d, page, order, dtype, causal, window):
+    """All visible keys weigh the same, hidden ones nothing: single tokens, chunks, both in one batch, and the last items
+    cut into shares."""
+    for new, total, max_kv in (([1, 2], [300, 501], 0), ([70, 1, 33], [70, 90, 701], 0), ([300, 41], [911, 333], 33000)):
+        c = case(new, total, d=d, page=page, order=order, dtype=dtype, max_kv=max_kv)
+        c["scale"] = 0.0
+        check(c, *call(c, causal=causal, window=window), causal=causal, window=window)
