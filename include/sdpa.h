@@ -408,7 +408,9 @@ typedef struct {
  * rotation's positions, or NULL for the cache positions. One launch.
  * A token is skipped, and the device error word set, when its sequence's lengths do not fit
  * (SDPA_ERR_BAD_SEQLENS) or its page or position lies outside its table (SDPA_ERR_BAD_INDEX).
- * Two tokens of one call that map to one slot leave one of their rows there. */
+ * Two tokens of one call that map to one slot leave one of their rows there. The caches may
+ * interleave (pages, slots or heads that hold K and V together) but not share values: rows of
+ * one or of both that do are refused as SDPA_ERR_OVERLAP. */
 SDPA_API int sdpa_paged_append(const sdpa_paged_problem* p, const sdpa_norm_rope_problem* n, const void* q,
                                const void* k, const void* v, const void* q_weight, const void* k_weight,
                                const float* cos_sin, const int32_t* positions, void* q_out, void* k_cache,

@@ -15,6 +15,7 @@
 #include <cstring>
 #include <limits>
 #include <mutex>
+#include <numeric>
 #include <set>
 #include <utility>
 #include <vector>
@@ -564,6 +565,35 @@ int encode_cache(CUtensorMap* m, const void* base, const sdpa_paged_problem* p, 
 // Bytes from a cache's first element to its last.
 size_t cache_span(const sdpa_paged_problem* p, long long page, long long slot, long long head, int width) {
   return (size_t)((p->num_pages - 1) * page + (p->page_size - 1) * slot + (p->num_heads_kv - 1) * head + width) * 2;
+}
+
+// Whether every row of the two caches lies apart from all others. Where their spans interleave (pages that hold K and V
+// together), addresses are compared modulo a step that both caches' strides from some level on are multiples of: the
+// stretch of a step that K fills and the one that V fills must not meet.
+bool caches_apart(const sdpa_paged_problem* p, const void* k_cache, const void* v_cache, bool spans_overlap) {
+  struct Level {
+    long long stride, fill;  // fill: values from the first to the last within one step of the stride
+  };
+  const bool one = p->num_heads_kv == 1;  // a single head's stride is never taken
+  auto levels = [&](long long page, long long slot, long long head, int width) {
+    const bool first = one || slot < head;  // slots vary before heads
+    const long long lo = first ? slot : head, hi = one || !first ? slot : head;
+    const long long inner = one ? width : ((first ? p->page_size : p->num_heads_kv) - 1) * lo + width;
+    const long long whole = ((first && !one ? p->num_heads_kv : p->page_size) - 1) * hi + inner;
+    return std::array<Level, 3>{Level{lo, width}, Level{hi, inner}, Level{page, whole}};
+  };
+  const auto k = levels(p->k_page_stride, p->k_slot_stride, p->k_head_stride, p->head_dim);
+  const auto v = levels(p->v_page_stride, p->v_slot_stride, p->v_head_stride, paged_dv(p));
+  const int used = p->num_pages > 1 ? 3 : 2;
+  for (int i = 0; i < used; ++i)
+    if (k[i].fill > k[i].stride || v[i].fill > v[i].stride) return false;
+  if (!spans_overlap) return true;
+  const long long off = (long long)(reinterpret_cast<uintptr_t>(v_cache) - reinterpret_cast<uintptr_t>(k_cache)) / 2;
+  for (int i = 0; i < used; ++i) {
+    const long long step = std::gcd(k[i].stride, v[i].stride), at = (off % step + step) % step;
+    if (at >= k[i].fill && at + v[i].fill <= step) return true;
+  }
+  return false;
 }
 
 }  // namespace
@@ -1234,7 +1264,7 @@ int sdpa_paged_append(const sdpa_paged_problem* p, const sdpa_norm_rope_problem*
   for (const Extent& out : outs)
     for (const Extent& in : ins)
       if (overlaps(out, in)) return SDPA_ERR_OVERLAP;
-  // the caches' spans may interleave (pages that hold K and V together), q_out's may not
+  if (!caches_apart(p, k_cache, v_cache, overlaps(outs[0], outs[1]))) return SDPA_ERR_OVERLAP;
   if (overlaps(outs[2], outs[0]) || overlaps(outs[2], outs[1])) return SDPA_ERR_OVERLAP;
   L.err = error_word();
   if (!L.err) return SDPA_ERR_CUDA;

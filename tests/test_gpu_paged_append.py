@@ -166,3 +166,26 @@ def test_a_token_whose_position_has_no_angles_is_skipped_whole(given):
     assert sdpa.sdpa_get_device_error() == 10
     assert torch.equal(s["kc"], kc) and torch.equal(s["vc"], vc)
     assert bool((q_out[1:3] == 5).all()) and bool((q_out[[0, 3, 4]] != 5).any())
+
+
+@pytest.mark.parametrize("order", ["nhd", "hnd"])
+@pytest.mark.parametrize("at", [1, 2, 3, 4])
+@pytest.mark.parametrize("v_first", [False, True])
+@pytest.mark.parametrize("hkv", [1, 3])
+def test_caches_that_interleave_at_every_level(order, at, v_first, hkv):
+    """K and V in turn by page, by the outer and the inner one of slot and head, and side by side in a row."""
+    s = batch(7, [3, 0, 20], [30, 5, 61], 16, hkv, 128, 128, order, torch.bfloat16, pad=1)
+    shape = list(s["kc"].shape)
+    both = torch.randn(*shape[:at], 2, *shape[at:], device="cuda").bfloat16()
+    if at == 4:  # [..., 2 x width]
+        both = torch.randn(*shape[:3], 256, device="cuda").bfloat16()
+        k, v = both[..., :128], both[..., 128:]
+    else:
+        k, v = both.select(at, 0), both.select(at, 1)
+    s["kc"], s["vc"] = (v, k) if v_first else (k, v)
+    kc, vc = expected(s, s["k"], s["v"])
+    sdpa.sdpa_paged_append(s["k"], s["v"], s["kc"], s["vc"], *s["dev"], cache_layout=order)
+    assert torch.equal(s["kc"], kc) and torch.equal(s["vc"], vc)
+    assert sdpa.sdpa_get_device_error() == 0
+    with pytest.raises(sdpa.SdpaError, match="OVERLAP"):
+        sdpa.sdpa_paged_append(s["k"], s["v"], s["kc"], s["kc"], *s["dev"], cache_layout=order)

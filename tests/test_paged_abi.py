@@ -290,3 +290,33 @@ def test_scalars_given_as_tensors_are_read_on_every_call(monkeypatch):
         eps.fill_(e)
         sdpa.sdpa_qk_norm_rope(c["q"], c["k"], c["w"], c["w"], eps=eps)
         assert seen.pop().eps == e
+
+
+@pytest.mark.parametrize("kw,shift", [
+    (dict(), 0),                                                      # one cache for both
+    (dict(), 8), (dict(), -8), (dict(), 64), (dict(), 16 * 256 - 64),  # V begins inside K's rows, or ends in them
+    (dict(), 16 * 256),                                               # V's pages are K's next ones
+    (dict(k_page_stride=2 * 16 * 256, v_page_stride=2 * 16 * 256), 16 * 256 - 8),
+    (dict(k_page_stride=2 * 16 * 256, v_page_stride=2 * 16 * 256), 16 * 256 + 8),
+    (dict(k_page_stride=2 * 16 * 256, v_page_stride=3 * 16 * 256), 16 * 256),
+    (dict(k_slot_stride=512, v_slot_stride=512, k_page_stride=8192, v_page_stride=8192), 128),
+    (dict(num_heads_kv=1, num_pages=1, k_slot_stride=256, v_slot_stride=256), 120),
+    (dict(num_heads_kv=1, num_pages=1, k_slot_stride=256, v_slot_stride=256), -120),
+])
+def test_append_refuses_caches_that_share_values(kw, shift):
+    base = dict(num_heads_q=8, num_pages=50)
+    p = paged_problem(**{**base, **kw})
+    addr = [BASE, BASE + M, BASE + 2 * M, None, None, None, None, None, BASE + 8 * M, BASE + 8 * M + 2 * shift, BASE + 30 * M,
+            BASE + 31 * M, BASE + 32 * M]
+    assert sdpa.sdpa_check_paged(p) == 0
+    assert sdpa.lib().sdpa_paged_append(ctypes.byref(p), None, *[PTR(x) for x in addr], None) == 4
+
+
+@pytest.mark.parametrize("kw", [dict(k_page_stride=8 * 256), dict(v_page_stride=256),
+                                dict(k_slot_stride=128, k_head_stride=1024, v_slot_stride=128, v_head_stride=1024)])
+def test_append_refuses_a_cache_whose_rows_share_values(kw):
+    p = paged_problem(**kw)
+    addr = [BASE, BASE + M, BASE + 2 * M, None, None, None, None, None, BASE + 8 * M, BASE + 20 * M, BASE + 30 * M,
+            BASE + 31 * M, BASE + 32 * M]
+    assert sdpa.sdpa_check_paged(p) == 0
+    assert sdpa.lib().sdpa_paged_append(ctypes.byref(p), None, *[PTR(x) for x in addr], None) == 4
