@@ -652,7 +652,8 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 1) norm_rope_bwd_kernel(const 
           float a = ss.x + ss.y, b = dot.x + dot.y;
           row_sums<R::LPH>(a, b, lane);
           if (hh + grp + x * R::SUB >= n) continue;
-          const float r1 = rsqrtf(a * (1.f / D) + p.eps), k1 = -r1 * r1 * r1 * (b * (1.f / D));
+          // r^3 by itself would leave fp32's range for rows of 1e15 (or, with eps 0, 1e-13): the mean, some 1 / r, first
+          const float r1 = rsqrtf(a * (1.f / D) + p.eps), k1 = -(r1 * (b * (1.f / D))) * r1 * r1;
           const float2 r = make_float2(r1, r1), k3 = make_float2(k1, k1);
 #pragma unroll
           for (int v = 0; v < R::VPL; ++v) {

@@ -231,3 +231,20 @@ def test_every_access_is_inside_the_buffers(d, rot, inter, n):
             gq, gk, qd, kd, *args, interleaved=inter)
         assert sdpa.sdpa_debug_address_report()[0] == 0
     assert all(torch.equal(a, b) for a, b in zip(plain, got))
+
+
+@pytest.mark.parametrize("d,rot,inter", [(128, 128, False), (128, 64, True), (192, 192, False), (256, 128, True), (512, 512, False)])
+@pytest.mark.parametrize("scale,eps", [(1e15, EPS), (1e17, EPS), (1e-13, 0.0), (1e-18, 0.0)])
+def test_gradient_of_rows_far_from_unit_scale(d, rot, inter, scale, eps):
+    """dx is some 1 / scale and dw does not depend on it, though r^3 alone leaves the range of fp32."""
+    q, k, _, _, wq, wk, table, pos = make(60, 6, 2, d, rot, torch.bfloat16, False)
+    q, k = (q.float() * scale).bfloat16(), (k.float() * scale).bfloat16()
+    g = torch.Generator().manual_seed(9)
+    gq, gk = torch.randn(q.shape, generator=g).bfloat16(), torch.randn(k.shape, generator=g).bfloat16()
+    got = sdpa.sdpa_qk_norm_rope_bwd(dev(gq), dev(gk), dev(q), dev(k), dev(wq), dev(wk), dev(table), dev(pos), eps=eps,
+                                     interleaved=inter)
+    for x, w, dy, dx, dw in ((q, wq, gq, got[0], got[2]), (k, wk, gk, got[1], got[3])):
+        want, mag, want_w, mag_w = ref.norm_rope_bwd(dy, x, w, table[pos.long()], rot, eps, inter)
+        within(dx, want, mag, ref.U[torch.bfloat16], 0.0, 2.0 ** -17)
+        within(dw, want_w, mag_w, 0.0, 0.0, 2.0 ** -15)
+    assert sdpa.sdpa_get_device_error() == 0
