@@ -467,7 +467,8 @@ __global__ void __launch_bounds__(kFwdWarps * 32, 1) norm_rope_ring_kernel(const
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           ca[v][e] = fmul2(wt[e], c[e]);
-          cb[v][e] = fmul2(INTER ? make_float2(wp[e].y, wp[e].x) : wp[e], s[e]);
+          // where nothing turns the sine is zero; a weight that is not finite must not meet it
+          cb[v][e] = at[v].on ? fmul2(INTER ? make_float2(wp[e].y, wp[e].x) : wp[e], s[e]) : make_float2(0.f, 0.f);
         }
       }
       T* dst = (is_q ? static_cast<T*>(p.q_out) + cur.row * p.hq * D : static_cast<T*>(p.k_out) + cur.row * p.hkv * D) + h0 * D;

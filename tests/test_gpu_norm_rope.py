@@ -248,3 +248,26 @@ def test_gradient_of_rows_far_from_unit_scale(d, rot, inter, scale, eps):
         within(dx, want, mag, ref.U[torch.bfloat16], 0.0, 2.0 ** -17)
         within(dw, want_w, mag_w, 0.0, 0.0, 2.0 ** -15)
     assert sdpa.sdpa_get_device_error() == 0
+
+
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("d,rot", [(128, 64), (192, 96), (256, 64), (512, 16)])
+@pytest.mark.parametrize("value", [float("inf"), float("-inf"), float("nan")])
+def test_a_weight_that_is_not_finite_stays_in_its_column(inter, d, rot, value):
+    """Where nothing turns the result is x r w alone, for few tokens and for many; a pair takes the weight in both halves."""
+    q, k, qd, kd, wq, wk, table, pos = make(3800, 4, 1, d, rot, torch.bfloat16, True)
+    table[:, rot // 2:] = table[:, rot // 2:].abs().clamp(min=0.1)  # a sine of zero times an infinity would be NaN
+    tail, pair = d - 3, 2                                           # an unrotated column, a rotated one
+    for at in (tail, pair):
+        w = wq.clone()
+        w[at] = value
+        hit = {at} if at == tail else {at, ref.pair_index(d, rot, inter)[0][at].item()}
+        keep = torch.tensor([i not in hit for i in range(d)])
+        for n in (3, 3800):
+            qo, ko = sdpa.sdpa_qk_norm_rope(qd[:n], kd[:n], dev(w), dev(w), dev(table), dev(pos[:n]), eps=EPS, interleaved=inter)
+            for out, x in ((qo.cpu(), q[:n]), (ko.cpu(), k[:n])):
+                want, mag = ref.norm_rope(x, w, table[pos[:n].long()], rot, EPS, inter)
+                within(out[..., keep], want[..., keep], mag[..., keep], ref.U[torch.bfloat16], 0.0, 2.0 ** -19)
+                for i in hit:  # x or its partner may be zero: NaN then, as in the definition
+                    assert torch.equal(out[..., i].float().nan_to_num(9.0, 2.0, -2.0),
+                                       want[..., i].float().nan_to_num(9.0, 2.0, -2.0))
