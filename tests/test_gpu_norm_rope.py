@@ -271,3 +271,46 @@ def test_a_weight_that_is_not_finite_stays_in_its_column(inter, d, rot, value):
                 for i in hit:  # x or its partner may be zero: NaN then, as in the definition
                     assert torch.equal(out[..., i].float().nan_to_num(9.0, 2.0, -2.0),
                                        want[..., i].float().nan_to_num(9.0, 2.0, -2.0))
+
+
+@pytest.mark.parametrize("hq,hkv,d,rot,inter,dtype,fused", [
+    (8, 2, 128, 128, False, torch.bfloat16, True), (17, 1, 128, 64, True, torch.float16, False),
+    (16, 4, 128, 32, False, torch.float16, True), (11, 3, 192, 192, False, torch.float16, True),
+    (4, 4, 192, 96, True, torch.bfloat16, False), (9, 1, 256, 256, True, torch.bfloat16, True),
+    (8, 2, 256, 64, False, torch.float16, False), (16, 16, 256, 192, False, torch.bfloat16, False),
+    (7, 2, 512, 512, False, torch.bfloat16, True), (4, 1, 512, 208, True, torch.float16, False),
+    (3, 2, 512, 16, False, torch.bfloat16, True)])
+def test_the_rings_of_many_tokens(hq, hkv, d, rot, inter, dtype, fused):
+    """At least three units for every one of the 24 warps of each SM (a unit is 4 KB of one tensor's heads of a token), with
+    one and two stages a warp; bad positions, in a row for one warp too, and infinities beside pairs and in them."""
+    per = 4096 // (2 * d)
+    parts = -(-hq // per) - (-hkv // per)
+    warps = 24 * torch.cuda.get_device_properties(0).multi_processor_count
+    rows = -(-3 * warps // parts) + 5
+    q, k, qd, kd, wq, wk, table, pos = make(rows, hq, hkv, d, rot, dtype, fused, seed=d + rot)
+    for row, head, col in ((3, 0, d - 1), (4, hq - 1, 1), (rows - 2, 0, rot - 1), (rows // 2, hq // 2, rot % d)):
+        q[row, head, col] = qd[row, head, col] = float("inf")
+    bad = torch.zeros(rows, dtype=torch.bool)
+    bad[[0, 7, rows - 1] + [11 + i * warps // parts for i in range(3)]] = True  # the last three: one warp's first units
+    p = pos.clone()
+    p[bad] = torch.tensor([-1, 5000, 2 ** 31 - 1, -2 ** 31, 6000, -7], dtype=torch.int32)
+    qo = torch.full((rows, hq, d), 6.0, dtype=dtype, device="cuda")
+    ko = torch.full((rows, hkv, d), 6.0, dtype=dtype, device="cuda")
+    args = (qd, kd, dev(wq), dev(wk), dev(table), dev(p))
+    sdpa.sdpa_qk_norm_rope(*args, eps=EPS, interleaved=inter, q_out=qo, k_out=ko)
+    assert sdpa.sdpa_get_device_error() == 10
+    assert bool((qo.cpu()[bad] == 6).all()) and bool((ko.cpu()[bad] == 6).all())
+    for out, x, w in ((qo, q, wq), (ko, k, wk)):
+        out = out.cpu()[~bad]
+        want, mag = ref.norm_rope(x[~bad], w, table[pos[~bad].long()], rot, EPS, inter)
+        finite = torch.isfinite(want)
+        assert torch.equal(torch.isfinite(out), finite)
+        within(out[finite], want[finite], mag[finite], ref.U[dtype], ref.TINY[dtype], 2.0 ** -19)
+    with sdpa.address_checked():
+        sdpa.sdpa_debug_address_report()
+        again = sdpa.sdpa_qk_norm_rope(*args, eps=EPS, interleaved=inter)
+        assert sdpa.sdpa_debug_address_report()[0] == 0
+        assert sdpa.sdpa_get_device_error() == 10
+    good = (~bad).cuda()
+    for a, b in zip(again, (qo, ko)):
+        assert torch.equal(a[good].view(torch.int16), b[good].view(torch.int16))
