@@ -510,3 +510,20 @@ def test_a_scale_of_zero(d, page, order, dtype, causal, window):
         c = case(new, total, d=d, page=page, order=order, dtype=dtype, max_kv=max_kv)
         c["scale"] = 0.0
         check(c, *call(c, causal=causal, window=window), causal=causal, window=window)
+
+
+@pytest.mark.parametrize("d", [128, 192])
+@pytest.mark.parametrize("n", [3, 31, 32, 33, 64, 65])
+@pytest.mark.parametrize("cut", [False, True])
+def test_ticket_order_on_both_sides_of_sorting(d, n, cut):
+    """Sorted by their keys up to 32 sequences, in their own order above, 32 of them a step; equal lengths and empty
+    sequences among them, whole items alone or the last ones cut into shares."""
+    rng = np.random.default_rng(n)
+    new = rng.integers(0, 60, n)
+    new[:2] = 59
+    total = np.maximum(new, rng.integers(0, 4, n) * 170 + 5)
+    c = case(new.tolist(), total.tolist(), hq=8, hkv=4, d=d, page=16, pad=2, max_kv=33000 if cut else 0)
+    a, b = call(c), call(c)
+    live = int(c["cu"][-1])
+    assert torch.equal(a[0][:live], b[0][:live]) and torch.equal(a[1][:live], b[1][:live])
+    check(c, *a)
