@@ -800,6 +800,9 @@ def _paged_plan(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens_q, max_seq
         raise ValueError(f"q must be [tokens, heads, head_dim], got {tuple(q[0])}")
     if window_right not in (-1, 0):
         raise ValueError(f"a paged window is (left, -1 or 0), got ({window_left}, {window_right})")
+    for name, n in (("the window", window_left), ("max_seqlen_q", max_seqlen_q), ("max_seqlen_kv", max_seqlen_kv or 0)):
+        if not -2 ** 31 <= n < 2 ** 31:  # the struct's field would keep its low bits
+            raise ValueError(f"{name} must fit 32 bits, got {n}")
     p = _paged_problem(q, hq, k_cache, v_cache, block_table, kv_lens, cu_seqlens_q, cache_layout, rows, max_seqlen_q,
                        max_seqlen_kv, MASKS[mask], window_left, d ** -0.5 if scale is None else scale, qs, 0, 0)
     if p.head_dim != d or hq % p.num_heads_kv:

@@ -320,3 +320,13 @@ def test_append_refuses_a_cache_whose_rows_share_values(kw):
             BASE + 31 * M, BASE + 32 * M]
     assert sdpa.sdpa_check_paged(p) == 0
     assert sdpa.lib().sdpa_paged_append(ctypes.byref(p), None, *[PTR(x) for x in addr], None) == 4
+
+
+@pytest.mark.parametrize("kw", [dict(window=(2 ** 32, -1)), dict(window=(2 ** 31, 0)), dict(window=(-2 ** 40, -1)),
+                                dict(max_seqlen_q=2 ** 32 + 2), dict(max_seqlen_kv=2 ** 32 + 16), dict(max_seqlen_kv=2 ** 31)])
+def test_sizes_beyond_32_bits_are_refused(monkeypatch, kw):
+    """The struct's fields would keep their low bits only: a window of 2^32 became one of 0."""
+    monkeypatch.setattr(sdpa, "_refuse_cpu", lambda t: None)
+    monkeypatch.setattr(sdpa, "_launch", lambda name, device, *args: None)
+    with pytest.raises(ValueError, match="32 bits"):
+        _paged(_batch(), **kw)
