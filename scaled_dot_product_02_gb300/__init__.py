@@ -39,6 +39,7 @@ EXPORTS = ("sdpa_fwd_workspace_size", "sdpa_bwd_workspace_size", "sdpa_check_pro
            "sdpa_paged_fwd")
 NOALLOC_MAX_BYTES = 32 << 20  # SDPA_BWD_NOALLOC_MAX_BYTES
 PAGED_WORKSPACE_MAX = 256 << 20  # SDPA_PAGED_WORKSPACE_MAX
+PAGED_KEYS_MAX = 1 << 30  # the longest kv_len that the library serves
 KERNEL_KINDS = ("fwd", "bwd", "preprocess", "dq_finalize", "guard", "merge", "bwd_dq", "v_transpose",
                 "norm_rope", "append", "paged")
 
@@ -755,8 +756,8 @@ def _paged_problem(q, hq, k_cache, v_cache, block_table, kv_lens, cu_seqlens_q, 
     pages, hkv, d, dv = ks[0], ks[head], ks[3], vs[3]
     # a dimension of one entry may carry any stride: its own row's width stands for it
     return PagedProblem(_dtype_code(dtype, "q"), batch, hq, hkv, d, dv, total_q, seqlen_q,
-                        max_pages * ks[slot] if seqlen_kv is None else seqlen_kv, ks[slot], pages, max_pages, mask_type,
-                        window_left, scale, tab_st[0] if batch > 1 else 0, k_st[0] if pages > 1 else d, k_st[slot],
+                        min(max_pages * ks[slot], PAGED_KEYS_MAX) if seqlen_kv is None else seqlen_kv, ks[slot], pages,
+                        max_pages, mask_type, window_left, scale, tab_st[0] if batch > 1 else 0, k_st[0] if pages > 1 else d, k_st[slot],
                         k_st[head] if hkv > 1 else d, v_st[0] if pages > 1 else dv, v_st[slot],
                         v_st[head] if hkv > 1 else dv, q_stride, k_stride, v_stride)
 

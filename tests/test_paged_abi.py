@@ -330,3 +330,20 @@ def test_sizes_beyond_32_bits_are_refused(monkeypatch, kw):
     monkeypatch.setattr(sdpa, "_launch", lambda name, device, *args: None)
     with pytest.raises(ValueError, match="32 bits"):
         _paged(_batch(), **kw)
+
+
+def test_a_table_of_more_keys_than_a_sequence_can_have(monkeypatch):
+    """The default bound of the lengths is what the table holds, but never more than the library serves (2^30)."""
+    seen = []
+    monkeypatch.setattr(sdpa, "_refuse_cpu", lambda t: None)
+    monkeypatch.setattr(sdpa, "_launch", lambda name, device, *args: seen.append(args[0]._obj))
+    c = _batch()
+    _paged(c)
+    assert seen.pop().seqlen_kv == 4 * 16
+    meta = lambda t: (t.shape, t.stride(), t.dtype, t.device)  # noqa: E731
+    q, lens, cu = meta(c["q"]), meta(c["lens"]), meta(c["cu"])
+    for page, cols in ((1 << 20, 1025), (1 << 20, 4096), (1 << 19, 1 << 13)):
+        cache = (torch.Size((1, page, 2, 128)), (page * 256, 256, 128, 1), torch.bfloat16, c["q"].device)
+        table = (torch.Size((3, cols)), (cols, 1), torch.int32, c["q"].device)
+        p, need = sdpa._paged_plan(q, cache, cache, table, lens, cu, 2, None, "nhd", "causal_br", -1, -1, None, None, None)
+        assert p.seqlen_kv == 1 << 30 and sdpa.sdpa_check_paged(p) == 0 and need > 0
