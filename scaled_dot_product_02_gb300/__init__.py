@@ -801,6 +801,8 @@ def _paged_plan(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens_q, max_seq
         raise ValueError(f"q must be [tokens, heads, head_dim], got {tuple(q[0])}")
     if window_right not in (-1, 0):
         raise ValueError(f"a paged window is (left, -1 or 0), got ({window_left}, {window_right})")
+    if window_right == 0 and mask == "none":
+        raise ValueError("a window that ends at the diagonal goes with mask causal_br")
     for name, n in (("the window", window_left), ("max_seqlen_q", max_seqlen_q), ("max_seqlen_kv", max_seqlen_kv or 0)):
         if not -2 ** 31 <= n < 2 ** 31:  # the struct's field would keep its low bits
             raise ValueError(f"{name} must fit 32 bits, got {n}")
@@ -856,7 +858,7 @@ def sdpa_paged_fwd(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens_q, *, m
     kv_lens int32 [batch], the new tokens included; cu_seqlens_q int32
     [batch + 1]. max_seqlen_q, max_seqlen_kv: the most new tokens and the
     longest kv_len (default: what the block table can hold). mask: "causal_br"
-    or "none"; window = (left, -1 or 0). Returns (o [T, Hq, Dv], lse float32
+    or "none"; window = (left, -1 or 0), with "none" (-1, -1). Returns (o [T, Hq, Dv], lse float32
     [T, Hq]); rows behind the last sequence are left as they are. A workspace
     of PAGED_WORKSPACE_MAX bytes serves every shape."""
     if stream is not None:

@@ -347,3 +347,16 @@ def test_a_table_of_more_keys_than_a_sequence_can_have(monkeypatch):
         table = (torch.Size((3, cols)), (cols, 1), torch.int32, c["q"].device)
         p, need = sdpa._paged_plan(q, cache, cache, table, lens, cu, 2, None, "nhd", "causal_br", -1, -1, None, None, None)
         assert p.seqlen_kv == 1 << 30 and sdpa.sdpa_check_paged(p) == 0 and need > 0
+
+
+def test_a_right_bound_without_a_causal_mask_is_refused(monkeypatch):
+    """sdpa_fwd hides the keys right of the diagonal then; the paged call has no such mask and saw them all."""
+    seen = []
+    monkeypatch.setattr(sdpa, "_refuse_cpu", lambda t: None)
+    monkeypatch.setattr(sdpa, "_launch", lambda name, device, *args: seen.append(name))
+    for window in ((-1, -1), (-1, 0), (3, 0)):
+        _paged(_batch(), window=window)
+    _paged(_batch(), mask="none")
+    assert len(seen) == 4
+    with pytest.raises(ValueError, match="causal_br"):
+        _paged(_batch(), mask="none", window=(-1, 0))
