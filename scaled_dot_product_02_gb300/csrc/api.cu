@@ -486,17 +486,27 @@ PagedCutting paged_cutting(const sdpa_paged_problem* p, int n, int q_rows, int m
     c.tail = 0;
   } else {
     // Whole items by ticket keep the CTAs on the same keys (with all items cut into equal shares, 2048 tokens over
-    // 131072 keys took 14 % longer, 8 x 1024 over 32768 41 %). The last, uneven round costs half an item on average:
-    // it is cut into shares where items are few and long enough to pay for the join (2048 tokens over 16384 keys, 3.4
-    // rounds: D192 643 -> 580 us, D512 1244 -> 1125 us; at head_dim 128, 2048 over 131072, 1.7 rounds: 2856 -> 2708
-    // us, but 8 x 512 over 4096 to 8192, 3.4 rounds: 285 -> 306 us). Items for at most half of the SMs are cut when
-    // much shorter (head_dim 256, 16 tokens over 4096 keys, one item: 66 -> 25 us; head_dim 128, 64 tokens on 8 kv
-    // heads over 2048 keys 35 -> 31 us, over 8192 100 -> 46 us; but 128 items of 16 tiles: 43 -> 80 us). A share for
-    // every CTA where all items are cut: 17 sequences at head_dim 256, 163 -> 143 us against two.
+    // 131072 keys took 14 % longer, 8 x 1024 over 32768 41 %). The last, uneven round is cut into shares where it leaves
+    // enough SMs idle, for long enough to pay for the join. Whole -> cut in us, by items of the batch and key tiles:
+    //   up to half of the SMs   192/128: 56 items of 16 tiles 32 -> 35, of 32 54 -> 41; 256: 72 of 20 46 -> 57, of 48 93 ->
+    //                           83; 128 (256-row items): 24 of 16 36 -> 41, of 32 58 -> 44; 72 of 32 58 -> 62, of 48 79 -> 71
+    //   up to two thirds        192/128: 88 of 48 74 -> 64; 256: 93 -> 96; 512: 126 -> 116
+    //   at most 3/4 full, long  192/128: 104 of 96 136 -> 116, 248 of 64 173 -> 174, of 96 257 -> 241; 256: 104 of 64 122 ->
+    //                           126, of 96 175 -> 166; but 512: 136 of 96 259 -> 316, 288 of 96 492 -> 537
+    //   at most half full       192/128: 224 of 32 99 -> 104, of 48 140 -> 136; 512: 512 of 48 482 -> 460; but 256: 576 of 64
+    //                           451 -> 509 (79 % full), 896 of 48 525 -> 549 (89 %)
+    //   128, up to two rounds   200 of 64 176 -> 178, of 256 715 -> 557; 256 of 256 727 -> 700; but 136 of 256 375 -> 404,
+    //                           296 of 256 768 -> 798
+    // A share for every CTA where all items are cut: 17 sequences at head_dim 256, 163 -> 143 us against two.
     c.split = false;
-    const bool cut = items * 2 <= most  ? tiles >= 16
-                     : items < most * 2 ? tiles >= (n == 256 ? 256 : 48)
-                                        : n != 256 && tiles >= 48 && items < 6 * most;
+    const long long rest = items % most, start = std::max(16LL, items * 2 / 5 + (n == 256 ? 8 : 0));
+    bool cut = false;
+    if (items * 2 <= most)
+      cut = tiles >= start;
+    else if (items < most * 2 && rest * 4 <= most * 3 && tiles >= (n == 256 ? 256 : 96))
+      cut = true;
+    else if (n == 128)
+      cut = tiles >= 48 && (items < most ? items * 3 <= most * 2 : items < most * 6 && rest * 2 <= most);
     c.tail = !cut ? 0 : items < most ? most : 2 * most;
   }
   // the length of a block and the ticket counter are 32-bit numbers

@@ -514,16 +514,39 @@ def test_a_scale_of_zero(d, page, order, dtype, causal, window):
 
 @pytest.mark.parametrize("d", [128, 192])
 @pytest.mark.parametrize("n", [3, 31, 32, 33, 64, 65])
+@pytest.mark.parametrize("hkv", [2, 4])
 @pytest.mark.parametrize("cut", [False, True])
-def test_ticket_order_on_both_sides_of_sorting(d, n, cut):
+def test_ticket_order_on_both_sides_of_sorting(d, n, hkv, cut):
     """Sorted by their keys up to 32 sequences, in their own order above, 32 of them a step; equal lengths and empty
     sequences among them, whole items alone or the last ones cut into shares."""
     rng = np.random.default_rng(n)
     new = rng.integers(0, 60, n)
     new[:2] = 59
     total = np.maximum(new, rng.integers(0, 4, n) * 170 + 5)
-    c = case(new.tolist(), total.tolist(), hq=8, hkv=4, d=d, page=16, pad=2, max_kv=33000 if cut else 0)
+    c = case(new.tolist(), total.tolist(), hq=8, hkv=hkv, d=d, page=16, pad=2, max_kv=33000 if cut else 0)
     a, b = call(c), call(c)
     live = int(c["cu"][-1])
     assert torch.equal(a[0][:live], b[0][:live]) and torch.equal(a[1][:live], b[1][:live])
+    check(c, *a)
+
+
+@pytest.mark.parametrize("d,items,tiles,cut", [
+    (d, *x) for d in (192, 256, 512) for x in (
+        (24, 15, False), (24, 16, True), (72, 27, False), (72, 28, True), (88, 47, False), (88, 48, True), (104, 95, False),
+        (104, 96, True), (136, 300, False), (176, 47, False), (176, 48, True), (248, 95, False), (248, 96, True),
+        (288, 300, False), (512, 48, True), (576, 300, False), (912, 300, False))
+] + [(128, *x) for x in ((24, 16, False), (24, 17, True), (72, 35, False), (72, 36, True), (88, 255, False), (88, 256, True),
+                         (136, 300, False), (168, 256, True), (256, 256, True), (288, 300, False), (512, 300, False))])
+def test_which_chunks_are_cut(d, items, tiles, cut, monkeypatch):
+    """Both sides of every border of the rule, by the number of items and the bound of the lengths; whole items need no
+    more than the counters' 256 bytes of workspace."""
+    heads = 4 if d == 512 else 8  # at 512 an item has half of the value columns
+    n = items // 8
+    rng = np.random.default_rng(items + tiles)
+    total = rng.integers(70, 400, n)
+    total[0] = 1900
+    c = case([70] * n, total.tolist(), hq=heads, hkv=heads, d=d, page=32, max_kv=tiles * 128)
+    assert (sdpa.sdpa_paged_fwd_workspace_size(bare_call(c, monkeypatch)) > 256) == cut
+    a, b = call(c), call(c)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
     check(c, *a)
