@@ -218,10 +218,10 @@ SDPA_API int sdpa_bwd_noalloc(const sdpa_problem* p, const void* q, const void* 
 
 /* Testing aid, off by default: caps how many CTAs any tcgen05 kernel of the
  * library has in flight at once (0 = no cap, the default; negative:
- * SDPA_ERR_INVALID_ARG). The persistent head_dim 128 forward launches at most
- * max_ctas CTAs, which then take every query tile from the ticket counter;
- * every other attention kernel is launched as successive grids of at most
- * max_ctas CTAs. Results must not depend on the cap (dQ of the head_dim 128
+ * SDPA_ERR_INVALID_ARG). The persistent kernels (the head_dim 128 forward and the
+ * paged-cache attention) launch at most max_ctas CTAs, which then take all of the
+ * work; every other attention kernel is launched as successive grids of at most
+ * max_ctas CTAs (norms, appends and joins of partial results are not capped). Results must not depend on the cap (dQ of the head_dim 128
  * backward with deterministic = 0 only up to the order of its fp32
  * reductions): it reschedules the same work, which is how a test shakes out
  * ordering, ticket, queue and barrier-phase assumptions that element-wise
@@ -398,7 +398,11 @@ typedef struct {
   long long table_stride;  /* elements between rows of block_table; 0 = max_pages */
   long long k_page_stride, k_slot_stride, k_head_stride;
   long long v_page_stride, v_slot_stride, v_head_stride;
-  long long q_stride, k_stride, v_stride;  /* elements between tokens of q, k, v (multiples of 8); 0 = contiguous */
+  long long q_stride, k_stride, v_stride;  /* elements between tokens of q, k, v (multiples of 8); 0 = contiguous.
+                                              sdpa_paged_fwd wants q_stride a multiple of head_dim, as a tensor
+                                              map's strides are multiples of one another, and returns
+                                              SDPA_ERR_UNSUPPORTED otherwise (a slice of a 192/128 projection may
+                                              be that: copy it, or take the append's q_out) */
 } sdpa_paged_problem;
 
 /* Writes the new tokens' K [total_q][Hkv][D] and V [total_q][Hkv][Dv] rows into their pages;

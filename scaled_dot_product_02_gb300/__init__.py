@@ -858,9 +858,10 @@ def sdpa_paged_fwd(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens_q, *, m
     kv_lens int32 [batch], the new tokens included; cu_seqlens_q int32
     [batch + 1]. max_seqlen_q, max_seqlen_kv: the most new tokens and the
     longest kv_len (default: what the block table can hold). mask: "causal_br"
-    or "none"; window = (left, -1 or 0), with "none" (-1, -1). Returns (o [T, Hq, Dv], lse float32
-    [T, Hq]); rows behind the last sequence are left as they are. A workspace
-    of PAGED_WORKSPACE_MAX bytes serves every shape."""
+    or "none"; window = (left, -1 or 0), with "none" (-1, -1). q may be a slice
+    of wider rows whose spacing is a multiple of D elements. Returns (o [T, Hq,
+    Dv], lse float32 [T, Hq]); rows behind the last sequence are left as they
+    are. A workspace of PAGED_WORKSPACE_MAX bytes serves every shape."""
     if stream is not None:
         return _on(stream, sdpa_paged_fwd, locals())
     p, need = _paged_plan(_meta(q), _meta(k_cache), _meta(v_cache), _meta(block_table), _meta(kv_lens),

@@ -27,9 +27,9 @@
 // stages (128 keys x 128 columns); S^T and P are double-buffered, so S^T of the
 // next tile is formed while the softmax works on this one.
 //
-// Measured with the join: that batch 344 to 356 us, 6.3 TB/s; 48 sequences at
+// Measured with the join: that batch 338 to 356 us, 6.2 to 6.5 TB/s; 48 sequences at
 // head_dim 256 with a window of 1024 70 to 73 us, 5.2 TB/s; one token over 999 keys
-// 9.1 to 9.5 us in a captured graph.
+// 9.1 to 9.6 us in a captured graph.
 #include <algorithm>
 #include <cuda.h>
 #include <cuda_runtime.h>

@@ -1,9 +1,9 @@
 // paged_chunk.cu -- attention over a paged cache for sequences with many new
 // tokens (chunks of a prompt) at head dims 192 to 512 (paged_pair.cu serves 128):
 // the work is bound by the tensor pipe and by K and V on their way from the L2 (at
-// 512 a tile of 192 KB for 128 rows). Measured: 4 x 1024 tokens over 32768 keys at
-// head_dim 256 1.64 ms, 1.32 PFLOP/s, at 512 4.55 ms, 0.95 PFLOP/s; 2048 over 16384
-// at 192/128 0.58 ms, 1.11 PFLOP/s.
+// 512 a tile of 192 KB for 128 rows). Measured, pages of 64: 4 x 1024 tokens over
+// 32768 keys at head_dim 256 1.60 ms, 1.36 PFLOP/s, at 512 4.52 ms, 0.96 PFLOP/s; 2048
+// over 16384 at 192/128 0.58 ms, 1.12 PFLOP/s (0.63 ms with pages of 32).
 //
 // An item is 128 query rows that share one kv head (tokens times the heads of
 // its GQA group, so a tile of keys serves the whole group) and, for head_dim

@@ -14,9 +14,9 @@
 // half a period apart. A block of fewer tokens than one tile holds leaves the
 // second half out.
 //
-// Measured, 32 query heads on 8 kv heads: 2048 tokens over 16384 keys 374 us, 1.38
-// PFLOP/s (256 items on 152 SMs, two rounds); 8 x 1024 over 32768 2.6 ms, 1.66
-// PFLOP/s; 2048 over 131072 2.73 ms, 1.60 PFLOP/s.
+// Measured, 32 query heads on 8 kv heads: 2048 tokens over 16384 keys 371 us, 1.39
+// PFLOP/s (256 items on 152 SMs, two rounds); 8 x 1024 over 32768 2.6 ms, 1.68
+// PFLOP/s; 2048 over 131072 2.72 ms, 1.60 PFLOP/s.
 #include <algorithm>
 #include <cuda.h>
 #include <cuda_runtime.h>
