@@ -221,7 +221,8 @@ SDPA_API int sdpa_bwd_noalloc(const sdpa_problem* p, const void* q, const void* 
  * SDPA_ERR_INVALID_ARG). The persistent kernels (the head_dim 128 forward and the
  * paged-cache attention) launch at most max_ctas CTAs, which then take all of the
  * work; every other attention kernel is launched as successive grids of at most
- * max_ctas CTAs (norms, appends and joins of partial results are not capped). Results must not depend on the cap (dQ of the head_dim 128
+ * max_ctas CTAs (norms, appends and joins of partial results are not capped).
+ * Results must not depend on the cap (dQ of the head_dim 128
  * backward with deterministic = 0 only up to the order of its fp32
  * reductions): it reschedules the same work, which is how a test shakes out
  * ordering, ticket, queue and barrier-phase assumptions that element-wise

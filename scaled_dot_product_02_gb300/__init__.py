@@ -757,7 +757,8 @@ def _paged_problem(q, hq, k_cache, v_cache, block_table, kv_lens, cu_seqlens_q, 
     # a dimension of one entry may carry any stride: its own row's width stands for it
     return PagedProblem(_dtype_code(dtype, "q"), batch, hq, hkv, d, dv, total_q, seqlen_q,
                         min(max_pages * ks[slot], PAGED_KEYS_MAX) if seqlen_kv is None else seqlen_kv, ks[slot], pages,
-                        max_pages, mask_type, window_left, scale, tab_st[0] if batch > 1 else 0, k_st[0] if pages > 1 else d, k_st[slot],
+                        max_pages, mask_type, window_left, scale, tab_st[0] if batch > 1 else 0,
+                        k_st[0] if pages > 1 else d, k_st[slot],
                         k_st[head] if hkv > 1 else d, v_st[0] if pages > 1 else dv, v_st[slot],
                         v_st[head] if hkv > 1 else dv, q_stride, k_stride, v_stride)
 
