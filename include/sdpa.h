@@ -368,6 +368,29 @@ SDPA_API int sdpa_qk_norm_rope_bwd(const sdpa_norm_rope_problem* p, const void* 
                                    const float* cos_sin, const int32_t* positions, void* dq, void* dk,
                                    float* dq_weight, float* dk_weight, void* workspace, size_t ws_bytes, void* stream);
 
+/* Rotation with several positions a token (images and video: time, height, width). The pairs of a
+ * row are divided between the axes in order: the first pairs[0] of them turn by the angles of the
+ * token's position on axis 0, the next pairs[1] by those on axis 1, and so on; pair i's angle is
+ * always column i of cos_sin, taken from the row of its axis's position. positions holds the axes'
+ * rows [num_axes][rows], position_stride elements apart. pairs sum to rotary_dim / 2, each at
+ * least 1, and need no alignment. A token with any position outside [0, max_positions) is treated as
+ * sdpa_qk_norm_rope treats one. */
+#define SDPA_ROPE_AXES_MAX 4
+typedef struct {
+  int num_axes;                    /* 1 .. SDPA_ROPE_AXES_MAX */
+  int pairs[SDPA_ROPE_AXES_MAX];   /* of each axis */
+  long long position_stride;       /* elements between axes; 0 = rows (of the append: total_q) */
+} sdpa_rope_axes;
+/* sdpa_qk_norm_rope and its backward with several axes; workspace and results as there. */
+SDPA_API int sdpa_qk_norm_rope_axes(const sdpa_norm_rope_problem* p, const sdpa_rope_axes* axes, const void* q,
+                                    const void* k, const void* q_weight, const void* k_weight, const float* cos_sin,
+                                    const int32_t* positions, void* q_out, void* k_out, void* stream);
+SDPA_API int sdpa_qk_norm_rope_axes_bwd(const sdpa_norm_rope_problem* p, const sdpa_rope_axes* axes, const void* dq_out,
+                                        const void* dk_out, const void* q, const void* k, const void* q_weight,
+                                        const void* k_weight, const float* cos_sin, const int32_t* positions, void* dq,
+                                        void* dk, float* dq_weight, float* dk_weight, void* workspace, size_t ws_bytes,
+                                        void* stream);
+
 /* A paged key/value cache and a batch of new tokens over it.
  * Cache: num_pages pages of page_size slots. Slot s, head h of page g of K starts at element
  *   g * k_page_stride + s * k_slot_stride + h * k_head_stride (head_dim contiguous values; V
@@ -422,6 +445,14 @@ SDPA_API int sdpa_paged_append(const sdpa_paged_problem* p, const sdpa_norm_rope
                                void* v_cache, const int32_t* cu_seqlens_q, const int32_t* kv_lens,
                                const int32_t* block_table, void* stream);
 
+/* The same with several axes; positions are required (a cache position has no axes). */
+SDPA_API int sdpa_paged_append_axes(const sdpa_paged_problem* p, const sdpa_norm_rope_problem* n,
+                                    const sdpa_rope_axes* axes, const void* q, const void* k, const void* v,
+                                    const void* q_weight, const void* k_weight, const float* cos_sin,
+                                    const int32_t* positions, void* q_out, void* k_cache, void* v_cache,
+                                    const int32_t* cu_seqlens_q, const int32_t* kv_lens, const int32_t* block_table,
+                                    void* stream);
+
 /* Attention of the new tokens over the cache (their own keys and values already in it):
  *   S = softmax_scale Q K^T, masked; O = softmax(S) V; LSE = ln sum_j exp(S_ij)
  * for single tokens (decoding), chunks of a prompt, and batches that mix them. q
@@ -443,6 +474,52 @@ SDPA_API int sdpa_paged_fwd(const sdpa_paged_problem* p, const void* q, const vo
                             void* o, float* lse, const int32_t* cu_seqlens_q, const int32_t* kv_lens,
                             const int32_t* block_table, void* workspace, size_t ws_bytes, void* stream);
 
+/* ---- a paged cache in 8 bits
+ * K and V as E4M3 codes (one byte a value, the finite-only format of sdpa_fwd_fp8) with one scale
+ * byte for every row (one head of one slot): value = code * 2^(byte - 127). A row's exponent is
+ * the least e with max |x| <= 448 * 2^e, kept within -80 .. 80 (SDPA_BF16) or -15 .. 7 (SDPA_FP16): a
+ * row's values are then exact in the 16-bit type, and larger ones saturate at 448 * 2^80 or 57344.
+ * NaN stays NaN. The fields of sdpa_paged_problem mean the same as for a 16-bit cache, with cache
+ * strides in codes and multiples of 16; dtype is the type of q, k, v and o. */
+typedef struct {
+  uint8_t* k;  /* byte of slot s, head h, page g: g * k_page_stride + s * k_slot_stride + h * k_head_stride */
+  uint8_t* v;
+  long long k_page_stride, k_slot_stride, k_head_stride;  /* bytes, at least 1 */
+  long long v_page_stride, v_slot_stride, v_head_stride;
+} sdpa_paged_scales;
+
+/* sdpa_paged_append into an 8-bit cache: rows are quantised as they are written, K from the fp32
+ * values of the norm and rotation where n is given. axes: several positions a token, or NULL. Codes
+ * and scale bytes may interleave (blocks that hold a page's K, V and scales) but not share bytes. */
+SDPA_API int sdpa_paged_append_fp8(const sdpa_paged_problem* p, const sdpa_norm_rope_problem* n,
+                                   const sdpa_rope_axes* axes, const sdpa_paged_scales* scales, const void* q,
+                                   const void* k, const void* v, const void* q_weight, const void* k_weight,
+                                   const float* cos_sin, const int32_t* positions, void* q_out, void* k_cache,
+                                   void* v_cache, const int32_t* cu_seqlens_q, const int32_t* kv_lens,
+                                   const int32_t* block_table, void* stream);
+
+/* The last keys and values of every sequence as packed 16-bit rows: rows cu_seqlens[b] ..
+ * cu_seqlens[b+1]-1 of k_out [total_q][Hkv][D] and v_out [total_q][Hkv][Dv] (dtype; rows k_stride
+ * and v_stride elements apart) receive sequence b's last cu_seqlens[b+1] - cu_seqlens[b] keys, of the
+ * kv_lens[b] it has -- all of them, the new tokens' (cu_seqlens_q), a window's. Each value is rounded
+ * once to dtype (exact in the type it was appended from). Rows from cu_seqlens[batch] on are left as
+ * they are. A row is skipped, and the device error word set, as a token of the append is. With the
+ * rows read back a prompt's chunk can run on sdpa_fwd (SDPA_THD, bottom-right). seqlen_q, seqlen_kv, masks and
+ * scale are checked but not used. One launch. */
+SDPA_API int sdpa_paged_read_fp8(const sdpa_paged_problem* p, const sdpa_paged_scales* scales, const void* k_cache,
+                                 const void* v_cache, void* k_out, void* v_out, const int32_t* cu_seqlens,
+                                 const int32_t* kv_lens, const int32_t* block_table, void* stream);
+
+/* sdpa_paged_fwd over an 8-bit cache: the attention over the values that codes and scales stand for,
+ * exactly (q stays 16-bit), with the same masks, outputs, errors and workspace rules. Scale bytes of
+ * keys that no query row sees may hold anything. Of the others 255 counts as infinite, 0 as zero. A row of q that
+ * is not finite gives NaN. */
+SDPA_API size_t sdpa_paged_fwd_fp8_workspace_size(const sdpa_paged_problem* p);
+SDPA_API int sdpa_paged_fwd_fp8(const sdpa_paged_problem* p, const sdpa_paged_scales* scales, const void* q,
+                                const void* k_cache, const void* v_cache, void* o, float* lse,
+                                const int32_t* cu_seqlens_q, const int32_t* kv_lens, const int32_t* block_table,
+                                void* workspace, size_t ws_bytes, void* stream);
+
 /* Kernel timing for benchmarks and tracing. Between sdpa_profile_begin and
  * sdpa_profile_end, every sdpa_fwd / sdpa_bwd call made by this host thread
  * (and sdpa_merge) records a pair of CUDA events on its stream around each kernel it
@@ -461,7 +538,8 @@ typedef enum {
   SDPA_KERNEL_NORM_ROPE = 8,   /* per-head norm + rotation, forward or backward */
   SDPA_KERNEL_APPEND = 9,      /* new rows into their pages (with the norm + rotation when fused) */
   SDPA_KERNEL_PAGED = 10,      /* attention over the paged cache, the join of its partial results included */
-  SDPA_KERNEL_KINDS = 11
+  SDPA_KERNEL_READ = 11,       /* rows of an 8-bit paged cache read back */
+  SDPA_KERNEL_KINDS = 12
 } sdpa_kernel_kind;
 SDPA_API int sdpa_profile_begin(void);
 SDPA_API int sdpa_profile_end(double* ms_by_kind, int* launches_by_kind, int n_kinds);

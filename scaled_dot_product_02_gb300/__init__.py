@@ -36,12 +36,14 @@ EXPORTS = ("sdpa_fwd_workspace_size", "sdpa_bwd_workspace_size", "sdpa_check_pro
            "sdpa_fwd_fp8_workspace_size", "sdpa_fwd_fp8", "sdpa_debug_set_max_ctas", "sdpa_debug_address_report",
            "sdpa_debug_address_shrink", "sdpa_qk_norm_rope", "sdpa_qk_norm_rope_bwd_workspace_size",
            "sdpa_qk_norm_rope_bwd", "sdpa_check_paged", "sdpa_paged_append", "sdpa_paged_fwd_workspace_size",
-           "sdpa_paged_fwd")
+           "sdpa_paged_fwd", "sdpa_qk_norm_rope_axes", "sdpa_qk_norm_rope_axes_bwd", "sdpa_paged_append_axes",
+           "sdpa_paged_append_fp8", "sdpa_paged_read_fp8", "sdpa_paged_fwd_fp8_workspace_size", "sdpa_paged_fwd_fp8")
 NOALLOC_MAX_BYTES = 32 << 20  # SDPA_BWD_NOALLOC_MAX_BYTES
 PAGED_WORKSPACE_MAX = 256 << 20  # SDPA_PAGED_WORKSPACE_MAX
+ROPE_AXES_MAX = 4  # SDPA_ROPE_AXES_MAX
 PAGED_KEYS_MAX = 1 << 30  # the longest kv_len that the library serves
 KERNEL_KINDS = ("fwd", "bwd", "preprocess", "dq_finalize", "guard", "merge", "bwd_dq", "v_transpose",
-                "norm_rope", "append", "paged")
+                "norm_rope", "append", "paged", "read")
 
 
 class SdpaError(RuntimeError):
@@ -62,6 +64,19 @@ class NormRopeProblem(ctypes.Structure):
                                             "interleaved")] + [("eps", ctypes.c_float),
                                                                ("max_positions", ctypes.c_int)] + [
         (n, ctypes.c_longlong) for n in ("rows", "q_stride", "k_stride", "dq_stride", "dk_stride")]
+
+
+class RopeAxes(ctypes.Structure):
+    """sdpa_rope_axes (include/sdpa.h)."""
+    _fields_ = [("num_axes", ctypes.c_int), ("pairs", ctypes.c_int * ROPE_AXES_MAX),
+                ("position_stride", ctypes.c_longlong)]
+
+
+class PagedScales(ctypes.Structure):
+    """sdpa_paged_scales (include/sdpa.h)."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p)] + [
+        (n, ctypes.c_longlong) for n in ("k_page_stride", "k_slot_stride", "k_head_stride", "v_page_stride",
+                                         "v_slot_stride", "v_head_stride")]
 
 
 class PagedProblem(ctypes.Structure):
@@ -129,6 +144,15 @@ def _load(path):
         L.sdpa_paged_fwd_workspace_size.argtypes = [ppp]
         L.sdpa_paged_fwd_workspace_size.restype = ctypes.c_size_t
         L.sdpa_paged_fwd.argtypes = [ppp] + [vp] * 9 + [ctypes.c_size_t, vp]
+        axp, scp = ctypes.POINTER(RopeAxes), ctypes.POINTER(PagedScales)
+        L.sdpa_qk_norm_rope_axes.argtypes = [npp, axp] + [vp] * 9
+        L.sdpa_qk_norm_rope_axes_bwd.argtypes = [npp, axp] + [vp] * 13 + [ctypes.c_size_t, vp]
+        L.sdpa_paged_append_axes.argtypes = [ppp, npp, axp] + [vp] * 14
+        L.sdpa_paged_append_fp8.argtypes = [ppp, npp, axp, scp] + [vp] * 14
+        L.sdpa_paged_read_fp8.argtypes = [ppp, scp] + [vp] * 8
+        L.sdpa_paged_fwd_fp8_workspace_size.argtypes = [ppp]
+        L.sdpa_paged_fwd_fp8_workspace_size.restype = ctypes.c_size_t
+        L.sdpa_paged_fwd_fp8.argtypes = [ppp, scp] + [vp] * 9 + [ctypes.c_size_t, vp]
         _libs[path] = L
     return _libs[path]
 
@@ -518,7 +542,8 @@ def _torch():
 
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
         like = functools.partial(torch.empty_like, memory_format=torch.contiguous_format)  # quicker than new_empty
-        _torch_state.update(torch=torch, like=like, codes={torch.bfloat16: 0, torch.float16: 1}, f32=torch.float32, i32=torch.int32,
+        _torch_state.update(torch=torch, like=like, codes={torch.bfloat16: 0, torch.float16: 1}, f32=torch.float32,
+                            i32=torch.int32, u8=torch.uint8,
                             raw=raw or (lambda index: torch.cuda.current_stream(index).cuda_stream))
     return _torch_state
 
@@ -622,17 +647,40 @@ def _rows_of_heads(name, meta, like=None):
     return rows, h, d, step if step is not None and rows else h * d
 
 
-def _rotation(q, d, rows, q_weight, k_weight, cos_sin, positions, needs_positions):
-    """(max_positions, rotary_dim) of the table; checks the weights, the table and the positions."""
+def _axes(sections):
+    """sections as a tuple of numbers (a key of the plans below); None: one position a token."""
+    return None if sections is None else tuple(int(x) for x in sections)
+
+
+def _rotation(q, d, rows, q_weight, k_weight, cos_sin, positions, needs_positions, sections):
+    """(max_positions, rotary_dim) of the table and the struct of its axes (None: one position a token); checks the
+    weights, the table and the positions."""
     _, _, dtype, dev = q
     _expect("q_weight", q_weight, (d,), dtype, dev)
     _expect("k_weight", k_weight, (d,), dtype, dev)
     if cos_sin is None:
-        return 0, 0
+        if sections is not None:
+            raise ValueError("sections go with cos_sin")
+        return 0, 0, None
     shape = cos_sin[0]
     if len(shape) != 2:
         raise ValueError(f"cos_sin must be [positions, rotary_dim], got {tuple(shape)}")
     _expect("cos_sin", cos_sin, shape, _torch()["f32"], dev)
+    axes = None
+    if sections is not None:
+        if not 1 <= len(sections) <= ROPE_AXES_MAX or min(sections) < 1 or 2 * sum(sections) != shape[1]:
+            raise ValueError(f"sections must be 1 to {ROPE_AXES_MAX} numbers of pairs that sum to rotary_dim / 2 = "
+                             f"{shape[1] / 2:g}, got {sections}")
+        if positions is None:
+            raise ValueError("a rotation with sections needs the tokens' positions on every axis")
+        got, st, got_dtype, got_dev = positions
+        if len(got) < 2 or got[0] != len(sections):
+            raise ValueError(f"positions must be [{len(sections)}, tokens], got {tuple(got)}")
+        stride = st[0] if len(sections) > 1 and rows else rows  # between the axes' rows, which are contiguous
+        if stride < rows:
+            raise ValueError(f"the axes of positions may not overlap: {rows} tokens, strides {tuple(st)}")
+        axes = RopeAxes(len(sections), (ctypes.c_int * ROPE_AXES_MAX)(*sections), stride)
+        positions = (got[1:], st[1:], got_dtype, got_dev)
     if positions is not None:
         n = 1
         for x in positions[0]:
@@ -642,19 +690,23 @@ def _rotation(q, d, rows, q_weight, k_weight, cos_sin, positions, needs_position
         _expect("positions", positions, positions[0], _torch()["i32"], dev)
     elif needs_positions and shape[1]:
         raise ValueError("a rotation needs the tokens' positions")
-    return shape
+    return (*shape, axes)
+
+
+def _ref(struct):
+    return None if struct is None else ctypes.byref(struct)
 
 
 @functools.lru_cache(maxsize=_PLANS)
 def _norm_rope_plan(q, k, q_weight, k_weight, cos_sin, positions, q_out, k_out, dq, dk, dq_out, dk_out, dq_weight,
-                    dk_weight, eps, interleaved):
-    """The struct of a norm + rotation call and its gradient's workspace size, from the tensors' metadata (an
-    output that is None is allocated by the caller)."""
+                    dk_weight, eps, interleaved, sections):
+    """The structs of a norm + rotation call (the axes' None with one position a token) and its gradient's workspace
+    size, from the tensors' metadata (an output that is None is allocated by the caller)."""
     rows, hq, d, qs = _rows_of_heads("q", q)
     _, hkv, d_k, ks = _rows_of_heads("k", k, q)
     if d_k != d or q[0][:-2] != k[0][:-2]:
         raise ValueError(f"q and k must agree on every dimension but the heads, got {tuple(q[0])} and {tuple(k[0])}")
-    max_pos, rot = _rotation(q, d, rows, q_weight, k_weight, cos_sin, positions, True)
+    max_pos, rot, axes = _rotation(q, d, rows, q_weight, k_weight, cos_sin, positions, True, sections)
     _, _, dtype, dev = q
     for name, t, like in (("q_out", q_out, q), ("k_out", k_out, k), ("dq_out", dq_out, q), ("dk_out", dk_out, k)):
         if t is not None:
@@ -669,35 +721,39 @@ def _norm_rope_plan(q, k, q_weight, k_weight, cos_sin, positions, q_out, k_out, 
             _expect(name, t, (d,), _torch()["f32"], dev)
     p = NormRopeProblem(_dtype_code(dtype, "q"), hq, hkv, d, rot, 1 if interleaved else 0, eps, max_pos, rows, qs, ks,
                         *strides)
-    return p, int(lib().sdpa_qk_norm_rope_bwd_workspace_size(ctypes.byref(p)))
+    return p, axes, int(lib().sdpa_qk_norm_rope_bwd_workspace_size(ctypes.byref(p)))
 
 
-def sdpa_qk_norm_rope(q, k, q_weight, k_weight, cos_sin=None, positions=None, *, eps=1e-6, interleaved=False, q_out=None,
-                      k_out=None, stream=None):
+def sdpa_qk_norm_rope(q, k, q_weight, k_weight, cos_sin=None, positions=None, *, eps=1e-6, interleaved=False, sections=None,
+                      q_out=None, k_out=None, stream=None):
     """Per-head norm of q [..., Hq, D] and k [..., Hkv, D] with the position
     rotation in the same pass (sdpa_qk_norm_rope in include/sdpa.h). Any
     layout's tensors do: the leading dimensions are the tokens. q and k may be
     slices of one projection's output. q_weight, k_weight: [D] of q's dtype.
     cos_sin: float32 [positions, rotary_dim], half cosines and half sines, or
-    None for the norm alone; positions: int32, one per token. Returns
+    None for the norm alone; positions: int32, one per token. sections: several
+    positions a token (time, height, width): the numbers of pairs, in order,
+    that turn by each axis's position; positions is then [axes, tokens]. Returns
     contiguous (q_out, k_out)."""
     if stream is not None:
         return _on(stream, sdpa_qk_norm_rope, locals())
-    p, _ = _norm_rope_plan(_meta(q), _meta(k), _meta(q_weight), _meta(k_weight), _meta(cos_sin), _meta(positions),
-                           _meta(q_out), _meta(k_out), None, None, None, None, None, None, float(eps), bool(interleaved))
+    p, axes, _ = _norm_rope_plan(_meta(q), _meta(k), _meta(q_weight), _meta(k_weight), _meta(cos_sin), _meta(positions),
+                                 _meta(q_out), _meta(k_out), None, None, None, None, None, None, float(eps),
+                                 bool(interleaved), _axes(sections))
     _refuse_cpu(q)
     like = _torch_state["like"]
     if q_out is None:
         q_out = like(q)
     if k_out is None:
         k_out = like(k)
-    _launch("sdpa_qk_norm_rope", q.device, ctypes.byref(p), q.data_ptr(), k.data_ptr(), q_weight.data_ptr(),
+    entry = ("sdpa_qk_norm_rope",) if axes is None else ("sdpa_qk_norm_rope_axes", ctypes.byref(axes))
+    _launch(entry[0], q.device, ctypes.byref(p), *entry[1:], q.data_ptr(), k.data_ptr(), q_weight.data_ptr(),
             k_weight.data_ptr(), _addr(cos_sin), _addr(positions), q_out.data_ptr(), k_out.data_ptr())
     return q_out, k_out
 
 
 def sdpa_qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, cos_sin=None, positions=None, *, eps=1e-6,
-                          interleaved=False, dq=None, dk=None, dq_weight=None, dk_weight=None, workspace=None,
+                          interleaved=False, sections=None, dq=None, dk=None, dq_weight=None, dk_weight=None, workspace=None,
                           stream=None):
     """Gradient of sdpa_qk_norm_rope: from the (contiguous) gradients of its
     outputs and its inputs, returns (dq, dk, dq_weight, dk_weight), the weights'
@@ -705,9 +761,9 @@ def sdpa_qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, cos_sin=None
     reproducible."""
     if stream is not None:
         return _on(stream, sdpa_qk_norm_rope_bwd, locals())
-    p, need = _norm_rope_plan(_meta(q), _meta(k), _meta(q_weight), _meta(k_weight), _meta(cos_sin), _meta(positions),
-                              None, None, _meta(dq), _meta(dk), _meta(dq_out), _meta(dk_out), _meta(dq_weight),
-                              _meta(dk_weight), float(eps), bool(interleaved))
+    p, axes, need = _norm_rope_plan(_meta(q), _meta(k), _meta(q_weight), _meta(k_weight), _meta(cos_sin),
+                                    _meta(positions), None, None, _meta(dq), _meta(dk), _meta(dq_out), _meta(dk_out),
+                                    _meta(dq_weight), _meta(dk_weight), float(eps), bool(interleaved), _axes(sections))
     _refuse_cpu(q)
     dev, f32 = q.device, _torch_state["f32"]
     like = _torch_state["like"]
@@ -719,7 +775,8 @@ def sdpa_qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, cos_sin=None
         workspace = dq_weight.new_empty(max(need // 4, 4))
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {dev}")
-    _launch("sdpa_qk_norm_rope_bwd", dev, ctypes.byref(p), dq_out.data_ptr(), dk_out.data_ptr(), q.data_ptr(),
+    entry = ("sdpa_qk_norm_rope_bwd",) if axes is None else ("sdpa_qk_norm_rope_axes_bwd", ctypes.byref(axes))
+    _launch(entry[0], dev, ctypes.byref(p), *entry[1:], dq_out.data_ptr(), dk_out.data_ptr(), q.data_ptr(),
             k.data_ptr(), q_weight.data_ptr(), k_weight.data_ptr(), _addr(cos_sin), _addr(positions), dq.data_ptr(),
             dk.data_ptr(), dq_weight.data_ptr(), dk_weight.data_ptr(), workspace.data_ptr(), workspace.nbytes)
     return dq, dk, dq_weight, dk_weight
@@ -729,17 +786,18 @@ CACHE_LAYOUTS = ("nhd", "hnd")  # [pages, page_size, Hkv, D] and [pages, Hkv, pa
 
 
 def _paged_problem(q, hq, k_cache, v_cache, block_table, kv_lens, cu_seqlens_q, cache_layout, total_q, seqlen_q, seqlen_kv,
-                   mask_type, window_left, scale, q_stride, k_stride, v_stride) -> PagedProblem:
+                   mask_type, window_left, scale, q_stride, k_stride, v_stride, codes=None) -> PagedProblem:
     """sdpa_paged_problem of a batch over a cache, checked from the tensors'
     metadata. Cache strides are free but for contiguous head_dim, so a cache
-    may be a slice of a larger tensor."""
+    may be a slice of a larger tensor. codes: the caches' type when it is not q's."""
     if cache_layout not in CACHE_LAYOUTS:
         raise ValueError(f"cache_layout must be one of {CACHE_LAYOUTS}, got {cache_layout!r}")
     _, _, dtype, dev = q
     i32 = _torch()["i32"]
+    held = dtype if codes is None else codes
     for name, (shape, st, got, got_dev) in (("k_cache", k_cache), ("v_cache", v_cache)):
-        if len(shape) != 4 or got is not dtype or got_dev != dev or st[3] != 1:
-            raise ValueError(f"{name} must be a 4-dimensional {dtype} tensor on {dev} with contiguous head_dim, got "
+        if len(shape) != 4 or got is not held or got_dev != dev or st[3] != 1:
+            raise ValueError(f"{name} must be a 4-dimensional {held} tensor on {dev} with contiguous head_dim, got "
                              f"{got} {tuple(shape)} on {got_dev}")
     (ks, k_st), (vs, v_st) = k_cache[:2], v_cache[:2]
     if ks[:3] != vs[:3]:
@@ -765,38 +823,65 @@ def _paged_problem(q, hq, k_cache, v_cache, block_table, kv_lens, cu_seqlens_q, 
 
 @functools.lru_cache(maxsize=_PLANS)
 def _append_plan(k, v, k_cache, v_cache, block_table, kv_lens, cu_seqlens_q, cache_layout, q, q_weight, k_weight, cos_sin,
-                 positions, q_out, eps, interleaved):
-    """The structs of an append (the second None without q)."""
+                 positions, q_out, eps, interleaved, sections, k_scale=None, v_scale=None):
+    """The structs of an append: the problem, the norm and rotation (None without q), its axes (None with one position a
+    token) and the strides of the scale bytes (None for a 16-bit cache)."""
     rows, hkv, d, ks = _rows_of_heads("k", k)
     rows_v, hkv_v, dv, vs = _rows_of_heads("v", v, k)
     if len(k[0]) != 3 or len(v[0]) != 3 or rows != rows_v or hkv != hkv_v:
         raise ValueError(f"k and v must be [tokens, heads, width] of the same tokens and heads, got {tuple(k[0])} and "
                          f"{tuple(v[0])}")
-    hq, qs, n = hkv, 0, None
+    hq, qs, n, axes = hkv, 0, None, None
     if q is not None:
         rows_q, hq, d_q, qs = _rows_of_heads("q", q, k)
         if len(q[0]) != 3 or rows_q != rows or d_q != d:
             raise ValueError(f"q must be [tokens, heads, head_dim] of k's tokens and head_dim, got {tuple(q[0])}")
         if q_weight is None or k_weight is None:
             raise ValueError("q needs q_weight and k_weight")
-        max_pos, rot = _rotation(q, d, rows, q_weight, k_weight, cos_sin, positions, False)
+        max_pos, rot, axes = _rotation(q, d, rows, q_weight, k_weight, cos_sin, positions, False, sections)
         n = NormRopeProblem(0, 0, 0, 0, rot, 1 if interleaved else 0, eps, max_pos)
         if q_out is not None:
             _expect("q_out", q_out, q[0], q[2], q[3])
-    elif not (q_weight is k_weight is cos_sin is positions is q_out is None):
-        raise ValueError("weights, cos_sin, positions and q_out go with q")
+    elif not (q_weight is k_weight is cos_sin is positions is q_out is sections is None):
+        raise ValueError("weights, cos_sin, positions, sections and q_out go with q")
     p = _paged_problem(k, hq, k_cache, v_cache, block_table, kv_lens, cu_seqlens_q, cache_layout, rows, 0, 0,
-                       MASKS["none"], -1, 0.0, qs, ks, vs)
+                       MASKS["none"], -1, 0.0, qs, ks, vs, None if k_scale is None else _torch()["u8"])
     if p.num_heads_kv != hkv or p.head_dim != d or p.head_dim_v != dv:
         raise ValueError(f"k and v {tuple(k[0])}, {tuple(v[0])} do not fit the caches {tuple(k_cache[0])}, "
                          f"{tuple(v_cache[0])} in layout {cache_layout}")
-    return p, n
+    return p, n, axes, None if k_scale is None else _scale_strides(k_cache, k_scale, v_scale, cache_layout)
 
 
-@functools.lru_cache(maxsize=_PLANS)
-def _paged_plan(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens_q, max_seqlen_q, max_seqlen_kv, cache_layout, mask,
-                window_left, window_right, scale, out, lse):
-    """The struct of an attention call over a cache, and its workspace size."""
+def _scale_strides(cache, k_scale, v_scale, cache_layout):
+    """The strides of sdpa_paged_scales, checked: a byte for each row of the caches, [pages, slots, heads] in their
+    order."""
+    out = []
+    for name, (shape, st, got, got_dev) in (("k_scale", k_scale), ("v_scale", v_scale)):
+        if tuple(shape) != tuple(cache[0][:3]) or got is not _torch()["u8"] or got_dev != cache[3]:
+            raise ValueError(f"{name} must be a uint8 tensor of shape {tuple(cache[0][:3])} on {cache[3]}, got {got} "
+                             f"{tuple(shape)} on {got_dev}")
+        if any(n > 1 and x < 1 for n, x in zip(shape, st)):
+            raise ValueError(f"{name} may not be a broadcast tensor, got strides {tuple(st)}")
+        st = [x if n > 1 else 1 for n, x in zip(shape, st)]  # of a dimension of one entry any stride does
+        # ... but a dimension of one entry must not look smaller than what it holds
+        order = ("page", "slot", "head") if cache_layout == "nhd" else ("page", "head", "slot")
+        by = dict(zip(order, st))
+        sizes = dict(zip(order, shape))
+        if sizes["page"] == 1:
+            by["page"] = max(by["slot"] * sizes["slot"], by["head"] * sizes["head"])
+        if sizes["head"] == 1:
+            by["head"] = by["slot"] if cache_layout == "nhd" else by["slot"] * sizes["slot"]
+        out += [by["page"], by["slot"], by["head"]]
+    return tuple(out)
+
+
+def _scales(strides, k_scale, v_scale):
+    return PagedScales(k_scale.data_ptr(), v_scale.data_ptr(), *strides)
+
+
+def _paged_call(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens_q, max_seqlen_q, max_seqlen_kv, cache_layout, mask,
+                window_left, window_right, scale, out, lse, codes=None):
+    """The struct of an attention call over a cache of q's type, or of `codes`."""
     rows, hq, d, qs = _rows_of_heads("q", q)
     if len(q[0]) != 3:
         raise ValueError(f"q must be [tokens, heads, head_dim], got {tuple(q[0])}")
@@ -808,14 +893,50 @@ def _paged_plan(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens_q, max_seq
         if not -2 ** 31 <= n < 2 ** 31:  # the struct's field would keep its low bits
             raise ValueError(f"{name} must fit 32 bits, got {n}")
     p = _paged_problem(q, hq, k_cache, v_cache, block_table, kv_lens, cu_seqlens_q, cache_layout, rows, max_seqlen_q,
-                       max_seqlen_kv, MASKS[mask], window_left, d ** -0.5 if scale is None else scale, qs, 0, 0)
+                       max_seqlen_kv, MASKS[mask], window_left, d ** -0.5 if scale is None else scale, qs, 0, 0, codes)
     if p.head_dim != d or hq % p.num_heads_kv:
         raise ValueError(f"q {tuple(q[0])} does not fit the cache {tuple(k_cache[0])} in layout {cache_layout}")
     if out is not None:
         _expect("out", out, (rows, hq, p.head_dim_v), q[2], q[3])
     if lse is not None:
         _expect("lse", lse, (rows, hq), _torch()["f32"], q[3])
+    return p
+
+
+@functools.lru_cache(maxsize=_PLANS)
+def _paged_plan(*call):
+    """The struct of a call over a 16-bit cache (_paged_call's arguments) and its workspace size."""
+    p = _paged_call(*call)
     return p, sdpa_paged_fwd_workspace_size(p)
+
+
+@functools.lru_cache(maxsize=_PLANS)
+def _paged_fp8_plan(k_scale, v_scale, *call):
+    """The same of a call over a cache in 8 bits, and the strides of its scale bytes."""
+    p = _paged_call(*call, _torch()["u8"])
+    return p, sdpa_paged_fwd_fp8_workspace_size(p), _scale_strides(call[1], k_scale, v_scale, call[8])
+
+
+@functools.lru_cache(maxsize=_PLANS)
+def _read_plan(k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, cu_seqlens, cache_layout, rows, dtype, k_out, v_out):
+    """The struct of a read of `rows` rows in `dtype` and the strides of the scale bytes."""
+    shape, _, _, dev = k_cache
+    like = ((), (), dtype, dev)
+    strides = []
+    if len(shape) != 4 or len(v_cache[0]) != 4:
+        raise ValueError(f"the caches must have 4 dimensions, got {tuple(shape)} and {tuple(v_cache[0])}")
+    hkv = shape[2 if cache_layout == "nhd" else 1]
+    for name, t, width in (("k_out", k_out, shape[3]), ("v_out", v_out, v_cache[0][3])):
+        if t is None:
+            strides.append(0)
+            continue
+        n, h, d, step = _rows_of_heads(name, t, like)
+        if len(t[0]) != 3 or (n, h, d) != (rows, hkv, width):
+            raise ValueError(f"{name} must be [{rows}, {hkv}, {width}], got {tuple(t[0])}")
+        strides.append(step)
+    p = _paged_problem(like, hkv, k_cache, v_cache, block_table, kv_lens, cu_seqlens, cache_layout, rows, 0, 0,
+                       MASKS["none"], -1, 0.0, 0, *strides, _torch()["u8"])
+    return p, _scale_strides(k_cache, k_scale, v_scale, cache_layout)
 
 
 def sdpa_check_paged(p: PagedProblem) -> int:
@@ -824,22 +945,25 @@ def sdpa_check_paged(p: PagedProblem) -> int:
 
 def sdpa_paged_append(k, v, k_cache, v_cache, block_table, kv_lens, cu_seqlens_q, *, cache_layout="nhd", q=None,
                       q_weight=None, k_weight=None, cos_sin=None, positions=None, eps=1e-6, interleaved=False,
-                      q_out=None, stream=None):
+                      sections=None, q_out=None, stream=None):
     """Write the new tokens' k [T, Hkv, D] and v [T, Hkv, Dv] into their pages
     of k_cache and v_cache (sdpa_paged_append in include/sdpa.h). kv_lens count
     the new tokens already. With q [T, Hq, D] (and q_weight, k_weight), k is
     normed and rotated on its way into the cache and q into q_out, as by
-    sdpa_qk_norm_rope; positions default to the cache positions. Returns q_out
-    (None without q). k, v and q may be slices of one projection's output."""
+    sdpa_qk_norm_rope; positions default to the cache positions (with sections
+    they are required). Returns q_out (None without q). k, v and q may be slices
+    of one projection's output."""
     if stream is not None:
         return _on(stream, sdpa_paged_append, locals())
-    p, n = _append_plan(_meta(k), _meta(v), _meta(k_cache), _meta(v_cache), _meta(block_table), _meta(kv_lens),
-                        _meta(cu_seqlens_q), cache_layout, _meta(q), _meta(q_weight), _meta(k_weight), _meta(cos_sin),
-                        _meta(positions), _meta(q_out), float(eps), bool(interleaved))
+    p, n, axes, _ = _append_plan(_meta(k), _meta(v), _meta(k_cache), _meta(v_cache), _meta(block_table), _meta(kv_lens),
+                                 _meta(cu_seqlens_q), cache_layout, _meta(q), _meta(q_weight), _meta(k_weight),
+                                 _meta(cos_sin), _meta(positions), _meta(q_out), float(eps), bool(interleaved),
+                                 _axes(sections))
     _refuse_cpu(k)
     if q is not None and q_out is None:
         q_out = _torch_state["like"](q)
-    _launch("sdpa_paged_append", k.device, ctypes.byref(p), None if n is None else ctypes.byref(n), _addr(q),
+    entry = ("sdpa_paged_append",) if axes is None else ("sdpa_paged_append_axes", ctypes.byref(axes))
+    _launch(entry[0], k.device, ctypes.byref(p), _ref(n), *entry[1:], _addr(q),
             k.data_ptr(), v.data_ptr(), _addr(q_weight), _addr(k_weight), _addr(cos_sin), _addr(positions), _addr(q_out),
             k_cache.data_ptr(), v_cache.data_ptr(), cu_seqlens_q.data_ptr(), kv_lens.data_ptr(), block_table.data_ptr())
     return q_out
@@ -882,6 +1006,98 @@ def sdpa_paged_fwd(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens_q, *, m
     _launch("sdpa_paged_fwd", dev, ctypes.byref(p), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
             out.data_ptr(), lse.data_ptr(), cu_seqlens_q.data_ptr(), kv_lens.data_ptr(), block_table.data_ptr(),
             workspace.data_ptr(), workspace.nbytes)
+    return out, lse
+
+
+def sdpa_paged_append_fp8(k, v, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, cu_seqlens_q, *,
+                          cache_layout="nhd", q=None, q_weight=None, k_weight=None, cos_sin=None, positions=None,
+                          eps=1e-6, interleaved=False, sections=None, q_out=None, stream=None):
+    """sdpa_paged_append into a cache in 8 bits (sdpa_paged_append_fp8 in
+    include/sdpa.h): k_cache, v_cache uint8 E4M3 codes in sdpa_paged_append's
+    shapes, k_scale, v_scale uint8 [pages, page_size, Hkv] ("hnd": [pages, Hkv,
+    page_size]) with a byte for every row, whose values are codes * 2^(byte -
+    127). Everything else as there."""
+    if stream is not None:
+        return _on(stream, sdpa_paged_append_fp8, locals())
+    p, n, axes, strides = _append_plan(_meta(k), _meta(v), _meta(k_cache), _meta(v_cache), _meta(block_table),
+                                       _meta(kv_lens), _meta(cu_seqlens_q), cache_layout, _meta(q), _meta(q_weight),
+                                       _meta(k_weight), _meta(cos_sin), _meta(positions), _meta(q_out), float(eps),
+                                       bool(interleaved), _axes(sections), _meta(k_scale), _meta(v_scale))
+    _refuse_cpu(k)
+    if q is not None and q_out is None:
+        q_out = _torch_state["like"](q)
+    scales = _scales(strides, k_scale, v_scale)
+    _launch("sdpa_paged_append_fp8", k.device, ctypes.byref(p), _ref(n), _ref(axes), ctypes.byref(scales), _addr(q),
+            k.data_ptr(), v.data_ptr(), _addr(q_weight), _addr(k_weight), _addr(cos_sin), _addr(positions), _addr(q_out),
+            k_cache.data_ptr(), v_cache.data_ptr(), cu_seqlens_q.data_ptr(), kv_lens.data_ptr(), block_table.data_ptr())
+    return q_out
+
+
+def sdpa_paged_read_fp8(k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, cu_seqlens, *, cache_layout="nhd",
+                        rows=None, dtype=None, k_out=None, v_out=None, stream=None):
+    """The last keys and values of every sequence of a cache in 8 bits as packed
+    16-bit rows (sdpa_paged_read_fp8 in include/sdpa.h): rows cu_seqlens[b] ..
+    cu_seqlens[b+1]-1 receive as many of sequence b's last keys, of the kv_lens[b]
+    that it has. Returns (k_out [rows, Hkv, D], v_out [rows, Hkv, Dv]), which may
+    be given (also slices of wider rows); otherwise rows and dtype say what to
+    allocate, and rows behind the last sequence are not set."""
+    if stream is not None:
+        return _on(stream, sdpa_paged_read_fp8, locals())
+    given = k_out if k_out is not None else v_out
+    if given is not None:
+        if (rows is not None and rows != given.shape[0]) or (dtype is not None and dtype is not given.dtype):
+            raise ValueError(f"rows {rows} and dtype {dtype} are not those of the given output {tuple(given.shape)} {given.dtype}")
+        rows, dtype = given.shape[0], given.dtype
+    elif rows is None or dtype is None:
+        raise ValueError("rows and dtype are needed unless an output is given")
+    rows = int(rows)
+    p, strides = _read_plan(_meta(k_cache), _meta(v_cache), _meta(k_scale), _meta(v_scale), _meta(block_table),
+                            _meta(kv_lens), _meta(cu_seqlens), cache_layout, rows, dtype, _meta(k_out), _meta(v_out))
+    _refuse_cpu(k_cache)
+    if k_out is None:
+        k_out = k_cache.new_empty((rows, p.num_heads_kv, p.head_dim), dtype=dtype)
+    if v_out is None:
+        v_out = k_cache.new_empty((rows, p.num_heads_kv, p.head_dim_v), dtype=dtype)
+    scales = _scales(strides, k_scale, v_scale)
+    _launch("sdpa_paged_read_fp8", k_cache.device, ctypes.byref(p), ctypes.byref(scales), k_cache.data_ptr(),
+            v_cache.data_ptr(), k_out.data_ptr(), v_out.data_ptr(), cu_seqlens.data_ptr(), kv_lens.data_ptr(),
+            block_table.data_ptr())
+    return k_out, v_out
+
+
+def sdpa_paged_fwd_fp8_workspace_size(p: PagedProblem) -> int:
+    return int(lib().sdpa_paged_fwd_fp8_workspace_size(ctypes.byref(p)))
+
+
+def sdpa_paged_fwd_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, cu_seqlens_q, *, max_seqlen_q,
+                       max_seqlen_kv=None, cache_layout="nhd", mask="causal_br", window=(-1, -1), scale=None, out=None,
+                       lse=None, workspace=None, stream=None):
+    """sdpa_paged_fwd over a cache in 8 bits, as sdpa_paged_append_fp8 writes
+    it: the attention over the values that codes and scale bytes stand for, with
+    q, out and the softmax as there. Made for single tokens and a few (decoding,
+    speculative tokens, the tail of a prompt); for a prompt's long chunks read
+    the keys back (sdpa_paged_read_fp8) and call sdpa_fwd."""
+    if stream is not None:
+        return _on(stream, sdpa_paged_fwd_fp8, locals())
+    p, need, strides = _paged_fp8_plan(_meta(k_scale), _meta(v_scale), _meta(q), _meta(k_cache), _meta(v_cache),
+                                       _meta(block_table), _meta(kv_lens), _meta(cu_seqlens_q), int(max_seqlen_q),
+                                       None if max_seqlen_kv is None else int(max_seqlen_kv), cache_layout, mask,
+                                       int(window[0]), int(window[1]), None if scale is None else float(scale),
+                                       _meta(out), _meta(lse))
+    _refuse_cpu(q)
+    dev = q.device
+    if out is None:
+        out = q.new_empty((p.total_q, p.num_heads_q, p.head_dim_v))
+    if lse is None:
+        lse = q.new_empty((p.total_q, p.num_heads_q), dtype=_torch_state["f32"])
+    if workspace is None:
+        workspace = lse.new_empty(max(need // 4, 64))
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+    scales = _scales(strides, k_scale, v_scale)
+    _launch("sdpa_paged_fwd_fp8", dev, ctypes.byref(p), ctypes.byref(scales), q.data_ptr(), k_cache.data_ptr(),
+            v_cache.data_ptr(), out.data_ptr(), lse.data_ptr(), cu_seqlens_q.data_ptr(), kv_lens.data_ptr(),
+            block_table.data_ptr(), workspace.data_ptr(), workspace.nbytes)
     return out, lse
 
 

@@ -390,6 +390,46 @@ int check_norm_rope(const sdpa_norm_rope_problem* p) {
   return SDPA_OK;
 }
 
+// Whether rows of `aw` and of `bw` 16-bit values, `as` and `bs` elements apart, lie apart: two outputs apart as a whole,
+// or slices of one tensor's rows, which interleave.
+bool rows_apart(Extent a, long long as, long long aw, Extent b, long long bs, long long bw) {
+  if (!overlaps(a, b)) return true;
+  if (as != bs || a.lo == b.lo) return false;
+  return b.lo > a.lo ? b.lo - a.lo >= (uintptr_t)aw * 2 && b.lo - a.lo + bw * 2 <= (uintptr_t)as * 2
+                     : a.lo - b.lo >= (uintptr_t)bw * 2 && a.lo - b.lo + aw * 2 <= (uintptr_t)as * 2;
+}
+
+// The axes of a rotation of `rot` values for the kernels; a: may be NULL (one position a token).
+int make_axes(const sdpa_rope_axes* a, int rot, long long rows, RopeAxes* out) {
+  std::memset(out, 0, sizeof(*out));
+  if (!a) return SDPA_OK;
+  if (a->num_axes < 1 || a->num_axes > SDPA_ROPE_AXES_MAX) return SDPA_ERR_INVALID_ARG;
+  if (a->position_stride != 0 && (a->position_stride < rows || a->position_stride >= (1LL << 36))) return SDPA_ERR_INVALID_ARG;
+  out->n = a->num_axes;
+  out->pos_stride = a->position_stride ? a->position_stride : rows;
+  int at = 0;
+  for (int x = 0; x < SDPA_ROPE_AXES_MAX; ++x) {
+    out->end[x] = std::numeric_limits<int>::max();
+    if (x >= a->num_axes) continue;
+    if (a->pairs[x] < 1 || a->pairs[x] > rot / 2 - at) return SDPA_ERR_INVALID_ARG;
+    const int end = at + a->pairs[x];
+    if (x + 1 < a->num_axes) out->end[x] = end;
+    // whole blocks of 4 pairs (16 bytes, what a bulk copy moves); rot / 2 is a multiple of 8
+    out->lo[x] = at & ~3;
+    out->len[x] = ((end + 3) & ~3) - out->lo[x];
+    out->cos_at[x] = out->floats - out->lo[x];
+    out->sin_at[x] = out->cos_at[x] + out->len[x];
+    out->floats += 2 * out->len[x];
+    at = end;
+  }
+  return at == rot / 2 ? SDPA_OK : SDPA_ERR_INVALID_ARG;
+}
+
+// Bytes of the positions of `rows` tokens.
+size_t positions_bytes(const RopeAxes& a, long long rows) {
+  return 4 * (size_t)((a.n ? (a.n - 1) * a.pos_stride : 0) + rows);
+}
+
 // Bytes spanned by `rows` rows of `width` 16-bit values, `stride` elements apart.
 size_t span(long long rows, long long stride, long long width) {
   return rows > 0 ? (size_t)((rows - 1) * stride + width) * 2 : 0;
@@ -517,6 +557,20 @@ PagedCutting paged_cutting(const sdpa_paged_problem* p, int n, int q_rows, int m
   return c;
 }
 
+// Where the two launches' records lie in the workspace.
+void paged_workspace(PagedPlan& pl) {
+  size_t at = 256;  // totals and tickets
+  for (int x = 0; x < 2; ++x) {
+    const PagedCutting& c = x ? pl.chunk : pl.rows;
+    pl.cuts_off[x] = at;
+    const size_t shares = !c.used ? 0 : c.tail ? c.tail : c.split ? c.workers : 0;
+    at = round_up(at + shares * paged_cut_bytes(), 256);
+    pl.parts_off[x] = at;
+    at = round_up(at + shares * 2 * c.n * (c.dv_item + 2) * 4, 256);
+  }
+  pl.total = at;
+}
+
 PagedPlan paged_plan(const sdpa_paged_problem* p) {
   PagedPlan pl;
   const int group = p->num_heads_q / p->num_heads_kv, dv = paged_dv(p);
@@ -534,17 +588,70 @@ PagedPlan paged_plan(const sdpa_paged_problem* p) {
     pl.rows = paged_cutting(p, n, n, max_q, dv);
   }
   if (p->seqlen_q > pl.small_q) pl.chunk = paged_cutting(p, p->head_dim == 128 ? 256 : 128, 128, p->seqlen_q, std::min(dv, 256));
-  size_t at = 256;  // totals and tickets
-  for (int x = 0; x < 2; ++x) {
-    const PagedCutting& c = x ? pl.chunk : pl.rows;
-    pl.cuts_off[x] = at;
-    const size_t shares = !c.used ? 0 : c.tail ? c.tail : c.split ? c.workers : 0;
-    at = round_up(at + shares * paged_cut_bytes(), 256);
-    pl.parts_off[x] = at;
-    at = round_up(at + shares * 2 * c.n * (c.dv_item + 2) * 4, 256);
-  }
-  pl.total = at;
+  paged_workspace(pl);
   return pl;
+}
+
+// The attention over an 8-bit cache: one kernel for any number of tokens, in items of 16 or 32 rows (a 512-wide O of 32
+// rows with its three terms does not fit the tensor memory).
+PagedPlan paged_fp8_plan(const sdpa_paged_problem* p) {
+  PagedPlan pl;
+  const int group = p->num_heads_q / p->num_heads_kv, dv = paged_dv(p);
+  pl.rows.used = pl.chunk.used = false;
+  pl.small_q = p->seqlen_q;
+  const int n = dv == 512 || (long long)group * std::max(p->seqlen_q, 1) <= 16 ? 16 : 32;
+  pl.rows = paged_cutting(p, n, n, p->seqlen_q, dv);
+  paged_workspace(pl);
+  return pl;
+}
+
+// What a launch of the paged attention is told, apart from its copies.
+PagedParams paged_params(const sdpa_paged_problem* p, const PagedPlan& pl, bool small, const int32_t* cu_seqlens_q,
+                         const int32_t* kv_lens, const int32_t* block_table, void* o, float* lse, uint8_t* ws, int* err,
+                         AddrTable* chk) {
+  const PagedCutting* c = small ? &pl.rows : &pl.chunk;
+  PagedParams P;
+  std::memset(&P, 0, sizeof(P));
+  P.batch = p->batch;
+  P.total_q = p->total_q;
+  P.max_q = p->seqlen_q;
+  P.max_kv = p->seqlen_kv;
+  P.hq = p->num_heads_q;
+  P.group = p->num_heads_q / p->num_heads_kv;
+  P.block_heads = c->block_heads;
+  P.head_blocks = c->head_blocks;
+  P.tokens = c->tokens;
+  P.dv = paged_dv(p);
+  P.dv_splits = c->dv_splits;
+  P.units_per_block = p->num_heads_kv * c->head_blocks * c->dv_splits;
+  P.small_q = pl.small_q;
+  P.small = small;
+  P.split = c->split;
+  P.tail = c->tail;
+  P.q_box_rows = c->q_tokens * c->block_heads;
+  P.causal = p->mask_type != SDPA_MASK_NONE;
+  P.window = p->window_left < p->seqlen_kv ? p->window_left : -1;  // as wide as every length: no window
+  // Never 0: the chunk kernel masks a score by -inf before the scale, and -inf x 0 is NaN. By the smallest number
+  // above 0 every finite score is below 2^-20 instead, whose 2^x is 1 to an fp32 rounding or two. (Zeroing the
+  // scores in the kernel: 4 x 1024 tokens over 32768 keys at head_dim 256 1.59 -> 1.72 ms, whatever the scale.)
+  P.scale_log2 = p->softmax_scale * 1.4426950408889634f;
+  if (!(P.scale_log2 > 0.f)) P.scale_log2 = std::numeric_limits<float>::denorm_min();
+  P.page_size = p->page_size;
+  P.num_pages = p->num_pages;
+  P.cu_q = cu_seqlens_q;
+  P.kv_lens = kv_lens;
+  P.block_table = block_table;
+  P.table_stride = p->table_stride ? p->table_stride : p->max_pages;
+  P.o = o;
+  P.lse = lse;
+  P.behind = !small && pl.rows.used;
+  P.total_tiles = reinterpret_cast<long long*>(ws + (small ? 0 : 64));
+  P.tickets = reinterpret_cast<int*>(ws + 128);
+  P.cuts = reinterpret_cast<PagedCut*>(ws + pl.cuts_off[small ? 0 : 1]);
+  P.parts = reinterpret_cast<float*>(ws + pl.parts_off[small ? 0 : 1]);
+  P.err = err;
+  P.chk = chk;
+  return P;
 }
 
 // Whether a slot's heads lie apart by more than its pages' slots ([page][head][slot]);
@@ -572,38 +679,71 @@ int encode_cache(CUtensorMap* m, const void* base, const sdpa_paged_problem* p, 
   return r == CUDA_SUCCESS ? SDPA_OK : SDPA_ERR_CUDA;
 }
 
-// Bytes from a cache's first element to its last.
-size_t cache_span(const sdpa_paged_problem* p, long long page, long long slot, long long head, int width) {
-  return (size_t)((p->num_pages - 1) * page + (p->page_size - 1) * slot + (p->num_heads_kv - 1) * head + width) * 2;
+// One of a paged cache's tensors: rows of `width` values of `bytes` each, one for every page, slot and head.
+struct CacheView {
+  const void* base;
+  long long page, slot, head;  // elements between pages, slots and heads
+  int width, bytes;
+};
+CacheView k_view(const sdpa_paged_problem* p, const void* base, int bytes = 2) {
+  return {base, p->k_page_stride, p->k_slot_stride, p->k_head_stride, p->head_dim, bytes};
+}
+CacheView v_view(const sdpa_paged_problem* p, const void* base, int bytes = 2) {
+  return {base, p->v_page_stride, p->v_slot_stride, p->v_head_stride, paged_dv(p), bytes};
 }
 
-// Whether every row of the two caches lies apart from all others. Where their spans interleave (pages that hold K and V
-// together), addresses are compared modulo a step that both caches' strides from some level on are multiples of: the
-// stretch of a step that K fills and the one that V fills must not meet.
-bool caches_apart(const sdpa_paged_problem* p, const void* k_cache, const void* v_cache, bool spans_overlap) {
+// The bytes from its first element to its last.
+Extent cache_extent(const sdpa_paged_problem* p, const CacheView& c) {
+  return extent(c.base, (size_t)((p->num_pages - 1) * c.page + (p->page_size - 1) * c.slot + (p->num_heads_kv - 1) * c.head +
+                                 c.width) * c.bytes);
+}
+
+// Whether every row of the two tensors lies apart from all others. Where their spans interleave (pages that hold K and V
+// together), addresses are compared modulo a step that both tensors' strides from some level on are multiples of: the
+// stretch of a step that one fills and the one that the other fills must not meet.
+bool caches_apart(const sdpa_paged_problem* p, const CacheView& kc, const CacheView& vc) {
   struct Level {
-    long long stride, fill;  // fill: values from the first to the last within one step of the stride
+    long long stride, fill;  // in bytes; fill: from the first to the last within one step of the stride
   };
   const bool one = p->num_heads_kv == 1;  // a single head's stride is never taken
-  auto levels = [&](long long page, long long slot, long long head, int width) {
-    const bool first = one || slot < head;  // slots vary before heads
-    const long long lo = first ? slot : head, hi = one || !first ? slot : head;
-    const long long inner = one ? width : ((first ? p->page_size : p->num_heads_kv) - 1) * lo + width;
+  auto levels = [&](const CacheView& c) {
+    const bool first = one || c.slot < c.head;  // slots vary before heads
+    const long long lo = first ? c.slot : c.head, hi = one || !first ? c.slot : c.head;
+    const long long inner = one ? c.width : ((first ? p->page_size : p->num_heads_kv) - 1) * lo + c.width;
     const long long whole = ((first && !one ? p->num_heads_kv : p->page_size) - 1) * hi + inner;
-    return std::array<Level, 3>{Level{lo, width}, Level{hi, inner}, Level{page, whole}};
+    const long long b = c.bytes;
+    return std::array<Level, 3>{Level{lo * b, c.width * b}, Level{hi * b, inner * b}, Level{c.page * b, whole * b}};
   };
-  const auto k = levels(p->k_page_stride, p->k_slot_stride, p->k_head_stride, p->head_dim);
-  const auto v = levels(p->v_page_stride, p->v_slot_stride, p->v_head_stride, paged_dv(p));
+  const auto k = levels(kc), v = levels(vc);
   const int used = p->num_pages > 1 ? 3 : 2;
   for (int i = 0; i < used; ++i)
     if (k[i].fill > k[i].stride || v[i].fill > v[i].stride) return false;
-  if (!spans_overlap) return true;
-  const long long off = (long long)(reinterpret_cast<uintptr_t>(v_cache) - reinterpret_cast<uintptr_t>(k_cache)) / 2;
+  if (!overlaps(cache_extent(p, kc), cache_extent(p, vc))) return true;
+  const long long off = (long long)(reinterpret_cast<uintptr_t>(vc.base) - reinterpret_cast<uintptr_t>(kc.base));
   for (int i = 0; i < used; ++i) {
     const long long step = std::gcd(k[i].stride, v[i].stride), at = (off % step + step) % step;
     if (at >= k[i].fill && at + v[i].fill <= step) return true;
   }
   return false;
+}
+
+// The scale bytes beside an 8-bit cache of a checked problem: whether they and the codes' strides can be served.
+int check_fp8_cache(const sdpa_paged_problem* p, const sdpa_paged_scales* c) {
+  if (!c || !c->k || !c->v) return SDPA_ERR_INVALID_ARG;
+  // codes are moved 16 bytes at a time
+  for (long long st : {p->k_page_stride, p->k_slot_stride, p->k_head_stride, p->v_page_stride, p->v_slot_stride,
+                       p->v_head_stride})
+    if (st % 16) return SDPA_ERR_INVALID_ARG;
+  for (long long st : {c->k_page_stride, c->k_slot_stride, c->k_head_stride, c->v_page_stride, c->v_slot_stride,
+                       c->v_head_stride})
+    if (st < 1 || st >= (1LL << 36)) return SDPA_ERR_INVALID_ARG;
+  return SDPA_OK;
+}
+CacheView k_scale_view(const sdpa_paged_scales* c) {
+  return {c->k, c->k_page_stride, c->k_slot_stride, c->k_head_stride, 1, 1};
+}
+CacheView v_scale_view(const sdpa_paged_scales* c) {
+  return {c->v, c->v_page_stride, c->v_slot_stride, c->v_head_stride, 1, 1};
 }
 
 }  // namespace
@@ -1042,12 +1182,14 @@ int sdpa_merge(const sdpa_merge_problem* p, const void* o_parts, const float* ls
   return SDPA_OK;
 }
 
-int sdpa_qk_norm_rope(const sdpa_norm_rope_problem* p, const void* q, const void* k, const void* q_weight,
-                      const void* k_weight, const float* cos_sin, const int32_t* positions, void* q_out, void* k_out,
-                      void* stream) {
+static int norm_rope_call(const sdpa_norm_rope_problem* p, const sdpa_rope_axes* axes, const void* q, const void* k,
+                          const void* q_weight, const void* k_weight, const float* cos_sin, const int32_t* positions,
+                          void* q_out, void* k_out, void* stream) {
   t_last_launches = 0;
   int rc = check_norm_rope(p);
   if (rc) return rc;
+  RopeAxes ax;
+  if ((rc = make_axes(axes, p->rotary_dim, p->rows, &ax))) return rc;
   if (p->rows == 0) return SDPA_OK;
   if (!q || !k || !q_weight || !k_weight || !q_out || !k_out) return SDPA_ERR_INVALID_ARG;
   if (p->rotary_dim > 0 && (!cos_sin || !positions)) return SDPA_ERR_INVALID_ARG;
@@ -1071,6 +1213,7 @@ int sdpa_qk_norm_rope(const sdpa_norm_rope_problem* p, const void* q, const void
   L.table = cos_sin;
   L.max_pos = p->max_positions;
   L.pos = positions;
+  L.axes = ax;
   L.q_out = q_out;
   L.k_out = k_out;
   const size_t wb = (size_t)p->head_dim * 2;
@@ -1078,7 +1221,7 @@ int sdpa_qk_norm_rope(const sdpa_norm_rope_problem* p, const void* q, const void
   const Extent ins[6] = {extent(q, span(p->rows, L.qs, qw)), extent(k, span(p->rows, L.ks, kw)),
                          extent(q_weight, wb), extent(k_weight, wb),
                          extent(cos_sin, p->rotary_dim ? (size_t)p->max_positions * p->rotary_dim * 4 : 0),
-                         extent(positions, p->rotary_dim ? (size_t)p->rows * 4 : 0)};
+                         extent(positions, p->rotary_dim ? positions_bytes(ax, p->rows) : 0)};
   for (const Extent& in : ins)
     if (overlaps(eq, in) || overlaps(ek, in)) return SDPA_ERR_OVERLAP;
   if (overlaps(eq, ek)) return SDPA_ERR_OVERLAP;
@@ -1094,18 +1237,33 @@ int sdpa_qk_norm_rope(const sdpa_norm_rope_problem* p, const void* q, const void
   return SDPA_OK;
 }
 
+int sdpa_qk_norm_rope(const sdpa_norm_rope_problem* p, const void* q, const void* k, const void* q_weight,
+                      const void* k_weight, const float* cos_sin, const int32_t* positions, void* q_out, void* k_out,
+                      void* stream) {
+  return norm_rope_call(p, nullptr, q, k, q_weight, k_weight, cos_sin, positions, q_out, k_out, stream);
+}
+
+int sdpa_qk_norm_rope_axes(const sdpa_norm_rope_problem* p, const sdpa_rope_axes* axes, const void* q, const void* k,
+                           const void* q_weight, const void* k_weight, const float* cos_sin, const int32_t* positions,
+                           void* q_out, void* k_out, void* stream) {
+  if (!axes) return SDPA_ERR_INVALID_ARG;
+  return norm_rope_call(p, axes, q, k, q_weight, k_weight, cos_sin, positions, q_out, k_out, stream);
+}
+
 size_t sdpa_qk_norm_rope_bwd_workspace_size(const sdpa_norm_rope_problem* p) {
   if (check_norm_rope(p) != SDPA_OK || p->rows == 0) return 0;
   return (size_t)(norm_rope_bwd_plan(p->rows, p->num_heads_q, p->num_heads_kv, p->head_dim).blocks + 1) * p->head_dim * 4;
 }
 
-int sdpa_qk_norm_rope_bwd(const sdpa_norm_rope_problem* p, const void* dq_out, const void* dk_out, const void* q,
-                          const void* k, const void* q_weight, const void* k_weight, const float* cos_sin,
-                          const int32_t* positions, void* dq, void* dk, float* dq_weight, float* dk_weight,
-                          void* workspace, size_t ws_bytes, void* stream) {
+static int norm_rope_bwd_call(const sdpa_norm_rope_problem* p, const sdpa_rope_axes* axes, const void* dq_out,
+                              const void* dk_out, const void* q, const void* k, const void* q_weight,
+                              const void* k_weight, const float* cos_sin, const int32_t* positions, void* dq, void* dk,
+                              float* dq_weight, float* dk_weight, void* workspace, size_t ws_bytes, void* stream) {
   t_last_launches = 0;
   int rc = check_norm_rope(p);
   if (rc) return rc;
+  RopeAxes ax;
+  if ((rc = make_axes(axes, p->rotary_dim, p->rows, &ax))) return rc;
   if (!dq_weight || !dk_weight) return SDPA_ERR_INVALID_ARG;
   if (!aligned16(dq_weight) || !aligned16(dk_weight)) return SDPA_ERR_ALIGNMENT;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -1144,6 +1302,7 @@ int sdpa_qk_norm_rope_bwd(const sdpa_norm_rope_problem* p, const void* dq_out, c
   L.table = cos_sin;
   L.max_pos = p->max_positions;
   L.pos = positions;
+  L.axes = ax;
   L.dq = dq;
   L.dk = dk;
   L.dqs = p->dq_stride ? p->dq_stride : qw;
@@ -1161,17 +1320,12 @@ int sdpa_qk_norm_rope_bwd(const sdpa_norm_rope_problem* p, const void* dq_out, c
                          extent(q, span(p->rows, L.qs, qw)), extent(k, span(p->rows, L.ks, kw)),
                          extent(q_weight, wb), extent(k_weight, wb),
                          extent(cos_sin, p->rotary_dim ? (size_t)p->max_positions * p->rotary_dim * 4 : 0),
-                         extent(positions, p->rotary_dim ? (size_t)p->rows * 4 : 0)};
+                         extent(positions, p->rotary_dim ? positions_bytes(ax, p->rows) : 0)};
   for (int a = 0; a < 5; ++a) {
     for (const Extent& in : ins)
       if (overlaps(outs[a], in)) return SDPA_ERR_OVERLAP;
     for (int b = a + 1; b < 5; ++b) {
-      // dq and dk may be slices of one fused gradient: their rows interleave
-      const bool slices = a == 0 && b == 1 && L.dqs == L.dks && outs[0].lo != outs[1].lo &&
-                          (outs[1].lo > outs[0].lo ? outs[1].lo - outs[0].lo >= (uintptr_t)qw * 2 &&
-                                                         outs[1].lo - outs[0].lo + kw * 2 <= (uintptr_t)L.dqs * 2
-                                                   : outs[0].lo - outs[1].lo >= (uintptr_t)kw * 2 &&
-                                                         outs[0].lo - outs[1].lo + qw * 2 <= (uintptr_t)L.dqs * 2);
+      const bool slices = a == 0 && b == 1 && rows_apart(outs[0], L.dqs, qw, outs[1], L.dks, kw);
       if (!slices && overlaps(outs[a], outs[b])) return SDPA_ERR_OVERLAP;
     }
   }
@@ -1189,12 +1343,31 @@ int sdpa_qk_norm_rope_bwd(const sdpa_norm_rope_problem* p, const void* dq_out, c
   return SDPA_OK;
 }
 
+int sdpa_qk_norm_rope_bwd(const sdpa_norm_rope_problem* p, const void* dq_out, const void* dk_out, const void* q,
+                          const void* k, const void* q_weight, const void* k_weight, const float* cos_sin,
+                          const int32_t* positions, void* dq, void* dk, float* dq_weight, float* dk_weight,
+                          void* workspace, size_t ws_bytes, void* stream) {
+  return norm_rope_bwd_call(p, nullptr, dq_out, dk_out, q, k, q_weight, k_weight, cos_sin, positions, dq, dk, dq_weight,
+                            dk_weight, workspace, ws_bytes, stream);
+}
+
+int sdpa_qk_norm_rope_axes_bwd(const sdpa_norm_rope_problem* p, const sdpa_rope_axes* axes, const void* dq_out,
+                               const void* dk_out, const void* q, const void* k, const void* q_weight,
+                               const void* k_weight, const float* cos_sin, const int32_t* positions, void* dq, void* dk,
+                               float* dq_weight, float* dk_weight, void* workspace, size_t ws_bytes, void* stream) {
+  if (!axes) return SDPA_ERR_INVALID_ARG;
+  return norm_rope_bwd_call(p, axes, dq_out, dk_out, q, k, q_weight, k_weight, cos_sin, positions, dq, dk, dq_weight,
+                            dk_weight, workspace, ws_bytes, stream);
+}
+
 int sdpa_check_paged(const sdpa_paged_problem* p) { return check_paged(p); }
 
-int sdpa_paged_append(const sdpa_paged_problem* p, const sdpa_norm_rope_problem* n, const void* q, const void* k,
-                      const void* v, const void* q_weight, const void* k_weight, const float* cos_sin,
-                      const int32_t* positions, void* q_out, void* k_cache, void* v_cache,
-                      const int32_t* cu_seqlens_q, const int32_t* kv_lens, const int32_t* block_table, void* stream) {
+// scales: of a cache of E4M3 codes, or NULL (a 16-bit cache).
+static int append_call(const sdpa_paged_problem* p, const sdpa_norm_rope_problem* n, const sdpa_rope_axes* axes,
+                       const sdpa_paged_scales* scales, const void* q, const void* k, const void* v, const void* q_weight,
+                       const void* k_weight, const float* cos_sin, const int32_t* positions, void* q_out, void* k_cache,
+                       void* v_cache, const int32_t* cu_seqlens_q, const int32_t* kv_lens, const int32_t* block_table,
+                       void* stream) {
   t_last_launches = 0;
   int rc = check_paged(p);
   if (rc) return rc;
@@ -1208,11 +1381,16 @@ int sdpa_paged_append(const sdpa_paged_problem* p, const sdpa_norm_rope_problem*
     full.q_stride = full.k_stride = full.dq_stride = full.dk_stride = 0;
     if ((rc = check_norm_rope(&full))) return rc;
   }
+  RopeAxes ax;
+  if (axes && !n) return SDPA_ERR_INVALID_ARG;
+  if ((rc = make_axes(axes, n ? n->rotary_dim : 0, p->total_q, &ax))) return rc;
+  if (scales && (rc = check_fp8_cache(p, scales))) return rc;
   if (p->batch == 0 || p->total_q == 0) return SDPA_OK;
   if (!k || !v || !k_cache || !v_cache || !cu_seqlens_q || !kv_lens || !block_table) return SDPA_ERR_INVALID_ARG;
   const bool rot = n && n->rotary_dim > 0;
   if (n && (!q || !q_out || !q_weight || !k_weight)) return SDPA_ERR_INVALID_ARG;
   if (rot && !cos_sin) return SDPA_ERR_INVALID_ARG;
+  if (axes && !positions) return SDPA_ERR_INVALID_ARG;  // a cache position has no axes
   for (const void* ptr : {k, v, (const void*)k_cache, (const void*)v_cache})
     if (!aligned16(ptr)) return SDPA_ERR_ALIGNMENT;
   if (n)
@@ -1241,6 +1419,7 @@ int sdpa_paged_append(const sdpa_paged_problem* p, const sdpa_norm_rope_problem*
     L.table = cos_sin;
     L.max_pos = n->max_positions;
     L.pos = rot ? positions : nullptr;
+    L.axes = ax;
     L.q_out = q_out;
   }
   L.batch = p->batch;
@@ -1259,31 +1438,141 @@ int sdpa_paged_append(const sdpa_paged_problem* p, const sdpa_norm_rope_problem*
   L.vc_page = p->v_page_stride;
   L.vc_slot = p->v_slot_stride;
   L.vc_head = p->v_head_stride;
+  if (scales) {
+    L.k_scale = scales->k;
+    L.v_scale = scales->v;
+    L.ks_page = scales->k_page_stride;
+    L.ks_slot = scales->k_slot_stride;
+    L.ks_head = scales->k_head_stride;
+    L.vs_page = scales->v_page_stride;
+    L.vs_slot = scales->v_slot_stride;
+    L.vs_head = scales->v_head_stride;
+  }
   const size_t wb = (size_t)d * 2;
-  const Extent outs[3] = {
-      extent(k_cache, cache_span(p, p->k_page_stride, p->k_slot_stride, p->k_head_stride, d)),
-      extent(v_cache, cache_span(p, p->v_page_stride, p->v_slot_stride, p->v_head_stride, dv)),
-      extent(q_out, n ? (size_t)p->total_q * qw * 2 : 0)};
+  CacheView views[4] = {k_view(p, k_cache, scales ? 1 : 2), v_view(p, v_cache, scales ? 1 : 2)};
+  const int n_views = scales ? 4 : 2;
+  Extent outs[5] = {cache_extent(p, views[0]), cache_extent(p, views[1]),
+                    extent(q_out, n ? (size_t)p->total_q * qw * 2 : 0), extent(nullptr, 0), extent(nullptr, 0)};
+  if (scales) {
+    views[2] = k_scale_view(scales);
+    views[3] = v_scale_view(scales);
+    outs[3] = cache_extent(p, views[2]);
+    outs[4] = cache_extent(p, views[3]);
+  }
   const Extent ins[10] = {extent(k, span(p->total_q, L.ks, kw)), extent(v, span(p->total_q, L.vs, vw)),
                           extent(q, n ? span(p->total_q, L.qs, qw) : 0), extent(q_weight, n ? wb : 0),
                           extent(k_weight, n ? wb : 0),
                           extent(cos_sin, rot ? (size_t)n->max_positions * n->rotary_dim * 4 : 0),
-                          extent(positions, L.pos ? (size_t)p->total_q * 4 : 0),
+                          extent(positions, L.pos ? positions_bytes(ax, p->total_q) : 0),
                           extent(cu_seqlens_q, 4 * ((size_t)p->batch + 1)), extent(kv_lens, 4 * (size_t)p->batch),
                           extent(block_table, 4 * (size_t)((p->batch - 1) * L.table_stride + p->max_pages))};
   for (const Extent& out : outs)
     for (const Extent& in : ins)
       if (overlaps(out, in)) return SDPA_ERR_OVERLAP;
-  if (!caches_apart(p, k_cache, v_cache, overlaps(outs[0], outs[1]))) return SDPA_ERR_OVERLAP;
-  if (overlaps(outs[2], outs[0]) || overlaps(outs[2], outs[1])) return SDPA_ERR_OVERLAP;
+  for (int a = 0; a < n_views; ++a)
+    for (int b = a + 1; b < n_views; ++b)
+      if (!caches_apart(p, views[a], views[b])) return SDPA_ERR_OVERLAP;
+  for (int a : {0, 1, 3, 4})
+    if (overlaps(outs[2], outs[a])) return SDPA_ERR_OVERLAP;
   L.err = error_word();
   if (!L.err) return SDPA_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  L.chk = bind_extents({outs[0], outs[1], outs[2], ins[0], ins[1], ins[2], ins[3], ins[4], ins[5], ins[6], ins[7],
+  L.chk = bind_extents({outs[0], outs[1], outs[2], outs[3], outs[4], ins[0], ins[1], ins[2], ins[3], ins[4], ins[5], ins[6], ins[7],
                         ins[8], ins[9]},
                        L.err, s);
   if (kAddrCheck && !L.chk) return SDPA_ERR_CUDA;
   rc = timed(SDPA_KERNEL_APPEND, s, [&] { return launch_norm_rope(L, d, p->dtype == SDPA_BF16, true, s); });
+  if (rc) return rc;
+  t_last_launches = 1;
+  return SDPA_OK;
+}
+
+int sdpa_paged_append(const sdpa_paged_problem* p, const sdpa_norm_rope_problem* n, const void* q, const void* k,
+                      const void* v, const void* q_weight, const void* k_weight, const float* cos_sin,
+                      const int32_t* positions, void* q_out, void* k_cache, void* v_cache,
+                      const int32_t* cu_seqlens_q, const int32_t* kv_lens, const int32_t* block_table, void* stream) {
+  return append_call(p, n, nullptr, nullptr, q, k, v, q_weight, k_weight, cos_sin, positions, q_out, k_cache, v_cache,
+                     cu_seqlens_q, kv_lens, block_table, stream);
+}
+
+int sdpa_paged_append_axes(const sdpa_paged_problem* p, const sdpa_norm_rope_problem* n, const sdpa_rope_axes* axes,
+                           const void* q, const void* k, const void* v, const void* q_weight, const void* k_weight,
+                           const float* cos_sin, const int32_t* positions, void* q_out, void* k_cache, void* v_cache,
+                           const int32_t* cu_seqlens_q, const int32_t* kv_lens, const int32_t* block_table, void* stream) {
+  if (!axes) return SDPA_ERR_INVALID_ARG;
+  return append_call(p, n, axes, nullptr, q, k, v, q_weight, k_weight, cos_sin, positions, q_out, k_cache, v_cache,
+                     cu_seqlens_q, kv_lens, block_table, stream);
+}
+
+int sdpa_paged_append_fp8(const sdpa_paged_problem* p, const sdpa_norm_rope_problem* n, const sdpa_rope_axes* axes,
+                          const sdpa_paged_scales* scales, const void* q, const void* k, const void* v,
+                          const void* q_weight, const void* k_weight, const float* cos_sin, const int32_t* positions,
+                          void* q_out, void* k_cache, void* v_cache, const int32_t* cu_seqlens_q, const int32_t* kv_lens,
+                          const int32_t* block_table, void* stream) {
+  if (!scales) return SDPA_ERR_INVALID_ARG;
+  return append_call(p, n, axes, scales, q, k, v, q_weight, k_weight, cos_sin, positions, q_out, k_cache, v_cache,
+                     cu_seqlens_q, kv_lens, block_table, stream);
+}
+
+int sdpa_paged_read_fp8(const sdpa_paged_problem* p, const sdpa_paged_scales* scales, const void* k_cache,
+                        const void* v_cache, void* k_out, void* v_out, const int32_t* cu_seqlens, const int32_t* kv_lens,
+                        const int32_t* block_table, void* stream) {
+  t_last_launches = 0;
+  int rc = check_paged(p);
+  if (rc) return rc;
+  if ((rc = check_fp8_cache(p, scales))) return rc;
+  if (p->batch == 0 || p->total_q == 0) return SDPA_OK;
+  if (!k_cache || !v_cache || !k_out || !v_out || !cu_seqlens || !kv_lens || !block_table) return SDPA_ERR_INVALID_ARG;
+  for (const void* ptr : {k_cache, v_cache, (const void*)k_out, (const void*)v_out})
+    if (!aligned16(ptr)) return SDPA_ERR_ALIGNMENT;
+  PagedReadParams L;
+  std::memset(&L, 0, sizeof(L));
+  L.rows = p->total_q;
+  L.batch = p->batch;
+  L.hkv = p->num_heads_kv;
+  L.page_size = p->page_size;
+  L.num_pages = p->num_pages;
+  L.max_pages = p->max_pages;
+  L.k_cache = static_cast<const uint8_t*>(k_cache);
+  L.v_cache = static_cast<const uint8_t*>(v_cache);
+  L.k_scale = scales->k;
+  L.v_scale = scales->v;
+  L.k_page = p->k_page_stride;
+  L.k_slot = p->k_slot_stride;
+  L.k_head = p->k_head_stride;
+  L.v_page = p->v_page_stride;
+  L.v_slot = p->v_slot_stride;
+  L.v_head = p->v_head_stride;
+  L.ks_page = scales->k_page_stride;
+  L.ks_slot = scales->k_slot_stride;
+  L.ks_head = scales->k_head_stride;
+  L.vs_page = scales->v_page_stride;
+  L.vs_slot = scales->v_slot_stride;
+  L.vs_head = scales->v_head_stride;
+  const long long kw = (long long)p->num_heads_kv * p->head_dim, vw = (long long)p->num_heads_kv * paged_dv(p);
+  L.k_out = k_out;
+  L.v_out = v_out;
+  L.k_row = p->k_stride ? p->k_stride : kw;
+  L.v_row = p->v_stride ? p->v_stride : vw;
+  L.cu = cu_seqlens;
+  L.kv_lens = kv_lens;
+  L.block_table = block_table;
+  L.table_stride = p->table_stride ? p->table_stride : p->max_pages;
+  const Extent outs[2] = {extent(k_out, span(p->total_q, L.k_row, kw)), extent(v_out, span(p->total_q, L.v_row, vw))};
+  const Extent ins[7] = {cache_extent(p, k_view(p, k_cache, 1)), cache_extent(p, v_view(p, v_cache, 1)),
+                         cache_extent(p, k_scale_view(scales)), cache_extent(p, v_scale_view(scales)),
+                         extent(cu_seqlens, 4 * ((size_t)p->batch + 1)), extent(kv_lens, 4 * (size_t)p->batch),
+                         extent(block_table, 4 * (size_t)((p->batch - 1) * L.table_stride + p->max_pages))};
+  for (const Extent& out : outs)
+    for (const Extent& in : ins)
+      if (overlaps(out, in)) return SDPA_ERR_OVERLAP;
+  if (!rows_apart(outs[0], L.k_row, kw, outs[1], L.v_row, vw)) return SDPA_ERR_OVERLAP;
+  L.err = error_word();
+  if (!L.err) return SDPA_ERR_CUDA;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  L.chk = bind_extents({outs[0], outs[1], ins[0], ins[1], ins[2], ins[3], ins[4], ins[5], ins[6]}, L.err, s);
+  if (kAddrCheck && !L.chk) return SDPA_ERR_CUDA;
+  rc = timed(SDPA_KERNEL_READ, s, [&] { return launch_paged_read(L, p->head_dim, p->dtype == SDPA_BF16, s); });
   if (rc) return rc;
   t_last_launches = 1;
   return SDPA_OK;
@@ -1315,8 +1604,7 @@ int sdpa_paged_fwd(const sdpa_paged_problem* p, const void* q, const void* k_cac
   const Extent outs[3] = {extent(o, (size_t)p->total_q * p->num_heads_q * dv * 2),
                           extent(lse, (size_t)p->total_q * p->num_heads_q * 4), extent(workspace, pl.total)};
   const Extent ins[6] = {extent(q, span(p->total_q, qs, qw)),
-                         extent(k_cache, cache_span(p, p->k_page_stride, p->k_slot_stride, p->k_head_stride, d)),
-                         extent(v_cache, cache_span(p, p->v_page_stride, p->v_slot_stride, p->v_head_stride, dv)),
+                         cache_extent(p, k_view(p, k_cache)), cache_extent(p, v_view(p, v_cache)),
                          extent(cu_seqlens_q, 4 * ((size_t)p->batch + 1)), extent(kv_lens, 4 * (size_t)p->batch),
                          extent(block_table, 4 * (size_t)((p->batch - 1) * ts + p->max_pages))};
   for (int a = 0; a < 3; ++a) {
@@ -1348,48 +1636,10 @@ int sdpa_paged_fwd(const sdpa_paged_problem* p, const void* q, const void* k_cac
     PagedLaunch L;
     std::memset(&L, 0, sizeof(L));
     PagedParams& P = L.p;
-    P.batch = p->batch;
-    P.total_q = p->total_q;
-    P.max_q = p->seqlen_q;
-    P.max_kv = p->seqlen_kv;
-    P.hq = p->num_heads_q;
-    P.group = p->num_heads_q / p->num_heads_kv;
-    P.block_heads = c->block_heads;
-    P.head_blocks = c->head_blocks;
-    P.tokens = c->tokens;
-    P.dv = dv;
-    P.dv_splits = c->dv_splits;
-    P.units_per_block = p->num_heads_kv * c->head_blocks * c->dv_splits;
-    P.small_q = pl.small_q;
-    P.small = small;
-    P.split = c->split;
-    P.tail = c->tail;
-    P.q_box_rows = c->q_tokens * c->block_heads;
-    P.causal = p->mask_type != SDPA_MASK_NONE;
-    P.window = p->window_left < p->seqlen_kv ? p->window_left : -1;  // as wide as every length: no window
-    // Never 0: the chunk kernel masks a score by -inf before the scale, and -inf x 0 is NaN. By the smallest number
-    // above 0 every finite score is below 2^-20 instead, whose 2^x is 1 to an fp32 rounding or two. (Zeroing the
-    // scores in the kernel: 4 x 1024 tokens over 32768 keys at head_dim 256 1.59 -> 1.72 ms, whatever the scale.)
-    P.scale_log2 = p->softmax_scale * 1.4426950408889634f;
-    if (!(P.scale_log2 > 0.f)) P.scale_log2 = std::numeric_limits<float>::denorm_min();
-    P.page_size = p->page_size;
-    P.num_pages = p->num_pages;
+    P = paged_params(p, pl, small, cu_seqlens_q, kv_lens, block_table, o, lse, ws, err, chk);
     // slots one copy brings: within a page and, for the chunk kernel, within a V stage
     P.box_rows = std::min(p->page_size & -p->page_size, small || c->dv_item == 128 ? 128 : 64);
     P.slot_first = slot_first(p);
-    P.cu_q = cu_seqlens_q;
-    P.kv_lens = kv_lens;
-    P.block_table = block_table;
-    P.table_stride = ts;
-    P.o = o;
-    P.lse = lse;
-    P.behind = !small && pl.rows.used;
-    P.total_tiles = reinterpret_cast<long long*>(ws + (small ? 0 : 64));
-    P.tickets = reinterpret_cast<int*>(ws + 128);
-    P.cuts = reinterpret_cast<PagedCut*>(ws + pl.cuts_off[small ? 0 : 1]);
-    P.parts = reinterpret_cast<float*>(ws + pl.parts_off[small ? 0 : 1]);
-    P.err = err;
-    P.chk = chk;
     const bool pair = !small && d == 128;
     L.workers = std::min(c->workers, sms);
     if (debug_max_ctas() > 0) L.workers = std::min(L.workers, debug_max_ctas());
@@ -1413,6 +1663,85 @@ int sdpa_paged_fwd(const sdpa_paged_problem* p, const void* q, const void* k_cac
     });
     if (rc) return rc;
   }
+  t_last_launches = launches;
+  return SDPA_OK;
+}
+
+size_t sdpa_paged_fwd_fp8_workspace_size(const sdpa_paged_problem* p) {
+  if (check_paged(p) != SDPA_OK || p->batch == 0 || p->total_q == 0) return 0;
+  return paged_fp8_plan(p).total;
+}
+
+int sdpa_paged_fwd_fp8(const sdpa_paged_problem* p, const sdpa_paged_scales* scales, const void* q, const void* k_cache,
+                       const void* v_cache, void* o, float* lse, const int32_t* cu_seqlens_q, const int32_t* kv_lens,
+                       const int32_t* block_table, void* workspace, size_t ws_bytes, void* stream) {
+  t_last_launches = 0;
+  int rc = check_paged(p);
+  if (rc) return rc;
+  if ((rc = check_fp8_cache(p, scales))) return rc;
+  if (p->batch == 0 || p->total_q == 0) return SDPA_OK;
+  if (!q || !k_cache || !v_cache || !o || !lse || !cu_seqlens_q || !kv_lens || !block_table) return SDPA_ERR_INVALID_ARG;
+  for (const void* ptr : {q, k_cache, v_cache, (const void*)o, (const void*)lse})
+    if (!aligned16(ptr)) return SDPA_ERR_ALIGNMENT;
+  const int d = p->head_dim, dv = paged_dv(p);
+  const long long qw = (long long)p->num_heads_q * d, qs = p->q_stride ? p->q_stride : qw;
+  const PagedPlan pl = paged_fp8_plan(p);
+  if (!pl.rows.fits) return SDPA_ERR_UNSUPPORTED;
+  if (!workspace || ws_bytes < pl.total) return SDPA_ERR_WORKSPACE_TOO_SMALL;
+  if (reinterpret_cast<uintptr_t>(workspace) & 255u) return SDPA_ERR_ALIGNMENT;
+  const Extent outs[3] = {extent(o, (size_t)p->total_q * p->num_heads_q * dv * 2),
+                          extent(lse, (size_t)p->total_q * p->num_heads_q * 4), extent(workspace, pl.total)};
+  const long long ts = p->table_stride ? p->table_stride : p->max_pages;
+  const Extent ins[8] = {extent(q, span(p->total_q, qs, qw)),
+                         cache_extent(p, k_view(p, k_cache, 1)), cache_extent(p, v_view(p, v_cache, 1)),
+                         cache_extent(p, k_scale_view(scales)), cache_extent(p, v_scale_view(scales)),
+                         extent(cu_seqlens_q, 4 * ((size_t)p->batch + 1)), extent(kv_lens, 4 * (size_t)p->batch),
+                         extent(block_table, 4 * (size_t)((p->batch - 1) * ts + p->max_pages))};
+  for (int a = 0; a < 3; ++a) {
+    for (const Extent& in : ins)
+      if (overlaps(outs[a], in)) return SDPA_ERR_OVERLAP;
+    for (int b = a + 1; b < 3; ++b)
+      if (overlaps(outs[a], outs[b])) return SDPA_ERR_OVERLAP;
+  }
+  int* err = error_word();
+  if (!err) return SDPA_ERR_CUDA;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return SDPA_ERR_CUDA;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  AddrTable* chk = bind_extents({outs[0], outs[1], outs[2], ins[0], ins[1], ins[2], ins[3], ins[4], ins[5], ins[6], ins[7]},
+                                err, s);
+  if (kAddrCheck && !chk) return SDPA_ERR_CUDA;
+  PagedFp8Launch L;
+  std::memset(&L, 0, sizeof(L));
+  L.p.a = paged_params(p, pl, true, cu_seqlens_q, kv_lens, block_table, o, lse, static_cast<uint8_t*>(workspace), err, chk);
+  L.p.a.box_rows = std::min(p->page_size & -p->page_size, 128);
+  L.p.a.slot_first = slot_first(p);
+  L.p.q = q;
+  L.p.q_stride = qs;
+  L.p.k_scale = scales->k;
+  L.p.v_scale = scales->v;
+  L.p.ks_page = scales->k_page_stride;
+  L.p.ks_slot = scales->k_slot_stride;
+  L.p.ks_head = scales->k_head_stride;
+  L.p.vs_page = scales->v_page_stride;
+  L.p.vs_slot = scales->v_slot_stride;
+  L.p.vs_head = scales->v_head_stride;
+  L.p.k_cache = static_cast<const uint8_t*>(k_cache);
+  L.p.v_cache = static_cast<const uint8_t*>(v_cache);
+  L.p.k_page = p->k_page_stride;
+  L.p.k_slot = p->k_slot_stride;
+  L.p.k_head = p->k_head_stride;
+  L.p.v_page = p->v_page_stride;
+  L.p.v_slot = p->v_slot_stride;
+  L.p.v_head = p->v_head_stride;
+  L.workers = std::min(pl.rows.workers, sms);
+  if (debug_max_ctas() > 0) L.workers = std::min(L.workers, debug_max_ctas());
+  L.stream = s;
+  int launches = 0;
+  rc = timed(SDPA_KERNEL_PAGED, s, [&] { return launch_paged_fp8(L, pl.rows.n, d, p->dtype == SDPA_BF16, &launches); });
+  if (rc) return rc;
   t_last_launches = launches;
   return SDPA_OK;
 }

@@ -49,6 +49,7 @@
 #include <cuda_runtime.h>
 
 #include "common.cuh"
+#include "fp8_row.cuh"
 #include "kernels.h"
 #include "ptx.cuh"
 
@@ -115,15 +116,6 @@ __device__ __forceinline__ void mma_f8_ts(uint32_t d_tmem, uint32_t a_tmem, uint
       "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
-}
-
-// Four fp32 values -> four E4M3 codes (round to nearest even, saturating to
-// +-448), x0 in the lowest byte: consecutive keys of the A operand in TMEM.
-__device__ __forceinline__ uint32_t pack_e4m3x4(float x0, float x1, float x2, float x3) {
-  uint16_t lo, hi;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(x1), "f"(x0));
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(x3), "f"(x2));
-  return (uint32_t)lo | ((uint32_t)hi << 16);
 }
 
 }  // namespace

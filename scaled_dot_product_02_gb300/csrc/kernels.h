@@ -201,6 +201,17 @@ int launch_preprocess(const PrepParams& pp, bool bf16, cudaStream_t s);
 int launch_wait_selftest(uint64_t limit_ns, int* err, cudaStream_t s);
 int launch_dq_finalize(const Geom& g, const float* dq_acc, void* dq, const int* guard, bool bf16, cudaStream_t s);
 
+// Rotation with several positions a token: pair i turns by the angle of axis a's
+// position, for the a with end[a - 1] <= i < end[a].
+struct RopeAxes {
+  int n;                       // axes; 0: one position a token
+  int end[4];                  // behind the last pair of each axis (INT_MAX for the last and what follows)
+  long long pos_stride;        // elements between the axes' positions
+  // A token's angles as staged in shared memory: of each axis the pairs [lo, lo + len), whole blocks of 4, cosines
+  // then sines; pair i's at cos_at + i and sin_at + i of floats in all.
+  int lo[4], len[4], cos_at[4], sin_at[4], floats;
+};
+
 // Per-head norm + rotation, and the append to a paged cache (norm_rope.cu).
 struct NormRopeParams {
   long long rows;              // tokens
@@ -213,7 +224,8 @@ struct NormRopeParams {
   const void *wq, *wk;         // nullptr: rows are copied as they are (append)
   const float* table;          // [max_pos][rot]
   int max_pos;
-  const int32_t* pos;          // [rows]; nullptr: cache positions (append)
+  const int32_t* pos;          // [rows] of each axis; nullptr: cache positions (append)
+  RopeAxes axes;
   void *q_out, *k_out;         // contiguous (k_out: not for the append)
   int parts, parts_q, parts_k;  // warps that share one token, its q heads, its k (and v) heads
   int stage_bytes, stages;     // a warp's ring in shared memory (many tokens)
@@ -223,6 +235,8 @@ struct NormRopeParams {
   long long table_stride;
   void *kc, *vc;
   long long kc_page, kc_slot, kc_head, vc_page, vc_slot, vc_head;
+  uint8_t *k_scale, *v_scale;  // scale bytes of a cache of E4M3 codes; nullptr: a 16-bit cache
+  long long ks_page, ks_slot, ks_head, vs_page, vs_slot, vs_head;
   int* err;
   AddrTable* chk;
 };
@@ -239,6 +253,7 @@ struct NormRopeBwdParams {
   const float* table;
   int max_pos;
   const int32_t* pos;
+  RopeAxes axes;
   void *dq, *dk;
   long long dqs, dks;
   float* part;                 // [blocks + 1][D] partial sums of dw
@@ -255,6 +270,22 @@ struct NormRopeBwdPlan {
 };
 NormRopeBwdPlan norm_rope_bwd_plan(long long rows, int hq, int hkv, int head_dim);
 int launch_norm_rope_bwd(const NormRopeBwdParams& p, int head_dim, bool bf16, int* launches, cudaStream_t s);
+
+// The last keys and values of every sequence of an 8-bit paged cache as packed 16-bit rows (paged_read.cu).
+struct PagedReadParams {
+  long long rows;              // of k_out and v_out
+  int batch, hkv, page_size, num_pages, max_pages;
+  const uint8_t *k_cache, *v_cache, *k_scale, *v_scale;
+  long long k_page, k_slot, k_head, v_page, v_slot, v_head;
+  long long ks_page, ks_slot, ks_head, vs_page, vs_slot, vs_head;
+  void *k_out, *v_out;
+  long long k_row, v_row;      // elements between their rows
+  const int32_t *cu, *kv_lens, *block_table;
+  long long table_stride;
+  int* err;
+  AddrTable* chk;
+};
+int launch_paged_read(const PagedReadParams& p, int head_dim, bool bf16, cudaStream_t s);
 
 // Attention over a paged cache: paged.cu serves sequences with few query rows,
 // paged_pair.cu (head_dim 128) and paged_chunk.cu the others.
@@ -301,6 +332,23 @@ int launch_paged_chunk(const PagedLaunch& L, int head_dim, bool bf16, int* launc
 int launch_paged_pair(const PagedLaunch& L, bool bf16, int* launches);
 // Joins the items that cross a cut between `shares` shares: n rows of dv values an item.
 int launch_paged_join(const PagedLaunch& L, int n, int dv, int shares, bool bf16);
+
+// Attention over a paged cache of E4M3 codes with a scale byte a row (paged_fp8.cu).
+struct PagedFp8Params {
+  PagedParams a;
+  const void* q;
+  long long q_stride;          // elements between tokens
+  const uint8_t *k_scale, *v_scale;
+  long long ks_page, ks_slot, ks_head, vs_page, vs_slot, vs_head;
+  const uint8_t *k_cache, *v_cache;
+  long long k_page, k_slot, k_head, v_page, v_slot, v_head;
+};
+struct PagedFp8Launch {
+  PagedFp8Params p;
+  int workers;                 // CTAs
+  cudaStream_t stream;
+};
+int launch_paged_fp8(const PagedFp8Launch& L, int n, int head_dim, bool bf16, int* launches);
 
 // Log-sum-exp merge of partial results over a split of the keys (merge.cu).
 int launch_merge(const void* o_parts, const float* lse_parts, void* o, float* lse, long long items, int head_dim,

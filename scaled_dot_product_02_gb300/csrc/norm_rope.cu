@@ -27,6 +27,7 @@
 #include <cuda_runtime.h>
 
 #include "common.cuh"
+#include "fp8_row.cuh"
 #include "kernels.h"
 #include "ptx.cuh"
 
@@ -109,13 +110,86 @@ __device__ __forceinline__ Place place_of(int idx, int rot, bool interleaved) {
   t.partner = !t.on || interleaved ? idx : t.second ? idx - half / 8 : idx + half / 8;
   return t;
 }
+// Where the angles come from: the cosines and sines of pairs i .. i + 3 (i a
+// multiple of 4).
+struct RowAngles {  // one row of the table
+  const float* row;
+  int half;
+  AddrTable* chk;
+  __device__ __forceinline__ void block(int i, uint4& c, uint4& s) const {
+    c = load16(chk, row + i);
+    s = load16(chk, row + half + i);
+  }
+};
+struct StagedAngles {  // the same, in shared memory
+  const float* row;
+  int half;
+  __device__ __forceinline__ void block(int i, uint4& c, uint4& s) const {
+    c = *reinterpret_cast<const uint4*>(row + i);
+    s = *reinterpret_cast<const uint4*>(row + half + i);
+  }
+};
+// With several axes a pair's angle is that of the token's position on the
+// pair's axis: each axis has its own row of the table. A block of pairs that
+// two axes share is put together value by value.
+__device__ __forceinline__ int axis_of(const RopeAxes& a, int i) {
+  return (i >= a.end[0]) + (i >= a.end[1]) + (i >= a.end[2]);
+}
+struct AxesAngles {
+  const RopeAxes& a;
+  const float* table;
+  long long row[4];  // where each axis's row starts
+  int half;
+  AddrTable* chk;
+  __device__ __forceinline__ const float* at(int axis) const {
+    return table + (axis == 0 ? row[0] : axis == 1 ? row[1] : axis == 2 ? row[2] : row[3]);
+  }
+  __device__ __forceinline__ void block(int i, uint4& c, uint4& s) const {
+    const int first = axis_of(a, i);
+    if (first == axis_of(a, i + 3)) {
+      c = load16(chk, at(first) + i);
+      s = load16(chk, at(first) + half + i);
+      return;
+    }
+    uint32_t x[4], y[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float* p = at(axis_of(a, i + e)) + i + e;
+      x[e] = SDPA_ADDR_OK(chk, p, 4) ? __float_as_uint(__ldg(p)) : 0u;
+      y[e] = SDPA_ADDR_OK(chk, p + half, 4) ? __float_as_uint(__ldg(p + half)) : 0u;
+    }
+    c = make_uint4(x[0], x[1], x[2], x[3]);
+    s = make_uint4(y[0], y[1], y[2], y[3]);
+  }
+};
+struct StagedAxes {  // each axis's pairs, cosines then sines, behind one another in shared memory
+  const RopeAxes& a;
+  const float* base;
+  __device__ __forceinline__ void block(int i, uint4& c, uint4& s) const {
+    const int first = axis_of(a, i);
+    if (first == axis_of(a, i + 3)) {
+      c = *reinterpret_cast<const uint4*>(base + a.cos_at[first] + i);
+      s = *reinterpret_cast<const uint4*>(base + a.sin_at[first] + i);
+      return;
+    }
+    uint32_t x[4], y[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int ax = axis_of(a, i + e);
+      x[e] = __float_as_uint(base[a.cos_at[ax] + i + e]);
+      y[e] = __float_as_uint(base[a.sin_at[ax] + i + e]);
+    }
+    c = make_uint4(x[0], x[1], x[2], x[3]);
+    s = make_uint4(y[0], y[1], y[2], y[3]);
+  }
+};
+
 // The cosines of vector idx and its sines, signed for turning forwards: value e
 // becomes y_e c_e + partner_e s_e.
-template <bool SHARED = false>
-__device__ __forceinline__ void angles_of(const Place& t, int idx, const float* row, int rot, bool interleaved,
-                                          float2 (&c)[4], float2 (&s)[4], AddrTable* chk) {
+template <class Angles>
+__device__ __forceinline__ void angles_of(const Place& t, int idx, const Angles& from, int rot, bool interleaved,
+                                          float2 (&c)[4], float2 (&s)[4]) {
   const int half = rot / 2;
-  auto get = [&](const float* from) { return SHARED ? *reinterpret_cast<const uint4*>(from) : load16(chk, from); };
   if (!t.on) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -123,7 +197,8 @@ __device__ __forceinline__ void angles_of(const Place& t, int idx, const float* 
       s[e] = make_float2(0.f, 0.f);
     }
   } else if (interleaved) {
-    const uint4 a = get(row + idx * 4), b = get(row + half + idx * 4);
+    uint4 a, b;
+    from.block(idx * 4, a, b);
     const float cs[4] = {__uint_as_float(a.x), __uint_as_float(a.y), __uint_as_float(a.z), __uint_as_float(a.w)};
     const float sn[4] = {__uint_as_float(b.x), __uint_as_float(b.y), __uint_as_float(b.z), __uint_as_float(b.w)};
 #pragma unroll
@@ -136,7 +211,8 @@ __device__ __forceinline__ void angles_of(const Place& t, int idx, const float* 
     const float sg = t.second ? 1.f : -1.f;
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
-      const uint4 a = get(row + i0 + q * 4), b = get(row + half + i0 + q * 4);
+      uint4 a, b;
+      from.block(i0 + q * 4, a, b);
       c[2 * q] = make_float2(__uint_as_float(a.x), __uint_as_float(a.y));
       c[2 * q + 1] = make_float2(__uint_as_float(a.z), __uint_as_float(a.w));
       s[2 * q] = make_float2(sg * __uint_as_float(b.x), sg * __uint_as_float(b.y));
@@ -150,6 +226,7 @@ struct Slot {
   bool live;     // its rows are written
   int position;  // in its sequence
   long long k_at, v_at;  // element offsets of head 0
+  int page, slot;
 };
 
 // The sequence of a token is the number of sequences that end at or before it
@@ -159,6 +236,7 @@ __device__ __forceinline__ Slot find_slot(const NormRopeParams& p, long long row
   s.live = false;
   s.position = 0;
   s.k_at = s.v_at = 0;
+  s.page = s.slot = 0;
   int b = 0;
   for (int base = 0; base < p.batch; base += 32) {
     const int i = base + lane;
@@ -181,14 +259,34 @@ __device__ __forceinline__ Slot find_slot(const NormRopeParams& p, long long row
   const int slot = (int)(pos - col * p.page_size);
   s.live = true;
   s.position = (int)pos;
+  s.page = page;
+  s.slot = slot;
   s.k_at = page * p.kc_page + slot * p.kc_slot;
   s.v_at = page * p.vc_page + slot * p.vc_slot;
   return s;
 }
 
+// A token's positions, one or each axis's (the others 0); false when one lies
+// outside the table. cached: the cache position serves.
+template <bool AXES>
+__device__ __forceinline__ bool positions_of(const NormRopeParams& p, long long row, bool cached, int position, int (&pos)[4]) {
+  bool fits = true;
+#pragma unroll
+  for (int a = 0; a < 4; ++a) {
+    pos[a] = 0;
+    if (p.rot > 0 && a < (AXES ? p.axes.n : 1)) {
+      pos[a] = cached ? position : load_i32(p.chk, p.pos + a * p.axes.pos_stride + row, -1);
+      fits = fits && pos[a] >= 0 && pos[a] < p.max_pos;
+    }
+  }
+  return fits;
+}
+
 // A warp takes Row::HEADS heads of one tensor (q, k or, appending, v) of one token.
-template <bool BF16, int D, bool APPEND, bool NORM>
-__global__ void __launch_bounds__(kThreads, Row<D>::VPL == 1 ? 6 : 4)
+// FP8 (appending): k and v go into the cache as E4M3 codes and a scale byte a
+// row (fp8_row.cuh), from the fp32 values, so they round once.
+template <bool BF16, int D, bool APPEND, bool NORM, bool AXES, bool FP8>
+__global__ void __launch_bounds__(kThreads, Row<D>::VPL == 1 && !AXES && !FP8 ? 6 : 4)
     norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
   using E = Elem<BF16>;
   using T = typename E::T;
@@ -238,20 +336,25 @@ __global__ void __launch_bounds__(kThreads, Row<D>::VPL == 1 ? 6 : 4)
   // where head h of this tensor goes
   T* dst = is_q ? static_cast<T*>(p.q_out) + row * p.hq * D : static_cast<T*>(p.k_out) + row * p.hkv * D;
   long long step = D;
+  uint8_t *codes = nullptr, *scale = nullptr;  // FP8
+  long long scale_step = 0;
   if (APPEND && !is_q) {
-    dst = is_v ? static_cast<T*>(p.vc) + slot.v_at : static_cast<T*>(p.kc) + slot.k_at;
     step = is_v ? p.vc_head : p.kc_head;
+    if constexpr (FP8) {
+      codes = is_v ? static_cast<uint8_t*>(p.vc) + slot.v_at : static_cast<uint8_t*>(p.kc) + slot.k_at;
+      scale = is_v ? p.v_scale + slot.page * p.vs_page + slot.slot * p.vs_slot
+                   : p.k_scale + slot.page * p.ks_page + slot.slot * p.ks_slot;
+      scale_step = is_v ? p.vs_head : p.ks_head;
+    } else {
+      dst = is_v ? static_cast<T*>(p.vc) + slot.v_at : static_cast<T*>(p.kc) + slot.k_at;
+    }
   }
   float2 ca[R::VPL][4], cb[R::VPL][4];
   if (NORM && !is_v) {
-    const float* angles = nullptr;
-    if (p.rot > 0) {
-      const int pos = APPEND && !p.pos ? slot.position : load_i32(p.chk, p.pos + row, -1);
-      if (pos < 0 || pos >= p.max_pos) {
-        if (lane == 0) record_error(p.err, SDPA_ERR_BAD_INDEX);
-        return;
-      }
-      angles = p.table + (long long)pos * p.rot;
+    int pos[4];
+    if (!positions_of<AXES>(p, row, APPEND && !p.pos, slot.position, pos)) {
+      if (lane == 0) record_error(p.err, SDPA_ERR_BAD_INDEX);
+      return;
     }
     const T* weight = static_cast<const T*>(is_q ? p.wq : p.wk);
 #pragma unroll
@@ -261,7 +364,14 @@ __global__ void __launch_bounds__(kThreads, Row<D>::VPL == 1 ? 6 : 4)
       const bool in = R::in(idx, D);
       unpack8<E>(in ? load16(p.chk, weight + idx * 8) : make_uint4(0u, 0u, 0u, 0u), wt);
       unpack8<E>(in ? load16(p.chk, weight + at[v].partner * 8) : make_uint4(0u, 0u, 0u, 0u), wp);
-      angles_of(at[v], idx, angles, p.rot, inter, c, s, p.chk);
+      if constexpr (!AXES)
+        angles_of(at[v], idx, RowAngles{p.table + (long long)pos[0] * p.rot, p.rot / 2, p.chk}, p.rot, inter, c, s);
+      else
+        angles_of(at[v], idx,
+                  AxesAngles{p.axes, p.table, {(long long)pos[0] * p.rot, (long long)pos[1] * p.rot,
+                                               (long long)pos[2] * p.rot, (long long)pos[3] * p.rot},
+                             p.rot / 2, p.chk},
+                  p.rot, inter, c, s);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         ca[v][e] = fmul2(wt[e], c[e]);
@@ -269,14 +379,15 @@ __global__ void __launch_bounds__(kThreads, Row<D>::VPL == 1 ? 6 : 4)
       }
     }
   } else if (NORM && APPEND && p.rot > 0) {
-    const int pos = p.pos ? load_i32(p.chk, p.pos + row, -1) : slot.position;  // a token with a bad one is skipped whole
-    if (pos < 0 || pos >= p.max_pos) return;
+    int pos[4];  // a token with a bad one is skipped whole
+    if (!positions_of<AXES>(p, row, !p.pos, slot.position, pos)) return;
   }
 
   while (true) {
 #pragma unroll
     for (int u = 0; u < R::UNROLL; ++u) {
       const int h = h0 + grp + u * R::SUB;
+      float2 y[R::VPL][4];  // FP8: the row in fp32
       if (NORM && !is_v) {
         float2 f[R::VPL][4], ss = make_float2(0.f, 0.f);
 #pragma unroll
@@ -297,8 +408,40 @@ __global__ void __launch_bounds__(kThreads, Row<D>::VPL == 1 ? 6 : 4)
             const float2 t = fmul2(f[v][e], ca[v][e]);
             g[e] = fmul2(at[v].on ? ffma2(other, cb[v][e], t) : t, r);
           }
-          x[u][v] = pack8<E>(g);
+          if (FP8 && !is_q) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[v][e] = g[e];
+          } else {
+            x[u][v] = pack8<E>(g);
+          }
         }
+      } else if (FP8) {
+#pragma unroll
+        for (int v = 0; v < R::VPL; ++v) unpack8<E>(x[u][v], y[v]);
+      }
+      if (FP8 && !is_q) {
+        float top = 0.f;  // fmaxf passes over NaN
+#pragma unroll
+        for (int v = 0; v < R::VPL; ++v)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) top = fmaxf(top, fmaxf(fabsf(y[v][e].x), fabsf(y[v][e].y)));
+#pragma unroll
+        for (int o = R::LPH / 2; o > 0; o /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const int ex = fp8_row_exponent<BF16>(top);
+        const float inv = exp2_int(-ex);
+        if (h >= h_end) continue;
+        uint8_t* to_scale = scale + h * scale_step;
+        if (sub == 0 && SDPA_ADDR_OK(p.chk, to_scale, 1)) *to_scale = (uint8_t)(ex + 127);
+#pragma unroll
+        for (int v = 0; v < R::VPL; ++v) {
+          const int idx = v * R::LPH + sub;
+          uint8_t* to = codes + h * step + idx * 8;
+          if (R::in(idx, width) && SDPA_ADDR_OK(p.chk, to, 8))
+            *reinterpret_cast<uint2*>(to) =
+                make_uint2(pack_e4m3x4(y[v][0].x * inv, y[v][0].y * inv, y[v][1].x * inv, y[v][1].y * inv),
+                           pack_e4m3x4(y[v][2].x * inv, y[v][2].y * inv, y[v][3].x * inv, y[v][3].y * inv));
+        }
+        continue;
       }
       if (h >= h_end) continue;
 #pragma unroll
@@ -371,7 +514,16 @@ __device__ __forceinline__ void ring_copy(AddrTable* chk, void* dst, const void*
     mbar_complete_tx(bar, bytes);
 }
 
-template <bool BF16, int D, bool INTER>
+// One axis's pairs of its row of the table, cosines and sines, whole blocks of 4.
+__device__ __forceinline__ void axis_copy(const RopeAxes& a, const float* row, int half, uint8_t* staged, uint64_t* bar,
+                                          int axis, AddrTable* chk) {
+  const int lo = a.lo[axis], n = a.len[axis];
+  float* to = reinterpret_cast<float*>(staged);
+  ring_copy(chk, to + a.cos_at[axis] + lo, row + lo, n * 4, bar);
+  ring_copy(chk, to + a.sin_at[axis] + lo, row + half + lo, n * 4, bar);
+}
+
+template <bool BF16, int D, bool INTER, bool AXES>
 __global__ void __launch_bounds__(kFwdWarps * 32, 1) norm_rope_ring_kernel(const __grid_constant__ NormRopeParams p) {
   using E = Elem<BF16>;
   using T = typename E::T;
@@ -400,12 +552,18 @@ __global__ void __launch_bounds__(kFwdWarps * 32, 1) norm_rope_ring_kernel(const
   fil = ahead = cur;
   int n_ahead = 0;
   auto position = [&]() {
-    const int x = p.rot > 0 && n_ahead < mine ? load_i32(p.chk, p.pos + ahead.row, -1) : 0;
+    // with several axes lane a has axis a's, the others none
+    const bool here = p.rot > 0 && n_ahead < mine && (!AXES || lane < p.axes.n);
+    const int x = here ? load_i32(p.chk, p.pos + (AXES ? lane * p.axes.pos_stride : 0) + ahead.row, -1) : 0;
     ++n_ahead;
     ahead.next();
     return x;
   };
-  auto bad = [&](int pos) { return p.rot > 0 && (pos < 0 || pos >= p.max_pos); };
+  auto bad = [&](int pos) {
+    const bool x = p.rot > 0 && (pos < 0 || pos >= p.max_pos);
+    return AXES ? __any_sync(0xffffffffu, x) != 0 : x;
+  };
+  const uint32_t angle_bytes = (AXES ? p.axes.floats : p.rot) * 4;
   // heads of a unit and where they start
   auto heads_of = [&](int part, bool& is_q, int& h0) {
     is_q = part < p.parts_q;
@@ -414,21 +572,25 @@ __global__ void __launch_bounds__(kFwdWarps * 32, 1) norm_rope_ring_kernel(const
   };
   int filled = 0;
   auto fill = [&](int pos) {
+    const bool skip = bad(pos);
     if (filled < mine && lane == 0) {
       uint64_t* bar = ring.bar_of(filled);
-      if (bad(pos)) {  // not copied: an empty arrival passes the stage's phase
+      if (skip) {  // not copied: an empty arrival passes the stage's phase
         mbar_arrive(bar);
       } else {
         bool is_q;
         int h0;
         const int n = heads_of(fil.part, is_q, h0);
         const T* src = (is_q ? static_cast<const T*>(p.q) + fil.row * p.qs : static_cast<const T*>(p.k) + fil.row * p.ks) + h0 * D;
-        mbar_arrive_expect_tx(bar, n * D * 2 + p.rot * 4);
+        mbar_arrive_expect_tx(bar, n * D * 2 + angle_bytes);
         ring_copy(p.chk, ring.at(filled), src, n * D * 2, bar);
-        if (p.rot > 0)
+        if (!AXES && p.rot > 0)
           ring_copy(p.chk, ring.at(filled) + HEADS * D * 2, p.table + (long long)pos * p.rot, p.rot * 4, bar);
       }
     }
+    if (AXES && filled < mine && !skip && lane < p.axes.n)
+      axis_copy(p.axes, p.table + (long long)pos * p.rot, p.rot / 2, ring.at(filled) + HEADS * D * 2, ring.bar_of(filled),
+                lane, p.chk);
     if (filled < mine) ++filled;
     fil.next();
   };
@@ -463,7 +625,11 @@ __global__ void __launch_bounds__(kFwdWarps * 32, 1) norm_rope_ring_kernel(const
         const bool in = R::in(idx, D);
         unpack8<E>(in ? load16(p.chk, weight + idx * 8) : make_uint4(0u, 0u, 0u, 0u), wt);
         unpack8<E>(in ? load16(p.chk, weight + at[v].partner * 8) : make_uint4(0u, 0u, 0u, 0u), wp);
-        angles_of<true>(at[v], idx, reinterpret_cast<const float*>(st + HEADS * D * 2), p.rot, INTER, c, s, p.chk);
+        const float* staged = reinterpret_cast<const float*>(st + HEADS * D * 2);
+        if constexpr (AXES)
+          angles_of(at[v], idx, StagedAxes{p.axes, staged}, p.rot, INTER, c, s);
+        else
+          angles_of(at[v], idx, StagedAngles{staged, p.rot / 2}, p.rot, INTER, c, s);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           ca[v][e] = fmul2(wt[e], c[e]);
@@ -523,7 +689,7 @@ __global__ void __launch_bounds__(kFwdWarps * 32, 1) norm_rope_ring_kernel(const
 // registers. Block b writes the sum of its q warps to slot b and that of its k
 // warps to slot b + 1 (only one block can have both); dw_kernel adds the slots
 // in order.
-template <bool BF16, int D, bool INTER>
+template <bool BF16, int D, bool INTER, bool AXES>
 __global__ void __launch_bounds__(kBwdWarps * 32, 1) norm_rope_bwd_kernel(const __grid_constant__ NormRopeBwdParams p) {
   using E = Elem<BF16>;
   using T = typename E::T;
@@ -568,28 +734,38 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 1) norm_rope_bwd_kernel(const 
   fil = ahead = cur;
   int n_ahead = 0;
   auto position = [&]() {
-    const int x = p.rot > 0 && n_ahead < mine ? load_i32(p.chk, p.pos + ahead.row, -1) : 0;
+    // with several axes lane a has axis a's, the others none
+    const bool here = p.rot > 0 && n_ahead < mine && (!AXES || lane < p.axes.n);
+    const int x = here ? load_i32(p.chk, p.pos + (AXES ? lane * p.axes.pos_stride : 0) + ahead.row, -1) : 0;
     ++n_ahead;
     ahead.next();
     return x;
   };
-  auto bad = [&](int pos) { return p.rot > 0 && (pos < 0 || pos >= p.max_pos); };
+  auto bad = [&](int pos) {
+    const bool x = p.rot > 0 && (pos < 0 || pos >= p.max_pos);
+    return AXES ? __any_sync(0xffffffffu, x) != 0 : x;
+  };
+  const uint32_t angle_bytes = (AXES ? p.axes.floats : p.rot) * 4;
   constexpr int SIDE = HEADS * D * 2;  // x, then dy, then the angles
   int filled = 0;
   auto fill = [&](int pos) {
+    const bool skip = bad(pos);
     if (filled < mine && lane == 0) {
       uint64_t* bar = ring.bar_of(filled);
-      if (bad(pos)) {  // not copied: an empty arrival passes the stage's phase
+      if (skip) {  // not copied: an empty arrival passes the stage's phase
         mbar_arrive(bar);
       } else {
         const int h0 = fil.part * HEADS, n = min(HEADS, heads - h0);
         uint8_t* st = ring.at(filled);
-        mbar_arrive_expect_tx(bar, 2 * n * D * 2 + p.rot * 4);
+        mbar_arrive_expect_tx(bar, 2 * n * D * 2 + angle_bytes);
         ring_copy(p.chk, st, x0 + fil.row * xs + h0 * D, n * D * 2, bar);
         ring_copy(p.chk, st + SIDE, g0 + (fil.row * heads + h0) * D, n * D * 2, bar);
-        if (p.rot > 0) ring_copy(p.chk, st + 2 * SIDE, p.table + (long long)pos * p.rot, p.rot * 4, bar);
+        if (!AXES && p.rot > 0) ring_copy(p.chk, st + 2 * SIDE, p.table + (long long)pos * p.rot, p.rot * 4, bar);
       }
     }
+    if (AXES && filled < mine && !skip && lane < p.axes.n)
+      axis_copy(p.axes, p.table + (long long)pos * p.rot, p.rot / 2, ring.at(filled) + 2 * SIDE, ring.bar_of(filled), lane,
+                p.chk);
     if (filled < mine) ++filled;
     fil.next();
   };
@@ -618,8 +794,11 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 1) norm_rope_bwd_kernel(const 
       float2 c[R::VPL][4], s[R::VPL][4];
 #pragma unroll
       for (int v = 0; v < R::VPL; ++v) {
-        angles_of<true>(at[v], v * R::LPH + sub, reinterpret_cast<const float*>(st + 2 * SIDE), p.rot, INTER, c[v], s[v],
-                        p.chk);
+        const float* staged = reinterpret_cast<const float*>(st + 2 * SIDE);
+        if constexpr (AXES)
+          angles_of(at[v], v * R::LPH + sub, StagedAxes{p.axes, staged}, p.rot, INTER, c[v], s[v]);
+        else
+          angles_of(at[v], v * R::LPH + sub, StagedAngles{staged, p.rot / 2}, p.rot, INTER, c[v], s[v]);
 #pragma unroll
         for (int e = 0; e < 4; ++e) s[v][e] = make_float2(-s[v][e].x, -s[v][e].y);  // turned back
       }
@@ -748,10 +927,11 @@ int launch_t(NormRopeParams p, bool append, cudaStream_t s) {
       return SDPA_ERR_CUDA;
     // the rings pay from a few units a warp on; below, registers are quicker to start
     if (p.rows * (parts_q + parts_k) >= (long long)sms * kFwdWarps * 2) {
-      auto kern = p.interleaved ? norm_rope_ring_kernel<BF16, D, true> : norm_rope_ring_kernel<BF16, D, false>;
+      auto kern = p.axes.n ? (p.interleaved ? norm_rope_ring_kernel<BF16, D, true, true> : norm_rope_ring_kernel<BF16, D, false, true>)
+                           : (p.interleaved ? norm_rope_ring_kernel<BF16, D, true, false> : norm_rope_ring_kernel<BF16, D, false, false>);
       p.parts_q = parts_q;
       p.parts = parts_q + parts_k;
-      p.stage_bytes = HEADS * D * 2 + p.rot * 4;
+      p.stage_bytes = HEADS * D * 2 + (p.axes.n ? p.axes.floats : p.rot) * 4;
       p.stages = ring_stages(p.stage_bytes, kFwdWarps);
       if (const int rc = set_kernel_smem(reinterpret_cast<const void*>(kern), kRingSmem, 100)) return rc;
       kern<<<(unsigned)sms, kFwdWarps * 32, kFwdWarps * p.stages * p.stage_bytes, s>>>(p);
@@ -764,19 +944,23 @@ int launch_t(NormRopeParams p, bool append, cudaStream_t s) {
   const long long blocks = (p.rows * p.parts + kWarps - 1) / kWarps;
   if (blocks > 0x7fffffffLL) return SDPA_ERR_UNSUPPORTED;
   const unsigned grid = (unsigned)blocks;
-  if (!append)
-    norm_rope_kernel<BF16, D, false, true><<<grid, kThreads, 0, s>>>(p);
-  else if (p.wk)
-    norm_rope_kernel<BF16, D, true, true><<<grid, kThreads, 0, s>>>(p);
-  else
-    norm_rope_kernel<BF16, D, true, false><<<grid, kThreads, 0, s>>>(p);
+  auto kern = !append        ? (p.axes.n ? norm_rope_kernel<BF16, D, false, true, true, false>
+                                         : norm_rope_kernel<BF16, D, false, true, false, false>)
+              : p.k_scale    ? (p.wk == nullptr ? norm_rope_kernel<BF16, D, true, false, false, true>
+                                : p.axes.n      ? norm_rope_kernel<BF16, D, true, true, true, true>
+                                                : norm_rope_kernel<BF16, D, true, true, false, true>)
+              : p.wk == nullptr ? norm_rope_kernel<BF16, D, true, false, false, false>
+              : p.axes.n        ? norm_rope_kernel<BF16, D, true, true, true, false>
+                                : norm_rope_kernel<BF16, D, true, true, false, false>;
+  kern<<<grid, kThreads, 0, s>>>(p);
   return cudaGetLastError() == cudaSuccess ? SDPA_OK : SDPA_ERR_CUDA;
 }
 
 template <bool BF16, int D>
 int launch_bwd_t(NormRopeBwdParams p, cudaStream_t s) {
-  auto kern = p.interleaved ? norm_rope_bwd_kernel<BF16, D, true> : norm_rope_bwd_kernel<BF16, D, false>;
-  p.stage_bytes = 2 * RingRows<D>::BWD_HEADS * D * 2 + p.rot * 4;
+  auto kern = p.axes.n ? (p.interleaved ? norm_rope_bwd_kernel<BF16, D, true, true> : norm_rope_bwd_kernel<BF16, D, false, true>)
+                       : (p.interleaved ? norm_rope_bwd_kernel<BF16, D, true, false> : norm_rope_bwd_kernel<BF16, D, false, false>);
+  p.stage_bytes = 2 * RingRows<D>::BWD_HEADS * D * 2 + (p.axes.n ? p.axes.floats : p.rot) * 4;
   p.stages = ring_stages(p.stage_bytes, kBwdWarps);
   if (const int rc = set_kernel_smem(reinterpret_cast<const void*>(kern), kRingSmem, 100)) return rc;
   const int bytes = std::max(kBwdWarps * p.stages * p.stage_bytes, kBwdWarps * D * 4);

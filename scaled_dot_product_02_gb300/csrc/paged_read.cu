@@ -1,0 +1,141 @@
+// paged_read.cu -- the last keys and values of every sequence of an 8-bit paged
+// cache as packed 16-bit rows: y = code 2^e (fp8_row.cuh), rounded once (not at
+// all when the type is the one the row was quantised from).
+//
+// Bound by memory: a byte read and two written a value. A warp takes a few
+// tokens, all heads: their places in the cache are found by a lane each (a
+// binary search among the sequences' ends), then all lanes walk the tokens'
+// values, eight a lane and step, with several steps' loads in flight.
+#include <algorithm>
+#include <cuda_runtime.h>
+
+#include "common.cuh"
+#include "fp8_row.cuh"
+#include "kernels.h"
+
+namespace sdpa {
+
+namespace {
+
+constexpr int kThreads = 128;
+constexpr int kTokens = 4;  // tokens of a warp
+constexpr int kSteps = 8;   // loads a lane has in flight
+
+struct Place {
+  long long k_at, v_at;    // head 0's codes
+  long long ks_at, vs_at;  // and scale bytes
+  bool live;
+};
+
+__device__ __forceinline__ Place place_of(const PagedReadParams& p, long long row) {
+  Place x;
+  x.live = false;
+  x.k_at = x.v_at = x.ks_at = x.vs_at = 0;
+  // the first sequence that ends behind the row
+  int lo = 0, hi = p.batch;
+  while (lo < hi) {
+    const int mid = (lo + hi) / 2;
+    const int32_t* end = p.cu + mid + 1;
+    if ((SDPA_ADDR_OK(p.chk, end, 4) ? __ldg(end) : 0) <= row)
+      lo = mid + 1;
+    else
+      hi = mid;
+  }
+  if (lo >= p.batch) return x;  // behind the last sequence
+  const bool in = SDPA_ADDR_OK(p.chk, p.cu + lo, 8) && SDPA_ADDR_OK(p.chk, p.kv_lens + lo, 4);
+  const int first = in ? __ldg(p.cu + lo) : 0, end = in ? __ldg(p.cu + lo + 1) : 0;
+  const long long pos = (long long)(in ? __ldg(p.kv_lens + lo) : 0) - (end - row);
+  const long long col = pos / p.page_size;
+  if (first > row || end <= row || end > p.rows || pos < 0 || col >= p.max_pages) {
+    record_error(p.err, SDPA_ERR_BAD_SEQLENS);
+    return x;
+  }
+  const int32_t* id = p.block_table + lo * p.table_stride + col;
+  const int page = SDPA_ADDR_OK(p.chk, id, 4) ? __ldg(id) : -1;
+  if (page < 0 || page >= p.num_pages) {
+    record_error(p.err, SDPA_ERR_BAD_INDEX);
+    return x;
+  }
+  const long long slot = pos - col * p.page_size;
+  x.live = true;
+  x.k_at = page * p.k_page + slot * p.k_slot;
+  x.v_at = page * p.v_page + slot * p.v_slot;
+  x.ks_at = page * p.ks_page + slot * p.ks_slot;
+  x.vs_at = page * p.vs_page + slot * p.vs_slot;
+  return x;
+}
+
+template <bool BF16, int D, int DV>
+__global__ void __launch_bounds__(kThreads) paged_read_kernel(const __grid_constant__ PagedReadParams p) {
+  using E = Elem<BF16>;
+  const int lane = threadIdx.x % 32;
+  const long long row0 = ((long long)blockIdx.x * (kThreads / 32) + threadIdx.x / 32) * kTokens;
+  if (row0 >= p.rows) return;
+  Place mine;
+  mine.live = false;
+  mine.k_at = mine.v_at = mine.ks_at = mine.vs_at = 0;
+  if (lane < kTokens && row0 + lane < p.rows) mine = place_of(p, row0 + lane);
+  const uint32_t live = __ballot_sync(0xffffffffu, mine.live);
+  const int vecs_k = p.hkv * (D / 8), vecs = vecs_k + p.hkv * (DV / 8);  // of a token: K's, then V's
+#pragma unroll 1
+  for (int t = 0; t < kTokens; ++t) {
+    if (!(live >> t & 1)) continue;
+    const uint8_t* k = p.k_cache + __shfl_sync(0xffffffffu, mine.k_at, t);
+    const uint8_t* v = p.v_cache + __shfl_sync(0xffffffffu, mine.v_at, t);
+    const uint8_t* ks = p.k_scale + __shfl_sync(0xffffffffu, mine.ks_at, t);
+    const uint8_t* vs = p.v_scale + __shfl_sync(0xffffffffu, mine.vs_at, t);
+    uint16_t* ko = static_cast<uint16_t*>(p.k_out) + (row0 + t) * p.k_row;
+    uint16_t* vo = static_cast<uint16_t*>(p.v_out) + (row0 + t) * p.v_row;
+#pragma unroll 1
+    for (int i0 = lane; i0 < vecs; i0 += 32 * kSteps) {
+      uint2 c[kSteps];
+      int e[kSteps];
+#pragma unroll
+      for (int x = 0; x < kSteps; ++x) {
+        const int i = i0 + x * 32;
+        const bool is_v = i >= vecs_k;
+        const int w = is_v ? DV / 8 : D / 8, j = is_v ? i - vecs_k : i, h = j / w;
+        const uint8_t* from = (is_v ? v + h * p.v_head : k + h * p.k_head) + (j - h * w) * 8;
+        const uint8_t* se = is_v ? vs + h * p.vs_head : ks + h * p.ks_head;
+        const bool in = i < vecs && SDPA_ADDR_OK(p.chk, from, 8) && SDPA_ADDR_OK(p.chk, se, 1);
+        c[x] = in ? __ldg(reinterpret_cast<const uint2*>(from)) : make_uint2(0u, 0u);
+        e[x] = in ? __ldg(se) : 127;
+      }
+#pragma unroll
+      for (int x = 0; x < kSteps; ++x) {
+        const int i = i0 + x * 32;
+        if (i >= vecs) break;
+        const bool is_v = i >= vecs_k;
+        uint16_t* to = is_v ? vo + (i - vecs_k) * 8 : ko + i * 8;
+        const float s = exp2_byte(e[x]);
+        uint32_t y[4];
+#pragma unroll
+        for (int z = 0; z < 4; ++z) {
+          const float2 f = Elem<false>::unpack(unpack_e4m3x2((uint16_t)((z < 2 ? c[x].x : c[x].y) >> (16 * (z & 1)))));
+          y[z] = E::pack(f.x * s, f.y * s);
+        }
+        if (SDPA_ADDR_OK(p.chk, to, 16)) *reinterpret_cast<uint4*>(to) = make_uint4(y[0], y[1], y[2], y[3]);
+      }
+    }
+  }
+}
+
+template <bool BF16>
+int launch_t(const PagedReadParams& p, int head_dim, cudaStream_t s) {
+  constexpr int per = kThreads / 32 * kTokens;
+  const unsigned grid = (unsigned)((p.rows + per - 1) / per);
+  auto kern = head_dim == 128   ? paged_read_kernel<BF16, 128, 128>
+              : head_dim == 192 ? paged_read_kernel<BF16, 192, 128>
+              : head_dim == 256 ? paged_read_kernel<BF16, 256, 256>
+                                : paged_read_kernel<BF16, 512, 512>;
+  kern<<<grid, kThreads, 0, s>>>(p);
+  return cudaGetLastError() == cudaSuccess ? SDPA_OK : SDPA_ERR_CUDA;
+}
+
+}  // namespace
+
+int launch_paged_read(const PagedReadParams& p, int head_dim, bool bf16, cudaStream_t s) {
+  return bf16 ? launch_t<true>(p, head_dim, s) : launch_t<false>(p, head_dim, s);
+}
+
+}  // namespace sdpa
