@@ -512,8 +512,8 @@ SDPA_API int sdpa_paged_read_fp8(const sdpa_paged_problem* p, const sdpa_paged_s
 
 /* sdpa_paged_fwd over an 8-bit cache: the attention over the values that codes and scales stand for,
  * exactly (q stays 16-bit), with the same masks, outputs, errors and workspace rules. Scale bytes of
- * keys that no query row sees may hold anything. Of the others 255 counts as infinite, 0 as zero. A row of q that
- * is not finite gives NaN. */
+ * keys that no query row sees may hold anything; others are taken into 47 .. 207, what the append
+ * writes. A row of q that is not finite gives NaN. */
 SDPA_API size_t sdpa_paged_fwd_fp8_workspace_size(const sdpa_paged_problem* p);
 SDPA_API int sdpa_paged_fwd_fp8(const sdpa_paged_problem* p, const sdpa_paged_scales* scales, const void* q,
                                 const void* k_cache, const void* v_cache, void* o, float* lse,

@@ -658,10 +658,10 @@ PagedParams paged_params(const sdpa_paged_problem* p, const PagedPlan& pl, bool 
 // a single head counts as [page][slot][head].
 bool slot_first(const sdpa_paged_problem* p) { return p->num_heads_kv > 1 && p->k_slot_stride < p->k_head_stride; }
 
-// 4-D map of a paged cache {width, then head and slot by increasing stride, page}:
-// boxes are 64 columns (128 bytes, 128-byte swizzle) x box_rows slots of one head of one page.
+// 4-D map of a paged cache {width, then head and slot by increasing stride, page}: boxes are 128 bytes of a row (64
+// 16-bit values or 128 codes, 128-byte swizzle) x box_rows slots of one head of one page.
 int encode_cache(CUtensorMap* m, const void* base, const sdpa_paged_problem* p, int width, long long page, long long slot,
-                 long long head, int box_rows, bool bf16) {
+                 long long head, int box_rows, CUtensorMapDataType type, int bytes) {
   auto fn = encode_fn();
   if (!fn) return SDPA_ERR_CUDA;
   const bool first = slot_first(p);
@@ -670,13 +670,21 @@ int encode_cache(CUtensorMap* m, const void* base, const sdpa_paged_problem* p, 
   if (p->num_pages == 1) page = hi;
   const cuuint64_t dims[4] = {(cuuint64_t)width, (cuuint64_t)(first ? p->page_size : p->num_heads_kv),
                               (cuuint64_t)(first ? p->num_heads_kv : p->page_size), (cuuint64_t)p->num_pages};
-  const cuuint64_t strides[3] = {(cuuint64_t)lo * 2, (cuuint64_t)hi * 2, (cuuint64_t)page * 2};
-  const cuuint32_t box[4] = {64, (cuuint32_t)(first ? box_rows : 1), (cuuint32_t)(first ? 1 : box_rows), 1};
+  const cuuint64_t strides[3] = {(cuuint64_t)lo * bytes, (cuuint64_t)hi * bytes, (cuuint64_t)page * bytes};
+  const cuuint32_t box[4] = {(cuuint32_t)(128 / bytes), (cuuint32_t)(first ? box_rows : 1), (cuuint32_t)(first ? 1 : box_rows), 1};
   const cuuint32_t estr[4] = {1, 1, 1, 1};
-  CUresult r = fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
-                  const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+  CUresult r = fn(m, type, 4, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? SDPA_OK : SDPA_ERR_CUDA;
+}
+int encode_cache(CUtensorMap* m, const void* base, const sdpa_paged_problem* p, int width, long long page, long long slot,
+                 long long head, int box_rows, bool bf16) {
+  return encode_cache(m, base, p, width, page, slot, head, box_rows,
+                      bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2);
+}
+int encode_codes(CUtensorMap* m, const void* base, const sdpa_paged_problem* p, int width, long long page, long long slot,
+                 long long head, int box_rows) {
+  return encode_cache(m, base, p, width, page, slot, head, box_rows, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1);
 }
 
 // One of a paged cache's tensors: rows of `width` values of `bytes` each, one for every page, slot and head.
@@ -1728,14 +1736,10 @@ int sdpa_paged_fwd_fp8(const sdpa_paged_problem* p, const sdpa_paged_scales* sca
   L.p.vs_page = scales->v_page_stride;
   L.p.vs_slot = scales->v_slot_stride;
   L.p.vs_head = scales->v_head_stride;
-  L.p.k_cache = static_cast<const uint8_t*>(k_cache);
-  L.p.v_cache = static_cast<const uint8_t*>(v_cache);
-  L.p.k_page = p->k_page_stride;
-  L.p.k_slot = p->k_slot_stride;
-  L.p.k_head = p->k_head_stride;
-  L.p.v_page = p->v_page_stride;
-  L.p.v_slot = p->v_slot_stride;
-  L.p.v_head = p->v_head_stride;
+  if ((rc = encode_codes(&L.tmK, k_cache, p, d, p->k_page_stride, p->k_slot_stride, p->k_head_stride, L.p.a.box_rows)))
+    return rc;
+  if ((rc = encode_codes(&L.tmV, v_cache, p, dv, p->v_page_stride, p->v_slot_stride, p->v_head_stride, L.p.a.box_rows)))
+    return rc;
   L.workers = std::min(pl.rows.workers, sms);
   if (debug_max_ctas() > 0) L.workers = std::min(L.workers, debug_max_ctas());
   L.stream = s;

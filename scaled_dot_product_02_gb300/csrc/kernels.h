@@ -340,10 +340,9 @@ struct PagedFp8Params {
   long long q_stride;          // elements between tokens
   const uint8_t *k_scale, *v_scale;
   long long ks_page, ks_slot, ks_head, vs_page, vs_slot, vs_head;
-  const uint8_t *k_cache, *v_cache;
-  long long k_page, k_slot, k_head, v_page, v_slot, v_head;
 };
 struct PagedFp8Launch {
+  CUtensorMap tmK, tmV;        // codes: 128 columns x box_rows slots
   PagedFp8Params p;
   int workers;                 // CTAs
   cudaStream_t stream;

@@ -35,6 +35,7 @@
 #include <cuda_runtime.h>
 
 #include "paged.cuh"
+#include "row_sums.cuh"
 
 namespace sdpa {
 
@@ -82,30 +83,6 @@ template <int N>
 __device__ __forceinline__ uint32_t p_offset(int r, int c) {
   const uint32_t a = r * (2 * N) + c * 16;
   return a ^ ((a >> 3) & (2 * N - 16));
-}
-
-__device__ __forceinline__ float warp_max(float v) {
-  float r;
-  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
-  return r;
-}
-
-// Sum v[n] over the 32 lanes, leaving N/32 sums (or one, twice) a lane: rows
-// N <= 32: lane / (32 / N), N = 64: 2 * lane + i.
-template <int N>
-__device__ __forceinline__ void scatter_sum(float (&v)[N], int lane) {
-  int o = 16;
-#pragma unroll
-  for (int cnt = N; cnt > 1 && o >= 1; cnt /= 2, o /= 2) {
-    const bool up = lane & o;
-#pragma unroll
-    for (int i = 0; i < cnt / 2; ++i) {
-      const float send = up ? v[i] : v[i + cnt / 2];
-      const float keep = up ? v[i + cnt / 2] : v[i];
-      v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
-    }
-  }
-  if (N == 16) v[0] += __shfl_xor_sync(0xffffffffu, v[0], 1);
 }
 
 template <int N>
@@ -691,6 +668,11 @@ int launch_rows_n(const PagedLaunch& L, int n, int* launches) {
 int launch_paged_join(const PagedLaunch& L, int n, int dv, int shares, bool bf16) {
   if (shares < 2) return SDPA_OK;
 #define JOIN(A, B) return bf16 ? launch_join_t<A, B, true>(L, shares) : launch_join_t<A, B, false>(L, shares)
+  if (n == 16 && dv == 128) JOIN(128, 16);
+  if (n == 32 && dv == 128) JOIN(128, 32);
+  if (n == 16 && dv == 256) JOIN(256, 16);
+  if (n == 32 && dv == 256) JOIN(256, 32);
+  if (n == 16 && dv == 512) JOIN(512, 16);
   if (n == 128 && dv == 128) JOIN(128, 128);
   if (n == 256 && dv == 128) JOIN(128, 256);
   if (n == 128 && dv == 256) JOIN(256, 128);
