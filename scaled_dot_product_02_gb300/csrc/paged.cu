@@ -668,11 +668,12 @@ int launch_rows_n(const PagedLaunch& L, int n, int* launches) {
 int launch_paged_join(const PagedLaunch& L, int n, int dv, int shares, bool bf16) {
   if (shares < 2) return SDPA_OK;
 #define JOIN(A, B) return bf16 ? launch_join_t<A, B, true>(L, shares) : launch_join_t<A, B, false>(L, shares)
+  if (n == 8 && dv == 128) JOIN(128, 8);
+  if (n == 8 && dv == 256) JOIN(256, 8);
+  if (n == 8 && dv == 512) JOIN(512, 8);
   if (n == 16 && dv == 128) JOIN(128, 16);
   if (n == 32 && dv == 128) JOIN(128, 32);
   if (n == 16 && dv == 256) JOIN(256, 16);
-  if (n == 32 && dv == 256) JOIN(256, 32);
-  if (n == 16 && dv == 512) JOIN(512, 16);
   if (n == 128 && dv == 128) JOIN(128, 128);
   if (n == 256 && dv == 128) JOIN(128, 256);
   if (n == 128 && dv == 256) JOIN(256, 128);

@@ -5,7 +5,7 @@
 // cache, so it is bound by HBM; codes go to the tensor cores as they are.
 //
 // The split into items, shares and partial results is the rows kernel's
-// (paged.cu): an item is up to N = 16 or 32 query rows that share a kv head,
+// (paged.cu): an item is up to N = 8, 16 or 32 query rows that share a kv head,
 // against 128 keys at a time, keys on the M side:
 //   S^T = K Q^T   (A: 128 keys x D codes),   O^T += V^T P^T   (A: 128 value columns x 128 keys).
 // An 8-bit MMA wants both operands in 8 bits, and Q and P have more. Each is
@@ -13,9 +13,13 @@
 // rounded to nearest: three significant bits and a sign each, 2^-11 of the
 // value left over and the range of fp16 (E5M2 is fp16's upper byte). For Q,
 // scaled by a power of two a row, the sum is exact: 11 bits at most are there.
-// The terms lie side by side on the N side -- 3 N rows of Q, 4 N columns of
-// P with the last N unused -- so a tile of codes is read once for all three,
-// and the threads that read the products from tensor memory add them up.
+// The terms lie side by side on the N side, so a tile of codes is read once for
+// all three, and the threads that read the products from tensor memory add them
+// up: every 4 rows take 16 columns, their first terms, second, third, and 4 of
+// no use. So 4 rows are one 16-column load and one 16-byte store, and the code
+// for rows that an item does not have is passed over (a decoding step of a GQA
+// group of 4 has 4 of them; fetching straight-line code for more, at the start
+// of a kernel, costs more than running it).
 // (Converting the codes to 16 bits in shared memory instead moves 96 KB more
 // per 32 KB of codes through it, as much as it passes in the time HBM takes to
 // deliver them.)
@@ -27,12 +31,15 @@
 // of a row is at least 2^11 and what E5M2's last step (2^-16) cannot hold is below
 // 2^-28 of it.
 //
-// Roles (384 threads): warps 0-3 softmax and output, one thread per key of a
-// tile (and per value column of the output); 4-6 TMA producers; 7 TMEM allocator
-// and MMA issuer; 8 takes the items' rows of Q apart, an item ahead; 9-11 fetch
-// the scale bytes, in turn a tile each, up to SST tiles ahead (table entry, then
-// byte: two trips to memory). K and V tiles go through a ring of 16 KB stages
-// (128 keys x 128 codes).
+// Roles (512 threads): warps 0-3 and 4-7 softmax, a tile each in turn, one thread
+// per key (and per value column of the output). Each of the two warpgroups has its
+// own S^T, P, maximum, sums and O^T, which meet at an item's end: a tile's way
+// through barriers, tensor memory and exponentials takes longer than its codes
+// from HBM. Warps 8-11 TMA producers (a warp issues its lanes' copies one after
+// another, some 100 cycles each, and pages of 16 make 8 of a stage); 12 TMEM
+// allocator and MMA issuer; 13-15 take an item's rows of Q apart and then fetch its
+// scale bytes, a tile each in turn, up to SST tiles ahead. K and V tiles go through
+// a ring of 16 KB stages (128 keys x 128 codes).
 #include <algorithm>
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -48,34 +55,38 @@ namespace {
 constexpr int kCodes = 16384;      // bytes of a ring stage
 constexpr float kLift = 11.f;      // log2 of what P is multiplied by
 constexpr float kSlack = 4.f;      // how far (log2) a weight may pass the maximum in use
+constexpr float kNone = -1e30f;    // in place of a maximum: no key yet (finite, so that nothing becomes inf - inf)
 constexpr int kScaleLo = 47, kScaleHi = 207;  // the scale bytes that rows are given
 
 template <int DQK, int DV, int N>
 struct Fp8Cfg {
-  static constexpr int THREADS = 384;
-  static constexpr int PRODUCERS = 3, LOADERS = 3;
+  static constexpr int THREADS = 512;
+  static constexpr int PRODUCERS = 4, AUX = 3;
+  static constexpr int W_MMA = 8 + PRODUCERS, W_AUX = W_MMA + 1;  // behind the softmax warps and the producers
+  static constexpr int LOADS = N == 32 ? 1 : 2;  // 16-column loads in flight (two spill at N = 32)
   static constexpr int KST = (DQK + 127) / 128;  // K stages of a tile
   static constexpr int VST = DV / 128;           // V stages of a tile
   static __device__ __forceinline__ constexpr int k_steps(int kb) { return DQK / 32 - 4 * kb >= 4 ? 4 : DQK / 32 - 4 * kb; }
-  static constexpr int NS = 3 * N;               // columns of S^T: Q's terms
-  static constexpr int NO = 4 * N;               // columns of O^T: P's terms, and a fourth of no use
+  static constexpr int QUADS = N / 4;
+  static constexpr int NT = 4 * N;               // columns of S^T and of 128 value columns' O^T: the rows' terms
   static constexpr int NQ = 2;                   // buffers of Q's terms
-  static constexpr int Q_ATOM = NS * 128;        // bytes of 128 columns of Q's terms
+  static constexpr int Q_ATOM = NT * 128;        // bytes of 128 columns of Q's terms
   static constexpr int Q_BYTES = KST * Q_ATOM;
-  static constexpr int P_BYTES = kTile * NO;
+  static constexpr int P_BYTES = kTile * NT;
   static constexpr int SST = 8;                  // tiles of scales
   static constexpr int SCALE_BYTES = SST * kTile * 8;
-  static constexpr int MISC = 1536 + (7 + NQ) * N * 4;
+  static constexpr int MISC = 1536 + (14 + NQ) * N * 4;
   static constexpr int NST_FIT = (kSmemMax - 1024 - NQ * Q_BYTES - 2 * P_BYTES - SCALE_BYTES - MISC) / kCodes;
   static constexpr int NST = NST_FIT > 12 ? 12 : NST_FIT;
   static constexpr int SMEM = 1024 + NQ * Q_BYTES + 2 * P_BYTES + NST * kCodes + SCALE_BYTES + MISC;
-  static constexpr int TM_S = VST * NO;          // TMEM columns: O^T, then two S^T buffers
-  static constexpr int TM_NEED = TM_S + 2 * NS;
-  static constexpr int TM_COLS = TM_NEED <= 256 ? 256 : 512;
+  static constexpr int TM_O = VST * NT;          // TMEM columns: each warpgroup's O^T, then its S^T
+  static constexpr int TM_S = 2 * TM_O;
+  static constexpr int TM_NEED = TM_S + 2 * NT;
+  static constexpr int TM_COLS = TM_NEED <= 128 ? 128 : TM_NEED <= 256 ? 256 : 512;
   static_assert(SMEM <= kSmemMax && TM_NEED <= 512, "the tile plan fits one SM");
   // the softmax waits for a whole tile of V (to clear unseen keys) before P V takes its first stage
   static_assert(NST >= VST && NST >= KST, "the ring holds a tile of V");
-  static_assert(N == 16 || N == 32, "one swizzle span of 4 N bytes");
+  static_assert(N == 8 || N == 16 || N == 32, "one swizzle span of 4 N bytes");
   static_assert((2 * NST + 2 * NQ + 8 + 2 * SST) * 8 + sizeof(PagedScan) + 16 <= 1536, "barriers and the scan");
 };
 
@@ -93,7 +104,7 @@ __device__ __forceinline__ uint64_t p_desc(uint32_t saddr) {
   d |= (uint64_t)((kTile * 4 * N) >> 4) << 16;
   d |= (uint64_t)((32 * N) >> 4) << 32;
   d |= (uint64_t)1 << 46;
-  d |= (uint64_t)(N == 32 ? 2 : 4) << 61;
+  d |= (uint64_t)(N == 32 ? 2 : N == 16 ? 4 : 6) << 61;
   return d;
 }
 // Byte offset of 16-byte chunk c of key r in P.
@@ -133,50 +144,28 @@ __device__ __forceinline__ void split4(float x0, float x1, float x2, float x3, u
   }
 }
 
-// S^T of a tile: this thread's key against the item's rows, Q's terms added up.
-template <int N>
-__device__ __forceinline__ void scores(uint32_t taddr, float (&s)[N]) {
-  if constexpr (N == 16) {
-    uint32_t a[16], b[16], c[16];
-    tmem_ld16(taddr, a);
-    tmem_ld16(taddr + 16, b);
-    tmem_ld16(taddr + 32, c);
-    tmem_wait_ld();
+// The sum of a value's three terms, of 16 columns of 4 rows.
+__device__ __forceinline__ float terms_sum(const uint32_t (&u)[16], int r) {
+  return (__uint_as_float(u[8 + r]) + __uint_as_float(u[4 + r])) + __uint_as_float(u[r]);
+}
+__device__ __forceinline__ void fence16(uint32_t (&u)[16]) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      asm volatile("" : "+r"(a[i]), "+r"(b[i]), "+r"(c[i]));
-      s[i] = (__uint_as_float(c[i]) + __uint_as_float(b[i])) + __uint_as_float(a[i]);
-    }
-  } else {
-    uint32_t a[32], b[32];
-    tmem_ld32(taddr + 64, a);
-    tmem_ld32(taddr + 32, b);
-    tmem_wait_ld();
-    reg_fence(a);
-    reg_fence(b);
-#pragma unroll
-    for (int i = 0; i < 32; ++i) s[i] = __uint_as_float(a[i]) + __uint_as_float(b[i]);
-    tmem_ld32(taddr, a);
-    tmem_wait_ld();
-    reg_fence(a);
-#pragma unroll
-    for (int i = 0; i < 32; ++i) s[i] += __uint_as_float(a[i]);
-  }
+  for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(u[i]));
 }
 
-// One item's rows of Q as their terms in shared memory ([128 columns][term][row], K-major, 128-byte swizzle), and what
-// undoes the power of two that a row was multiplied by. A warp calls it. Rows that the item does not have are zeros.
-template <int DQK, int N, bool BF16>
+// One item's rows of Q as their terms in shared memory (K-major, 128-byte swizzle), and what undoes the power of two that
+// a row was multiplied by: the share of warp `part` of PARTS. Rows past the item's stay as they are: nothing of theirs is
+// looked at.
+template <int DQK, int N, bool BF16, int PARTS>
 __device__ __forceinline__ void split_q(const PagedFp8Params& f, const PagedWalk& w, const PagedUnit& un, uint8_t* sQ,
-                                        float* s_fq, int lane) {
+                                        float* s_fq, int part, int lane) {
   using E = Elem<BF16>;
   constexpr int VECS = DQK / 8, LPR = VECS >= 32 ? 32 : VECS == 24 ? 32 : VECS, RP = 32 / LPR, VPL = (VECS + 31) / 32;
-  constexpr int U = 4;  // passes whose loads are in flight together
-  static_assert(N % (RP * U) == 0, "whole passes");
+  constexpr int U = VPL == 1 ? 4 : 2;  // rows of a lane whose loads are in flight together
   const PagedParams& p = f.a;
-  const int tok = w.i1(p) - w.i0 + 1, sub = lane % LPR;
+  const int rows = (w.i1(p) - w.i0 + 1) * p.block_heads, sub = lane % LPR;
 #pragma unroll 1
-  for (int r0 = lane / LPR; r0 < N; r0 += RP * U) {
+  for (int r0 = part * RP * U + lane / LPR; r0 - lane / LPR < rows; r0 += PARTS * RP * U) {
     uint4 x[U][VPL];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -187,7 +176,7 @@ __device__ __forceinline__ void split_q(const PagedFp8Params& f, const PagedWalk
       for (int v = 0; v < VPL; ++v) {
         const int vec = v * 32 + sub;
         x[u][v] = make_uint4(0u, 0u, 0u, 0u);
-        if (ti < tok && h < un.heads && vec < VECS && SDPA_ADDR_OK(p.chk, row + vec * 16, 16))
+        if (r < rows && h < un.heads && vec < VECS && SDPA_ADDR_OK(p.chk, row + vec * 16, 16))
           x[u][v] = __ldg(reinterpret_cast<const uint4*>(row + vec * 16));
       }
     }
@@ -210,6 +199,7 @@ __device__ __forceinline__ void split_q(const PagedFp8Params& f, const PagedWalk
       // the row's largest magnitude to 2^14 .. 2^15
       const int up = top > 0.f ? min(14 + 127 - (__float_as_int(top) >> 23), 126) : 0;
       const float by = exp2_int(up);
+      if (r >= rows) continue;
       if (sub == 0) s_fq[r] = exp2_int(-up);
       auto term_of = [&](float a) { return fabsf(a) == INFINITY ? NAN : a * by; };  // the terms have no infinity
 #pragma unroll
@@ -219,16 +209,19 @@ __device__ __forceinline__ void split_q(const PagedFp8Params& f, const PagedWalk
         split4(term_of(y[v][0].x), term_of(y[v][0].y), term_of(y[v][1].x), term_of(y[v][1].y), lo);
         split4(term_of(y[v][2].x), term_of(y[v][2].y), term_of(y[v][3].x), term_of(y[v][3].y), hi);
         if (vec >= VECS) continue;
-        uint8_t* to = sQ + (vec / 16) * (3 * N * 128) + r * 128 + ((((vec % 16) / 2) ^ (r & 7)) << 4) + (vec & 1) * 8;
+        uint8_t* to = sQ + (vec / 16) * (4 * N * 128) + (vec & 1) * 8;
 #pragma unroll
-        for (int k = 0; k < 3; ++k) *reinterpret_cast<uint2*>(to + k * N * 128) = make_uint2(lo[k], hi[k]);
+        for (int k = 0; k < 3; ++k) {
+          const int at = (r / 4) * 16 + k * 4 + r % 4;
+          *reinterpret_cast<uint2*>(to + at * 128 + ((((vec % 16) / 2) ^ (at & 7)) << 4)) = make_uint2(lo[k], hi[k]);
+        }
       }
     }
   }
 }
 
 template <int DQK, int DV, int N, bool BF16>
-__global__ void __launch_bounds__(384, 1)
+__global__ void __launch_bounds__(512, 1)
     paged_fp8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                      const __grid_constant__ PagedFp8Params f) {
   using C = Fp8Cfg<DQK, DV, N>;
@@ -255,23 +248,23 @@ __global__ void __launch_bounds__(384, 1)
   PagedScan* scan = reinterpret_cast<PagedScan*>(bar_drain + 1);
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(scan + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
-  float* s_m = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(full) + 1536);  // [N] running maxima (log2 units)
-  float* s_f = s_m + N;        // [N] factors of a rescale
-  float* s_w = s_f + N;        // [4][N] warps' maxima, then their sums
-  float* s_l = s_w + 4 * N;    // [N] sums of an item
-  float* s_fq = s_l + N;       // [NQ][N] what undoes the rows' scaling
+  float* s_m = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(full) + 1536);  // [N] running maxima (log2 units) less kLift
+  float* s_f = s_m + 2 * N;    // [N] factors of a rescale
+  float* s_w = s_f + 2 * N;    // [4][N] warps' maxima, then their sums
+  float* s_l = s_w + 8 * N;    // [N] factors of an item's output (these four for each softmax warpgroup)
+  float* s_fq = s_l + 2 * N;   // [NQ][N] what undoes the rows' scaling
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  if (threadIdx.x == 128) {  // not one of the threads that read a small batch
+  if (threadIdx.x == 256) {  // not one of the threads that read a small batch
     for (int i = 0; i < C::NST; ++i) {
       mbar_init(&full[i], C::PRODUCERS);  // every producer, so that none falls a phase behind
       mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < C::NQ; ++i) {
-      mbar_init(&bar_q[i], 32);
-      mbar_init(&q_free[i], 1 + 128);
+      mbar_init(&bar_q[i], 32 * C::AUX);
+      mbar_init(&q_free[i], 1 + 256);
     }
     for (int i = 0; i < C::SST; ++i) {
       mbar_init(&sc_full[i], 32);
@@ -282,12 +275,12 @@ __global__ void __launch_bounds__(384, 1)
       mbar_init(&bar_p[i], 128);
       mbar_init(&bar_o[i], 1);
     }
-    mbar_init(o_free, 128);
+    mbar_init(o_free, 256);
     mbar_init(bar_drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 7) {
+  if (warp == C::W_MMA) {
     tmem_alloc(tmem_holder, C::TM_COLS);
     tmem_relinquish();
   }
@@ -308,20 +301,61 @@ __global__ void __launch_bounds__(384, 1)
       PagedCut* cut = p.cuts + me;
       if (SDPA_ADDR_OK(p.chk, cut, sizeof(PagedCut))) *cut = w.cut(p);
     }
-    if (warp >= 4 && warp < 7) {
+    if (warp >= 8 && warp < C::W_MMA) {
       // ---------------------------------------------------------- producers
-      const int pw = warp - 4, box = lane * C::PRODUCERS + pw;  // this lane's box of a tile
+      const int pw = warp - 8, box = lane * C::PRODUCERS + pw;  // this lane's box of a tile
       if (lane == 0 && pw == 0) {
         prefetch_tmap(&tmK);
         prefetch_tmap(&tmV);
       }
       const uint32_t box_bytes = p.box_rows * 128;
+      const int shift = __ffs(p.box_rows) - 1;  // a power of two
+      const int step_col = kTile / p.page_size, step_slot = kTile - step_col * p.page_size;  // from a tile to the next
       int c = 0;
       bool ok = true;
       do {
         if (w.span.tiles == 0) continue;
         const PagedUnit un = paged_unit(p, w.unit);
-        auto box_of = [&](int j) { return paged_box(p, w.span, w.b, (w.span.tile0 + j) * kTile, box); };
+        // The page numbers come 32 at a time, one a lane, the next 32 behind them: a load for every tile made every tile
+        // wait for it.
+        const int first = (w.span.tile0 + w.j0) * kTile, last_col = (w.span.hi - 1) / p.page_size;
+        int tile_col = first / p.page_size, tile_slot = first - tile_col * p.page_size;  // where the tile starts
+        int col = (first + box * p.box_rows) / p.page_size;                              // where this lane's box does
+        int slot_in = first + box * p.box_rows - col * p.page_size;
+        const int32_t* row = p.block_table + w.b * p.table_stride;
+        auto entry = [&](int x) {
+          return x >= w.span.lo / p.page_size && x <= last_col && SDPA_ADDR_OK(p.chk, row + x, 4) ? __ldg(row + x) : -1;
+        };
+        int base = tile_col, ids = entry(base + lane), ids_next = entry(base + 32 + lane);
+        auto box_here = [&](int j) {
+          const int key0 = (w.span.tile0 + j) * kTile, key = key0 + box * p.box_rows;
+          if (tile_col - base >= 32) {
+            base += 32;
+            ids = ids_next;
+            ids_next = entry(base + 32 + lane);
+          }
+          const int at = col - base;  // below 64: a tile starts within the first 32 and lies on at most 9 pages
+          const int a = __shfl_sync(0xffffffffu, ids, at & 31), b = __shfl_sync(0xffffffffu, ids_next, at & 31);
+          PagedBox x;
+          x.mine = box < kTile >> shift && key < w.span.hi && key + p.box_rows > w.span.lo;
+          x.page = at < 32 ? a : b;
+          x.slot = slot_in;
+          if (x.mine && (unsigned)x.page >= (unsigned)p.num_pages) {
+            x.page = p.num_pages;  // outside the map: reads as zeros
+            record_error(p.err, SDPA_ERR_BAD_INDEX);
+          }
+          auto advance = [&](int& at_col, int& at_slot) {
+            at_col += step_col;
+            at_slot += step_slot;
+            if (at_slot >= p.page_size) {
+              at_slot -= p.page_size;
+              ++at_col;
+            }
+          };
+          advance(tile_col, tile_slot);
+          advance(col, slot_in);
+          return x;
+        };
         auto fetch = [&](const CUtensorMap* m, const PagedBox& x, int boxes, int col) -> bool {
           const int slot = c % C::NST;
           if (!__all_sync(0xffffffffu, mbar_wait(&empty[slot], ((c / C::NST) & 1) ^ 1, abort_flag))) return false;
@@ -340,21 +374,22 @@ __global__ void __launch_bounds__(384, 1)
           ++c;
           return true;
         };
-        auto boxes_of = [&](int j) { return paged_boxes(p, w.span, (w.span.tile0 + j) * kTile, 0, kTile); };
-        PagedBox cur = box_of(w.j0), prev = cur;
+        auto boxes_of = [&](int j) {
+          const int key0 = (w.span.tile0 + j) * kTile, lo = max(w.span.lo - key0, 0), hi = min(w.span.hi - key0, kTile);
+          return ((hi + p.box_rows - 1) >> shift) - (lo >> shift);
+        };
+        PagedBox prev;
+        int before = 0;
         for (int j = w.j0; j < w.j1 && ok; ++j) {
-          const PagedBox ahead = j + 1 < w.j1 ? box_of(j + 1) : cur;  // its table entry arrives while this tile's copies go out
+          const PagedBox cur = box_here(j);
           const int boxes = boxes_of(j);
           for (int kb = 0; kb < C::KST && ok; ++kb) ok = fetch(&tmK, cur, boxes, kb * 128);
-          if (j > w.j0) {
-            const int before = boxes_of(j - 1);
+          if (j > w.j0)
             for (int vb = 0; vb < C::VST && ok; ++vb) ok = fetch(&tmV, prev, before, vb * 128);
-          }
           prev = cur;
-          cur = ahead;
+          before = boxes;
         }
-        const int last = boxes_of(w.j1 - 1);
-        for (int vb = 0; vb < C::VST && ok; ++vb) ok = fetch(&tmV, prev, last, vb * 128);
+        for (int vb = 0; vb < C::VST && ok; ++vb) ok = fetch(&tmV, prev, before, vb * 128);
       } while (ok && w.next(p));
       if (lane == 0) {
         if (!ok) {
@@ -364,38 +399,22 @@ __global__ void __launch_bounds__(384, 1)
         // every copy lands before the CTA ends
         for (int k = max(0, c - C::NST); k < c; ++k) mbar_wait_drain(&full[k % C::NST], (k / C::NST) & 1);
       }
-    } else if (warp == 8) {
-      // ---------------------------------------------------------- Q's terms
-      int nq = 0;
+    } else if (warp >= C::W_AUX) {
+      // ---------------------------------------------------------- Q's terms, and scales
+      const int aux = warp - C::W_AUX;
+      int nq = 0, gs = 0;  // items with keys, tiles of earlier items
       bool ok = true;
       do {
         if (w.span.tiles == 0) continue;
-        const int qb = nq % C::NQ;
-        if (nq >= C::NQ && !__all_sync(0xffffffffu, mbar_wait(&q_free[qb], (nq / C::NQ - 1) & 1, abort_flag))) {
-          ok = false;
-          break;
-        }
-        split_q<DQK, N, BF16>(f, w, paged_unit(p, w.unit), sQ + qb * C::Q_BYTES, s_fq + qb * N, lane);
-        fence_proxy_async_smem();
-        mbar_arrive(&bar_q[qb]);
-        ++nq;
-      } while (ok && w.next(p));
-      if (!ok && lane == 0) {
-        *abort_flag = 1;
-        record_error(p.err, SDPA_ERR_TIMEOUT);
-      }
-    } else if (warp > 8) {
-      // ---------------------------------------------------------- scales
-      int g = 0;  // tiles so far
-      bool ok = true;
-      do {
         const PagedUnit un = paged_unit(p, w.unit);
-        for (int j = w.j0; j < w.j1 && ok; ++j, ++g) {
-          if (g % C::LOADERS != warp - 9) continue;
-          // four keys a lane, which lie in one page
-          const int key = (w.span.tile0 + j) * kTile + 4 * lane;
-          int ek[4] = {127, 127, 127, 127}, ev[4] = {127, 127, 127, 127};
-          if (key < w.span.hi && key + 4 > w.span.lo) {
+        const int n = w.j1 - w.j0;
+        // four keys a lane, which lie in one page; not looked at before they are stored, a tile later
+        int ek[4], ev[4];
+        auto load = [&](int j) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) ek[e] = ev[e] = 127;
+          const int key = (w.span.tile0 + w.j0 + j) * kTile + 4 * lane;
+          if (j < n && key < w.span.hi && key + 4 > w.span.lo) {
             const int col = key / p.page_size, slot = key - col * p.page_size;
             const int32_t* at = p.block_table + w.b * p.table_stride + col;
             const int id = SDPA_ADDR_OK(p.chk, at, 4) ? __ldg(at) : -1;
@@ -410,8 +429,21 @@ __global__ void __launch_bounds__(384, 1)
               }
             }
           }
-          const int slot = g % C::SST;
-          if (!__all_sync(0xffffffffu, mbar_wait(&sc_free[slot], ((g / C::SST) & 1) ^ 1, abort_flag))) {
+        };
+        int j = (aux + C::AUX - gs % C::AUX) % C::AUX;  // tiles in turn, whatever item they belong to
+        load(j);
+        const int qb = nq % C::NQ;
+        if (nq >= C::NQ && !__all_sync(0xffffffffu, mbar_wait(&q_free[qb], (nq / C::NQ - 1) & 1, abort_flag))) {
+          ok = false;
+          break;
+        }
+        split_q<DQK, N, BF16, C::AUX>(f, w, un, sQ + qb * C::Q_BYTES, s_fq + qb * N, aux, lane);
+        fence_proxy_async_smem();
+        mbar_arrive(&bar_q[qb]);
+        ++nq;
+        for (; j < n; j += C::AUX) {
+          const int slot = (gs + j) % C::SST;
+          if (!__all_sync(0xffffffffu, mbar_wait(&sc_free[slot], (((gs + j) / C::SST) & 1) ^ 1, abort_flag))) {
             ok = false;
             break;
           }
@@ -420,17 +452,19 @@ __global__ void __launch_bounds__(384, 1)
             sScale[slot * kTile + 4 * lane + e] = make_float2(exp2_byte(min(max(ek[e], kScaleLo), kScaleHi)),
                                                               (float)(min(max(ev[e], kScaleLo), kScaleHi) - 127));
           mbar_arrive(&sc_full[slot]);
+          load(j + C::AUX);
         }
+        gs += n;
       } while (ok && w.next(p));
       if (!ok && lane == 0) {
         *abort_flag = 1;
         record_error(p.err, SDPA_ERR_TIMEOUT);
       }
-    } else if (warp == 7) {
+    } else if (warp == C::W_MMA) {
       // ---------------------------------------------------------- MMA issuer
       if (elect_one()) {
-        constexpr uint32_t ID_S = idesc_f8(C::NS, false, false);
-        constexpr uint32_t ID_O = idesc_f8(C::NO, true, true);
+        constexpr uint32_t ID_S = idesc_f8(C::NT, false, false);
+        constexpr uint32_t ID_O = idesc_f8(C::NT, true, true);
         int c = 0, nq = 0, gs = 0;  // ring stages, items with keys, tiles of earlier items
         bool ok = true;
         do {
@@ -446,7 +480,7 @@ __global__ void __launch_bounds__(384, 1)
           tc_fence_after();
           auto mma_s = [&](int j) -> bool {
             const int sj = gs + j;
-            const uint32_t d = tmem + C::TM_S + (sj & 1) * C::NS;
+            const uint32_t d = tmem + C::TM_S + (sj & 1) * C::NT;
             for (int kb = 0; kb < C::KST; ++kb, ++c) {
               const int slot = c % C::NST;
               if (!mbar_wait(&full[slot], (c / C::NST) & 1, abort_flag)) return false;
@@ -478,8 +512,8 @@ __global__ void __launch_bounds__(384, 1)
               const uint32_t v_base = smem_u32(sStage + slot * kCodes);
 #pragma unroll
               for (int ks = 0; ks < 4; ++ks)  // 32 keys each
-                mma_f8_ss(tmem + vb * C::NO, smem_desc_sw128(v_base + ks * 4096, kCodes, 1024),
-                          p_desc<N>(p_base + ks * (128 * N)), ID_O, (j | ks) != 0);
+                mma_f8_ss(tmem + (sj & 1) * C::TM_O + vb * C::NT, smem_desc_sw128(v_base + ks * 4096, kCodes, 1024),
+                          p_desc<N>(p_base + ks * (128 * N)), ID_O, j >= 2 || ks > 0);
               mma_commit(&empty[slot]);
             }
             mma_commit(&bar_o[sj & 1]);
@@ -501,8 +535,12 @@ __global__ void __launch_bounds__(384, 1)
       }
     } else {
       // ---------------------------------------------------------- softmax and output
-      const int tid = threadIdx.x;  // key of a tile, and value column
-      const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
+      const int me_g = warp / 4, tid = threadIdx.x % 128;  // warpgroup; key of a tile, and value column
+      const uint32_t lanes = tmem + ((uint32_t)((warp % 4) * 32) << 16);
+      const uint32_t my_o = lanes + me_g * C::TM_O, my_s = lanes + C::TM_S + me_g * C::NT;
+      const int bar_id = 1 + me_g;  // named barriers: a warpgroup's, and 3 for both
+      float *const m_g = s_m + me_g * N, *const f_g = s_f + me_g * N, *const w_g = s_w + me_g * 4 * N;
+      uint8_t* const pb = sP + me_g * C::P_BYTES;
       const float sl2 = p.scale_log2;
       int gs = 0, c0 = 0, nq = 0;  // tiles and ring stages of earlier items, items with keys
       bool ok = true;
@@ -510,24 +548,18 @@ __global__ void __launch_bounds__(384, 1)
         const int n = w.j1 - w.j0;
         const bool keys = w.span.tiles > 0;
         const PagedUnit un = paged_unit(p, w.unit);
-        const int tok = w.i1(p) - w.i0 + 1, rows = tok * p.block_heads;
+        const int tok = w.i1(p) - w.i0 + 1, rows = tok * p.block_heads, quads = (rows + 3) / 4;
         const int off = w.s.kv_len - w.s.q_len;
         const float* fq = s_fq + (nq % C::NQ) * N;
-        if (tid < N) s_m[tid] = -INFINITY;
-        named_bar_sync(1, 128);
+        if (tid < N) m_g[tid] = kNone;
+        named_bar_sync(bar_id, 128);
         if (keys && !__all_sync(0xffffffffu, mbar_wait(&bar_q[nq % C::NQ], (nq / C::NQ) & 1, abort_flag))) ok = false;
         float l[N];
 #pragma unroll
         for (int i = 0; i < N; ++i) l[i] = 0.f;
-        for (int j = 0; keys && j < n; ++j) {
+        const int j_first = (gs ^ me_g) & 1;  // tiles in turn, whatever item they belong to
+        for (int j = j_first; keys && j < n; j += 2) {
           const int sj = gs + j, slot = sj % C::SST;
-          if (!__all_sync(0xffffffffu, mbar_wait(&sc_full[slot], (sj / C::SST) & 1, abort_flag))) ok = false;
-          const float2 sc = sScale[slot * kTile + tid];
-          mbar_arrive(&sc_free[slot]);
-          if (!__all_sync(0xffffffffu, mbar_wait(&bar_s[sj & 1], (sj >> 1) & 1, abort_flag))) ok = false;
-          tc_fence_after();
-          float s[N];
-          scores<N>(lanes + C::TM_S + (sj & 1) * C::NS, s);
           // the rows that see this thread's key: [r_lo, r_hi). Row r is head r % block_heads of token r / block_heads
           const int kb = (w.span.tile0 + w.j0 + j) * kTile, key = kb + tid;
           int t_lo = 0, t_hi = key < w.span.hi ? tok : 0;
@@ -537,87 +569,99 @@ __global__ void __launch_bounds__(384, 1)
           }
           const int r_lo = t_lo * p.block_heads, r_hi = t_hi * p.block_heads;
           const unsigned span = max(0, r_hi - r_lo);
+          // S^T of this tile; with it P V of two tiles ago is done, and its P may be replaced (they were issued in that order)
+          if (!__all_sync(0xffffffffu, mbar_wait_both(&sc_full[slot], (sj / C::SST) & 1, &bar_s[me_g], (sj >> 1) & 1, abort_flag)))
+            ok = false;
+          tc_fence_after();
+          const float2 sc = sScale[slot * kTile + tid];
           const float sk = sl2 * sc.x;
+          float s[N], top = -INFINITY;
 #pragma unroll
-          for (int i = 0; i < N; ++i) s[i] = (unsigned)(i - r_lo) < span ? fmaf(s[i] * fq[i], sk, sc.y) : -INFINITY;
-          float top = -INFINITY;
-          float t[N];
+          for (int c = 0; c < C::QUADS; c += C::LOADS) {
+            if (c >= quads) break;
+            uint32_t u[C::LOADS][16];
 #pragma unroll
-          for (int i = 0; i < N; ++i) {
-            t[i] = s[i] - s_m[i];  // +inf where a row has no maximum yet
-            t[i] = s[i] == -INFINITY ? -INFINITY : t[i];
-            top = fmaxf(top, t[i]);
+            for (int x = 0; x < C::LOADS; ++x)
+              if (c + x < quads) tmem_ld16(my_s + (c + x) * 16, u[x]);
+            tmem_wait_ld();
+#pragma unroll
+            for (int x = 0; x < C::LOADS; ++x) fence16(u[x]);
+#pragma unroll
+            for (int x = 0; x < C::LOADS; ++x) {
+              if (c + x >= quads) break;
+              const float4 f4 = *reinterpret_cast<const float4*>(fq + (c + x) * 4);
+              const float4 m4 = *reinterpret_cast<const float4*>(m_g + (c + x) * 4);
+              const float fr[4] = {f4.x, f4.y, f4.z, f4.w}, mr[4] = {m4.x, m4.y, m4.z, m4.w};
+#pragma unroll
+              for (int r = 0; r < 4; ++r) {
+                const int i = (c + x) * 4 + r;
+                s[i] = (unsigned)(i - r_lo) < span ? fmaf(terms_sum(u[x], r) * fr[r], sk, sc.y) : -INFINITY;
+                top = fmaxf(top, s[i] - mr[r]);
+              }
+            }
           }
+          mbar_arrive(&sc_free[slot]);
           // only a row that jumps past the maximum in use (or sees its first key) has it moved and O^T and the sums rescaled
-          if (!named_bar_and(1, 128, ok && !(top > kSlack))) {
-            if (!named_bar_and(1, 128, ok)) {
+          if (!named_bar_and(bar_id, 128, ok && !(top > kLift + kSlack))) {
+            if (!named_bar_and(bar_id, 128, ok)) {
               ok = false;
               break;
             }
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-              const float m = warp_max(s[i]);
-              if (lane == 0) s_w[warp * N + i] = m;
-            }
-            named_bar_sync(1, 128);
-            if (tid < N) {
-              const float m = fmaxf(fmaxf(s_w[tid], s_w[N + tid]), fmaxf(s_w[2 * N + tid], s_w[3 * N + tid]));
-              const float old = s_m[tid];
-              const bool move = m > old + kSlack || (old == -INFINITY && m > -INFINITY);
-              s_f[tid] = !move ? 1.f : old == -INFINITY ? 0.f : ex2(old - m);
-              if (move) s_m[tid] = m;
-            }
-            named_bar_sync(1, 128);
+            for (int c = 0; c < C::QUADS; ++c) {
+              if (c >= quads) break;
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-              l[i] *= s_f[i];
-              t[i] = s[i] == -INFINITY ? -INFINITY : s[i] - s_m[i];
+              for (int r = 0; r < 4; ++r) {
+                const float m = warp_max(s[c * 4 + r]);
+                if (lane == 0) w_g[(warp % 4) * N + c * 4 + r] = m;
+              }
             }
-            if (j > 0) {
-              if (!__all_sync(0xffffffffu, mbar_wait(&bar_o[(sj - 1) & 1], ((sj - 1) >> 1) & 1, abort_flag))) ok = false;
-              tc_fence_after();
+            named_bar_sync(bar_id, 128);
+            if (tid < quads * 4) {
+              const float m = fmaxf(fmaxf(w_g[tid], w_g[N + tid]), fmaxf(w_g[2 * N + tid], w_g[3 * N + tid])) - kLift;
+              const float old = m_g[tid];
+              const bool move = m > old + kSlack;
+              f_g[tid] = move ? ex2(old - m) : 1.f;
+              if (move) m_g[tid] = m;
+            }
+            named_bar_sync(bar_id, 128);
+#pragma unroll
+            for (int c = 0; c < C::QUADS; ++c) {
+              if (c >= quads) break;
+#pragma unroll
+              for (int r = 0; r < 4; ++r) l[c * 4 + r] *= f_g[c * 4 + r];
+            }
+            if (j >= 2) {  // this warpgroup's last P V is done: see above
 #pragma unroll 1
               for (int vb = 0; vb < C::VST; ++vb)
 #pragma unroll 1
-                for (int x = 0; x < C::NS / 16; ++x) {
+                for (int c = 0; c < quads; ++c) {
                   uint32_t u[16];
-                  tmem_ld16(lanes + vb * C::NO + x * 16, u);
+                  tmem_ld16(my_o + vb * C::NT + c * 16, u);
                   tmem_wait_ld();
+                  fence16(u);
 #pragma unroll
-                  for (int i = 0; i < 16; ++i) {
-                    asm volatile("" : "+r"(u[i]));
-                    u[i] = __float_as_uint(__uint_as_float(u[i]) * s_f[(x * 16 + i) % N]);
-                  }
-                  tmem_st16(lanes + vb * C::NO + x * 16, u);
+                  for (int i = 0; i < 12; ++i) u[i] = __float_as_uint(__uint_as_float(u[i]) * f_g[c * 4 + i % 4]);
+                  tmem_st16(my_o + vb * C::NT + c * 16, u);
                 }
               tmem_wait_st();
             }
           }
-          // P of two tiles ago has been read
-          if (sj >= 2 && !__all_sync(0xffffffffu, mbar_wait(&bar_o[sj & 1], ((sj - 2) >> 1) & 1, abort_flag))) ok = false;
-          uint8_t* pb = sP + (sj & 1) * C::P_BYTES;
           const float un_v = ex2(-sc.y);
 #pragma unroll
-          for (int ch = 0; ch < N / 16; ++ch) {
-            uint32_t u[3][4];
+          for (int c = 0; c < C::QUADS; ++c) {
+            if (c >= quads) break;
+            const float4 m4 = *reinterpret_cast<const float4*>(m_g + c * 4);
+            const float mr[4] = {m4.x, m4.y, m4.z, m4.w};
+            float x[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              float x[4];
-#pragma unroll
-              for (int y = 0; y < 4; ++y) {
-                const int i = ch * 16 + e * 4 + y;
-                x[y] = ex2(t[i] + kLift);
-                l[i] = fmaf(x[y], un_v, l[i]);
-              }
-              uint32_t term[3];
-              split4(x[0], x[1], x[2], x[3], term);
-              u[0][e] = term[0];
-              u[1][e] = term[1];
-              u[2][e] = term[2];
+            for (int r = 0; r < 4; ++r) {
+              x[r] = ex2(s[c * 4 + r] - mr[r]);
+              l[c * 4 + r] = fmaf(x[r], un_v, l[c * 4 + r]);
             }
-#pragma unroll
-            for (int k = 0; k < 3; ++k)
-              *reinterpret_cast<uint4*>(pb + p_offset<N>(tid, k * (N / 16) + ch)) = make_uint4(u[k][0], u[k][1], u[k][2], u[k][3]);
+            uint32_t term[3];
+            split4(x[0], x[1], x[2], x[3], term);
+            *reinterpret_cast<uint4*>(pb + p_offset<N>(tid, c)) = make_uint4(term[0], term[1], term[2], 0u);
           }
           // keys that none of the item's rows sees have P = 0, but their values
           // may be anything (unused slots): zeros in their place keep 0 x NaN out
@@ -642,16 +686,16 @@ __global__ void __launch_bounds__(384, 1)
           }
           fence_proxy_async_smem();
           tc_fence_before();
-          mbar_arrive(&bar_p[sj & 1]);
+          mbar_arrive(&bar_p[me_g]);
         }
+        // the item's sums: lanes, then warps, then warpgroups
+        scatter_sum<N>(l, lane);
+        w_g[(warp % 4) * N + lane / (32 / N)] = l[0];
         if (keys) {
           mbar_arrive(&q_free[nq % C::NQ]);
           ++nq;
         }
-        // the item's sums: lanes, then warps
-        scatter_sum<N>(l, lane);
-        s_w[warp * N + lane / (32 / N)] = l[0];
-        if (!named_bar_and(1, 128, ok)) {
+        if (!named_bar_and(3, 256, ok)) {
           ok = false;
           break;
         }
@@ -659,12 +703,17 @@ __global__ void __launch_bounds__(384, 1)
         const bool whole = w.whole();
         // at most one item continues from the CTA before, and one into the next
         float* part = p.parts + ((long long)me * 2 + (w.at < u0 ? 0 : 1)) * (N * (DV + 2));
-        if (tid < N) {
-          // l and O^T carry 2^kLift alike: it counts into the maximum. A sum that is NaN makes the part's maximum so, or the
-          // join would take a part without one for a part without keys
-          const float sum = (s_w[tid] + s_w[N + tid]) + (s_w[2 * N + tid] + s_w[3 * N + tid]);
-          const float m = isnan(sum) ? sum : s_m[tid] - kLift;
-          s_l[tid] = whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
+        if (threadIdx.x < N) {
+          const float* a = s_w + tid;
+          const float* b = a + 4 * N;
+          const float top = fmaxf(s_m[tid], s_m[N + tid]);
+          const float fa = ex2(s_m[tid] - top), fb = ex2(s_m[N + tid] - top);  // 0 without a key
+          const float sum = fa * ((a[0] + a[N]) + (a[2 * N] + a[3 * N])) + fb * ((b[0] + b[N]) + (b[2 * N] + b[3 * N]));
+          // a sum that is NaN makes the part's maximum so, or the join would take a part without one for one without keys
+          const float m = isnan(sum) ? sum : sum == 0.f ? -INFINITY : top;
+          const float f = whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
+          s_l[tid] = fa * f;
+          s_l[N + tid] = fb * f;
           if (tid < rows && tid % p.block_heads < un.heads) {
             if (whole) {
               float* at = p.lse + (row0 + tid / p.block_heads) * p.hq + un.head0 + tid % p.block_heads;
@@ -675,44 +724,46 @@ __global__ void __launch_bounds__(384, 1)
             }
           }
         }
-        if (keys) {
+        if (keys) {  // the last P V, and with it all before
           const int last = gs + n - 1;
           if (!__all_sync(0xffffffffu, mbar_wait(&bar_o[last & 1], (last >> 1) & 1, abort_flag))) ok = false;
           tc_fence_after();
         }
-        if (!named_bar_and(1, 128, ok)) {
+        if (!named_bar_and(3, 256, ok)) {
           ok = false;
           break;
         }
+        const bool has[2] = {keys && (n > 1 || !(gs & 1)), keys && (n > 1 || (gs & 1))};  // warpgroups that had a tile
 #pragma unroll 1
-        for (int vb = 0; vb < C::VST; ++vb) {
-          int ti = 0, h = 0;
-#pragma unroll 1
-          for (int i0 = 0; i0 < rows; i0 += 4) {
-            uint32_t o[3][4] = {};
-            if (keys) {
+        for (int x = me_g; x < C::VST * quads; x += 2) {
+          const int vb = x / quads, c = x - vb * quads;
+          float v[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-              for (int k = 0; k < 3; ++k) tmem_ld4(lanes + vb * C::NO + k * N + i0, o[k]);
-              tmem_wait_ld();
+          for (int g = 0; g < 2; ++g) {
+            if (!has[g]) continue;
+            uint32_t u[16];
+            tmem_ld16(lanes + g * C::TM_O + vb * C::NT + c * 16, u);
+            tmem_wait_ld();
+            fence16(u);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) v[r] = fmaf(terms_sum(u, r), s_l[g * N + c * 4 + r], v[r]);
+          }
+          int ti = c * 4 / p.block_heads, h = c * 4 - ti * p.block_heads;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int i = c * 4 + r;
+            if (i < rows && h < un.heads) {
+              if (whole) {
+                T* at = static_cast<T*>(p.o) + ((row0 + ti) * p.hq + un.head0 + h) * DV + vb * 128 + tid;
+                if (SDPA_ADDR_OK(p.chk, at, 2)) *reinterpret_cast<uint16_t*>(at) = (uint16_t)E::pack(v[r], 0.f);
+              } else {
+                float* at = part + i * DV + vb * 128 + tid;
+                if (SDPA_ADDR_OK(p.chk, at, 4)) *at = v[r];
+              }
             }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              asm volatile("" : "+r"(o[0][e]), "+r"(o[1][e]), "+r"(o[2][e]));
-              const int i = i0 + e;
-              const float v = ((__uint_as_float(o[2][e]) + __uint_as_float(o[1][e])) + __uint_as_float(o[0][e])) * s_l[i];
-              if (i < rows && h < un.heads) {
-                if (whole) {
-                  T* at = static_cast<T*>(p.o) + ((row0 + ti) * p.hq + un.head0 + h) * DV + vb * 128 + tid;
-                  if (SDPA_ADDR_OK(p.chk, at, 2)) *reinterpret_cast<uint16_t*>(at) = (uint16_t)E::pack(v, 0.f);
-                } else {
-                  float* at = part + i * DV + vb * 128 + tid;
-                  if (SDPA_ADDR_OK(p.chk, at, 4)) *at = v;
-                }
-              }
-              if (++h == p.block_heads) {
-                h = 0;
-                ++ti;
-              }
+            if (++h == p.block_heads) {
+              h = 0;
+              ++ti;
             }
           }
         }
@@ -732,7 +783,7 @@ __global__ void __launch_bounds__(384, 1)
 
   tc_fence_before();
   __syncthreads();
-  if (warp == 7) {
+  if (warp == C::W_MMA) {
     tc_fence_after();
     tmem_dealloc(tmem, C::TM_COLS);
   }
@@ -759,13 +810,15 @@ int launch_t(const PagedFp8Launch& L, int* launches) {
 
 int launch_paged_fp8(const PagedFp8Launch& L, int n, int head_dim, bool bf16, int* launches) {
 #define ROWS(A, B, NN) return bf16 ? launch_t<A, B, NN, true>(L, launches) : launch_t<A, B, NN, false>(L, launches)
+  if (head_dim == 128 && n == 8) ROWS(128, 128, 8);
+  if (head_dim == 192 && n == 8) ROWS(192, 128, 8);
+  if (head_dim == 256 && n == 8) ROWS(256, 256, 8);
+  if (head_dim == 512 && n == 8) ROWS(512, 512, 8);
   if (head_dim == 128 && n == 16) ROWS(128, 128, 16);
   if (head_dim == 128 && n == 32) ROWS(128, 128, 32);
   if (head_dim == 192 && n == 16) ROWS(192, 128, 16);
   if (head_dim == 192 && n == 32) ROWS(192, 128, 32);
   if (head_dim == 256 && n == 16) ROWS(256, 256, 16);
-  if (head_dim == 256 && n == 32) ROWS(256, 256, 32);
-  if (head_dim == 512 && n == 16) ROWS(512, 512, 16);
 #undef ROWS
   return SDPA_ERR_UNSUPPORTED;
 }

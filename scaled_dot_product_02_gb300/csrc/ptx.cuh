@@ -68,6 +68,13 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
   }
 }
 
+// The same for two barriers, the first looks at them side by side (one costs some hundred cycles).
+__device__ __forceinline__ bool mbar_wait_both(uint64_t* a, uint32_t parity_a, uint64_t* b, uint32_t parity_b,
+                                               volatile int* abort) {
+  const bool x = mbar_try_wait(a, parity_a), y = mbar_try_wait(b, parity_b);
+  return (x || mbar_wait(a, parity_a, abort)) && (y || mbar_wait(b, parity_b, abort));
+}
+
 // Wait on `bar` without the abort flag, for at most 200 ms: used to drain
 // copies or MMAs already in flight before a CTA exits.
 __device__ __forceinline__ bool mbar_wait_drain(uint64_t* bar, uint32_t parity) {

@@ -26,7 +26,8 @@ __device__ __forceinline__ void scatter_sum(float (&v)[N], int lane) {
       v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
     }
   }
-  if (N == 16) v[0] += __shfl_xor_sync(0xffffffffu, v[0], 1);
+#pragma unroll
+  for (int x = 16 / N; x >= 1; x /= 2) v[0] += __shfl_xor_sync(0xffffffffu, v[0], x);
 }
 
 }  // namespace sdpa
