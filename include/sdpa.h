@@ -490,7 +490,8 @@ typedef struct {
 
 /* sdpa_paged_append into an 8-bit cache: rows are quantised as they are written, K from the fp32
  * values of the norm and rotation where n is given. axes: several positions a token, or NULL. Codes
- * and scale bytes may interleave (blocks that hold a page's K, V and scales) but not share bytes. */
+ * and scale bytes may interleave (blocks that hold a page's K, V and scales) but not share bytes.
+ * Two tokens of one call that map to one slot may leave the codes of one beside the scale of the other. */
 SDPA_API int sdpa_paged_append_fp8(const sdpa_paged_problem* p, const sdpa_norm_rope_problem* n,
                                    const sdpa_rope_axes* axes, const sdpa_paged_scales* scales, const void* q,
                                    const void* k, const void* v, const void* q_weight, const void* k_weight,
@@ -510,10 +511,13 @@ SDPA_API int sdpa_paged_read_fp8(const sdpa_paged_problem* p, const sdpa_paged_s
                                  const void* v_cache, void* k_out, void* v_out, const int32_t* cu_seqlens,
                                  const int32_t* kv_lens, const int32_t* block_table, void* stream);
 
-/* sdpa_paged_fwd over an 8-bit cache: the attention over the values that codes and scales stand for,
- * exactly (q stays 16-bit), with the same masks, outputs, errors and workspace rules. Scale bytes of
- * keys that no query row sees may hold anything; others are taken into 47 .. 207, what the append
- * writes. A row of q that is not finite gives NaN. */
+/* sdpa_paged_fwd over an 8-bit cache: the attention over the values that codes and scales stand for
+ * (q stays in 16 bits; scores are exact up to fp32 sums, probabilities are held to 2^-10), with the
+ * same masks, outputs, errors and workspace rules. Scale bytes of keys that no query row sees may hold
+ * anything; others are taken into 47 .. 207, what the append writes. A row of q that is not finite gives
+ * NaN. Rows of q lie any multiple of 8 elements apart. Made for few new tokens a sequence (decoding,
+ * speculative tokens, a prompt's tail): the cache is read once for every 8 (head_dim 512), 16 (256) or
+ * 32 query rows of a kv head; for longer chunks read the rows back and call sdpa_fwd. */
 SDPA_API size_t sdpa_paged_fwd_fp8_workspace_size(const sdpa_paged_problem* p);
 SDPA_API int sdpa_paged_fwd_fp8(const sdpa_paged_problem* p, const sdpa_paged_scales* scales, const void* q,
                                 const void* k_cache, const void* v_cache, void* o, float* lse,

@@ -161,7 +161,7 @@ __device__ __forceinline__ void split_q(const PagedFp8Params& f, const PagedWalk
                                         float* s_fq, int part, int lane) {
   using E = Elem<BF16>;
   constexpr int VECS = DQK / 8, LPR = VECS >= 32 ? 32 : VECS == 24 ? 32 : VECS, RP = 32 / LPR, VPL = (VECS + 31) / 32;
-  constexpr int U = VPL == 1 ? 4 : 2;  // rows of a lane whose loads are in flight together
+  constexpr int U = VPL > 1 ? 1 : N == 32 ? 4 : 2;  // rows of a lane whose loads are in flight together
   const PagedParams& p = f.a;
   const int rows = (w.i1(p) - w.i0 + 1) * p.block_heads, sub = lane % LPR;
 #pragma unroll 1
@@ -380,16 +380,22 @@ __global__ void __launch_bounds__(512, 1)
         };
         PagedBox prev;
         int before = 0;
-        for (int j = w.j0; j < w.j1 && ok; ++j) {
-          const PagedBox cur = box_here(j);
-          const int boxes = boxes_of(j);
-          for (int kb = 0; kb < C::KST && ok; ++kb) ok = fetch(&tmK, cur, boxes, kb * 128);
+#pragma unroll 1
+        for (int j = w.j0; j <= w.j1 && ok; ++j) {
+          PagedBox cur;
+          int boxes = 0;
+          if (j < w.j1) {
+            cur = box_here(j);
+            boxes = boxes_of(j);
+#pragma unroll 1
+            for (int kb = 0; kb < C::KST && ok; ++kb) ok = fetch(&tmK, cur, boxes, kb * 128);
+          }
           if (j > w.j0)
+#pragma unroll 1
             for (int vb = 0; vb < C::VST && ok; ++vb) ok = fetch(&tmV, prev, before, vb * 128);
           prev = cur;
           before = boxes;
         }
-        for (int vb = 0; vb < C::VST && ok; ++vb) ok = fetch(&tmV, prev, before, vb * 128);
       } while (ok && w.next(p));
       if (lane == 0) {
         if (!ok) {
@@ -519,11 +525,11 @@ __global__ void __launch_bounds__(512, 1)
             mma_commit(&bar_o[sj & 1]);
             return true;
           };
-          for (int j = 0; j < n && ok; ++j) {
-            ok = mma_s(j);
+#pragma unroll 1
+          for (int j = 0; j <= n && ok; ++j) {
+            if (j < n) ok = mma_s(j);
             if (ok && j >= 1) ok = mma_o(j - 1);
           }
-          if (ok) ok = mma_o(n - 1);
           gs += n;
         } while (ok && w.next(p));
         if (!ok) {
@@ -610,11 +616,8 @@ __global__ void __launch_bounds__(512, 1)
 #pragma unroll
             for (int c = 0; c < C::QUADS; ++c) {
               if (c >= quads) break;
-#pragma unroll
-              for (int r = 0; r < 4; ++r) {
-                const float m = warp_max(s[c * 4 + r]);
-                if (lane == 0) w_g[(warp % 4) * N + c * 4 + r] = m;
-              }
+              const float4 m4 = make_float4(warp_max(s[c * 4]), warp_max(s[c * 4 + 1]), warp_max(s[c * 4 + 2]), warp_max(s[c * 4 + 3]));
+              if (lane == 0) *reinterpret_cast<float4*>(w_g + (warp % 4) * N + c * 4) = m4;
             }
             named_bar_sync(bar_id, 128);
             if (tid < quads * 4) {
@@ -628,8 +631,11 @@ __global__ void __launch_bounds__(512, 1)
 #pragma unroll
             for (int c = 0; c < C::QUADS; ++c) {
               if (c >= quads) break;
-#pragma unroll
-              for (int r = 0; r < 4; ++r) l[c * 4 + r] *= f_g[c * 4 + r];
+              const float4 f4 = *reinterpret_cast<const float4*>(f_g + c * 4);
+              l[c * 4] *= f4.x;
+              l[c * 4 + 1] *= f4.y;
+              l[c * 4 + 2] *= f4.z;
+              l[c * 4 + 3] *= f4.w;
             }
             if (j >= 2) {  // this warpgroup's last P V is done: see above
 #pragma unroll 1
@@ -640,8 +646,10 @@ __global__ void __launch_bounds__(512, 1)
                   tmem_ld16(my_o + vb * C::NT + c * 16, u);
                   tmem_wait_ld();
                   fence16(u);
+                  const float4 f4 = *reinterpret_cast<const float4*>(f_g + c * 4);
+                  const float fr[4] = {f4.x, f4.y, f4.z, f4.w};
 #pragma unroll
-                  for (int i = 0; i < 12; ++i) u[i] = __float_as_uint(__uint_as_float(u[i]) * f_g[c * 4 + i % 4]);
+                  for (int i = 0; i < 12; ++i) u[i] = __float_as_uint(__uint_as_float(u[i]) * fr[i % 4]);
                   tmem_st16(my_o + vb * C::NT + c * 16, u);
                 }
               tmem_wait_st();

@@ -554,3 +554,203 @@ def test_prompt_then_decoding(d, hq, hkv):
             _, _, pv, _ = ref.paged_attention(c["q"], c["kc"], c["vc"], c["table"], c["lens"], c["cu"], page, "nhd", True, -1, c["scale"])
             assert bool(((o - o2).cpu().double().abs() <= (2.0 ** -8 + 2.0 ** -10 + 2.0 ** -7 + 2.0 ** -10) * pv + 1e-6).all())
             assert bool(((lse - lse2).abs() <= 2.0 ** -15 * (1 + lse.abs())).all())
+
+
+# ---------------------------------------------------------------- how a program calls them
+
+def test_many_tiles_and_many_items():
+    """Rings go round many times, items cross many cuts, every tile of a short item is an edge."""
+    for new, total, d, kw in (([1] * 40, [1 + 97 * i for i in range(40)], 128, {}), ([3] * 200, [3 + i % 61 for i in range(200)], 256, {}),
+                              ([2] * 12, [5000] * 12, 512, {}), ([64], [3000], 128, {}), ([100, 1], [4000, 9000], 192, {})):
+        c = case(new, total, d=d, page=16, **kw)
+        c["vmax"] = used_vmax(c)
+        check(c, *call(c))
+        check(c, *call(c, window=200), window=200)
+
+
+def test_a_large_batch():
+    n = 700
+    c = case([i % 3 for i in range(n)], [max(i % 3, (i * 37) % 400) for i in range(n)], hq=4, hkv=1, d=128)
+    c["vmax"] = used_vmax(c)
+    check(c, *call(c))
+
+
+def test_strided_queries_and_a_wide_table():
+    """q rows in a wider projection, not a multiple of head_dim apart; a block table that is a slice of a wider one."""
+    for d in (128, 192):
+        c = case([2, 1, 4], [130, 300, 77], d=d, page=32)
+        wide = torch.full((7, 8 * d + 24), float("nan"), dtype=BF, device="cuda")
+        wide[:, 8:8 + 8 * d] = c["dev"][0].reshape(7, -1)
+        table = torch.full((3, c["dev"][5].shape[1] + 5), -1, dtype=torch.int32, device="cuda")
+        table[:, 2:-3] = c["dev"][5]
+        want = call(c)
+        c["dev"][0], c["dev"][5] = wide[:, 8:8 + 8 * d].unflatten(1, (8, d)), table[:, 2:-3]
+        got = call(c)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        c["vmax"] = used_vmax(c)
+        check(c, *got)
+
+
+def test_offsets_beyond_32_bits():
+    """Pages whose codes lie more than 4 GiB into the cache: written, read back and attended."""
+    d, page, hkv, pages = 128, 16, 8, 270000
+    kc, vc = (torch.empty(pages, page, hkv, d, dtype=torch.uint8, device="cuda") for _ in "kv")
+    ks, vs = (torch.empty(pages, page, hkv, dtype=torch.uint8, device="cuda") for _ in "kv")
+    assert kc.numel() > 2 ** 32
+    ids = torch.tensor([[269999, 3, 265000, 131072, 262145]], dtype=torch.int32, device="cuda")
+    lens, cu = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([75], [0, 75]))
+    g = torch.Generator(device="cuda").manual_seed(1)
+    k, v = (torch.randn(75, hkv, d, device="cuda", generator=g).bfloat16() for _ in "kv")
+    sdpa.sdpa_paged_append_fp8(k, v, kc, vc, ks, vs, ids, lens, cu)
+    kr, vr = sdpa.sdpa_paged_read_fp8(kc, vc, ks, vs, ids, lens, cu, rows=75, dtype=BF)
+    for x, y in ((k, kr), (v, vr)):
+        assert torch.equal(y.cpu().double(), fp8_ref.decode(*fp8_ref.quantise(x.cpu(), BF)))
+    q = torch.randn(3, 8, d, device="cuda", generator=g).bfloat16()
+    small = [x[ids[0].long()].contiguous() for x in (kc, vc, ks, vs)]
+    near = torch.arange(5, dtype=torch.int32, device="cuda")[None]
+    cu3 = torch.tensor([0, 3], dtype=torch.int32, device="cuda")
+    a = sdpa.sdpa_paged_fwd_fp8(q, kc, vc, ks, vs, ids, lens, cu3, max_seqlen_q=3)
+    b = sdpa.sdpa_paged_fwd_fp8(q, *small, near, lens, cu3, max_seqlen_q=3)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1]) and sdpa.sdpa_get_device_error() == 0
+
+
+def test_two_calls_at_once_on_two_streams():
+    c, e = case([6, 1, 5], [900, 2000, 300], pad=1), case([1, 3, 20], [1500, 700, 800], d=256, page=64, order="hnd")
+    streams = torch.cuda.Stream(), torch.cuda.Stream()
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = [(call(c, stream=streams[0]), call(e, stream=streams[1])) for _ in range(10)]
+    torch.cuda.synchronize()
+    for a, b in got:
+        assert torch.equal(a[0][:-1], got[0][0][0][:-1]) and torch.equal(b[0], got[0][1][0])
+    for x, y in ((c, got[-1][0]), (e, got[-1][1])):
+        x["vmax"] = used_vmax(x)
+        check(x, *y)
+    # append and read on a stream of their own
+    s = write_batch(1, [3, 0, 70], [3, 40, 129], 16, 2, 128, 128, "nhd", BF)
+    want = expected(s, s["k"], s["v"])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    append(s, stream=side)
+    kr, vr = sdpa.sdpa_paged_read_fp8(*s["caches"], *s["dev"], rows=73, dtype=BF, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    assert all(torch.equal(a.cpu(), b) for a, b in zip(s["caches"], want))
+    assert torch.equal(kr.cpu().double(), fp8_ref.decode(*fp8_ref.quantise(s["k"].cpu(), BF)))
+
+
+def test_captured_steps_follow_the_lengths_and_share_a_workspace():
+    """Two captured graphs, an append with attention each, that use one workspace in turn; lengths, tables and tokens
+    change in place between replays."""
+    d, hq, hkv, page, batch = 128, 8, 2, 16, 4
+    g = torch.Generator(device="cuda").manual_seed(3)
+    caches = [torch.zeros(40, page, hkv, d, dtype=torch.uint8, device="cuda") for _ in "kv"]
+    caches += [torch.full((40, page, hkv), 127, dtype=torch.uint8, device="cuda") for _ in "kv"]
+    ids = torch.arange(40, dtype=torch.int32, device="cuda").view(batch, 10).contiguous()
+    lens, cu = torch.ones(batch, dtype=torch.int32, device="cuda"), torch.arange(batch + 1, dtype=torch.int32, device="cuda")
+    x = torch.randn(batch, (hq + 2 * hkv) * d, device="cuda", generator=g).bfloat16()
+    q, k, v = (y.unflatten(1, (-1, d)) for y in x.split([hq * d, hkv * d, hkv * d], dim=1))
+    ws = torch.empty(sdpa.PAGED_WORKSPACE_MAX, dtype=torch.uint8, device="cuda")
+    outs, graphs = [], []
+    for bound in (160, 64):
+        o, lse = torch.zeros(batch, hq, d, dtype=BF, device="cuda"), torch.zeros(batch, hq, device="cuda")
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            sdpa.sdpa_paged_append_fp8(k, v, *caches, ids, lens, cu)
+            sdpa.sdpa_paged_fwd_fp8(q, *caches, ids, lens, cu, max_seqlen_q=1, max_seqlen_kv=bound, out=o, lse=lse, workspace=ws)
+        outs.append((o, lse))
+        graphs.append(graph)
+    for step in range(12):
+        n = [1 + step, 1 + 2 * step, 1 + 3 * step, 1 + 4 * step]
+        lens.copy_(torch.tensor(n, dtype=torch.int32))
+        x.copy_(torch.randn(x.shape, device="cuda", generator=g))
+        for graph in graphs:
+            graph.replay()
+        assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
+        c = dict(q=q.cpu(), kc=fp8_ref.decode(caches[0].cpu(), caches[2].cpu()), vc=fp8_ref.decode(caches[1].cpu(), caches[3].cpu()),
+                 table=ids.cpu().numpy(), cu=cu.cpu().numpy(), lens=np.array(n, dtype=np.int32), page=page, max_kv=max(n),
+                 scale=d ** -0.5, dtype=BF)
+        check(c, *outs[0])
+
+
+@pytest.mark.parametrize("name,d", [("ragged", 128), ("spec", 192), ("chunk", 256), ("spec", 512)])
+def test_a_workspace_of_the_reported_size_is_enough(name, d, monkeypatch):
+    c = case(*BATCHES[name], d=d)
+    c["vmax"] = used_vmax(c)
+    sizes, launch = [], sdpa._launch
+    monkeypatch.setattr(sdpa, "_launch", lambda n, dev, *a: (sizes.append(a[-1]), launch(n, dev, *a)))
+    call(c)
+    guard = torch.full((sizes[0] + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+    o, lse = call(c, workspace=guard[:sizes[0]])
+    check(c, o, lse)
+    assert bool((guard[sizes[0]:] == 0xA5).all())
+
+
+@pytest.mark.parametrize("d,order", [(128, "nhd"), (192, "hnd"), (256, "hnd"), (512, "nhd")])
+def test_every_access_is_inside_the_buffers(d, order):
+    """The address-checked build: attention, append (copied; normed, with axes) and read, the same bits as the other one."""
+    for name in ("ragged", "spec", "chunk", "short_cache"):
+        c = case(*BATCHES[name], d=d, order=order, page=48)
+        want = call(c)
+        cu = torch.from_numpy(np.concatenate([[0], np.cumsum(c["lens"])]).astype(np.int32)).cuda()
+        rows = int(c["lens"].sum())
+        back = sdpa.sdpa_paged_read_fp8(*c["dev"][1:7], cu, cache_layout=order, rows=rows, dtype=BF)
+        s = write_batch(3, *WRITES[1], 16, 2, d, 128 if d == 192 else d, order, BF, pad=3, hq=4)
+        w = torch.ones(d, device="cuda").bfloat16()
+        t, pos = ref.angles_table(100, 48).cuda(), torch.randint(0, 100, (2, s["k"].shape[0]), device="cuda", dtype=torch.int32)
+        norm = dict(q=s["q"], q_weight=w, k_weight=w, cos_sin=t, positions=pos, sections=(11, 13))
+        clean = [x.clone() for x in s["caches"]]
+        append(s), append(s, **norm)
+        written = [x.clone() for x in s["caches"]]
+        both = sdpa.sdpa_qk_norm_rope(s["q"], s["k"], w, w, t, pos, sections=(11, 13))
+        with sdpa.address_checked():
+            sdpa.sdpa_debug_address_report()
+            got = call(c)
+            again = sdpa.sdpa_paged_read_fp8(*c["dev"][1:7], cu, cache_layout=order, rows=rows, dtype=BF)
+            for x, y in zip(s["caches"], clean):
+                x.copy_(y)
+            append(s), append(s, **norm)
+            rope = sdpa.sdpa_qk_norm_rope(s["q"], s["k"], w, w, t, pos, sections=(11, 13))
+            assert sdpa.sdpa_debug_address_report()[0] == 0 and sdpa.sdpa_get_device_error() == 0
+        for a, b in zip(got + again + rope + tuple(s["caches"]), want + back + both + tuple(written)):
+            assert torch.equal(a, b)
+
+
+def test_the_checker_sees_the_new_accesses():
+    """With every extent 16 bytes short the last bytes of the scales and outputs count as outside, and are not written."""
+    c = case([1, 1], [16, 32], hq=2, hkv=2, d=128)
+    want = call(c)
+    with sdpa.address_checked():
+        sdpa.sdpa_debug_address_report()
+        try:
+            sdpa.sdpa_debug_address_shrink(16)
+            out = torch.full_like(want[0], 7.0)
+            call(c, out=out)
+            assert sdpa.sdpa_debug_address_report()[0] > 0 and sdpa.sdpa_get_device_error() == 9
+        finally:
+            sdpa.sdpa_debug_address_shrink(0)
+        assert bool((out.flatten()[-8:] == 7).all())
+
+
+def test_kernel_kinds_are_timed():
+    c = case([1, 2], [300, 40])
+    cu = torch.tensor([0, 1, 3], dtype=torch.int32, device="cuda")
+    sdpa.sdpa_profile_begin()
+    call(c)
+    sdpa.sdpa_paged_read_fp8(*c["dev"][1:7], cu, rows=3, dtype=BF)
+    got = sdpa.sdpa_profile_end()
+    assert got["paged"][1] == 1 and got["read"][1] == 1 and got["paged"][0] > 0 and got["read"][0] > 0
+
+
+def test_attention_of_a_long_chunk_agrees_with_rows_read_back():
+    """300 tokens over 1000 keys: the kernel for few tokens in many items, and sdpa_fwd over the rows read back."""
+    c = case([300], [1000], hq=8, hkv=2, d=128)
+    c["vmax"] = used_vmax(c)
+    o, lse = call(c)
+    check(c, o, lse)
+    cu_q, cu_k = (torch.tensor([0, n], dtype=torch.int32, device="cuda") for n in (300, 1000))
+    k, v = sdpa.sdpa_paged_read_fp8(*c["dev"][1:7], cu_k, rows=1000, dtype=BF)
+    o2, lse2 = sdpa.sdpa_fwd(c["dev"][0], k, v, layout="thd", mask="causal_br", cu_seqlens_q=cu_q, cu_seqlens_kv=cu_k,
+                             max_seqlen_q=300, max_seqlen_kv=1000)
+    _, _, pv, _ = ref.paged_attention(c["q"], c["kc"], c["vc"], c["table"], c["lens"], c["cu"], 16, "nhd", True, -1, c["scale"])
+    assert bool(((o - o2).cpu().double().abs() <= (2.0 ** -8 + 2.0 ** -10 + 2.0 ** -7 + 2.0 ** -10) * pv + 1e-6).all())
+    assert bool(((lse - lse2).abs() <= 2.0 ** -15 * (1 + lse.abs())).all())
