@@ -299,6 +299,7 @@ struct PagedParams {
   int units_per_block;         // items of one block of tokens: kv heads x head_blocks x dv_splits
   int small_q, small;          // this launch serves the sequences of at most small_q tokens (small), or the others
   int split;                   // rows kernel: items may be split over workers
+  int lead;                    // and an item counts for that many key tiles more than it has
   int tail;                    // chunk kernels: shares that the last items are cut into (0: none)
   int behind;                  // started while the rows kernel of the same call (and its join) still run
   int q_box_rows;              // rows one Q copy brings (half of an item's at head_dim 128 chunks)

@@ -105,13 +105,14 @@ __device__ __forceinline__ PagedUnit paged_unit(const PagedParams& p, int unit) 
   return u;
 }
 
+// An item's length in the row of all items: its tiles, behind p.lead places that stand for what an item costs by itself.
 __device__ __forceinline__ int paged_weight(const PagedParams& p, const PagedSpan& s) {
-  return p.split ? max(1, s.tiles) : 1;
+  return p.split && s.tiles > 0 ? s.tiles + p.lead : 1;
 }
 
 // Items of one sequence: blocks of `tokens` tokens, and within a block the kv
 // heads (times the head blocks of a wide group). An item without keys counts
-// as one tile, so that someone writes its zeros. Unless items are split
+// as one place, so that someone writes its zeros. Unless items are split
 // (p.split), each weighs one, whatever its keys: shares are whole items.
 __device__ __forceinline__ long long paged_units(const PagedParams& p, const PagedSeq& s) {
   if (!p.split) return (long long)((s.q_len + p.tokens - 1) / p.tokens) * p.units_per_block;
@@ -136,12 +137,14 @@ struct PagedWalk {
 
   __device__ __forceinline__ int i1(const PagedParams& p) const { return min(i0 + p.tokens, s.q_len) - 1; }
   __device__ __forceinline__ bool whole() const { return j0 == 0 && j1 == span.tiles; }
+  // Whether the share holds all of the item's places (with p.lead it may hold all tiles, but not those in front).
+  __device__ __forceinline__ bool covers() const { return u <= at && at + weight <= u_end; }
   __device__ __forceinline__ void locate(const PagedParams& p) {
     weight = paged_weight(p, span);
     unit = (int)((unsigned)(u - block_at) / (unsigned)weight);  // the host bounds a block's length
     at = block_at + (long long)unit * weight;
-    j0 = (int)(u - at);
-    j1 = p.split ? min(span.tiles, (int)min((long long)weight, u_end - at)) : span.tiles;
+    j0 = max(0, (int)(u - at) - p.lead);
+    j1 = p.split ? min(span.tiles, max(0, (int)min((long long)weight, u_end - at) - p.lead)) : span.tiles;
   }
   __device__ __forceinline__ PagedCut cut(const PagedParams& p) const {
     return PagedCut{at, weight, s.row0 + i0, i1(p) - i0 + 1, unit};

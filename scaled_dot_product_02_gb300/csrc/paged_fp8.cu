@@ -40,6 +40,18 @@
 // allocator and MMA issuer; 13-15 take an item's rows of Q apart and then fetch its
 // scale bytes, a tile each in turn, up to SST tiles ahead. K and V tiles go through
 // a ring of 16 KB stages (128 keys x 128 codes).
+//
+// In the equal shares an item counts for a few tiles more than it has, about what
+// its start and end cost (PagedParams::lead); a share may so get none of the tiles of
+// an item that it touches, and leaves an empty part.
+//
+// Measured with the join, captured: 64 sequences of 500 to 16384 keys, 32 heads on 8
+// of 128, 190 to 211 us across boxes, 5.3 to 5.9 TB/s (the 16-bit cache 356); the
+// same bytes at head_dim 256 193, 512 188 us (5.9, 6.1 TB/s); 48 sequences with a
+// window of 1024 at head_dim 256 46 (72); one token over 999 keys 12.4 (12.4). Items
+// of many rows are bound by the softmax: 4 tokens of 4 heads 264 us, 8 tokens 410, over
+// the first batch's keys; a group of 32 heads on one kv head 70 against the 16-bit
+// cache's 60.
 #include <algorithm>
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -314,7 +326,7 @@ __global__ void __launch_bounds__(512, 1)
       int c = 0;
       bool ok = true;
       do {
-        if (w.span.tiles == 0) continue;
+        if (w.j1 == w.j0) continue;  // no keys, or none of its tiles
         const PagedUnit un = paged_unit(p, w.unit);
         // The page numbers come 32 at a time, one a lane, the next 32 behind them: a load for every tile made every tile
         // wait for it.
@@ -411,7 +423,7 @@ __global__ void __launch_bounds__(512, 1)
       int nq = 0, gs = 0;  // items with keys, tiles of earlier items
       bool ok = true;
       do {
-        if (w.span.tiles == 0) continue;
+        if (w.j1 == w.j0) continue;  // no keys, or none of its tiles
         const PagedUnit un = paged_unit(p, w.unit);
         const int n = w.j1 - w.j0;
         // four keys a lane, which lie in one page; not looked at before they are stored, a tile later
@@ -474,7 +486,7 @@ __global__ void __launch_bounds__(512, 1)
         int c = 0, nq = 0, gs = 0;  // ring stages, items with keys, tiles of earlier items
         bool ok = true;
         do {
-          if (w.span.tiles == 0) continue;
+          if (w.j1 == w.j0) continue;  // no keys, or none of its tiles
           const int n = w.j1 - w.j0;
           const uint32_t q_base = smem_u32(sQ + (nq % C::NQ) * C::Q_BYTES);
           uint64_t* my_q_free = &q_free[nq % C::NQ];
@@ -552,7 +564,7 @@ __global__ void __launch_bounds__(512, 1)
       bool ok = true;
       do {
         const int n = w.j1 - w.j0;
-        const bool keys = w.span.tiles > 0;
+        const bool keys = n > 0;
         const PagedUnit un = paged_unit(p, w.unit);
         const int tok = w.i1(p) - w.i0 + 1, rows = tok * p.block_heads, quads = (rows + 3) / 4;
         const int off = w.s.kv_len - w.s.q_len;
@@ -711,7 +723,7 @@ __global__ void __launch_bounds__(512, 1)
           break;
         }
         const long long row0 = w.s.row0 + w.i0;
-        const bool whole = w.whole();
+        const bool whole = w.covers();
         // at most one item continues from the CTA before, and one into the next
         float* part = p.parts + ((long long)me * 2 + (w.at < u0 ? 0 : 1)) * (N * (DV + 2));
         if (threadIdx.x < N) {
