@@ -2,8 +2,8 @@
 // cache as packed 16-bit rows: y = code 2^e (fp8_row.cuh), rounded once (not at
 // all when the type is the one the row was quantised from).
 //
-// Bound by memory: a byte read and two written a value. A warp takes four
-// tokens, all heads: their places in the cache are found by a lane each (a
+// Bound by memory: a byte read and two written a value. A warp takes 1, 4
+// or 8 tokens, all heads: their places in the cache are found by a lane each (a
 // binary search among the sequences' ends), then all lanes walk the tokens'
 // values, eight a lane and step, with several steps' loads in flight.
 //
@@ -25,6 +25,11 @@ constexpr int kSteps = 8;   // loads a lane has in flight
 // Rows up to which a warp takes one token (8 kv heads of 128; us with one / four): 1000 rows 6.2 / 10.4, 8000 16.1 / 17.0,
 // 32000 39.1 / 41.2, 73500 82.1 / 77.9. (The K or the V of one token a warp: 16000 rows 31.2 against 23.5.)
 constexpr int kFew = 40000;
+// A token of up to kNarrow 16-byte vectors leaves lanes and steps idle: from kFewNarrow tokens a vector up a warp's lanes walk
+// kFlat tokens at once (heads of 128; us so / as above): 1 kv head, 2000 rows 6.3 / 6.3, 16000 8.3 / 15.8, 64000 18.5 / 41.1; 2
+// heads, 16000 rows 10.9 / 16.5; 4 heads, 8000 rows 14.4 / 11.2, 16000 18.6 / 18.5, 64000 42.3 / 48.3; 6 heads, 16000 rows 25.6 /
+// 20.7, 64000 61.4 / 56.9.
+constexpr int kNarrow = 128, kFewNarrow = 100, kFlat = 8;
 
 struct Place {
   long long k_at, v_at;    // head 0's codes
@@ -70,10 +75,24 @@ __device__ __forceinline__ Place place_of(const PagedReadParams& p, long long ro
   return x;
 }
 
-// TOKENS: of a warp.
-template <bool BF16, int D, int DV, int TOKENS>
+__device__ __forceinline__ long long from_lane(long long x, int lane) { return __shfl_sync(0xffffffffu, x, lane); }
+
+// Eight codes as 16-bit values, written.
+template <bool BF16>
+__device__ __forceinline__ void write_vec(const PagedReadParams& p, uint16_t* to, uint2 c, int e) {
+  const float s = exp2_byte(e);
+  uint32_t y[4];
+#pragma unroll
+  for (int z = 0; z < 4; ++z) {
+    const float2 f = Elem<false>::unpack(unpack_e4m3x2((uint16_t)((z < 2 ? c.x : c.y) >> (16 * (z & 1)))));
+    y[z] = Elem<BF16>::pack(f.x * s, f.y * s);
+  }
+  if (SDPA_ADDR_OK(p.chk, to, 16)) *reinterpret_cast<uint4*>(to) = make_uint4(y[0], y[1], y[2], y[3]);
+}
+
+// TOKENS: of a warp. FLAT: the lanes walk all of them at once, else one after the other.
+template <bool BF16, int D, int DV, int TOKENS, bool FLAT>
 __global__ void __launch_bounds__(kThreads) paged_read_kernel(const __grid_constant__ PagedReadParams p) {
-  using E = Elem<BF16>;
   const int lane = threadIdx.x % 32;
   const long long row0 = ((long long)blockIdx.x * (kThreads / 32) + threadIdx.x / 32) * TOKENS;
   if (row0 >= p.rows) return;
@@ -83,44 +102,53 @@ __global__ void __launch_bounds__(kThreads) paged_read_kernel(const __grid_const
   if (lane < TOKENS && row0 + lane < p.rows) mine = place_of(p, row0 + lane);
   const uint32_t live = __ballot_sync(0xffffffffu, mine.live);
   const int vecs_k = p.hkv * (D / 8), vecs = vecs_k + p.hkv * (DV / 8);  // of a token: K's, then V's
+  auto load = [&](const uint8_t* k, const uint8_t* v, const uint8_t* ks, const uint8_t* vs, int i, bool here, uint2& c, int& e) {
+    const bool is_v = i >= vecs_k;
+    const int w = is_v ? DV / 8 : D / 8, j = is_v ? i - vecs_k : i, h = j / w;
+    const uint8_t* from = (is_v ? v + h * p.v_head : k + h * p.k_head) + (j - h * w) * 8;
+    const uint8_t* se = is_v ? vs + h * p.vs_head : ks + h * p.ks_head;
+    const bool in = here && SDPA_ADDR_OK(p.chk, from, 8) && SDPA_ADDR_OK(p.chk, se, 1);
+    c = in ? __ldg(reinterpret_cast<const uint2*>(from)) : make_uint2(0u, 0u);
+    e = in ? __ldg(se) : 127;
+  };
+  uint16_t* ko = static_cast<uint16_t*>(p.k_out) + row0 * p.k_row;
+  uint16_t* vo = static_cast<uint16_t*>(p.v_out) + row0 * p.v_row;
+  if constexpr (FLAT) {
 #pragma unroll 1
-  for (int t = 0; t < TOKENS; ++t) {
-    if (!(live >> t & 1)) continue;
-    const uint8_t* k = p.k_cache + __shfl_sync(0xffffffffu, mine.k_at, t);
-    const uint8_t* v = p.v_cache + __shfl_sync(0xffffffffu, mine.v_at, t);
-    const uint8_t* ks = p.k_scale + __shfl_sync(0xffffffffu, mine.ks_at, t);
-    const uint8_t* vs = p.v_scale + __shfl_sync(0xffffffffu, mine.vs_at, t);
-    uint16_t* ko = static_cast<uint16_t*>(p.k_out) + (row0 + t) * p.k_row;
-    uint16_t* vo = static_cast<uint16_t*>(p.v_out) + (row0 + t) * p.v_row;
-#pragma unroll 1
-    for (int i0 = lane; i0 < vecs; i0 += 32 * kSteps) {
+    for (int i0 = 0; i0 < vecs * TOKENS; i0 += 32 * kSteps) {
       uint2 c[kSteps];
       int e[kSteps];
 #pragma unroll
       for (int x = 0; x < kSteps; ++x) {
-        const int i = i0 + x * 32;
-        const bool is_v = i >= vecs_k;
-        const int w = is_v ? DV / 8 : D / 8, j = is_v ? i - vecs_k : i, h = j / w;
-        const uint8_t* from = (is_v ? v + h * p.v_head : k + h * p.k_head) + (j - h * w) * 8;
-        const uint8_t* se = is_v ? vs + h * p.vs_head : ks + h * p.ks_head;
-        const bool in = i < vecs && SDPA_ADDR_OK(p.chk, from, 8) && SDPA_ADDR_OK(p.chk, se, 1);
-        c[x] = in ? __ldg(reinterpret_cast<const uint2*>(from)) : make_uint2(0u, 0u);
-        e[x] = in ? __ldg(se) : 127;
+        const int n = i0 + x * 32 + lane, t = min(n / vecs, TOKENS - 1);
+        load(p.k_cache + from_lane(mine.k_at, t), p.v_cache + from_lane(mine.v_at, t), p.k_scale + from_lane(mine.ks_at, t),
+             p.v_scale + from_lane(mine.vs_at, t), n - t * vecs, n < vecs * TOKENS && (live >> t & 1), c[x], e[x]);
       }
 #pragma unroll
       for (int x = 0; x < kSteps; ++x) {
-        const int i = i0 + x * 32;
-        if (i >= vecs) break;
-        const bool is_v = i >= vecs_k;
-        uint16_t* to = is_v ? vo + (i - vecs_k) * 8 : ko + i * 8;
-        const float s = exp2_byte(e[x]);
-        uint32_t y[4];
+        const int n = i0 + x * 32 + lane, t = n / vecs, i = n - t * vecs;
+        if (t >= TOKENS || !(live >> t & 1)) continue;
+        write_vec<BF16>(p, i >= vecs_k ? vo + t * p.v_row + (i - vecs_k) * 8 : ko + t * p.k_row + i * 8, c[x], e[x]);
+      }
+    }
+  } else {
+#pragma unroll 1
+    for (int t = 0; t < TOKENS; ++t, ko += p.k_row, vo += p.v_row) {
+      if (!(live >> t & 1)) continue;
+      const uint8_t *k = p.k_cache + from_lane(mine.k_at, t), *v = p.v_cache + from_lane(mine.v_at, t);
+      const uint8_t *ks = p.k_scale + from_lane(mine.ks_at, t), *vs = p.v_scale + from_lane(mine.vs_at, t);
+#pragma unroll 1
+      for (int i0 = lane; i0 < vecs; i0 += 32 * kSteps) {
+        uint2 c[kSteps];
+        int e[kSteps];
 #pragma unroll
-        for (int z = 0; z < 4; ++z) {
-          const float2 f = Elem<false>::unpack(unpack_e4m3x2((uint16_t)((z < 2 ? c[x].x : c[x].y) >> (16 * (z & 1)))));
-          y[z] = E::pack(f.x * s, f.y * s);
+        for (int x = 0; x < kSteps; ++x) load(k, v, ks, vs, i0 + x * 32, i0 + x * 32 < vecs, c[x], e[x]);
+#pragma unroll
+        for (int x = 0; x < kSteps; ++x) {
+          const int i = i0 + x * 32;
+          if (i >= vecs) break;
+          write_vec<BF16>(p, i >= vecs_k ? vo + (i - vecs_k) * 8 : ko + i * 8, c[x], e[x]);
         }
-        if (SDPA_ADDR_OK(p.chk, to, 16)) *reinterpret_cast<uint4*>(to) = make_uint4(y[0], y[1], y[2], y[3]);
       }
     }
   }
@@ -128,10 +156,14 @@ __global__ void __launch_bounds__(kThreads) paged_read_kernel(const __grid_const
 
 template <bool BF16, int D, int DV>
 int launch_t(const PagedReadParams& p, cudaStream_t s) {
-  const bool few = p.rows <= kFew;
-  const int per = kThreads / 32 * (few ? 1 : 4);  // rows of a block
+  const int vecs = p.hkv * (D + DV) / 8;
+  const bool flat = vecs <= kNarrow && p.rows > kFewNarrow * (long long)vecs;
+  const int tokens = flat ? kFlat : p.rows <= kFew ? 1 : 4;
+  const int per = kThreads / 32 * tokens;  // rows of a block
   const unsigned grid = (unsigned)((p.rows + per - 1) / per);
-  auto kern = few ? paged_read_kernel<BF16, D, DV, 1> : paged_read_kernel<BF16, D, DV, 4>;
+  auto kern = flat          ? paged_read_kernel<BF16, D, DV, kFlat, true>
+              : tokens == 1 ? paged_read_kernel<BF16, D, DV, 1, false>
+                            : paged_read_kernel<BF16, D, DV, 4, false>;
   kern<<<grid, kThreads, 0, s>>>(p);
   return cudaGetLastError() == cudaSuccess ? SDPA_OK : SDPA_ERR_CUDA;
 }

@@ -479,6 +479,28 @@ def test_read(take, total, d, page, order, dtype):
     assert bool((wide[:, 3 * (d + dv):] == 7).all()) and sdpa.sdpa_get_device_error() == 0
 
 
+@pytest.mark.parametrize("take", [[3333, 0, 1, 3403], [3300, 3303], [1] * 7 + [12793]])
+@pytest.mark.parametrize("hkv,d,order", [(1, 128, "nhd"), (2, 192, "hnd"), (1, 512, "nhd"), (4, 128, "nhd"), (5, 128, "nhd")])
+def test_read_of_many_rows_of_few_heads(take, hkv, d, order):
+    """Rows enough that a warp walks several tokens of few heads at once; its last ones end behind the batch."""
+    total = [t + 5 for t in take]
+    c = case([1] * len(total), total, hkv=hkv, hq=hkv, d=d, order=order, seed=4)
+    cu = np.concatenate([[0], np.cumsum(take)]).astype(np.int32)
+    n = int(cu[-1])
+    row, pg, slot, _, _ = (torch.from_numpy(a) for a in ref.token_places(cu, c["lens"], c["page"], c["table"]))
+    table = c["dev"][5].clone()
+    bad = max(range(len(take)), key=lambda b: take[b])
+    table[bad, 20] = -1
+    gone = (pg == int(c["table"][bad, 20]))
+    k, v = sdpa.sdpa_paged_read_fp8(*c["dev"][1:5], table, c["dev"][6], torch.from_numpy(cu).cuda(), cache_layout=order,
+                                    k_out=torch.full((n + 3, hkv, d), 7.0, dtype=BF, device="cuda"),
+                                    v_out=torch.full((n + 3, hkv, c["vc"].shape[-1]), 7.0, dtype=BF, device="cuda"))
+    assert sdpa.sdpa_get_device_error() == 10 and int(gone.sum()) == 16
+    for out, x in ((k.cpu(), c["kc"]), (v.cpu(), c["vc"])):
+        assert torch.equal(out[row[~gone]].double(), x[pg[~gone], slot[~gone]])
+        assert bool((out[row[gone]] == 7).all()) and bool((out[n:] == 7).all())
+
+
 def test_read_special_codes_and_other_types():
     """Every code with scales from one end to the other, rounded once into the other type too."""
     scales = [0, 1, 20, 47, 60, 112, 118, 126, 127, 128, 134, 150, 207, 230, 254, 255]
@@ -754,3 +776,29 @@ def test_attention_of_a_long_chunk_agrees_with_rows_read_back():
     _, _, pv, _ = ref.paged_attention(c["q"], c["kc"], c["vc"], c["table"], c["lens"], c["cu"], 16, "nhd", True, -1, c["scale"])
     assert bool(((o - o2).cpu().double().abs() <= (2.0 ** -8 + 2.0 ** -10 + 2.0 ** -7 + 2.0 ** -10) * pv + 1e-6).all())
     assert bool(((lse - lse2).abs() <= 2.0 ** -15 * (1 + lse.abs())).all())
+
+
+@pytest.mark.parametrize("d", [128, 256, 512])
+def test_cuts_anywhere(d):
+    """Every number of CTAs up to 48: shares begin and end at every place of an item, also where it has no tiles yet."""
+    c = case([1, 2, 1, 0, 1], [700, 530, 1, 40, 1025], hq=4, hkv=2, d=d, page=32)
+    c["vmax"] = used_vmax(c)
+    try:
+        for cap in range(1, 49):
+            sdpa.sdpa_debug_set_max_ctas(cap)
+            check(c, *call(c))
+    finally:
+        sdpa.sdpa_debug_set_max_ctas(0)
+
+
+def test_not_finite_across_cuts():
+    """A query that is not finite stays NaN where its keys are divided between CTAs, whose parts are joined."""
+    c = case([1, 1], [6000, 3000], hq=4, hkv=2, d=128)
+    good, good_l = call(c)
+    c["dev"][0] = c["dev"][0].clone()
+    c["dev"][0][0, 1, 5], c["dev"][0][1, 2, 7] = float("-inf"), float("nan")
+    o, lse = call(c)
+    bad = torch.zeros(2, 4, dtype=torch.bool, device="cuda")
+    bad[0, 1] = bad[1, 2] = True
+    assert bool(torch.isnan(o[bad]).all()) and not bool(torch.isfinite(lse[bad]).any())
+    assert torch.equal(o[~bad], good[~bad]) and torch.equal(lse[~bad], good_l[~bad])
