@@ -737,6 +737,19 @@ def test_every_access_is_inside_the_buffers(d, order):
             assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("hkv,d,n", [(1, 128, 4005), (2, 192, 8201), (1, 512, 13001), (8, 128, 40100)])
+def test_long_reads_stay_inside_the_buffers(hkv, d, n):
+    """The read's forms for many rows: their outputs and scales end where the last row does."""
+    c = case([1, 1], [n - 3, 3], hkv=hkv, hq=hkv, d=d, seed=6, poison=False)
+    cu = torch.tensor([0, n - 3, n], dtype=torch.int32, device="cuda")
+    want = sdpa.sdpa_paged_read_fp8(*c["dev"][1:7], cu, rows=n, dtype=BF)
+    with sdpa.address_checked():
+        sdpa.sdpa_debug_address_report()
+        got = sdpa.sdpa_paged_read_fp8(*c["dev"][1:7], cu, rows=n, dtype=BF)
+        assert sdpa.sdpa_debug_address_report()[0] == 0 and sdpa.sdpa_get_device_error() == 0
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
 def test_the_checker_sees_the_new_accesses():
     """With every extent 16 bytes short the last bytes of the scales and outputs count as outside, and are not written."""
     c = case([1, 1], [16, 32], hq=2, hkv=2, d=128)

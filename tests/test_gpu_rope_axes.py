@@ -156,3 +156,45 @@ def test_append(d, dv, inter, sections):
     assert torch.equal(s["kc"], kc) and torch.equal(s["vc"], vc)
     assert torch.equal(q_out[:-3], q_ref[:-3]) and bool((q_out[-3:] == 5).all())
     assert sdpa.sdpa_get_device_error() == 0
+
+
+@pytest.mark.parametrize("rows,hq,hkv,d,inter,fused,sections",
+                         [c for c in CASES if c[0] < 100] + [(5000, 8, 2, 128, False, True, (22, 21, 21))])
+def test_every_access_is_inside_the_buffers(rows, hq, hkv, d, inter, fused, sections):
+    """The address-checked build, forward and gradient, positions in rows of a wider tensor: the other build's bits."""
+    q, k, qd, kd, wq, wk, table, _ = make(rows, hq, hkv, d, 2 * sum(sections), BF, fused)
+    wide = torch.full((len(sections), rows + 5), -1, dtype=torch.int32)
+    wide[:, :rows] = axes_positions(rows, len(sections), 8)
+    pos = wide.cuda()[:, :rows]
+    args = (qd, kd, dev(wq), dev(wk), dev(table))
+    kw = dict(eps=EPS, interleaved=inter, sections=sections)
+    gq, gk = torch.randn_like(qd).contiguous(), torch.randn_like(kd).contiguous()
+    want = sdpa.sdpa_qk_norm_rope(*args, pos, **kw) + sdpa.sdpa_qk_norm_rope_bwd(gq, gk, *args, pos, **kw)
+    with sdpa.address_checked():
+        sdpa.sdpa_debug_address_report()
+        got = sdpa.sdpa_qk_norm_rope(*args, pos, **kw) + sdpa.sdpa_qk_norm_rope_bwd(gq, gk, *args, pos, **kw)
+        assert sdpa.sdpa_debug_address_report()[0] == 0 and sdpa.sdpa_get_device_error() == 0
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_gradient_captured_and_on_two_streams():
+    sections, rows = (16, 24, 24), 4000
+    q, k, qd, kd, wq, wk, table, _ = make(rows, 8, 2, 128, 128, BF, True)
+    args = (qd, kd, dev(wq), dev(wk), dev(table))
+    a, b = (axes_positions(rows, 3, seed).cuda() for seed in (9, 10))
+    gq, gk = torch.randn_like(qd).contiguous(), torch.randn_like(kd).contiguous()
+    want = [sdpa.sdpa_qk_norm_rope_bwd(gq, gk, *args, p, sections=sections) for p in (a, b)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = [sdpa.sdpa_qk_norm_rope_bwd(gq, gk, *args, p, sections=sections, stream=s) for p, s in zip((a, b), streams)]
+    torch.cuda.synchronize()
+    for x, y in zip(got, want):
+        assert all(torch.equal(u, v) for u, v in zip(x, y))
+    held, graph = a.clone(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = sdpa.sdpa_qk_norm_rope_bwd(gq, gk, *args, held, sections=sections)
+    for p, y in ((b, want[1]), (a, want[0])):
+        held.copy_(p)
+        graph.replay()
+        assert all(torch.equal(u, v) for u, v in zip(out, y))
