@@ -25,11 +25,19 @@
 // deliver them.)
 //
 // The scales: a thread of the softmax has one key, so 2^ek is one factor for its
-// scores; and as 2^ev belongs to its weight, the running maximum is taken over
-// score + ev (log2 units) and P = 2^(score + ev - m). The denominator adds up P 2^-ev.
-// With P at most 2^4 past the maximum in use, times 2^11, the largest weight
-// of a row is at least 2^11 and what E5M2's last step (2^-16) cannot hold is below
-// 2^-28 of it.
+// scores; and as 2^ev belongs to its weight, the running maximum m is taken over
+// score + ev (log2 units): d = 2^(score - m) goes into the denominator and P = d 2^ev
+// to the product. With P at most 2^4 past the maximum in use, times 2^11, the largest
+// weight of a row is at least 2^11 and what E5M2's last step (2^-16) cannot hold is
+// below 2^-28 of it.
+// Denominators know nothing of ev: beside value rows of 2^80, a row of zeros (ev = -80)
+// with the same score has the same share of them. With one maximum for both, they lie
+// between 2^(11 - 80) (all of their weight on the largest values) and 2^(15 + 80) a key,
+// within fp32's range for 2^30 keys, and what is too small for a d is below 2^-57 of the
+// row's. Where two of them meet (a new maximum, the two warpgroups, parts of an item)
+// the factor between their maxima can be 2^-160: a new maximum takes half of it twice,
+// and what leaves a warpgroup is written as 2^m l with l in 1 .. 2, so that m compares
+// denominators and no longer the largest values.
 //
 // Roles (512 threads): warps 0-3 and 4-7 softmax, a tile each in turn, one thread
 // per key (and per value column of the output). Each of the two warpgroups has its
@@ -155,6 +163,9 @@ __device__ __forceinline__ void split4(float x0, float x1, float x2, float x3, u
     }
   }
 }
+
+// The exponent of a positive number; of 0, infinity and NaN one whose power of two leaves them what they are.
+__device__ __forceinline__ int exponent_of(float x) { return min((__float_as_int(x) >> 23) - 127, 126); }
 
 // The sum of a value's three terms, of 16 columns of 4 rows.
 __device__ __forceinline__ float terms_sum(const uint32_t (&u)[16], int r) {
@@ -613,14 +624,14 @@ __global__ void __launch_bounds__(512, 1)
 #pragma unroll
               for (int r = 0; r < 4; ++r) {
                 const int i = (c + x) * 4 + r;
-                s[i] = (unsigned)(i - r_lo) < span ? fmaf(terms_sum(u[x], r) * fr[r], sk, sc.y) : -INFINITY;
+                s[i] = (unsigned)(i - r_lo) < span ? terms_sum(u[x], r) * fr[r] * sk : -INFINITY;
                 top = fmaxf(top, s[i] - mr[r]);
               }
             }
           }
           mbar_arrive(&sc_free[slot]);
           // only a row that jumps past the maximum in use (or sees its first key) has it moved and O^T and the sums rescaled
-          if (!named_bar_and(bar_id, 128, ok && !(top > kLift + kSlack))) {
+          if (!named_bar_and(bar_id, 128, ok && !(top + sc.y > kLift + kSlack))) {
             if (!named_bar_and(bar_id, 128, ok)) {
               ok = false;
               break;
@@ -628,7 +639,8 @@ __global__ void __launch_bounds__(512, 1)
 #pragma unroll
             for (int c = 0; c < C::QUADS; ++c) {
               if (c >= quads) break;
-              const float4 m4 = make_float4(warp_max(s[c * 4]), warp_max(s[c * 4 + 1]), warp_max(s[c * 4 + 2]), warp_max(s[c * 4 + 3]));
+              const float4 m4 = make_float4(warp_max(s[c * 4] + sc.y), warp_max(s[c * 4 + 1] + sc.y),
+                                            warp_max(s[c * 4 + 2] + sc.y), warp_max(s[c * 4 + 3] + sc.y));
               if (lane == 0) *reinterpret_cast<float4*>(w_g + (warp % 4) * N + c * 4) = m4;
             }
             named_bar_sync(bar_id, 128);
@@ -636,7 +648,7 @@ __global__ void __launch_bounds__(512, 1)
               const float m = fmaxf(fmaxf(w_g[tid], w_g[N + tid]), fmaxf(w_g[2 * N + tid], w_g[3 * N + tid])) - kLift;
               const float old = m_g[tid];
               const bool move = m > old + kSlack;
-              f_g[tid] = move ? ex2(old - m) : 1.f;
+              f_g[tid] = move ? ex2(0.5f * (old - m)) : 1.f;  // the root of the factor
               if (move) m_g[tid] = m;
             }
             named_bar_sync(bar_id, 128);
@@ -644,10 +656,10 @@ __global__ void __launch_bounds__(512, 1)
             for (int c = 0; c < C::QUADS; ++c) {
               if (c >= quads) break;
               const float4 f4 = *reinterpret_cast<const float4*>(f_g + c * 4);
-              l[c * 4] *= f4.x;
-              l[c * 4 + 1] *= f4.y;
-              l[c * 4 + 2] *= f4.z;
-              l[c * 4 + 3] *= f4.w;
+              l[c * 4] = l[c * 4] * f4.x * f4.x;
+              l[c * 4 + 1] = l[c * 4 + 1] * f4.y * f4.y;
+              l[c * 4 + 2] = l[c * 4 + 2] * f4.z * f4.z;
+              l[c * 4 + 3] = l[c * 4 + 3] * f4.w * f4.w;
             }
             if (j >= 2) {  // this warpgroup's last P V is done: see above
 #pragma unroll 1
@@ -659,7 +671,7 @@ __global__ void __launch_bounds__(512, 1)
                   tmem_wait_ld();
                   fence16(u);
                   const float4 f4 = *reinterpret_cast<const float4*>(f_g + c * 4);
-                  const float fr[4] = {f4.x, f4.y, f4.z, f4.w};
+                  const float fr[4] = {f4.x * f4.x, f4.y * f4.y, f4.z * f4.z, f4.w * f4.w};
 #pragma unroll
                   for (int i = 0; i < 12; ++i) u[i] = __float_as_uint(__uint_as_float(u[i]) * fr[i % 4]);
                   tmem_st16(my_o + vb * C::NT + c * 16, u);
@@ -667,7 +679,7 @@ __global__ void __launch_bounds__(512, 1)
               tmem_wait_st();
             }
           }
-          const float un_v = ex2(-sc.y);
+          const float by_v = exp2_int((int)sc.y);
 #pragma unroll
           for (int c = 0; c < C::QUADS; ++c) {
             if (c >= quads) break;
@@ -676,8 +688,9 @@ __global__ void __launch_bounds__(512, 1)
             float x[4];
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-              x[r] = ex2(s[c * 4 + r] - mr[r]);
-              l[c * 4 + r] = fmaf(x[r], un_v, l[c * 4 + r]);
+              const float d = ex2(s[c * 4 + r] - mr[r]);
+              l[c * 4 + r] += d;
+              x[r] = d * by_v;
             }
             uint32_t term[3];
             split4(x[0], x[1], x[2], x[3], term);
@@ -729,14 +742,18 @@ __global__ void __launch_bounds__(512, 1)
         if (threadIdx.x < N) {
           const float* a = s_w + tid;
           const float* b = a + 4 * N;
-          const float top = fmaxf(s_m[tid], s_m[N + tid]);
-          const float fa = ex2(s_m[tid] - top), fb = ex2(s_m[N + tid] - top);  // 0 without a key
-          const float sum = fa * ((a[0] + a[N]) + (a[2 * N] + a[3 * N])) + fb * ((b[0] + b[N]) + (b[2 * N] + b[3 * N]));
+          const float la = (a[0] + a[N]) + (a[2 * N] + a[3 * N]), lb = (b[0] + b[N]) + (b[2 * N] + b[3 * N]);
+          const int ea = exponent_of(la), eb = exponent_of(lb);
+          const float ua = exp2_int(-ea), ub = exp2_int(-eb);
+          const float apart = (s_m[tid] - s_m[N + tid]) + (float)(ea - eb);
+          const float fa = ex2(fminf(apart, 0.f)), fb = ex2(fminf(-apart, 0.f));  // 0 without a key
+          const float top = apart >= 0.f ? s_m[tid] + (float)ea : s_m[N + tid] + (float)eb;
+          const float sum = fa * (la * ua) + fb * (lb * ub);
           // a sum that is NaN makes the part's maximum so, or the join would take a part without one for one without keys
           const float m = isnan(sum) ? sum : sum == 0.f ? -INFINITY : top;
           const float f = whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
-          s_l[tid] = fa * f;
-          s_l[N + tid] = fb * f;
+          s_l[tid] = fa * f * ua;
+          s_l[N + tid] = fb * f * ub;
           if (tid < rows && tid % p.block_heads < un.heads) {
             if (whole) {
               float* at = p.lse + (row0 + tid / p.block_heads) * p.hq + un.head0 + tid % p.block_heads;
