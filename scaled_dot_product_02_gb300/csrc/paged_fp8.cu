@@ -75,7 +75,7 @@ namespace {
 constexpr int kCodes = 16384;      // bytes of a ring stage
 constexpr float kLift = 11.f;      // log2 of what P is multiplied by
 constexpr float kSlack = 4.f;      // how far (log2) a weight may pass the maximum in use
-constexpr float kNone = -1e30f;    // in place of a maximum: no key yet (finite, so that nothing becomes inf - inf)
+constexpr float kNone = -3.402823466e38f;  // in place of a maximum: no key yet (the least number: finite, so that no inf - inf arises)
 constexpr int kScaleLo = 47, kScaleHi = 207;  // the scale bytes that rows are given
 
 template <int DQK, int DV, int N>

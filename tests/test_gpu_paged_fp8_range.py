@@ -167,3 +167,35 @@ def test_small_values_are_kept_beside_large_ones(d, hq, hkv, spread):
         assert bool((tol.amax(-1) <= 2.0 ** -4 * want.abs().amax(-1)).all())
         assert bool(((tol < want.abs()).double().mean(-1) > 0.5).all())
         check(c, *call(c), expected)
+
+
+@pytest.mark.parametrize("d,hq,hkv", [(128, 4, 1), (512, 2, 2)])
+def test_scores_that_are_all_far_below_zero(d, hq, hkv):
+    """Scores of -2^108 and below, one product each: the largest ones of a row share its weight, as any others would."""
+    c = case([1, 3], [700, 200], hq=hq, hkv=hkv, d=d)
+    c["q"] = torch.zeros_like(c["q"])
+    c["q"][..., 0] = 2.0 ** 110
+    c["dev"][0] = c["q"].cuda()
+
+    def rows(b):
+        k = torch.zeros(int(c["lens"][b]), hkv, d)
+        k[..., 0] = -torch.exp2(3.0 + torch.arange(int(c["lens"][b])) % 5)[:, None]
+        return k
+    rewrite(c, "k", rows)
+    step = 2 * max(c["vc"][places(c, b)].abs().max().item() for b in range(2))  # above 448 2^ev: a row's largest code is over 224
+    for cap in (0, 1, 5):
+        sdpa.sdpa_debug_set_max_ctas(cap)
+        try:
+            o, lse = call(c)
+        finally:
+            sdpa.sdpa_debug_set_max_ctas(0)
+        want_l = -2.0 ** 113 * c["scale"]  # the count's logarithm is far below a step
+        assert bool(((lse.cpu().double() - want_l).abs() <= 2.0 ** -19 * abs(want_l)).all())
+        for b, n in enumerate(c["lens"]):
+            for i in range(int(c["cu"][b]), int(c["cu"][b + 1])):
+                seen = int(n) - (int(c["cu"][b + 1]) - 1 - i)
+                v = c["vc"][places(c, b)][:seen:5].repeat_interleave(hq // hkv, 1)
+                want, pv = v.mean(0), v.abs().mean(0)
+                tol = 2.0 ** -8 * want.abs() + (2.0 ** -10 + 2.0 ** -19) * pv + n * 2.0 ** -28 * step
+                assert bool(((o[i].cpu().double() - want).abs() <= tol).all())
+    assert sdpa.sdpa_get_device_error() == 0
