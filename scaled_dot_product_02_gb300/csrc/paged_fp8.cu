@@ -36,8 +36,9 @@
 // within fp32's range for 2^30 keys, and what is too small for a d is below 2^-57 of the
 // row's. Where two of them meet (a new maximum, the two warpgroups, parts of an item)
 // the factor between their maxima can be 2^-160: a new maximum takes half of it twice,
-// and what leaves a warpgroup is written as 2^m l with l in 1 .. 2, so that m compares
-// denominators and no longer the largest values.
+// the two warpgroups compare denominators instead of maxima, and so do parts whose
+// denominator l is beyond 2^-48 .. 2^48: there m takes the power of two (elsewhere it
+// stays what it is, as large scores leave a sum no room for it).
 //
 // Roles (512 threads): warps 0-3 and 4-7 softmax, a tile each in turn, one thread
 // per key (and per value column of the output). Each of the two warpgroups has its
@@ -76,6 +77,7 @@ constexpr int kCodes = 16384;      // bytes of a ring stage
 constexpr float kLift = 11.f;      // log2 of what P is multiplied by
 constexpr float kSlack = 4.f;      // how far (log2) a weight may pass the maximum in use
 constexpr float kNone = -3.402823466e38f;  // in place of a maximum: no key yet (the least number: finite, so that no inf - inf arises)
+constexpr int kStay = 48;           // the largest power of two that stays with a part's sum
 constexpr int kScaleLo = 47, kScaleHi = 207;  // the scale bytes that rows are given
 
 template <int DQK, int DV, int N>
@@ -747,11 +749,13 @@ __global__ void __launch_bounds__(512, 1)
           const float ua = exp2_int(-ea), ub = exp2_int(-eb);
           const float apart = (s_m[tid] - s_m[N + tid]) + (float)(ea - eb);
           const float fa = ex2(fminf(apart, 0.f)), fb = ex2(fminf(-apart, 0.f));  // 0 without a key
-          const float top = apart >= 0.f ? s_m[tid] + (float)ea : s_m[N + tid] + (float)eb;
-          const float sum = fa * (la * ua) + fb * (lb * ub);
+          const float base = apart >= 0.f ? s_m[tid] : s_m[N + tid];
+          const int up = apart >= 0.f ? ea : eb, stay = whole || abs(up) > kStay ? 0 : up;
+          float sum = fa * (la * ua) + fb * (lb * ub);  // times 2^(base + up)
           // a sum that is NaN makes the part's maximum so, or the join would take a part without one for one without keys
-          const float m = isnan(sum) ? sum : sum == 0.f ? -INFINITY : top;
-          const float f = whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
+          const float m = isnan(sum) ? sum : sum == 0.f ? -INFINITY : base + (float)(up - stay);
+          const float f = whole ? (sum == 0.f ? 0.f : 1.f / sum) : exp2_int(stay);
+          if (!whole) sum *= f;
           s_l[tid] = fa * f * ua;
           s_l[N + tid] = fb * f * ub;
           if (tid < rows && tid % p.block_heads < un.heads) {
