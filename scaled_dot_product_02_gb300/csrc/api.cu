@@ -1729,6 +1729,7 @@ int sdpa_paged_fwd_fp8(const sdpa_paged_problem* p, const sdpa_paged_scales* sca
   PagedFp8Launch L;
   std::memset(&L, 0, sizeof(L));
   L.p.a = paged_params(p, pl, true, cu_seqlens_q, kv_lens, block_table, o, lse, static_cast<uint8_t*>(workspace), err, chk);
+  L.p.a.scale_log2 = p->softmax_scale * 1.4426950408889634f;  // 0 may be 0: masked scores never meet it
   L.p.a.box_rows = std::min(p->page_size & -p->page_size, 128);
   L.p.a.slot_first = slot_first(p);
   // An item's own cost, in key tiles: some 2.5 us for its first scores, its end and its output, against 0.8 us for the 32 KB

@@ -25,11 +25,12 @@
 // deliver them.)
 //
 // The scales: a thread of the softmax has one key, so 2^ek is one factor for its
-// scores; and as 2^ev belongs to its weight, the running maximum m is taken over
-// score + ev (log2 units): d = 2^(score - m) goes into the denominator and P = d 2^ev
-// to the product. With P at most 2^4 past the maximum in use, times 2^11, the largest
-// weight of a row is at least 2^11 and what E5M2's last step (2^-16) cannot hold is
-// below 2^-28 of it.
+// scores, applied before the row's (products of at most 2^33 times 2^ek stay within
+// fp32, times a row's power of two alone they need not); and as 2^ev belongs to its
+// weight, the running maximum m is taken over score + ev (log2 units): d = 2^(score - m)
+// goes into the denominator and P = d 2^ev to the product. With P at most 2^4 past the
+// maximum in use, times 2^11, the largest weight of a row is at least 2^11 and what
+// E5M2's last step (2^-16) cannot hold is below 2^-28 of it.
 // Denominators know nothing of ev: beside value rows of 2^80, a row of zeros (ev = -80)
 // with the same score has the same share of them. With one maximum for both, they lie
 // between 2^(11 - 80) (all of their weight on the largest values) and 2^(15 + 80) a key,
@@ -178,9 +179,9 @@ __device__ __forceinline__ void fence16(uint32_t (&u)[16]) {
   for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(u[i]));
 }
 
-// One item's rows of Q as their terms in shared memory (K-major, 128-byte swizzle), and what undoes the power of two that
-// a row was multiplied by: the share of warp `part` of PARTS. Rows past the item's stay as they are: nothing of theirs is
-// looked at.
+// One item's rows of Q as their terms in shared memory (K-major, 128-byte swizzle), and what makes scores of their
+// products, the softmax scale (log2 units) over the power of two that a row was multiplied by: the share of warp `part` of
+// PARTS. Rows past the item's stay as they are: nothing of theirs is looked at.
 template <int DQK, int N, bool BF16, int PARTS>
 __device__ __forceinline__ void split_q(const PagedFp8Params& f, const PagedWalk& w, const PagedUnit& un, uint8_t* sQ,
                                         float* s_fq, int part, int lane) {
@@ -225,7 +226,7 @@ __device__ __forceinline__ void split_q(const PagedFp8Params& f, const PagedWalk
       const int up = top > 0.f ? min(14 + 127 - (__float_as_int(top) >> 23), 126) : 0;
       const float by = exp2_int(up);
       if (r >= rows) continue;
-      if (sub == 0) s_fq[r] = exp2_int(-up);
+      if (sub == 0) s_fq[r] = exp2_int(-up) * p.scale_log2;
       auto term_of = [&](float a) { return fabsf(a) == INFINITY ? NAN : a * by; };  // the terms have no infinity
 #pragma unroll
       for (int v = 0; v < VPL; ++v) {
@@ -277,7 +278,7 @@ __global__ void __launch_bounds__(512, 1)
   float* s_f = s_m + 2 * N;    // [N] factors of a rescale
   float* s_w = s_f + 2 * N;    // [4][N] warps' maxima, then their sums
   float* s_l = s_w + 8 * N;    // [N] factors of an item's output (these four for each softmax warpgroup)
-  float* s_fq = s_l + 2 * N;   // [NQ][N] what undoes the rows' scaling
+  float* s_fq = s_l + 2 * N;   // [NQ][N] the rows' factors of split_q
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -572,7 +573,6 @@ __global__ void __launch_bounds__(512, 1)
       const int bar_id = 1 + me_g;  // named barriers: a warpgroup's, and 3 for both
       float *const m_g = s_m + me_g * N, *const f_g = s_f + me_g * N, *const w_g = s_w + me_g * 4 * N;
       uint8_t* const pb = sP + me_g * C::P_BYTES;
-      const float sl2 = p.scale_log2;
       int gs = 0, c0 = 0, nq = 0;  // tiles and ring stages of earlier items, items with keys
       bool ok = true;
       do {
@@ -605,7 +605,6 @@ __global__ void __launch_bounds__(512, 1)
             ok = false;
           tc_fence_after();
           const float2 sc = sScale[slot * kTile + tid];
-          const float sk = sl2 * sc.x;
           float s[N], top = -INFINITY;
 #pragma unroll
           for (int c = 0; c < C::QUADS; c += C::LOADS) {
@@ -626,7 +625,7 @@ __global__ void __launch_bounds__(512, 1)
 #pragma unroll
               for (int r = 0; r < 4; ++r) {
                 const int i = (c + x) * 4 + r;
-                s[i] = (unsigned)(i - r_lo) < span ? terms_sum(u[x], r) * fr[r] * sk : -INFINITY;
+                s[i] = (unsigned)(i - r_lo) < span ? terms_sum(u[x], r) * sc.x * fr[r] : -INFINITY;
                 top = fmaxf(top, s[i] - mr[r]);
               }
             }

@@ -199,3 +199,17 @@ def test_scores_that_are_all_far_below_zero(d, hq, hkv):
                 tol = 2.0 ** -8 * want.abs() + (2.0 ** -10 + 2.0 ** -19) * pv + n * 2.0 ** -28 * step
                 assert bool(((o[i].cpu().double() - want).abs() <= tol).all())
     assert sdpa.sdpa_get_device_error() == 0
+
+
+@pytest.mark.parametrize("d,hq,hkv", [(128, 8, 2), (256, 4, 1)])
+def test_queries_at_the_end_of_their_type(d, hq, hkv):
+    """Queries whose products with codes pass fp32's largest number before the keys' scales make them small, or a scale of
+    zero does; and the reverse."""
+    c = case([1, 3], [700, 200], hq=hq, hkv=hkv, d=d)
+    g = torch.Generator().manual_seed(9)
+    k = [torch.randn(int(n), hkv, d, generator=g).double() for n in c["lens"]]
+    for q_exp, k_exp, scale in ((120, -75, 2.0 ** -46), (100, 60, 0.0), (122, 2, 0.0), (-110, 80, 2.0 ** 29)):
+        c["q"] = (torch.randn(4, hq, d, generator=g) * 2.0 ** q_exp).bfloat16()
+        c["dev"][0], c["scale"] = c["q"].cuda(), scale
+        rewrite(c, "k", lambda b: k[b] * 2.0 ** k_exp)
+        check(c, *call(c), tolerances(c))
