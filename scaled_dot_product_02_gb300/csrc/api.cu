@@ -712,8 +712,9 @@ Extent cache_extent(const sdpa_paged_problem* p, const CacheView& c) {
 }
 
 // Whether every row of the two tensors lies apart from all others. Where their spans interleave (pages that hold K and V
-// together), addresses are compared modulo a step that both tensors' strides from some level on are multiples of: the
-// stretch of a step that one fills and the one that the other fills must not meet.
+// together), addresses are compared modulo a step that both tensors' strides from some level on are multiples of, all of
+// them (scale bytes' strides need not be multiples of one another): the stretch of a step that one fills and the one that
+// the other fills must not meet.
 bool caches_apart(const sdpa_paged_problem* p, const CacheView& kc, const CacheView& vc) {
   struct Level {
     long long stride, fill;  // in bytes; fill: from the first to the last within one step of the stride
@@ -734,7 +735,9 @@ bool caches_apart(const sdpa_paged_problem* p, const CacheView& kc, const CacheV
   if (!overlaps(cache_extent(p, kc), cache_extent(p, vc))) return true;
   const long long off = (long long)(reinterpret_cast<uintptr_t>(vc.base) - reinterpret_cast<uintptr_t>(kc.base));
   for (int i = 0; i < used; ++i) {
-    const long long step = std::gcd(k[i].stride, v[i].stride), at = (off % step + step) % step;
+    long long step = 0;
+    for (int j = i; j < used; ++j) step = std::gcd(step, std::gcd(k[j].stride, v[j].stride));
+    const long long at = (off % step + step) % step;
     if (at >= k[i].fill && at + v[i].fill <= step) return true;
   }
   return false;
