@@ -363,8 +363,20 @@ __global__ void __launch_bounds__(kThreads, Row<D>::VPL == 1 && !AXES && !FP8 ? 
   }
   float2 ca[R::VPL][4], cb[R::VPL][4];
   if (NORM && !is_v) {
+    // Without axes and append the angles' row has a branch of its own: through positions_of the bf16 kernels spill 18 to 24
+    // bytes instead of 8 to 12 (600 tokens of 32 + 8 heads of 128 4.4 us against 4.1). The append is quicker through it
+    // (7007 tokens, 16 + 8 heads of 256, 68 us against 71; of 192 in fp16 58 against 62), a step's tokens the same.
     int pos[4];
-    if (!positions_of<AXES>(p, row, APPEND && !p.pos, slot.position, pos)) {
+    bool fits = true;
+    const float* angles = nullptr;
+    if constexpr (AXES || APPEND) {
+      fits = positions_of<AXES>(p, row, APPEND && !p.pos, slot.position, pos);
+    } else if (p.rot > 0) {
+      const int x = load_i32(p.chk, p.pos + row, -1);
+      fits = x >= 0 && x < p.max_pos;
+      angles = p.table + (long long)x * p.rot;
+    }
+    if (!fits) {
       if (lane == 0) record_error(p.err, SDPA_ERR_BAD_INDEX);
       return;
     }
@@ -377,7 +389,8 @@ __global__ void __launch_bounds__(kThreads, Row<D>::VPL == 1 && !AXES && !FP8 ? 
       unpack8<E>(in ? load16(p.chk, weight + idx * 8) : make_uint4(0u, 0u, 0u, 0u), wt);
       unpack8<E>(in ? load16(p.chk, weight + at[v].partner * 8) : make_uint4(0u, 0u, 0u, 0u), wp);
       if constexpr (!AXES)
-        angles_of(at[v], idx, RowAngles{p.table + (long long)pos[0] * p.rot, p.rot / 2, p.chk}, p.rot, inter, c, s);
+        angles_of(at[v], idx, RowAngles{APPEND ? p.table + (long long)pos[0] * p.rot : angles, p.rot / 2, p.chk}, p.rot,
+                  inter, c, s);
       else
         angles_of(at[v], idx,
                   AxesAngles{p.axes, p.table, {(long long)pos[0] * p.rot, (long long)pos[1] * p.rot,
