@@ -675,8 +675,10 @@ int encode_cache(CUtensorMap* m, const void* base, const sdpa_paged_problem* p, 
   const cuuint64_t strides[3] = {(cuuint64_t)lo * bytes, (cuuint64_t)hi * bytes, (cuuint64_t)page * bytes};
   const cuuint32_t box[4] = {(cuuint32_t)(128 / bytes), (cuuint32_t)(first ? box_rows : 1), (cuuint32_t)(first ? 1 : box_rows), 1};
   const cuuint32_t estr[4] = {1, 1, 1, 1};
-  // 256 bytes from memory at a time only where they belong to one row: a 128-byte row would bring the next head's along,
-  // for nobody (64 sequences of 500 to 16384 keys in codes of head_dim 128: 297 us with them, 253 without)
+  // 256 bytes from memory at a time only where they belong to one row: a 128-byte row, or the last 128 bytes of one of 384,
+  // would bring the next head's along, for nobody (64 sequences of 500 to 16384 keys, 256 bytes at a time everywhere / as
+  // here: codes of head_dim 128 297 / 253 us; 16-bit rows of 192 446 / 420, 16 sequences of 1 to 16 tokens 71 to 78 / 68 to
+  // 76; with [head][slot] pages, whose next row is wanted too, and in the chunk kernels within 0.4 %)
   const auto promotion = (long long)width * bytes % 256 == 0 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_L2_128B;
   CUresult r = fn(m, type, 4, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                   CU_TENSOR_MAP_SWIZZLE_128B, promotion, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
