@@ -11,8 +11,11 @@
 // An 8-bit MMA wants both operands in 8 bits, and Q and P have more. Each is
 // written as a sum of three E5M2 terms, every one the rest of those before it
 // rounded to nearest: three significant bits and a sign each, 2^-11 of the
-// value left over and the range of fp16 (E5M2 is fp16's upper byte). For Q,
-// scaled by a power of two a row, the sum is exact: 11 bits at most are there.
+// value left over and the range of fp16 (E5M2 is fp16's upper byte). A row of Q is
+// scaled by a power of two that brings its largest magnitude to 2^14 .. 2^15; then
+// the sum is exact for values down to 2^-23 of the largest (bf16; fp16, of 11 bits,
+// 2^-20), and below that off by at most half of the last term's least step (2^-16):
+// 2^-31 of the row's largest, in every value.
 // The terms lie side by side on the N side, so a tile of codes is read once for
 // all three, and the threads that read the products from tensor memory add them
 // up: every 4 rows take 16 columns, their first terms, second, third, and 4 of

@@ -213,3 +213,30 @@ def test_queries_at_the_end_of_their_type(d, hq, hkv):
         c["dev"][0], c["scale"] = c["q"].cuda(), scale
         rewrite(c, "k", lambda b: k[b] * 2.0 ** k_exp)
         check(c, *call(c), tolerances(c))
+
+
+@pytest.mark.parametrize("dtype,top", [(BF, 2.0 ** 10), (BF, 2.0 ** 20), (BF, 2.0 ** 40), (HF, 2.0 ** 15)])
+@pytest.mark.parametrize("d,hq,hkv", [(128, 8, 2), (512, 8, 8)])
+def test_a_channel_of_q_that_no_key_has(d, hq, hkv, dtype, top):
+    """One value of a row outweighs all others and meets codes of zero. The others are held to half of the last term's least
+    step, 2^-17, where the largest is brought to 2^14 or more: each is off by at most 2^-31 of it."""
+    c = case([1, 3], [700, 200], hq=hq, hkv=hkv, d=d, dtype=dtype)
+    c["q"][..., 7] = top
+    c["dev"][0] = c["q"].cuda()
+    g = torch.Generator().manual_seed(2)
+
+    def rows(b):
+        k = torch.randn(int(c["lens"][b]), hkv, d, generator=g)
+        k[..., 7] = 0
+        return k
+    rewrite(c, "k", rows)
+    largest = max(c["kc"][places(c, b)].abs().sum(-1).max().item() for b in range(2))
+    extra = 2.0 ** -31 * top * largest * c["scale"]  # of a score
+    want, want_l, tol, tol_l = tolerances(c)
+    _, _, pv, _ = ref.paged_attention(c["q"], c["kc"], c["vc"], c["table"], c["lens"], c["cu"], c["page"], "nhd", True, -1, c["scale"])
+    o, lse = call(c)
+    if extra < 0.1:  # a weight's and the sum's share: e^(2 x) - 1 <= 2.3 x
+        check(c, o, lse, (want, want_l, tol + 2.3 * extra * pv, tol_l + extra))
+    else:  # the scores say nothing any more: the mean of some values, and no more than that
+        assert bool((o.cpu().double().abs() <= 1.01 * max(c["vc"][places(c, b)].abs().max().item() for b in range(2))).all())
+        assert sdpa.sdpa_get_device_error() == 0
