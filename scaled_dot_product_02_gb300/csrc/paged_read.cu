@@ -22,8 +22,11 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kSteps = 8;   // loads a lane has in flight
-// Rows up to which a warp takes one token (8 kv heads of 128; us with one / four): 1000 rows 6.2 / 10.4, 8000 16.1 / 17.0,
-// 32000 39.1 / 41.2, 73500 82.1 / 77.9. (The K or the V of one token a warp: 16000 rows 31.2 against 23.5.)
+// A warp takes one token, or four from kFew rows on where a token's vectors are one round of its loads or less. Captured
+// us with one / four: 8 kv heads of 128 (256 vectors), 1000 rows 4.1 / 7.7, 10000 14.6 / 15.4, 39000 43.9 / 44.4, 60000 64.9
+// / 63.5; 2 of 512 (256), 39000 43.8 / 44.2, 60000 64.5 / 63.4; of more vectors one is quicker throughout: 16 of 128 or 8 of
+// 256 (512), 20000 41.6 / 50.5, 60000 112 / 122; 8 of 512 (1024), 20000 80 / 93, 39000 146 / 164. (The K or the V of one
+// token a warp: 8 of 128, 16000 rows 31.2 against 23.5.)
 constexpr int kFew = 40000;
 // A token of up to kNarrow 16-byte vectors leaves lanes and steps idle: from kFewNarrow tokens a vector up a warp's lanes walk
 // kFlat tokens at once (heads of 128; us so / as above): 1 kv head, 2000 rows 6.3 / 6.3, 16000 8.3 / 15.8, 64000 18.5 / 41.1; 2
@@ -158,7 +161,7 @@ template <bool BF16, int D, int DV>
 int launch_t(const PagedReadParams& p, cudaStream_t s) {
   const int vecs = p.hkv * (D + DV) / 8;
   const bool flat = vecs <= kNarrow && p.rows > kFewNarrow * (long long)vecs;
-  const int tokens = flat ? kFlat : p.rows <= kFew ? 1 : 4;
+  const int tokens = flat ? kFlat : vecs > 32 * kSteps || p.rows <= kFew ? 1 : 4;
   const int per = kThreads / 32 * tokens;  // rows of a block
   const unsigned grid = (unsigned)((p.rows + per - 1) / per);
   auto kern = flat          ? paged_read_kernel<BF16, D, DV, kFlat, true>
