@@ -513,11 +513,12 @@ SDPA_API int sdpa_paged_read_fp8(const sdpa_paged_problem* p, const sdpa_paged_s
 
 /* sdpa_paged_fwd over an 8-bit cache: the attention over the values that codes and scales stand for
  * (q stays in 16 bits, its values held to 2^-31 of their row's largest; scores are exact up to that and
- * to fp32 sums, probabilities are held to 2^-11), with the same masks, outputs, errors and workspace rules. Scale bytes of keys that no query row sees may hold
- * anything; others are taken into 47 .. 207, what the append writes. A row of q that is not finite gives
- * NaN. Rows of q lie any multiple of 8 elements apart. Made for few new tokens a sequence (decoding,
- * speculative tokens, a prompt's tail): the cache is read once for every 8 (head_dim 512), 16 (256) or
- * 32 query rows of a kv head; for longer chunks read the rows back and call sdpa_fwd. */
+ * to fp32 sums, probabilities are held to 2^-11), with the same masks, outputs, errors and workspace
+ * rules. Scale bytes of keys that no query row sees may hold anything; others are taken into 47 .. 207,
+ * what the append writes. A row of q that is not finite gives NaN. Rows of q lie any multiple of 8
+ * elements apart. Made for few new tokens a sequence (decoding, speculative tokens, a prompt's tail): the
+ * cache is read once for every 8 (head_dim 512), 16 (256) or 32 query rows of a kv head; for longer
+ * chunks read the rows back and call sdpa_fwd. */
 SDPA_API size_t sdpa_paged_fwd_fp8_workspace_size(const sdpa_paged_problem* p);
 SDPA_API int sdpa_paged_fwd_fp8(const sdpa_paged_problem* p, const sdpa_paged_scales* scales, const void* q,
                                 const void* k_cache, const void* v_cache, void* o, float* lse,

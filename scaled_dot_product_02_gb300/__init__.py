@@ -733,8 +733,9 @@ def sdpa_qk_norm_rope(q, k, q_weight, k_weight, cos_sin=None, positions=None, *,
     cos_sin: float32 [positions, rotary_dim], half cosines and half sines, or
     None for the norm alone; positions: int32, one per token. sections: several
     positions a token (time, height, width): the numbers of pairs, in order,
-    that turn by each axis's position; positions is then [axes, tokens]. Returns
-    contiguous (q_out, k_out)."""
+    that turn by each axis's position; positions is then [axes, tokens], rows
+    that may not overlap (one row for every axis: leave sections out, which
+    gives the same bits). Returns contiguous (q_out, k_out)."""
     if stream is not None:
         return _on(stream, sdpa_qk_norm_rope, locals())
     p, axes, _ = _norm_rope_plan(_meta(q), _meta(k), _meta(q_weight), _meta(k_weight), _meta(cos_sin), _meta(positions),

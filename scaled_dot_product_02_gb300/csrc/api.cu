@@ -1738,10 +1738,10 @@ int sdpa_paged_fwd_fp8(const sdpa_paged_problem* p, const sdpa_paged_scales* sca
   L.p.a.box_rows = std::min(p->page_size & -p->page_size, 128);
   L.p.a.slot_first = slot_first(p);
   // An item's own cost, in key tiles: some 2.5 us for its first scores, its end and its output, against 0.8 us for the 32 KB
-  // of a tile at head_dim 128 and 3 for the 128 KB at 512. Counted as nothing, the CTAs with many short items ended last. us
-  // by 0 / 2, 1, 1 / 3, 2, 1 / 4, 3, 2 / 6, 4, 2 tiles at 128, 192 and 256, 512: 64 sequences of 100 to 1000 keys at 128 49.2,
-  // 39.5, 37.7, 37.7, 37.5, at 512 45.3, 42.1, 42.1, 42.6, 42.6; 48 sequences, window of 1024, at 256 57.4, 50.4, 47.2, 46.2,
-  // 46.7; 9 of up to 5 tokens at 192 34.5, 31.4, 30.3, 29.1, 29.0; 64 of 500 to 16384 keys at 128 all 210 to 211.
+  // of a tile at head_dim 128 and 3 for the 128 KB at 512. Counted as nothing, the CTAs with many short items ended last. us (a
+  // pass a graph) by 0 / 2, 1, 1 / 3, 2, 1 / 4, 3, 2 / 6, 4, 2 tiles at 128, 192 and 256, 512: 64 sequences of 100 to 1000 keys at
+  // 128 49.2, 39.5, 37.7, 37.7, 37.5, at 512 45.3, 42.1, 42.1, 42.6, 42.6; 48 sequences, window of 1024, at 256 57.4, 50.4, 47.2,
+  // 46.2, 46.7; 9 of up to 5 tokens at 192 34.5, 31.4, 30.3, 29.1, 29.0; 64 of 500 to 16384 keys at 128 all 210 to 211.
   L.p.a.lead = pl.rows.split ? (d == 128 ? 4 : d == 512 ? 1 : 3) : 0;
   L.p.q = q;
   L.p.q_stride = qs;

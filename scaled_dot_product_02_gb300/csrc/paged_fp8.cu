@@ -58,13 +58,13 @@
 // its start and end cost (PagedParams::lead); a share may so get none of the tiles of
 // an item that it touches, and leaves an empty part.
 //
-// Measured with the join, captured: 64 sequences of 500 to 16384 keys, 32 heads on 8
-// of 128, 190 to 211 us across boxes, 5.3 to 5.9 TB/s (the 16-bit cache 356); the
-// same bytes at head_dim 256 193, 512 188 us (5.9, 6.1 TB/s); 48 sequences with a
-// window of 1024 at head_dim 256 46 (72); one token over 999 keys 12.4 (12.4). Items
-// of many rows are bound by the softmax: 4 tokens of 4 heads 264 us, 8 tokens 410, over
-// the first batch's keys; a group of 32 heads on one kv head 70 against the 16-bit
-// cache's 60.
+// Measured with the join, twelve passes in a captured graph (the 16-bit cache, so
+// measured, in brackets): 64 sequences of 500 to 16384 keys, 32 heads on 8 of 128,
+// 206 to 212 us, 5.3 to 5.4 TB/s (348 to 356), with [page][head][slot] pages 173; 32 of
+// them at head_dim 256 180, 16 at 512 173 us (6.2, 6.4 TB/s); 48 sequences with a window
+// of 1024 at head_dim 256 43 (69.5); one token over 999 keys 9.9 (9.4). Items of many
+// rows are bound by the softmax: over the first batch's keys 4 tokens of 4 heads 234 us
+// (347), 8 tokens 363 (353); 32 sequences with 32 heads on one kv head of 128 41 (37).
 #include <algorithm>
 #include <cuda.h>
 #include <cuda_runtime.h>

@@ -7,8 +7,9 @@
 // binary search among the sequences' ends), then all lanes walk the tokens'
 // values, eight a lane and step, with several steps' loads in flight.
 //
-// Measured (captured): 73536 tokens of 8 heads of 128 78 us, 5.8 TB/s; 6669 of 8
-// heads of 256 26.7 us, 3.1 TB/s (a chain of search, table, codes and stores once).
+// Measured (twelve passes in a captured graph): 73536 tokens of 8 heads of 128 74.5 us,
+// 6.1 TB/s; 6669 of 8 heads of 256 23.4 us, 3.5 TB/s (a chain of search, table, codes and
+// stores once).
 #include <algorithm>
 #include <cuda_runtime.h>
 
@@ -29,9 +30,9 @@ constexpr int kSteps = 8;   // loads a lane has in flight
 // token a warp: 8 of 128, 16000 rows 31.2 against 23.5.)
 constexpr int kFew = 40000;
 // A token of up to kNarrow 16-byte vectors leaves lanes and steps idle: from kFewNarrow tokens a vector up a warp's lanes walk
-// kFlat tokens at once (heads of 128; us so / as above): 1 kv head, 2000 rows 6.3 / 6.3, 16000 8.3 / 15.8, 64000 18.5 / 41.1; 2
-// heads, 16000 rows 10.9 / 16.5; 4 heads, 8000 rows 14.4 / 11.2, 16000 18.6 / 18.5, 64000 42.3 / 48.3; 6 heads, 16000 rows 25.6 /
-// 20.7, 64000 61.4 / 56.9.
+// kFlat tokens at once (heads of 128; us so / as above, both a pass a graph, 2 to 3 us more): 1 kv head, 2000 rows 6.3 / 6.3,
+// 16000 8.3 / 15.8, 64000 18.5 / 41.1; 2 heads, 16000 rows 10.9 / 16.5; 4 heads, 8000 rows 14.4 / 11.2, 16000 18.6 / 18.5, 64000
+// 42.3 / 48.3; 6 heads, 16000 rows 25.6 / 20.7, 64000 61.4 / 56.9.
 constexpr int kNarrow = 128, kFewNarrow = 100, kFlat = 8;
 
 struct Place {
